@@ -401,6 +401,46 @@ int w4_moe_layer_from_logits(const uint16_t *x, const float *logits, int M, int 
                              w4_stream_t stream);
 
 /* --------------------------------------------------------------------------
+ * w4_moe_layer_few -- the whole routed-expert layer for a few tokens, in two
+ * launches: M <= 32 tokens and M * k <= 256 assignments, where an expert sees
+ * a handful of tokens and the layer is the stream of the touched experts'
+ * packed weights.  Same inputs and output as w4_moe_layer; the result differs
+ * from it in rounding only.  The packed codes enter the tensor cores as they
+ * are (exact fp16 subnormals) and a group's scale and zero are applied to the
+ * fp32 sums, so no weight is rounded; activations and h are fp16 (beyond its
+ * finite range: saturated, W4_DEV_FP16_RANGE), sums and the combine (fma
+ * chain in slot order) are fp32, out is rounded once.  Bit-identical reruns.
+ *
+ *   x [M, d] bf16, topk_ids [M, k] int32, topk_weights [M, k] fp32,
+ *   out [M, d] bf16; ids outside [0, E) contribute nothing and set
+ *   W4_DEV_BAD_EXPERT_ID; an expert may occur twice in a token's list
+ *   workspace   at least w4_moe_layer_few_workspace_size(...) bytes, 256-byte
+ *               aligned, contents need no initialisation
+ * Requires d % 128 == 0, m % 64 == 0, gu_group == 128, dn_group == 64,
+ * k <= 32, E <= 1024, and that two tasks' rows fit shared memory beside 8
+ * tokens (d up to 6144, m up to 2560).  M = 0 does nothing.
+ * ------------------------------------------------------------------------ */
+size_t w4_moe_layer_few_workspace_size(int M, int d, int m, int E, int k);
+int w4_moe_layer_few(const uint16_t *x, const int32_t *topk_ids, const float *topk_weights,
+                     int M, int d, int m, int E, int k,
+                     const uint8_t *gu_q, const uint16_t *gu_s, const uint16_t *gu_z, int gu_group,
+                     const uint8_t *dn_q, const uint16_t *dn_s, const uint16_t *dn_z, int dn_group,
+                     void *workspace, size_t workspace_bytes, uint16_t *out,
+                     int32_t *dev_status, w4_stream_t stream);
+
+/* w4_moe_layer_few_from_logits -- w4_moe_layer_few with the router in its
+ * first launch: from the logits [M, E] fp32.  topk_ids and topk_weights are
+ * outputs, bit-identical to w4_moe_route's; out is bit-identical to
+ * w4_moe_route followed by w4_moe_layer_few.  k <= E. */
+int w4_moe_layer_few_from_logits(const uint16_t *x, const float *logits, int M, int d, int m,
+                                 int E, int k, const uint8_t *gu_q, const uint16_t *gu_s,
+                                 const uint16_t *gu_z, int gu_group, const uint8_t *dn_q,
+                                 const uint16_t *dn_s, const uint16_t *dn_z, int dn_group,
+                                 void *workspace, size_t workspace_bytes, int32_t *topk_ids,
+                                 float *topk_weights, uint16_t *out, int32_t *dev_status,
+                                 w4_stream_t stream);
+
+/* --------------------------------------------------------------------------
  * w4_moe_layer_static_scratch -- w4_moe_layer without a workspace argument.
  * The paper has no counterpart: this is a library convenience for callers
  * that cannot allocate device memory when they call the layer, e.g. a plain

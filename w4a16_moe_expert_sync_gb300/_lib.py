@@ -89,6 +89,11 @@ def load_library(path: str | None = None):
                                              V, V, V], I),
             "w4_moe_layer_from_logits": ([V, V, I, I, I, I, I, I, V, V, V, I, V, V, V, I, V,
                                           SZ, V, V, V, V, V], I),
+            "w4_moe_layer_few_workspace_size": ([I, I, I, I, I], SZ),
+            "w4_moe_layer_few": ([V, V, V, I, I, I, I, I, V, V, V, I, V, V, V, I, V, SZ, V, V, V],
+                                 I),
+            "w4_moe_layer_few_from_logits": ([V, V, I, I, I, I, I, V, V, V, I, V, V, V, I, V, SZ,
+                                              V, V, V, V, V], I),
             "w4_w4a16_linear_workspace_size": ([I, I, I, I], SZ),
             "w4_w4a16_linear": ([V, I, I, I, V, V, V, I, V, SZ, V, V, V], I),
             "w4_rmsnorm": ([V, V, I, I, ctypes.c_float, V, V], I),
@@ -459,6 +464,65 @@ def w4_moe_layer_from_logits(x, logits, k: int, gu, dn, block_m: int = 16, gu_gr
         gu_group, _ptr(dn_q), _ptr(dn_s), _ptr(dn_z), dn_group, _ptr(workspace),
         workspace.numel(), _ptr(ids), _ptr(weights), _ptr(out), _ptr(dev_status),
         _stream(stream)), "w4_moe_layer_from_logits")
+    return out, ids, weights
+
+
+def w4_moe_layer_few_workspace_size(M, d, m, E, k) -> int:
+    return int(load_library().w4_moe_layer_few_workspace_size(M, d, m, E, k))
+
+
+def _few_dims(x, gu, dn):
+    """(M, d, m, E) of a few-token call, with the weights' shapes checked."""
+    M, d = x.shape
+    E, two_m, half_d = gu[0].shape
+    m = two_m // 2
+    if half_d * 2 != d or tuple(dn[0].shape) != (E, d, m // 2):
+        raise ValueError("the expert weights' shapes do not fit x and each other")
+    return M, d, m, E
+
+
+def w4_moe_layer_few(x, topk_ids, topk_weights, gu, dn, gu_group: int = 128, dn_group: int = 64,
+                     workspace=None, out=None, dev_status=None, stream=None):
+    """The whole routed-expert layer for a few tokens (M <= 32, M k <= 256)
+    in two launches; arguments and result as w4_moe_layer."""
+    import torch
+    _require_cuda(x, topk_ids, topk_weights, *gu, *dn, workspace, out, dev_status)
+    M, d, m, E = _few_dims(x, gu, dn)
+    k = topk_ids.shape[1]
+    if workspace is None:
+        workspace = torch.empty(w4_moe_layer_few_workspace_size(M, d, m, E, k),
+                                dtype=torch.uint8, device=x.device)
+    if out is None:
+        out = torch.empty((M, d), dtype=torch.bfloat16, device=x.device)
+    _check(load_library().w4_moe_layer_few(
+        _ptr(x), _ptr(topk_ids), _ptr(topk_weights), M, d, m, E, k, _ptr(gu[0]), _ptr(gu[1]),
+        _ptr(gu[2]), gu_group, _ptr(dn[0]), _ptr(dn[1]), _ptr(dn[2]), dn_group, _ptr(workspace),
+        workspace.numel(), _ptr(out), _ptr(dev_status), _stream(stream)), "w4_moe_layer_few")
+    return out
+
+
+def w4_moe_layer_few_from_logits(x, logits, k: int, gu, dn, gu_group: int = 128,
+                                 dn_group: int = 64, workspace=None, out=None, ids=None,
+                                 weights=None, dev_status=None, stream=None):
+    """w4_moe_layer_few with the router in its first launch: from the logits
+    [M, E] fp32.  Returns (out, topk_ids, topk_weights)."""
+    import torch
+    _require_cuda(x, logits, *gu, *dn, workspace, out, ids, weights, dev_status)
+    M, d, m, E = _few_dims(x, gu, dn)
+    if workspace is None:
+        workspace = torch.empty(w4_moe_layer_few_workspace_size(M, d, m, E, k),
+                                dtype=torch.uint8, device=x.device)
+    if out is None:
+        out = torch.empty((M, d), dtype=torch.bfloat16, device=x.device)
+    if ids is None:
+        ids = torch.empty((M, k), dtype=torch.int32, device=x.device)
+    if weights is None:
+        weights = torch.empty((M, k), dtype=torch.float32, device=x.device)
+    _check(load_library().w4_moe_layer_few_from_logits(
+        _ptr(x), _ptr(logits), M, d, m, E, k, _ptr(gu[0]), _ptr(gu[1]), _ptr(gu[2]), gu_group,
+        _ptr(dn[0]), _ptr(dn[1]), _ptr(dn[2]), dn_group, _ptr(workspace), workspace.numel(),
+        _ptr(ids), _ptr(weights), _ptr(out), _ptr(dev_status), _stream(stream)),
+        "w4_moe_layer_few_from_logits")
     return out, ids, weights
 
 

@@ -738,6 +738,117 @@ int w4_moe_layer_from_logits(const uint16_t *x, const float *logits, int M, int 
 
 }  // extern "C"
 
+// ------------------------------------------------- the layer for a few tokens
+namespace {
+int check_few(const void *x, int M, int d, int m, int E, int k, const void *gu_q,
+              const void *gu_s, const void *gu_z, int gu_group, const void *dn_q,
+              const void *dn_s, const void *dn_z, int dn_group, const void *workspace,
+              size_t workspace_bytes, const void *ids, const void *w, const void *out)
+{
+    if (M < 0 || d <= 0 || m <= 0 || E <= 0 || k <= 0)
+        return fail(W4_ERR_INVALID_ARG, "sizes must be positive (M >= 0)");
+    if (!gu_q || !gu_s || !gu_z || !dn_q || !dn_s || !dn_z ||
+        (M > 0 && (!x || !ids || !w || !out)))
+        return fail(W4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (d % 128 || m % 64 || gu_group != 128 || dn_group != 64)
+        return fail(W4_ERR_UNSUPPORTED_SHAPE,
+                    "need d %% 128 == 0, m %% 64 == 0 and groups of 128 and 64 (d=%d, m=%d, "
+                    "groups %d and %d)", d, m, gu_group, dn_group);
+    if (E > 1024 || k > 32)
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "need E <= 1024 and k <= 32");
+    if (!w4::few_supported(M, d, m, k))
+        return fail(W4_ERR_UNSUPPORTED_SHAPE,
+                    "need M <= 32, M * k <= 256 and rows that fit shared memory (M=%d, k=%d, d=%d, "
+                    "m=%d)", M, k, d, m);
+    if (!aligned16(x) || !aligned16(gu_q) || !aligned16(gu_s) || !aligned16(gu_z) ||
+        !aligned16(dn_q) || !aligned16(dn_s) || !aligned16(dn_z) || !aligned16(out))
+        return fail(W4_ERR_MISALIGNED, "x, weights, scales, zeros and out must be 16-byte aligned");
+    if (!aligned4(ids) || !aligned4(w))
+        return fail(W4_ERR_MISALIGNED, "ids and weights must be 4-byte aligned");
+    const size_t need = w4_moe_layer_few_workspace_size(M, d, m, E, k);
+    if (M > 0 && (!workspace || workspace_bytes < need))
+        return fail(W4_ERR_WORKSPACE, "workspace needs %zu bytes", need);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return fail(W4_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+    return W4_OK;
+}
+
+int run_few(const uint16_t *x, const float *logits, int M, int d, int m, int E, int k,
+            const uint8_t *gu_q, const uint16_t *gu_s, const uint16_t *gu_z, const uint8_t *dn_q,
+            const uint16_t *dn_s, const uint16_t *dn_z, void *workspace, int32_t *ids, float *w,
+            uint16_t *out, int32_t *dev_status, w4_stream_t stream)
+{
+    if (M == 0)
+        return W4_OK;
+    if (int rc = check_device())
+        return rc;
+    w4::FewProblem p{};
+    p.x = x;
+    p.logits = logits;
+    p.ids = ids;
+    p.w = w;
+    p.gu_q = gu_q;
+    p.gu_s = gu_s;
+    p.gu_z = gu_z;
+    p.dn_q = dn_q;
+    p.dn_s = dn_s;
+    p.dn_z = dn_z;
+    p.h = static_cast<uint16_t *>(workspace);
+    p.out = out;
+    p.dev_status = dev_status;
+    p.M = M;
+    p.d = d;
+    p.m = m;
+    p.E = E;
+    p.k = k;
+    cudaError_t err = w4::launch_few(p, as_stream(stream));
+    return err == cudaSuccess ? W4_OK : cuda_fail(err, "few-token layer launch");
+}
+}  // namespace
+
+size_t w4_moe_layer_few_workspace_size(int M, int d, int m, int E, int k)
+{
+    if (M < 0 || d <= 0 || m <= 0 || E <= 0 || k <= 0)
+        return 0;
+    return (static_cast<size_t>(M) * k * m * 2 + 255) / 256 * 256;
+}
+
+int w4_moe_layer_few(const uint16_t *x, const int32_t *topk_ids, const float *topk_weights, int M,
+                     int d, int m, int E, int k, const uint8_t *gu_q, const uint16_t *gu_s,
+                     const uint16_t *gu_z, int gu_group, const uint8_t *dn_q, const uint16_t *dn_s,
+                     const uint16_t *dn_z, int dn_group, void *workspace, size_t workspace_bytes,
+                     uint16_t *out, int32_t *dev_status, w4_stream_t stream)
+{
+    if (int rc = check_few(x, M, d, m, E, k, gu_q, gu_s, gu_z, gu_group, dn_q, dn_s, dn_z, dn_group,
+                           workspace, workspace_bytes, topk_ids, topk_weights, out))
+        return rc;
+    // read only: without logits the kernels write neither
+    return run_few(x, nullptr, M, d, m, E, k, gu_q, gu_s, gu_z, dn_q, dn_s, dn_z, workspace,
+                   const_cast<int32_t *>(topk_ids), const_cast<float *>(topk_weights), out,
+                   dev_status, stream);
+}
+
+int w4_moe_layer_few_from_logits(const uint16_t *x, const float *logits, int M, int d, int m, int E,
+                                 int k, const uint8_t *gu_q, const uint16_t *gu_s,
+                                 const uint16_t *gu_z, int gu_group, const uint8_t *dn_q,
+                                 const uint16_t *dn_s, const uint16_t *dn_z, int dn_group,
+                                 void *workspace, size_t workspace_bytes, int32_t *topk_ids,
+                                 float *topk_weights, uint16_t *out, int32_t *dev_status,
+                                 w4_stream_t stream)
+{
+    if (int rc = check_few(x, M, d, m, E, k, gu_q, gu_s, gu_z, gu_group, dn_q, dn_s, dn_z, dn_group,
+                           workspace, workspace_bytes, topk_ids, topk_weights, out))
+        return rc;
+    if (M > 0 && !logits)
+        return fail(W4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (k > E)
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "need k <= E (k=%d, E=%d)", k, E);
+    if (!aligned4(logits))
+        return fail(W4_ERR_MISALIGNED, "logits must be 4-byte aligned");
+    return run_few(x, logits, M, d, m, E, k, gu_q, gu_s, gu_z, dn_q, dn_s, dn_z, workspace,
+                   topk_ids, topk_weights, out, dev_status, stream);
+}
+
 // ------------------------------------------------------------------ RMSNorm
 int w4_rmsnorm(const uint16_t *x, const uint16_t *weight, int M, int d, float eps, uint16_t *y,
                w4_stream_t stream)
