@@ -401,8 +401,8 @@ int w4_moe_layer_from_logits(const uint16_t *x, const float *logits, int M, int 
                              w4_stream_t stream);
 
 /* --------------------------------------------------------------------------
- * w4_moe_layer_few -- the whole routed-expert layer for a few tokens, in two
- * launches: M <= 32 tokens and M * k <= 256 assignments, where an expert sees
+ * w4_moe_layer_few -- the whole routed-expert layer for a few tokens, in one
+ * cooperative launch (a CTA per SM, grid barriers between its steps): M <= 32 tokens and M * k <= 256 assignments, where an expert sees
  * a handful of tokens and the layer is the stream of the touched experts'
  * packed weights.  Same inputs and output as w4_moe_layer; the result differs
  * from it in rounding only.  The packed codes enter the tensor cores as they
@@ -417,8 +417,8 @@ int w4_moe_layer_from_logits(const uint16_t *x, const float *logits, int M, int 
  *   workspace   at least w4_moe_layer_few_workspace_size(...) bytes, 256-byte
  *               aligned, contents need no initialisation
  * Requires d % 128 == 0, m % 64 == 0, gu_group == 128, dn_group == 64,
- * k <= 32, E <= 1024, and that two tasks' rows fit shared memory beside 8
- * tokens (d up to 6144, m up to 2560).  M = 0 does nothing.
+ * k <= 32, E <= 1024, and that 8 rows of activations fit shared memory beside
+ * the weights' stages (d up to 6144, m up to 2560).  M = 0 does nothing.
  * ------------------------------------------------------------------------ */
 size_t w4_moe_layer_few_workspace_size(int M, int d, int m, int E, int k);
 int w4_moe_layer_few(const uint16_t *x, const int32_t *topk_ids, const float *topk_weights,
@@ -428,8 +428,8 @@ int w4_moe_layer_few(const uint16_t *x, const int32_t *topk_ids, const float *to
                      void *workspace, size_t workspace_bytes, uint16_t *out,
                      int32_t *dev_status, w4_stream_t stream);
 
-/* w4_moe_layer_few_from_logits -- w4_moe_layer_few with the router in its
- * first launch: from the logits [M, E] fp32.  topk_ids and topk_weights are
+/* w4_moe_layer_few_from_logits -- w4_moe_layer_few with the router in
+ * its launch: from the logits [M, E] fp32.  topk_ids and topk_weights are
  * outputs, bit-identical to w4_moe_route's; out is bit-identical to
  * w4_moe_route followed by w4_moe_layer_few.  k <= E. */
 int w4_moe_layer_few_from_logits(const uint16_t *x, const float *logits, int M, int d, int m,

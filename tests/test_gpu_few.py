@@ -172,10 +172,10 @@ def test_refusals_without_launching():
     assert call(x=None) == 1 and call(ids=None) == 1 and call(q=None) == 1 and call(M=-1) == 1
     assert call(M=33) == 2 and call(M=32, k=9, E=16) == 2 and call(k=33, M=1, E=64) == 2
     assert call(d=200) == 2 and call(m=96) == 2 and call(gg=64) == 2 and call(dg=128) == 2
-    assert call(E=1025) == 2 and call(d=8192) == 2 and call(m=4096) == 2
+    assert call(E=1025) == 2 and call(d=9216) == 2 and call(m=9216) == 2
     assert call(x=odd) == 3 and call(out=odd) == 3 and call(q=P(0x10008)) == 3
     assert call(ids=P(0x10002)) == 3 and call(ws=P(0x10080)) == 3
-    assert call(ws=None) == 6 and call(nb=4 * 2 * 128 * 2 - 1) == 6
+    assert call(ws=None) == 6 and call(nb=4 * 2 * (128 * 2 + 256 * 4) - 1) == 6
     assert call(x=None, M=0, ws=None, nb=0, out=None, ids=None) == 0
     args = [fake, fake, 4, 256, 128, 8, 2, fake, fake, fake, 128, fake, fake, fake, 64, fake, big,
             fake, fake, fake, None, None]

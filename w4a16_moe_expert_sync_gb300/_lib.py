@@ -484,7 +484,7 @@ def _few_dims(x, gu, dn):
 def w4_moe_layer_few(x, topk_ids, topk_weights, gu, dn, gu_group: int = 128, dn_group: int = 64,
                      workspace=None, out=None, dev_status=None, stream=None):
     """The whole routed-expert layer for a few tokens (M <= 32, M k <= 256)
-    in two launches; arguments and result as w4_moe_layer."""
+    in one cooperative launch; arguments and result as w4_moe_layer."""
     import torch
     _require_cuda(x, topk_ids, topk_weights, *gu, *dn, workspace, out, dev_status)
     M, d, m, E = _few_dims(x, gu, dn)
@@ -504,7 +504,7 @@ def w4_moe_layer_few(x, topk_ids, topk_weights, gu, dn, gu_group: int = 128, dn_
 def w4_moe_layer_few_from_logits(x, logits, k: int, gu, dn, gu_group: int = 128,
                                  dn_group: int = 64, workspace=None, out=None, ids=None,
                                  weights=None, dev_status=None, stream=None):
-    """w4_moe_layer_few with the router in its first launch: from the logits
+    """w4_moe_layer_few with the router in its launch: from the logits
     [M, E] fp32.  Returns (out, topk_ids, topk_weights)."""
     import torch
     _require_cuda(x, logits, *gu, *dn, workspace, out, ids, weights, dev_status)

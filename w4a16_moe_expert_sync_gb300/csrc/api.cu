@@ -793,7 +793,7 @@ int run_few(const uint16_t *x, const float *logits, int M, int d, int m, int E, 
     p.dn_q = dn_q;
     p.dn_s = dn_s;
     p.dn_z = dn_z;
-    p.h = static_cast<uint16_t *>(workspace);
+    p.workspace = workspace;
     p.out = out;
     p.dev_status = dev_status;
     p.M = M;
@@ -810,7 +810,7 @@ size_t w4_moe_layer_few_workspace_size(int M, int d, int m, int E, int k)
 {
     if (M < 0 || d <= 0 || m <= 0 || E <= 0 || k <= 0)
         return 0;
-    return (static_cast<size_t>(M) * k * m * 2 + 255) / 256 * 256;
+    return w4::few_workspace_bytes(M, d, m, k);
 }
 
 int w4_moe_layer_few(const uint16_t *x, const int32_t *topk_ids, const float *topk_weights, int M,

@@ -1,6 +1,8 @@
-// few.cu -- the whole routed-expert layer for a few tokens, in two kernels:
-//   few_gate_up: (router,) jobs, h[a] = gelu_tanh(x_t . deq(Wg[e])^T) * (x_t . deq(Wu[e])^T)
-//   few_down:    out_t = sum_j w_j (h[t k + j] . deq(Wd[e_j])^T)
+// few.cu -- the whole routed-expert layer for a few tokens, in one kernel:
+//   gate_up: h[a] = gelu_tanh(x_t . deq(Wg[e])^T) * (x_t . deq(Wu[e])^T)
+//   down:    y[a] = h[a] . deq(Wd[e])^T
+//   combine: out_t = sum_j w_j y[t k + j], j in order
+// with a grid barrier between the steps (a cooperative launch, one CTA per SM).
 //
 // With a few tokens an expert sees one or two of them, so the layer is the
 // stream of the touched experts' packed weights and every weight is used
@@ -10,13 +12,22 @@
 // subnormal q 2^-24 (low nibble of a byte) or 16 q 2^-24 (high nibble), both
 // exact, and so is its product with an fp16 activation.  The group's scale
 // and zero are applied to the fp32 sums,
-//     sum_k s (q_k - z) x_k = s (2^24 (lo + hi / 16)) - s z sum_k x_k,
+//     sum_k s (q_k - z) x_k = s (2^24 (lo + hi / 16) - z sum_k x_k),
 // so no weight is rounded at all.  The contraction order inside a group is
 // free as long as codes and activations agree on it: a lane takes 8 codes at
 // a time as they lie in a word, and the activations are stored permuted.
 //
-// A job is one expert with up to 8 of its assignments (the MMA's columns).
+// A job is one expert with up to 8 of its assignments (the MMA's columns); a
+// task is a job's 16 weight rows of one MMA (gate_up: 8 gate rows and the 8 up
+// rows beside them, so g and u of an intermediate end in the same lane); a
+// unit is 256 codes of a task's 16 rows, one 2 KB TMA box.  A CTA takes an
+// equal contiguous share of the tasks and its warps equal shares of those
+// tasks' units, so the bytes are spread evenly from one token to 32; a task
+// that crosses warps is added up through shared memory, in warp order.  Every
+// warp streams its own units through a private ring.  The first units of down
+// are requested before the grid barrier that ends gate_up.
 #include <algorithm>
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include "../../include/w4moe.h"
@@ -32,30 +43,22 @@ constexpr int kCols = 8;          // tokens per job: the MMA's N
 constexpr int kMaxA = 256;        // assignments of a call
 constexpr int kMaxM = 32;
 
-// gate_up: 16 consumer warps in groups of four that share a task's
-// contraction, and one producer warp.
-constexpr int kGuGroups = 4, kGuSplit = 4;
-constexpr int kGuThreads = 32 * (kGuGroups * kGuSplit + 1);
-constexpr int kGuMaxSlots = 8;
-// down: every warp on its own
-constexpr int kDnWarps = 8, kDnThreads = 32 * kDnWarps, kDnMaxSlots = 2;
-constexpr int kDnRows = 16;
-
 struct FewArgs {
+    CUtensorMap gu_map;                // gu_q as [2 E][m][d/2] bytes, box 2 x 8 x 128
+    CUtensorMap dn_map;                // dn_q as [E][d][m/2] bytes, box 1 x 16 x 128
     const uint16_t *x;                 // [M, d] bf16
     const float *logits;               // [M, E], or NULL: ids and w are inputs
     int32_t *ids;                      // [M, k]
     float *w;                          // [M, k]
-    const uint8_t *gu_q, *dn_q;
     const uint16_t *gu_s, *gu_z, *dn_s, *dn_z;
-    uint16_t *h;                       // [M k, m] fp16, permuted
+    uint16_t *h;                       // [M k, m] fp16
+    float *y;                          // [M k, d] fp32
     uint16_t *out;                     // [M, d] bf16
     int32_t *dev_status;
     uint64_t wait_ns;
     int M, d, m, E, k;
-    int slots, slot_bytes, x_stride;   // gate_up's ring; bytes between columns of x
-    int dn_slots;                      // down's slots per warp
-    bool routed;                       // ids and w come from gate_up
+    int scale_bytes;                   // a warp's ring of scales
+    int cols;                          // activation columns that fit
 };
 
 // ------------------------------------------------------------------- jobs
@@ -69,14 +72,14 @@ struct Jobs {
 struct Shared {
     Jobs jobs;
     int heads[32];
+    int16_t col0[kMaxA];              // of a pass: each job's first column
     alignas(16) int ids[kMaxA];
     float w[kMaxA];
-    int abort_flag;
 };
 
 // The routing in shared memory: the router for every token (one warp per
-// token), or the caller's ids.  CTA 0 of gate_up also writes the router's
-// results out.
+// token), or the caller's ids.  CTA 0 also writes the router's results
+// out.
 __device__ void load_routing(const FewArgs &p, Shared &s, bool publish)
 {
     const int tid = threadIdx.x, A = p.M * p.k, nt = blockDim.x;
@@ -207,337 +210,474 @@ __device__ __forceinline__ uint16_t to_half_sat(float v)
     return __half_as_ushort(__float2half_rn(fabsf(v) > 65504.0f ? copysignf(65504.0f, v) : v));
 }
 
-// ---------------------------------------------------------------- gate_up
-// Tasks are (job, 8 intermediates): 8 gate rows and the 8 up rows beside
-// them make the MMA's 16 rows, so g and u of an intermediate end in the same
-// lane.  CTA c takes an equal contiguous share of the tasks; its producer
-// streams each task's rows (two contiguous blocks of 8 rows, and their
-// scales and zeros) through a ring of slots.
-__global__ void __launch_bounds__(kGuThreads, 1) few_gate_up_kernel(const __grid_constant__ FewArgs p)
+// ----------------------------------------------------------------- streams
+// One of the two contractions: gate_up (UP: groups of 128, rows r and m + r)
+// or down (groups of 64, rows r and r + 8).
+template <bool UP> struct Step {
+    static constexpr int kGroup = UP ? 128 : 64;
+    static constexpr int kWords = kGroup / 32;          // a lane's words of a row's group
+    static constexpr int kUnitGroups = 256 / kGroup;
+};
+
+constexpr int kUnitBytes = 2048;                        // 16 rows x 128 bytes
+
+__host__ __device__ constexpr int units_of(int K) { return (K + 255) / 256; }
+__host__ __device__ constexpr int scale_bufs(int depth, int K)
 {
-    extern __shared__ __align__(128) uint8_t dyn[];
-    __shared__ Shared s;
-    __shared__ __align__(8) uint64_t full[kGuMaxSlots], empty[kGuMaxSlots];
-    __shared__ float red[2][kGuGroups][kGuSplit][32][4];
+    return (depth + units_of(K) - 1) / units_of(K) + 1;
+}
+__host__ __device__ constexpr int col_stride(int K, int G)
+{
+    // fp16 values, then the fp32 sums of the groups; an odd multiple of 64 so
+    // that neighbouring columns' chunks fall in distinct banks
+    return (2 * K + 4 * G + 127) / 128 * 128 + 64;
+}
 
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int G = p.d / 128, A = p.M * p.k;
-    uint8_t *ring = dyn;
-    uint8_t *xbuf = ring + p.slots * p.slot_bytes;                       // 8 columns of x
-    float *xs = reinterpret_cast<float *>(xbuf + kCols * p.x_stride);    // [G][8] group sums
+// NW warps, each with a ring of DEPTH units.
+template <int NW, int DEPTH>
+struct Layer {
+    static constexpr int kRingBytes = DEPTH * kUnitBytes;
 
-    if (tid == 0) {
-        for (int i = 0; i < p.slots; i++) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], kGuSplit);
+    struct Mem {
+        alignas(8) uint64_t full[NW][DEPTH];
+        int abort_flag;
+        int head_task[NW];
+        alignas(16) float head[NW][32][4];
+    };
+
+    // A warp's place in its ring; it runs on through both steps.
+    struct Ring {
+        uint8_t *buf;
+        uint64_t *full;
+        int ask_stage, stage;
+        uint32_t phase;
+    };
+
+    // Requests unit `unit` of a task into the ring's next stage (and, with a
+    // task's first unit in this warp's share, the task's scales and zeros:
+    // 8 rows of them are 16 G contiguous bytes).  One lane.
+    template <bool UP>
+    static __device__ __forceinline__ void request(const FewArgs &p, const Shared &s, int task,
+                                                   int unit, bool first, uint8_t *stage,
+                                                   uint64_t *bar, uint8_t *scales)
+    {
+        const int K = UP ? p.d : p.m, G = K / Step<UP>::kGroup;
+        const int per_job = UP ? p.m / 8 : p.d / 16;
+        const int job = task / per_job, tile = task - job * per_job, e = s.jobs.expert[job];
+        mbar_arrive_expect_tx(bar, kUnitBytes + (first ? 64 * G : 0));
+        tma_load_3d(stage, UP ? &p.gu_map : &p.dn_map, unit * 128, tile * (UP ? 8 : 16),
+                    UP ? 2 * e : e, bar);
+        if (first) {
+            const uint16_t *sc = UP ? p.gu_s : p.dn_s, *zp = UP ? p.gu_z : p.dn_z;
+            const int64_t r0 = UP ? static_cast<int64_t>(e) * 2 * p.m + tile * 8
+                                  : static_cast<int64_t>(e) * p.d + tile * 16;
+            const int64_t r1 = UP ? r0 + p.m : r0 + 8;
+            bulk_load_nohint(scales, sc + r0 * G, 16 * G, bar);
+            bulk_load_nohint(scales + 16 * G, sc + r1 * G, 16 * G, bar);
+            bulk_load_nohint(scales + 32 * G, zp + r0 * G, 16 * G, bar);
+            bulk_load_nohint(scales + 48 * G, zp + r1 * G, 16 * G, bar);
         }
-        s.abort_flag = 0;
-        fence_mbar_init();
     }
-    pdl_wait();
-    pdl_trigger();
-    load_routing(p, s, blockIdx.x == 0);
-    build_jobs(s, A);
 
-    const int per_job = p.m / 8;
-    const int64_t total = static_cast<int64_t>(s.jobs.n) * per_job;
-    const int t0 = static_cast<int>(total * blockIdx.x / gridDim.x);
-    const int t1 = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
-    const int block = 4 * p.d;                 // bytes of 8 rows of codes
-    const int sblock = 16 * G;                 // bytes of 8 rows of scales
-
-    if (warp == kGuGroups * kGuSplit) {        // producer
-        if (lane == 0) {
-            int issued = 0;
-            for (int t = t0; t < t1; t++) {
-                const int i = t - t0, slot = i % p.slots;
-                if (i >= p.slots && !mbar_wait(&empty[slot], (i / p.slots - 1) & 1, &s.abort_flag,
-                                               p.dev_status, kDevPipelineTimeout, p.wait_ns))
-                    break;
-                const int e = s.jobs.expert[t / per_job];
-                const int64_t gate = (static_cast<int64_t>(e) * 2 * p.m + (t % per_job) * 8);
-                const int64_t up = gate + p.m;
-                uint8_t *dst = ring + slot * p.slot_bytes;
-                mbar_arrive_expect_tx(&full[slot], 2 * block + 4 * sblock);
-                bulk_load_nohint(dst, p.gu_q + gate * (p.d / 2), block, &full[slot]);
-                bulk_load_nohint(dst + block, p.gu_q + up * (p.d / 2), block, &full[slot]);
-                dst += 2 * block;
-                bulk_load_nohint(dst, p.gu_s + gate * G, sblock, &full[slot]);
-                bulk_load_nohint(dst + sblock, p.gu_s + up * G, sblock, &full[slot]);
-                bulk_load_nohint(dst + 2 * sblock, p.gu_z + gate * G, sblock, &full[slot]);
-                bulk_load_nohint(dst + 3 * sblock, p.gu_z + up * G, sblock, &full[slot]);
-                issued++;
+    // A finished task's sums: acc[0..1] weight row `row` (gate), acc[2..3]
+    // row + 8 (up) of columns 2 t4 and 2 t4 + 1.
+    template <bool UP>
+    static __device__ __forceinline__ void finish(const FewArgs &p, const Shared &s, int task,
+                                                  const float (&acc)[4], int row, int t4)
+    {
+        const int per_job = UP ? p.m / 8 : p.d / 16;
+        const int job = task / per_job, tile = task - job * per_job;
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+            if (2 * t4 + c >= s.jobs.count[job])
+                continue;
+            const int64_t a = s.jobs.a[job][2 * t4 + c];
+            if constexpr (UP) {
+                const float hv = gelu_tanh_f(acc[c]) * acc[2 + c];
+                if (!(fabsf(hv) <= 65504.0f) && p.dev_status)
+                    atomicOr(p.dev_status, kDevFp16Range);
+                p.h[a * p.m + tile * 8 + row] = to_half_sat(hv);
+            } else {
+                float *y = p.y + a * p.d + tile * 16 + row;
+                y[0] = acc[c];
+                y[8] = acc[2 + c];
             }
-            // the CTA may not end while a copy into its memory is in flight
-            for (int i = max(0, issued - p.slots); i < issued; i++)
-                mbar_wait(&full[i % p.slots], (i / p.slots) & 1, &s.abort_flag, p.dev_status,
-                          kDevPipelineTimeout, p.wait_ns);
         }
-        return;
     }
 
-    const int grp = warp / kGuSplit, part = warp % kGuSplit;
-    const int g = lane >> 2, t4 = lane & 3;
-    constexpr int kConsumers = 32 * kGuGroups * kGuSplit;
-    int it = 0;                                // this group's tasks so far
-    for (int seg = t0; seg < t1;) {            // the tasks of one job at a time
-        const int job = seg / per_job;
-        const int end = min(t1, (job + 1) * per_job);
-        const int n = s.jobs.count[job];
-        asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");   // xbuf is free
-        // x rows of the job in fp16, permuted: word w of lane t4's 32 codes of
-        // group gi at chunk (gi, w, t4); a warp takes one (column, group)
+    // Activations of the jobs [job0, job1): fp16 in the MMA's order and the
+    // groups' sums.  A warp takes one column's 128 elements at a time.
+    template <bool UP>
+    static __device__ __forceinline__ void stage_columns(const FewArgs &p, Shared &s, uint8_t *xbuf,
+                                                         int job0, int job1, int warp, int lane)
+    {
+        using T = Step<UP>;
+        const int K = UP ? p.d : p.m, stride = col_stride(K, K / T::kGroup);
+        const int blocks = (K + 127) / 128;
         bool range = false;
-        for (int c = warp; c < kCols * G; c += kGuGroups * kGuSplit) {
-            const int col = c / G, gi = c % G;
-            if (col >= n)
-                break;
-            const int tok = s.jobs.a[job][col] / p.k;
-            const uint2 v = *reinterpret_cast<const uint2 *>(
-                p.x + static_cast<int64_t>(tok) * p.d + gi * 128 + lane * 4);
-            float sum = 0.0f;
-            uint8_t *dst = xbuf + col * p.x_stride +
-                           ((gi * 4 + ((lane >> 1) & 3)) * 4 + (lane >> 3)) * 16;
+        for (int job = job0; job < job1; job++) {
+            const int n = s.jobs.count[job];
+            for (int c = warp; c < n * blocks; c += NW) {
+                const int col = c / blocks, el = (c - col * blocks) * 128 + lane * 4;
+                const bool in = el < K;
+                const int a = s.jobs.a[job][col];
+                uint8_t *xc = xbuf + (s.col0[job] + col) * stride;
+                const uint16_t *src = UP ? p.x + static_cast<int64_t>(a / p.k) * p.d
+                                         : p.h + static_cast<int64_t>(a) * p.m;
+                uint2 v = make_uint2(0, 0);
+                if (in)
+                    v = __ldcg(reinterpret_cast<const uint2 *>(src + el));
+                const int gi = el / T::kGroup, i8 = (el % T::kGroup) / 8;   // word in the group
+                uint16_t *dst = reinterpret_cast<uint16_t *>(
+                    xc + gi * T::kGroup * 2 + (i8 % T::kWords) * 64 + (i8 / T::kWords) * 16);
+                float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const uint32_t bits = i < 2 ? v.x : v.y;
-                const float f = __uint_as_float(i & 1 ? bits & 0xFFFF0000u : bits << 16);
-                range |= !(fabsf(f) <= 65504.0f);
-                const uint16_t hb = to_half_sat(f);
-                sum += __half2float(__ushort_as_half(hb));
-                reinterpret_cast<uint16_t *>(dst)[perm8((lane & 1) * 4 + i)] = hb;
+                for (int i = 0; i < 4; i++) {
+                    const uint32_t bits = i < 2 ? v.x : v.y;
+                    uint16_t hb = static_cast<uint16_t>(i & 1 ? bits >> 16 : bits);
+                    if constexpr (UP) {
+                        const float f = __uint_as_float(static_cast<uint32_t>(hb) << 16);
+                        range |= !(fabsf(f) <= 65504.0f);
+                        hb = to_half_sat(f);
+                    }
+                    sum += __half2float(__ushort_as_half(hb));
+                    if (in)
+                        dst[perm8((lane & 1) * 4 + i)] = hb;
+                }
+#pragma unroll
+                for (int o = T::kGroup / 8; o > 0; o >>= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (in && (lane & (T::kGroup / 4 - 1)) == 0)
+                    reinterpret_cast<float *>(xc + 2 * K)[gi] = sum;
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == 0)
-                xs[gi * kCols + col] = sum;
         }
         if (range && p.dev_status)
             atomicOr(p.dev_status, kDevFp16Range);
-        asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+    }
 
-        const uint8_t *xcol = xbuf + (g < n ? g : 0) * p.x_stride + t4 * 16;
-        for (int t = seg; t < end; t++) {
-            const int i = t - t0;
-            if (i % kGuGroups != grp)
-                continue;
-            const int slot = i % p.slots;
-            mbar_wait_warp(&full[slot], (i / p.slots) & 1, &s.abort_flag, p.dev_status,
-                           kDevPipelineTimeout, p.wait_ns);
-            const uint8_t *base = ring + slot * p.slot_bytes;
-            const uint8_t *c0 = base + g * (p.d / 2) + t4 * 16;
-            const uint16_t *sc = reinterpret_cast<const uint16_t *>(base + 2 * block) + g * G;
-            float acc[4] = {};
-            for (int gi = part; gi < G; gi += kGuSplit) {
-                const uint4 q0 = *reinterpret_cast<const uint4 *>(c0 + gi * 64);
-                const uint4 q1 = *reinterpret_cast<const uint4 *>(c0 + block + gi * 64);
-                const float s0 = half_bits(sc + gi), s1 = half_bits(sc + sblock / 2 + gi);
-                const float z0 = half_bits(sc + sblock + gi);
-                const float z1 = half_bits(sc + sblock / 2 * 3 + gi);
-                const float2 sum = *reinterpret_cast<const float2 *>(xs + gi * kCols + 2 * t4);
-                const uint4 *b = reinterpret_cast<const uint4 *>(xcol + gi * 256);
-                float lo[4] = {}, hi[4] = {};
-                mma_word(lo, hi, q0.x, q1.x, b[0]);
-                mma_word(lo, hi, q0.y, q1.y, b[4]);
-                mma_word(lo, hi, q0.z, q1.z, b[8]);
-                mma_word(lo, hi, q0.w, q1.w, b[12]);
-                acc[0] += s0 * fmaf(-z0, sum.x, kSub * fmaf(hi[0], 0.0625f, lo[0]));
-                acc[1] += s0 * fmaf(-z0, sum.y, kSub * fmaf(hi[1], 0.0625f, lo[1]));
-                acc[2] += s1 * fmaf(-z1, sum.x, kSub * fmaf(hi[2], 0.0625f, lo[2]));
-                acc[3] += s1 * fmaf(-z1, sum.y, kSub * fmaf(hi[3], 0.0625f, lo[3]));
+    // The CTA's share of a step.  `between` runs once, after the first
+    // requests are on their way and before the activations are read.
+    template <bool UP, class F>
+    static __device__ __forceinline__ void run(const FewArgs &p, Shared &s, Mem &mem, Ring &ring,
+                                               uint8_t *scales, uint8_t *xbuf, F between)
+    {
+        using T = Step<UP>;
+        const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+        const int K = UP ? p.d : p.m, G = K / T::kGroup, stride = col_stride(K, G);
+        const int per_task = units_of(K), nbuf = scale_bufs(DEPTH, K);
+        const int per_job = UP ? p.m / 8 : p.d / 16;
+        const int64_t total = static_cast<int64_t>(s.jobs.n) * per_job;
+        const int t0 = static_cast<int>(total * blockIdx.x / gridDim.x);
+        const int t1 = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
+        const int t4 = lane & 3, g = lane >> 2;
+        // The weight row of this lane's MMA row g: g with its bits reversed,
+        // so that the lanes of one shared-memory phase read distinct banks of
+        // the 128-byte-swizzled box (rows 0 4 | 2 6 | 1 5 | 3 7).
+        const int row = ((g & 1) << 2) | (g & 2) | (g >> 2);
+        const int code0 = UP ? row * 128 + ((t4 ^ row) * 16)
+                             : row * 128 + (((t4 >> 1) ^ row) * 16) + (t4 & 1) * 8;
+        bool first_pass = true;
+
+        for (int p0 = t0; p0 < t1 || first_pass;) {
+            // the jobs whose columns fit together (one pass, unless many
+            // tokens share few experts)
+            const int job0 = p0 / per_job;
+            int job1 = job0, cols = 0;
+            while (p0 < t1 && job1 * per_job < t1 && cols + s.jobs.count[job1] <= p.cols) {
+                if (threadIdx.x == 0)
+                    s.col0[job1] = static_cast<int16_t>(cols);
+                cols += s.jobs.count[job1++];
             }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&empty[slot]);
-            float(*r)[32][4] = red[it & 1][grp];
-            it++;
-            *reinterpret_cast<float4 *>(r[part][lane]) =
-                make_float4(acc[0], acc[1], acc[2], acc[3]);
-            asm volatile("bar.sync %0, %1;" ::"r"(2 + grp), "n"(32 * kGuSplit) : "memory");
-            const int o = part * 32 + lane;    // 64 outputs: (column, intermediate)
-            if (o < 64 && (o >> 3) < n) {
-                const int col = o >> 3, row = o & 7, src = row * 4 + (col >> 1);
-                float gv = 0.0f, uv = 0.0f;
-#pragma unroll
-                for (int q = 0; q < kGuSplit; q++) {
-                    gv += r[q][src][col & 1];
-                    uv += r[q][src][2 + (col & 1)];
+            const int p1 = min(t1, max(p0, job1 * per_job));
+            const int units = (p1 - p0) * per_task;
+            const int u0 = static_cast<int>(static_cast<int64_t>(units) * warp / NW);
+            const int u1 = static_cast<int>(static_cast<int64_t>(units) * (warp + 1) / NW);
+
+            int task = p0 + u0 / per_task, unit = u0 % per_task;
+            int rt = task, rb = unit, rn = 0, left = u1 - u0;      // next request
+            auto ask = [&]() {                 // one lane asks; all keep count
+                if (left > 0) {
+                    if (lane == 0)
+                        request<UP>(p, s, rt, rb, left == u1 - u0 || rb == 0,
+                                    ring.buf + ring.ask_stage * kUnitBytes,
+                                    ring.full + ring.ask_stage, scales + rn * 64 * G);
+                    left--;
+                    ring.ask_stage = ring.ask_stage + 1 == DEPTH ? 0 : ring.ask_stage + 1;
+                    if (++rb == per_task) {
+                        rb = 0;
+                        rt++;
+                        rn = rn + 1 == nbuf ? 0 : rn + 1;
+                    }
                 }
-                const float hv = gelu_tanh_f(gv) * uv;
-                if (!(fabsf(hv) <= 65504.0f) && p.dev_status)
-                    atomicOr(p.dev_status, kDevFp16Range);
-                // down's order: 8 intermediates to a chunk, chunk (group of 64, w, t4)
-                const int ch = t % per_job;
-                const int pos = (ch >> 3) * 64 + ((ch & 1) * 4 + ((ch >> 1) & 3)) * 8 + perm8(row);
-                p.h[static_cast<int64_t>(s.jobs.a[job][col]) * p.m + pos] = to_half_sat(hv);
-            }
-        }
-        seg = end;
-    }
-}
+            };
+            for (int i = 0; i < DEPTH; i++)
+                ask();
+            if (first_pass)
+                between();
+            first_pass = false;
+            __syncthreads();                   // col0; the columns are free
+            stage_columns<UP>(p, s, xbuf, job0, job1, warp, lane);
+            if (lane == 0)
+                mem.head_task[warp] = -1;
+            __syncthreads();
 
-// ------------------------------------------------------------------- down
-// CTA b owns output columns [16 b, 16 b + 16) of every token, so the combine
-// stays inside it: warps take the jobs in turn, each streaming the 16 weight
-// rows of its jobs through its own slots, and leave y[a][16] in shared
-// memory; then each token's terms are added in slot order.
-__global__ void __launch_bounds__(kDnThreads, 2) few_down_kernel(const __grid_constant__ FewArgs p)
-{
-    extern __shared__ __align__(128) uint8_t dyn[];
-    __shared__ Shared s;
-    __shared__ __align__(8) uint64_t full[kDnWarps][kDnMaxSlots];
-
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int G = p.m / 64, A = p.M * p.k;
-    const int block = 8 * p.m, sblock = 32 * G;          // 16 rows of codes, of scales
-    const int slot_bytes = block + 2 * sblock;
-    uint8_t *ring = dyn + warp * p.dn_slots * slot_bytes;
-    float *y = reinterpret_cast<float *>(dyn + kDnWarps * p.dn_slots * slot_bytes);   // [A][16]
-
-    if (tid == 0)
-        s.abort_flag = 0;
-    if (lane == 0) {
-        for (int i = 0; i < p.dn_slots; i++)
-            mbar_init(&full[warp][i], 1);
-        fence_mbar_init();
-    }
-    // A caller's routing and the weights are older than gate_up, which began
-    // only after its predecessors had ended: they may be read before this
-    // kernel waits for gate_up's h.
-    if (p.routed)
-        pdl_wait();
-    load_routing(p, s, false);
-    build_jobs(s, A);
-
-    const int nj = s.jobs.n;
-    auto issue = [&](int j, int slot) {
-        const int64_t row = static_cast<int64_t>(s.jobs.expert[j]) * p.d + blockIdx.x * kDnRows;
-        uint8_t *dst = ring + slot * slot_bytes;
-        uint64_t *bar = &full[warp][slot];
-        mbar_arrive_expect_tx(bar, slot_bytes);
-        bulk_load_nohint(dst, p.dn_q + row * (p.m / 2), block, bar);
-        bulk_load_nohint(dst + block, p.dn_s + row * G, sblock, bar);
-        bulk_load_nohint(dst + block + sblock, p.dn_z + row * G, sblock, bar);
-    };
-    if (lane == 0)
-        for (int i = 0; i < p.dn_slots; i++)
-            if (warp + i * kDnWarps < nj)
-                issue(warp + i * kDnWarps, i);
-    if (!p.routed)
-        pdl_wait();
-    pdl_trigger();
-
-    const int g = lane >> 2, t4 = lane & 3;
-    int it = 0;
-    for (int j = warp; j < nj; j += kDnWarps, it++) {
-        const int n = s.jobs.count[j], slot = it % p.dn_slots;
-        const uint8_t *hrow = reinterpret_cast<const uint8_t *>(
-                                  p.h + static_cast<int64_t>(s.jobs.a[j][g < n ? g : 0]) * p.m) +
-                              t4 * 16;
-        mbar_wait_warp(&full[warp][slot], (it / p.dn_slots) & 1, &s.abort_flag, p.dev_status,
-                       kDevPipelineTimeout, p.wait_ns);
-        const uint8_t *base = ring + slot * slot_bytes;
-        const uint8_t *c0 = base + g * (p.m / 2) + t4 * 8;
-        const uint16_t *sc = reinterpret_cast<const uint16_t *>(base + block) + g * G;
-        float acc[4] = {};
-#pragma unroll 4
-        for (int gi = 0; gi < G; gi++) {
-            const uint4 b0 = __ldcg(reinterpret_cast<const uint4 *>(hrow + gi * 128));
-            const uint4 b1 = __ldcg(reinterpret_cast<const uint4 *>(hrow + gi * 128 + 64));
-            const uint2 q0 = *reinterpret_cast<const uint2 *>(c0 + gi * 32);
-            const uint2 q1 = *reinterpret_cast<const uint2 *>(c0 + 4 * p.m + gi * 32);
-            const float s0 = half_bits(sc + gi), s1 = half_bits(sc + 8 * G + gi);
-            const float z0 = half_bits(sc + 16 * G + gi), z1 = half_bits(sc + 24 * G + gi);
-            float lo[4] = {}, hi[4] = {}, sum[4] = {};
-            mma_word(lo, hi, q0.x, q1.x, b0);
-            mma_word(lo, hi, q0.y, q1.y, b1);
-            constexpr uint32_t one = 0x3C003C00u;      // the sums of h, by rows of ones
-            mma16816(sum, one, one, one, one, b0.x, b0.y);
-            mma16816(sum, one, one, one, one, b0.z, b0.w);
-            mma16816(sum, one, one, one, one, b1.x, b1.y);
-            mma16816(sum, one, one, one, one, b1.z, b1.w);
-            acc[0] += s0 * fmaf(-z0, sum[0], kSub * fmaf(hi[0], 0.0625f, lo[0]));
-            acc[1] += s0 * fmaf(-z0, sum[1], kSub * fmaf(hi[1], 0.0625f, lo[1]));
-            acc[2] += s1 * fmaf(-z1, sum[0], kSub * fmaf(hi[2], 0.0625f, lo[2]));
-            acc[3] += s1 * fmaf(-z1, sum[1], kSub * fmaf(hi[3], 0.0625f, lo[3]));
-        }
-        __syncwarp();
-        if (lane == 0 && j + p.dn_slots * kDnWarps < nj)
-            issue(j + p.dn_slots * kDnWarps, slot);
+            int sn = 0;
+            bool begun = unit == 0;            // this warp holds the task's first unit
+            float acc[4] = {};
+            for (int u = u0; u < u1;) {
+                const int job = task / per_job, n = s.jobs.count[job];
+                const uint8_t *xj = xbuf + s.col0[job] * stride;
+                const uint8_t *xc = xj + (g < n ? g : 0) * stride + t4 * 16 + unit * 512;
+                const int first_group = unit * T::kUnitGroups;
+                const float *sum0 = reinterpret_cast<const float *>(
+                    xj + (2 * t4 < n ? 2 * t4 : 0) * stride + 2 * K) + first_group;
+                const float *sum1 = reinterpret_cast<const float *>(
+                    xj + (2 * t4 + 1 < n ? 2 * t4 + 1 : 0) * stride + 2 * K) + first_group;
+                const uint16_t *sc = reinterpret_cast<const uint16_t *>(scales + sn * 64 * G) +
+                                     row * G + first_group;
+                const int end = min(per_task, unit + u1 - u);
+                u += end - unit;
+                int groups = G - first_group;              // left in the task
+                for (; unit < end; unit++) {
+                    mbar_wait_warp(ring.full + ring.stage, ring.phase, &mem.abort_flag,
+                                   p.dev_status, kDevPipelineTimeout, p.wait_ns);
+                    const uint8_t *st = ring.buf + ring.stage * kUnitBytes;
 #pragma unroll
-        for (int c = 0; c < 2; c++) {
-            if (2 * t4 + c < n) {
-                float *yr = y + s.jobs.a[j][2 * t4 + c] * kDnRows;
-                yr[g] = acc[c];
-                yr[g + 8] = acc[2 + c];
+                    for (int j = 0; j < T::kUnitGroups; j++) {
+                        if (j >= groups)
+                            break;
+                        uint32_t q0[T::kWords], q1[T::kWords];
+                        if constexpr (UP) {
+                            const uint8_t *c = st + (code0 ^ (64 * j));
+                            *reinterpret_cast<uint4 *>(q0) = *reinterpret_cast<const uint4 *>(c);
+                            *reinterpret_cast<uint4 *>(q1) =
+                                *reinterpret_cast<const uint4 *>(c + 1024);
+                        } else {
+                            const uint8_t *c = st + (code0 ^ (32 * j));
+                            *reinterpret_cast<uint2 *>(q0) = *reinterpret_cast<const uint2 *>(c);
+                            *reinterpret_cast<uint2 *>(q1) =
+                                *reinterpret_cast<const uint2 *>(c + 1024);
+                        }
+                        const uint4 *b = reinterpret_cast<const uint4 *>(xc + j * T::kGroup * 2);
+                        float lo[4] = {}, hi[4] = {};
+#pragma unroll
+                        for (int w = 0; w < T::kWords; w++)
+                            mma_word(lo, hi, q0[w], q1[w], b[4 * w]);
+                        // acc += s 2^24 (lo + hi / 16 - 2^-24 z sum)
+                        const float s0 = half_bits(sc + j) * kSub;
+                        const float s1 = half_bits(sc + 8 * G + j) * kSub;
+                        const float z0 = half_bits(sc + 16 * G + j) * (-1.0f / kSub);
+                        const float z1 = half_bits(sc + 24 * G + j) * (-1.0f / kSub);
+                        const float a0 = sum0[j], a1 = sum1[j];
+                        acc[0] = fmaf(s0, fmaf(z0, a0, fmaf(hi[0], 0.0625f, lo[0])), acc[0]);
+                        acc[1] = fmaf(s0, fmaf(z0, a1, fmaf(hi[1], 0.0625f, lo[1])), acc[1]);
+                        acc[2] = fmaf(s1, fmaf(z1, a0, fmaf(hi[2], 0.0625f, lo[2])), acc[2]);
+                        acc[3] = fmaf(s1, fmaf(z1, a1, fmaf(hi[3], 0.0625f, lo[3])), acc[3]);
+                    }
+                    groups -= T::kUnitGroups;
+                    xc += 512;
+                    sum0 += T::kUnitGroups;
+                    sum1 += T::kUnitGroups;
+                    sc += T::kUnitGroups;
+                    if (++ring.stage == DEPTH) {
+                        ring.stage = 0;
+                        ring.phase ^= 1;
+                    }
+                    __syncwarp();
+                    ask();
+                }
+                if (unit == per_task) {
+                    if (begun)
+                        finish<UP>(p, s, task, acc, row, t4);
+                    else {                     // begun by an earlier warp
+                        *reinterpret_cast<float4 *>(mem.head[warp][lane]) =
+                            make_float4(acc[0], acc[1], acc[2], acc[3]);
+                        if (lane == 0)
+                            mem.head_task[warp] = task;
+                    }
+                    unit = 0;
+                    task++;
+                    begun = true;
+                    sn = sn + 1 == nbuf ? 0 : sn + 1;
+                    acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+                }
             }
+            const bool open = u0 < u1 && unit != 0;    // the last task goes on in a later warp
+            if (open && !begun) {                      // and began in an earlier one
+                *reinterpret_cast<float4 *>(mem.head[warp][lane]) =
+                    make_float4(acc[0], acc[1], acc[2], acc[3]);
+                if (lane == 0)
+                    mem.head_task[warp] = task;
+            }
+            __syncthreads();
+            if (open && begun) {
+                for (int w = warp + 1; w < NW; w++) {
+                    if (mem.head_task[w] == task) {
+                        const float4 v = *reinterpret_cast<const float4 *>(mem.head[w][lane]);
+                        acc[0] += v.x;
+                        acc[1] += v.y;
+                        acc[2] += v.z;
+                        acc[3] += v.w;
+                    }
+                }
+                finish<UP>(p, s, task, acc, row, t4);
+            }
+            if (p1 >= t1)
+                break;
+            __syncthreads();
+            p0 = p1;
         }
     }
-    __syncthreads();
-    for (int o = tid; o < p.M * kDnRows; o += kDnThreads) {
-        const int t = o / kDnRows, r = o % kDnRows;
-        float v = 0.0f;
-        for (int j = 0; j < p.k; j++) {
-            const int a = t * p.k + j;
-            if (s.ids[a] >= 0)
-                v = fmaf(s.w[a], y[a * kDnRows + r], v);
-        }
-        const uint32_t u = __float_as_uint(v);           // bf16, nearest even
-        const uint32_t b = v != v ? 0x7FFFu : (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-        p.out[static_cast<int64_t>(t) * p.d + blockIdx.x * kDnRows + r] = static_cast<uint16_t>(b);
-    }
-}
-
-struct FewPlan {
-    int slots, slot_bytes, x_stride;
-    int dn_slots;
-    size_t gu_smem, dn_smem;
 };
 
-// Shared memory of both kernels; false when the shape does not fit.
-bool few_plan(int M, int d, int m, int k, FewPlan *f)
+template <int NW, int DEPTH>
+__global__ void __launch_bounds__(32 * NW, 1) few_layer_kernel(const __grid_constant__ FewArgs p)
 {
-    constexpr int kDynMax = 227 * 1024 - 25 * 1024;      // beside the static arrays
-    f->slot_bytes = 8 * d + 64 * (d / 128);
-    f->x_stride = 2 * d + 64;            // + 64 B: the columns' chunks fall in distinct banks
-    const int fixed = kCols * f->x_stride + (d / 128) * kCols * 4;
-    f->slots = std::min(kGuMaxSlots, (kDynMax - fixed) / f->slot_bytes);
-    f->gu_smem = static_cast<size_t>(fixed) + static_cast<size_t>(f->slots) * f->slot_bytes;
-    // down: two slots per warp where two CTAs then still fit an SM, else one
-    const size_t dn_ring = static_cast<size_t>(kDnWarps) * (8 * m + 64 * (m / 64));
-    const size_t y = static_cast<size_t>(M) * k * kDnRows * 4;
-    f->dn_slots = 2 * dn_ring + y <= 104 * 1024 ? 2 : 1;
-    f->dn_smem = f->dn_slots * dn_ring + y;
-    return f->slots >= 2 && f->dn_smem <= kDynMax;
+    using L = Layer<NW, DEPTH>;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    __shared__ Shared s;
+    __shared__ typename L::Mem mem;
+    // the boxes' swizzle goes by address: 1024-byte aligned
+    uint8_t *dyn = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    const int warp = threadIdx.x >> 5;
+    typename L::Ring ring = {dyn + warp * L::kRingBytes, mem.full[warp], 0, 0, 0};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NW * DEPTH; i++)
+            mbar_init(&mem.full[0][0] + i, 1);
+        mem.abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&p.gu_map);
+        prefetch_tmap(&p.dn_map);
+    }
+    uint8_t *scales = dyn + NW * L::kRingBytes + warp * p.scale_bytes;
+    uint8_t *xbuf = dyn + NW * (L::kRingBytes + p.scale_bytes);
+    auto grid = cooperative_groups::this_grid();
+
+    load_routing(p, s, blockIdx.x == 0);
+    build_jobs(s, p.M * p.k);
+    L::template run<true>(p, s, mem, ring, scales, xbuf, [] {});
+    L::template run<false>(p, s, mem, ring, scales, xbuf, [&] { grid.sync(); });
+    grid.sync();
+    const int d4 = p.d / 4;
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < p.M * d4; i += gridDim.x * blockDim.x) {
+        const int t = i / d4, c = (i - t * d4) * 4;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int j = 0; j < p.k; j++) {
+            const int a = t * p.k + j;
+            if (s.ids[a] < 0)
+                continue;
+            const float4 y = __ldcg(reinterpret_cast<const float4 *>(
+                p.y + static_cast<int64_t>(a) * p.d + c));
+            const float w = s.w[a];
+            v.x = fmaf(w, y.x, v.x);
+            v.y = fmaf(w, y.y, v.y);
+            v.z = fmaf(w, y.z, v.z);
+            v.w = fmaf(w, y.w, v.w);
+        }
+        uint2 o;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.x) : "f"(v.y), "f"(v.x));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.y) : "f"(v.w), "f"(v.z));
+        *reinterpret_cast<uint2 *>(p.out + static_cast<int64_t>(t) * p.d + c) = o;
+    }
 }
+
+// Shared memory of a variant for a shape: the scales' rings and the columns
+// that fit beside them.  Needs room for one full job.
+template <int NW, int DEPTH>
+bool plan(int d, int m, int *scale_bytes, int *cols, size_t *smem)
+{
+    const int Gu = d / 128, Gd = m / 64;
+    *scale_bytes = 64 * std::max(scale_bufs(DEPTH, d) * Gu, scale_bufs(DEPTH, m) * Gd);
+    // the static arrays, up to the dynamic part's alignment
+    const int stat =
+        (sizeof(Shared) + sizeof(typename Layer<NW, DEPTH>::Mem) + 64 + 1023) / 1024 * 1024;
+    const int rings = 1024 + NW * (DEPTH * kUnitBytes + *scale_bytes);
+    const int room = 227 * 1024 - stat - rings;
+    const int stride = std::max(col_stride(d, Gu), col_stride(m, Gd));
+    *cols = room < 0 ? 0 : std::min(room / stride, kMaxA);
+    *smem = static_cast<size_t>(rings) + static_cast<size_t>(*cols) * stride;
+    return *cols >= kCols;
+}
+
+template <int NW, int DEPTH>
+cudaError_t launch_variant(FewArgs a, int sms, cudaStream_t stream)
+{
+    size_t smem;
+    if (!plan<NW, DEPTH>(a.d, a.m, &a.scale_bytes, &a.cols, &smem))
+        return cudaErrorInvalidValue;
+    auto kern = few_layer_kernel<NW, DEPTH>;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           static_cast<int>(smem));
+    if (err != cudaSuccess)
+        return err;
+    void *args[] = {&a};
+    return cudaLaunchCooperativeKernel(kern, dim3(sms), dim3(32 * NW), args, smem, stream);
+}
+
+// Sixteen warps with three units each in flight where the scales' rings and a
+// job's columns leave room for it, else eight warps.
+bool wide_fits(int d, int m)
+{
+    int sb, cols;
+    size_t smem;
+    return plan<16, 3>(d, m, &sb, &cols, &smem);
+}
+
+using EncodeFn = decltype(&cuTensorMapEncodeTiled);
+
+EncodeFn encode_fn()
+{
+    static EncodeFn fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                             cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<EncodeFn>(ptr);
+    }();
+    return fn;
+}
+
+// Packed rows as [outer][rows][row_bytes], boxes of 128 bytes x 16 rows in
+// all, 128-byte swizzle; what lies past a row's end reads as zero.
+bool encode_rows(CUtensorMap *map, const uint8_t *base, int row_bytes, int rows, int outer,
+                 int box_rows, int box_outer)
+{
+    const cuuint64_t dim[3] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows),
+                               static_cast<cuuint64_t>(outer)};
+    const cuuint64_t stride[2] = {dim[0], dim[0] * dim[1]};
+    const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows),
+                               static_cast<cuuint32_t>(box_outer)};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(base), dim,
+                       stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t h_bytes(int M, int m, int k) { return (static_cast<size_t>(M) * k * m * 2 + 255) / 256 * 256; }
 
 }  // namespace
 
 bool few_supported(int M, int d, int m, int k)
 {
-    FewPlan f;
-    return M <= kMaxM && M * k <= kMaxA && few_plan(M, d, m, k, &f);
+    int sb, cols;
+    size_t smem;
+    return M <= kMaxM && M * k <= kMaxA && (wide_fits(d, m) || plan<8, 3>(d, m, &sb, &cols, &smem));
+}
+
+size_t few_workspace_bytes(int M, int d, int m, int k)
+{
+    return h_bytes(M, m, k) + static_cast<size_t>(M) * k * d * 4;
 }
 
 cudaError_t launch_few(const FewProblem &q, cudaStream_t stream)
 {
-    FewPlan f;
-    if (!few_plan(q.M, q.d, q.m, q.k, &f))
-        return cudaErrorInvalidValue;
     int dev = 0, sms = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err == cudaSuccess)
         err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (err != cudaSuccess)
-        return err;
-    err = cudaFuncSetAttribute(few_gate_up_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(f.gu_smem));
-    if (err == cudaSuccess)
-        err = cudaFuncSetAttribute(few_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   static_cast<int>(f.dn_smem));
     if (err != cudaSuccess)
         return err;
     FewArgs a{};
@@ -545,13 +685,12 @@ cudaError_t launch_few(const FewProblem &q, cudaStream_t stream)
     a.logits = q.logits;
     a.ids = q.ids;
     a.w = q.w;
-    a.gu_q = q.gu_q;
     a.gu_s = q.gu_s;
     a.gu_z = q.gu_z;
-    a.dn_q = q.dn_q;
     a.dn_s = q.dn_s;
     a.dn_z = q.dn_z;
-    a.h = q.h;
+    a.h = static_cast<uint16_t *>(q.workspace);
+    a.y = reinterpret_cast<float *>(static_cast<uint8_t *>(q.workspace) + h_bytes(q.M, q.m, q.k));
     a.out = q.out;
     a.dev_status = q.dev_status;
     a.wait_ns = pipeline_test_hooks().wait_ns;
@@ -560,16 +699,13 @@ cudaError_t launch_few(const FewProblem &q, cudaStream_t stream)
     a.m = q.m;
     a.E = q.E;
     a.k = q.k;
-    a.slots = f.slots;
-    a.slot_bytes = f.slot_bytes;
-    a.x_stride = f.x_stride;
-    a.dn_slots = f.dn_slots;
-    err = launch_pdl(few_gate_up_kernel, dim3(sms), dim3(kGuThreads), f.gu_smem, stream, a);
-    if (err != cudaSuccess)
-        return err;
-    a.routed = a.logits != nullptr;
-    a.logits = nullptr;
-    return launch_pdl(few_down_kernel, dim3(q.d / kDnRows), dim3(kDnThreads), f.dn_smem, stream, a);
+    if (!encode_fn())
+        return cudaErrorNotSupported;
+    if (!encode_rows(&a.gu_map, q.gu_q, q.d / 2, q.m, 2 * q.E, 8, 2) ||
+        !encode_rows(&a.dn_map, q.dn_q, q.m / 2, q.d, q.E, 16, 1))
+        return cudaErrorInvalidValue;
+    return wide_fits(q.d, q.m) ? launch_variant<16, 3>(a, sms, stream)
+                               : launch_variant<8, 3>(a, sms, stream);
 }
 
 }  // namespace w4

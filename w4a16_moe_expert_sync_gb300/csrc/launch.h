@@ -140,7 +140,7 @@ bool grouped_gemm_fits(bool gate_up, int K, int group, int E);
 cudaError_t launch_grouped_gemm(const GroupedGemmProblem &p, cudaStream_t stream,
                                 const char **why);
 
-// The whole layer for a few tokens (few.cu), two launches.  logits NULL: ids
+// The whole layer for a few tokens (few.cu), one cooperative launch.  logits NULL: ids
 // and w are inputs, else outputs.
 struct FewProblem {
     const uint16_t *x;          // [M, d] bf16
@@ -149,12 +149,13 @@ struct FewProblem {
     float *w;                   // [M, k]
     const uint8_t *gu_q, *dn_q;
     const uint16_t *gu_s, *gu_z, *dn_s, *dn_z;
-    uint16_t *h;                // workspace: [M k, m] fp16
+    void *workspace;            // few_workspace_bytes: h fp16, y fp32
     uint16_t *out;              // [M, d] bf16
     int32_t *dev_status;
     int M, d, m, E, k;
 };
 bool few_supported(int M, int d, int m, int k);
+size_t few_workspace_bytes(int M, int d, int m, int k);
 cudaError_t launch_few(const FewProblem &p, cudaStream_t stream);
 
 // W4_OK when the current device is an sm_103 part, else W4_ERR_NO_DEVICE or
