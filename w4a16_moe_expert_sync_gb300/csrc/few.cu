@@ -33,7 +33,6 @@
 #include "../../include/w4moe.h"
 #include "launch.h"
 #include "ptx.cuh"
-#include "route_token.cuh"
 
 namespace w4 {
 
@@ -56,114 +55,170 @@ struct FewArgs {
     uint16_t *out;                     // [M, d] bf16
     int32_t *dev_status;
     uint64_t wait_ns;
-    int M, d, m, E, k;
+    int M, d, m, E, k;                 // M <= the grid
     int scale_bytes;                   // a warp's ring of scales
     int cols;                          // activation columns that fit
 };
 
 // ------------------------------------------------------------------- jobs
-struct Jobs {
-    int n;
+constexpr int kMaxE = 1024;
+constexpr int kChunks = kMaxA / 32;
+// An expert's assignments among each 32; lives where the activations' columns
+// come later.
+using Seen = uint8_t[kChunks][kMaxE];
+
+struct Shared {
+    int n;                             // jobs
+    int warp_sum[32];
     int16_t expert[kMaxA];
     int16_t count[kMaxA];
     int16_t a[kMaxA][kCols];
+    int16_t col0[kMaxA];               // of a pass: each job's first column
+    int16_t base[kMaxE];               // an expert's first job
+    alignas(16) int ids[kMaxA];
 };
 
-struct Shared {
-    Jobs jobs;
-    int heads[32];
-    int16_t col0[kMaxA];              // of a pass: each job's first column
-    alignas(16) int ids[kMaxA];
-    float w[kMaxA];
-};
+// The k experts of one token by one warp, ties to the lower index: the same
+// ids as route_token's (for logits that are not NaN).  Floats are compared as
+// integers in the same order, a round is two warp reductions.  Lane j < k
+// returns the j-th choice.
+template <int EPL>
+__device__ __forceinline__ int top_experts(const float *__restrict__ row, int E, int k, int lane)
+{
+    uint32_t key[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; i++) {
+        const int e = lane + 32 * i;
+        const uint32_t u = e < E ? __float_as_uint(__ldg(row + e) + 0.0f) : 0u;   // -0 -> +0
+        key[i] = e < E ? (u & 0x80000000u ? ~u : u | 0x80000000u) : 0u;
+    }
+    int mine = -1;
+    for (int j = 0; j < k; j++) {
+        uint32_t best = key[0];
+        int at = 0;
+#pragma unroll
+        for (int i = 1; i < EPL; i++)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        const int e = __reduce_min_sync(0xffffffffu, best == top ? lane + 32 * at : 0x7fffffff);
+#pragma unroll
+        for (int i = 0; i < EPL; i++)
+            if (lane + 32 * i == e)
+                key[i] = 0;
+        if (lane == j)
+            mine = e;
+    }
+    return mine;
+}
 
 // The routing in shared memory: the router for every token (one warp per
-// token), or the caller's ids.  CTA 0 also writes the router's results
-// out.
-__device__ void load_routing(const FewArgs &p, Shared &s, bool publish)
+// token), or the caller's ids.
+__device__ void load_routing(const FewArgs &p, Shared &s, Seen &seen)
 {
     const int tid = threadIdx.x, A = p.M * p.k, nt = blockDim.x;
+    for (int i = tid; i < kChunks * kMaxE / 16; i += nt)
+        reinterpret_cast<int4 *>(seen)[i] = make_int4(0, 0, 0, 0);
     if (p.logits) {
         const int lane = tid & 31;
         for (int t = tid >> 5; t < p.M; t += nt >> 5) {
-            int id;
-            float w;
             const float *row = p.logits + static_cast<int64_t>(t) * p.E;
-            if (p.E <= 128)
-                route_token<4>(row, p.E, p.k, lane, &id, &w);
-            else
-                route_token<32>(row, p.E, p.k, lane, &id, &w);
-            if (lane < p.k) {
-                s.ids[t * p.k + lane] = id;
-                s.w[t * p.k + lane] = w;
-                if (publish) {
-                    p.ids[t * p.k + lane] = id;
-                    p.w[t * p.k + lane] = w;
-                }
-            }
+            const int e = p.E <= 128 ? top_experts<4>(row, p.E, p.k, lane)
+                                     : top_experts<32>(row, p.E, p.k, lane);
+            if (lane < p.k)
+                s.ids[t * p.k + lane] = e;
         }
     } else {
         for (int a = tid; a < A; a += nt) {
             const int e = p.ids[a];
             const bool ok = e >= 0 && e < p.E;
             s.ids[a] = ok ? e : -1;
-            s.w[a] = p.w[a];
-            if (!ok && publish && p.dev_status)
+            if (!ok && blockIdx.x == 0 && p.dev_status)
                 atomicOr(p.dev_status, kDevBadExpertId);
         }
     }
-    for (int a = A + tid; a < ((A + 3) & ~3); a += nt)
-        s.ids[a] = -2;
     __syncthreads();
 }
 
-// Assignments grouped into jobs, every CTA for itself: assignment a opens a
-// job when the number of earlier assignments to its expert is a multiple of
-// 8, and the job holds it and the next seven.  Jobs are numbered in order of
-// their first assignment.
-__device__ void build_jobs(Shared &s, int A)
+// The router's results of token t, by one warp: its ids and their weights
+// with route_token's arithmetic (float64, summed in slot order).
+__device__ void publish_routing(const FewArgs &p, const Shared &s, int t, int lane)
+{
+    const int e = lane < p.k ? s.ids[t * p.k + lane] : 0;
+    const float v = lane < p.k ? __ldg(p.logits + static_cast<int64_t>(t) * p.E + e) : 0.0f;
+    const float top = __shfl_sync(0xffffffffu, v, 0);
+    const double ex =
+        lane < p.k ? exp(static_cast<double>(v) - static_cast<double>(top)) : 0.0;
+    double sum = 0.0;
+    for (int j = 0; j < p.k; j++)
+        sum += __shfl_sync(0xffffffffu, ex, j);
+    if (lane < p.k) {
+        p.ids[t * p.k + lane] = e;
+        p.w[t * p.k + lane] = static_cast<float>(ex / sum);
+    }
+}
+
+// Assignments grouped into jobs, every CTA for itself and all alike: jobs in
+// the order of their experts, an expert's assignments in order, 8 to a job.
+// An assignment's rank among its expert's is the number of earlier lanes of
+// its 32 with the same expert, plus the counts of the earlier 32s.
+__device__ void build_jobs(Shared &s, Seen &seen, int A, int E)
 {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
-    int base = 0;
-    for (int a0 = 0; a0 < A; a0 += nt) {
-        const int a = a0 + tid;
-        bool head = false;
-        int e = -1;
-        if (a < A) {
-            e = s.ids[a];
-            int rank = 0;
-            const int4 *v = reinterpret_cast<const int4 *>(s.ids);
-            for (int i = 0; i < a; i += 4) {
-                const int4 q = v[i >> 2];
-                rank += (q.x == e) + (q.y == e && i + 1 < a) + (q.z == e && i + 2 < a) +
-                        (q.w == e && i + 3 < a);
-            }
-            head = e >= 0 && rank % kCols == 0;
-        }
-        const unsigned bal = __ballot_sync(0xffffffffu, head);
-        if (lane == 0)
-            s.heads[warp] = __popc(bal);
-        __syncthreads();
-        int before = base + __popc(bal & ((1u << lane) - 1u)), total = base;
-        for (int i = 0; i < nt >> 5; i++) {
-            before += i < warp ? s.heads[i] : 0;
-            total += s.heads[i];
-        }
-        if (head) {
-            s.jobs.expert[before] = static_cast<int16_t>(e);
-            int n = 0;
-            for (int i = a; i < A && n < kCols; i++)
-                if (s.ids[i] == e)
-                    s.jobs.a[before][n++] = static_cast<int16_t>(i);
-            s.jobs.count[before] = static_cast<int16_t>(n);
-            for (int i = n; i < kCols; i++)       // unused columns repeat the first
-                s.jobs.a[before][i] = static_cast<int16_t>(a);
-        }
-        base = total;
-        __syncthreads();
+    const int chunks = (A + 31) / 32;
+    for (int c = warp; c < chunks; c += nt >> 5) {
+        const int a = c * 32 + lane, e = a < A ? s.ids[a] : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        if (e >= 0 && lane == __ffs(same) - 1)
+            seen[c][e] = static_cast<uint8_t>(__popc(same));
     }
-    if (tid == 0)
-        s.jobs.n = base;
+    __syncthreads();
+    // exclusive scan of the experts' job counts, a run of experts per thread
+    const int run = (E + nt - 1) / nt, e0 = min(E, tid * run), e1 = min(E, e0 + run);
+    int mine = 0;
+    for (int e = e0; e < e1; e++) {
+        int n = 0;
+        for (int c = 0; c < chunks; c++)
+            n += seen[c][e];
+        mine += (n + kCols - 1) / kCols;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        incl += lane >= o ? v : 0;
+    }
+    if (lane == 31)
+        s.warp_sum[warp] = incl;
+    __syncthreads();
+    int job = incl - mine;
+    for (int w = 0; w < warp; w++)
+        job += s.warp_sum[w];
+    if (tid == nt - 1)
+        s.n = job + mine;
+    for (int e = e0; e < e1; e++) {
+        int n = 0;
+        for (int c = 0; c < chunks; c++)
+            n += seen[c][e];
+        s.base[e] = static_cast<int16_t>(job);
+        for (; n > 0; n -= kCols, job++) {
+            s.expert[job] = static_cast<int16_t>(e);
+            s.count[job] = static_cast<int16_t>(min(n, kCols));
+        }
+    }
+    __syncthreads();
+    for (int c = warp; c < chunks; c += nt >> 5) {
+        const int a = c * 32 + lane, e = a < A ? s.ids[a] : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        if (e >= 0) {
+            int rank = __popc(same & ((1u << lane) - 1u));
+            for (int i = 0; i < c; i++)
+                rank += seen[i][e];
+            s.a[s.base[e] + rank / kCols][rank % kCols] = static_cast<int16_t>(a);
+        }
+    }
     __syncthreads();
 }
 
@@ -257,13 +312,11 @@ struct Layer {
     // task's first unit in this warp's share, the task's scales and zeros:
     // 8 rows of them are 16 G contiguous bytes).  One lane.
     template <bool UP>
-    static __device__ __forceinline__ void request(const FewArgs &p, const Shared &s, int task,
-                                                   int unit, bool first, uint8_t *stage,
-                                                   uint64_t *bar, uint8_t *scales)
+    static __device__ __forceinline__ void request(const FewArgs &p, int e, int tile, int unit,
+                                                   bool first, uint8_t *stage, uint64_t *bar,
+                                                   uint8_t *scales)
     {
         const int K = UP ? p.d : p.m, G = K / Step<UP>::kGroup;
-        const int per_job = UP ? p.m / 8 : p.d / 16;
-        const int job = task / per_job, tile = task - job * per_job, e = s.jobs.expert[job];
         mbar_arrive_expect_tx(bar, kUnitBytes + (first ? 64 * G : 0));
         tma_load_3d(stage, UP ? &p.gu_map : &p.dn_map, unit * 128, tile * (UP ? 8 : 16),
                     UP ? 2 * e : e, bar);
@@ -279,7 +332,7 @@ struct Layer {
         }
     }
 
-    // A finished task's sums: acc[0..1] weight row `row` (gate), acc[2..3]
+    // A finished task's sums, times 2^-24: acc[0..1] weight row `row` (gate), acc[2..3]
     // row + 8 (up) of columns 2 t4 and 2 t4 + 1.
     template <bool UP>
     static __device__ __forceinline__ void finish(const FewArgs &p, const Shared &s, int task,
@@ -289,24 +342,25 @@ struct Layer {
         const int job = task / per_job, tile = task - job * per_job;
 #pragma unroll
         for (int c = 0; c < 2; c++) {
-            if (2 * t4 + c >= s.jobs.count[job])
+            if (2 * t4 + c >= s.count[job])
                 continue;
-            const int64_t a = s.jobs.a[job][2 * t4 + c];
+            const int64_t a = s.a[job][2 * t4 + c];
             if constexpr (UP) {
-                const float hv = gelu_tanh_f(acc[c]) * acc[2 + c];
+                const float hv = gelu_tanh_f(acc[c] * kSub) * (acc[2 + c] * kSub);
                 if (!(fabsf(hv) <= 65504.0f) && p.dev_status)
                     atomicOr(p.dev_status, kDevFp16Range);
                 p.h[a * p.m + tile * 8 + row] = to_half_sat(hv);
             } else {
                 float *y = p.y + a * p.d + tile * 16 + row;
-                y[0] = acc[c];
-                y[8] = acc[2 + c];
+                y[0] = acc[c] * kSub;
+                y[8] = acc[2 + c] * kSub;
             }
         }
     }
 
     // Activations of the jobs [job0, job1): fp16 in the MMA's order and the
-    // groups' sums.  A warp takes one column's 128 elements at a time.
+    // groups' sums, times -2^-24.  A warp takes one column's 128 elements at a
+    // time.
     template <bool UP>
     static __device__ __forceinline__ void stage_columns(const FewArgs &p, Shared &s, uint8_t *xbuf,
                                                          int job0, int job1, int warp, int lane)
@@ -316,11 +370,11 @@ struct Layer {
         const int blocks = (K + 127) / 128;
         bool range = false;
         for (int job = job0; job < job1; job++) {
-            const int n = s.jobs.count[job];
+            const int n = s.count[job];
             for (int c = warp; c < n * blocks; c += NW) {
                 const int col = c / blocks, el = (c - col * blocks) * 128 + lane * 4;
                 const bool in = el < K;
-                const int a = s.jobs.a[job][col];
+                const int a = s.a[job][col];
                 uint8_t *xc = xbuf + (s.col0[job] + col) * stride;
                 const uint16_t *src = UP ? p.x + static_cast<int64_t>(a / p.k) * p.d
                                          : p.h + static_cast<int64_t>(a) * p.m;
@@ -348,7 +402,7 @@ struct Layer {
                 for (int o = T::kGroup / 8; o > 0; o >>= 1)
                     sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 if (in && (lane & (T::kGroup / 4 - 1)) == 0)
-                    reinterpret_cast<float *>(xc + 2 * K)[gi] = sum;
+                    reinterpret_cast<float *>(xc + 2 * K)[gi] = -sum / kSub;
             }
         }
         if (range && p.dev_status)
@@ -366,7 +420,7 @@ struct Layer {
         const int K = UP ? p.d : p.m, G = K / T::kGroup, stride = col_stride(K, G);
         const int per_task = units_of(K), nbuf = scale_bufs(DEPTH, K);
         const int per_job = UP ? p.m / 8 : p.d / 16;
-        const int64_t total = static_cast<int64_t>(s.jobs.n) * per_job;
+        const int64_t total = static_cast<int64_t>(s.n) * per_job;
         const int t0 = static_cast<int>(total * blockIdx.x / gridDim.x);
         const int t1 = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
         const int t4 = lane & 3, g = lane >> 2;
@@ -383,10 +437,10 @@ struct Layer {
             // tokens share few experts)
             const int job0 = p0 / per_job;
             int job1 = job0, cols = 0;
-            while (p0 < t1 && job1 * per_job < t1 && cols + s.jobs.count[job1] <= p.cols) {
+            while (p0 < t1 && job1 * per_job < t1 && cols + s.count[job1] <= p.cols) {
                 if (threadIdx.x == 0)
                     s.col0[job1] = static_cast<int16_t>(cols);
-                cols += s.jobs.count[job1++];
+                cols += s.count[job1++];
             }
             const int p1 = min(t1, max(p0, job1 * per_job));
             const int units = (p1 - p0) * per_task;
@@ -394,22 +448,29 @@ struct Layer {
             const int u1 = static_cast<int>(static_cast<int64_t>(units) * (warp + 1) / NW);
 
             int task = p0 + u0 / per_task, unit = u0 % per_task;
-            int rt = task, rb = unit, rn = 0, left = u1 - u0;      // next request
+            // the next request: job, tile of its rows, unit, scale buffer
+            int rj = min(task / per_job, max(s.n - 1, 0)), rt = task - rj * per_job;
+            int rb = unit, rn = 0, left = u1 - u0;
+            int re = s.expert[rj];
             auto ask = [&]() {                 // one lane asks; all keep count
                 if (left > 0) {
                     if (lane == 0)
-                        request<UP>(p, s, rt, rb, left == u1 - u0 || rb == 0,
-                                    ring.buf + ring.ask_stage * kUnitBytes,
+                        request<UP>(p, re, rt, rb, left == u1 - u0 || rb == 0, ring.buf + ring.ask_stage * kUnitBytes,
                                     ring.full + ring.ask_stage, scales + rn * 64 * G);
                     left--;
                     ring.ask_stage = ring.ask_stage + 1 == DEPTH ? 0 : ring.ask_stage + 1;
                     if (++rb == per_task) {
                         rb = 0;
-                        rt++;
                         rn = rn + 1 == nbuf ? 0 : rn + 1;
+                        if (++rt == per_job) {
+                            rt = 0;
+                            rj = min(rj + 1, s.n - 1);
+                            re = s.expert[rj];
+                        }
                     }
                 }
             };
+#pragma unroll 1
             for (int i = 0; i < DEPTH; i++)
                 ask();
             if (first_pass)
@@ -425,7 +486,7 @@ struct Layer {
             bool begun = unit == 0;            // this warp holds the task's first unit
             float acc[4] = {};
             for (int u = u0; u < u1;) {
-                const int job = task / per_job, n = s.jobs.count[job];
+                const int job = task / per_job, n = s.count[job];
                 const uint8_t *xj = xbuf + s.col0[job] * stride;
                 const uint8_t *xc = xj + (g < n ? g : 0) * stride + t4 * 16 + unit * 512;
                 const int first_group = unit * T::kUnitGroups;
@@ -463,11 +524,9 @@ struct Layer {
 #pragma unroll
                         for (int w = 0; w < T::kWords; w++)
                             mma_word(lo, hi, q0[w], q1[w], b[4 * w]);
-                        // acc += s 2^24 (lo + hi / 16 - 2^-24 z sum)
-                        const float s0 = half_bits(sc + j) * kSub;
-                        const float s1 = half_bits(sc + 8 * G + j) * kSub;
-                        const float z0 = half_bits(sc + 16 * G + j) * (-1.0f / kSub);
-                        const float z1 = half_bits(sc + 24 * G + j) * (-1.0f / kSub);
+                        // 2^-24 of the sum: acc += s (lo + hi / 16 - z 2^-24 sum)
+                        const float s0 = half_bits(sc + j), s1 = half_bits(sc + 8 * G + j);
+                        const float z0 = half_bits(sc + 16 * G + j), z1 = half_bits(sc + 24 * G + j);
                         const float a0 = sum0[j], a1 = sum1[j];
                         acc[0] = fmaf(s0, fmaf(z0, a0, fmaf(hi[0], 0.0625f, lo[0])), acc[0]);
                         acc[1] = fmaf(s0, fmaf(z0, a1, fmaf(hi[1], 0.0625f, lo[1])), acc[1]);
@@ -553,9 +612,14 @@ __global__ void __launch_bounds__(32 * NW, 1) few_layer_kernel(const __grid_cons
     uint8_t *xbuf = dyn + NW * (L::kRingBytes + p.scale_bytes);
     auto grid = cooperative_groups::this_grid();
 
-    load_routing(p, s, blockIdx.x == 0);
-    build_jobs(s, p.M * p.k);
-    L::template run<true>(p, s, mem, ring, scales, xbuf, [] {});
+    Seen &seen = *reinterpret_cast<Seen *>(xbuf);
+    load_routing(p, s, seen);
+    build_jobs(s, seen, p.M * p.k, p.E);
+    L::template run<true>(p, s, mem, ring, scales, xbuf, [&] {
+        // the weights, which only the combine needs, while the first bytes are on their way
+        if (p.logits && blockIdx.x < p.M && warp == NW - 1)
+            publish_routing(p, s, blockIdx.x, threadIdx.x & 31);
+    });
     L::template run<false>(p, s, mem, ring, scales, xbuf, [&] { grid.sync(); });
     grid.sync();
     const int d4 = p.d / 4;
@@ -568,7 +632,7 @@ __global__ void __launch_bounds__(32 * NW, 1) few_layer_kernel(const __grid_cons
                 continue;
             const float4 y = __ldcg(reinterpret_cast<const float4 *>(
                 p.y + static_cast<int64_t>(a) * p.d + c));
-            const float w = s.w[a];
+            const float w = __ldcg(p.w + a);
             v.x = fmaf(w, y.x, v.x);
             v.y = fmaf(w, y.y, v.y);
             v.z = fmaf(w, y.z, v.z);
@@ -596,7 +660,7 @@ bool plan(int d, int m, int *scale_bytes, int *cols, size_t *smem)
     const int stride = std::max(col_stride(d, Gu), col_stride(m, Gd));
     *cols = room < 0 ? 0 : std::min(room / stride, kMaxA);
     *smem = static_cast<size_t>(rings) + static_cast<size_t>(*cols) * stride;
-    return *cols >= kCols;
+    return *cols >= kCols && *cols * stride >= static_cast<int>(sizeof(Seen));
 }
 
 template <int NW, int DEPTH>
