@@ -1,6 +1,7 @@
 // api.cu -- the extern "C" entry points declared in include/w4moe.h: argument
 // validation on the host, then kernel launches on the caller's stream.  No
 // device allocation, no synchronisation, no device-to-host reads.
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -46,12 +47,17 @@ int check_device()
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess)
         return cuda_fail(err, "cudaGetDevice");
+    static std::atomic<uint64_t> known{0};       // devices found to be sm_103
+    if (dev < 64 && (known.load(std::memory_order_relaxed) >> dev & 1u))
+        return W4_OK;
     int major = 0, minor = 0;
     cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
     cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
     if (major != 10 || minor != 3)
         return fail(W4_ERR_NO_DEVICE, "device %d is sm_%d%d; this library is built for sm_103a",
                     dev, major, minor);
+    if (dev < 64)
+        known.fetch_or(1ull << dev, std::memory_order_relaxed);
     return W4_OK;
 }
 

@@ -27,6 +27,7 @@
 // warp streams its own units through a private ring.  The first units of down
 // are requested before the grid barrier that ends gate_up.
 #include <algorithm>
+#include <atomic>
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
@@ -368,41 +369,53 @@ struct Layer {
         using T = Step<UP>;
         const int K = UP ? p.d : p.m, stride = col_stride(K, K / T::kGroup);
         const int blocks = (K + 127) / 128;
+        constexpr int kBatch = 4;              // loads in flight at a time
         bool range = false;
         for (int job = job0; job < job1; job++) {
-            const int n = s.count[job];
-            for (int c = warp; c < n * blocks; c += NW) {
-                const int col = c / blocks, el = (c - col * blocks) * 128 + lane * 4;
-                const bool in = el < K;
-                const int a = s.a[job][col];
-                uint8_t *xc = xbuf + (s.col0[job] + col) * stride;
-                const uint16_t *src = UP ? p.x + static_cast<int64_t>(a / p.k) * p.d
-                                         : p.h + static_cast<int64_t>(a) * p.m;
-                uint2 v = make_uint2(0, 0);
-                if (in)
-                    v = __ldcg(reinterpret_cast<const uint2 *>(src + el));
-                const int gi = el / T::kGroup, i8 = (el % T::kGroup) / 8;   // word in the group
-                uint16_t *dst = reinterpret_cast<uint16_t *>(
-                    xc + gi * T::kGroup * 2 + (i8 % T::kWords) * 64 + (i8 / T::kWords) * 16);
-                float sum = 0.0f;
+            const int items = s.count[job] * blocks;
+            for (int c0 = warp; c0 < items; c0 += NW * kBatch) {
+                uint2 v[kBatch];
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const uint32_t bits = i < 2 ? v.x : v.y;
-                    uint16_t hb = static_cast<uint16_t>(i & 1 ? bits >> 16 : bits);
-                    if constexpr (UP) {
-                        const float f = __uint_as_float(static_cast<uint32_t>(hb) << 16);
-                        range |= !(fabsf(f) <= 65504.0f);
-                        hb = to_half_sat(f);
+                for (int u = 0; u < kBatch; u++) {
+                    const int c = c0 + u * NW, col = c / blocks;
+                    const int el = (c - col * blocks) * 128 + lane * 4;
+                    v[u] = make_uint2(0, 0);
+                    if (c < items && el < K) {
+                        const int a = s.a[job][col];
+                        const uint16_t *src = UP ? p.x + static_cast<int64_t>(a / p.k) * p.d
+                                                 : p.h + static_cast<int64_t>(a) * p.m;
+                        v[u] = __ldcg(reinterpret_cast<const uint2 *>(src + el));
                     }
-                    sum += __half2float(__ushort_as_half(hb));
-                    if (in)
-                        dst[perm8((lane & 1) * 4 + i)] = hb;
                 }
 #pragma unroll
-                for (int o = T::kGroup / 8; o > 0; o >>= 1)
-                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (in && (lane & (T::kGroup / 4 - 1)) == 0)
-                    reinterpret_cast<float *>(xc + 2 * K)[gi] = -sum / kSub;
+                for (int u = 0; u < kBatch; u++) {
+                    const int c = c0 + u * NW, col = c / blocks;
+                    const int el = (c - col * blocks) * 128 + lane * 4;
+                    const bool in = c < items && el < K;
+                    uint8_t *xc = xbuf + (s.col0[job] + col) * stride;
+                    const int gi = el / T::kGroup, i8 = (el % T::kGroup) / 8;   // word in the group
+                    uint16_t *dst = reinterpret_cast<uint16_t *>(
+                        xc + gi * T::kGroup * 2 + (i8 % T::kWords) * 64 + (i8 / T::kWords) * 16);
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const uint32_t bits = i < 2 ? v[u].x : v[u].y;
+                        uint16_t hb = static_cast<uint16_t>(i & 1 ? bits >> 16 : bits);
+                        if constexpr (UP) {
+                            const float f = __uint_as_float(static_cast<uint32_t>(hb) << 16);
+                            range |= !(fabsf(f) <= 65504.0f);
+                            hb = to_half_sat(f);
+                        }
+                        sum += __half2float(__ushort_as_half(hb));
+                        if (in)
+                            dst[perm8((lane & 1) * 4 + i)] = hb;
+                    }
+#pragma unroll
+                    for (int o = T::kGroup / 8; o > 0; o >>= 1)
+                        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (in && (lane & (T::kGroup / 4 - 1)) == 0)
+                        reinterpret_cast<float *>(xc + 2 * K)[gi] = -sum / kSub;
+                }
             }
         }
         if (range && p.dev_status)
@@ -664,16 +677,23 @@ bool plan(int d, int m, int *scale_bytes, int *cols, size_t *smem)
 }
 
 template <int NW, int DEPTH>
-cudaError_t launch_variant(FewArgs a, int sms, cudaStream_t stream)
+cudaError_t launch_variant(FewArgs a, int dev, int sms, cudaStream_t stream)
 {
     size_t smem;
     if (!plan<NW, DEPTH>(a.d, a.m, &a.scale_bytes, &a.cols, &smem))
         return cudaErrorInvalidValue;
     auto kern = few_layer_kernel<NW, DEPTH>;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(smem));
-    if (err != cudaSuccess)
-        return err;
+    static std::atomic<uint64_t> raised{0};      // devices whose limit is raised already
+    if (!(raised.load(std::memory_order_relaxed) >> (dev & 63) & 1u)) {
+        cudaFuncAttributes at;
+        cudaError_t err = cudaFuncGetAttributes(&at, kern);
+        if (err == cudaSuccess)
+            err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       227 * 1024 - static_cast<int>(at.sharedSizeBytes));
+        if (err != cudaSuccess)
+            return err;
+        raised.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+    }
     void *args[] = {&a};
     return cudaLaunchCooperativeKernel(kern, dim3(sms), dim3(32 * NW), args, smem, stream);
 }
@@ -768,8 +788,8 @@ cudaError_t launch_few(const FewProblem &q, cudaStream_t stream)
     if (!encode_rows(&a.gu_map, q.gu_q, q.d / 2, q.m, 2 * q.E, 8, 2) ||
         !encode_rows(&a.dn_map, q.dn_q, q.m / 2, q.d, q.E, 16, 1))
         return cudaErrorInvalidValue;
-    return wide_fits(q.d, q.m) ? launch_variant<16, 3>(a, sms, stream)
-                               : launch_variant<8, 3>(a, sms, stream);
+    return wide_fits(q.d, q.m) ? launch_variant<16, 3>(a, dev, sms, stream)
+                               : launch_variant<8, 3>(a, dev, sms, stream);
 }
 
 }  // namespace w4
