@@ -75,6 +75,15 @@ typedef enum {
                                          skipped (only in a library built with
                                          -DW4_CHECK_BOUNDS, a test build)       */
 
+#define W4_DEV_BAD_SLOT 0x20           /* a sequence slot (or its length, or its
+                                         place in q_offsets) is out of range,
+                                         named twice or not empty; skipped       */
+#define W4_DEV_BAD_PAGE 0x40           /* a page id outside [0, P), or a page
+                                         freed more often than held; skipped     */
+#define W4_DEV_NO_PAGES 0x80           /* too few free pages; the sequences from
+                                         the first that lacks one on are left
+                                         as they were                            */
+
 /* Human-readable name of a w4_status value (static string). */
 const char *w4_status_string(int status);
 
@@ -566,6 +575,85 @@ int w4_fused_entropy(const float *logits, int M, int64_t V, float *entropy, void
 int w4_gumbel_argmax_sample(const float *logits, int M, int64_t V, uint64_t seed,
                             uint64_t offset, int64_t *sample, int64_t *argmax, void *workspace,
                             size_t workspace_bytes, w4_stream_t stream);
+
+/* ==========================================================================
+ * A paged key/value cache
+ *
+ * The pool is one buffer [planes, P, page_bytes]: `planes` is layers x {K, V}
+ * (any order), a page holds `page_size` tokens of one plane as
+ * [page_size, Hkv, D] 16-bit values.  A page id stands for that page of every
+ * plane.  Device state, all int32 and owned by the caller:
+ *   table [B, W]  the pages of each sequence slot in order; -1: none
+ *   lens  [B]     tokens of each slot; 0: empty
+ *   refs  [P]     slots that hold a page; 0: free
+ * A cleared cache is table = -1, lens = 0, refs = 0.  A page held by several
+ * slots is full, so nothing is ever written to it: forking shares the full
+ * pages and copies the one that a sequence ends in.  Pages are handed out
+ * lowest free id first, to the requests in order, so a sequence of calls
+ * gives the same pages on every run.  Nothing is read back: what the device
+ * finds wrong is skipped and OR-ed into *dev_status (may be NULL).
+ * Requires page_size >= 1, page_bytes a multiple of 16 page_size, a 16-byte
+ * aligned pool, B * W and P below 2^30, and n <= 1024 per call of reserve and
+ * fork.  n = 0 does nothing.
+ * ========================================================================== */
+
+/* w4_kv_reserve -- grow slots[i] to new_lens[i] tokens (>= its length), taking
+ * the pages that needs; lens is set to new_lens.  One launch. */
+int w4_kv_reserve(int32_t *table, int B, int W, int32_t *lens, int32_t *refs, int P,
+                  const int32_t *slots, const int32_t *new_lens, int n, int page_size,
+                  int32_t *dev_status, w4_stream_t stream);
+
+/* w4_kv_free -- empty slots[i]: its table row becomes -1, its length 0, and
+ * each of its pages is held by one slot less.  The cached values stay where
+ * they are.  A slot named twice is freed once.  One launch. */
+int w4_kv_free(int32_t *table, int B, int W, int32_t *lens, int32_t *refs, int P,
+               const int32_t *slots, int n, int32_t *dev_status, w4_stream_t stream);
+
+/* w4_kv_fork -- make the empty slot children[i] a copy of slot parents[i]:
+ * the parent's full pages are shared (refs + 1), the tokens in its last,
+ * partly filled page are copied to a fresh page, in every plane.  A parent may
+ * have many children in one call.  workspace: w4_kv_workspace_size(P, n) bytes,
+ * 16-byte aligned.  Two launches. */
+int w4_kv_fork(void *pool, int planes, int64_t page_bytes, int32_t *table, int B, int W,
+               int32_t *lens, int32_t *refs, int P, const int32_t *parents,
+               const int32_t *children, int n, int page_size, void *workspace,
+               size_t workspace_bytes, int32_t *dev_status, w4_stream_t stream);
+
+/* w4_kv_copy_pages -- page dst[i] of every plane becomes a copy of page src[i].
+ * The pairs are copied concurrently: no page may be a destination twice, or
+ * both a source and a destination.  table and refs are the caller's affair.
+ * One launch. */
+int w4_kv_copy_pages(void *pool, int planes, int64_t page_bytes, int P, const int32_t *src,
+                     const int32_t *dst, int n, int32_t *dev_status, w4_stream_t stream);
+
+/* w4_kv_compact -- move the pages in use to the front of the pool: with L
+ * pages in use, the k-th (by id) in use with an id >= L is copied to the k-th
+ * free one below L, and table_out / refs_out are table / refs with the ids
+ * renamed (they may be the same buffers).  Afterwards pages [0, L) are in use
+ * and the rest is free.  workspace: w4_kv_workspace_size(P, 0) bytes, 16-byte
+ * aligned.  Two launches. */
+size_t w4_kv_workspace_size(int P, int n);
+int w4_kv_compact(void *pool, int planes, int64_t page_bytes, const int32_t *table, int B, int W,
+                  const int32_t *refs, int P, int32_t *table_out, int32_t *refs_out,
+                  void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                  w4_stream_t stream);
+
+/* w4_kv_append -- write the keys and values of new tokens into their pages:
+ * slot b's tokens are rows q_offsets[b] .. q_offsets[b + 1] of k and v
+ * [T, Hkv, D] 16-bit, and they are its last ones (lens counts them already, as
+ * after w4_kv_reserve).
+ *   k_pages, v_pages  one layer's planes, [P, page_size, Hkv, D]; strides of
+ *                     pages, tokens and heads in elements, alike in both
+ *   k, v              strides of tokens and heads in elements
+ *   q_offsets         [B + 1] int32, ascending, from 0 to T
+ * The innermost axis is contiguous; D, every stride and every pointer (in
+ * bytes) are multiples of 8 elements.  One launch. */
+int w4_kv_append(uint16_t *k_pages, uint16_t *v_pages, int64_t page_stride, int64_t tok_stride,
+                 int64_t head_stride, int P, int page_size, int Hkv, int D, const int32_t *table,
+                 int B, int W, const int32_t *lens, const uint16_t *k, int64_t k_tok_stride,
+                 int64_t k_head_stride, const uint16_t *v, int64_t v_tok_stride,
+                 int64_t v_head_stride, const int32_t *q_offsets, int T, int32_t *dev_status,
+                 w4_stream_t stream);
 
 /* --------------------------------------------------------------------------
  * w4_test_pipeline_hooks -- a test hook of the grouped GEMMs (not for

@@ -26,6 +26,9 @@ W4_DEV_PIPELINE_TIMEOUT = 0x2
 W4_DEV_TOO_MANY_JOBS = 0x4
 W4_DEV_FP16_RANGE = 0x8
 W4_DEV_OUT_OF_BOUNDS = 0x10
+W4_DEV_BAD_SLOT = 0x20
+W4_DEV_BAD_PAGE = 0x40
+W4_DEV_NO_PAGES = 0x80
 # xg and h rows end in one block of 64 columns of activation group sums, the
 # grouped GEMMs' input for the low parts of their dequantisation constants
 SUM_COLS = 64
@@ -98,6 +101,14 @@ def load_library(path: str | None = None):
                                               V, V, V, V, V], I),
             "w4_w4a16_linear_workspace_size": ([I, I, I, I], SZ),
             "w4_w4a16_linear": ([V, I, I, I, V, V, V, I, V, SZ, V, V, V], I),
+            "w4_kv_workspace_size": ([I, I], SZ),
+            "w4_kv_reserve": ([V, I, I, V, V, I, V, V, I, I, V, V], I),
+            "w4_kv_free": ([V, I, I, V, V, I, V, I, V, V], I),
+            "w4_kv_fork": ([V, I, I64, V, I, I, V, V, I, V, V, I, I, V, SZ, V, V], I),
+            "w4_kv_copy_pages": ([V, I, I64, I, V, V, I, V, V], I),
+            "w4_kv_compact": ([V, I, I64, V, I, I, V, I, V, V, V, SZ, V, V], I),
+            "w4_kv_append": ([V, V, I64, I64, I64, I, I, I, I, V, I, I, V, V, I64, I64, V, I64, I64,
+                              V, I, V, V], I),
             "w4_rmsnorm": ([V, V, I, I, ctypes.c_float, V, V], I),
             "w4_sample_logits_workspace_size": ([I, I64], SZ),
             "w4_sample_logits": ([V, I, I64, U64, U64, V, V, V, V, SZ, V], I),
@@ -646,3 +657,160 @@ def w4_gumbel_argmax_sample(logits, seed: int, offset: int = 0, workspace=None, 
     _, smp, amx = w4_sample_logits(logits, seed, offset, entropy=False, sample=True,
                                    argmax=True, workspace=workspace, stream=stream)
     return smp, amx
+
+
+# --------------------------------------------------------------------------
+# A paged key/value cache: the pool is a tensor [..., P, page_size, Hkv, D] of
+# 16-bit values (the leading axes, layers and K / V, are its planes), the state
+# three int32 tensors table [B, W] (-1: no page), lens [B] and refs [P].
+# --------------------------------------------------------------------------
+def _require_int32(*ts):
+    import torch
+    for t in ts:
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError("tables, lengths, slots and page lists must be int32")
+
+
+def _kv_state(table, lens, refs):
+    """(B, W, P) of a cache's state, with its tensors checked."""
+    _require_cuda(table, lens, refs)
+    _require_int32(table, lens, refs)
+    B, W = table.shape
+    if lens.shape != (B,) or refs.dim() != 1:
+        raise ValueError("lens must be [B] and refs [P] for a table [B, W]")
+    return B, W, refs.shape[0]
+
+
+def _kv_pool(pool, P):
+    """(planes, bytes of a page in one plane, page_size) of a pool."""
+    _require_cuda(pool)
+    if pool.dim() < 4 or pool.shape[-4] != P or pool.element_size() != 2:
+        raise ValueError("the pool must be [..., P, page_size, Hkv, D] of 16-bit values")
+    page, Hkv, D = pool.shape[-3:]
+    page_bytes = page * Hkv * D * 2
+    return pool.numel() * 2 // max(P * page_bytes, 1), page_bytes, page
+
+
+def _kv_lists(*ts):
+    """The length of equally long int32 lists."""
+    _require_cuda(*ts)
+    _require_int32(*ts)
+    if any(t.dim() != 1 or t.shape != ts[0].shape for t in ts):
+        raise ValueError("slots and page lists must be one-dimensional and equally long")
+    return ts[0].shape[0]
+
+
+def _kv_workspace(workspace, P, n, device):
+    import torch
+    if workspace is None:
+        workspace = torch.empty(w4_kv_workspace_size(P, n), dtype=torch.uint8, device=device)
+    _require_cuda(workspace)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def w4_kv_workspace_size(P: int, n: int = 0) -> int:
+    return int(load_library().w4_kv_workspace_size(P, n))
+
+
+def w4_kv_reserve(table, lens, refs, slots, new_lens, page_size: int, dev_status=None,
+                  stream=None):
+    """Grow slots[i] to new_lens[i] tokens; pages are taken lowest free first."""
+    B, W, P = _kv_state(table, lens, refs)
+    n = _kv_lists(slots, new_lens)
+    _check(load_library().w4_kv_reserve(_ptr(table), B, W, _ptr(lens), _ptr(refs), P, _ptr(slots),
+                                        _ptr(new_lens), n, page_size, _ptr(dev_status),
+                                        _stream(stream)), "w4_kv_reserve")
+
+
+def w4_kv_free(table, lens, refs, slots, dev_status=None, stream=None):
+    """Empty slots[i] and let go of its pages."""
+    B, W, P = _kv_state(table, lens, refs)
+    n = _kv_lists(slots)
+    _check(load_library().w4_kv_free(_ptr(table), B, W, _ptr(lens), _ptr(refs), P, _ptr(slots), n,
+                                     _ptr(dev_status), _stream(stream)), "w4_kv_free")
+
+
+def w4_kv_fork(pool, table, lens, refs, parents, children, workspace=None, dev_status=None,
+               stream=None):
+    """Make the empty slots children[i] copies of parents[i]: full pages are
+    shared, the last, partly filled one is copied in every plane."""
+    B, W, P = _kv_state(table, lens, refs)
+    planes, page_bytes, page = _kv_pool(pool, P)
+    n = _kv_lists(parents, children)
+    workspace, nbytes = _kv_workspace(workspace, P, n, pool.device)
+    _check(load_library().w4_kv_fork(_ptr(pool), planes, page_bytes, _ptr(table), B, W, _ptr(lens),
+                                     _ptr(refs), P, _ptr(parents), _ptr(children), n, page,
+                                     _ptr(workspace), nbytes, _ptr(dev_status), _stream(stream)),
+           "w4_kv_fork")
+
+
+def w4_kv_copy_pages(pool, src, dst, dev_status=None, stream=None):
+    """Copy page src[i] to page dst[i] in every plane (disjoint pages)."""
+    P = pool.shape[-4] if pool.dim() >= 4 else 0
+    planes, page_bytes, _ = _kv_pool(pool, P)
+    n = _kv_lists(src, dst)
+    _check(load_library().w4_kv_copy_pages(_ptr(pool), planes, page_bytes, P, _ptr(src), _ptr(dst),
+                                           n, _ptr(dev_status), _stream(stream)),
+           "w4_kv_copy_pages")
+
+
+def w4_kv_compact(pool, table, refs, table_out=None, refs_out=None, workspace=None,
+                  dev_status=None, stream=None):
+    """Move the pages in use to the front of the pool.  Returns (table, refs)
+    with the pages renamed: table_out and refs_out, by default table and refs
+    themselves."""
+    table_out = table if table_out is None else table_out
+    refs_out = refs if refs_out is None else refs_out
+    _require_cuda(table, refs, table_out, refs_out)
+    _require_int32(table, refs, table_out, refs_out)
+    if table.dim() != 2 or table_out.shape != table.shape or refs_out.shape != refs.shape:
+        raise ValueError("table_out and refs_out must have the shapes of table and refs")
+    B, W = table.shape
+    P = refs.shape[0]
+    planes, page_bytes, _ = _kv_pool(pool, P)
+    workspace, nbytes = _kv_workspace(workspace, P, 0, pool.device)
+    _check(load_library().w4_kv_compact(_ptr(pool), planes, page_bytes, _ptr(table), B, W,
+                                        _ptr(refs), P, _ptr(table_out), _ptr(refs_out),
+                                        _ptr(workspace), nbytes, _ptr(dev_status),
+                                        _stream(stream)), "w4_kv_compact")
+    return table_out, refs_out
+
+
+def _rows16(t, what):
+    """A CUDA tensor [.., .., D] of 16-bit values, contiguous along D only."""
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the CUDA library must live on the GPU")
+    if t.element_size() != 2 or t.stride(-1) != 1:
+        raise ValueError(f"{what} must be 16-bit values, contiguous along the last axis")
+
+
+def _kv_planes(k_pages, v_pages):
+    """(P, page_size, Hkv, D) of one layer's planes, with their strides checked."""
+    _rows16(k_pages, "k_pages")
+    _rows16(v_pages, "v_pages")
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or \
+            k_pages.stride() != v_pages.stride() or k_pages.dtype != v_pages.dtype:
+        raise ValueError("k_pages and v_pages must be alike, [P, page_size, Hkv, D]")
+    return tuple(k_pages.shape)
+
+
+def w4_kv_append(k_pages, v_pages, table, lens, k, v, q_offsets, dev_status=None, stream=None):
+    """Write the new tokens' keys and values [T, Hkv, D] (any strides of tokens
+    and heads) into their pages; slot b's are rows q_offsets[b] ..
+    q_offsets[b + 1] and its last tokens."""
+    P, page, Hkv, D = _kv_planes(k_pages, v_pages)
+    _rows16(k, "k")
+    _rows16(v, "v")
+    _require_cuda(table, lens, q_offsets, dev_status)
+    _require_int32(table, lens, q_offsets)
+    if k.shape != v.shape or tuple(k.shape[1:]) != (Hkv, D) or k.dtype != k_pages.dtype or \
+            v.dtype != k_pages.dtype:
+        raise ValueError("k and v must be [T, Hkv, D] of the pages' type")
+    B = q_offsets.shape[0] - 1
+    if B < 1 or table.dim() != 2 or table.shape[0] < B or lens.shape[0] < B:
+        raise ValueError("q_offsets must be [B + 1] for a table [B, W] and lens [B]")
+    _check(load_library().w4_kv_append(
+        _ptr(k_pages), _ptr(v_pages), *k_pages.stride()[:3], P, page, Hkv, D, _ptr(table), B,
+        table.shape[1], _ptr(lens), _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0),
+        v.stride(1), _ptr(q_offsets), k.shape[0], _ptr(dev_status), _stream(stream)),
+        "w4_kv_append")

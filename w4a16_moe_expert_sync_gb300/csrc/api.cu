@@ -855,6 +855,202 @@ int w4_moe_layer_few_from_logits(const uint16_t *x, const float *logits, int M, 
                    topk_ids, topk_weights, out, dev_status, stream);
 }
 
+// -------------------------------------------------------------- paged cache
+namespace {
+int check_kv_state(const void *table, int B, int W, const void *lens, const void *refs, int P)
+{
+    if (!table || !lens || !refs)
+        return fail(W4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (B <= 0 || W <= 0 || P <= 0)
+        return fail(W4_ERR_INVALID_ARG, "bad sizes B=%d W=%d P=%d", B, W, P);
+    if (static_cast<int64_t>(B) * W >= (1ll << 30) || P >= (1 << 30))
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "need B * W and P below 2^30");
+    if (!aligned4(table) || !aligned4(lens) || !aligned4(refs))
+        return fail(W4_ERR_MISALIGNED, "table, lens and refs must be 4-byte aligned");
+    return W4_OK;
+}
+
+int check_kv_pool(const void *pool, int planes, int64_t page_bytes, int page_size)
+{
+    if (!pool)
+        return fail(W4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (planes <= 0 || page_bytes <= 0 || page_size <= 0)
+        return fail(W4_ERR_INVALID_ARG, "bad sizes planes=%d page_bytes=%lld page_size=%d", planes,
+                    static_cast<long long>(page_bytes), page_size);
+    if (planes > 65535 || page_bytes % (16ll * page_size))
+        return fail(W4_ERR_UNSUPPORTED_SHAPE,
+                    "need at most 65535 planes and tokens of a multiple of 16 bytes");
+    if (!aligned16(pool))
+        return fail(W4_ERR_MISALIGNED, "the pool must be 16-byte aligned");
+    return W4_OK;
+}
+
+int check_kv_workspace(const void *workspace, size_t bytes, int P, int n)
+{
+    const size_t need = w4_kv_workspace_size(P, n);
+    if (!workspace || bytes < need)
+        return fail(W4_ERR_WORKSPACE, "workspace needs %zu bytes", need);
+    if (!aligned16(workspace))
+        return fail(W4_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    return W4_OK;
+}
+}  // namespace
+
+size_t w4_kv_workspace_size(int P, int n)
+{
+    return P < 0 || n < 0 ? 0 : w4::kv_workspace_bytes(P, n);
+}
+
+int w4_kv_reserve(int32_t *table, int B, int W, int32_t *lens, int32_t *refs, int P,
+                  const int32_t *slots, const int32_t *new_lens, int n, int page_size,
+                  int32_t *dev_status, w4_stream_t stream)
+{
+    if (int rc = check_kv_state(table, B, W, lens, refs, P))
+        return rc;
+    if (n < 0 || page_size <= 0 || (n > 0 && (!slots || !new_lens)))
+        return fail(W4_ERR_INVALID_ARG, "bad n=%d, page_size=%d or NULL slots", n, page_size);
+    if (n > 1024)
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "at most 1024 slots per call (got %d)", n);
+    if (n == 0)
+        return W4_OK;
+    if (int rc = check_device())
+        return rc;
+    cudaError_t err = w4::launch_kv_reserve(table, B, W, lens, refs, P, slots, new_lens, n,
+                                            page_size, dev_status, as_stream(stream));
+    return err == cudaSuccess ? W4_OK : cuda_fail(err, "kv_reserve launch");
+}
+
+int w4_kv_free(int32_t *table, int B, int W, int32_t *lens, int32_t *refs, int P,
+               const int32_t *slots, int n, int32_t *dev_status, w4_stream_t stream)
+{
+    if (int rc = check_kv_state(table, B, W, lens, refs, P))
+        return rc;
+    if (n < 0 || (n > 0 && !slots))
+        return fail(W4_ERR_INVALID_ARG, "bad n=%d or NULL slots", n);
+    if (n == 0)
+        return W4_OK;
+    if (int rc = check_device())
+        return rc;
+    cudaError_t err = w4::launch_kv_free(table, B, W, lens, refs, P, slots, n, dev_status,
+                                         as_stream(stream));
+    return err == cudaSuccess ? W4_OK : cuda_fail(err, "kv_free launch");
+}
+
+int w4_kv_fork(void *pool, int planes, int64_t page_bytes, int32_t *table, int B, int W,
+               int32_t *lens, int32_t *refs, int P, const int32_t *parents,
+               const int32_t *children, int n, int page_size, void *workspace,
+               size_t workspace_bytes, int32_t *dev_status, w4_stream_t stream)
+{
+    if (int rc = check_kv_state(table, B, W, lens, refs, P))
+        return rc;
+    if (int rc = check_kv_pool(pool, planes, page_bytes, page_size))
+        return rc;
+    if (n < 0 || (n > 0 && (!parents || !children)))
+        return fail(W4_ERR_INVALID_ARG, "bad n=%d or NULL slots", n);
+    if (n > 1024)
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "at most 1024 forks per call (got %d)", n);
+    if (n == 0)
+        return W4_OK;
+    if (int rc = check_kv_workspace(workspace, workspace_bytes, P, n))
+        return rc;
+    if (int rc = check_device())
+        return rc;
+    cudaError_t err = w4::launch_kv_fork(static_cast<uint8_t *>(pool), planes, page_bytes, table, B,
+                                         W, lens, refs, P, parents, children, n, page_size,
+                                         workspace, dev_status, as_stream(stream));
+    return err == cudaSuccess ? W4_OK : cuda_fail(err, "kv_fork launch");
+}
+
+int w4_kv_copy_pages(void *pool, int planes, int64_t page_bytes, int P, const int32_t *src,
+                     const int32_t *dst, int n, int32_t *dev_status, w4_stream_t stream)
+{
+    if (int rc = check_kv_pool(pool, planes, page_bytes, 1))
+        return rc;
+    if (P <= 0 || n < 0 || (n > 0 && (!src || !dst)))
+        return fail(W4_ERR_INVALID_ARG, "bad P=%d, n=%d or NULL lists", P, n);
+    if (n == 0)
+        return W4_OK;
+    if (int rc = check_device())
+        return rc;
+    cudaError_t err = w4::launch_kv_copy(static_cast<uint8_t *>(pool), planes, page_bytes, P, src,
+                                         dst, n, dev_status, as_stream(stream));
+    return err == cudaSuccess ? W4_OK : cuda_fail(err, "kv_copy_pages launch");
+}
+
+int w4_kv_compact(void *pool, int planes, int64_t page_bytes, const int32_t *table, int B, int W,
+                  const int32_t *refs, int P, int32_t *table_out, int32_t *refs_out,
+                  void *workspace, size_t workspace_bytes, int32_t *dev_status, w4_stream_t stream)
+{
+    if (int rc = check_kv_state(table, B, W, refs, refs, P))
+        return rc;
+    if (!table_out || !refs_out)
+        return fail(W4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned4(table_out) || !aligned4(refs_out))
+        return fail(W4_ERR_MISALIGNED, "table_out and refs_out must be 4-byte aligned");
+    if (int rc = check_kv_pool(pool, planes, page_bytes, 1))
+        return rc;
+    if (int rc = check_kv_workspace(workspace, workspace_bytes, P, 0))
+        return rc;
+    if (int rc = check_device())
+        return rc;
+    cudaError_t err = w4::launch_kv_compact(static_cast<uint8_t *>(pool), planes, page_bytes, table,
+                                            static_cast<int64_t>(B) * W, refs, P, table_out,
+                                            refs_out, workspace, dev_status, as_stream(stream));
+    return err == cudaSuccess ? W4_OK : cuda_fail(err, "kv_compact launch");
+}
+
+int w4_kv_append(uint16_t *k_pages, uint16_t *v_pages, int64_t page_stride, int64_t tok_stride,
+                 int64_t head_stride, int P, int page_size, int Hkv, int D, const int32_t *table,
+                 int B, int W, const int32_t *lens, const uint16_t *k, int64_t k_tok_stride,
+                 int64_t k_head_stride, const uint16_t *v, int64_t v_tok_stride,
+                 int64_t v_head_stride, const int32_t *q_offsets, int T, int32_t *dev_status,
+                 w4_stream_t stream)
+{
+    if (int rc = check_kv_state(table, B, W, lens, lens, P))
+        return rc;
+    if (!k_pages || !v_pages || !q_offsets || (T > 0 && (!k || !v)))
+        return fail(W4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (page_size <= 0 || Hkv <= 0 || D <= 0 || T < 0)
+        return fail(W4_ERR_INVALID_ARG, "bad sizes page_size=%d Hkv=%d D=%d T=%d", page_size, Hkv,
+                    D, T);
+    if (D % 8 || static_cast<int64_t>(Hkv) * D >= (1ll << 30))
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "D must be a multiple of 8 (got %d)", D);
+    if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k) || !aligned16(v) ||
+        (page_stride | tok_stride | head_stride | k_tok_stride | k_head_stride | v_tok_stride |
+         v_head_stride) & 7 || !aligned4(q_offsets))
+        return fail(W4_ERR_MISALIGNED, "pointers must be 16-byte aligned and strides multiples of "
+                                       "8 elements");
+    if (T == 0)
+        return W4_OK;
+    if (int rc = check_device())
+        return rc;
+    w4::KvAppend a{};
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.page_stride = page_stride;
+    a.tok_stride = tok_stride;
+    a.head_stride = head_stride;
+    a.k = k;
+    a.v = v;
+    a.k_tok = k_tok_stride;
+    a.k_head = k_head_stride;
+    a.v_tok = v_tok_stride;
+    a.v_head = v_head_stride;
+    a.table = table;
+    a.lens = lens;
+    a.q_offsets = q_offsets;
+    a.dev_status = dev_status;
+    a.P = P;
+    a.page = page_size;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.B = B;
+    a.W = W;
+    a.T = T;
+    cudaError_t err = w4::launch_kv_append(a, as_stream(stream));
+    return err == cudaSuccess ? W4_OK : cuda_fail(err, "kv_append launch");
+}
+
 // ------------------------------------------------------------------ RMSNorm
 int w4_rmsnorm(const uint16_t *x, const uint16_t *weight, int M, int d, float eps, uint16_t *y,
                w4_stream_t stream)

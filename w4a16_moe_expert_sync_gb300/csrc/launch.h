@@ -158,6 +158,35 @@ bool few_supported(int M, int d, int m, int k);
 size_t few_workspace_bytes(int M, int d, int m, int k);
 cudaError_t launch_few(const FewProblem &p, cudaStream_t stream);
 
+// Pages of a key/value cache (kv.cu).  status may be NULL.
+cudaError_t launch_kv_reserve(int32_t *table, int B, int W, int32_t *lens, int32_t *refs, int P,
+                              const int32_t *slots, const int32_t *new_lens, int n, int page,
+                              int32_t *status, cudaStream_t stream);
+cudaError_t launch_kv_free(int32_t *table, int B, int W, int32_t *lens, int32_t *refs, int P,
+                           const int32_t *slots, int n, int32_t *status, cudaStream_t stream);
+cudaError_t launch_kv_fork(uint8_t *cache, int planes, int64_t page_bytes, int32_t *table, int B,
+                           int W, int32_t *lens, int32_t *refs, int P, const int32_t *parents,
+                           const int32_t *children, int n, int page, void *workspace,
+                           int32_t *status, cudaStream_t stream);
+cudaError_t launch_kv_copy(uint8_t *cache, int planes, int64_t page_bytes, int P,
+                           const int32_t *src, const int32_t *dst, int n, int32_t *status,
+                           cudaStream_t stream);
+cudaError_t launch_kv_compact(uint8_t *cache, int planes, int64_t page_bytes, const int32_t *table,
+                              int64_t entries, const int32_t *refs, int P, int32_t *table_out,
+                              int32_t *refs_out, void *workspace, int32_t *status,
+                              cudaStream_t stream);
+size_t kv_workspace_bytes(int P, int n);
+struct KvAppend {
+    uint16_t *k_pages, *v_pages;        // [P][page][Hkv][D], strides in elements
+    int64_t page_stride, tok_stride, head_stride;
+    const uint16_t *k, *v;              // [T][Hkv][D], strides in elements
+    int64_t k_tok, k_head, v_tok, v_head;
+    const int32_t *table, *lens, *q_offsets;
+    int32_t *dev_status;
+    int P, page, Hkv, D, B, W, T;
+};
+cudaError_t launch_kv_append(const KvAppend &p, cudaStream_t stream);
+
 // W4_OK when the current device is an sm_103 part, else W4_ERR_NO_DEVICE or
 // W4_ERR_CUDA with the detail recorded (the argument checks of every entry
 // point call it before launching).
