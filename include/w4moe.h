@@ -656,6 +656,58 @@ int w4_kv_append(uint16_t *k_pages, uint16_t *v_pages, int64_t page_stride, int6
                  w4_stream_t stream);
 
 /* --------------------------------------------------------------------------
+ * w4_attn_shared_prefix -- attention over the paged cache for a batch whose
+ * sequences share prefixes, each prefix read and multiplied once for its group
+ *
+ *   out[t, h] = sum_l softmax_l(scale q[t, h] . k[l, h']) v[l, h'],
+ *   h' = h / (Hq / Hkv), over the keys l = 0 .. n(t) - 1 of t's sequence
+ *
+ *   q          [T, Hq, D] 16-bit, strides of tokens and heads in elements
+ *   k_pages, v_pages  one layer's planes [P, page_size, Hkv, D], strides of
+ *              pages, tokens and heads in elements, alike in both
+ *   table      [B, W] int32, lens [B] int32: each sequence's pages and length
+ *              (its new tokens counted, as after w4_kv_append)
+ *   q_offsets  [B + 1] int32, ascending: sequence b's queries are rows
+ *              q_offsets[b] .. q_offsets[b + 1], at most max_q of them, and
+ *              stand at its last positions
+ *   causal     nonzero: a query sees the keys up to its own position; zero:
+ *              every query sees its sequence's whole length
+ *   group_offsets [G + 1] int32, ascending, and shared_lens [G] int32:
+ *              sequences group_offsets[g] .. group_offsets[g + 1] have the same
+ *              first shared_lens[g] tokens, which are read through the first
+ *              one's pages.  Any length, also inside a page; more than the
+ *              first one's length counts as that length.  Sequences of no group
+ *              share nothing; G = 0 (both may be NULL): plain paged attention
+ *   out        [T, Hq, D] 16-bit, contiguous; a query that sees no key: zeros.
+ *              Rows of no sequence are not written
+ *   workspace  w4_attn_shared_prefix_workspace_size(...) bytes, 256-byte
+ *              aligned; contents need no initialisation
+ *   dtype      0: bf16, 1: fp16 (q, the cache and out)
+ * Cached values past a sequence's length are never used, whatever they are.
+ * Inputs on the device that make no sense (lengths below 0 or beyond W pages,
+ * more than max_q queries: W4_DEV_BAD_SLOT; a page id outside [0, P):
+ * W4_DEV_BAD_PAGE) are flagged; the queries concerned get unspecified values.
+ * With offsets that do not ascend nothing is computed (W4_DEV_BAD_SLOT).
+ * Scores, maximum and denominator are fp32; the weights are rounded to the
+ * values' type for the product with V; partial sums are fp32, joined in a
+ * fixed order: bit-identical reruns on one GPU model.  Two launches.
+ * Requires D = 64 or 128, page_size 16, 32, 64 or 128, Hkv dividing Hq,
+ * max_q >= 1, scale > 0, B + G <= 4096, pointers 16-byte aligned, strides
+ * multiples of 8 elements, T * Hq * D and the tiles below 2^31.
+ * ------------------------------------------------------------------------ */
+size_t w4_attn_shared_prefix_workspace_size(int T, int B, int G, int max_q, int Hq, int Hkv,
+                                            int D);
+int w4_attn_shared_prefix(const uint16_t *q, int64_t q_tok_stride, int64_t q_head_stride,
+                          const uint16_t *k_pages, const uint16_t *v_pages, int64_t page_stride,
+                          int64_t tok_stride, int64_t head_stride, int P, int page_size,
+                          const int32_t *table, int W, const int32_t *lens,
+                          const int32_t *q_offsets, int T, int B, int max_q,
+                          const int32_t *group_offsets, const int32_t *shared_lens, int G, int Hq,
+                          int Hkv, int D, int dtype, int causal, float scale, void *workspace,
+                          size_t workspace_bytes, uint16_t *out, int32_t *dev_status,
+                          w4_stream_t stream);
+
+/* --------------------------------------------------------------------------
  * w4_test_pipeline_hooks -- a test hook of the grouped GEMMs (not for
  * production use): for later w4_grouped_gemm_gate_up / _down / _down_combine
  * calls and the layer's GEMMs made from the calling thread, every pipeline

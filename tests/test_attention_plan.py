@@ -1,0 +1,165 @@
+"""CPU models of the attention kernel's bookkeeping: the split of tiles over
+workers and pieces, the order of the ring's fills, and the ring itself under
+random interleavings."""
+import random
+
+import pytest
+
+
+def worker_begin(tiles, workers, w):
+    return tiles * w // workers
+
+
+def worker_of(tiles, workers, x):
+    return ((x + 1) * workers - 1) // tiles
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_every_tile_has_one_piece_and_no_two_pieces_share_a_place(seed):
+    r = random.Random(seed)
+    items = [r.choice([0, 1, 2, 3, 17, 200]) for _ in range(r.choice([1, 2, 9, 120]))]
+    starts, total = [], 0
+    for n in items:
+        starts.append(total)
+        total += n
+    if total == 0:
+        return
+    workers = min(total, r.choice([1, 7, 152, 304]))
+    pieces = {}
+    for w in range(workers):
+        lo, hi = worker_begin(total, workers, w), worker_begin(total, workers, w + 1)
+        assert hi > lo
+        for i, n in enumerate(items):
+            a, b = max(lo, starts[i]), min(hi, starts[i] + n)
+            if a < b:
+                assert i + w not in pieces
+                pieces[i + w] = (i, a, b)
+                assert worker_of(total, workers, a) == w == worker_of(total, workers, b - 1)
+    seen = sorted((a, b) for _, a, b in pieces.values())
+    assert seen[0][0] == 0 and seen[-1][1] == total
+    assert all(x[1] == y[0] for x, y in zip(seen, seen[1:]))
+    assert max(pieces) < len(items) + workers
+    # the joining kernel's loop meets exactly an item's pieces
+    for i, n in enumerate(items):
+        if n:
+            w0 = worker_of(total, workers, starts[i])
+            w1 = worker_of(total, workers, starts[i] + n - 1)
+            assert all(pieces[i + w][0] == i for w in range(w0, w1 + 1))
+            assert sum(pieces[i + w][2] - pieces[i + w][1] for w in range(w0, w1 + 1)) == n
+
+
+def fill_of(tiles, which, r):
+    if which == 2:
+        return r
+    return tiles[2] + r + (min(r, tiles[1]) if which == 0 else min(r + 1, tiles[0]))
+
+
+def load_order(tiles):
+    order = [(2, r) for r in range(tiles[2])]
+    for r in range(max(tiles[0], tiles[1])):
+        order += [(s, r) for s in (0, 1) if r < tiles[s]]
+    return order
+
+
+@pytest.mark.parametrize("slots", [5, 10])
+@pytest.mark.parametrize("seed", range(25))
+def test_ring_fills_and_releases(slots, seed):
+    """Loader, two issuers and two softmax groups as state machines: the parity
+    that each waits for is that of the fill it means, and all finish."""
+    r = random.Random(seed)
+    tiles = [r.choice([0, 1, 2, 5, 13]) for _ in range(3)]
+    order = load_order(tiles)
+    for n, (s, t) in enumerate(order):
+        assert fill_of(tiles, s, t) == n
+    full = [0] * slots               # completed phases of full[slot]
+    empty = [0] * slots              # arrivals on empty[slot], two to a phase
+    content = [None] * slots
+
+    def loader():
+        for fill, (s, t) in enumerate(order):
+            for part in (0, 1):
+                n = 2 * fill + part
+                slot, use = n % slots, n // slots
+                if use:
+                    while not (empty[slot] // 2 - 1 >= use - 1):
+                        yield
+                    assert empty[slot] == 2 * use       # parity unambiguous
+                content[slot] = (s, t, part)
+                if s != 2:
+                    empty[slot] += 1
+                yield
+                full[slot] += 1
+
+    s_full, p_ready = [0, 0], [0, 0]
+
+    def issuer(stream):
+        done = 0
+        for which in (2, stream):
+            for t in range(tiles[which]):
+                n = 2 * fill_of(tiles, which, t)
+                for part in (0, 1):
+                    slot, use = (n + part) % slots, (n + part) // slots
+                    while full[slot] < use + 1:
+                        yield
+                    assert full[slot] == use + 1
+                    assert content[slot] == (which, t, part)
+                    if part == 0:
+                        s_full[stream] += 1
+                        empty[slot] += 1
+                        done += 1
+                        while p_ready[stream] < done:
+                            yield
+                        assert p_ready[stream] == done
+                    else:
+                        empty[slot] += 1
+                    yield
+
+    def softmax(stream):
+        for n in range(tiles[2] + tiles[stream]):
+            while s_full[stream] < n + 1:
+                yield
+            assert s_full[stream] == n + 1
+            yield
+            p_ready[stream] += 1
+
+    roles = [loader(), issuer(0), issuer(1), softmax(0), softmax(1)]
+    for _ in range(200000):
+        if not roles:
+            break
+        g = r.choice(roles)
+        try:
+            next(g)
+        except StopIteration:
+            roles.remove(g)
+    assert not roles
+
+
+def test_refusals_without_launching():
+    import ctypes
+
+    import w4a16_moe_expert_sync_gb300 as w4
+    from w4a16_moe_expert_sync_gb300 import build as w4build
+    w4build.build()
+    lib = w4.load_library()
+    P = ctypes.c_void_p
+    f, odd, odd4 = P(0x10000), P(0x10004), P(0x10002)
+    ok = [f, 2048, 128, f, f, 16384, 1024, 128, 50, 16, f, 8, f, f, 6, 3, 4, f, f, 1, 16, 8, 128, 0,
+          1, 0.1, f, 1 << 40, f, None, None]
+
+    def bad(**kw):
+        a = list(ok)
+        for i, v in kw.items():
+            a[int(i[1:])] = v
+        return lib.w4_attn_shared_prefix(*a)
+    for i in (0, 3, 4, 10, 12, 13, 17, 18, 28):
+        assert bad(**{f"a{i}": None}) == 1, i
+    assert bad(a14=-1) == 1 and bad(a16=0) == 1 and bad(a23=2) == 1 and bad(a25=0.0) == 1
+    assert bad(a25=float("nan")) == 1 and bad(a25=float("inf")) == 1
+    assert bad(a22=96) == 2 and bad(a9=24) == 2 and bad(a20=12) == 2 and bad(a15=4096) == 2
+    assert bad(a11=1 << 28) == 2 and bad(a14=1 << 21) == 2
+    assert bad(a0=odd) == 3 and bad(a3=odd) == 3 and bad(a1=2044) == 3 and bad(a7=4) == 3
+    assert bad(a10=odd4) == 3 and bad(a26=P(0x10010)) == 3
+    assert bad(a26=None) == 6 and bad(a27=100) == 6
+    assert bad(a14=0) == 0 and bad(a15=0) == 0
+    ws = lib.w4_attn_shared_prefix_workspace_size
+    assert ws(6, 3, 1, 4, 16, 8, 128) > 0 and ws(6, 3, 1, 4, 16, 5, 128) == 0

@@ -21,6 +21,7 @@ from ._lib import (W4_DEV_BAD_EXPERT_ID, W4_DEV_FP16_RANGE, W4_DEV_OUT_OF_BOUNDS
                    w4_moe_layer_host_workspace_size,
                    w4_moe_layer_few, w4_moe_layer_few_from_logits,
                    w4_moe_layer_few_workspace_size,
+                   w4_attn_shared_prefix, w4_attn_shared_prefix_workspace_size,
                    w4_kv_append, w4_kv_compact, w4_kv_copy_pages, w4_kv_fork, w4_kv_free,
                    w4_kv_reserve, w4_kv_workspace_size,
                    w4_moe_route, w4_moe_route_align_gather, w4_quantize, w4_rmsnorm,
@@ -39,6 +40,7 @@ __all__ = [
     "w4_moe_route_align_gather", "w4_moe_layer_from_logits", "w4_rmsnorm", "w4_sample_logits",
     "w4_sample_logits_workspace_size", "w4_fused_entropy", "w4_gumbel_argmax_sample",
     "w4_w4a16_linear", "w4_w4a16_linear_workspace_size",
+    "w4_attn_shared_prefix", "w4_attn_shared_prefix_workspace_size",
     "w4_kv_reserve", "w4_kv_free", "w4_kv_fork", "w4_kv_copy_pages", "w4_kv_compact",
     "w4_kv_append", "w4_kv_workspace_size",
     "W4_DEV_BAD_SLOT", "W4_DEV_BAD_PAGE", "W4_DEV_NO_PAGES",

@@ -109,6 +109,9 @@ def load_library(path: str | None = None):
             "w4_kv_compact": ([V, I, I64, V, I, I, V, I, V, V, V, SZ, V, V], I),
             "w4_kv_append": ([V, V, I64, I64, I64, I, I, I, I, V, I, I, V, V, I64, I64, V, I64, I64,
                               V, I, V, V], I),
+            "w4_attn_shared_prefix_workspace_size": ([I, I, I, I, I, I, I], SZ),
+            "w4_attn_shared_prefix": ([V, I64, I64, V, V, I64, I64, I64, I, I, V, I, V, V, I, I, I,
+                                       V, V, I, I, I, I, I, I, ctypes.c_float, V, SZ, V, V, V], I),
             "w4_rmsnorm": ([V, V, I, I, ctypes.c_float, V, V], I),
             "w4_sample_logits_workspace_size": ([I, I64], SZ),
             "w4_sample_logits": ([V, I, I64, U64, U64, V, V, V, V, SZ, V], I),
@@ -814,3 +817,48 @@ def w4_kv_append(k_pages, v_pages, table, lens, k, v, q_offsets, dev_status=None
         table.shape[1], _ptr(lens), _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0),
         v.stride(1), _ptr(q_offsets), k.shape[0], _ptr(dev_status), _stream(stream)),
         "w4_kv_append")
+
+
+def w4_attn_shared_prefix_workspace_size(T: int, B: int, G: int, max_q: int, Hq: int, Hkv: int,
+                                         D: int) -> int:
+    return int(load_library().w4_attn_shared_prefix_workspace_size(T, B, G, max_q, Hq, Hkv, D))
+
+
+def w4_attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets, group_offsets=None,
+                          shared_lens=None, max_q: int = 1, causal: bool = True, scale=None,
+                          workspace=None, out=None, dev_status=None, stream=None):
+    """Attention of q [T, Hq, D] (any strides of tokens and heads) over one
+    layer's pages [P, page_size, Hkv, D]; sequences group_offsets[g] ..
+    group_offsets[g + 1] share their first shared_lens[g] tokens, which are read
+    once for the group.  scale defaults to 1 / sqrt(D).  Returns out [T, Hq, D]."""
+    import torch
+    P, page, Hkv, D = _kv_planes(k_pages, v_pages)
+    _rows16(q, "q")
+    _require_cuda(table, lens, q_offsets, group_offsets, shared_lens, workspace, out, dev_status)
+    _require_int32(table, lens, q_offsets, group_offsets, shared_lens)
+    if q.dim() != 3 or q.shape[2] != D or q.dtype != k_pages.dtype or \
+            q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q must be [T, Hq, D] of the pages' type, bf16 or fp16")
+    T, Hq, _ = q.shape
+    B = q_offsets.shape[0] - 1
+    if B < 0 or table.dim() != 2 or table.shape[0] < B or lens.shape[0] < B:
+        raise ValueError("q_offsets must be [B + 1] for a table [B, W] and lens [B]")
+    G = 0 if group_offsets is None else group_offsets.shape[0] - 1
+    if G < 0 or (G > 0 and (shared_lens is None or shared_lens.shape[0] != G)):
+        raise ValueError("group_offsets must be [G + 1] and shared_lens [G]")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    elif tuple(out.shape) != (T, Hq, D) or out.dtype != q.dtype:
+        raise ValueError("out must be [T, Hq, D] of q's type")
+    if workspace is None:
+        workspace = torch.empty(
+            max(w4_attn_shared_prefix_workspace_size(T, B, G, max_q, Hq, Hkv, D), 256)
+            if Hkv and Hq % Hkv == 0 else 256, dtype=torch.uint8, device=q.device)
+    _check(load_library().w4_attn_shared_prefix(
+        _ptr(q), q.stride(0), q.stride(1), _ptr(k_pages), _ptr(v_pages), *k_pages.stride()[:3], P,
+        page, _ptr(table), table.shape[1], _ptr(lens), _ptr(q_offsets), T, B, max_q,
+        _ptr(group_offsets), _ptr(shared_lens), G, Hq, Hkv, D,
+        0 if q.dtype == torch.bfloat16 else 1, int(causal), D ** -0.5 if scale is None else scale,
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out),
+        _ptr(dev_status), _stream(stream)), "w4_attn_shared_prefix")
+    return out

@@ -1051,6 +1051,100 @@ int w4_kv_append(uint16_t *k_pages, uint16_t *v_pages, int64_t page_stride, int6
     return err == cudaSuccess ? W4_OK : cuda_fail(err, "kv_append launch");
 }
 
+// ---------------------------------------------------------------- attention
+size_t w4_attn_shared_prefix_workspace_size(int T, int B, int G, int max_q, int Hq, int Hkv, int D)
+{
+    if (T < 0 || B < 0 || G < 0 || max_q <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0)
+        return 0;
+    return w4::attn_workspace_bytes(T, B, G, max_q, Hq, Hkv, D);
+}
+
+int w4_attn_shared_prefix(const uint16_t *q, int64_t q_tok_stride, int64_t q_head_stride,
+                          const uint16_t *k_pages, const uint16_t *v_pages, int64_t page_stride,
+                          int64_t tok_stride, int64_t head_stride, int P, int page_size,
+                          const int32_t *table, int W, const int32_t *lens,
+                          const int32_t *q_offsets, int T, int B, int max_q,
+                          const int32_t *group_offsets, const int32_t *shared_lens, int G, int Hq,
+                          int Hkv, int D, int dtype, int causal, float scale, void *workspace,
+                          size_t workspace_bytes, uint16_t *out, int32_t *dev_status,
+                          w4_stream_t stream)
+{
+    if (T < 0 || B < 0 || G < 0 || max_q <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || P <= 0 ||
+        W <= 0 || (dtype != 0 && dtype != 1))
+        return fail(W4_ERR_INVALID_ARG, "bad sizes or dtype (T=%d B=%d G=%d max_q=%d Hq=%d Hkv=%d "
+                    "D=%d P=%d W=%d dtype=%d)", T, B, G, max_q, Hq, Hkv, D, P, W, dtype);
+    if (!(scale > 0.0f) || scale > 1e30f)
+        return fail(W4_ERR_INVALID_ARG, "scale must be positive and finite");
+    if (D != 64 && D != 128)
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "D must be 64 or 128 (got %d)", D);
+    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "page_size must be 16, 32, 64 or 128 (got %d)",
+                    page_size);
+    if (Hq % Hkv)
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "Hkv must divide Hq (%d, %d)", Hkv, Hq);
+    if (static_cast<int64_t>(B) + G > 4096)
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "need B + G <= 4096 (got %d + %d)", B, G);
+    const int64_t rows = static_cast<int64_t>(T) * Hq;
+    const int64_t keys = static_cast<int64_t>(W) * page_size;
+    const int64_t items = 2 * (rows / 128 + 1) + (static_cast<int64_t>(B) + G) * Hkv;
+    if (rows * D >= (1ll << 31) || keys >= (1ll << 30) || items * (keys / 128 + 2) >= (1ll << 31) ||
+        static_cast<int64_t>(max_q) * Hq >= (1ll << 30))
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "problem too large for 32-bit counts");
+    if (T == 0 || B == 0)
+        return W4_OK;
+    if (!q || !k_pages || !v_pages || !table || !lens || !q_offsets || !out ||
+        (G > 0 && (!group_offsets || !shared_lens)))
+        return fail(W4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) ||
+        (q_tok_stride | q_head_stride | page_stride | tok_stride | head_stride) & 7)
+        return fail(W4_ERR_MISALIGNED, "q, the pages and out must be 16-byte aligned and strides "
+                                       "multiples of 8 elements");
+    if (!aligned4(table) || !aligned4(lens) || !aligned4(q_offsets) || !aligned4(group_offsets) ||
+        !aligned4(shared_lens))
+        return fail(W4_ERR_MISALIGNED, "index arrays must be 4-byte aligned");
+    if (page_stride <= 0 || tok_stride <= 0 || head_stride <= 0)
+        return fail(W4_ERR_INVALID_ARG, "the pages' strides must be positive");
+    const size_t need = w4_attn_shared_prefix_workspace_size(T, B, G, max_q, Hq, Hkv, D);
+    if (!workspace || workspace_bytes < need)
+        return fail(W4_ERR_WORKSPACE, "workspace needs %zu bytes", need);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return fail(W4_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+    if (int rc = check_device())
+        return rc;
+    w4::AttnProblem p{};
+    p.q = q;
+    p.q_tok = q_tok_stride;
+    p.q_head = q_head_stride;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.page_stride = page_stride;
+    p.tok_stride = tok_stride;
+    p.head_stride = head_stride;
+    p.table = table;
+    p.lens = lens;
+    p.q_offsets = q_offsets;
+    p.group_offsets = group_offsets;
+    p.shared = shared_lens;
+    p.workspace = workspace;
+    p.out = out;
+    p.dev_status = dev_status;
+    p.T = T;
+    p.B = B;
+    p.G = G;
+    p.W = W;
+    p.P = P;
+    p.page = page_size;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.max_q = max_q;
+    p.causal = causal != 0;
+    p.bf16 = dtype == 0;
+    p.scale = scale;
+    cudaError_t err = w4::launch_attn(p, as_stream(stream));
+    return err == cudaSuccess ? W4_OK : cuda_fail(err, "attention launch");
+}
+
 // ------------------------------------------------------------------ RMSNorm
 int w4_rmsnorm(const uint16_t *x, const uint16_t *weight, int M, int d, float eps, uint16_t *y,
                w4_stream_t stream)

@@ -1,0 +1,1092 @@
+// attention.cu -- attention over a paged cache for a batch whose sequences
+// share a prefix, the prefix computed once for all of them:
+//   o = sum_l p_l v_l / sum_l p_l,  p_l = exp(scale q.k_l - m)
+// over the keys l that a query sees.
+//
+// Per kv head, the queries of a whole group of sequences (and of the query
+// heads that share the kv head) are the rows of one matrix against the
+// prefix's keys; each sequence's own rows meet only its own keys.  Both kinds
+// of work are the same tile step, S = Q K^T and O += P V on tcgen05 with 128
+// rows x 128 keys, so a K or V tile is read from HBM once whatever the number
+// of rows, and a step with few valid rows costs no more than the memory time
+// of its 64 KB tile.
+//
+// An entry is a group's prefix or a sequence's own keys; an item is an entry's
+// row tile for one kv head.  Entries with more rows than any one sequence has,
+// or than 128, are taken as pairs: two 128-row tiles of one CTA against the
+// same K and V tile.  The tiles of
+// all pair items laid end to end are split evenly over the CTAs, those of all
+// single items over the CTAs' two streams, wherever item borders fall; each
+// piece leaves unnormalised sums with their maximum and denominator, which a
+// second kernel joins per row.  So one long prefix fills the GPU as evenly as
+// a thousand short ones.  The split follows from the lengths, which live on
+// the device: every CTA works it out for itself (a scan over the entries).
+//
+// Roles of a CTA's eleven warps: warps 0-3 and 4-7 are the softmax of streams
+// 0 and 1 (a thread per row), warp 8 loads K and V by TMA into a ring of
+// slots, warps 9 and 10 issue the MMAs of streams 0 and 1.  While one stream's
+// softmax runs the tensor cores work for the other.
+#include <algorithm>
+#include <atomic>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "../../include/w4moe.h"
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace w4 {
+
+namespace {
+
+constexpr int kRows = 128;                 // rows of a stream's tile
+constexpr int kKeys = 128;                 // keys of a tile
+constexpr int kThreads = 32 * 11;
+constexpr int kMaxEntries = 4096;
+
+// A group's prefix (first G) or a sequence's own keys.
+struct Entry {
+    int tile0, item0;                      // before it, in its region
+    int tiles;                             // of one item
+    int row_tiles;                         // items per kv head
+    int pair;
+    int pad;
+};
+
+struct Totals {
+    int tiles[2], items[2];                // of single [0] and pair [1] items
+};
+
+// A worker's piece of one item.
+struct Seg {
+    int row_of_table, kbase;               // where its keys are: absolute position of tile 0
+    int k0, k1;                            // the entry's keys
+    int tile0, tiles;                      // this piece's tiles
+    int row0, rows;                        // its rows (of the entry), both streams' in a pair
+    int tok0;                              // the entry's first token
+    int seq;                               // the sequence, or -1 for a group's prefix
+    int head;                              // kv head
+    int piece;                             // where its sums go; -1: nowhere
+};
+
+struct AttnArgs {
+    CUtensorMap k_map, v_map;              // [P][Hkv][page][D], box 1 x 1 x page x 64
+    const uint16_t *q;
+    uint16_t *out;
+    const int32_t *table, *lens, *q_offsets, *group_offsets, *shared;
+    int32_t *status;
+    Seg *segs;                      // workspace: the pieces of all workers
+    Entry *entries;                 // workspace: for the joining kernel
+    Totals *totals;
+    float *part_a, *part_b;                // workspace: pieces of pair / single items
+    float2 *ml_a, *ml_b;                   // and their rows' maximum and denominator
+    int64_t q_tok, q_head;
+    float scale_log2;
+    uint64_t wait_ns;
+    int T, B, G, W, P, page, Hq, Hkv, rep, max_q, causal;
+    int rows_b;                            // a single item's rows at most: min(rep max_q, 128)
+    int cap_a, cap_b;                      // pieces that the workspace holds
+};
+
+__host__ __device__ inline int64_t worker_begin(int64_t tiles, int workers, int w)
+{
+    return tiles * w / workers;
+}
+// The worker that a tile belongs to.
+__host__ __device__ inline int worker_of(int64_t tiles, int workers, int64_t tile)
+{
+    return static_cast<int>(((tile + 1) * workers - 1) / tiles);
+}
+// No worker goes without a tile.
+__host__ __device__ inline int workers_for(int tiles, int most) { return tiles < most ? tiles : most; }
+
+// ------------------------------------------------------------- tensor memory
+// All 128 columns of this thread's lane, and the wait for them.
+__device__ __forceinline__ void tmem_ld_32x32b_x128(uint32_t taddr, uint32_t (&r)[128])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
+        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
+          "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
+          "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
+          "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
+          "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
+          "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
+          "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
+          "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
+          "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+        : "r"(taddr)
+        : "memory");
+}
+
+// D (+)= A B^T with both operands in shared memory, by one elected lane.
+__device__ __forceinline__ void mma_ss_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// A 128-byte-swizzled operand whose contiguous axis is N (V: a token's
+// values): 64 values x 8 tokens to an atom of 1024 bytes, 8-token groups
+// 1024 bytes apart, 64-value blocks `block` bytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t addr, uint32_t block)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(block >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                            int w, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool BF16> __device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    uint32_t r;
+    if constexpr (BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// -------------------------------------------------------------------- plan
+// Whether the offsets ascend within their bounds; nothing is done if not, so
+// what follows may rely on it.  Called by the whole CTA.
+__device__ __forceinline__ bool offsets_ascend(const AttnArgs &p)
+{
+    bool bad = false;
+    for (int i = threadIdx.x; i < p.B; i += blockDim.x) {
+        const int a = p.q_offsets[i], b = p.q_offsets[i + 1];
+        bad |= a < 0 || b < a || b > p.T;
+    }
+    for (int i = threadIdx.x; i < p.G; i += blockDim.x) {
+        const int a = p.group_offsets[i], b = p.group_offsets[i + 1];
+        bad |= a < 0 || b < a || b > p.B;
+    }
+    return !__syncthreads_or(bad);
+}
+
+// What an entry asks for: no tokens where there are more than max_q.
+struct Want {
+    int tok0, tokens, k0, k1;
+};
+
+// The shared length of group g, never beyond its first sequence.
+__device__ __forceinline__ int shared_of(const AttnArgs &p, int g)
+{
+    const int first = p.group_offsets[g];
+    if (first < 0 || first >= p.B)
+        return 0;
+    return max(0, min(min(p.shared[g], p.lens[first]), p.W * p.page));
+}
+
+// The group of sequence b, or -1: the last whose first sequence is <= b, if
+// b lies before its end.
+__device__ __forceinline__ int group_of(const AttnArgs &p, int b)
+{
+    int lo = 0, hi = p.G - 1;
+    if (p.G == 0 || p.group_offsets[0] > b)
+        return -1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.group_offsets[mid] <= b)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return b < p.group_offsets[lo + 1] ? lo : -1;
+}
+
+__device__ __forceinline__ Want want_of(const AttnArgs &p, int e, bool flag)
+{
+    Want w{0, 0, 0, 0};
+    bool ok = true;
+    if (e < p.G) {
+        const int b0 = p.group_offsets[e], b1 = p.group_offsets[e + 1];
+        w.tok0 = p.q_offsets[b0];
+        w.tokens = p.q_offsets[b1] - w.tok0;
+        ok = w.tokens <= static_cast<int64_t>(b1 - b0) * p.max_q;
+        w.k1 = b1 > b0 ? shared_of(p, e) : 0;
+    } else {
+        const int b = e - p.G, g = group_of(p, b), len = p.lens[b];
+        w.tok0 = p.q_offsets[b];
+        w.tokens = p.q_offsets[b + 1] - w.tok0;
+        ok = w.tokens <= p.max_q;
+        w.k1 = min(max(len, 0), p.W * p.page);
+        w.k0 = g >= 0 ? min(shared_of(p, g), w.k1) : 0;
+        if (w.k1 != len && flag && p.status)
+            atomicOr(p.status, W4_DEV_BAD_SLOT);
+    }
+    if (!ok)
+        w.tokens = 0;
+    if (!ok && flag && p.status)
+        atomicOr(p.status, W4_DEV_BAD_SLOT);
+    return w;
+}
+
+__device__ __forceinline__ Entry entry_of(const AttnArgs &p, const Want &w)
+{
+    Entry e{};
+    const int rows = w.tokens * p.rep;
+    if (rows > 0 && w.k1 > w.k0) {
+        const int base = w.k0 / p.page * p.page;
+        e.tiles = (w.k1 - base + kKeys - 1) / kKeys;
+        e.pair = rows > p.rows_b;
+        e.row_tiles = e.pair ? (rows + 2 * kRows - 1) / (2 * kRows) : 1;
+    }
+    return e;
+}
+
+// Exclusive sums of four counts over the CTA's threads.
+__device__ __forceinline__ int4 scan4(int4 v, int4 *sums, int4 *total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int4 s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, s.x, o), y = __shfl_up_sync(0xffffffffu, s.y, o);
+        const int z = __shfl_up_sync(0xffffffffu, s.z, o), w = __shfl_up_sync(0xffffffffu, s.w, o);
+        if (lane >= o) {
+            s.x += x;
+            s.y += y;
+            s.z += z;
+            s.w += w;
+        }
+    }
+    if (lane == 31)
+        sums[warp] = s;
+    __syncthreads();
+    int4 before = make_int4(0, 0, 0, 0), all = before;
+    for (int i = 0; i < kThreads / 32; i++) {
+        const int4 u = sums[i];
+        if (i < warp) {
+            before.x += u.x;
+            before.y += u.y;
+            before.z += u.z;
+            before.w += u.w;
+        }
+        all.x += u.x;
+        all.y += u.y;
+        all.z += u.z;
+        all.w += u.w;
+    }
+    *total = all;
+    return make_int4(before.x + s.x - v.x, before.y + s.y - v.y, before.z + s.z - v.z,
+                     before.w + s.w - v.w);
+}
+
+// The entry that tile (or item) x of a region belongs to: the last with a
+// running count <= x, for entries with nothing in the region carry the count
+// on and the owner's successor has more than x.
+__device__ __forceinline__ int find_entry(const int *start, int n, int x)
+{
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (start[mid] <= x)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+template <int D, bool BF16>
+struct Kernel {
+    static constexpr int kBlocks = D / 64;                     // 128-byte column blocks
+    static constexpr int kTileBytes = kKeys * D * 2;           // a K, V or Q tile
+    static constexpr int kSlots = 160 * 1024 / kTileBytes;
+    static constexpr int kQBytes = 2 * kTileBytes;
+    static constexpr int kRingBytes = kSlots * kTileBytes;
+    static constexpr size_t kSmem = 1024 + kQBytes + kRingBytes;
+    static constexpr uint32_t kS = 0, kO = 256;                // TMEM columns of stream 0
+    static constexpr uint32_t kQk = idesc_16bit_f32(128, kKeys, BF16);
+    static constexpr uint32_t kPv = idesc_16bit_f32(128, D, BF16) | (1u << 16);   // V is N-major
+
+    struct Shared {
+        alignas(8) uint64_t full[kSlots], empty[kSlots];
+        uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2];
+        uint32_t tmem;
+        int abort_flag;
+        int seg0[3], segs[3], tiles[3];        // single items of streams 0 and 1; pairs
+        int4 sums[kThreads / 32];
+    };
+
+    // The plan: this CTA's pieces into the workspace.  Scratch is the ring,
+    // before anything is loaded into it.
+    static __device__ void plan(const AttnArgs &p, Shared &s, uint8_t *scratch)
+    {
+        const int n = p.G + p.B, tid = threadIdx.x;
+        const bool sane = offsets_ascend(p);
+        if (!sane && tid == 0 && blockIdx.x == 0 && p.status)
+            atomicOr(p.status, W4_DEV_BAD_SLOT);
+        // running counts before each entry: tiles and items, singles and pairs
+        int *start = reinterpret_cast<int *>(scratch);          // [4][n]
+        const int run = (n + kThreads - 1) / kThreads, e0 = min(n, tid * run);
+        const int e1 = min(n, e0 + run);
+        int4 sum = make_int4(0, 0, 0, 0);
+        for (int e = e0; e < e1; e++) {
+            const Entry en = sane ? entry_of(p, want_of(p, e, blockIdx.x == 0)) : Entry{};
+            const int items = en.row_tiles * p.Hkv;
+            (en.pair ? sum.z : sum.x) += items * en.tiles;
+            (en.pair ? sum.w : sum.y) += items;
+        }
+        int4 total;
+        int4 at = scan4(sum, s.sums, &total);
+        for (int e = e0; e < e1; e++) {
+            Entry en = sane ? entry_of(p, want_of(p, e, false)) : Entry{};
+            const int items = en.row_tiles * p.Hkv;
+            start[e] = at.x;
+            start[n + e] = at.y;
+            start[2 * n + e] = at.z;
+            start[3 * n + e] = at.w;
+            if (blockIdx.x == 0) {
+                en.tile0 = en.pair ? at.z : at.x;
+                en.item0 = en.pair ? at.w : at.y;
+                p.entries[e] = en;
+            }
+            (en.pair ? at.z : at.x) += items * en.tiles;
+            (en.pair ? at.w : at.y) += items;
+        }
+        if (blockIdx.x == 0 && tid == 0) {
+            p.totals->tiles[0] = total.x;
+            p.totals->items[0] = total.y;
+            p.totals->tiles[1] = total.z;
+            p.totals->items[1] = total.w;
+        }
+        __syncthreads();
+        for (int which = 0; which < 3; which++) {
+            const bool pair = which == 2;
+            const int tiles = pair ? total.z : total.x;
+            const int workers = workers_for(tiles, pair ? gridDim.x : 2 * gridDim.x);
+            const int w = pair ? blockIdx.x : 2 * blockIdx.x + which;
+            const int *ts = start + (pair ? 2 * n : 0), *is = start + (pair ? 3 * n : n);
+            int first = 0, count = 0, lo = 0, hi = 0;
+            if (w < workers) {
+                lo = static_cast<int>(worker_begin(tiles, workers, w));
+                hi = static_cast<int>(worker_begin(tiles, workers, w + 1));
+                const int ea = find_entry(ts, n, lo);
+                const int eb = find_entry(ts, n, hi - 1);
+                const Entry a = entry_of(p, want_of(p, ea, false));
+                const Entry b = entry_of(p, want_of(p, eb, false));
+                first = is[ea] + (lo - ts[ea]) / a.tiles;
+                count = is[eb] + (hi - 1 - ts[eb]) / b.tiles - first + 1;
+            }
+            // pieces are numbered by item + worker, which no two share
+            Seg *segs = p.segs + (pair ? p.cap_b : 0);
+            const int cap = pair ? p.cap_a : p.cap_b;
+            if (tid == 0) {
+                const bool fits = first + w + count <= cap;
+                s.seg0[which] = first + w;
+                s.segs[which] = fits ? count : 0;
+                if (!fits && p.status)
+                    atomicOr(p.status, W4_DEV_BAD_SLOT);
+                s.tiles[which] = 0;
+            }
+            __syncthreads();
+            for (int i = tid; i < s.segs[which]; i += kThreads) {
+                const int item = first + i, e = find_entry(is, n, item);
+                const Want wa = want_of(p, e, false);
+                const Entry en = entry_of(p, wa);
+                const int local = item - is[e];
+                const int t0 = ts[e] + local * en.tiles;         // the item's first tile
+                Seg g;
+                g.seq = e < p.G ? -1 : e - p.G;
+                g.row_of_table = e < p.G ? p.group_offsets[e] : e - p.G;
+                g.k0 = wa.k0;
+                g.k1 = wa.k1;
+                g.kbase = wa.k0 / p.page * p.page;
+                g.tok0 = wa.tok0;
+                g.head = local / en.row_tiles;
+                const int step = (pair ? 2 : 1) * kRows, all = wa.tokens * p.rep;
+                g.row0 = (local % en.row_tiles) * step;
+                g.rows = min(step, all - g.row0);
+                g.tile0 = max(lo - t0, 0);
+                int end = min(hi - t0, en.tiles);
+                if (p.causal && g.seq >= 0) {
+                    // no row of this item sees beyond its last token's position
+                    const int last = (g.row0 + g.rows - 1) / p.rep;
+                    const int limit = wa.k1 - wa.tokens + last + 1;
+                    end = min(end, (max(limit - g.kbase, 0) + kKeys - 1) / kKeys);
+                }
+                g.tiles = max(end - g.tile0, 0);
+                g.piece = item + w;
+                segs[g.piece] = g;
+                atomicAdd(&s.tiles[which], g.tiles);
+            }
+        }
+        __syncthreads();
+    }
+
+    // The pair of slots (K, then V) of a stream's tile `r` of its single items
+    // or of a pair's tile r: the loader takes the pairs first, then the
+    // streams' tiles in turn, and a stream that has none left drops out.
+    static __device__ __forceinline__ int fill_of(const Shared &s, int which, int r)
+    {
+        if (which == 2)
+            return r;
+        return s.tiles[2] + r + (which == 0 ? min(r, s.tiles[1]) : min(r + 1, s.tiles[0]));
+    }
+
+    static __device__ __forceinline__ bool wait(const AttnArgs &p, Shared &s, uint64_t *bar,
+                                                uint32_t parity)
+    {
+        return mbar_wait_warp(bar, parity, &s.abort_flag, p.status, kDevPipelineTimeout,
+                              p.wait_ns);
+    }
+
+    // ------------------------------------------------------------- loading
+    static __device__ void load_slot(const AttnArgs &p, Shared &s, uint8_t *ring, int fill,
+                                     const CUtensorMap *map, const Seg &g, int page_id,
+                                     bool shared_by_both, int lane)
+    {
+        const int slot = fill % kSlots, use = fill / kSlots;
+        if (use > 0)
+            wait(p, s, &s.empty[slot], (use - 1) & 1);
+        uint8_t *dst = ring + slot * kTileBytes;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&s.full[slot], kTileBytes);
+            if (!shared_by_both)               // the stream that does not use it
+                mbar_arrive(&s.empty[slot]);
+        }
+        __syncwarp();
+        const int boxes = kKeys / p.page * kBlocks;
+        const int pg = __shfl_sync(0xffffffffu, page_id, lane / kBlocks);
+        if (lane < boxes)
+            tma_load_4d(dst + (lane % kBlocks) * (kKeys * 128) + (lane / kBlocks) * p.page * 128,
+                        map, (lane % kBlocks) * 64, 0, g.head, pg, &s.full[slot]);
+    }
+
+    // Tile t of a piece: its pages' ids (P, which reads as zeros, past the
+    // entry's keys and for an id that is none), then its K and its V.
+    static __device__ void load_tile(const AttnArgs &p, Shared &s, uint8_t *ring, int fill,
+                                     const Seg &g, int t, bool shared_by_both, int lane)
+    {
+        const int key = g.kbase + t * kKeys + lane * p.page;
+        int id = p.P;
+        if (lane < kKeys / p.page && key < g.k1) {
+            const int got = __ldg(p.table + static_cast<int64_t>(g.row_of_table) * p.W +
+                                  key / p.page);
+            if (got >= 0 && got < p.P)
+                id = got;
+            else if (p.status)
+                atomicOr(p.status, W4_DEV_BAD_PAGE);
+        }
+        load_slot(p, s, ring, 2 * fill, &p.k_map, g, id, shared_by_both, lane);
+        load_slot(p, s, ring, 2 * fill + 1, &p.v_map, g, id, shared_by_both, lane);
+    }
+
+    // The pieces of a worker in turn, tile by tile.
+    struct Walk {
+        const Seg *next;
+        int left, t, end;                      // pieces behind this one; tile, its end
+        Seg g;
+        __device__ __forceinline__ bool more()
+        {
+            while (t >= end) {
+                if (left == 0)
+                    return false;
+                g = *next++;
+                left--;
+                t = g.tile0;
+                end = g.tile0 + g.tiles;
+            }
+            return true;
+        }
+    };
+
+    static __device__ __forceinline__ Walk walk(const AttnArgs &p, const Shared &s, int which)
+    {
+        Walk w;
+        w.next = p.segs + (which == 2 ? p.cap_b : 0) + s.seg0[which];
+        w.left = s.segs[which];
+        w.t = w.end = 0;
+        return w;
+    }
+
+    static __device__ void loader(const AttnArgs &p, Shared &s, uint8_t *ring, int lane)
+    {
+        int fill = 0;
+        for (Walk w = walk(p, s, 2); w.more(); w.t++)
+            load_tile(p, s, ring, fill++, w.g, w.t, true, lane);
+        Walk w0 = walk(p, s, 0), w1 = walk(p, s, 1);
+        for (bool go = true; go;) {
+            go = false;
+            if (w0.more()) {
+                load_tile(p, s, ring, fill++, w0.g, w0.t++, false, lane);
+                go = true;
+            }
+            if (w1.more()) {
+                load_tile(p, s, ring, fill++, w1.g, w1.t++, false, lane);
+                go = true;
+            }
+        }
+    }
+
+    // ------------------------------------------------------------- issuing
+    // One stream's MMAs: S = Q K^T of a tile, then, when its P is there,
+    // O (+)= P V.  The next tile's S overwrites this one's P: MMAs of one
+    // thread complete in order.
+    static __device__ void issuer(const AttnArgs &p, Shared &s, uint8_t *qbuf, uint8_t *ring,
+                                  int stream)
+    {
+        const uint32_t ts = s.tmem + kS + 128 * stream, to = s.tmem + kO + D * stream;
+        const uint64_t qd = sdesc_sw128(smem_u32(qbuf + stream * kTileBytes));
+        uint32_t seg_phase = 0, tile_phase = 0;
+        for (int pass = 0; pass < 2; pass++) {
+            const int which = pass == 0 ? 2 : stream;
+            const Seg *segs = p.segs + (which == 2 ? p.cap_b : 0) + s.seg0[which];
+            for (int i = 0, r = 0; i < s.segs[which]; i++) {
+                const int tiles = segs[i].tiles, tile0 = segs[i].tile0;
+                const int keys = segs[i].k1 - segs[i].kbase;
+                if (tiles == 0)
+                    continue;
+                wait(p, s, &s.q_ready[stream], seg_phase);
+                seg_phase ^= 1;
+                for (int t = 0; t < tiles; t++, r++) {
+                    const int fill = 2 * fill_of(s, which, r);
+                    const int ks = fill % kSlots, vs = (fill + 1) % kSlots;
+                    wait(p, s, &s.full[ks], (fill / kSlots) & 1);
+                    tc_fence_after();
+                    const uint64_t kd = sdesc_sw128(smem_u32(ring + ks * kTileBytes));
+#pragma unroll
+                    for (int k = 0; k < D / 16; k++) {
+                        const int off = (k / 4) * (kKeys * 128 >> 4) + (k % 4) * 2;
+                        mma_ss_elect(ts, qd + off, kd + off, kQk, k > 0);
+                    }
+                    tc_commit_elect(&s.s_full[stream]);
+                    tc_commit_elect(&s.empty[ks]);
+                    wait(p, s, &s.p_ready[stream], tile_phase);
+                    tile_phase ^= 1;
+                    wait(p, s, &s.full[vs], ((fill + 1) / kSlots) & 1);
+                    tc_fence_after();
+                    const uint32_t va = smem_u32(ring + vs * kTileBytes);
+                    // 16 keys at a time; what lies 16 or more past the end stays out
+                    const int steps = (min(keys - (tile0 + t) * kKeys, kKeys) + 15) / 16;
+                    for (int k = 0; k < steps; k++)
+                        tc_mma_ts_elect(to, ts + 8 * k, sdesc_mn_sw128(va + k * 2048, kKeys * 128),
+                                        kPv, t > 0 || k > 0);
+                    tc_commit_elect(&s.empty[vs]);
+                    if (t == tiles - 1)
+                        tc_commit_elect(&s.o_full[stream]);
+                }
+            }
+        }
+    }
+
+    // ------------------------------------------------------------- softmax
+    // A stream's rows: Q into shared memory, P from S tile by tile, and the
+    // sums out at the end of a piece.  Thread i holds row i.
+    static __device__ void softmax(const AttnArgs &p, Shared &s, uint8_t *qbuf, uint8_t *ring,
+                                   int stream)
+    {
+        const int tid = threadIdx.x & 127, warp = tid >> 5;
+        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+        const uint32_t ts = s.tmem + lanes + kS + 128 * stream;
+        const uint32_t to = s.tmem + lanes + kO + D * stream;
+        uint8_t *q = qbuf + stream * kTileBytes;
+        uint32_t s_phase = 0, o_phase = 0;
+        for (int pass = 0; pass < 2; pass++) {
+            const int which = pass == 0 ? 2 : stream;
+            const Seg *segs = p.segs + (which == 2 ? p.cap_b : 0) + s.seg0[which];
+            for (int i = 0, r = 0; i < s.segs[which]; i++) {
+                const Seg g = segs[i];
+                const int row0 = g.row0 + (which == 2 ? stream * kRows : 0);
+                const int rows = min(max(g.row0 + g.rows - row0, 0), kRows);
+                if (g.tiles > 0)
+                    load_q(p, q, g, row0, rows, tid);
+                // this row's visible keys: [k0, limit)
+                int limit = 0;
+                if (tid < rows) {
+                    const int tok = g.tok0 + (row0 + tid) / p.rep;
+                    limit = min(limit_of(p, g, tok), g.k1);
+                }
+                fence_proxy_async_smem();
+                if (g.tiles > 0)
+                    mbar_arrive(&s.q_ready[stream]);
+                float m = -INFINITY, l = 0.0f;     // m in units of log2
+                for (int t = g.tile0; t < g.tile0 + g.tiles; t++, r++) {
+                    const int base = g.kbase + t * kKeys;
+                    wait(p, s, &s.s_full[stream], s_phase);
+                    s_phase ^= 1;
+                    tc_fence_after();
+                    tile(p, ts, to, g.k0 - base, limit - base, t > g.tile0, m, l);
+                    if (g.k1 - base < kKeys && (g.k1 & 15))
+                        clear_tail(p, s, ring, 2 * fill_of(s, which, r) + 1, g.k1 - base,
+                                   which == 2, stream, tid);
+                    tc_fence_before();
+                    mbar_arrive(&s.p_ready[stream]);
+                }
+                if (g.tiles > 0) {
+                    wait(p, s, &s.o_full[stream], o_phase);
+                    o_phase ^= 1;
+                    tc_fence_after();
+                }
+                store(p, g, which == 2, row0 - g.row0, rows, to, m, l, tid);
+            }
+        }
+    }
+
+    // Rows [row0, row0 + rows) of a piece's queries, 16 bytes a thread and
+    // step; rows past the end are zero.
+    static __device__ void load_q(const AttnArgs &p, uint8_t *q, const Seg &g, int row0, int rows,
+                                  int tid)
+    {
+        constexpr int kChunks = D / 8;
+        for (int i = tid; i < kRows * kChunks; i += 128) {
+            const int row = i / kChunks, c = i % kChunks;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < rows) {
+                const int at = row0 + row, tok = g.tok0 + at / p.rep;
+                const int head = g.head * p.rep + at % p.rep;
+                v = __ldg(reinterpret_cast<const uint4 *>(p.q + tok * p.q_tok + head * p.q_head +
+                                                          c * 8));
+            }
+            *reinterpret_cast<uint4 *>(q + (c / 8) * (kRows * 128) + row * 128 +
+                                       ((c % 8) ^ (row & 7)) * 16) = v;
+        }
+    }
+
+    // How many keys, from position 0, the query token sees.
+    static __device__ int limit_of(const AttnArgs &p, const Seg &g, int tok)
+    {
+        int b = g.seq;
+        if (b < 0) {                           // the sequence of a group that has the token
+            int lo = g.row_of_table, hi = p.B - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (p.q_offsets[mid] <= tok)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            b = lo;
+        }
+        const int len = min(max(p.lens[b], 0), p.W * p.page);
+        return p.causal ? len - (p.q_offsets[b + 1] - tok) + 1 : len;
+    }
+
+    // P of one tile from its S; columns outside [lo, hi) are masked.  m is the
+    // reference of the exponents, not always the maximum: it moves only when
+    // the maximum has outgrown it by 2^8, so O is seldom rescaled; P <= 2^8
+    // stays within fp16.  P is rounded to the values' type for the MMA (its
+    // denominator sums the unrounded).  When S is here, every MMA before it has
+    // completed, so O may be changed.
+    static __device__ __forceinline__ void tile(const AttnArgs &p, uint32_t ts, uint32_t to, int lo,
+                                                int hi, bool has_o, float &m, float &l)
+    {
+        uint32_t v[128];
+        tmem_ld_32x32b_x128(ts, v);
+        if (__any_sync(0xffffffffu, lo > 0 || hi < kKeys)) {
+#pragma unroll
+            for (int c = 0; c < 128; c++)
+                if (c < lo || c >= hi)
+                    v[c] = 0xff800000u;        // -inf
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 128; c++)
+            top[c & 3] = fmaxf(top[c & 3], __uint_as_float(v[c]));
+        const float tm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+        const bool move = tm > m + 8.0f;       // also from -inf
+        if (__any_sync(0xffffffffu, move)) {
+            const float alpha = move ? ex2(m - tm) : 1.0f;
+            m = move ? tm : m;
+            l *= alpha;
+            if (has_o)
+                rescale(to, alpha);
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;
+        float sum[4] = {};
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+                const float a = ex2(fmaf(__uint_as_float(v[c + 2 * j]), p.scale_log2, -ref));
+                const float b = ex2(fmaf(__uint_as_float(v[c + 2 * j + 1]), p.scale_log2, -ref));
+                sum[j & 3] += a + b;
+                pk[j] = pack2<BF16>(a, b);
+            }
+            tmem_st_32x32b_x16(ts + c / 2, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+    }
+
+    static __device__ __forceinline__ void rescale(uint32_t to, float alpha)
+    {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(to + c, o);
+#pragma unroll
+            for (int j = 0; j < 32; j++)
+                o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            tmem_st_32x32b_x32(to + c, o);
+        }
+        tmem_wait_st();
+    }
+
+    // Values past the last key, up to the 16-key step that it ends in: P is
+    // zero there, but memory nobody has written may hold NaN.  In a pair both
+    // streams clear, and wait for each other, before either uses the tile.
+    static __device__ void clear_tail(const AttnArgs &p, Shared &s, uint8_t *ring, int fill,
+                                      int valid, bool pair, int stream, int tid)
+    {
+        const int slot = fill % kSlots;
+        wait(p, s, &s.full[slot], (fill / kSlots) & 1);
+        uint8_t *v = ring + slot * kTileBytes;
+        const int end = (valid + 15) & ~15, n = (end - valid) * 8 * kBlocks;
+        const int at = pair ? stream * 128 + tid : tid, step = pair ? 256 : 128;
+        for (int i = at; i < n; i += step) {
+            const int row = valid + i / (8 * kBlocks), c = i % (8 * kBlocks);
+            *reinterpret_cast<uint4 *>(v + (c / 8) * (kKeys * 128) + row * 128 + (c % 8) * 16) =
+                make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        if (pair)
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+    }
+
+    // A piece's sums: [D / 4][rows][4] floats, so that a warp's rows are
+    // written side by side.
+    static __device__ void store(const AttnArgs &p, const Seg &g, bool pair, int row, int rows,
+                                 uint32_t to, float m, float l, int tid)
+    {
+        const int all = pair ? 2 * kRows : p.rows_b;
+        const int64_t base = static_cast<int64_t>(g.piece) * all;
+        if (tid < rows)
+            (pair ? p.ml_a : p.ml_b)[base + row + tid] = make_float2(m, l);
+        if (g.tiles == 0)
+            return;
+        float4 *out = reinterpret_cast<float4 *>(pair ? p.part_a : p.part_b) + base * (D / 4) + row +
+                      tid;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(to + c, o);
+            if (tid < rows) {
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    out[static_cast<int64_t>(c / 4 + j) * all] =
+                        make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                                    __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+            }
+        }
+        tc_fence_before();
+    }
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ AttnArgs p)
+{
+    using K = Kernel<D, BF16>;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    __shared__ __align__(16) typename K::Shared s;
+    uint8_t *qbuf = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    uint8_t *ring = qbuf + K::kQBytes;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    if (tid == 0) {
+        for (int i = 0; i < K::kSlots; i++) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 2);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&s.q_ready[i], kRows);
+            mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.p_ready[i], kRows);
+            mbar_init(&s.o_full[i], 1);
+        }
+        s.abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&p.k_map);
+        prefetch_tmap(&p.v_map);
+    }
+    if (warp == 8) {
+        tmem_alloc(&s.tmem, 512);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_trigger();
+    K::plan(p, s, ring);
+    fence_proxy_async_smem();              // the plan's scratch becomes the ring
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp < 8)
+        K::softmax(p, s, qbuf, ring, warp >> 2);
+    else if (warp == 8)
+        K::loader(p, s, ring, lane);
+    else
+        K::issuer(p, s, qbuf, ring, warp - 9);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(s.tmem, 512);
+    }
+}
+
+// -------------------------------------------------------------------- join
+// A row's pieces joined: CTA (b, y) takes sequence b's rows (token, head), a
+// thread four values of a row; neighbouring threads are neighbouring rows of
+// one kv head, as the pieces lie.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs p,
+                                                        int grid)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int b = blockIdx.x;
+    const int t0 = p.q_offsets[b], t1 = p.q_offsets[b + 1];
+    if (t0 < 0 || t1 <= t0 || t1 > p.T || t1 - t0 > p.max_q)
+        return;
+    const int g = group_of(p, b);
+    const int rows = (t1 - t0) * p.rep;        // of one kv head
+    const int n = rows * p.Hkv * (D / 4);
+    for (int i = blockIdx.y * 256 + threadIdx.x; i < n; i += gridDim.y * 256) {
+        const int row = i % rows, c = i / rows % (D / 4), head = i / rows / (D / 4);
+        float m = -INFINITY, l = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k = 0; k < 2; k++) {
+            const int e = k == 0 ? g : p.G + b;
+            if (e < 0)
+                continue;
+            const Entry en = p.entries[e];
+            if (en.tiles == 0)
+                continue;
+            const int pair = en.pair, step = pair ? 2 * kRows : kRows;
+            // this sequence's rows lie behind those of its group's earlier tokens
+            const int er = k == 0 ? row + (t0 - p.q_offsets[p.group_offsets[g]]) * p.rep : row;
+            const int local = head * en.row_tiles + er / step;
+            const int64_t tiles = p.totals->tiles[pair];
+            const int workers = workers_for(p.totals->tiles[pair], pair ? grid : 2 * grid);
+            const int64_t x0 = en.tile0 + static_cast<int64_t>(local) * en.tiles;
+            const int w0 = worker_of(tiles, workers, x0);
+            const int w1 = worker_of(tiles, workers, x0 + en.tiles - 1);
+            const int all = pair ? 2 * kRows : p.rows_b, at = er % step;
+            const float2 *ml = pair ? p.ml_a : p.ml_b;
+            const float4 *part = reinterpret_cast<const float4 *>(pair ? p.part_a : p.part_b);
+            if (en.item0 + local + w1 >= (pair ? p.cap_a : p.cap_b))
+                continue;
+            for (int w = w0; w <= w1; w++) {
+                const int64_t base = static_cast<int64_t>(en.item0 + local + w) * all;
+                const float2 s = ml[base + at];
+                if (!(s.y > 0.0f) && s.y == s.y)
+                    continue;                  // nothing visible in this piece
+                const float4 v = part[base * (D / 4) + static_cast<int64_t>(c) * all + at];
+                const float nm = fmaxf(m, s.x);
+                const float fa = ex2(m - nm), fb = ex2(s.x - nm);
+                m = nm;
+                l = l * fa + s.y * fb;
+                o.x = o.x * fa + v.x * fb;
+                o.y = o.y * fa + v.y * fb;
+                o.z = o.z * fa + v.z * fb;
+                o.w = o.w * fa + v.w * fb;
+            }
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;     // a row that sees nothing is zero
+        const int tok = t0 + row / p.rep, h = head * p.rep + row % p.rep;
+        uint2 r;
+        r.x = pack2<BF16>(o.x * inv, o.y * inv);
+        r.y = pack2<BF16>(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(tok) * p.Hq + h) * D + 4 * c) = r;
+    }
+}
+
+using EncodeFn = decltype(&cuTensorMapEncodeTiled);
+
+EncodeFn encode_fn()
+{
+    static EncodeFn fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                             cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<EncodeFn>(ptr);
+    }();
+    return fn;
+}
+
+bool encode_pages(CUtensorMap *map, const AttnProblem &q, const uint16_t *base)
+{
+    const cuuint64_t dim[4] = {static_cast<cuuint64_t>(q.D), static_cast<cuuint64_t>(q.page),
+                               static_cast<cuuint64_t>(q.Hkv), static_cast<cuuint64_t>(q.P)};
+    const cuuint64_t stride[3] = {static_cast<cuuint64_t>(q.tok_stride) * 2,
+                                  static_cast<cuuint64_t>(q.head_stride) * 2,
+                                  static_cast<cuuint64_t>(q.page_stride) * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(q.page), 1, 1};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    return encode_fn()(map, q.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                       4, const_cast<uint16_t *>(base), dim, stride, box, step,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Where a call's pieces lie in its workspace.
+struct Space {
+    int cap_a, cap_b, rows_b;
+    size_t totals, entries, segs, ml_a, ml_b, part_a, part_b, total;
+};
+
+constexpr int kMaxGrid = 256;              // CTAs that a workspace allows for
+
+Space space_of(int T, int B, int G, int max_q, int Hq, int Hkv, int D)
+{
+    Space s{};
+    const int64_t rep = Hq / Hkv;
+    // A row is in two entries, and an entry of R rows has at most R / 256 + 1
+    // pair items (R / 128 where it is a sequence: R > 128 then).  Each worker
+    // cuts at most one item more.
+    s.cap_a = static_cast<int>(std::min<int64_t>((2 * T * rep / kRows + G + 1) * Hkv, 1 << 24)) +
+              kMaxGrid;
+    s.cap_b = (B + G) * Hkv + 2 * kMaxGrid;
+    s.rows_b = static_cast<int>(std::min<int64_t>(rep * max_q, kRows));
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    s.totals = take(sizeof(Totals));
+    s.entries = take(sizeof(Entry) * (static_cast<size_t>(B) + G));
+    s.segs = take(sizeof(Seg) * (static_cast<size_t>(s.cap_a) + s.cap_b));
+    s.ml_a = take(sizeof(float2) * static_cast<size_t>(s.cap_a) * 2 * kRows);
+    s.ml_b = take(sizeof(float2) * static_cast<size_t>(s.cap_b) * s.rows_b);
+    s.part_a = take(sizeof(float) * static_cast<size_t>(s.cap_a) * 2 * kRows * D);
+    s.part_b = take(sizeof(float) * static_cast<size_t>(s.cap_b) * s.rows_b * D);
+    s.total = at;
+    return s;
+}
+
+template <int D, bool BF16>
+cudaError_t launch_variant(const AttnArgs &a, int dev, int sms, cudaStream_t stream)
+{
+    using K = Kernel<D, BF16>;
+    auto kern = attn_kernel<D, BF16>;
+    static std::atomic<uint64_t> raised{0};      // devices whose limit is raised already
+    cudaError_t err;
+    if (!(raised.load(std::memory_order_relaxed) >> (dev & 63) & 1u)) {
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   static_cast<int>(K::kSmem));
+        if (err != cudaSuccess)
+            return err;
+        raised.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+    }
+    const int grid = std::min(sms, kMaxGrid);
+    err = launch_pdl(kern, dim3(grid), dim3(kThreads), K::kSmem, stream, a);
+    if (err != cudaSuccess)
+        return err;
+    const int64_t n = static_cast<int64_t>(a.max_q) * a.Hq * (D / 4);
+    const int y = static_cast<int>(std::min<int64_t>((n + 255) / 256, 64));
+    return launch_pdl(attn_join_kernel<D, BF16>, dim3(a.B, y), dim3(256), 0, stream, a, grid);
+}
+
+}  // namespace
+
+size_t attn_workspace_bytes(int T, int B, int G, int max_q, int Hq, int Hkv, int D)
+{
+    return space_of(T, B, G, max_q, Hq, Hkv, D).total;
+}
+
+cudaError_t launch_attn(const AttnProblem &q, cudaStream_t stream)
+{
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess)
+        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess)
+        return err;
+    AttnArgs a{};
+    if (!encode_fn())
+        return cudaErrorNotSupported;
+    if (!encode_pages(&a.k_map, q, q.k_pages) || !encode_pages(&a.v_map, q, q.v_pages))
+        return cudaErrorInvalidValue;
+    const Space s = space_of(q.T, q.B, q.G, q.max_q, q.Hq, q.Hkv, q.D);
+    uint8_t *ws = static_cast<uint8_t *>(q.workspace);
+    a.totals = reinterpret_cast<Totals *>(ws + s.totals);
+    a.entries = reinterpret_cast<Entry *>(ws + s.entries);
+    a.segs = reinterpret_cast<Seg *>(ws + s.segs);
+    a.ml_a = reinterpret_cast<float2 *>(ws + s.ml_a);
+    a.ml_b = reinterpret_cast<float2 *>(ws + s.ml_b);
+    a.part_a = reinterpret_cast<float *>(ws + s.part_a);
+    a.part_b = reinterpret_cast<float *>(ws + s.part_b);
+    a.cap_a = s.cap_a;
+    a.cap_b = s.cap_b;
+    a.rows_b = s.rows_b;
+    a.q = q.q;
+    a.out = q.out;
+    a.table = q.table;
+    a.lens = q.lens;
+    a.q_offsets = q.q_offsets;
+    a.group_offsets = q.group_offsets;
+    a.shared = q.shared;
+    a.status = q.dev_status;
+    a.q_tok = q.q_tok;
+    a.q_head = q.q_head;
+    a.scale_log2 = q.scale * 1.4426950408889634f;
+    a.wait_ns = pipeline_test_hooks().wait_ns;
+    a.T = q.T;
+    a.B = q.B;
+    a.G = q.G;
+    a.W = q.W;
+    a.P = q.P;
+    a.page = q.page;
+    a.Hq = q.Hq;
+    a.Hkv = q.Hkv;
+    a.rep = q.Hq / q.Hkv;
+    a.max_q = q.max_q;
+    a.causal = q.causal;
+    if (q.D == 128)
+        return q.bf16 ? launch_variant<128, true>(a, dev, sms, stream)
+                      : launch_variant<128, false>(a, dev, sms, stream);
+    return q.bf16 ? launch_variant<64, true>(a, dev, sms, stream)
+                  : launch_variant<64, false>(a, dev, sms, stream);
+}
+
+}  // namespace w4

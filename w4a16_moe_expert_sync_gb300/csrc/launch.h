@@ -187,6 +187,24 @@ struct KvAppend {
 };
 cudaError_t launch_kv_append(const KvAppend &p, cudaStream_t stream);
 
+// Attention over a paged cache with shared prefixes (attention.cu): two
+// launches.  Strides in elements.
+struct AttnProblem {
+    const uint16_t *q;                  // [T][Hq][D]
+    int64_t q_tok, q_head;
+    const uint16_t *k_pages, *v_pages;  // [P][page][Hkv][D]
+    int64_t page_stride, tok_stride, head_stride;
+    const int32_t *table, *lens, *q_offsets, *group_offsets, *shared;
+    void *workspace;                    // attn_workspace_bytes
+    uint16_t *out;                      // [T][Hq][D]
+    int32_t *dev_status;
+    int T, B, G, W, P, page, Hq, Hkv, D, max_q, causal;
+    bool bf16;
+    float scale;
+};
+size_t attn_workspace_bytes(int T, int B, int G, int max_q, int Hq, int Hkv, int D);
+cudaError_t launch_attn(const AttnProblem &p, cudaStream_t stream);
+
 // W4_OK when the current device is an sm_103 part, else W4_ERR_NO_DEVICE or
 // W4_ERR_CUDA with the detail recorded (the argument checks of every entry
 // point call it before launching).
