@@ -72,7 +72,7 @@ def test_ring_fills_and_releases(slots, seed):
     for n, (s, t) in enumerate(order):
         assert fill_of(tiles, s, t) == n
     full = [0] * slots               # completed phases of full[slot]
-    empty = [0] * slots              # arrivals on empty[slot], two to a phase
+    empty = [0] * slots              # completed phases of empty[slot]
     content = [None] * slots
 
     def loader():
@@ -80,39 +80,51 @@ def test_ring_fills_and_releases(slots, seed):
             for part in (0, 1):
                 n = 2 * fill + part
                 slot, use = n % slots, n // slots
-                if use:
-                    while not (empty[slot] // 2 - 1 >= use - 1):
-                        yield
-                    assert empty[slot] == 2 * use       # parity unambiguous
+                while empty[slot] < use:
+                    yield
+                assert empty[slot] == use               # parity unambiguous
                 content[slot] = (s, t, part)
-                if s != 2:
-                    empty[slot] += 1
                 yield
                 full[slot] += 1
 
-    s_full, p_ready = [0, 0], [0, 0]
+    s_full, p_ready, pairs_done = [0, 0], [0, 0], []
+
+    def use(which, t, part, last):
+        n = 2 * fill_of(tiles, which, t) + part
+        slot, count = n % slots, n // slots
+        while full[slot] < count + 1:
+            yield
+        assert full[slot] == count + 1 and content[slot] == (which, t, part)
+        if last:
+            empty[slot] += 1
+        yield
+
+    def wait_p(stream, n):
+        while p_ready[stream] < n:
+            yield
+        assert p_ready[stream] == n
 
     def issuer(stream):
-        done = 0
-        for which in (2, stream):
-            for t in range(tiles[which]):
-                n = 2 * fill_of(tiles, which, t)
-                for part in (0, 1):
-                    slot, use = (n + part) % slots, (n + part) // slots
-                    while full[slot] < use + 1:
-                        yield
-                    assert full[slot] == use + 1
-                    assert content[slot] == (which, t, part)
-                    if part == 0:
-                        s_full[stream] += 1
-                        empty[slot] += 1
-                        done += 1
-                        while p_ready[stream] < done:
-                            yield
-                        assert p_ready[stream] == done
-                    else:
-                        empty[slot] += 1
-                    yield
+        if stream == 0:
+            for t in range(tiles[2]):
+                for st in (0, 1):
+                    if t == 0:
+                        yield from use(2, 0, 0, st == 1)
+                        s_full[st] += 1
+                for st in (0, 1):
+                    yield from wait_p(st, t + 1)
+                    yield from use(2, t, 1, st == 1)
+                    if t + 1 < tiles[2]:
+                        yield from use(2, t + 1, 0, st == 1)
+                        s_full[st] += 1
+            pairs_done.append(1)
+        while not pairs_done:
+            yield
+        for t in range(tiles[stream]):
+            yield from use(stream, t, 0, True)
+            s_full[stream] += 1
+            yield from wait_p(stream, tiles[2] + t + 1)
+            yield from use(stream, t, 1, True)
 
     def softmax(stream):
         for n in range(tiles[2] + tiles[stream]):

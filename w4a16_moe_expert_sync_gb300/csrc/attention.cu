@@ -24,8 +24,8 @@
 //
 // Roles of a CTA's eleven warps: warps 0-3 and 4-7 are the softmax of streams
 // 0 and 1 (a thread per row), warp 8 loads K and V by TMA into a ring of
-// slots, warps 9 and 10 issue the MMAs of streams 0 and 1.  While one stream's
-// softmax runs the tensor cores work for the other.
+// slots, warps 9 and 10 issue the MMAs (of both streams of a pair; of streams 0
+// and 1).  While one stream's softmax runs the tensor cores work for the other.
 #include <algorithm>
 #include <atomic>
 #include <cuda_bf16.h>
@@ -50,11 +50,14 @@ struct Entry {
     int tiles;                             // of one item
     int row_tiles;                         // items per kv head
     int pair;
-    int pad;
+    int row;                               // a sequence's first row among its group's
 };
 
-struct Totals {
-    int tiles[2], items[2];                // of single [0] and pair [1] items
+// What the joining kernel needs to know of a sequence.
+struct alignas(16) Joint {
+    int tok0, tokens;                      // tokens < 0: nothing to write
+    int all[2];                            // tiles of all single [0] and pair [1] items
+    Entry e[2];                            // of its group's prefix and of its own keys
 };
 
 // A worker's piece of one item.
@@ -76,8 +79,7 @@ struct AttnArgs {
     const int32_t *table, *lens, *q_offsets, *group_offsets, *shared;
     int32_t *status;
     Seg *segs;                      // workspace: the pieces of all workers
-    Entry *entries;                 // workspace: for the joining kernel
-    Totals *totals;
+    Joint *joints;                         // workspace: [B], for the joining kernel
     float *part_a, *part_b;                // workspace: pieces of pair / single items
     float2 *ml_a, *ml_b;                   // and their rows' maximum and denominator
     int64_t q_tok, q_head;
@@ -190,20 +192,52 @@ template <bool BF16> __device__ __forceinline__ uint32_t pack2(float lo, float h
 }
 
 // -------------------------------------------------------------------- plan
+// The index arrays as the plan reads them: staged in shared memory, for its
+// searches are chains of dependent reads.
+struct Index {
+    const int *lens, *q_offsets, *group_offsets, *shared;
+};
+
 // Whether the offsets ascend within their bounds; nothing is done if not, so
 // what follows may rely on it.  Called by the whole CTA.
-__device__ __forceinline__ bool offsets_ascend(const AttnArgs &p)
+__device__ __forceinline__ bool offsets_ascend(const AttnArgs &p, const Index &x)
 {
     bool bad = false;
     for (int i = threadIdx.x; i < p.B; i += blockDim.x) {
-        const int a = p.q_offsets[i], b = p.q_offsets[i + 1];
+        const int a = x.q_offsets[i], b = x.q_offsets[i + 1];
         bad |= a < 0 || b < a || b > p.T;
     }
     for (int i = threadIdx.x; i < p.G; i += blockDim.x) {
-        const int a = p.group_offsets[i], b = p.group_offsets[i + 1];
+        const int a = x.group_offsets[i], b = x.group_offsets[i + 1];
         bad |= a < 0 || b < a || b > p.B;
     }
     return !__syncthreads_or(bad);
+}
+
+// The shared length of group g, never beyond its first sequence.
+__device__ __forceinline__ int shared_of(const AttnArgs &p, const Index &x, int g)
+{
+    const int first = x.group_offsets[g];
+    if (first >= p.B)
+        return 0;
+    return max(0, min(min(x.shared[g], x.lens[first]), p.W * p.page));
+}
+
+// The group of sequence b, or -1: the last whose first sequence is <= b, if
+// b lies before its end.
+__device__ __forceinline__ int group_of(const AttnArgs &p, const Index &x, int b)
+{
+    int lo = 0, hi = p.G - 1;
+    if (p.G == 0 || x.group_offsets[0] > b)
+        return -1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (x.group_offsets[mid] <= b)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return b < x.group_offsets[lo + 1] ? lo : -1;
 }
 
 // What an entry asks for: no tokens where there are more than max_q.
@@ -211,49 +245,23 @@ struct Want {
     int tok0, tokens, k0, k1;
 };
 
-// The shared length of group g, never beyond its first sequence.
-__device__ __forceinline__ int shared_of(const AttnArgs &p, int g)
-{
-    const int first = p.group_offsets[g];
-    if (first < 0 || first >= p.B)
-        return 0;
-    return max(0, min(min(p.shared[g], p.lens[first]), p.W * p.page));
-}
-
-// The group of sequence b, or -1: the last whose first sequence is <= b, if
-// b lies before its end.
-__device__ __forceinline__ int group_of(const AttnArgs &p, int b)
-{
-    int lo = 0, hi = p.G - 1;
-    if (p.G == 0 || p.group_offsets[0] > b)
-        return -1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.group_offsets[mid] <= b)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    return b < p.group_offsets[lo + 1] ? lo : -1;
-}
-
-__device__ __forceinline__ Want want_of(const AttnArgs &p, int e, bool flag)
+__device__ __forceinline__ Want want_of(const AttnArgs &p, const Index &x, int e, bool flag)
 {
     Want w{0, 0, 0, 0};
     bool ok = true;
     if (e < p.G) {
-        const int b0 = p.group_offsets[e], b1 = p.group_offsets[e + 1];
-        w.tok0 = p.q_offsets[b0];
-        w.tokens = p.q_offsets[b1] - w.tok0;
+        const int b0 = x.group_offsets[e], b1 = x.group_offsets[e + 1];
+        w.tok0 = x.q_offsets[b0];
+        w.tokens = x.q_offsets[b1] - w.tok0;
         ok = w.tokens <= static_cast<int64_t>(b1 - b0) * p.max_q;
-        w.k1 = b1 > b0 ? shared_of(p, e) : 0;
+        w.k1 = b1 > b0 ? shared_of(p, x, e) : 0;
     } else {
-        const int b = e - p.G, g = group_of(p, b), len = p.lens[b];
-        w.tok0 = p.q_offsets[b];
-        w.tokens = p.q_offsets[b + 1] - w.tok0;
+        const int b = e - p.G, g = group_of(p, x, b), len = x.lens[b];
+        w.tok0 = x.q_offsets[b];
+        w.tokens = x.q_offsets[b + 1] - w.tok0;
         ok = w.tokens <= p.max_q;
         w.k1 = min(max(len, 0), p.W * p.page);
-        w.k0 = g >= 0 ? min(shared_of(p, g), w.k1) : 0;
+        w.k0 = g >= 0 ? min(shared_of(p, x, g), w.k1) : 0;
         if (w.k1 != len && flag && p.status)
             atomicOr(p.status, W4_DEV_BAD_SLOT);
     }
@@ -345,7 +353,7 @@ struct Kernel {
 
     struct Shared {
         alignas(8) uint64_t full[kSlots], empty[kSlots];
-        uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2];
+        uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2], pairs_done;
         uint32_t tmem;
         int abort_flag;
         int seg0[3], segs[3], tiles[3];        // single items of streams 0 and 1; pairs
@@ -357,16 +365,30 @@ struct Kernel {
     static __device__ void plan(const AttnArgs &p, Shared &s, uint8_t *scratch)
     {
         const int n = p.G + p.B, tid = threadIdx.x;
-        const bool sane = offsets_ascend(p);
+        int *lens = reinterpret_cast<int *>(scratch), *qo = lens + p.B, *go = qo + p.B + 1;
+        int *sh = go + p.G + 1;
+        for (int i = tid; i <= p.B; i += kThreads) {
+            qo[i] = p.q_offsets[i];
+            if (i < p.B)
+                lens[i] = p.lens[i];
+        }
+        for (int i = tid; i <= p.G && p.G > 0; i += kThreads) {
+            go[i] = p.group_offsets[i];
+            if (i < p.G)
+                sh[i] = p.shared[i];
+        }
+        __syncthreads();
+        const Index x{lens, qo, go, sh};
+        const bool sane = offsets_ascend(p, x);
         if (!sane && tid == 0 && blockIdx.x == 0 && p.status)
             atomicOr(p.status, W4_DEV_BAD_SLOT);
         // running counts before each entry: tiles and items, singles and pairs
-        int *start = reinterpret_cast<int *>(scratch);          // [4][n]
+        int *start = sh + p.G;                                  // [4][n]
         const int run = (n + kThreads - 1) / kThreads, e0 = min(n, tid * run);
         const int e1 = min(n, e0 + run);
         int4 sum = make_int4(0, 0, 0, 0);
         for (int e = e0; e < e1; e++) {
-            const Entry en = sane ? entry_of(p, want_of(p, e, blockIdx.x == 0)) : Entry{};
+            const Entry en = sane ? entry_of(p, want_of(p, x, e, blockIdx.x == 0)) : Entry{};
             const int items = en.row_tiles * p.Hkv;
             (en.pair ? sum.z : sum.x) += items * en.tiles;
             (en.pair ? sum.w : sum.y) += items;
@@ -374,28 +396,25 @@ struct Kernel {
         int4 total;
         int4 at = scan4(sum, s.sums, &total);
         for (int e = e0; e < e1; e++) {
-            Entry en = sane ? entry_of(p, want_of(p, e, false)) : Entry{};
+            const Entry en = sane ? entry_of(p, want_of(p, x, e, false)) : Entry{};
             const int items = en.row_tiles * p.Hkv;
             start[e] = at.x;
             start[n + e] = at.y;
             start[2 * n + e] = at.z;
             start[3 * n + e] = at.w;
-            if (blockIdx.x == 0) {
-                en.tile0 = en.pair ? at.z : at.x;
-                en.item0 = en.pair ? at.w : at.y;
-                p.entries[e] = en;
-            }
             (en.pair ? at.z : at.x) += items * en.tiles;
             (en.pair ? at.w : at.y) += items;
         }
-        if (blockIdx.x == 0 && tid == 0) {
-            p.totals->tiles[0] = total.x;
-            p.totals->items[0] = total.y;
-            p.totals->tiles[1] = total.z;
-            p.totals->items[1] = total.w;
-        }
         __syncthreads();
-        for (int which = 0; which < 3; which++) {
+        auto placed = [&](int e) {
+            Entry en = sane ? entry_of(p, want_of(p, x, e, false)) : Entry{};
+            en.tile0 = start[(en.pair ? 2 * n : 0) + e];
+            en.item0 = start[(en.pair ? 3 * n : n) + e];
+            return en;
+        };
+        // warps 0, 1 and 2 work out the pieces of streams 0 and 1 and of the pairs
+        const int which = tid >> 5, lane = tid & 31;
+        if (which < 3) {
             const bool pair = which == 2;
             const int tiles = pair ? total.z : total.x;
             const int workers = workers_for(tiles, pair ? gridDim.x : 2 * gridDim.x);
@@ -405,34 +424,29 @@ struct Kernel {
             if (w < workers) {
                 lo = static_cast<int>(worker_begin(tiles, workers, w));
                 hi = static_cast<int>(worker_begin(tiles, workers, w + 1));
-                const int ea = find_entry(ts, n, lo);
-                const int eb = find_entry(ts, n, hi - 1);
-                const Entry a = entry_of(p, want_of(p, ea, false));
-                const Entry b = entry_of(p, want_of(p, eb, false));
-                first = is[ea] + (lo - ts[ea]) / a.tiles;
-                count = is[eb] + (hi - 1 - ts[eb]) / b.tiles - first + 1;
+                // lane 0 finds the first tile's item, lane 1 the last's
+                const int at = lane == 0 ? lo : hi - 1, e = find_entry(ts, n, at);
+                const int item = is[e] + (at - ts[e]) / entry_of(p, want_of(p, x, e, false)).tiles;
+                first = __shfl_sync(0xffffffffu, item, 0);
+                count = __shfl_sync(0xffffffffu, item, 1) - first + 1;
             }
             // pieces are numbered by item + worker, which no two share
             Seg *segs = p.segs + (pair ? p.cap_b : 0);
-            const int cap = pair ? p.cap_a : p.cap_b;
-            if (tid == 0) {
-                const bool fits = first + w + count <= cap;
-                s.seg0[which] = first + w;
-                s.segs[which] = fits ? count : 0;
-                if (!fits && p.status)
+            if (first + w + count > (pair ? p.cap_a : p.cap_b)) {
+                count = 0;
+                if (lane == 0 && p.status)
                     atomicOr(p.status, W4_DEV_BAD_SLOT);
-                s.tiles[which] = 0;
             }
-            __syncthreads();
-            for (int i = tid; i < s.segs[which]; i += kThreads) {
+            int mine = 0;
+            for (int i = lane; i < count; i += 32) {
                 const int item = first + i, e = find_entry(is, n, item);
-                const Want wa = want_of(p, e, false);
+                const Want wa = want_of(p, x, e, false);
                 const Entry en = entry_of(p, wa);
                 const int local = item - is[e];
                 const int t0 = ts[e] + local * en.tiles;         // the item's first tile
                 Seg g;
                 g.seq = e < p.G ? -1 : e - p.G;
-                g.row_of_table = e < p.G ? p.group_offsets[e] : e - p.G;
+                g.row_of_table = e < p.G ? x.group_offsets[e] : e - p.G;
                 g.k0 = wa.k0;
                 g.k1 = wa.k1;
                 g.kbase = wa.k0 / p.page * p.page;
@@ -452,7 +466,30 @@ struct Kernel {
                 g.tiles = max(end - g.tile0, 0);
                 g.piece = item + w;
                 segs[g.piece] = g;
-                atomicAdd(&s.tiles[which], g.tiles);
+                mine += g.tiles;
+            }
+            mine = __reduce_add_sync(0xffffffffu, mine);
+            if (lane == 0) {
+                s.seg0[which] = first + w;
+                s.segs[which] = count;
+                s.tiles[which] = mine;
+            }
+        } else {
+            // the others tell the joining kernel of the sequences, a share per CTA
+            for (int b = blockIdx.x + (tid - 96) * gridDim.x; b < p.B;
+                 b += (kThreads - 96) * gridDim.x) {
+                Joint j{};
+                j.tok0 = qo[b];
+                j.tokens = sane && qo[b + 1] - qo[b] <= p.max_q ? qo[b + 1] - qo[b] : -1;
+                j.all[0] = total.x;
+                j.all[1] = total.z;
+                const int g = sane ? group_of(p, x, b) : -1;
+                if (g >= 0) {
+                    j.e[0] = placed(g);
+                    j.e[0].row = (qo[b] - qo[go[g]]) * p.rep;
+                }
+                j.e[1] = placed(p.G + b);
+                p.joints[b] = j;
             }
         }
         __syncthreads();
@@ -477,43 +514,36 @@ struct Kernel {
 
     // ------------------------------------------------------------- loading
     static __device__ void load_slot(const AttnArgs &p, Shared &s, uint8_t *ring, int fill,
-                                     const CUtensorMap *map, const Seg &g, int page_id,
-                                     bool shared_by_both, int lane)
+                                     const CUtensorMap *map, int head, int page_id,
+                                     int lane)
     {
         const int slot = fill % kSlots, use = fill / kSlots;
         if (use > 0)
             wait(p, s, &s.empty[slot], (use - 1) & 1);
         uint8_t *dst = ring + slot * kTileBytes;
-        if (lane == 0) {
+        if (lane == 0)
             mbar_arrive_expect_tx(&s.full[slot], kTileBytes);
-            if (!shared_by_both)               // the stream that does not use it
-                mbar_arrive(&s.empty[slot]);
-        }
         __syncwarp();
         const int boxes = kKeys / p.page * kBlocks;
         const int pg = __shfl_sync(0xffffffffu, page_id, lane / kBlocks);
         if (lane < boxes)
             tma_load_4d(dst + (lane % kBlocks) * (kKeys * 128) + (lane / kBlocks) * p.page * 128,
-                        map, (lane % kBlocks) * 64, 0, g.head, pg, &s.full[slot]);
+                        map, (lane % kBlocks) * 64, 0, head, pg, &s.full[slot]);
     }
 
-    // Tile t of a piece: its pages' ids (P, which reads as zeros, past the
-    // entry's keys and for an id that is none), then its K and its V.
-    static __device__ void load_tile(const AttnArgs &p, Shared &s, uint8_t *ring, int fill,
-                                     const Seg &g, int t, bool shared_by_both, int lane)
+    // The id of this lane's page of tile t: P, which reads as zeros, past the
+    // entry's keys and for an id that is none.
+    static __device__ __forceinline__ int page_of(const AttnArgs &p, const Seg &g, int t, int lane)
     {
         const int key = g.kbase + t * kKeys + lane * p.page;
-        int id = p.P;
-        if (lane < kKeys / p.page && key < g.k1) {
-            const int got = __ldg(p.table + static_cast<int64_t>(g.row_of_table) * p.W +
-                                  key / p.page);
-            if (got >= 0 && got < p.P)
-                id = got;
-            else if (p.status)
-                atomicOr(p.status, W4_DEV_BAD_PAGE);
-        }
-        load_slot(p, s, ring, 2 * fill, &p.k_map, g, id, shared_by_both, lane);
-        load_slot(p, s, ring, 2 * fill + 1, &p.v_map, g, id, shared_by_both, lane);
+        if (lane >= kKeys / p.page || key >= g.k1)
+            return p.P;
+        const int id = __ldg(p.table + static_cast<int64_t>(g.row_of_table) * p.W + key / p.page);
+        if (id >= 0 && id < p.P)
+            return id;
+        if (p.status)
+            atomicOr(p.status, W4_DEV_BAD_PAGE);
+        return p.P;
     }
 
     // The pieces of a worker in turn, tile by tile.
@@ -544,72 +574,146 @@ struct Kernel {
         return w;
     }
 
+    // The tiles in the order of fill_of; a tile's page ids are read while the
+    // tile before it waits for its slots.
     static __device__ void loader(const AttnArgs &p, Shared &s, uint8_t *ring, int lane)
     {
-        int fill = 0;
-        for (Walk w = walk(p, s, 2); w.more(); w.t++)
-            load_tile(p, s, ring, fill++, w.g, w.t, true, lane);
-        Walk w0 = walk(p, s, 0), w1 = walk(p, s, 1);
-        for (bool go = true; go;) {
-            go = false;
-            if (w0.more()) {
-                load_tile(p, s, ring, fill++, w0.g, w0.t++, false, lane);
-                go = true;
+        Walk pairs = walk(p, s, 2), one = walk(p, s, 0), two = walk(p, s, 1);
+        bool first = false;                    // whose turn it was last
+        bool held = false;
+        int held_head = 0, held_id = 0, fill = 0;
+        for (bool more = true; more || held;) {
+            bool got = true;
+            int head = 0, id = 0;
+            if (pairs.more()) {
+                head = pairs.g.head;
+                id = page_of(p, pairs.g, pairs.t++, lane);
+            } else {
+                const bool a = one.more(), b = two.more();
+                first = a && !(first && b);    // streams in turn; one that is out drops out
+                if (first) {
+                    head = one.g.head;
+                    id = page_of(p, one.g, one.t++, lane);
+                } else if (b) {
+                    head = two.g.head;
+                    id = page_of(p, two.g, two.t++, lane);
+                } else {
+                    got = false;
+                }
             }
-            if (w1.more()) {
-                load_tile(p, s, ring, fill++, w1.g, w1.t++, false, lane);
-                go = true;
+            if (held) {
+                load_slot(p, s, ring, 2 * fill, &p.k_map, held_head, held_id, lane);
+                load_slot(p, s, ring, 2 * fill + 1, &p.v_map, held_head, held_id, lane);
+                fill++;
             }
+            more = held = got;
+            held_head = head;
+            held_id = id;
         }
     }
 
     // ------------------------------------------------------------- issuing
-    // One stream's MMAs: S = Q K^T of a tile, then, when its P is there,
-    // O (+)= P V.  The next tile's S overwrites this one's P: MMAs of one
-    // thread complete in order.
+    // S = Q K^T of a stream's tile; its K is let go with the last use.
+    static __device__ __forceinline__ void issue_qk(const AttnArgs &p, Shared &s, uint8_t *qbuf,
+                                                    uint8_t *ring, int stream, int fill, bool last_use)
+    {
+        const int slot = fill % kSlots;
+        wait(p, s, &s.full[slot], (fill / kSlots) & 1);
+        tc_fence_after();
+        const uint64_t qd = sdesc_sw128(smem_u32(qbuf + stream * kTileBytes));
+        const uint64_t kd = sdesc_sw128(smem_u32(ring + slot * kTileBytes));
+#pragma unroll
+        for (int k = 0; k < D / 16; k++) {
+            const int off = (k / 4) * (kKeys * 128 >> 4) + (k % 4) * 2;
+            mma_ss_elect(s.tmem + kS + 128 * stream, qd + off, kd + off, kQk, k > 0);
+        }
+        tc_commit_elect(&s.s_full[stream]);
+        if (last_use)
+            tc_commit_elect(&s.empty[slot]);
+    }
+
+    // O (+)= P V of a stream's tile, 16 keys at a time; what lies 16 or more
+    // past the entry's end stays out.
+    static __device__ __forceinline__ void issue_pv(const AttnArgs &p, Shared &s, uint8_t *ring,
+                                                    int stream, int fill, int keys, bool first,
+                                                    bool last, bool last_use)
+    {
+        const int slot = fill % kSlots;
+        wait(p, s, &s.full[slot], (fill / kSlots) & 1);
+        tc_fence_after();
+        const uint32_t va = smem_u32(ring + slot * kTileBytes);
+        const uint32_t ts = s.tmem + kS + 128 * stream, to = s.tmem + kO + D * stream;
+        const int steps = (min(keys, kKeys) + 15) / 16;
+        for (int k = 0; k < steps; k++)
+            tc_mma_ts_elect(to, ts + 8 * k, sdesc_mn_sw128(va + k * 2048, kKeys * 128), kPv,
+                            !first || k > 0);
+        if (last_use)
+            tc_commit_elect(&s.empty[slot]);
+        if (last)
+            tc_commit_elect(&s.o_full[stream]);
+    }
+
+    // A stream's MMAs in turn: S of a tile, then, when its P is there, O.  The
+    // next tile's S overwrites this one's P: MMAs of one thread complete in
+    // order.
+    //
+    // Pairs have one issuer for both streams, which alternates strictly: PV
+    // and the next QK of stream 0, then of stream 1.  That keeps the streams half
+    // a period apart, one's softmax under the other's MMAs; two issuers drift
+    // into step and leave the tensor cores idle during both softmaxes
+    // (4400 cycles a pair tile, against 2048 of MMAs).  Single items' streams are
+    // independent and bound by their loads; each has its own issuer.
     static __device__ void issuer(const AttnArgs &p, Shared &s, uint8_t *qbuf, uint8_t *ring,
                                   int stream)
     {
-        const uint32_t ts = s.tmem + kS + 128 * stream, to = s.tmem + kO + D * stream;
-        const uint64_t qd = sdesc_sw128(smem_u32(qbuf + stream * kTileBytes));
         uint32_t seg_phase = 0, tile_phase = 0;
-        for (int pass = 0; pass < 2; pass++) {
-            const int which = pass == 0 ? 2 : stream;
-            const Seg *segs = p.segs + (which == 2 ? p.cap_b : 0) + s.seg0[which];
-            for (int i = 0, r = 0; i < s.segs[which]; i++) {
+        if (stream == 0) {
+            const Seg *segs = p.segs + p.cap_b + s.seg0[2];
+            for (int i = 0, r = 0; i < s.segs[2]; i++) {
                 const int tiles = segs[i].tiles, tile0 = segs[i].tile0;
                 const int keys = segs[i].k1 - segs[i].kbase;
                 if (tiles == 0)
                     continue;
-                wait(p, s, &s.q_ready[stream], seg_phase);
+                for (int st = 0; st < 2; st++) {
+                    wait(p, s, &s.q_ready[st], seg_phase);
+                    issue_qk(p, s, qbuf, ring, st, 2 * r, st == 1);
+                }
                 seg_phase ^= 1;
                 for (int t = 0; t < tiles; t++, r++) {
-                    const int fill = 2 * fill_of(s, which, r);
-                    const int ks = fill % kSlots, vs = (fill + 1) % kSlots;
-                    wait(p, s, &s.full[ks], (fill / kSlots) & 1);
-                    tc_fence_after();
-                    const uint64_t kd = sdesc_sw128(smem_u32(ring + ks * kTileBytes));
-#pragma unroll
-                    for (int k = 0; k < D / 16; k++) {
-                        const int off = (k / 4) * (kKeys * 128 >> 4) + (k % 4) * 2;
-                        mma_ss_elect(ts, qd + off, kd + off, kQk, k > 0);
+                    for (int st = 0; st < 2; st++) {
+                        wait(p, s, &s.p_ready[st], tile_phase);
+                        issue_pv(p, s, ring, st, 2 * r + 1, keys - (tile0 + t) * kKeys, t == 0,
+                                 t == tiles - 1, st == 1);
+                        if (t + 1 < tiles)
+                            issue_qk(p, s, qbuf, ring, st, 2 * r + 2, st == 1);
                     }
-                    tc_commit_elect(&s.s_full[stream]);
-                    tc_commit_elect(&s.empty[ks]);
-                    wait(p, s, &s.p_ready[stream], tile_phase);
                     tile_phase ^= 1;
-                    wait(p, s, &s.full[vs], ((fill + 1) / kSlots) & 1);
-                    tc_fence_after();
-                    const uint32_t va = smem_u32(ring + vs * kTileBytes);
-                    // 16 keys at a time; what lies 16 or more past the end stays out
-                    const int steps = (min(keys - (tile0 + t) * kKeys, kKeys) + 15) / 16;
-                    for (int k = 0; k < steps; k++)
-                        tc_mma_ts_elect(to, ts + 8 * k, sdesc_mn_sw128(va + k * 2048, kKeys * 128),
-                                        kPv, t > 0 || k > 0);
-                    tc_commit_elect(&s.empty[vs]);
-                    if (t == tiles - 1)
-                        tc_commit_elect(&s.o_full[stream]);
                 }
+            }
+            mbar_arrive_elect(&s.pairs_done);
+        } else {                               // the phases go on where the pairs' end
+            wait(p, s, &s.pairs_done, 0);
+            for (int i = 0; i < s.segs[2]; i++) {
+                const int tiles = p.segs[p.cap_b + s.seg0[2] + i].tiles;
+                seg_phase ^= tiles > 0;
+                tile_phase ^= tiles & 1;
+            }
+        }
+        const Seg *segs = p.segs + s.seg0[stream];
+        for (int i = 0, r = 0; i < s.segs[stream]; i++) {
+            const int tiles = segs[i].tiles, tile0 = segs[i].tile0;
+            const int keys = segs[i].k1 - segs[i].kbase;
+            if (tiles == 0)
+                continue;
+            wait(p, s, &s.q_ready[stream], seg_phase);
+            seg_phase ^= 1;
+            for (int t = 0; t < tiles; t++, r++) {
+                const int fill = 2 * fill_of(s, stream, r);
+                issue_qk(p, s, qbuf, ring, stream, fill, true);
+                wait(p, s, &s.p_ready[stream], tile_phase);
+                tile_phase ^= 1;
+                issue_pv(p, s, ring, stream, fill + 1, keys - (tile0 + t) * kKeys, t == 0,
+                         t == tiles - 1, true);
             }
         }
     }
@@ -668,22 +772,30 @@ struct Kernel {
     }
 
     // Rows [row0, row0 + rows) of a piece's queries, 16 bytes a thread and
-    // step; rows past the end are zero.
-    static __device__ void load_q(const AttnArgs &p, uint8_t *q, const Seg &g, int row0, int rows,
-                                  int tid)
+    // step, eight steps' loads in flight; rows past the end are zero.
+    static __device__ __forceinline__ void load_q(const AttnArgs &p, uint8_t *q, const Seg &g,
+                                                  int row0, int rows, int tid)
     {
-        constexpr int kChunks = D / 8;
-        for (int i = tid; i < kRows * kChunks; i += 128) {
-            const int row = i / kChunks, c = i % kChunks;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < rows) {
-                const int at = row0 + row, tok = g.tok0 + at / p.rep;
-                const int head = g.head * p.rep + at % p.rep;
-                v = __ldg(reinterpret_cast<const uint4 *>(p.q + tok * p.q_tok + head * p.q_head +
-                                                          c * 8));
+        constexpr int kChunks = D / 8, kStep = 128 / kChunks, kBatch = 8;
+        const int c = tid % kChunks;
+        const uint16_t *src = p.q + g.tok0 * p.q_tok +
+                              static_cast<int64_t>(g.head) * p.rep * p.q_head + c * 8;
+        for (int r0 = tid / kChunks; r0 < kRows; r0 += kStep * kBatch) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; u++) {
+                const int row = r0 + u * kStep, at = row0 + row, tok = at / p.rep;
+                v[u] = make_uint4(0, 0, 0, 0);
+                if (row < rows)
+                    v[u] = __ldg(reinterpret_cast<const uint4 *>(
+                        src + tok * p.q_tok + (at - tok * p.rep) * p.q_head));
             }
-            *reinterpret_cast<uint4 *>(q + (c / 8) * (kRows * 128) + row * 128 +
-                                       ((c % 8) ^ (row & 7)) * 16) = v;
+#pragma unroll
+            for (int u = 0; u < kBatch; u++) {
+                const int row = r0 + u * kStep;
+                *reinterpret_cast<uint4 *>(q + (c / 8) * (kRows * 128) + row * 128 +
+                                           ((c % 8) ^ (row & 7)) * 16) = v[u];
+            }
         }
     }
 
@@ -831,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     if (tid == 0) {
         for (int i = 0; i < K::kSlots; i++) {
             mbar_init(&s.full[i], 1);
-            mbar_init(&s.empty[i], 2);
+            mbar_init(&s.empty[i], 1);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(&s.q_ready[i], kRows);
@@ -839,6 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             mbar_init(&s.p_ready[i], kRows);
             mbar_init(&s.o_full[i], 1);
         }
+        mbar_init(&s.pairs_done, 1);
         s.abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&p.k_map);
@@ -870,69 +983,114 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 }
 
 // -------------------------------------------------------------------- join
-// A row's pieces joined: CTA (b, y) takes sequence b's rows (token, head), a
-// thread four values of a row; neighbouring threads are neighbouring rows of
-// one kv head, as the pieces lie.
+// A row's pieces joined: CTA (b, y) takes 64 of sequence b's (row, four
+// values), neighbouring rows side by side as the pieces lie, with four threads
+// each: thread q takes every fourth piece, kBatch loads in flight, and the four
+// are added up in order.  So a row of forty pieces costs two memory latencies.
+constexpr int kJoinSplit = 4, kJoinItems = 64;
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs p,
-                                                        int grid)
+__global__ void __launch_bounds__(kJoinSplit *kJoinItems)
+    attn_join_kernel(const __grid_constant__ AttnArgs p, int grid)
 {
+    constexpr int kBatch = 8;
+    __shared__ float4 so[kJoinSplit][kJoinItems];
+    __shared__ float2 sm[kJoinSplit][kJoinItems];
     pdl_wait();
     pdl_trigger();
-    const int b = blockIdx.x;
-    const int t0 = p.q_offsets[b], t1 = p.q_offsets[b + 1];
-    if (t0 < 0 || t1 <= t0 || t1 > p.T || t1 - t0 > p.max_q)
-        return;
-    const int g = group_of(p, b);
-    const int rows = (t1 - t0) * p.rep;        // of one kv head
+    const Joint j = p.joints[blockIdx.x];
+    const int rows = j.tokens * p.rep;         // of one kv head
     const int n = rows * p.Hkv * (D / 4);
-    for (int i = blockIdx.y * 256 + threadIdx.x; i < n; i += gridDim.y * 256) {
+    const int local_i = threadIdx.x % kJoinItems, q = threadIdx.x / kJoinItems;
+    for (int i0 = blockIdx.y * kJoinItems; i0 < n; i0 += gridDim.y * kJoinItems) {
+        const int i = min(i0 + local_i, n - 1);
         const int row = i % rows, c = i / rows % (D / 4), head = i / rows / (D / 4);
         float m = -INFINITY, l = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int k = 0; k < 2; k++) {
-            const int e = k == 0 ? g : p.G + b;
-            if (e < 0)
-                continue;
-            const Entry en = p.entries[e];
+#pragma unroll
+        for (int k = 0; k < 2; k++) {          // the prefix's pieces, the sequence's own
+            const Entry &en = j.e[k];
             if (en.tiles == 0)
                 continue;
-            const int pair = en.pair, step = pair ? 2 * kRows : kRows;
-            // this sequence's rows lie behind those of its group's earlier tokens
-            const int er = k == 0 ? row + (t0 - p.q_offsets[p.group_offsets[g]]) * p.rep : row;
+            const int er = row + en.row, step = en.pair ? 2 * kRows : kRows;
+            const int all = en.pair ? 2 * kRows : p.rows_b, at = er % step;
             const int local = head * en.row_tiles + er / step;
-            const int64_t tiles = p.totals->tiles[pair];
-            const int workers = workers_for(p.totals->tiles[pair], pair ? grid : 2 * grid);
+            const int tiles = en.pair ? j.all[1] : j.all[0];
+            const int workers = workers_for(tiles, en.pair ? grid : 2 * grid);
             const int64_t x0 = en.tile0 + static_cast<int64_t>(local) * en.tiles;
             const int w0 = worker_of(tiles, workers, x0);
             const int w1 = worker_of(tiles, workers, x0 + en.tiles - 1);
-            const int all = pair ? 2 * kRows : p.rows_b, at = er % step;
-            const float2 *ml = pair ? p.ml_a : p.ml_b;
-            const float4 *part = reinterpret_cast<const float4 *>(pair ? p.part_a : p.part_b);
-            if (en.item0 + local + w1 >= (pair ? p.cap_a : p.cap_b))
+            if (en.item0 + local + w1 >= (en.pair ? p.cap_a : p.cap_b))
                 continue;
-            for (int w = w0; w <= w1; w++) {
-                const int64_t base = static_cast<int64_t>(en.item0 + local + w) * all;
-                const float2 s = ml[base + at];
-                if (!(s.y > 0.0f) && s.y == s.y)
-                    continue;                  // nothing visible in this piece
-                const float4 v = part[base * (D / 4) + static_cast<int64_t>(c) * all + at];
-                const float nm = fmaxf(m, s.x);
-                const float fa = ex2(m - nm), fb = ex2(s.x - nm);
-                m = nm;
-                l = l * fa + s.y * fb;
-                o.x = o.x * fa + v.x * fb;
-                o.y = o.y * fa + v.y * fb;
-                o.z = o.z * fa + v.z * fb;
-                o.w = o.w * fa + v.w * fb;
+            const int64_t first = static_cast<int64_t>(en.item0 + local) * all;
+            const float2 *ml = (en.pair ? p.ml_a : p.ml_b) + first + at;
+            const float4 *part = reinterpret_cast<const float4 *>(en.pair ? p.part_a : p.part_b) +
+                                 first * (D / 4) + c * all + at;
+            for (int w = w0 + q; w <= w1; w += kJoinSplit * kBatch) {
+                float4 v[kBatch];
+                float2 s[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; u++) {
+                    const int64_t x = w + u * kJoinSplit;
+                    s[u] = make_float2(-INFINITY, 0.0f);
+                    v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (x <= w1) {
+                        s[u] = ml[x * all];
+                        v[u] = part[x * all * (D / 4)];
+                    }
+                }
+                float top = m;
+#pragma unroll
+                for (int u = 0; u < kBatch; u++)
+                    top = fmaxf(top, s[u].x);
+                // with nothing visible yet every factor is zero
+                const float ref = top == -INFINITY ? 0.0f : top;
+                const float f0 = ex2(m - ref);
+                m = top;
+                l *= f0;
+                o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+                for (int u = 0; u < kBatch; u++) {
+                    if (!(s[u].y > 0.0f) && s[u].y == s[u].y)
+                        continue;              // nothing visible in this piece
+                    const float f = ex2(s[u].x - ref);
+                    l = fmaf(s[u].y, f, l);
+                    o.x = fmaf(v[u].x, f, o.x);
+                    o.y = fmaf(v[u].y, f, o.y);
+                    o.z = fmaf(v[u].z, f, o.z);
+                    o.w = fmaf(v[u].w, f, o.w);
+                }
             }
         }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;     // a row that sees nothing is zero
-        const int tok = t0 + row / p.rep, h = head * p.rep + row % p.rep;
-        uint2 r;
-        r.x = pack2<BF16>(o.x * inv, o.y * inv);
-        r.y = pack2<BF16>(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(tok) * p.Hq + h) * D + 4 * c) = r;
+        so[q][local_i] = o;
+        sm[q][local_i] = make_float2(m, l);
+        __syncthreads();
+        if (q == 0 && i0 + local_i < n) {
+#pragma unroll
+            for (int k = 1; k < kJoinSplit; k++)
+                m = fmaxf(m, sm[k][local_i].x);
+            l = 0.0f;
+            o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < kJoinSplit; k++) {
+                const float2 s = sm[k][local_i];
+                const float4 v = so[k][local_i];
+                const float f = s.x == -INFINITY ? 0.0f : ex2(s.x - m);
+                l = fmaf(s.y, f, l);
+                o.x = fmaf(v.x, f, o.x);
+                o.y = fmaf(v.y, f, o.y);
+                o.z = fmaf(v.z, f, o.z);
+                o.w = fmaf(v.w, f, o.w);
+            }
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;     // a row that sees nothing is zero
+            const int tok = j.tok0 + row / p.rep, h = head * p.rep + row % p.rep;
+            uint2 r;
+            r.x = pack2<BF16>(o.x * inv, o.y * inv);
+            r.y = pack2<BF16>(o.z * inv, o.w * inv);
+            *reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(tok) * p.Hq + h) * D + 4 * c) =
+                r;
+        }
+        __syncthreads();
     }
 }
 
@@ -971,7 +1129,7 @@ bool encode_pages(CUtensorMap *map, const AttnProblem &q, const uint16_t *base)
 // Where a call's pieces lie in its workspace.
 struct Space {
     int cap_a, cap_b, rows_b;
-    size_t totals, entries, segs, ml_a, ml_b, part_a, part_b, total;
+    size_t joints, segs, ml_a, ml_b, part_a, part_b, total;
 };
 
 constexpr int kMaxGrid = 256;              // CTAs that a workspace allows for
@@ -993,8 +1151,7 @@ Space space_of(int T, int B, int G, int max_q, int Hq, int Hkv, int D)
         at += (bytes + 255) / 256 * 256;
         return here;
     };
-    s.totals = take(sizeof(Totals));
-    s.entries = take(sizeof(Entry) * (static_cast<size_t>(B) + G));
+    s.joints = take(sizeof(Joint) * static_cast<size_t>(B));
     s.segs = take(sizeof(Seg) * (static_cast<size_t>(s.cap_a) + s.cap_b));
     s.ml_a = take(sizeof(float2) * static_cast<size_t>(s.cap_a) * 2 * kRows);
     s.ml_b = take(sizeof(float2) * static_cast<size_t>(s.cap_b) * s.rows_b);
@@ -1023,8 +1180,10 @@ cudaError_t launch_variant(const AttnArgs &a, int dev, int sms, cudaStream_t str
     if (err != cudaSuccess)
         return err;
     const int64_t n = static_cast<int64_t>(a.max_q) * a.Hq * (D / 4);
-    const int y = static_cast<int>(std::min<int64_t>((n + 255) / 256, 64));
-    return launch_pdl(attn_join_kernel<D, BF16>, dim3(a.B, y), dim3(256), 0, stream, a, grid);
+    const int y = static_cast<int>(
+        std::min<int64_t>((n + kJoinItems - 1) / kJoinItems, std::max(65536 / a.B, 1)));
+    return launch_pdl(attn_join_kernel<D, BF16>, dim3(a.B, y), dim3(kJoinSplit * kJoinItems), 0,
+                      stream, a, grid);
 }
 
 }  // namespace
@@ -1049,8 +1208,7 @@ cudaError_t launch_attn(const AttnProblem &q, cudaStream_t stream)
         return cudaErrorInvalidValue;
     const Space s = space_of(q.T, q.B, q.G, q.max_q, q.Hq, q.Hkv, q.D);
     uint8_t *ws = static_cast<uint8_t *>(q.workspace);
-    a.totals = reinterpret_cast<Totals *>(ws + s.totals);
-    a.entries = reinterpret_cast<Entry *>(ws + s.entries);
+    a.joints = reinterpret_cast<Joint *>(ws + s.joints);
     a.segs = reinterpret_cast<Seg *>(ws + s.segs);
     a.ml_a = reinterpret_cast<float2 *>(ws + s.ml_a);
     a.ml_b = reinterpret_cast<float2 *>(ws + s.ml_b);
