@@ -1087,7 +1087,7 @@ int w4_attn_shared_prefix(const uint16_t *q, int64_t q_tok_stride, int64_t q_hea
     const int64_t rows = static_cast<int64_t>(T) * Hq;
     const int64_t keys = static_cast<int64_t>(W) * page_size;
     const int64_t items = 2 * (rows / 128 + 1) + (static_cast<int64_t>(B) + G) * Hkv;
-    if (rows * D >= (1ll << 31) || keys >= (1ll << 30) || items * (keys / 128 + 2) >= (1ll << 31) ||
+    if (rows * D >= (1ll << 31) || keys >= (1ll << 30) || items * (keys / 128 + 4) >= (1ll << 31) ||
         static_cast<int64_t>(max_q) * Hq >= (1ll << 30))
         return fail(W4_ERR_UNSUPPORTED_SHAPE, "problem too large for 32-bit counts");
     if (T == 0 || B == 0)

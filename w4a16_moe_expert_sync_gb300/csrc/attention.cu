@@ -46,8 +46,8 @@ constexpr int kMaxEntries = 4096;
 
 // A group's prefix (first G) or a sequence's own keys.
 struct Entry {
-    int tile0, item0;                      // before it, in its region
-    int tiles;                             // of one item
+    int place, item0;                      // length and items before it, in its region
+    int span;                              // of one item: kItemCost + tiles; 0: nothing
     int row_tiles;                         // items per kv head
     int pair;
     int row;                               // a sequence's first row among its group's
@@ -56,7 +56,7 @@ struct Entry {
 // What the joining kernel needs to know of a sequence.
 struct alignas(16) Joint {
     int tok0, tokens;                      // tokens < 0: nothing to write
-    int all[2];                            // tiles of all single [0] and pair [1] items
+    int all[2];                            // length of the single [0] and pair [1] region
     Entry e[2];                            // of its group's prefix and of its own keys
 };
 
@@ -90,17 +90,24 @@ struct AttnArgs {
     int cap_a, cap_b;                      // pieces that the workspace holds
 };
 
-__host__ __device__ inline int64_t worker_begin(int64_t tiles, int workers, int w)
+// An item is kItemCost + its tiles long when the work is split: fetching its
+// queries and storing its sums takes about as long as that many tiles.
+constexpr int kItemCost = 2;
+
+// Worker w's share of a region's `all` begins here.
+__device__ __forceinline__ int worker_begin(int all, int workers, int w)
 {
-    return tiles * w / workers;
+    return static_cast<int>(static_cast<int64_t>(all) * w / workers);
 }
-// The worker that a tile belongs to.
-__host__ __device__ inline int worker_of(int64_t tiles, int workers, int64_t tile)
+// The worker whose share place x is in.
+__device__ __forceinline__ int worker_of(int all, int workers, int x)
 {
-    return static_cast<int>(((tile + 1) * workers - 1) / tiles);
+    if (all < (1 << 22))                       // workers <= 512: 32 bits do
+        return static_cast<int>((static_cast<uint32_t>(x + 1) * workers - 1) / all);
+    return static_cast<int>((static_cast<int64_t>(x + 1) * workers - 1) / all);
 }
-// No worker goes without a tile.
-__host__ __device__ inline int workers_for(int tiles, int most) { return tiles < most ? tiles : most; }
+// No worker goes without a share.
+__device__ __forceinline__ int workers_for(int all, int most) { return all < most ? all : most; }
 
 // ------------------------------------------------------------- tensor memory
 // All 128 columns of this thread's lane, and the wait for them.
@@ -172,6 +179,11 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, i
         " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
         : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all()
+{
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -278,7 +290,7 @@ __device__ __forceinline__ Entry entry_of(const AttnArgs &p, const Want &w)
     const int rows = w.tokens * p.rep;
     if (rows > 0 && w.k1 > w.k0) {
         const int base = w.k0 / p.page * p.page;
-        e.tiles = (w.k1 - base + kKeys - 1) / kKeys;
+        e.span = (w.k1 - base + kKeys - 1) / kKeys + kItemCost;
         e.pair = rows > p.rows_b;
         e.row_tiles = e.pair ? (rows + 2 * kRows - 1) / (2 * kRows) : 1;
     }
@@ -390,7 +402,7 @@ struct Kernel {
         for (int e = e0; e < e1; e++) {
             const Entry en = sane ? entry_of(p, want_of(p, x, e, blockIdx.x == 0)) : Entry{};
             const int items = en.row_tiles * p.Hkv;
-            (en.pair ? sum.z : sum.x) += items * en.tiles;
+            (en.pair ? sum.z : sum.x) += items * en.span;
             (en.pair ? sum.w : sum.y) += items;
         }
         int4 total;
@@ -402,13 +414,13 @@ struct Kernel {
             start[n + e] = at.y;
             start[2 * n + e] = at.z;
             start[3 * n + e] = at.w;
-            (en.pair ? at.z : at.x) += items * en.tiles;
+            (en.pair ? at.z : at.x) += items * en.span;
             (en.pair ? at.w : at.y) += items;
         }
         __syncthreads();
         auto placed = [&](int e) {
             Entry en = sane ? entry_of(p, want_of(p, x, e, false)) : Entry{};
-            en.tile0 = start[(en.pair ? 2 * n : 0) + e];
+            en.place = start[(en.pair ? 2 * n : 0) + e];
             en.item0 = start[(en.pair ? 3 * n : n) + e];
             return en;
         };
@@ -416,17 +428,20 @@ struct Kernel {
         const int which = tid >> 5, lane = tid & 31;
         if (which < 3) {
             const bool pair = which == 2;
-            const int tiles = pair ? total.z : total.x;
-            const int workers = workers_for(tiles, pair ? gridDim.x : 2 * gridDim.x);
-            const int w = pair ? blockIdx.x : 2 * blockIdx.x + which;
+            const int all = pair ? total.z : total.x, grid = gridDim.x;
+            const int workers = workers_for(all, pair ? grid : 2 * grid);
+            // single items start at the first CTA that has no pairs, one stream
+            // of every CTA before the other
+            const int turned = blockIdx.x - workers_for(total.z, grid);
+            const int w = pair ? blockIdx.x : which * grid + (turned < 0 ? turned + grid : turned);
             const int *ts = start + (pair ? 2 * n : 0), *is = start + (pair ? 3 * n : n);
             int first = 0, count = 0, lo = 0, hi = 0;
             if (w < workers) {
-                lo = static_cast<int>(worker_begin(tiles, workers, w));
-                hi = static_cast<int>(worker_begin(tiles, workers, w + 1));
+                lo = worker_begin(all, workers, w);
+                hi = worker_begin(all, workers, w + 1);
                 // lane 0 finds the first tile's item, lane 1 the last's
                 const int at = lane == 0 ? lo : hi - 1, e = find_entry(ts, n, at);
-                const int item = is[e] + (at - ts[e]) / entry_of(p, want_of(p, x, e, false)).tiles;
+                const int item = is[e] + (at - ts[e]) / entry_of(p, want_of(p, x, e, false)).span;
                 first = __shfl_sync(0xffffffffu, item, 0);
                 count = __shfl_sync(0xffffffffu, item, 1) - first + 1;
             }
@@ -443,7 +458,7 @@ struct Kernel {
                 const Want wa = want_of(p, x, e, false);
                 const Entry en = entry_of(p, wa);
                 const int local = item - is[e];
-                const int t0 = ts[e] + local * en.tiles;         // the item's first tile
+                const int t0 = ts[e] + local * en.span + kItemCost;   // its first tile's place
                 Seg g;
                 g.seq = e < p.G ? -1 : e - p.G;
                 g.row_of_table = e < p.G ? x.group_offsets[e] : e - p.G;
@@ -452,11 +467,11 @@ struct Kernel {
                 g.kbase = wa.k0 / p.page * p.page;
                 g.tok0 = wa.tok0;
                 g.head = local / en.row_tiles;
-                const int step = (pair ? 2 : 1) * kRows, all = wa.tokens * p.rep;
+                const int step = (pair ? 2 : 1) * kRows;
                 g.row0 = (local % en.row_tiles) * step;
-                g.rows = min(step, all - g.row0);
+                g.rows = min(step, wa.tokens * p.rep - g.row0);
                 g.tile0 = max(lo - t0, 0);
-                int end = min(hi - t0, en.tiles);
+                int end = min(hi - t0, en.span - kItemCost);
                 if (p.causal && g.seq >= 0) {
                     // no row of this item sees beyond its last token's position
                     const int last = (g.row0 + g.rows - 1) / p.rep;
@@ -730,71 +745,90 @@ struct Kernel {
         const uint32_t to = s.tmem + lanes + kO + D * stream;
         uint8_t *q = qbuf + stream * kTileBytes;
         uint32_t s_phase = 0, o_phase = 0;
-        for (int pass = 0; pass < 2; pass++) {
-            const int which = pass == 0 ? 2 : stream;
-            const Seg *segs = p.segs + (which == 2 ? p.cap_b : 0) + s.seg0[which];
-            for (int i = 0, r = 0; i < s.segs[which]; i++) {
-                const Seg g = segs[i];
-                const int row0 = g.row0 + (which == 2 ? stream * kRows : 0);
-                const int rows = min(max(g.row0 + g.rows - row0, 0), kRows);
-                if (g.tiles > 0)
-                    load_q(p, q, g, row0, rows, tid);
-                // this row's visible keys: [k0, limit)
-                int limit = 0;
-                if (tid < rows) {
-                    const int tok = g.tok0 + (row0 + tid) / p.rep;
-                    limit = min(limit_of(p, g, tok), g.k1);
-                }
-                fence_proxy_async_smem();
-                if (g.tiles > 0)
-                    mbar_arrive(&s.q_ready[stream]);
-                float m = -INFINITY, l = 0.0f;     // m in units of log2
-                for (int t = g.tile0; t < g.tile0 + g.tiles; t++, r++) {
-                    const int base = g.kbase + t * kKeys;
-                    wait(p, s, &s.s_full[stream], s_phase);
-                    s_phase ^= 1;
-                    tc_fence_after();
-                    tile(p, ts, to, g.k0 - base, limit - base, t > g.tile0, m, l);
-                    if (g.k1 - base < kKeys && (g.k1 & 15))
-                        clear_tail(p, s, ring, 2 * fill_of(s, which, r) + 1, g.k1 - base,
-                                   which == 2, stream, tid);
-                    tc_fence_before();
-                    mbar_arrive(&s.p_ready[stream]);
-                }
-                if (g.tiles > 0) {
-                    wait(p, s, &s.o_full[stream], o_phase);
-                    o_phase ^= 1;
-                    tc_fence_after();
-                }
-                store(p, g, which == 2, row0 - g.row0, rows, to, m, l, tid);
+        // the pairs' pieces, then this stream's own
+        const int pairs = s.segs[2], pieces = pairs + s.segs[stream];
+        auto piece = [&](int i) -> const Seg & {
+            return i < pairs ? p.segs[p.cap_b + s.seg0[2] + i]
+                             : p.segs[s.seg0[stream] + i - pairs];
+        };
+        // A piece's queries on their way to shared memory, and how many keys this
+        // thread's row sees.  Called when no MMA reads the queries any more.
+        auto prepare = [&](int i) {
+            const Seg &g = piece(i);
+            const int row0 = g.row0 + (i < pairs ? stream * kRows : 0);
+            const int rows = min(max(g.row0 + g.rows - row0, 0), kRows);
+            if (g.tiles > 0)
+                load_q(p, q, g, row0, rows, tid);
+            if (tid >= rows)
+                return 0;
+            return min(limit_of(p, g, g.tok0 + (row0 + tid) / p.rep), g.k1);
+        };
+        auto hand_over = [&](int i) {          // the queries to the issuer
+            if (piece(i).tiles == 0)
+                return;
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            mbar_arrive(&s.q_ready[stream]);
+        };
+        int limit = 0, next = 0;
+        if (pieces > 0) {
+            limit = prepare(0);
+            hand_over(0);
+        }
+        for (int i = 0, r = 0; i < pieces; i++, limit = next) {
+            const Seg g = piece(i);
+            const bool pair = i < pairs, another = i + 1 < pieces;
+            if (i == pairs)
+                r = 0;
+            float m = -INFINITY, l = 0.0f;     // m in units of log2
+            const int end = g.tile0 + g.tiles;
+            for (int t = g.tile0; t < end; t++, r++) {
+                const int base = g.kbase + t * kKeys;
+                wait(p, s, &s.s_full[stream], s_phase);
+                s_phase ^= 1;
+                tc_fence_after();
+                if (t == end - 1 && another)
+                    next = prepare(i + 1);
+                tile(p, ts, to, g.k0 - base, limit - base, t > g.tile0, m, l);
+                if (g.k1 - base < kKeys && (g.k1 & 15))
+                    clear_tail(p, s, ring, 2 * fill_of(s, pair ? 2 : stream, r) + 1, g.k1 - base,
+                               pair, stream, tid);
+                tc_fence_before();
+                mbar_arrive(&s.p_ready[stream]);
             }
+            if (g.tiles == 0 && another)
+                next = prepare(i + 1);
+            // the next piece's first S may be made while this one's sums are stored
+            if (another)
+                hand_over(i + 1);
+            if (g.tiles > 0) {
+                wait(p, s, &s.o_full[stream], o_phase);
+                o_phase ^= 1;
+                tc_fence_after();
+            }
+            const int row = pair ? stream * kRows : 0;
+            store(p, g, pair, row, min(max(g.rows - row, 0), kRows), to, m, l, tid);
         }
     }
 
     // Rows [row0, row0 + rows) of a piece's queries, 16 bytes a thread and
-    // step, eight steps' loads in flight; rows past the end are zero.
+    // step; rows past the end are zero.
     static __device__ __forceinline__ void load_q(const AttnArgs &p, uint8_t *q, const Seg &g,
                                                   int row0, int rows, int tid)
     {
-        constexpr int kChunks = D / 8, kStep = 128 / kChunks, kBatch = 8;
+        constexpr int kChunks = D / 8, kStep = 128 / kChunks;
         const int c = tid % kChunks;
         const uint16_t *src = p.q + g.tok0 * p.q_tok +
                               static_cast<int64_t>(g.head) * p.rep * p.q_head + c * 8;
-        for (int r0 = tid / kChunks; r0 < kRows; r0 += kStep * kBatch) {
-            uint4 v[kBatch];
-#pragma unroll
-            for (int u = 0; u < kBatch; u++) {
-                const int row = r0 + u * kStep, at = row0 + row, tok = at / p.rep;
-                v[u] = make_uint4(0, 0, 0, 0);
-                if (row < rows)
-                    v[u] = __ldg(reinterpret_cast<const uint4 *>(
-                        src + tok * p.q_tok + (at - tok * p.rep) * p.q_head));
-            }
-#pragma unroll
-            for (int u = 0; u < kBatch; u++) {
-                const int row = r0 + u * kStep;
-                *reinterpret_cast<uint4 *>(q + (c / 8) * (kRows * 128) + row * 128 +
-                                           ((c % 8) ^ (row & 7)) * 16) = v[u];
+        for (int row = tid / kChunks; row < kRows; row += kStep) {
+            uint8_t *dst = q + (c / 8) * (kRows * 128) + row * 128 + ((c % 8) ^ (row & 7)) * 16;
+            if (row < rows) {
+                const int at = row0 + row, tok = at / p.rep;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
+                             "l"(src + tok * p.q_tok + (at - tok * p.rep) * p.q_head)
+                             : "memory");
+            } else {
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
             }
         }
     }
@@ -983,60 +1017,61 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 }
 
 // -------------------------------------------------------------------- join
-// A row's pieces joined: CTA (b, y) takes 64 of sequence b's (row, four
-// values), neighbouring rows side by side as the pieces lie, with four threads
-// each: thread q takes every fourth piece, kBatch loads in flight, and the four
-// are added up in order.  So a row of forty pieces costs two memory latencies.
-constexpr int kJoinSplit = 4, kJoinItems = 64;
+// A row's pieces joined: CTA (b, y) takes 32 of sequence b's rows (a lane
+// each: neighbouring rows are side by side in a piece).  A warp has 16 of the
+// D values and every other piece, four pieces' loads in flight; the two halves
+// are added up at the end, in a fixed order.
+template <int D> constexpr int kJoinThreads = 32 * (D / 16) * 2;
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kJoinSplit *kJoinItems)
+__global__ void __launch_bounds__(kJoinThreads<D>)
     attn_join_kernel(const __grid_constant__ AttnArgs p, int grid)
 {
-    constexpr int kBatch = 8;
-    __shared__ float4 so[kJoinSplit][kJoinItems];
-    __shared__ float2 sm[kJoinSplit][kJoinItems];
+    constexpr int kBatch = 4, kGroups = D / 16;
+    __shared__ float4 so[4][kGroups][32];
+    __shared__ float2 sm[kGroups][32];
     pdl_wait();
     pdl_trigger();
     const Joint j = p.joints[blockIdx.x];
     const int rows = j.tokens * p.rep;         // of one kv head
-    const int n = rows * p.Hkv * (D / 4);
-    const int local_i = threadIdx.x % kJoinItems, q = threadIdx.x / kJoinItems;
-    for (int i0 = blockIdx.y * kJoinItems; i0 < n; i0 += gridDim.y * kJoinItems) {
-        const int i = min(i0 + local_i, n - 1);
-        const int row = i % rows, c = i / rows % (D / 4), head = i / rows / (D / 4);
+    const int n = rows * p.Hkv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int cg = warp % kGroups, half = warp / kGroups;
+    for (int i0 = blockIdx.y * 32; i0 < n; i0 += gridDim.y * 32) {
+        const int i = min(i0 + lane, n - 1), head = i / rows, row = i - head * rows;
         float m = -INFINITY, l = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float4 o[4] = {};
 #pragma unroll
         for (int k = 0; k < 2; k++) {          // the prefix's pieces, the sequence's own
             const Entry &en = j.e[k];
-            if (en.tiles == 0)
+            if (en.span == 0)
                 continue;
             const int er = row + en.row, step = en.pair ? 2 * kRows : kRows;
-            const int all = en.pair ? 2 * kRows : p.rows_b, at = er % step;
+            const int stride = en.pair ? 2 * kRows : p.rows_b, at = er % step;
             const int local = head * en.row_tiles + er / step;
-            const int tiles = en.pair ? j.all[1] : j.all[0];
-            const int workers = workers_for(tiles, en.pair ? grid : 2 * grid);
-            const int64_t x0 = en.tile0 + static_cast<int64_t>(local) * en.tiles;
-            const int w0 = worker_of(tiles, workers, x0);
-            const int w1 = worker_of(tiles, workers, x0 + en.tiles - 1);
+            const int all = en.pair ? j.all[1] : j.all[0];
+            const int workers = workers_for(all, en.pair ? grid : 2 * grid);
+            const int x0 = en.place + local * en.span;
+            const int w0 = worker_of(all, workers, x0);
+            const int w1 = worker_of(all, workers, x0 + en.span - 1);
             if (en.item0 + local + w1 >= (en.pair ? p.cap_a : p.cap_b))
                 continue;
-            const int64_t first = static_cast<int64_t>(en.item0 + local) * all;
+            const int64_t first = static_cast<int64_t>(en.item0 + local) * stride;
             const float2 *ml = (en.pair ? p.ml_a : p.ml_b) + first + at;
             const float4 *part = reinterpret_cast<const float4 *>(en.pair ? p.part_a : p.part_b) +
-                                 first * (D / 4) + c * all + at;
-            for (int w = w0 + q; w <= w1; w += kJoinSplit * kBatch) {
-                float4 v[kBatch];
+                                 first * (D / 4) + cg * 4 * stride + at;
+            for (int w = w0 + half; w <= w1; w += 2 * kBatch) {
+                float4 v[kBatch][4];
                 float2 s[kBatch];
 #pragma unroll
                 for (int u = 0; u < kBatch; u++) {
-                    const int64_t x = w + u * kJoinSplit;
+                    const int64_t x = w + 2 * u;
                     s[u] = make_float2(-INFINITY, 0.0f);
-                    v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     if (x <= w1) {
-                        s[u] = ml[x * all];
-                        v[u] = part[x * all * (D / 4)];
+                        s[u] = ml[x * stride];
+#pragma unroll
+                        for (int c = 0; c < 4; c++)
+                            v[u][c] = part[x * stride * (D / 4) + c * stride];
                     }
                 }
                 float top = m;
@@ -1048,47 +1083,51 @@ __global__ void __launch_bounds__(kJoinSplit *kJoinItems)
                 const float f0 = ex2(m - ref);
                 m = top;
                 l *= f0;
-                o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+                for (int c = 0; c < 4; c++)
+                    o[c] = make_float4(o[c].x * f0, o[c].y * f0, o[c].z * f0, o[c].w * f0);
 #pragma unroll
                 for (int u = 0; u < kBatch; u++) {
                     if (!(s[u].y > 0.0f) && s[u].y == s[u].y)
                         continue;              // nothing visible in this piece
                     const float f = ex2(s[u].x - ref);
                     l = fmaf(s[u].y, f, l);
-                    o.x = fmaf(v[u].x, f, o.x);
-                    o.y = fmaf(v[u].y, f, o.y);
-                    o.z = fmaf(v[u].z, f, o.z);
-                    o.w = fmaf(v[u].w, f, o.w);
+#pragma unroll
+                    for (int c = 0; c < 4; c++) {
+                        o[c].x = fmaf(v[u][c].x, f, o[c].x);
+                        o[c].y = fmaf(v[u][c].y, f, o[c].y);
+                        o[c].z = fmaf(v[u][c].z, f, o[c].z);
+                        o[c].w = fmaf(v[u][c].w, f, o[c].w);
+                    }
                 }
             }
         }
-        so[q][local_i] = o;
-        sm[q][local_i] = make_float2(m, l);
+        if (half == 1) {
+            sm[cg][lane] = make_float2(m, l);
+#pragma unroll
+            for (int c = 0; c < 4; c++)
+                so[c][cg][lane] = o[c];
+        }
         __syncthreads();
-        if (q == 0 && i0 + local_i < n) {
-#pragma unroll
-            for (int k = 1; k < kJoinSplit; k++)
-                m = fmaxf(m, sm[k][local_i].x);
-            l = 0.0f;
-            o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int k = 0; k < kJoinSplit; k++) {
-                const float2 s = sm[k][local_i];
-                const float4 v = so[k][local_i];
-                const float f = s.x == -INFINITY ? 0.0f : ex2(s.x - m);
-                l = fmaf(s.y, f, l);
-                o.x = fmaf(v.x, f, o.x);
-                o.y = fmaf(v.y, f, o.y);
-                o.z = fmaf(v.z, f, o.z);
-                o.w = fmaf(v.w, f, o.w);
-            }
+        if (half == 0 && i0 + lane < n) {
+            const float2 s = sm[cg][lane];
+            const float top = fmaxf(m, s.x), ref = top == -INFINITY ? 0.0f : top;
+            const float f0 = ex2(m - ref), f1 = ex2(s.x - ref);
+            l = l * f0 + s.y * f1;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;     // a row that sees nothing is zero
             const int tok = j.tok0 + row / p.rep, h = head * p.rep + row % p.rep;
-            uint2 r;
-            r.x = pack2<BF16>(o.x * inv, o.y * inv);
-            r.y = pack2<BF16>(o.z * inv, o.w * inv);
-            *reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(tok) * p.Hq + h) * D + 4 * c) =
-                r;
+            uint32_t r[8];
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                const float4 v = so[c][cg][lane];
+                r[2 * c] = pack2<BF16>((o[c].x * f0 + v.x * f1) * inv, (o[c].y * f0 + v.y * f1) * inv);
+                r[2 * c + 1] =
+                    pack2<BF16>((o[c].z * f0 + v.z * f1) * inv, (o[c].w * f0 + v.w * f1) * inv);
+            }
+            uint4 *out = reinterpret_cast<uint4 *>(
+                p.out + (static_cast<int64_t>(tok) * p.Hq + h) * D + cg * 16);
+            out[0] = make_uint4(r[0], r[1], r[2], r[3]);
+            out[1] = make_uint4(r[4], r[5], r[6], r[7]);
         }
         __syncthreads();
     }
@@ -1179,11 +1218,9 @@ cudaError_t launch_variant(const AttnArgs &a, int dev, int sms, cudaStream_t str
     err = launch_pdl(kern, dim3(grid), dim3(kThreads), K::kSmem, stream, a);
     if (err != cudaSuccess)
         return err;
-    const int64_t n = static_cast<int64_t>(a.max_q) * a.Hq * (D / 4);
-    const int y = static_cast<int>(
-        std::min<int64_t>((n + kJoinItems - 1) / kJoinItems, std::max(65536 / a.B, 1)));
-    return launch_pdl(attn_join_kernel<D, BF16>, dim3(a.B, y), dim3(kJoinSplit * kJoinItems), 0,
-                      stream, a, grid);
+    const int y = std::min((a.max_q * a.Hq + 31) / 32, std::max(65535 / a.B, 1));
+    return launch_pdl(attn_join_kernel<D, BF16>, dim3(a.B, y), dim3(kJoinThreads<D>), 0, stream, a,
+                      grid);
 }
 
 }  // namespace
