@@ -12,9 +12,8 @@
 // of its 64 KB tile.
 //
 // An entry is a group's prefix or a sequence's own keys; an item is an entry's
-// row tile for one kv head.  Entries with more rows than any one sequence has,
-// or than 128, are taken as pairs: two 128-row tiles of one CTA against the
-// same K and V tile.  The tiles of
+// row tile for one kv head.  Entries of more than 128 rows are taken as pairs:
+// two 128-row tiles of one CTA against the same K and V tile.  The tiles of
 // all pair items laid end to end are split evenly over the CTAs, those of all
 // single items over the CTAs' two streams, wherever item borders fall; each
 // piece leaves unnormalised sums with their maximum and denominator, which a
@@ -22,12 +21,13 @@
 // a thousand short ones.  The split follows from the lengths, which live on
 // the device: every CTA works it out for itself (a scan over the entries).
 //
-// Roles of a CTA's eleven warps: warps 0-3 and 4-7 are the softmax of streams
+// Roles of a CTA's twelve warps: warps 0-3 and 4-7 are the softmax of streams
 // 0 and 1 (a thread per row), warp 8 loads K and V by TMA into a ring of
 // slots, warps 9 and 10 issue the MMAs (of both streams of a pair; of streams 0
-// and 1).  While one stream's softmax runs the tensor cores work for the other.
+// and 1), warp 11 only completes its group of four.  While one stream's softmax runs the tensor cores work for the other.
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -41,8 +41,10 @@ namespace {
 
 constexpr int kRows = 128;                 // rows of a stream's tile
 constexpr int kKeys = 128;                 // keys of a tile
-constexpr int kThreads = 32 * 11;
-constexpr int kMaxEntries = 4096;
+constexpr int kThreads = 32 * 12;
+// Registers a thread: 168 at launch; the loading warps give some of theirs to
+// the softmax warps, which hold a row of 128 scores (2 x 216 + 72 = 3 x 168).
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 
 // A group's prefix (first G) or a sequence's own keys.
 struct Entry {
@@ -80,14 +82,16 @@ struct AttnArgs {
     int32_t *status;
     Seg *segs;                      // workspace: the pieces of all workers
     Joint *joints;                         // workspace: [B], for the joining kernel
-    float *part_a, *part_b;                // workspace: pieces of pair / single items
-    float2 *ml_a, *ml_b;                   // and their rows' maximum and denominator
+    // workspace: the sums of pieces of pairs, of single items of groups and of
+    // sequences, and their rows' maximum and denominator
+    float *part[3];
+    float2 *ml[3];
     int64_t q_tok, q_head;
     float scale_log2;
     uint64_t wait_ns;
     int T, B, G, W, P, page, Hq, Hkv, rep, max_q, causal;
-    int rows_b;                            // a single item's rows at most: min(rep max_q, 128)
-    int cap_a, cap_b;                      // pieces that the workspace holds
+    int rows_b;                            // a sequence's single item's rows at most
+    int cap_a, cap_g, cap_b;               // pieces that the workspace holds; cap_b: all single
 };
 
 // An item is kItemCost + its tiles long when the work is split: fetching its
@@ -193,6 +197,30 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// Two fp32 values in a register pair, and the paired operations.
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t both(float x)
+{
+    return pair_of(__float_as_uint(x), __float_as_uint(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 template <bool BF16> __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
     uint32_t r;
@@ -252,6 +280,12 @@ __device__ __forceinline__ int group_of(const AttnArgs &p, const Index &x, int b
     return b < x.group_offsets[lo + 1] ? lo : -1;
 }
 
+// Rows of a piece's place: of a pair, a group's single item, a sequence's.
+__device__ __forceinline__ int rows_of(const AttnArgs &p, int kind)
+{
+    return kind == 0 ? 2 * kRows : kind == 1 ? kRows : p.rows_b;
+}
+
 // What an entry asks for: no tokens where there are more than max_q.
 struct Want {
     int tok0, tokens, k0, k1;
@@ -291,7 +325,7 @@ __device__ __forceinline__ Entry entry_of(const AttnArgs &p, const Want &w)
     if (rows > 0 && w.k1 > w.k0) {
         const int base = w.k0 / p.page * p.page;
         e.span = (w.k1 - base + kKeys - 1) / kKeys + kItemCost;
-        e.pair = rows > p.rows_b;
+        e.pair = rows > kRows;
         e.row_tiles = e.pair ? (rows + 2 * kRows - 1) / (2 * kRows) : 1;
     }
     return e;
@@ -760,7 +794,7 @@ struct Kernel {
             if (g.tiles > 0)
                 load_q(p, q, g, row0, rows, tid);
             if (tid >= rows)
-                return 0;
+                return INT_MAX;                // no row: nothing to mask, nothing kept
             return min(limit_of(p, g, g.tok0 + (row0 + tid) / p.rep), g.k1);
         };
         auto hand_over = [&](int i) {          // the queries to the issuer
@@ -776,38 +810,43 @@ struct Kernel {
             hand_over(0);
         }
         for (int i = 0, r = 0; i < pieces; i++, limit = next) {
-            const Seg g = piece(i);
             const bool pair = i < pairs, another = i + 1 < pieces;
+            const int row = pair ? stream * kRows : 0;
+            const int rows = min(max(piece(i).rows - row, 0), kRows);
+            const int tiles = piece(i).tiles, k1 = piece(i).k1;
+            const bool busy = rows > (tid & ~31);
             if (i == pairs)
                 r = 0;
             float m = -INFINITY, l = 0.0f;     // m in units of log2
-            const int end = g.tile0 + g.tiles;
-            for (int t = g.tile0; t < end; t++, r++) {
-                const int base = g.kbase + t * kKeys;
+            int base = piece(i).kbase + piece(i).tile0 * kKeys;
+            // visible columns of the first tile: from `from` to limit - base
+            int from = limit == INT_MAX ? 0 : piece(i).k0 - base;
+            for (int t = 0; t < tiles; t++, r++, base += kKeys, from -= kKeys) {
                 wait(p, s, &s.s_full[stream], s_phase);
                 s_phase ^= 1;
                 tc_fence_after();
-                if (t == end - 1 && another)
+                if (t == tiles - 1 && another)
                     next = prepare(i + 1);
-                tile(p, ts, to, g.k0 - base, limit - base, t > g.tile0, m, l);
-                if (g.k1 - base < kKeys && (g.k1 & 15))
-                    clear_tail(p, s, ring, 2 * fill_of(s, pair ? 2 : stream, r) + 1, g.k1 - base,
+                // a warp without rows leaves P as it is: a row's P only meets its own O
+                if (busy)
+                    tile(p, ts, to, from, limit == INT_MAX ? kKeys : limit - base, t > 0, m, l);
+                if (k1 - base < kKeys && (k1 & 15))
+                    clear_tail(p, s, ring, 2 * fill_of(s, pair ? 2 : stream, r) + 1, k1 - base,
                                pair, stream, tid);
                 tc_fence_before();
                 mbar_arrive(&s.p_ready[stream]);
             }
-            if (g.tiles == 0 && another)
+            if (tiles == 0 && another)
                 next = prepare(i + 1);
             // the next piece's first S may be made while this one's sums are stored
             if (another)
                 hand_over(i + 1);
-            if (g.tiles > 0) {
+            if (tiles > 0) {
                 wait(p, s, &s.o_full[stream], o_phase);
                 o_phase ^= 1;
                 tc_fence_after();
             }
-            const int row = pair ? stream * kRows : 0;
-            store(p, g, pair, row, min(max(g.rows - row, 0), kRows), to, m, l, tid);
+            store(p, piece(i), pair, row, rows, to, m, l, tid);
         }
     }
 
@@ -883,20 +922,24 @@ struct Kernel {
                 rescale(to, alpha);
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-        float sum[4] = {};
+        const uint64_t scale2 = both(p.scale_log2), ref2 = both(-ref);
+        uint64_t sum[2] = {both(0.0f), both(0.0f)};
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
             uint32_t pk[16];
 #pragma unroll
             for (int j = 0; j < 16; j++) {
-                const float a = ex2(fmaf(__uint_as_float(v[c + 2 * j]), p.scale_log2, -ref));
-                const float b = ex2(fmaf(__uint_as_float(v[c + 2 * j + 1]), p.scale_log2, -ref));
-                sum[j & 3] += a + b;
+                const uint64_t x = fma2(pair_of(v[c + 2 * j], v[c + 2 * j + 1]), scale2, ref2);
+                const float a = ex2(__uint_as_float(static_cast<uint32_t>(x)));
+                const float b = ex2(__uint_as_float(static_cast<uint32_t>(x >> 32)));
+                sum[j & 1] = add2(sum[j & 1], pair_of(__float_as_uint(a), __float_as_uint(b)));
                 pk[j] = pack2<BF16>(a, b);
             }
             tmem_st_32x32b_x16(ts + c / 2, pk);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const uint64_t all = add2(sum[0], sum[1]);
+        l += __uint_as_float(static_cast<uint32_t>(all)) +
+             __uint_as_float(static_cast<uint32_t>(all >> 32));
         tmem_wait_st();
     }
 
@@ -940,14 +983,16 @@ struct Kernel {
     static __device__ void store(const AttnArgs &p, const Seg &g, bool pair, int row, int rows,
                                  uint32_t to, float m, float l, int tid)
     {
-        const int all = pair ? 2 * kRows : p.rows_b;
+        const int kind = pair ? 0 : g.seq < 0 ? 1 : 2;
+        const int all = rows_of(p, kind);
         const int64_t base = static_cast<int64_t>(g.piece) * all;
         if (tid < rows)
-            (pair ? p.ml_a : p.ml_b)[base + row + tid] = make_float2(m, l);
-        if (g.tiles == 0)
+            (pair ? p.ml[0] : kind == 1 ? p.ml[1] : p.ml[2])[base + row + tid] = make_float2(m, l);
+        if (g.tiles == 0 || rows <= (tid & ~31))
             return;
-        float4 *out = reinterpret_cast<float4 *>(pair ? p.part_a : p.part_b) + base * (D / 4) + row +
-                      tid;
+        float4 *out = reinterpret_cast<float4 *>(pair ? p.part[0] : kind == 1 ? p.part[1]
+                                                                              : p.part[2]) +
+                      base * (D / 4) + row + tid;
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
             uint32_t o[16];
@@ -1002,12 +1047,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp < 8)
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         K::softmax(p, s, qbuf, ring, warp >> 2);
-    else if (warp == 8)
-        K::loader(p, s, ring, lane);
-    else
-        K::issuer(p, s, qbuf, ring, warp - 9);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 8)
+            K::loader(p, s, ring, lane);
+        else if (warp < 11)
+            K::issuer(p, s, qbuf, ring, warp - 9);
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 8) {
@@ -1017,26 +1066,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 }
 
 // -------------------------------------------------------------------- join
-// A row's pieces joined: CTA (b, y) takes 32 of sequence b's rows (a lane
-// each: neighbouring rows are side by side in a piece).  A warp has 16 of the
-// D values and every other piece, four pieces' loads in flight; the two halves
-// are added up at the end, in a fixed order.
-template <int D> constexpr int kJoinThreads = 32 * (D / 16) * 2;
+// A row's pieces joined: CTA (b, y, z) takes 32 of sequence b's rows (a lane
+// each: neighbouring rows are side by side in a piece) and some of the D
+// values.  A warp has 16 of those and every SPLIT-th piece, kBatch pieces'
+// loads in flight; the SPLIT parts are added up at the end, in a fixed order.
+// Few rows can have many pieces (one long prefix cut for every CTA), many rows
+// have few: SPLIT is 4 up to kJoinFewRows rows in all and 1 above.
+constexpr int kJoinFewRows = 4096;
+template <int D, int SPLIT> constexpr int kJoinSides = 8 / SPLIT < D / 16 ? 8 / SPLIT : D / 16;
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kJoinThreads<D>)
+template <int D, bool BF16, int SPLIT>
+__global__ void __launch_bounds__(32 * SPLIT *kJoinSides<D, SPLIT>, SPLIT == 1 ? 3 : 2)
     attn_join_kernel(const __grid_constant__ AttnArgs p, int grid)
 {
-    constexpr int kBatch = 4, kGroups = D / 16;
-    __shared__ float4 so[4][kGroups][32];
-    __shared__ float2 sm[kGroups][32];
+    constexpr int kBatch = SPLIT == 1 ? 2 : 4, kSides = kJoinSides<D, SPLIT>;
+    __shared__ float4 so[SPLIT][4][kSides][32];
+    __shared__ float2 sm[SPLIT][kSides][32];
     pdl_wait();
     pdl_trigger();
     const Joint j = p.joints[blockIdx.x];
     const int rows = j.tokens * p.rep;         // of one kv head
     const int n = rows * p.Hkv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int cg = warp % kGroups, half = warp / kGroups;
+    const int side = warp % kSides, cg = kSides * blockIdx.z + side, split = warp / kSides;
     for (int i0 = blockIdx.y * 32; i0 < n; i0 += gridDim.y * 32) {
         const int i = min(i0 + lane, n - 1), head = i / rows, row = i - head * rows;
         float m = -INFINITY, l = 0.0f;
@@ -1047,25 +1099,26 @@ __global__ void __launch_bounds__(kJoinThreads<D>)
             if (en.span == 0)
                 continue;
             const int er = row + en.row, step = en.pair ? 2 * kRows : kRows;
-            const int stride = en.pair ? 2 * kRows : p.rows_b, at = er % step;
+            const int kind = en.pair ? 0 : k + 1, stride = rows_of(p, kind), at = er % step;
             const int local = head * en.row_tiles + er / step;
             const int all = en.pair ? j.all[1] : j.all[0];
             const int workers = workers_for(all, en.pair ? grid : 2 * grid);
             const int x0 = en.place + local * en.span;
             const int w0 = worker_of(all, workers, x0);
             const int w1 = worker_of(all, workers, x0 + en.span - 1);
-            if (en.item0 + local + w1 >= (en.pair ? p.cap_a : p.cap_b))
+            if (en.item0 + local + w1 >= (kind == 0 ? p.cap_a : kind == 1 ? p.cap_g : p.cap_b))
                 continue;
             const int64_t first = static_cast<int64_t>(en.item0 + local) * stride;
-            const float2 *ml = (en.pair ? p.ml_a : p.ml_b) + first + at;
-            const float4 *part = reinterpret_cast<const float4 *>(en.pair ? p.part_a : p.part_b) +
+            const float2 *ml = (en.pair ? p.ml[0] : p.ml[k + 1]) + first + at;
+            const float4 *part = reinterpret_cast<const float4 *>(en.pair ? p.part[0]
+                                                                          : p.part[k + 1]) +
                                  first * (D / 4) + cg * 4 * stride + at;
-            for (int w = w0 + half; w <= w1; w += 2 * kBatch) {
+            for (int w = w0 + split; w <= w1; w += SPLIT * kBatch) {
                 float4 v[kBatch][4];
                 float2 s[kBatch];
 #pragma unroll
                 for (int u = 0; u < kBatch; u++) {
-                    const int64_t x = w + 2 * u;
+                    const int64_t x = w + SPLIT * u;
                     s[u] = make_float2(-INFINITY, 0.0f);
                     if (x <= w1) {
                         s[u] = ml[x * stride];
@@ -1102,27 +1155,35 @@ __global__ void __launch_bounds__(kJoinThreads<D>)
                 }
             }
         }
-        if (half == 1) {
-            sm[cg][lane] = make_float2(m, l);
+        if (split > 0) {
+            sm[split - 1][side][lane] = make_float2(m, l);
 #pragma unroll
             for (int c = 0; c < 4; c++)
-                so[c][cg][lane] = o[c];
+                so[split - 1][c][side][lane] = o[c];
         }
         __syncthreads();
-        if (half == 0 && i0 + lane < n) {
-            const float2 s = sm[cg][lane];
-            const float top = fmaxf(m, s.x), ref = top == -INFINITY ? 0.0f : top;
-            const float f0 = ex2(m - ref), f1 = ex2(s.x - ref);
-            l = l * f0 + s.y * f1;
+        if (split == 0 && i0 + lane < n) {
+#pragma unroll
+            for (int k = 0; k < SPLIT - 1; k++) {
+                const float2 s = sm[k][side][lane];
+                const float top = fmaxf(m, s.x), ref = top == -INFINITY ? 0.0f : top;
+                const float f0 = ex2(m - ref), f1 = ex2(s.x - ref);
+                m = top;
+                l = l * f0 + s.y * f1;
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    const float4 v = so[k][c][side][lane];
+                    o[c] = make_float4(o[c].x * f0 + v.x * f1, o[c].y * f0 + v.y * f1,
+                                       o[c].z * f0 + v.z * f1, o[c].w * f0 + v.w * f1);
+                }
+            }
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;     // a row that sees nothing is zero
             const int tok = j.tok0 + row / p.rep, h = head * p.rep + row % p.rep;
             uint32_t r[8];
 #pragma unroll
             for (int c = 0; c < 4; c++) {
-                const float4 v = so[c][cg][lane];
-                r[2 * c] = pack2<BF16>((o[c].x * f0 + v.x * f1) * inv, (o[c].y * f0 + v.y * f1) * inv);
-                r[2 * c + 1] =
-                    pack2<BF16>((o[c].z * f0 + v.z * f1) * inv, (o[c].w * f0 + v.w * f1) * inv);
+                r[2 * c] = pack2<BF16>(o[c].x * inv, o[c].y * inv);
+                r[2 * c + 1] = pack2<BF16>(o[c].z * inv, o[c].w * inv);
             }
             uint4 *out = reinterpret_cast<uint4 *>(
                 p.out + (static_cast<int64_t>(tok) * p.Hq + h) * D + cg * 16);
@@ -1167,8 +1228,8 @@ bool encode_pages(CUtensorMap *map, const AttnProblem &q, const uint16_t *base)
 
 // Where a call's pieces lie in its workspace.
 struct Space {
-    int cap_a, cap_b, rows_b;
-    size_t joints, segs, ml_a, ml_b, part_a, part_b, total;
+    int cap_a, cap_g, cap_b, rows_b;
+    size_t joints, segs, ml[3], part[3], total;
 };
 
 constexpr int kMaxGrid = 256;              // CTAs that a workspace allows for
@@ -1177,12 +1238,12 @@ Space space_of(int T, int B, int G, int max_q, int Hq, int Hkv, int D)
 {
     Space s{};
     const int64_t rep = Hq / Hkv;
-    // A row is in two entries, and an entry of R rows has at most R / 256 + 1
-    // pair items (R / 128 where it is a sequence: R > 128 then).  Each worker
-    // cuts at most one item more.
-    s.cap_a = static_cast<int>(std::min<int64_t>((2 * T * rep / kRows + G + 1) * Hkv, 1 << 24)) +
-              kMaxGrid;
-    s.cap_b = (B + G) * Hkv + 2 * kMaxGrid;
+    // Each worker cuts at most one item more.  An entry of R > 128 rows has at
+    // most R / 128 pair items, and a row is in two entries; groups come first
+    // among the single items.
+    s.cap_a = static_cast<int>(std::min<int64_t>(2 * T * rep / kRows * Hkv, 1 << 24)) + kMaxGrid;
+    s.cap_g = G * Hkv + 2 * kMaxGrid;
+    s.cap_b = s.cap_g + B * Hkv;
     s.rows_b = static_cast<int>(std::min<int64_t>(rep * max_q, kRows));
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -1192,10 +1253,13 @@ Space space_of(int T, int B, int G, int max_q, int Hq, int Hkv, int D)
     };
     s.joints = take(sizeof(Joint) * static_cast<size_t>(B));
     s.segs = take(sizeof(Seg) * (static_cast<size_t>(s.cap_a) + s.cap_b));
-    s.ml_a = take(sizeof(float2) * static_cast<size_t>(s.cap_a) * 2 * kRows);
-    s.ml_b = take(sizeof(float2) * static_cast<size_t>(s.cap_b) * s.rows_b);
-    s.part_a = take(sizeof(float) * static_cast<size_t>(s.cap_a) * 2 * kRows * D);
-    s.part_b = take(sizeof(float) * static_cast<size_t>(s.cap_b) * s.rows_b * D);
+    const size_t rows[3] = {static_cast<size_t>(s.cap_a) * 2 * kRows,
+                            G > 0 ? static_cast<size_t>(s.cap_g) * kRows : 0,
+                            static_cast<size_t>(s.cap_b) * s.rows_b};
+    for (int i = 0; i < 3; i++) {
+        s.ml[i] = take(sizeof(float2) * rows[i]);
+        s.part[i] = take(sizeof(float) * rows[i] * D);
+    }
     s.total = at;
     return s;
 }
@@ -1219,8 +1283,11 @@ cudaError_t launch_variant(const AttnArgs &a, int dev, int sms, cudaStream_t str
     if (err != cudaSuccess)
         return err;
     const int y = std::min((a.max_q * a.Hq + 31) / 32, std::max(65535 / a.B, 1));
-    return launch_pdl(attn_join_kernel<D, BF16>, dim3(a.B, y), dim3(kJoinThreads<D>), 0, stream, a,
-                      grid);
+    if (static_cast<int64_t>(a.T) * a.Hq <= kJoinFewRows)
+        return launch_pdl(attn_join_kernel<D, BF16, 4>, dim3(a.B, y, D / 16 / kJoinSides<D, 4>),
+                          dim3(128 * kJoinSides<D, 4>), 0, stream, a, grid);
+    return launch_pdl(attn_join_kernel<D, BF16, 1>, dim3(a.B, y, D / 16 / kJoinSides<D, 1>),
+                      dim3(32 * kJoinSides<D, 1>), 0, stream, a, grid);
 }
 
 }  // namespace
@@ -1247,11 +1314,12 @@ cudaError_t launch_attn(const AttnProblem &q, cudaStream_t stream)
     uint8_t *ws = static_cast<uint8_t *>(q.workspace);
     a.joints = reinterpret_cast<Joint *>(ws + s.joints);
     a.segs = reinterpret_cast<Seg *>(ws + s.segs);
-    a.ml_a = reinterpret_cast<float2 *>(ws + s.ml_a);
-    a.ml_b = reinterpret_cast<float2 *>(ws + s.ml_b);
-    a.part_a = reinterpret_cast<float *>(ws + s.part_a);
-    a.part_b = reinterpret_cast<float *>(ws + s.part_b);
+    for (int i = 0; i < 3; i++) {
+        a.ml[i] = reinterpret_cast<float2 *>(ws + s.ml[i]);
+        a.part[i] = reinterpret_cast<float *>(ws + s.part[i]);
+    }
     a.cap_a = s.cap_a;
+    a.cap_g = s.cap_g;
     a.cap_b = s.cap_b;
     a.rows_b = s.rows_b;
     a.q = q.q;
