@@ -21,10 +21,10 @@
 // a thousand short ones.  The split follows from the lengths, which live on
 // the device: every CTA works it out for itself (a scan over the entries).
 //
-// Roles of a CTA's twelve warps: warps 0-3 and 4-7 are the softmax of streams
+// Roles of a CTA's eleven warps: warps 0-3 and 4-7 are the softmax of streams
 // 0 and 1 (a thread per row), warp 8 loads K and V by TMA into a ring of
 // slots, warps 9 and 10 issue the MMAs (of both streams of a pair; of streams 0
-// and 1), warp 11 only completes its group of four.  While one stream's softmax runs the tensor cores work for the other.
+// and 1).  While one stream's softmax runs the tensor cores work for the other.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -41,10 +41,7 @@ namespace {
 
 constexpr int kRows = 128;                 // rows of a stream's tile
 constexpr int kKeys = 128;                 // keys of a tile
-constexpr int kThreads = 32 * 12;
-// Registers a thread: 168 at launch; the loading warps give some of theirs to
-// the softmax warps, which hold a row of 128 scores (2 x 216 + 72 = 3 x 168).
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr int kThreads = 32 * 11;
 
 // A group's prefix (first G) or a sequence's own keys.
 struct Entry {
@@ -399,7 +396,7 @@ struct Kernel {
 
     struct Shared {
         alignas(8) uint64_t full[kSlots], empty[kSlots];
-        uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2], pairs_done;
+        uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2], drained[2], pairs_done;
         uint32_t tmem;
         int abort_flag;
         int seg0[3], segs[3], tiles[3];        // single items of streams 0 and 1; pairs
@@ -669,6 +666,7 @@ struct Kernel {
         const int slot = fill % kSlots;
         wait(p, s, &s.full[slot], (fill / kSlots) & 1);
         tc_fence_after();
+        __syncwarp();
         const uint64_t qd = sdesc_sw128(smem_u32(qbuf + stream * kTileBytes));
         const uint64_t kd = sdesc_sw128(smem_u32(ring + slot * kTileBytes));
 #pragma unroll
@@ -690,6 +688,7 @@ struct Kernel {
         const int slot = fill % kSlots;
         wait(p, s, &s.full[slot], (fill / kSlots) & 1);
         tc_fence_after();
+        __syncwarp();
         const uint32_t va = smem_u32(ring + slot * kTileBytes);
         const uint32_t ts = s.tmem + kS + 128 * stream, to = s.tmem + kO + D * stream;
         const int steps = (min(keys, kKeys) + 15) / 16;
@@ -765,6 +764,10 @@ struct Kernel {
                          t == tiles - 1, true);
             }
         }
+        // nothing of this warp's is under way when the CTA ends
+        __syncwarp();
+        tc_commit_elect(&s.drained[stream]);
+        wait(p, s, &s.drained[stream], 0);
     }
 
     // ------------------------------------------------------------- softmax
@@ -787,15 +790,19 @@ struct Kernel {
         };
         // A piece's queries on their way to shared memory, and how many keys this
         // thread's row sees.  Called when no MMA reads the queries any more.
+        // The lanes part ways in it, and the tensor-memory instructions that
+        // follow need them together again.
         auto prepare = [&](int i) {
             const Seg &g = piece(i);
             const int row0 = g.row0 + (i < pairs ? stream * kRows : 0);
             const int rows = min(max(g.row0 + g.rows - row0, 0), kRows);
             if (g.tiles > 0)
                 load_q(p, q, g, row0, rows, tid);
-            if (tid >= rows)
-                return INT_MAX;                // no row: nothing to mask, nothing kept
-            return min(limit_of(p, g, g.tok0 + (row0 + tid) / p.rep), g.k1);
+            int sees = INT_MAX;                // no row: nothing to mask, nothing kept
+            if (tid < rows)
+                sees = min(limit_of(p, g, g.tok0 + (row0 + tid) / p.rep), g.k1);
+            __syncwarp();
+            return sees;
         };
         auto hand_over = [&](int i) {          // the queries to the issuer
             if (piece(i).tiles == 0)
@@ -828,6 +835,7 @@ struct Kernel {
                 if (t == tiles - 1 && another)
                     next = prepare(i + 1);
                 // a warp without rows leaves P as it is: a row's P only meets its own O
+                __syncwarp();
                 if (busy)
                     tile(p, ts, to, from, limit == INT_MAX ? kKeys : limit - base, t > 0, m, l);
                 if (k1 - base < kKeys && (k1 & 15))
@@ -945,6 +953,7 @@ struct Kernel {
 
     static __device__ __forceinline__ void rescale(uint32_t to, float alpha)
     {
+        __syncwarp();
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
@@ -974,6 +983,7 @@ struct Kernel {
                 make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
+        __syncwarp();
         if (pair)
             asm volatile("bar.sync 1, 256;" ::: "memory");
     }
@@ -988,6 +998,7 @@ struct Kernel {
         const int64_t base = static_cast<int64_t>(g.piece) * all;
         if (tid < rows)
             (pair ? p.ml[0] : kind == 1 ? p.ml[1] : p.ml[2])[base + row + tid] = make_float2(m, l);
+        __syncwarp();
         if (g.tiles == 0 || rows <= (tid & ~31))
             return;
         float4 *out = reinterpret_cast<float4 *>(pair ? p.part[0] : kind == 1 ? p.part[1]
@@ -996,6 +1007,7 @@ struct Kernel {
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
             uint32_t o[16];
+            __syncwarp();
             tmem_ld_32x32b_x16(to + c, o);
             if (tid < rows) {
 #pragma unroll
@@ -1029,6 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_ready[i], kRows);
             mbar_init(&s.o_full[i], 1);
+            mbar_init(&s.drained[i], 1);
         }
         mbar_init(&s.pairs_done, 1);
         s.abort_flag = 0;
@@ -1047,20 +1060,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    if (warp < 8)
         K::softmax(p, s, qbuf, ring, warp >> 2);
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == 8)
-            K::loader(p, s, ring, lane);
-        else if (warp < 11)
-            K::issuer(p, s, qbuf, ring, warp - 9);
-    }
+    else if (warp == 8)
+        K::loader(p, s, ring, lane);
+    else
+        K::issuer(p, s, qbuf, ring, warp - 9);
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == 8) {
         tc_fence_after();
+        __syncwarp();
         tmem_dealloc(s.tmem, 512);
     }
 }
