@@ -399,6 +399,7 @@ struct Kernel {
         uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2], drained[2], pairs_done;
         uint32_t tmem;
         int abort_flag;
+        int requested;                         // fills requested of the ring so far
         int seg0[3], segs[3], tiles[3];        // single items of streams 0 and 1; pairs
         int4 sums[kThreads / 32];
     };
@@ -558,6 +559,34 @@ struct Kernel {
                               p.wait_ns);
     }
 
+    // Fill `fill` has landed.  A slot's fills may alternate between the streams,
+    // so this one may be awaited while the slot's last, the other stream's, has
+    // yet to land; by its parity alone that would pass for landed.  Hence first
+    // the count of fills requested: when this one has been, the slot's last has
+    // been used, and the parity says what it means.
+    static __device__ __forceinline__ void wait_full(const AttnArgs &p, Shared &s, int fill)
+    {
+        volatile int *requested = &s.requested;
+        if (!__all_sync(0xffffffffu, *requested > fill)) {
+            const uint64_t t0 = global_timer_ns();
+            for (uint32_t it = 1; !__all_sync(0xffffffffu, *requested > fill); it++) {
+                __nanosleep(20);
+                if ((it & 63u) == 0) {
+                    const bool late = global_timer_ns() - t0 > p.wait_ns;
+                    if (__any_sync(0xffffffffu, late)) {
+                        if ((threadIdx.x & 31) == 0) {
+                            s.abort_flag = 1;
+                            if (p.status)
+                                atomicOr(p.status, kDevPipelineTimeout);
+                        }
+                        return;
+                    }
+                }
+            }
+        }
+        wait(p, s, &s.full[fill % kSlots], (fill / kSlots) & 1);
+    }
+
     // ------------------------------------------------------------- loading
     static __device__ void load_slot(const AttnArgs &p, Shared &s, uint8_t *ring, int fill,
                                      const CUtensorMap *map, int head, int page_id,
@@ -567,8 +596,11 @@ struct Kernel {
         if (use > 0)
             wait(p, s, &s.empty[slot], (use - 1) & 1);
         uint8_t *dst = ring + slot * kTileBytes;
-        if (lane == 0)
+        if (lane == 0) {
             mbar_arrive_expect_tx(&s.full[slot], kTileBytes);
+            __threadfence_block();
+            *static_cast<volatile int *>(&s.requested) = fill + 1;
+        }
         __syncwarp();
         const int boxes = kKeys / p.page * kBlocks;
         const int pg = __shfl_sync(0xffffffffu, page_id, lane / kBlocks);
@@ -664,7 +696,7 @@ struct Kernel {
                                                     uint8_t *ring, int stream, int fill, bool last_use)
     {
         const int slot = fill % kSlots;
-        wait(p, s, &s.full[slot], (fill / kSlots) & 1);
+        wait_full(p, s, fill);
         tc_fence_after();
         __syncwarp();
         const uint64_t qd = sdesc_sw128(smem_u32(qbuf + stream * kTileBytes));
@@ -686,7 +718,7 @@ struct Kernel {
                                                     bool last, bool last_use)
     {
         const int slot = fill % kSlots;
-        wait(p, s, &s.full[slot], (fill / kSlots) & 1);
+        wait_full(p, s, fill);
         tc_fence_after();
         __syncwarp();
         const uint32_t va = smem_u32(ring + slot * kTileBytes);
@@ -783,19 +815,19 @@ struct Kernel {
         uint8_t *q = qbuf + stream * kTileBytes;
         uint32_t s_phase = 0, o_phase = 0;
         // the pairs' pieces, then this stream's own
-        const int pairs = s.segs[2], pieces = pairs + s.segs[stream];
         auto piece = [&](int i) -> const Seg & {
-            return i < pairs ? p.segs[p.cap_b + s.seg0[2] + i]
-                             : p.segs[s.seg0[stream] + i - pairs];
+            return i < s.segs[2] ? p.segs[p.cap_b + s.seg0[2] + i]
+                                 : p.segs[s.seg0[stream] + i - s.segs[2]];
         };
+        auto pieces = [&] { return s.segs[2] + s.segs[stream]; };
         // A piece's queries on their way to shared memory, and how many keys this
         // thread's row sees.  Called when no MMA reads the queries any more.
         // The lanes part ways in it, and the tensor-memory instructions that
         // follow need them together again.
         auto prepare = [&](int i) {
             const Seg &g = piece(i);
-            const int row0 = g.row0 + (i < pairs ? stream * kRows : 0);
-            const int rows = min(max(g.row0 + g.rows - row0, 0), kRows);
+            const int row0 = g.row0 + (i < s.segs[2] ? stream * kRows : 0);
+            const int rows = rows_here(g, i < s.segs[2], stream);
             if (g.tiles > 0)
                 load_q(p, q, g, row0, rows, tid);
             int sees = INT_MAX;                // no row: nothing to mask, nothing kept
@@ -812,50 +844,56 @@ struct Kernel {
             mbar_arrive(&s.q_ready[stream]);
         };
         int limit = 0, next = 0;
-        if (pieces > 0) {
+        if (pieces() > 0) {
             limit = prepare(0);
             hand_over(0);
         }
-        for (int i = 0, r = 0; i < pieces; i++, limit = next) {
-            const bool pair = i < pairs, another = i + 1 < pieces;
-            const int row = pair ? stream * kRows : 0;
-            const int rows = min(max(piece(i).rows - row, 0), kRows);
-            const int tiles = piece(i).tiles, k1 = piece(i).k1;
-            const bool busy = rows > (tid & ~31);
-            if (i == pairs)
+        for (int i = 0, r = 0; i < pieces(); i++, limit = next) {
+            if (i == s.segs[2])
                 r = 0;
+            const bool busy = rows_here(piece(i), i < s.segs[2], stream) > (tid & ~31);
             float m = -INFINITY, l = 0.0f;     // m in units of log2
             int base = piece(i).kbase + piece(i).tile0 * kKeys;
-            // visible columns of the first tile: from `from` to limit - base
-            int from = limit == INT_MAX ? 0 : piece(i).k0 - base;
-            for (int t = 0; t < tiles; t++, r++, base += kKeys, from -= kKeys) {
+            int left = piece(i).tiles;
+            for (bool first = true; left > 0; left--, r++, base += kKeys, first = false) {
                 wait(p, s, &s.s_full[stream], s_phase);
                 s_phase ^= 1;
                 tc_fence_after();
-                if (t == tiles - 1 && another)
+                if (left == 1 && i + 1 < pieces())
                     next = prepare(i + 1);
                 // a warp without rows leaves P as it is: a row's P only meets its own O
                 __syncwarp();
                 if (busy)
-                    tile(p, ts, to, from, limit == INT_MAX ? kKeys : limit - base, t > 0, m, l);
-                if (k1 - base < kKeys && (k1 & 15))
-                    clear_tail(p, s, ring, 2 * fill_of(s, pair ? 2 : stream, r) + 1, k1 - base,
-                               pair, stream, tid);
+                    tile(p, ts, to, limit == INT_MAX ? 0 : piece(i).k0 - base,
+                         limit == INT_MAX ? kKeys : limit - base, !first, m, l);
+                const int valid = piece(i).k1 - base;
+                if (valid < kKeys && (valid & 15))
+                    clear_tail(p, s, ring, 2 * fill_of(s, i < s.segs[2] ? 2 : stream, r) + 1, valid,
+                               i < s.segs[2], stream, tid);
                 tc_fence_before();
                 mbar_arrive(&s.p_ready[stream]);
             }
-            if (tiles == 0 && another)
-                next = prepare(i + 1);
-            // the next piece's first S may be made while this one's sums are stored
-            if (another)
+            if (i + 1 < pieces()) {
+                if (piece(i).tiles == 0)
+                    next = prepare(i + 1);
+                // the next piece's first S may be made while this one's sums are stored
                 hand_over(i + 1);
-            if (tiles > 0) {
+            }
+            if (piece(i).tiles > 0) {
                 wait(p, s, &s.o_full[stream], o_phase);
                 o_phase ^= 1;
                 tc_fence_after();
             }
-            store(p, piece(i), pair, row, rows, to, m, l, tid);
+            const bool pair = i < s.segs[2];
+            store(p, piece(i), pair, pair ? stream * kRows : 0, rows_here(piece(i), pair, stream), to,
+                  m, l, tid);
         }
+    }
+
+    // A stream's rows of a piece.
+    static __device__ __forceinline__ int rows_here(const Seg &g, bool pair, int stream)
+    {
+        return min(max(g.rows - (pair ? stream * kRows : 0), 0), kRows);
     }
 
     // Rows [row0, row0 + rows) of a piece's queries, 16 bytes a thread and
@@ -973,7 +1011,7 @@ struct Kernel {
                                       int valid, bool pair, int stream, int tid)
     {
         const int slot = fill % kSlots;
-        wait(p, s, &s.full[slot], (fill / kSlots) & 1);
+        wait_full(p, s, fill);
         uint8_t *v = ring + slot * kTileBytes;
         const int end = (valid + 15) & ~15, n = (end - valid) * 8 * kBlocks;
         const int at = pair ? stream * 128 + tid : tid, step = pair ? 256 : 128;
@@ -1045,6 +1083,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         }
         mbar_init(&s.pairs_done, 1);
         s.abort_flag = 0;
+        s.requested = 0;
         fence_mbar_init();
         prefetch_tmap(&p.k_map);
         prefetch_tmap(&p.v_map);

@@ -9,6 +9,7 @@
 // the pool's front stays dense.  Finding them is a scan of refs by one CTA
 // (4096 pages a round); the rest are plain grid-wide copies, bound by HBM.
 #include <algorithm>
+#include <atomic>
 
 #include "../../include/w4moe.h"
 #include "launch.h"
@@ -320,36 +321,112 @@ __global__ void __launch_bounds__(256) kv_fork_kernel(uint8_t *cache, int64_t pa
 }
 
 // ------------------------------------------------------------- copy pages
-__global__ void __launch_bounds__(256) kv_copy_kernel(uint8_t *cache, int planes,
-                                                      int64_t page_bytes, int P,
-                                                      const int32_t *src, const int32_t *dst,
-                                                      const int32_t *count, int n,
-                                                      int32_t *status, const int32_t *table_in,
-                                                      int32_t *table_out, int64_t entries,
-                                                      const int32_t *remap)
+// Whole pages by bulk copies through shared memory: one warp a CTA walks its
+// chunks of at most 16 KB, lane 0 issuing; the loads run kAhead chunks before
+// the stores, and a slot is loaded again once its store has read it.  No value
+// passes through registers, so two warps an SM keep 2 x 96 KB under way.
+constexpr int kSlots = 6, kAhead = 3, kChunk = 16 * 1024;
+
+__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes)
 {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
+                 "cp.async.bulk.commit_group;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
+
+__global__ void __launch_bounds__(32) kv_copy_kernel(uint8_t *cache, int planes,
+                                                     int64_t page_bytes, int P, const int32_t *src,
+                                                     const int32_t *dst, const int32_t *count,
+                                                     int n, int32_t *status,
+                                                     const int32_t *table_in, int32_t *table_out,
+                                                     int64_t entries, const int32_t *remap)
+{
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ __align__(8) uint64_t full[kSlots];
+    __shared__ int abort_flag;
+    const int lane = threadIdx.x;
+    if (lane == 0) {
+        for (int i = 0; i < kSlots; i++)
+            mbar_init(&full[i], 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncwarp();
     pdl_wait();
     pdl_trigger();
-    const int64_t pairs = count ? *count : n;
     // a share of the table's entries first (compaction only)
-    for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < entries;
-         e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    for (int64_t e = static_cast<int64_t>(blockIdx.x) * 32 + lane; e < entries;
+         e += static_cast<int64_t>(gridDim.x) * 32) {
         const int p = table_in[e];
         const bool ok = p >= 0 && p < P;
         if (!ok && p != -1)
             raise_status(status, W4_DEV_BAD_PAGE);
         table_out[e] = ok ? remap[p] : p;
     }
-    for (int64_t item = blockIdx.x; item < pairs * planes; item += gridDim.x) {
-        const int64_t plane = item % planes, i = item / planes;
-        const int a = src[i], b = dst[i];
-        if (a < 0 || a >= P || b < 0 || b >= P) {
-            if (plane == 0 && threadIdx.x == 0)
+    const int64_t pairs = count ? *count : n, parts = (page_bytes + kChunk - 1) / kChunk;
+    const int64_t chunks = pairs * planes * parts;
+    uint8_t *to[kAhead];                   // of the chunks loaded and not yet stored (lane 0)
+    uint32_t size[kAhead];
+    int issued = 0, stored = 0;
+    auto store_next = [&](uint8_t *out, uint32_t bytes) {
+        const int slot = stored % kSlots;
+        if (mbar_wait(&full[slot], (stored / kSlots) & 1, &abort_flag, status, kDevPipelineTimeout))
+            bulk_store(out, ring + slot * kChunk, bytes);
+        stored++;
+    };
+    for (int64_t c0 = blockIdx.x; c0 < chunks; c0 += 32ll * gridDim.x) {
+        // the next 32 chunks' places, a lane each: one memory latency for all
+        const int64_t c = c0 + static_cast<int64_t>(lane) * gridDim.x;
+        int64_t from = -1, into = 0;
+        uint32_t bytes = 0;
+        if (c < chunks) {
+            const int64_t part = c % parts, item = c / parts, plane = item % planes;
+            const int64_t i = item / planes;
+            const int a = src[i], b = dst[i];
+            if (a >= 0 && a < P && b >= 0 && b < P) {
+                from = (plane * P + a) * page_bytes + part * kChunk;
+                into = (plane * P + b) * page_bytes + part * kChunk;
+                bytes = static_cast<uint32_t>(min(static_cast<int64_t>(kChunk),
+                                                  page_bytes - part * kChunk));
+            } else if (plane == 0 && part == 0) {
                 raise_status(status, W4_DEV_BAD_PAGE);
-            continue;
+            }
         }
-        uint8_t *base = cache + plane * P * page_bytes;
-        copy_bytes(base + b * page_bytes, base + a * page_bytes, page_bytes);
+        for (int l = 0; l < 32; l++) {
+            const int64_t f = __shfl_sync(0xffffffffu, from, l), t = __shfl_sync(0xffffffffu, into, l);
+            const uint32_t size_l = __shfl_sync(0xffffffffu, bytes, l);
+            if (f < 0 || lane != 0)
+                continue;
+            if (issued - stored == kAhead) {
+                store_next(to[0], size[0]);
+#pragma unroll
+                for (int u = 0; u + 1 < kAhead; u++) {
+                    to[u] = to[u + 1];
+                    size[u] = size[u + 1];
+                }
+            }
+            // the store of kSlots chunks ago has read its slot when all but the last
+            // kSlots - kAhead have
+            if (issued >= kSlots)
+                asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kSlots - kAhead) : "memory");
+            const int slot = issued % kSlots;
+            mbar_arrive_expect_tx(&full[slot], size_l);
+            bulk_load_nohint(ring + slot * kChunk, cache + f, size_l, &full[slot]);
+#pragma unroll
+            for (int u = 0; u < kAhead; u++)
+                if (u == issued - stored) {
+                    to[u] = cache + t;
+                    size[u] = size_l;
+                }
+            issued++;
+        }
+    }
+    if (lane == 0) {
+#pragma unroll
+        for (int u = 0; u < kAhead; u++)
+            if (stored < issued)
+                store_next(to[u], size[u]);
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 }
 
@@ -456,6 +533,20 @@ int sm_count()
     return std::max(sms, 1);
 }
 
+cudaError_t raise_copy_limit()
+{
+    static std::atomic<uint64_t> raised{0};      // devices whose limit is raised already
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess || (raised.load(std::memory_order_relaxed) >> (dev & 63) & 1u))
+        return err;
+    err = cudaFuncSetAttribute(kv_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kSlots * kChunk);
+    if (err == cudaSuccess)
+        raised.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+    return err;
+}
+
 }  // namespace
 
 cudaError_t launch_kv_reserve(int32_t *table, int B, int W, int32_t *lens, int32_t *refs, int P,
@@ -494,10 +585,13 @@ cudaError_t launch_kv_copy(uint8_t *cache, int planes, int64_t page_bytes, int P
                            const int32_t *src, const int32_t *dst, int n, int32_t *status,
                            cudaStream_t stream)
 {
-    const int64_t items = static_cast<int64_t>(n) * planes;
-    const int grid = static_cast<int>(std::min<int64_t>(items, 8ll * sm_count()));
-    return launch_pdl(kv_copy_kernel, dim3(grid), dim3(256), 0, stream, cache, planes, page_bytes,
-                      P, src, dst, static_cast<const int32_t *>(nullptr), n, status,
+    const int64_t chunks = static_cast<int64_t>(n) * planes * ((page_bytes + kChunk - 1) / kChunk);
+    cudaError_t err = raise_copy_limit();
+    if (err != cudaSuccess)
+        return err;
+    const int grid = static_cast<int>(std::min<int64_t>(chunks, 2ll * sm_count()));
+    return launch_pdl(kv_copy_kernel, dim3(grid), dim3(32), kSlots * kChunk, stream, cache, planes,
+                      page_bytes, P, src, dst, static_cast<const int32_t *>(nullptr), n, status,
                       static_cast<const int32_t *>(nullptr), static_cast<int32_t *>(nullptr),
                       static_cast<int64_t>(0), static_cast<const int32_t *>(nullptr));
 }
@@ -513,8 +607,11 @@ cudaError_t launch_kv_compact(uint8_t *cache, int planes, int64_t page_bytes, co
                                  refs, refs_out, P, count, src, dst, remap);
     if (err != cudaSuccess)
         return err;
-    return launch_pdl(kv_copy_kernel, dim3(8 * sm_count()), dim3(256), 0, stream, cache, planes,
-                      page_bytes, P, static_cast<const int32_t *>(src),
+    err = raise_copy_limit();
+    if (err != cudaSuccess)
+        return err;
+    return launch_pdl(kv_copy_kernel, dim3(2 * sm_count()), dim3(32), kSlots * kChunk, stream, cache,
+                      planes, page_bytes, P, static_cast<const int32_t *>(src),
                       static_cast<const int32_t *>(dst), static_cast<const int32_t *>(count), 0,
                       status, table, table_out, entries, static_cast<const int32_t *>(remap));
 }
