@@ -224,14 +224,14 @@ __device__ void build_jobs(Shared &s, Seen &seen, int A, int E)
 }
 
 // --------------------------------------------------------------- MMA core
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1)
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1, const float (&c)[4])
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+          "f"(c[3]));
 }
 
 // Eight codes of two weight rows (one word each) against eight activations
@@ -240,8 +240,10 @@ __device__ __forceinline__ void mma_word(float (&lo)[4], float (&hi)[4], uint32_
                                          const uint4 &b)
 {
     const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
-    mma16816(lo, w0 & 0x000F000Fu, w1 & 0x000F000Fu, v0 & 0x000F000Fu, v1 & 0x000F000Fu, b.x, b.y);
-    mma16816(hi, w0 & 0x00F000F0u, w1 & 0x00F000F0u, v0 & 0x00F000F0u, v1 & 0x00F000F0u, b.z, b.w);
+    mma16816(lo, w0 & 0x000F000Fu, w1 & 0x000F000Fu, v0 & 0x000F000Fu, v1 & 0x000F000Fu, b.x, b.y,
+             lo);
+    mma16816(hi, w0 & 0x00F000F0u, w1 & 0x00F000F0u, v0 & 0x00F000F0u, v1 & 0x00F000F0u, b.z, b.w,
+             hi);
 }
 
 constexpr float kSub = 16777216.0f;            // 2^24: the codes' subnormal scale
@@ -287,6 +289,13 @@ __host__ __device__ constexpr int col_stride(int K, int G)
     // fp16 values, then the fp32 sums of the groups; an odd multiple of 64 so
     // that neighbouring columns' chunks fall in distinct banks
     return (2 * K + 4 * G + 127) / 128 * 128 + 64;
+}
+
+// The rest of a wait that its first try did not end, out of the hot loop.
+__device__ __noinline__ void wait_long(uint32_t bar, uint32_t phase, volatile int *abort_flag,
+                                       int32_t *status, uint64_t limit_ns)
+{
+    mbar_wait_warp_a(bar, phase, abort_flag, status, kDevPipelineTimeout, limit_ns);
 }
 
 // NW warps, each with a ring of DEPTH units.
@@ -513,13 +522,11 @@ struct Layer {
                 u += end - unit;
                 int groups = G - first_group;              // left in the task
                 for (; unit < end; unit++) {
-                    mbar_wait_warp(ring.full + ring.stage, ring.phase, &mem.abort_flag,
-                                   p.dev_status, kDevPipelineTimeout, p.wait_ns);
+                    const uint32_t bar = smem_u32(ring.full + ring.stage);
+                    if (!__all_sync(0xffffffffu, mbar_try_wait_a(bar, ring.phase)))
+                        wait_long(bar, ring.phase, &mem.abort_flag, p.dev_status, p.wait_ns);
                     const uint8_t *st = ring.buf + ring.stage * kUnitBytes;
-#pragma unroll
-                    for (int j = 0; j < T::kUnitGroups; j++) {
-                        if (j >= groups)
-                            break;
+                    auto group = [&](int j) {
                         uint32_t q0[T::kWords], q1[T::kWords];
                         if constexpr (UP) {
                             const uint8_t *c = st + (code0 ^ (64 * j));
@@ -545,6 +552,17 @@ struct Layer {
                         acc[1] = fmaf(s0, fmaf(z0, a1, fmaf(hi[1], 0.0625f, lo[1])), acc[1]);
                         acc[2] = fmaf(s1, fmaf(z1, a0, fmaf(hi[2], 0.0625f, lo[2])), acc[2]);
                         acc[3] = fmaf(s1, fmaf(z1, a1, fmaf(hi[3], 0.0625f, lo[3])), acc[3]);
+                    };
+                    // whole units without a branch between their groups, so that
+                    // the groups' loads and MMAs overlap
+                    if (groups >= T::kUnitGroups) {
+#pragma unroll
+                        for (int j = 0; j < T::kUnitGroups; j++)
+                            group(j);
+                    } else {
+#pragma unroll 1
+                        for (int j = 0; j < groups; j++)
+                            group(j);
                     }
                     groups -= T::kUnitGroups;
                     xc += 512;
