@@ -74,7 +74,8 @@ struct Shared {
     int16_t expert[kMaxA];
     int16_t count[kMaxA];
     int16_t a[kMaxA][kCols];
-    int16_t col0[kMaxA];               // of a pass: each job's first column
+    int16_t col0[kMaxA];               // of a pass: each job's first column,
+    int16_t col_a[kMaxA];              // each column's assignment
     int16_t base[kMaxE];               // an expert's first job
     alignas(16) int ids[kMaxA];
 };
@@ -334,11 +335,16 @@ struct Layer {
             const uint16_t *sc = UP ? p.gu_s : p.dn_s, *zp = UP ? p.gu_z : p.dn_z;
             const int64_t r0 = UP ? static_cast<int64_t>(e) * 2 * p.m + tile * 8
                                   : static_cast<int64_t>(e) * p.d + tile * 16;
-            const int64_t r1 = UP ? r0 + p.m : r0 + 8;
-            bulk_load_nohint(scales, sc + r0 * G, 16 * G, bar);
-            bulk_load_nohint(scales + 16 * G, sc + r1 * G, 16 * G, bar);
-            bulk_load_nohint(scales + 32 * G, zp + r0 * G, 16 * G, bar);
-            bulk_load_nohint(scales + 48 * G, zp + r1 * G, 16 * G, bar);
+            const int64_t r1 = r0 + p.m;
+            if constexpr (UP) {
+                bulk_load_nohint(scales, sc + r0 * G, 16 * G, bar);
+                bulk_load_nohint(scales + 16 * G, sc + r1 * G, 16 * G, bar);
+                bulk_load_nohint(scales + 32 * G, zp + r0 * G, 16 * G, bar);
+                bulk_load_nohint(scales + 48 * G, zp + r1 * G, 16 * G, bar);
+            } else {                       // rows r0 .. r0 + 15 are one block
+                bulk_load_nohint(scales, sc + r0 * G, 32 * G, bar);
+                bulk_load_nohint(scales + 32 * G, zp + r0 * G, 32 * G, bar);
+            }
         }
     }
 
@@ -368,71 +374,85 @@ struct Layer {
         }
     }
 
-    // Activations of the jobs [job0, job1): fp16 in the MMA's order and the
-    // groups' sums, times -2^-24.  A warp takes one column's 128 elements at a
-    // time.
-    template <bool UP>
-    static __device__ __forceinline__ void stage_columns(const FewArgs &p, Shared &s, uint8_t *xbuf,
-                                                         int job0, int job1, int warp, int lane)
-    {
+    // The activations of a pass's columns, fp16 in the MMA's order, and their
+    // groups' sums times -2^-24.  A warp takes one column's 128 elements at a
+    // time, kBatch of them per call: load reads them, put stores them.
+    template <bool UP> struct Columns {
         using T = Step<UP>;
-        const int K = UP ? p.d : p.m, stride = col_stride(K, K / T::kGroup);
-        const int blocks = (K + 127) / 128;
-        constexpr int kBatch = 4;              // loads in flight at a time
-        bool range = false;
-        for (int job = job0; job < job1; job++) {
-            const int items = s.count[job] * blocks;
-            for (int c0 = warp; c0 < items; c0 += NW * kBatch) {
-                uint2 v[kBatch];
+        static constexpr int kBatch = 4;
+        const FewArgs &p;
+        const Shared &s;
+        uint8_t *xbuf;
+        int items, blocks, warp, lane;
+        uint2 v[kBatch];
+
+        __device__ __forceinline__ Columns(const FewArgs &p_, const Shared &s_, uint8_t *xbuf_,
+                                           int cols, int warp_, int lane_)
+            : p(p_), s(s_), xbuf(xbuf_), warp(warp_), lane(lane_)
+        {
+            blocks = ((UP ? p.d : p.m) + 127) / 128;
+            items = cols * blocks;
+        }
+        __device__ __forceinline__ bool more(int batch) const
+        {
+            return warp + batch * kBatch * NW < items;
+        }
+        __device__ __forceinline__ void load(int batch)
+        {
+            const int K = UP ? p.d : p.m;
 #pragma unroll
-                for (int u = 0; u < kBatch; u++) {
-                    const int c = c0 + u * NW, col = c / blocks;
-                    const int el = (c - col * blocks) * 128 + lane * 4;
-                    v[u] = make_uint2(0, 0);
-                    if (c < items && el < K) {
-                        const int a = s.a[job][col];
-                        const uint16_t *src = UP ? p.x + static_cast<int64_t>(a / p.k) * p.d
-                                                 : p.h + static_cast<int64_t>(a) * p.m;
-                        v[u] = __ldcg(reinterpret_cast<const uint2 *>(src + el));
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < kBatch; u++) {
-                    const int c = c0 + u * NW, col = c / blocks;
-                    const int el = (c - col * blocks) * 128 + lane * 4;
-                    const bool in = c < items && el < K;
-                    uint8_t *xc = xbuf + (s.col0[job] + col) * stride;
-                    const int gi = el / T::kGroup, i8 = (el % T::kGroup) / 8;   // word in the group
-                    uint16_t *dst = reinterpret_cast<uint16_t *>(
-                        xc + gi * T::kGroup * 2 + (i8 % T::kWords) * 64 + (i8 / T::kWords) * 16);
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const uint32_t bits = i < 2 ? v[u].x : v[u].y;
-                        uint16_t hb = static_cast<uint16_t>(i & 1 ? bits >> 16 : bits);
-                        if constexpr (UP) {
-                            const float f = __uint_as_float(static_cast<uint32_t>(hb) << 16);
-                            range |= !(fabsf(f) <= 65504.0f);
-                            hb = to_half_sat(f);
-                        }
-                        sum += __half2float(__ushort_as_half(hb));
-                        if (in)
-                            dst[perm8((lane & 1) * 4 + i)] = hb;
-                    }
-#pragma unroll
-                    for (int o = T::kGroup / 8; o > 0; o >>= 1)
-                        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    if (in && (lane & (T::kGroup / 4 - 1)) == 0)
-                        reinterpret_cast<float *>(xc + 2 * K)[gi] = -sum / kSub;
+            for (int u = 0; u < kBatch; u++) {
+                const int c = warp + (batch * kBatch + u) * NW, col = c / blocks;
+                const int el = (c - col * blocks) * 128 + lane * 4;
+                v[u] = make_uint2(0, 0);
+                if (c < items && el < K) {
+                    const int64_t a = s.col_a[col];
+                    v[u] = __ldcg(reinterpret_cast<const uint2 *>(
+                        (UP ? p.x + a / p.k * p.d : p.h + a * p.m) + el));
                 }
             }
         }
-        if (range && p.dev_status)
-            atomicOr(p.dev_status, kDevFp16Range);
-    }
+        __device__ __forceinline__ void put(int batch) const
+        {
+            const int K = UP ? p.d : p.m, stride = col_stride(K, K / T::kGroup);
+            bool range = false;
+#pragma unroll
+            for (int u = 0; u < kBatch; u++) {
+                const int c = warp + (batch * kBatch + u) * NW, col = c / blocks;
+                const int el = (c - col * blocks) * 128 + lane * 4;
+                const bool in = c < items && el < K;
+                uint8_t *xc = xbuf + col * stride;
+                const int gi = el / T::kGroup, i8 = (el % T::kGroup) / 8;   // word in the group
+                uint16_t *dst = reinterpret_cast<uint16_t *>(
+                    xc + gi * T::kGroup * 2 + (i8 % T::kWords) * 64 + (i8 / T::kWords) * 16);
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const uint32_t bits = i < 2 ? v[u].x : v[u].y;
+                    uint16_t hb = static_cast<uint16_t>(i & 1 ? bits >> 16 : bits);
+                    if constexpr (UP) {
+                        const float f = __uint_as_float(static_cast<uint32_t>(hb) << 16);
+                        range |= !(fabsf(f) <= 65504.0f);
+                        hb = to_half_sat(f);
+                    }
+                    sum += __half2float(__ushort_as_half(hb));
+                    if (in)
+                        dst[perm8((lane & 1) * 4 + i)] = hb;
+                }
+#pragma unroll
+                for (int o = T::kGroup / 8; o > 0; o >>= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (in && (lane & (T::kGroup / 4 - 1)) == 0)
+                    reinterpret_cast<float *>(xc + 2 * K)[gi] = -sum / kSub;
+            }
+            if (range && p.dev_status)
+                atomicOr(p.dev_status, kDevFp16Range);
+        }
+    };
 
     // The CTA's share of a step.  `between` runs once, after the first
-    // requests are on their way and before the activations are read.
+    // requests are on their way; down's activations are read after it, gate_up's
+    // first ones before the requests.
     template <bool UP, class F>
     static __device__ __forceinline__ void run(const FewArgs &p, Shared &s, Mem &mem, Ring &ring,
                                                uint8_t *scales, uint8_t *xbuf, F between)
@@ -442,7 +462,9 @@ struct Layer {
         const int K = UP ? p.d : p.m, G = K / T::kGroup, stride = col_stride(K, G);
         const int per_task = units_of(K), nbuf = scale_bufs(DEPTH, K);
         const int per_job = UP ? p.m / 8 : p.d / 16;
-        const int64_t total = static_cast<int64_t>(s.n) * per_job;
+        // at most 256 jobs of 512 tasks of 32 units: 32 bits hold their products
+        // with the grid and with the warps
+        const uint32_t total = static_cast<uint32_t>(s.n) * per_job;
         const int t0 = static_cast<int>(total * blockIdx.x / gridDim.x);
         const int t1 = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
         const int t4 = lane & 3, g = lane >> 2;
@@ -460,14 +482,18 @@ struct Layer {
             const int job0 = p0 / per_job;
             int job1 = job0, cols = 0;
             while (p0 < t1 && job1 * per_job < t1 && cols + s.count[job1] <= p.cols) {
+                const int n = s.count[job1];
                 if (threadIdx.x == 0)
                     s.col0[job1] = static_cast<int16_t>(cols);
-                cols += s.count[job1++];
+                if (threadIdx.x < n)
+                    s.col_a[cols + threadIdx.x] = s.a[job1][threadIdx.x];
+                cols += n;
+                job1++;
             }
             const int p1 = min(t1, max(p0, job1 * per_job));
-            const int units = (p1 - p0) * per_task;
-            const int u0 = static_cast<int>(static_cast<int64_t>(units) * warp / NW);
-            const int u1 = static_cast<int>(static_cast<int64_t>(units) * (warp + 1) / NW);
+            const uint32_t units = static_cast<uint32_t>(p1 - p0) * per_task;
+            const int u0 = static_cast<int>(units * warp / NW);
+            const int u1 = static_cast<int>(units * (warp + 1) / NW);
 
             int task = p0 + u0 / per_task, unit = u0 % per_task;
             // the next request: job, tile of its rows, unit, scale buffer
@@ -477,7 +503,8 @@ struct Layer {
             auto ask = [&]() {                 // one lane asks; all keep count
                 if (left > 0) {
                     if (lane == 0)
-                        request<UP>(p, re, rt, rb, left == u1 - u0 || rb == 0, ring.buf + ring.ask_stage * kUnitBytes,
+                        request<UP>(p, re, rt, rb, left == u1 - u0 || rb == 0,
+                                    ring.buf + ring.ask_stage * kUnitBytes,
                                     ring.full + ring.ask_stage, scales + rn * 64 * G);
                     left--;
                     ring.ask_stage = ring.ask_stage + 1 == DEPTH ? 0 : ring.ask_stage + 1;
@@ -492,14 +519,28 @@ struct Layer {
                     }
                 }
             };
+            Columns<UP> columns(p, s, xbuf, cols, warp, lane);
+            if constexpr (UP) {
+                __syncthreads();               // col0 and col_a
+                columns.load(0);
+            }
 #pragma unroll 1
             for (int i = 0; i < DEPTH; i++)
                 ask();
             if (first_pass)
                 between();
+            if constexpr (!UP) {
+                if (!first_pass)
+                    __syncthreads();           // `between` has synchronised the CTA
+                columns.load(0);
+            }
             first_pass = false;
-            __syncthreads();                   // col0; the columns are free
-            stage_columns<UP>(p, s, xbuf, job0, job1, warp, lane);
+            columns.put(0);
+#pragma unroll 1
+            for (int b = 1; columns.more(b); b++) {
+                columns.load(b);
+                columns.put(b);
+            }
             if (lane == 0)
                 mem.head_task[warp] = -1;
             __syncthreads();
@@ -716,13 +757,13 @@ cudaError_t launch_variant(FewArgs a, int dev, int sms, cudaStream_t stream)
     return cudaLaunchCooperativeKernel(kern, dim3(sms), dim3(32 * NW), args, smem, stream);
 }
 
-// Sixteen warps with three units each in flight where the scales' rings and a
+// Sixteen warps with two units each in flight where the scales' rings and a
 // job's columns leave room for it, else eight warps.
 bool wide_fits(int d, int m)
 {
     int sb, cols;
     size_t smem;
-    return plan<16, 3>(d, m, &sb, &cols, &smem);
+    return plan<16, 2>(d, m, &sb, &cols, &smem);
 }
 
 using EncodeFn = decltype(&cuTensorMapEncodeTiled);
@@ -806,7 +847,7 @@ cudaError_t launch_few(const FewProblem &q, cudaStream_t stream)
     if (!encode_rows(&a.gu_map, q.gu_q, q.d / 2, q.m, 2 * q.E, 8, 2) ||
         !encode_rows(&a.dn_map, q.dn_q, q.m / 2, q.d, q.E, 16, 1))
         return cudaErrorInvalidValue;
-    return wide_fits(q.d, q.m) ? launch_variant<16, 3>(a, dev, sms, stream)
+    return wide_fits(q.d, q.m) ? launch_variant<16, 2>(a, dev, sms, stream)
                                : launch_variant<8, 3>(a, dev, sms, stream);
 }
 
