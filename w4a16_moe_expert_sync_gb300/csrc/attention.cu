@@ -21,10 +21,10 @@
 // a thousand short ones.  The split follows from the lengths, which live on
 // the device: every CTA works it out for itself (a scan over the entries).
 //
-// Roles of a CTA's eleven warps: warps 0-3 and 4-7 are the softmax of streams
+// Roles of a CTA's twelve warps: warps 0-3 and 4-7 are the softmax of streams
 // 0 and 1 (a thread per row), warp 8 loads K and V by TMA into a ring of
 // slots, warps 9 and 10 issue the MMAs (of both streams of a pair; of streams 0
-// and 1).  While one stream's softmax runs the tensor cores work for the other.
+// and 1), warp 11 only completes its group of four.  While one stream's softmax runs the tensor cores work for the other.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -41,7 +41,10 @@ namespace {
 
 constexpr int kRows = 128;                 // rows of a stream's tile
 constexpr int kKeys = 128;                 // keys of a tile
-constexpr int kThreads = 32 * 11;
+constexpr int kThreads = 32 * 12;
+// Registers a thread: 168 at launch; the loading warps give some of theirs to
+// the softmax warps, which hold a row of 128 scores (2 x 216 + 72 = 3 x 168).
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 
 // A group's prefix (first G) or a sequence's own keys.
 struct Entry {
@@ -1099,12 +1102,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp < 8)
+    __syncwarp();
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         K::softmax(p, s, qbuf, ring, warp >> 2);
-    else if (warp == 8)
-        K::loader(p, s, ring, lane);
-    else
-        K::issuer(p, s, qbuf, ring, warp - 9);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 8)
+            K::loader(p, s, ring, lane);
+        else if (warp < 11)
+            K::issuer(p, s, qbuf, ring, warp - 9);
+    }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
