@@ -823,21 +823,26 @@ struct Kernel {
                                  : p.segs[s.seg0[stream] + i - s.segs[2]];
         };
         auto pieces = [&] { return s.segs[2] + s.segs[stream]; };
-        // A piece's queries on their way to shared memory, and how many keys this
-        // thread's row sees.  Called when no MMA reads the queries any more.
-        // The lanes part ways in it, and the tensor-memory instructions that
-        // follow need them together again.
-        auto prepare = [&](int i) {
+        // A piece's queries on their way to shared memory.  Called when no MMA
+        // reads the queries any more.
+        auto fetch = [&](int i) {
             const Seg &g = piece(i);
-            const int row0 = g.row0 + (i < s.segs[2] ? stream * kRows : 0);
-            const int rows = rows_here(g, i < s.segs[2], stream);
             if (g.tiles > 0)
-                load_q(p, q, g, row0, rows, tid);
-            int sees = INT_MAX;                // no row: nothing to mask, nothing kept
-            if (tid < rows)
-                sees = min(limit_of(p, g, g.tok0 + (row0 + tid) / p.rep), g.k1);
+                load_q(p, q, g, g.row0 + (i < s.segs[2] ? stream * kRows : 0),
+                       rows_here(g, i < s.segs[2], stream), tid);
+        };
+        // How many keys this thread's row of a piece sees.  The lanes part ways in
+        // it, and the tensor-memory instructions that follow need them together
+        // again.
+        auto sees = [&](int i) {
+            const Seg &g = piece(i);
+            int n = INT_MAX;                   // no row: nothing to mask, nothing kept
+            if (tid < rows_here(g, i < s.segs[2], stream)) {
+                const int row = g.row0 + (i < s.segs[2] ? stream * kRows : 0) + tid;
+                n = min(limit_of(p, g, g.tok0 + row / p.rep), g.k1);
+            }
             __syncwarp();
-            return sees;
+            return n;
         };
         auto hand_over = [&](int i) {          // the queries to the issuer
             if (piece(i).tiles == 0)
@@ -848,48 +853,53 @@ struct Kernel {
         };
         int limit = 0, next = 0;
         if (pieces() > 0) {
-            limit = prepare(0);
+            fetch(0);
             hand_over(0);
+            limit = sees(0);
         }
-        for (int i = 0, r = 0; i < pieces(); i++, limit = next) {
-            if (i == s.segs[2])
+        const int pairs = s.segs[2], count = pieces();
+        for (int i = 0, r = 0; i < count; i++, limit = next) {
+            const bool pair = i < pairs, another = i + 1 < count;
+            if (i == pairs)
                 r = 0;
-            const bool busy = rows_here(piece(i), i < s.segs[2], stream) > (tid & ~31);
+            const Seg g = piece(i);
+            const int rows = rows_here(g, pair, stream);
+            const bool busy = rows > (tid & ~31);
             float m = -INFINITY, l = 0.0f;     // m in units of log2
-            int base = piece(i).kbase + piece(i).tile0 * kKeys;
-            int left = piece(i).tiles;
-            for (bool first = true; left > 0; left--, r++, base += kKeys, first = false) {
+            int base = g.kbase + g.tile0 * kKeys;
+            for (int t = 0; t < g.tiles; t++, r++, base += kKeys) {
                 wait(p, s, &s.s_full[stream], s_phase);
                 s_phase ^= 1;
                 tc_fence_after();
-                if (left == 1 && i + 1 < pieces())
-                    next = prepare(i + 1);
+                if (t == g.tiles - 1 && another) {
+                    fetch(i + 1);
+                    next = sees(i + 1);
+                }
                 // a warp without rows leaves P as it is: a row's P only meets its own O
                 __syncwarp();
                 if (busy)
-                    tile(p, ts, to, limit == INT_MAX ? 0 : piece(i).k0 - base,
-                         limit == INT_MAX ? kKeys : limit - base, !first, m, l);
-                const int valid = piece(i).k1 - base;
-                if (valid < kKeys && (valid & 15))
-                    clear_tail(p, s, ring, 2 * fill_of(s, i < s.segs[2] ? 2 : stream, r) + 1, valid,
-                               i < s.segs[2], stream, tid);
+                    tile(p, ts, to, limit == INT_MAX ? 0 : g.k0 - base,
+                         limit == INT_MAX ? kKeys : limit - base, t > 0, m, l);
+                if (g.k1 - base < kKeys && (g.k1 & 15))
+                    clear_tail(p, s, ring, 2 * fill_of(s, pair ? 2 : stream, r) + 1, g.k1 - base,
+                               pair, stream, tid);
                 tc_fence_before();
                 mbar_arrive(&s.p_ready[stream]);
             }
-            if (i + 1 < pieces()) {
-                if (piece(i).tiles == 0)
-                    next = prepare(i + 1);
+            if (another) {
+                if (g.tiles == 0) {
+                    fetch(i + 1);
+                    next = sees(i + 1);
+                }
                 // the next piece's first S may be made while this one's sums are stored
                 hand_over(i + 1);
             }
-            if (piece(i).tiles > 0) {
+            if (g.tiles > 0) {
                 wait(p, s, &s.o_full[stream], o_phase);
                 o_phase ^= 1;
                 tc_fence_after();
             }
-            const bool pair = i < s.segs[2];
-            store(p, piece(i), pair, pair ? stream * kRows : 0, rows_here(piece(i), pair, stream), to,
-                  m, l, tid);
+            store(p, g, pair, pair ? stream * kRows : 0, rows, to, m, l, tid);
         }
     }
 
@@ -926,15 +936,19 @@ struct Kernel {
     {
         int b = g.seq;
         if (b < 0) {                           // the sequence of a group that has the token
-            int lo = g.row_of_table, hi = p.B - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (p.q_offsets[mid] <= tok)
-                    lo = mid;
-                else
-                    hi = mid - 1;
+            // where every sequence has max_q tokens it can be told at once
+            b = min(g.row_of_table + (tok - g.tok0) / p.max_q, p.B - 1);
+            if (p.q_offsets[b] > tok || p.q_offsets[b + 1] <= tok) {
+                int lo = g.row_of_table, hi = p.B - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (p.q_offsets[mid] <= tok)
+                        lo = mid;
+                    else
+                        hi = mid - 1;
+                }
+                b = lo;
             }
-            b = lo;
         }
         const int len = min(max(p.lens[b], 0), p.W * p.page);
         return p.causal ? len - (p.q_offsets[b + 1] - tok) + 1 : len;
