@@ -692,7 +692,7 @@ int w4_kv_append(uint16_t *k_pages, uint16_t *v_pages, int64_t page_stride, int6
  * values' type for the product with V; partial sums are fp32, joined in a
  * fixed order: bit-identical reruns on one GPU model.  Two launches.
  * Requires D = 64 or 128, page_size 16, 32, 64 or 128, Hkv dividing Hq,
- * max_q >= 1, scale > 0, B + G <= 4096, pointers 16-byte aligned, strides
+ * max_q >= 1, scale > 0, B + G <= 4000, pointers 16-byte aligned, strides
  * multiples of 8 elements, T * Hq * D and the tiles below 2^31.
  * ------------------------------------------------------------------------ */
 size_t w4_attn_shared_prefix_workspace_size(int T, int B, int G, int max_q, int Hq, int Hkv,

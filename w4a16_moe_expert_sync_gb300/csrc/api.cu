@@ -1082,8 +1082,8 @@ int w4_attn_shared_prefix(const uint16_t *q, int64_t q_tok_stride, int64_t q_hea
                     page_size);
     if (Hq % Hkv)
         return fail(W4_ERR_UNSUPPORTED_SHAPE, "Hkv must divide Hq (%d, %d)", Hkv, Hq);
-    if (static_cast<int64_t>(B) + G > 4096)
-        return fail(W4_ERR_UNSUPPORTED_SHAPE, "need B + G <= 4096 (got %d + %d)", B, G);
+    if (static_cast<int64_t>(B) + G > 4000)
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "need B + G <= 4000 (got %d + %d)", B, G);
     const int64_t rows = static_cast<int64_t>(T) * Hq;
     const int64_t keys = static_cast<int64_t>(W) * page_size;
     const int64_t items = 2 * (rows / 128 + 1) + (static_cast<int64_t>(B) + G) * Hkv;

@@ -89,7 +89,7 @@ struct AttnArgs {
     int64_t q_tok, q_head;
     float scale_log2;
     uint64_t wait_ns;
-    int T, B, G, W, P, page, Hq, Hkv, rep, max_q, causal;
+    int T, B, G, W, P, page, page_shift, Hq, Hkv, rep, max_q, causal;
     int rows_b;                            // a sequence's single item's rows at most
     int cap_a, cap_g, cap_b;               // pieces that the workspace holds; cap_b: all single
 };
@@ -101,6 +101,8 @@ constexpr int kItemCost = 2;
 // Worker w's share of a region's `all` begins here.
 __device__ __forceinline__ int worker_begin(int all, int workers, int w)
 {
+    if (all < (1 << 22))                       // workers <= 512: 32 bits do
+        return static_cast<int>(static_cast<uint32_t>(all) * w / workers);
     return static_cast<int>(static_cast<int64_t>(all) * w / workers);
 }
 // The worker whose share place x is in.
@@ -238,27 +240,11 @@ struct Index {
     const int *lens, *q_offsets, *group_offsets, *shared;
 };
 
-// Whether the offsets ascend within their bounds; nothing is done if not, so
-// what follows may rely on it.  Called by the whole CTA.
-__device__ __forceinline__ bool offsets_ascend(const AttnArgs &p, const Index &x)
-{
-    bool bad = false;
-    for (int i = threadIdx.x; i < p.B; i += blockDim.x) {
-        const int a = x.q_offsets[i], b = x.q_offsets[i + 1];
-        bad |= a < 0 || b < a || b > p.T;
-    }
-    for (int i = threadIdx.x; i < p.G; i += blockDim.x) {
-        const int a = x.group_offsets[i], b = x.group_offsets[i + 1];
-        bad |= a < 0 || b < a || b > p.B;
-    }
-    return !__syncthreads_or(bad);
-}
-
 // The shared length of group g, never beyond its first sequence.
 __device__ __forceinline__ int shared_of(const AttnArgs &p, const Index &x, int g)
 {
     const int first = x.group_offsets[g];
-    if (first >= p.B)
+    if (first < 0 || first >= p.B)
         return 0;
     return max(0, min(min(x.shared[g], x.lens[first]), p.W * p.page));
 }
@@ -286,53 +272,64 @@ __device__ __forceinline__ int rows_of(const AttnArgs &p, int kind)
     return kind == 0 ? 2 * kRows : kind == 1 ? kRows : p.rows_b;
 }
 
-// What an entry asks for: no tokens where there are more than max_q.
-struct Want {
+// An entry's queries and keys, and its items: span is an item's length in the
+// split (kItemCost + tiles; 0: nothing to do), items of one kv head.
+struct Work {
     int tok0, tokens, k0, k1;
+    int span, row_tiles_pair;              // 2 row_tiles + pair
+    __device__ __forceinline__ int row_tiles() const { return row_tiles_pair >> 1; }
+    __device__ __forceinline__ bool pair() const { return row_tiles_pair & 1; }
 };
 
-__device__ __forceinline__ Want want_of(const AttnArgs &p, const Index &x, int e, bool flag)
+// What entry e asks for.  More than max_q tokens a sequence: nothing.  Offsets
+// that do not ascend within their bounds set bad.
+__device__ __forceinline__ Work work_of(const AttnArgs &p, const Index &x, int e, bool flag,
+                                        bool &bad)
 {
-    Want w{0, 0, 0, 0};
-    bool ok = true;
+    Work w{};
+    int members = 1;
     if (e < p.G) {
         const int b0 = x.group_offsets[e], b1 = x.group_offsets[e + 1];
+        if (b0 < 0 || b1 < b0 || b1 > p.B) {
+            bad = true;
+            return w;
+        }
         w.tok0 = x.q_offsets[b0];
         w.tokens = x.q_offsets[b1] - w.tok0;
-        ok = w.tokens <= static_cast<int64_t>(b1 - b0) * p.max_q;
         w.k1 = b1 > b0 ? shared_of(p, x, e) : 0;
+        members = b1 - b0;
     } else {
         const int b = e - p.G, g = group_of(p, x, b), len = x.lens[b];
-        w.tok0 = x.q_offsets[b];
-        w.tokens = x.q_offsets[b + 1] - w.tok0;
-        ok = w.tokens <= p.max_q;
-        w.k1 = min(max(len, 0), p.W * p.page);
+        const int t0 = x.q_offsets[b], t1 = x.q_offsets[b + 1];
+        if (t0 < 0 || t1 < t0 || t1 > p.T) {
+            bad = true;
+            return w;
+        }
+        w.tok0 = t0;
+        w.tokens = t1 - t0;
+        w.k1 = min(max(len, 0), p.W << p.page_shift);
         w.k0 = g >= 0 ? min(shared_of(p, x, g), w.k1) : 0;
         if (w.k1 != len && flag && p.status)
             atomicOr(p.status, W4_DEV_BAD_SLOT);
     }
-    if (!ok)
+    if (w.tokens > static_cast<int64_t>(members) * p.max_q) {
         w.tokens = 0;
-    if (!ok && flag && p.status)
-        atomicOr(p.status, W4_DEV_BAD_SLOT);
+        if (flag && p.status)
+            atomicOr(p.status, W4_DEV_BAD_SLOT);
+    }
+    const int rows = w.tokens * p.rep;
+    if (rows > 0 && w.k1 > w.k0) {
+        const int base = w.k0 >> p.page_shift << p.page_shift;
+        const bool pair = rows > kRows;
+        w.span = (w.k1 - base + kKeys - 1) / kKeys + kItemCost;
+        w.row_tiles_pair = pair ? 2 * ((rows + 2 * kRows - 1) / (2 * kRows)) + 1 : 2;
+    }
     return w;
 }
 
-__device__ __forceinline__ Entry entry_of(const AttnArgs &p, const Want &w)
-{
-    Entry e{};
-    const int rows = w.tokens * p.rep;
-    if (rows > 0 && w.k1 > w.k0) {
-        const int base = w.k0 / p.page * p.page;
-        e.span = (w.k1 - base + kKeys - 1) / kKeys + kItemCost;
-        e.pair = rows > kRows;
-        e.row_tiles = e.pair ? (rows + 2 * kRows - 1) / (2 * kRows) : 1;
-    }
-    return e;
-}
-
-// Exclusive sums of four counts over the CTA's threads.
-__device__ __forceinline__ int4 scan4(int4 v, int4 *sums, int4 *total)
+// Exclusive sums of four counts over the CTA's threads; whether any thread is
+// bad comes with the same barrier.
+__device__ __forceinline__ int4 scan4(int4 v, int4 *sums, int4 *total, bool *bad)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int4 s = v;
@@ -349,7 +346,7 @@ __device__ __forceinline__ int4 scan4(int4 v, int4 *sums, int4 *total)
     }
     if (lane == 31)
         sums[warp] = s;
-    __syncthreads();
+    *bad = __syncthreads_or(*bad);
     int4 before = make_int4(0, 0, 0, 0), all = before;
     for (int i = 0; i < kThreads / 32; i++) {
         const int4 u = sums[i];
@@ -404,16 +401,20 @@ struct Kernel {
         int abort_flag;
         int requested;                         // fills requested of the ring so far
         int seg0[3], segs[3], tiles[3];        // single items of streams 0 and 1; pairs
+        Seg first[3];                          // the first piece of each
         int4 sums[kThreads / 32];
     };
 
-    // The plan: this CTA's pieces into the workspace.  Scratch is the ring,
-    // before anything is loaded into it.
+    // The plan: this CTA's pieces into the workspace, the first ones also into
+    // shared memory.  Scratch is the queries' room and the ring (192 KB at least,
+    // 48 bytes an entry), before anything is loaded into them.
     static __device__ void plan(const AttnArgs &p, Shared &s, uint8_t *scratch)
     {
         const int n = p.G + p.B, tid = threadIdx.x;
-        int *lens = reinterpret_cast<int *>(scratch), *qo = lens + p.B, *go = qo + p.B + 1;
-        int *sh = go + p.G + 1;
+        Work *work = reinterpret_cast<Work *>(scratch);                // [n]
+        // running counts before each entry: length and items, singles and pairs
+        int *start = reinterpret_cast<int *>(work + n);                // [4][n]
+        int *lens = start + 4 * n, *qo = lens + p.B, *go = qo + p.B + 1, *sh = go + p.G + 1;
         for (int i = tid; i <= p.B; i += kThreads) {
             qo[i] = p.q_offsets[i];
             if (i < p.B)
@@ -426,35 +427,41 @@ struct Kernel {
         }
         __syncthreads();
         const Index x{lens, qo, go, sh};
-        const bool sane = offsets_ascend(p, x);
-        if (!sane && tid == 0 && blockIdx.x == 0 && p.status)
-            atomicOr(p.status, W4_DEV_BAD_SLOT);
-        // running counts before each entry: tiles and items, singles and pairs
-        int *start = sh + p.G;                                  // [4][n]
         const int run = (n + kThreads - 1) / kThreads, e0 = min(n, tid * run);
         const int e1 = min(n, e0 + run);
         int4 sum = make_int4(0, 0, 0, 0);
+        bool bad = false;
         for (int e = e0; e < e1; e++) {
-            const Entry en = sane ? entry_of(p, want_of(p, x, e, blockIdx.x == 0)) : Entry{};
-            const int items = en.row_tiles * p.Hkv;
-            (en.pair ? sum.z : sum.x) += items * en.span;
-            (en.pair ? sum.w : sum.y) += items;
+            const Work w = work_of(p, x, e, blockIdx.x == 0, bad);
+            const int items = w.row_tiles() * p.Hkv;
+            work[e] = w;
+            (w.pair() ? sum.z : sum.x) += items * w.span;
+            (w.pair() ? sum.w : sum.y) += items;
         }
         int4 total;
-        int4 at = scan4(sum, s.sums, &total);
+        int4 at = scan4(sum, s.sums, &total, &bad);
+        if (bad) {                             // nothing is done
+            total = make_int4(0, 0, 0, 0);
+            if (tid == 0 && blockIdx.x == 0 && p.status)
+                atomicOr(p.status, W4_DEV_BAD_SLOT);
+        }
         for (int e = e0; e < e1; e++) {
-            const Entry en = sane ? entry_of(p, want_of(p, x, e, false)) : Entry{};
-            const int items = en.row_tiles * p.Hkv;
+            const Work w = work[e];
+            const int items = w.row_tiles() * p.Hkv;
             start[e] = at.x;
             start[n + e] = at.y;
             start[2 * n + e] = at.z;
             start[3 * n + e] = at.w;
-            (en.pair ? at.z : at.x) += items * en.span;
-            (en.pair ? at.w : at.y) += items;
+            (w.pair() ? at.z : at.x) += items * w.span;
+            (w.pair() ? at.w : at.y) += items;
         }
         __syncthreads();
         auto placed = [&](int e) {
-            Entry en = sane ? entry_of(p, want_of(p, x, e, false)) : Entry{};
+            const Work w = work[e];
+            Entry en{};
+            en.span = w.span;
+            en.row_tiles = w.row_tiles();
+            en.pair = w.pair();
             en.place = start[(en.pair ? 2 * n : 0) + e];
             en.item0 = start[(en.pair ? 3 * n : n) + e];
             return en;
@@ -476,7 +483,7 @@ struct Kernel {
                 hi = worker_begin(all, workers, w + 1);
                 // lane 0 finds the first tile's item, lane 1 the last's
                 const int at = lane == 0 ? lo : hi - 1, e = find_entry(ts, n, at);
-                const int item = is[e] + (at - ts[e]) / entry_of(p, want_of(p, x, e, false)).span;
+                const int item = is[e] + (at - ts[e]) / work[e].span;
                 first = __shfl_sync(0xffffffffu, item, 0);
                 count = __shfl_sync(0xffffffffu, item, 1) - first + 1;
             }
@@ -490,23 +497,22 @@ struct Kernel {
             int mine = 0;
             for (int i = lane; i < count; i += 32) {
                 const int item = first + i, e = find_entry(is, n, item);
-                const Want wa = want_of(p, x, e, false);
-                const Entry en = entry_of(p, wa);
+                const Work wa = work[e];
                 const int local = item - is[e];
-                const int t0 = ts[e] + local * en.span + kItemCost;   // its first tile's place
+                const int t0 = ts[e] + local * wa.span + kItemCost;   // its first tile's place
                 Seg g;
                 g.seq = e < p.G ? -1 : e - p.G;
                 g.row_of_table = e < p.G ? x.group_offsets[e] : e - p.G;
                 g.k0 = wa.k0;
                 g.k1 = wa.k1;
-                g.kbase = wa.k0 / p.page * p.page;
+                g.kbase = wa.k0 >> p.page_shift << p.page_shift;
                 g.tok0 = wa.tok0;
-                g.head = local / en.row_tiles;
+                g.head = pair ? local / wa.row_tiles() : local;
                 const int step = (pair ? 2 : 1) * kRows;
-                g.row0 = (local % en.row_tiles) * step;
+                g.row0 = (local - g.head * wa.row_tiles()) * step;
                 g.rows = min(step, wa.tokens * p.rep - g.row0);
                 g.tile0 = max(lo - t0, 0);
-                int end = min(hi - t0, en.span - kItemCost);
+                int end = min(hi - t0, wa.span - kItemCost);
                 if (p.causal && g.seq >= 0) {
                     // no row of this item sees beyond its last token's position
                     const int last = (g.row0 + g.rows - 1) / p.rep;
@@ -516,6 +522,8 @@ struct Kernel {
                 g.tiles = max(end - g.tile0, 0);
                 g.piece = item + w;
                 segs[g.piece] = g;
+                if (i == 0)
+                    s.first[which] = g;
                 mine += g.tiles;
             }
             mine = __reduce_add_sync(0xffffffffu, mine);
@@ -530,15 +538,16 @@ struct Kernel {
                  b += (kThreads - 96) * gridDim.x) {
                 Joint j{};
                 j.tok0 = qo[b];
-                j.tokens = sane && qo[b + 1] - qo[b] <= p.max_q ? qo[b + 1] - qo[b] : -1;
+                j.tokens = !bad && qo[b + 1] - qo[b] <= p.max_q ? qo[b + 1] - qo[b] : -1;
                 j.all[0] = total.x;
                 j.all[1] = total.z;
-                const int g = sane ? group_of(p, x, b) : -1;
+                const int g = bad ? -1 : group_of(p, x, b);
                 if (g >= 0) {
                     j.e[0] = placed(g);
                     j.e[0].row = (qo[b] - qo[go[g]]) * p.rep;
                 }
-                j.e[1] = placed(p.G + b);
+                if (!bad)
+                    j.e[1] = placed(p.G + b);
                 p.joints[b] = j;
             }
         }
@@ -629,7 +638,7 @@ struct Kernel {
 
     // The pieces of a worker in turn, tile by tile.
     struct Walk {
-        const Seg *next;
+        const Seg *next, *first;
         int left, t, end;                      // pieces behind this one; tile, its end
         Seg g;
         __device__ __forceinline__ bool more()
@@ -637,7 +646,9 @@ struct Kernel {
             while (t >= end) {
                 if (left == 0)
                     return false;
-                g = *next++;
+                g = first ? *first : *next;
+                first = nullptr;
+                next++;
                 left--;
                 t = g.tile0;
                 end = g.tile0 + g.tiles;
@@ -651,6 +662,7 @@ struct Kernel {
         Walk w;
         w.next = p.segs + (which == 2 ? p.cap_b : 0) + s.seg0[which];
         w.left = s.segs[which];
+        w.first = &s.first[which];
         w.t = w.end = 0;
         return w;
     }
@@ -753,8 +765,8 @@ struct Kernel {
         if (stream == 0) {
             const Seg *segs = p.segs + p.cap_b + s.seg0[2];
             for (int i = 0, r = 0; i < s.segs[2]; i++) {
-                const int tiles = segs[i].tiles, tile0 = segs[i].tile0;
-                const int keys = segs[i].k1 - segs[i].kbase;
+                const Seg &g = i == 0 ? s.first[2] : segs[i];
+                const int tiles = g.tiles, tile0 = g.tile0, keys = g.k1 - g.kbase;
                 if (tiles == 0)
                     continue;
                 for (int st = 0; st < 2; st++) {
@@ -784,8 +796,8 @@ struct Kernel {
         }
         const Seg *segs = p.segs + s.seg0[stream];
         for (int i = 0, r = 0; i < s.segs[stream]; i++) {
-            const int tiles = segs[i].tiles, tile0 = segs[i].tile0;
-            const int keys = segs[i].k1 - segs[i].kbase;
+            const Seg &g = i == 0 ? s.first[stream] : segs[i];
+            const int tiles = g.tiles, tile0 = g.tile0, keys = g.k1 - g.kbase;
             if (tiles == 0)
                 continue;
             wait(p, s, &s.q_ready[stream], seg_phase);
@@ -819,8 +831,9 @@ struct Kernel {
         uint32_t s_phase = 0, o_phase = 0;
         // the pairs' pieces, then this stream's own
         auto piece = [&](int i) -> const Seg & {
-            return i < s.segs[2] ? p.segs[p.cap_b + s.seg0[2] + i]
-                                 : p.segs[s.seg0[stream] + i - s.segs[2]];
+            const int which = i < s.segs[2] ? 2 : stream, at = which == 2 ? i : i - s.segs[2];
+            return at == 0 ? s.first[which]
+                           : p.segs[(which == 2 ? p.cap_b : 0) + s.seg0[which] + at];
         };
         auto pieces = [&] { return s.segs[2] + s.segs[stream]; };
         // A piece's queries on their way to shared memory.  Called when no MMA
@@ -918,15 +931,24 @@ struct Kernel {
         const int c = tid % kChunks;
         const uint16_t *src = p.q + g.tok0 * p.q_tok +
                               static_cast<int64_t>(g.head) * p.rep * p.q_head + c * 8;
-        for (int row = tid / kChunks; row < kRows; row += kStep) {
+        int row = tid / kChunks;
+        int64_t tok = (row0 + row) / p.rep;
+        int h = row0 + row - static_cast<int>(tok) * p.rep;
+        const int tok_step = kStep / p.rep, h_step = kStep - tok_step * p.rep;
+#pragma unroll 4
+        for (; row < kRows; row += kStep) {
             uint8_t *dst = q + (c / 8) * (kRows * 128) + row * 128 + ((c % 8) ^ (row & 7)) * 16;
-            if (row < rows) {
-                const int at = row0 + row, tok = at / p.rep;
+            if (row < rows)
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
-                             "l"(src + tok * p.q_tok + (at - tok * p.rep) * p.q_head)
+                             "l"(src + tok * p.q_tok + h * p.q_head)
                              : "memory");
-            } else {
+            else
                 *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
+            tok += tok_step;
+            h += h_step;
+            if (h >= p.rep) {
+                h -= p.rep;
+                tok++;
             }
         }
     }
@@ -1111,8 +1133,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
     pdl_wait();
     pdl_trigger();
-    K::plan(p, s, ring);
-    fence_proxy_async_smem();              // the plan's scratch becomes the ring
+    K::plan(p, s, qbuf);
+    fence_proxy_async_smem();              // the plan's scratch becomes queries and ring
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1412,6 +1434,7 @@ cudaError_t launch_attn(const AttnProblem &q, cudaStream_t stream)
     a.W = q.W;
     a.P = q.P;
     a.page = q.page;
+    a.page_shift = q.page == 16 ? 4 : q.page == 32 ? 5 : q.page == 64 ? 6 : 7;
     a.Hq = q.Hq;
     a.Hkv = q.Hkv;
     a.rep = q.Hq / q.Hkv;
