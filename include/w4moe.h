@@ -683,7 +683,9 @@ int w4_kv_append(uint16_t *k_pages, uint16_t *v_pages, int64_t page_stride, int6
  *   workspace  w4_attn_shared_prefix_workspace_size(...) bytes, 256-byte
  *              aligned; contents need no initialisation
  *   dtype      0: bf16, 1: fp16 (q, the cache and out)
- * Cached values past a sequence's length are never used, whatever they are.
+ * Cached values past a sequence's length are never used, whatever they are, nor
+ * are a later member's own copies of its group's shared tokens.  A value v of a
+ * token that is not finite may also reach its sequence's queries before it.
  * Inputs on the device that make no sense (lengths below 0 or beyond W pages,
  * more than max_q queries: W4_DEV_BAD_SLOT; a page id outside [0, P):
  * W4_DEV_BAD_PAGE) are flagged; the queries concerned get unspecified values.

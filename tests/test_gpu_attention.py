@@ -175,6 +175,27 @@ def test_large_scores_and_a_late_maximum(lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shared", [45, 250, 271, 17])
+@pytest.mark.parametrize("nq", [1, 40])
+def test_a_prefix_is_read_through_the_first_alone(lib, shared, nq):
+    """The others' own pages may hold anything before the shared length, and
+    their tables nothing where a page lies wholly before it."""
+    import torch
+    page = 32
+    c = _build([shared + 60, shared + nq, shared + 130], [nq, nq, nq], [3], [shared], 8, 2, 64,
+               page, "bfloat16", seed=shared)
+    want = _run(lib, c, True)
+    _check(want, c, True)
+    full, part = divmod(shared, page)
+    for b in (1, 2):
+        c["table"][b, :full] = -1
+        if part:
+            c["cache"][:, c["table"][b, full].long(), :part] = float("nan")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert torch.equal(_run(lib, c, True, dev_status=st), want) and int(st) == 0
+
+
+@pytest.mark.gpu
 def test_sharing_changes_nothing_but_rounding(lib):
     import torch
     c = _build([1500] * 6, [1] * 6, [6], [1300], 8, 2, 128, 16, "bfloat16", seed=3)

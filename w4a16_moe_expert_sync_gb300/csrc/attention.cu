@@ -726,11 +726,11 @@ struct Kernel {
             tc_commit_elect(&s.empty[slot]);
     }
 
-    // O (+)= P V of a stream's tile, 16 keys at a time; what lies 16 or more
-    // past the entry's end stays out.
+    // O (+)= P V of a stream's tile, 16 keys at a time; steps that lie wholly
+    // before the entry's first key or past its last stay out.
     static __device__ __forceinline__ void issue_pv(const AttnArgs &p, Shared &s, uint8_t *ring,
-                                                    int stream, int fill, int keys, bool first,
-                                                    bool last, bool last_use)
+                                                    int stream, int fill, int before, int keys,
+                                                    bool first, bool last, bool last_use)
     {
         const int slot = fill % kSlots;
         wait_full(p, s, fill);
@@ -738,10 +738,10 @@ struct Kernel {
         __syncwarp();
         const uint32_t va = smem_u32(ring + slot * kTileBytes);
         const uint32_t ts = s.tmem + kS + 128 * stream, to = s.tmem + kO + D * stream;
-        const int steps = (min(keys, kKeys) + 15) / 16;
-        for (int k = 0; k < steps; k++)
+        const int begin = max(before, 0) / 16, end = (min(keys, kKeys) + 15) / 16;
+        for (int k = begin; k < end; k++)
             tc_mma_ts_elect(to, ts + 8 * k, sdesc_mn_sw128(va + k * 2048, kKeys * 128), kPv,
-                            !first || k > 0);
+                            !first || k > begin);
         if (last_use)
             tc_commit_elect(&s.empty[slot]);
         if (last)
@@ -766,7 +766,7 @@ struct Kernel {
             const Seg *segs = p.segs + p.cap_b + s.seg0[2];
             for (int i = 0, r = 0; i < s.segs[2]; i++) {
                 const Seg &g = i == 0 ? s.first[2] : segs[i];
-                const int tiles = g.tiles, tile0 = g.tile0, keys = g.k1 - g.kbase;
+                const int tiles = g.tiles, base = g.kbase + g.tile0 * kKeys;
                 if (tiles == 0)
                     continue;
                 for (int st = 0; st < 2; st++) {
@@ -777,7 +777,8 @@ struct Kernel {
                 for (int t = 0; t < tiles; t++, r++) {
                     for (int st = 0; st < 2; st++) {
                         wait(p, s, &s.p_ready[st], tile_phase);
-                        issue_pv(p, s, ring, st, 2 * r + 1, keys - (tile0 + t) * kKeys, t == 0,
+                        const int at = base + t * kKeys;
+                        issue_pv(p, s, ring, st, 2 * r + 1, g.k0 - at, g.k1 - at, t == 0,
                                  t == tiles - 1, st == 1);
                         if (t + 1 < tiles)
                             issue_qk(p, s, qbuf, ring, st, 2 * r + 2, st == 1);
@@ -797,7 +798,7 @@ struct Kernel {
         const Seg *segs = p.segs + s.seg0[stream];
         for (int i = 0, r = 0; i < s.segs[stream]; i++) {
             const Seg &g = i == 0 ? s.first[stream] : segs[i];
-            const int tiles = g.tiles, tile0 = g.tile0, keys = g.k1 - g.kbase;
+            const int tiles = g.tiles, base = g.kbase + g.tile0 * kKeys;
             if (tiles == 0)
                 continue;
             wait(p, s, &s.q_ready[stream], seg_phase);
@@ -807,7 +808,8 @@ struct Kernel {
                 issue_qk(p, s, qbuf, ring, stream, fill, true);
                 wait(p, s, &s.p_ready[stream], tile_phase);
                 tile_phase ^= 1;
-                issue_pv(p, s, ring, stream, fill + 1, keys - (tile0 + t) * kKeys, t == 0,
+                const int at = base + t * kKeys;
+                issue_pv(p, s, ring, stream, fill + 1, g.k0 - at, g.k1 - at, t == 0,
                          t == tiles - 1, true);
             }
         }
@@ -893,9 +895,9 @@ struct Kernel {
                 if (busy)
                     tile(p, ts, to, limit == INT_MAX ? 0 : g.k0 - base,
                          limit == INT_MAX ? kKeys : limit - base, t > 0, m, l);
-                if (g.k1 - base < kKeys && (g.k1 & 15))
-                    clear_tail(p, s, ring, 2 * fill_of(s, pair ? 2 : stream, r) + 1, g.k1 - base,
-                               pair, stream, tid);
+                if ((g.k1 - base < kKeys && (g.k1 & 15)) || (g.k0 > base && (g.k0 & 15)))
+                    clear_ends(p, s, ring, 2 * fill_of(s, pair ? 2 : stream, r) + 1, g.k0 - base,
+                               g.k1 - base, pair, stream, tid);
                 tc_fence_before();
                 mbar_arrive(&s.p_ready[stream]);
             }
@@ -1043,22 +1045,28 @@ struct Kernel {
         tmem_wait_st();
     }
 
-    // Values past the last key, up to the 16-key step that it ends in: P is
-    // zero there, but memory nobody has written may hold NaN.  In a pair both
-    // streams clear, and wait for each other, before either uses the tile.
-    static __device__ void clear_tail(const AttnArgs &p, Shared &s, uint8_t *ring, int fill,
-                                      int valid, bool pair, int stream, int tid)
+    // Values before the first key and past the last, in the 16-key steps that
+    // these lie in: P is zero there, but memory nobody has written may hold NaN.
+    // In a pair both streams clear, and wait for each other, before either uses
+    // the tile.
+    static __device__ void clear_ends(const AttnArgs &p, Shared &s, uint8_t *ring, int fill,
+                                      int before, int valid, bool pair, int stream, int tid)
     {
         const int slot = fill % kSlots;
         wait_full(p, s, fill);
         uint8_t *v = ring + slot * kTileBytes;
-        const int end = (valid + 15) & ~15, n = (end - valid) * 8 * kBlocks;
         const int at = pair ? stream * 128 + tid : tid, step = pair ? 256 : 128;
-        for (int i = at; i < n; i += step) {
-            const int row = valid + i / (8 * kBlocks), c = i % (8 * kBlocks);
-            *reinterpret_cast<uint4 *>(v + (c / 8) * (kKeys * 128) + row * 128 + (c % 8) * 16) =
-                make_uint4(0, 0, 0, 0);
-        }
+        auto clear = [&](int from, int to) {
+            for (int i = at; i < (to - from) * 8 * kBlocks; i += step) {
+                const int row = from + i / (8 * kBlocks), c = i % (8 * kBlocks);
+                *reinterpret_cast<uint4 *>(v + (c / 8) * (kKeys * 128) + row * 128 +
+                                           (c % 8) * 16) = make_uint4(0, 0, 0, 0);
+            }
+        };
+        if (before > 0)
+            clear(before & ~15, before);
+        if (valid < kKeys)
+            clear(valid, (valid + 15) & ~15);
         fence_proxy_async_smem();
         __syncwarp();
         if (pair)
