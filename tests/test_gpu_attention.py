@@ -288,3 +288,23 @@ def test_binding_refuses_what_does_not_fit():
     i = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError):
         w4.w4_attn_shared_prefix(z[:, 0], z, z, i[None], i, i)
+
+
+@pytest.mark.gpu
+def test_binding_refuses_other_types_and_shapes(lib):
+    import torch
+    c = _build([100, 90], [1, 2], [2], [64], 4, 2, 64, 16, "bfloat16", seed=1)
+    k = c["cache"][0]
+    assert _run(lib, c, True).shape == c["q"].shape
+    for bad in (dict(q=c["q"].half()), dict(q=c["q"][:, :, :32]), dict(q=c["q"].float()),
+                dict(q=c["q"][0]), dict(table=c["table"].long()), dict(table=c["table"][:1]),
+                dict(table=c["table"][:, ::2]), dict(lens=c["lens"].float()),
+                dict(lens=c["lens"][:1]), dict(q_offsets=c["q_offsets"].cpu()),
+                dict(group_offsets=c["group_offsets"].long()), dict(shared=None),
+                dict(shared=c["shared"].repeat(2)), dict(cache=torch.stack((k, k)).float())):
+        with pytest.raises(ValueError):
+            _run(lib, dict(c, **bad), True)
+    for bad in (dict(out=c["q"][:2]), dict(out=torch.empty_like(c["q"]).half()),
+                dict(dev_status=torch.zeros(1, device="cuda"))):
+        with pytest.raises(ValueError):
+            _run(lib, c, True, **bad)

@@ -192,3 +192,43 @@ def test_binding_refuses_mismatched_shapes():
     x = torch.zeros((2, 256))
     with pytest.raises(ValueError):
         w4.w4_moe_layer_few(x, x, x, (x, x, x), (x, x, x))
+
+
+@pytest.mark.gpu
+def test_binding_refuses_other_types_and_shapes(lib):
+    import torch
+    E, d, m, k = 4, 256, 128, 2
+    dev = dict(device="cuda")
+    gu = (torch.zeros((E, 2 * m, d // 2), dtype=torch.uint8, **dev),
+          torch.zeros((E, 2 * m, d // 128), dtype=torch.float16, **dev),
+          torch.zeros((E, 2 * m, d // 128), dtype=torch.float16, **dev))
+    dn = (torch.zeros((E, d, m // 2), dtype=torch.uint8, **dev),
+          torch.zeros((E, d, m // 64), dtype=torch.float16, **dev),
+          torch.zeros((E, d, m // 64), dtype=torch.float16, **dev))
+    x = torch.zeros((3, d), dtype=torch.bfloat16, **dev)
+    ids = torch.zeros((3, k), dtype=torch.int32, **dev)
+    w = torch.zeros((3, k), **dev)
+    logits = torch.zeros((3, E), **dev)
+
+    def few(**kw):
+        a = dict(x=x, topk_ids=ids, topk_weights=w, gu=gu, dn=dn)
+        a.update(kw)
+        return w4.w4_moe_layer_few(**a)
+
+    def routed(**kw):
+        a = dict(x=x, logits=logits, k=k, gu=gu, dn=dn)
+        a.update(kw)
+        return w4.w4_moe_layer_few_from_logits(**a)
+    assert few().shape == x.shape and routed()[1].shape == ids.shape
+    for bad in (dict(x=x.half()), dict(x=x[:, :128]), dict(topk_ids=ids.long()),
+                dict(topk_ids=ids[:2]), dict(topk_weights=w.half()), dict(topk_weights=w[:, :1]),
+                dict(gu=(gu[0], gu[1].float(), gu[2])), dict(gu=(gu[0], gu[1], gu[2][:, :, :1])),
+                dict(gu=(gu[0][:, :, ::2], gu[1], gu[2])), dict(gu=(gu[0][:3], gu[1], gu[2])),
+                dict(dn=(dn[0], dn[1][:2], dn[2])), dict(dn=(dn[0].short(), dn[1], dn[2])),
+                dict(out=x[:2]), dict(out=x.float()), dict(gu_group=64), dict(x=x.cpu())):
+        with pytest.raises(ValueError):
+            few(**bad)
+    for bad in (dict(logits=logits.double()), dict(logits=logits[:, :3]), dict(ids=ids.long()),
+                dict(weights=w[:1]), dict(x=x.float())):
+        with pytest.raises(ValueError):
+            routed(**bad)

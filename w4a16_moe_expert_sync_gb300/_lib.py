@@ -153,6 +153,17 @@ def _require_cuda(*ts):
             raise ValueError("tensors passed to the CUDA library must be contiguous")
 
 
+def _require(specs):
+    """Every (tensor, type, shape, name) is a contiguous CUDA tensor like that."""
+    for t, dtype, shape, name in specs:
+        if not t.is_cuda:
+            raise ValueError("tensors passed to the CUDA library must live on the GPU")
+        if not t.is_contiguous():
+            raise ValueError("tensors passed to the CUDA library must be contiguous")
+        if t.dtype is not dtype or t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)} {dtype}, not {list(t.shape)} {t.dtype}")
+
+
 # --------------------------------------------------------------------------
 # entry points (same names as the C ABI)
 # --------------------------------------------------------------------------
@@ -489,14 +500,27 @@ def w4_moe_layer_few_workspace_size(M, d, m, E, k) -> int:
     return int(load_library().w4_moe_layer_few_workspace_size(M, d, m, E, k))
 
 
-def _few_dims(x, gu, dn):
-    """(M, d, m, E) of a few-token call, with the weights' shapes checked."""
+def _few_inputs(x, k, gu, dn, gu_group, dn_group, workspace, dev_status):
+    """(M, d, m, E, the workspace) of a few-token call, with x, the weights and
+    the workspace checked."""
+    import torch
+    (gq, gs, gz), (dq, ds, dz) = gu, dn
+    if x.dim() != 2 or gq.dim() != 3 or gu_group <= 0 or dn_group <= 0:
+        raise ValueError("x must be [M, d] and the packed weights [E, rows, columns / 2]")
     M, d = x.shape
-    E, two_m, half_d = gu[0].shape
+    E, two_m, _ = gq.shape
     m = two_m // 2
-    if half_d * 2 != d or tuple(dn[0].shape) != (E, d, m // 2):
-        raise ValueError("the expert weights' shapes do not fit x and each other")
-    return M, d, m, E
+    u8, f16 = torch.uint8, torch.float16
+    g_shape, d_shape = (E, 2 * m, d // gu_group), (E, d, m // dn_group)
+    _require(((x, torch.bfloat16, (M, d), "x"),
+              (gq, u8, (E, 2 * m, d // 2), "gu's codes"), (gs, f16, g_shape, "gu's scales"),
+              (gz, f16, g_shape, "gu's zeros"), (dq, u8, (E, d, m // 2), "dn's codes"),
+              (ds, f16, d_shape, "dn's scales"), (dz, f16, d_shape, "dn's zeros")))
+    if workspace is None:
+        workspace = torch.empty(w4_moe_layer_few_workspace_size(M, d, m, E, k), dtype=u8,
+                                device=x.device)
+    _require_cuda(workspace, dev_status)
+    return M, d, m, E, workspace
 
 
 def w4_moe_layer_few(x, topk_ids, topk_weights, gu, dn, gu_group: int = 128, dn_group: int = 64,
@@ -504,18 +528,21 @@ def w4_moe_layer_few(x, topk_ids, topk_weights, gu, dn, gu_group: int = 128, dn_
     """The whole routed-expert layer for a few tokens (M <= 32, M k <= 256)
     in one cooperative launch; arguments and result as w4_moe_layer."""
     import torch
-    _require_cuda(x, topk_ids, topk_weights, *gu, *dn, workspace, out, dev_status)
-    M, d, m, E = _few_dims(x, gu, dn)
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be [M, k]")
     k = topk_ids.shape[1]
-    if workspace is None:
-        workspace = torch.empty(w4_moe_layer_few_workspace_size(M, d, m, E, k),
-                                dtype=torch.uint8, device=x.device)
+    M, d, m, E, workspace = _few_inputs(x, k, gu, dn, gu_group, dn_group, workspace, dev_status)
+    _require(((topk_ids, torch.int32, (M, k), "topk_ids"),
+              (topk_weights, torch.float32, (M, k), "topk_weights")))
     if out is None:
-        out = torch.empty((M, d), dtype=torch.bfloat16, device=x.device)
+        out = torch.empty_like(x)
+    else:
+        _require(((out, torch.bfloat16, (M, d), "out"),))
     _check(load_library().w4_moe_layer_few(
-        _ptr(x), _ptr(topk_ids), _ptr(topk_weights), M, d, m, E, k, _ptr(gu[0]), _ptr(gu[1]),
-        _ptr(gu[2]), gu_group, _ptr(dn[0]), _ptr(dn[1]), _ptr(dn[2]), dn_group, _ptr(workspace),
-        workspace.numel(), _ptr(out), _ptr(dev_status), _stream(stream)), "w4_moe_layer_few")
+        x.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), M, d, m, E, k,
+        gu[0].data_ptr(), gu[1].data_ptr(), gu[2].data_ptr(), gu_group, dn[0].data_ptr(),
+        dn[1].data_ptr(), dn[2].data_ptr(), dn_group, workspace.data_ptr(), workspace.nbytes,
+        out.data_ptr(), _ptr(dev_status), _stream(stream)), "w4_moe_layer_few")
     return out
 
 
@@ -525,22 +552,25 @@ def w4_moe_layer_few_from_logits(x, logits, k: int, gu, dn, gu_group: int = 128,
     """w4_moe_layer_few with the router in its launch: from the logits
     [M, E] fp32.  Returns (out, topk_ids, topk_weights)."""
     import torch
-    _require_cuda(x, logits, *gu, *dn, workspace, out, ids, weights, dev_status)
-    M, d, m, E = _few_dims(x, gu, dn)
-    if workspace is None:
-        workspace = torch.empty(w4_moe_layer_few_workspace_size(M, d, m, E, k),
-                                dtype=torch.uint8, device=x.device)
+    M, d, m, E, workspace = _few_inputs(x, k, gu, dn, gu_group, dn_group, workspace, dev_status)
+    _require(((logits, torch.float32, (M, E), "logits"),))
     if out is None:
-        out = torch.empty((M, d), dtype=torch.bfloat16, device=x.device)
+        out = torch.empty_like(x)
+    else:
+        _require(((out, torch.bfloat16, (M, d), "out"),))
     if ids is None:
         ids = torch.empty((M, k), dtype=torch.int32, device=x.device)
+    else:
+        _require(((ids, torch.int32, (M, k), "ids"),))
     if weights is None:
         weights = torch.empty((M, k), dtype=torch.float32, device=x.device)
+    else:
+        _require(((weights, torch.float32, (M, k), "weights"),))
     _check(load_library().w4_moe_layer_few_from_logits(
-        _ptr(x), _ptr(logits), M, d, m, E, k, _ptr(gu[0]), _ptr(gu[1]), _ptr(gu[2]), gu_group,
-        _ptr(dn[0]), _ptr(dn[1]), _ptr(dn[2]), dn_group, _ptr(workspace), workspace.numel(),
-        _ptr(ids), _ptr(weights), _ptr(out), _ptr(dev_status), _stream(stream)),
-        "w4_moe_layer_few_from_logits")
+        x.data_ptr(), logits.data_ptr(), M, d, m, E, k, gu[0].data_ptr(), gu[1].data_ptr(),
+        gu[2].data_ptr(), gu_group, dn[0].data_ptr(), dn[1].data_ptr(), dn[2].data_ptr(), dn_group,
+        workspace.data_ptr(), workspace.nbytes, ids.data_ptr(), weights.data_ptr(), out.data_ptr(),
+        _ptr(dev_status), _stream(stream)), "w4_moe_layer_few_from_logits")
     return out, ids, weights
 
 
@@ -668,19 +698,26 @@ def w4_gumbel_argmax_sample(logits, seed: int, offset: int = 0, workspace=None, 
 # three int32 tensors table [B, W] (-1: no page), lens [B] and refs [P].
 # --------------------------------------------------------------------------
 def _require_int32(*ts):
+    """Contiguous int32 CUDA tensors (or None)."""
     import torch
+    int32 = torch.int32
     for t in ts:
-        if t is not None and t.dtype != torch.int32:
-            raise ValueError("tables, lengths, slots and page lists must be int32")
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors passed to the CUDA library must live on the GPU")
+        if not t.is_contiguous():
+            raise ValueError("tensors passed to the CUDA library must be contiguous")
+        if t.dtype is not int32:
+            raise ValueError("tables, lengths, slots, page lists and status must be int32")
 
 
-def _kv_state(table, lens, refs):
+def _kv_state(table, lens, refs, dev_status):
     """(B, W, P) of a cache's state, with its tensors checked."""
-    _require_cuda(table, lens, refs)
-    _require_int32(table, lens, refs)
-    B, W = table.shape
-    if lens.shape != (B,) or refs.dim() != 1:
+    _require_int32(table, lens, refs, dev_status)
+    if table.dim() != 2 or refs.dim() != 1 or lens.shape != table.shape[:1]:
         raise ValueError("lens must be [B] and refs [P] for a table [B, W]")
+    B, W = table.shape
     return B, W, refs.shape[0]
 
 
@@ -696,7 +733,6 @@ def _kv_pool(pool, P):
 
 def _kv_lists(*ts):
     """The length of equally long int32 lists."""
-    _require_cuda(*ts)
     _require_int32(*ts)
     if any(t.dim() != 1 or t.shape != ts[0].shape for t in ts):
         raise ValueError("slots and page lists must be one-dimensional and equally long")
@@ -708,7 +744,7 @@ def _kv_workspace(workspace, P, n, device):
     if workspace is None:
         workspace = torch.empty(w4_kv_workspace_size(P, n), dtype=torch.uint8, device=device)
     _require_cuda(workspace)
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.nbytes
 
 
 def w4_kv_workspace_size(P: int, n: int = 0) -> int:
@@ -718,7 +754,7 @@ def w4_kv_workspace_size(P: int, n: int = 0) -> int:
 def w4_kv_reserve(table, lens, refs, slots, new_lens, page_size: int, dev_status=None,
                   stream=None):
     """Grow slots[i] to new_lens[i] tokens; pages are taken lowest free first."""
-    B, W, P = _kv_state(table, lens, refs)
+    B, W, P = _kv_state(table, lens, refs, dev_status)
     n = _kv_lists(slots, new_lens)
     _check(load_library().w4_kv_reserve(_ptr(table), B, W, _ptr(lens), _ptr(refs), P, _ptr(slots),
                                         _ptr(new_lens), n, page_size, _ptr(dev_status),
@@ -727,7 +763,7 @@ def w4_kv_reserve(table, lens, refs, slots, new_lens, page_size: int, dev_status
 
 def w4_kv_free(table, lens, refs, slots, dev_status=None, stream=None):
     """Empty slots[i] and let go of its pages."""
-    B, W, P = _kv_state(table, lens, refs)
+    B, W, P = _kv_state(table, lens, refs, dev_status)
     n = _kv_lists(slots)
     _check(load_library().w4_kv_free(_ptr(table), B, W, _ptr(lens), _ptr(refs), P, _ptr(slots), n,
                                      _ptr(dev_status), _stream(stream)), "w4_kv_free")
@@ -737,7 +773,7 @@ def w4_kv_fork(pool, table, lens, refs, parents, children, workspace=None, dev_s
                stream=None):
     """Make the empty slots children[i] copies of parents[i]: full pages are
     shared, the last, partly filled one is copied in every plane."""
-    B, W, P = _kv_state(table, lens, refs)
+    B, W, P = _kv_state(table, lens, refs, dev_status)
     planes, page_bytes, page = _kv_pool(pool, P)
     n = _kv_lists(parents, children)
     workspace, nbytes = _kv_workspace(workspace, P, n, pool.device)
@@ -751,6 +787,7 @@ def w4_kv_copy_pages(pool, src, dst, dev_status=None, stream=None):
     """Copy page src[i] to page dst[i] in every plane (disjoint pages)."""
     P = pool.shape[-4] if pool.dim() >= 4 else 0
     planes, page_bytes, _ = _kv_pool(pool, P)
+    _require_int32(dev_status)
     n = _kv_lists(src, dst)
     _check(load_library().w4_kv_copy_pages(_ptr(pool), planes, page_bytes, P, _ptr(src), _ptr(dst),
                                            n, _ptr(dev_status), _stream(stream)),
@@ -764,9 +801,8 @@ def w4_kv_compact(pool, table, refs, table_out=None, refs_out=None, workspace=No
     themselves."""
     table_out = table if table_out is None else table_out
     refs_out = refs if refs_out is None else refs_out
-    _require_cuda(table, refs, table_out, refs_out)
-    _require_int32(table, refs, table_out, refs_out)
-    if table.dim() != 2 or table_out.shape != table.shape or refs_out.shape != refs.shape:
+    _require_int32(table, refs, table_out, refs_out, dev_status)
+    if table.dim() != 2 or refs.dim() != 1 or table_out.shape != table.shape or refs_out.shape != refs.shape:
         raise ValueError("table_out and refs_out must have the shapes of table and refs")
     B, W = table.shape
     P = refs.shape[0]
@@ -779,44 +815,53 @@ def w4_kv_compact(pool, table, refs, table_out=None, refs_out=None, workspace=No
     return table_out, refs_out
 
 
-def _rows16(t, what):
-    """A CUDA tensor [.., .., D] of 16-bit values, contiguous along D only."""
+def _rows16(t, dtype, what):
+    """A CUDA tensor of the type, contiguous along its last axis.  Returns its strides."""
     if not t.is_cuda:
         raise ValueError("tensors passed to the CUDA library must live on the GPU")
-    if t.element_size() != 2 or t.stride(-1) != 1:
-        raise ValueError(f"{what} must be 16-bit values, contiguous along the last axis")
+    strides = t.stride()
+    if t.dtype is not dtype or not strides or strides[-1] != 1:
+        raise ValueError(f"{what} must be {dtype}, contiguous along the last axis")
+    return strides
 
 
 def _kv_planes(k_pages, v_pages):
-    """(P, page_size, Hkv, D) of one layer's planes, with their strides checked."""
-    _rows16(k_pages, "k_pages")
-    _rows16(v_pages, "v_pages")
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or \
-            k_pages.stride() != v_pages.stride() or k_pages.dtype != v_pages.dtype:
-        raise ValueError("k_pages and v_pages must be alike, [P, page_size, Hkv, D]")
-    return tuple(k_pages.shape)
+    """(type, shape [P, page_size, Hkv, D], strides) of one layer's planes."""
+    dtype, shape = k_pages.dtype, k_pages.shape
+    strides = _rows16(k_pages, dtype, "k_pages")
+    if k_pages.dim() != 4 or k_pages.element_size() != 2 or v_pages.shape != shape or \
+            _rows16(v_pages, dtype, "v_pages") != strides:
+        raise ValueError("k_pages and v_pages must be alike, [P, page_size, Hkv, D] of 16 bits")
+    return dtype, shape, strides
+
+
+def _kv_batch(table, lens, q_offsets):
+    """(B, W) of q_offsets [B + 1], with a table and lengths for as many."""
+    B = q_offsets.numel() - 1
+    if B < 0 or q_offsets.dim() != 1 or table.dim() != 2 or lens.dim() != 1:
+        raise ValueError("q_offsets must be [B + 1] for a table [B, W] and lens [B]")
+    rows, W = table.shape
+    if rows < B or lens.numel() < B:
+        raise ValueError("q_offsets must be [B + 1] for a table [B, W] and lens [B]")
+    return B, W
 
 
 def w4_kv_append(k_pages, v_pages, table, lens, k, v, q_offsets, dev_status=None, stream=None):
     """Write the new tokens' keys and values [T, Hkv, D] (any strides of tokens
     and heads) into their pages; slot b's are rows q_offsets[b] ..
     q_offsets[b + 1] and its last tokens."""
-    P, page, Hkv, D = _kv_planes(k_pages, v_pages)
-    _rows16(k, "k")
-    _rows16(v, "v")
-    _require_cuda(table, lens, q_offsets, dev_status)
-    _require_int32(table, lens, q_offsets)
-    if k.shape != v.shape or tuple(k.shape[1:]) != (Hkv, D) or k.dtype != k_pages.dtype or \
-            v.dtype != k_pages.dtype:
+    dtype, (P, page, Hkv, D), strides = _kv_planes(k_pages, v_pages)
+    ks, vs = _rows16(k, dtype, "k"), _rows16(v, dtype, "v")
+    _require_int32(table, lens, q_offsets, dev_status)
+    if k.dim() != 3 or k.shape != v.shape or k.shape[1:] != (Hkv, D):
         raise ValueError("k and v must be [T, Hkv, D] of the pages' type")
-    B = q_offsets.shape[0] - 1
-    if B < 1 or table.dim() != 2 or table.shape[0] < B or lens.shape[0] < B:
-        raise ValueError("q_offsets must be [B + 1] for a table [B, W] and lens [B]")
+    B, W = _kv_batch(table, lens, q_offsets)
+    if B == 0:
+        return
     _check(load_library().w4_kv_append(
-        _ptr(k_pages), _ptr(v_pages), *k_pages.stride()[:3], P, page, Hkv, D, _ptr(table), B,
-        table.shape[1], _ptr(lens), _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0),
-        v.stride(1), _ptr(q_offsets), k.shape[0], _ptr(dev_status), _stream(stream)),
-        "w4_kv_append")
+        k_pages.data_ptr(), v_pages.data_ptr(), *strides[:3], P, page, Hkv, D, table.data_ptr(), B,
+        W, lens.data_ptr(), k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+        q_offsets.data_ptr(), k.shape[0], _ptr(dev_status), _stream(stream)), "w4_kv_append")
 
 
 def w4_attn_shared_prefix_workspace_size(T: int, B: int, G: int, max_q: int, Hq: int, Hkv: int,
@@ -832,33 +877,32 @@ def w4_attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets, group_off
     group_offsets[g + 1] share their first shared_lens[g] tokens, which are read
     once for the group.  scale defaults to 1 / sqrt(D).  Returns out [T, Hq, D]."""
     import torch
-    P, page, Hkv, D = _kv_planes(k_pages, v_pages)
-    _rows16(q, "q")
-    _require_cuda(table, lens, q_offsets, group_offsets, shared_lens, workspace, out, dev_status)
-    _require_int32(table, lens, q_offsets, group_offsets, shared_lens)
-    if q.dim() != 3 or q.shape[2] != D or q.dtype != k_pages.dtype or \
-            q.dtype not in (torch.bfloat16, torch.float16):
+    dtype, (P, page, Hkv, D), strides = _kv_planes(k_pages, v_pages)
+    qs = _rows16(q, dtype, "q")
+    _require_int32(table, lens, q_offsets, group_offsets, shared_lens, dev_status)
+    if q.dim() != 3 or (dtype is not torch.bfloat16 and dtype is not torch.float16):
         raise ValueError("q must be [T, Hq, D] of the pages' type, bf16 or fp16")
-    T, Hq, _ = q.shape
-    B = q_offsets.shape[0] - 1
-    if B < 0 or table.dim() != 2 or table.shape[0] < B or lens.shape[0] < B:
-        raise ValueError("q_offsets must be [B + 1] for a table [B, W] and lens [B]")
-    G = 0 if group_offsets is None else group_offsets.shape[0] - 1
-    if G < 0 or (G > 0 and (shared_lens is None or shared_lens.shape[0] != G)):
+    T, Hq, q_d = q.shape
+    if q_d != D:
+        raise ValueError("q must be [T, Hq, D] of the pages' type, bf16 or fp16")
+    B, W = _kv_batch(table, lens, q_offsets)
+    G = 0 if group_offsets is None else group_offsets.numel() - 1
+    if G < 0 or (G > 0 and (shared_lens is None or shared_lens.numel() != G)):
         raise ValueError("group_offsets must be [G + 1] and shared_lens [G]")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    elif tuple(out.shape) != (T, Hq, D) or out.dtype != q.dtype:
-        raise ValueError("out must be [T, Hq, D] of q's type")
+        out = torch.empty((T, Hq, D), dtype=dtype, device=q.device)
+    else:
+        _require(((out, dtype, (T, Hq, D), "out"),))
     if workspace is None:
         workspace = torch.empty(
             max(w4_attn_shared_prefix_workspace_size(T, B, G, max_q, Hq, Hkv, D), 256)
             if Hkv and Hq % Hkv == 0 else 256, dtype=torch.uint8, device=q.device)
+    _require_cuda(workspace)
     _check(load_library().w4_attn_shared_prefix(
-        _ptr(q), q.stride(0), q.stride(1), _ptr(k_pages), _ptr(v_pages), *k_pages.stride()[:3], P,
-        page, _ptr(table), table.shape[1], _ptr(lens), _ptr(q_offsets), T, B, max_q,
+        q.data_ptr(), qs[0], qs[1], k_pages.data_ptr(), v_pages.data_ptr(), *strides[:3], P, page,
+        table.data_ptr(), W, lens.data_ptr(), q_offsets.data_ptr(), T, B, max_q,
         _ptr(group_offsets), _ptr(shared_lens), G, Hq, Hkv, D,
-        0 if q.dtype == torch.bfloat16 else 1, int(causal), D ** -0.5 if scale is None else scale,
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out),
-        _ptr(dev_status), _stream(stream)), "w4_attn_shared_prefix")
+        0 if dtype is torch.bfloat16 else 1, int(causal), D ** -0.5 if scale is None else scale,
+        workspace.data_ptr(), workspace.nbytes, out.data_ptr(), _ptr(dev_status),
+        _stream(stream)), "w4_attn_shared_prefix")
     return out
