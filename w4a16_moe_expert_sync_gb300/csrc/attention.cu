@@ -14,8 +14,8 @@
 // An entry is a group's prefix or a sequence's own keys; an item is an entry's
 // row tile for one kv head.  Entries of more than 128 rows are taken as pairs:
 // two 128-row tiles of one CTA against the same K and V tile.  The tiles of
-// all pair items laid end to end are split evenly over the CTAs, those of all
-// single items over the CTAs' two streams, wherever item borders fall; each
+// all pair items laid end to end are split evenly over some of the CTAs, those of
+// all single items over the others' two streams, wherever item borders fall; each
 // piece leaves unnormalised sums with their maximum and denominator, which a
 // second kernel joins per row.  So one long prefix fills the GPU as evenly as
 // a thousand short ones.  The split follows from the lengths, which live on
@@ -59,6 +59,7 @@ struct Entry {
 struct alignas(16) Joint {
     int tok0, tokens;                      // tokens < 0: nothing to write
     int all[2];                            // length of the single [0] and pair [1] region
+    int workers[2];                        // and among how many it is split
     Entry e[2];                            // of its group's prefix and of its own keys
 };
 
@@ -97,6 +98,9 @@ struct AttnArgs {
 // An item is kItemCost + its tiles long when the work is split: fetching its
 // queries and storing its sums takes about as long as that many tiles.
 constexpr int kItemCost = 2;
+// A CTA's time for a single tile in those of a pair's, as the CTAs are divided
+// between the two.
+constexpr float kSingleWeight = 0.7f;
 
 // Worker w's share of a region's `all` begins here.
 __device__ __forceinline__ int worker_begin(int all, int workers, int w)
@@ -112,8 +116,15 @@ __device__ __forceinline__ int worker_of(int all, int workers, int x)
         return static_cast<int>((static_cast<uint32_t>(x + 1) * workers - 1) / all);
     return static_cast<int>((static_cast<int64_t>(x + 1) * workers - 1) / all);
 }
-// No worker goes without a share.
-__device__ __forceinline__ int workers_for(int all, int most) { return all < most ? all : most; }
+// How many CTAs take the pairs; the others, two streams each, take the single
+// items.  No worker goes without a share.
+__device__ __forceinline__ int pair_ctas(int singles, int pairs, int grid)
+{
+    if (pairs == 0 || singles == 0)
+        return min(pairs, grid);
+    const float part = pairs / (pairs + kSingleWeight * singles);
+    return min(pairs, max(1, min(grid - 1, static_cast<int>(part * grid + 0.5f))));
+}
 
 // ------------------------------------------------------------- tensor memory
 // All 128 columns of this thread's lane, and the wait for them.
@@ -220,6 +231,19 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ float low(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float high(uint64_t x)
+{
+    return __uint_as_float(static_cast<uint32_t>(x >> 32));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -396,7 +420,7 @@ struct Kernel {
 
     struct Shared {
         alignas(8) uint64_t full[kSlots], empty[kSlots];
-        uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2], drained[2], pairs_done;
+        uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2], drained[2];
         uint32_t tmem;
         int abort_flag;
         int requested;                         // fills requested of the ring so far
@@ -466,16 +490,17 @@ struct Kernel {
             en.item0 = start[(en.pair ? 3 * n : n) + e];
             return en;
         };
+        const int for_pairs = pair_ctas(total.x, total.z, gridDim.x);
+        const int for_singles = gridDim.x - for_pairs;
         // warps 0, 1 and 2 work out the pieces of streams 0 and 1 and of the pairs
         const int which = tid >> 5, lane = tid & 31;
         if (which < 3) {
             const bool pair = which == 2;
-            const int all = pair ? total.z : total.x, grid = gridDim.x;
-            const int workers = workers_for(all, pair ? grid : 2 * grid);
-            // single items start at the first CTA that has no pairs, one stream
-            // of every CTA before the other
-            const int turned = blockIdx.x - workers_for(total.z, grid);
-            const int w = pair ? blockIdx.x : which * grid + (turned < 0 ? turned + grid : turned);
+            const int all = pair ? total.z : total.x, cta = blockIdx.x;
+            const int workers = pair ? for_pairs : min(all, 2 * for_singles);
+            // one stream of every CTA before the other
+            const int w = pair ? cta : cta < for_pairs ? workers
+                                                       : which * for_singles + cta - for_pairs;
             const int *ts = start + (pair ? 2 * n : 0), *is = start + (pair ? 3 * n : n);
             int first = 0, count = 0, lo = 0, hi = 0;
             if (w < workers) {
@@ -541,6 +566,8 @@ struct Kernel {
                 j.tokens = !bad && qo[b + 1] - qo[b] <= p.max_q ? qo[b + 1] - qo[b] : -1;
                 j.all[0] = total.x;
                 j.all[1] = total.z;
+                j.workers[0] = min(total.x, 2 * for_singles);
+                j.workers[1] = for_pairs;
                 const int g = bad ? -1 : group_of(p, x, b);
                 if (g >= 0) {
                     j.e[0] = placed(g);
@@ -554,14 +581,14 @@ struct Kernel {
         __syncthreads();
     }
 
-    // The pair of slots (K, then V) of a stream's tile `r` of its single items
-    // or of a pair's tile r: the loader takes the pairs first, then the
-    // streams' tiles in turn, and a stream that has none left drops out.
+    // The pair of slots (K, then V) of a pair's tile r, or of a stream's tile r
+    // of its single items: the loader takes the streams' tiles in turn, and a
+    // stream that has none left drops out.  A CTA has pairs or single items.
     static __device__ __forceinline__ int fill_of(const Shared &s, int which, int r)
     {
         if (which == 2)
             return r;
-        return s.tiles[2] + r + (which == 0 ? min(r, s.tiles[1]) : min(r + 1, s.tiles[0]));
+        return r + (which == 0 ? min(r, s.tiles[1]) : min(r + 1, s.tiles[0]));
     }
 
     static __device__ __forceinline__ bool wait(const AttnArgs &p, Shared &s, uint64_t *bar,
@@ -738,10 +765,16 @@ struct Kernel {
         __syncwarp();
         const uint32_t va = smem_u32(ring + slot * kTileBytes);
         const uint32_t ts = s.tmem + kS + 128 * stream, to = s.tmem + kO + D * stream;
-        const int begin = max(before, 0) / 16, end = (min(keys, kKeys) + 15) / 16;
-        for (int k = begin; k < end; k++)
-            tc_mma_ts_elect(to, ts + 8 * k, sdesc_mn_sw128(va + k * 2048, kKeys * 128), kPv,
-                            !first || k > begin);
+        const uint64_t vd = sdesc_mn_sw128(va, kKeys * 128);
+        if (before <= 0 && keys > kKeys - 16) {
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; k++)
+                tc_mma_ts_elect(to, ts + 8 * k, vd + k * (2048 >> 4), kPv, !first || k > 0);
+        } else {
+            const int begin = max(before, 0) / 16, end = (min(keys, kKeys) + 15) / 16;
+            for (int k = begin; k < end; k++)
+                tc_mma_ts_elect(to, ts + 8 * k, vd + k * (2048 >> 4), kPv, !first || k > begin);
+        }
         if (last_use)
             tc_commit_elect(&s.empty[slot]);
         if (last)
@@ -786,14 +819,6 @@ struct Kernel {
                     tile_phase ^= 1;
                 }
             }
-            mbar_arrive_elect(&s.pairs_done);
-        } else {                               // the phases go on where the pairs' end
-            wait(p, s, &s.pairs_done, 0);
-            for (int i = 0; i < s.segs[2]; i++) {
-                const int tiles = p.segs[p.cap_b + s.seg0[2] + i].tiles;
-                seg_phase ^= tiles > 0;
-                tile_phase ^= tiles & 1;
-            }
         }
         const Seg *segs = p.segs + s.seg0[stream];
         for (int i = 0, r = 0; i < s.segs[stream]; i++) {
@@ -831,20 +856,18 @@ struct Kernel {
         const uint32_t to = s.tmem + lanes + kO + D * stream;
         uint8_t *q = qbuf + stream * kTileBytes;
         uint32_t s_phase = 0, o_phase = 0;
-        // the pairs' pieces, then this stream's own
-        auto piece = [&](int i) -> const Seg & {
-            const int which = i < s.segs[2] ? 2 : stream, at = which == 2 ? i : i - s.segs[2];
-            return at == 0 ? s.first[which]
-                           : p.segs[(which == 2 ? p.cap_b : 0) + s.seg0[which] + at];
-        };
-        auto pieces = [&] { return s.segs[2] + s.segs[stream]; };
+        // a CTA has pairs, or each stream its own single items
+        const bool pair = s.segs[2] > 0;
+        const int which = pair ? 2 : stream, count = s.segs[which];
+        const Seg *segs = p.segs + (pair ? p.cap_b : 0) + s.seg0[which];
+        auto piece = [&](int i) -> const Seg & { return i == 0 ? s.first[which] : segs[i]; };
         // A piece's queries on their way to shared memory.  Called when no MMA
         // reads the queries any more.
         auto fetch = [&](int i) {
             const Seg &g = piece(i);
             if (g.tiles > 0)
-                load_q(p, q, g, g.row0 + (i < s.segs[2] ? stream * kRows : 0),
-                       rows_here(g, i < s.segs[2], stream), tid);
+                load_q(p, q, g, g.row0 + (pair ? stream * kRows : 0), rows_here(g, pair, stream),
+                       tid);
         };
         // How many keys this thread's row of a piece sees.  The lanes part ways in
         // it, and the tensor-memory instructions that follow need them together
@@ -852,8 +875,8 @@ struct Kernel {
         auto sees = [&](int i) {
             const Seg &g = piece(i);
             int n = INT_MAX;                   // no row: nothing to mask, nothing kept
-            if (tid < rows_here(g, i < s.segs[2], stream)) {
-                const int row = g.row0 + (i < s.segs[2] ? stream * kRows : 0) + tid;
+            if (tid < rows_here(g, pair, stream)) {
+                const int row = g.row0 + (pair ? stream * kRows : 0) + tid;
                 n = min(limit_of(p, g, g.tok0 + row / p.rep), g.k1);
             }
             __syncwarp();
@@ -864,19 +887,17 @@ struct Kernel {
                 return;
             cp_async_wait_all();
             fence_proxy_async_smem();
-            mbar_arrive(&s.q_ready[stream]);
+            __syncwarp();
+            mbar_arrive_elect(&s.q_ready[stream]);
         };
         int limit = 0, next = 0;
-        if (pieces() > 0) {
+        if (count > 0) {
             fetch(0);
             hand_over(0);
             limit = sees(0);
         }
-        const int pairs = s.segs[2], count = pieces();
         for (int i = 0, r = 0; i < count; i++, limit = next) {
-            const bool pair = i < pairs, another = i + 1 < count;
-            if (i == pairs)
-                r = 0;
+            const bool another = i + 1 < count;
             const Seg g = piece(i);
             const int rows = rows_here(g, pair, stream);
             const bool busy = rows > (tid & ~31);
@@ -896,10 +917,12 @@ struct Kernel {
                     tile(p, ts, to, limit == INT_MAX ? 0 : g.k0 - base,
                          limit == INT_MAX ? kKeys : limit - base, t > 0, m, l);
                 if ((g.k1 - base < kKeys && (g.k1 & 15)) || (g.k0 > base && (g.k0 & 15)))
-                    clear_ends(p, s, ring, 2 * fill_of(s, pair ? 2 : stream, r) + 1, g.k0 - base,
+                    clear_ends(p, s, ring, 2 * fill_of(s, which, r) + 1, g.k0 - base,
                                g.k1 - base, pair, stream, tid);
+                // one arrival a warp: a thread's each would take a few cycles of the barrier
                 tc_fence_before();
-                mbar_arrive(&s.p_ready[stream]);
+                __syncwarp();
+                mbar_arrive_elect(&s.p_ready[stream]);
             }
             if (another) {
                 if (g.tiles == 0) {
@@ -997,9 +1020,9 @@ struct Kernel {
         }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 128; c++)
-            top[c & 3] = fmaxf(top[c & 3], __uint_as_float(v[c]));
-        const float tm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+        for (int c = 0; c < 128; c += 2)
+            top[c / 2 & 3] = max3(top[c / 2 & 3], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+        const float tm = max3(fmaxf(top[0], top[1]), top[2], top[3]) * p.scale_log2;
         const bool move = tm > m + 8.0f;       // also from -inf
         if (__any_sync(0xffffffffu, move)) {
             const float alpha = move ? ex2(m - tm) : 1.0f;
@@ -1017,16 +1040,14 @@ struct Kernel {
 #pragma unroll
             for (int j = 0; j < 16; j++) {
                 const uint64_t x = fma2(pair_of(v[c + 2 * j], v[c + 2 * j + 1]), scale2, ref2);
-                const float a = ex2(__uint_as_float(static_cast<uint32_t>(x)));
-                const float b = ex2(__uint_as_float(static_cast<uint32_t>(x >> 32)));
+                const float a = ex2(low(x)), b = ex2(high(x));
                 sum[j & 1] = add2(sum[j & 1], pair_of(__float_as_uint(a), __float_as_uint(b)));
                 pk[j] = pack2<BF16>(a, b);
             }
             tmem_st_32x32b_x16(ts + c / 2, pk);
         }
         const uint64_t all = add2(sum[0], sum[1]);
-        l += __uint_as_float(static_cast<uint32_t>(all)) +
-             __uint_as_float(static_cast<uint32_t>(all >> 32));
+        l += low(all) + high(all);
         tmem_wait_st();
     }
 
@@ -1122,13 +1143,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             mbar_init(&s.empty[i], 1);
         }
         for (int i = 0; i < 2; i++) {
-            mbar_init(&s.q_ready[i], kRows);
+            mbar_init(&s.q_ready[i], kRows / 32);
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.p_ready[i], kRows);
+            mbar_init(&s.p_ready[i], kRows / 32);
             mbar_init(&s.o_full[i], 1);
             mbar_init(&s.drained[i], 1);
         }
-        mbar_init(&s.pairs_done, 1);
         s.abort_flag = 0;
         s.requested = 0;
         fence_mbar_init();
@@ -1179,7 +1199,7 @@ template <int D, int SPLIT> constexpr int kJoinSides = 8 / SPLIT < D / 16 ? 8 / 
 
 template <int D, bool BF16, int SPLIT>
 __global__ void __launch_bounds__(32 * SPLIT *kJoinSides<D, SPLIT>, SPLIT == 1 ? 3 : 2)
-    attn_join_kernel(const __grid_constant__ AttnArgs p, int grid)
+    attn_join_kernel(const __grid_constant__ AttnArgs p)
 {
     constexpr int kBatch = SPLIT == 1 ? 2 : 4, kSides = kJoinSides<D, SPLIT>;
     __shared__ float4 so[SPLIT][4][kSides][32];
@@ -1204,7 +1224,7 @@ __global__ void __launch_bounds__(32 * SPLIT *kJoinSides<D, SPLIT>, SPLIT == 1 ?
             const int kind = en.pair ? 0 : k + 1, stride = rows_of(p, kind), at = er % step;
             const int local = head * en.row_tiles + er / step;
             const int all = en.pair ? j.all[1] : j.all[0];
-            const int workers = workers_for(all, en.pair ? grid : 2 * grid);
+            const int workers = en.pair ? j.workers[1] : j.workers[0];
             const int x0 = en.place + local * en.span;
             const int w0 = worker_of(all, workers, x0);
             const int w1 = worker_of(all, workers, x0 + en.span - 1);
@@ -1387,9 +1407,9 @@ cudaError_t launch_variant(const AttnArgs &a, int dev, int sms, cudaStream_t str
     const int y = std::min((a.max_q * a.Hq + 31) / 32, std::max(65535 / a.B, 1));
     if (static_cast<int64_t>(a.T) * a.Hq <= kJoinFewRows)
         return launch_pdl(attn_join_kernel<D, BF16, 4>, dim3(a.B, y, D / 16 / kJoinSides<D, 4>),
-                          dim3(128 * kJoinSides<D, 4>), 0, stream, a, grid);
+                          dim3(128 * kJoinSides<D, 4>), 0, stream, a);
     return launch_pdl(attn_join_kernel<D, BF16, 1>, dim3(a.B, y, D / 16 / kJoinSides<D, 1>),
-                      dim3(32 * kJoinSides<D, 1>), 0, stream, a, grid);
+                      dim3(32 * kJoinSides<D, 1>), 0, stream, a);
 }
 
 }  // namespace
