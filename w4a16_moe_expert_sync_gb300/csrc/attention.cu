@@ -626,6 +626,14 @@ struct Kernel {
         wait(p, s, &s.full[fill % kSlots], (fill / kSlots) & 1);
     }
 
+    // One look at whether fill `fill` has landed.
+    static __device__ __forceinline__ bool landed(Shared &s, int fill)
+    {
+        volatile int *requested = &s.requested;
+        return __all_sync(0xffffffffu, *requested > fill) &&
+               __all_sync(0xffffffffu, mbar_try_wait(&s.full[fill % kSlots], (fill / kSlots) & 1));
+    }
+
     // ------------------------------------------------------------- loading
     static __device__ void load_slot(const AttnArgs &p, Shared &s, uint8_t *ring, int fill,
                                      const CUtensorMap *map, int head, int page_id,
@@ -733,12 +741,11 @@ struct Kernel {
     }
 
     // ------------------------------------------------------------- issuing
-    // S = Q K^T of a stream's tile; its K is let go with the last use.
+    // S = Q K^T of a stream's tile, whose K has landed; it is let go with the last use.
     static __device__ __forceinline__ void issue_qk(const AttnArgs &p, Shared &s, uint8_t *qbuf,
                                                     uint8_t *ring, int stream, int fill, bool last_use)
     {
         const int slot = fill % kSlots;
-        wait_full(p, s, fill);
         tc_fence_after();
         __syncwarp();
         const uint64_t qd = sdesc_sw128(smem_u32(qbuf + stream * kTileBytes));
@@ -753,14 +760,13 @@ struct Kernel {
             tc_commit_elect(&s.empty[slot]);
     }
 
-    // O (+)= P V of a stream's tile, 16 keys at a time; steps that lie wholly
+    // O (+)= P V of a stream's tile, whose V has landed, 16 keys at a time; steps that lie wholly
     // before the entry's first key or past its last stay out.
     static __device__ __forceinline__ void issue_pv(const AttnArgs &p, Shared &s, uint8_t *ring,
                                                     int stream, int fill, int before, int keys,
                                                     bool first, bool last, bool last_use)
     {
         const int slot = fill % kSlots;
-        wait_full(p, s, fill);
         tc_fence_after();
         __syncwarp();
         const uint32_t va = smem_u32(ring + slot * kTileBytes);
@@ -802,17 +808,24 @@ struct Kernel {
                 const int tiles = g.tiles, base = g.kbase + g.tile0 * kKeys;
                 if (tiles == 0)
                     continue;
+                wait_full(p, s, 2 * r);
                 for (int st = 0; st < 2; st++) {
                     wait(p, s, &s.q_ready[st], seg_phase);
                     issue_qk(p, s, qbuf, ring, st, 2 * r, st == 1);
                 }
                 seg_phase ^= 1;
                 for (int t = 0; t < tiles; t++, r++) {
+                    wait_full(p, s, 2 * r + 1);
+                    bool here = t + 1 < tiles && landed(s, 2 * r + 2);
                     for (int st = 0; st < 2; st++) {
                         wait(p, s, &s.p_ready[st], tile_phase);
                         const int at = base + t * kKeys;
                         issue_pv(p, s, ring, st, 2 * r + 1, g.k0 - at, g.k1 - at, t == 0,
                                  t == tiles - 1, st == 1);
+                        if (t + 1 < tiles && !here) {
+                            wait_full(p, s, 2 * r + 2);
+                            here = true;
+                        }
                         if (t + 1 < tiles)
                             issue_qk(p, s, qbuf, ring, st, 2 * r + 2, st == 1);
                     }
@@ -830,7 +843,9 @@ struct Kernel {
             seg_phase ^= 1;
             for (int t = 0; t < tiles; t++, r++) {
                 const int fill = 2 * fill_of(s, stream, r);
+                wait_full(p, s, fill);
                 issue_qk(p, s, qbuf, ring, stream, fill, true);
+                wait_full(p, s, fill + 1);
                 wait(p, s, &s.p_ready[stream], tile_phase);
                 tile_phase ^= 1;
                 const int at = base + t * kKeys;
