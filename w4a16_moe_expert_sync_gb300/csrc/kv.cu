@@ -61,7 +61,7 @@ __device__ __forceinline__ int block_exclusive_sum(int v, int *sums, int *total)
 
 struct PlanShared {
     int sums[2][33];
-    int slot[kMaxSlots];
+    alignas(16) int slot[kMaxSlots];
     int start[kMaxSlots + 1];      // pages asked for before request i
     int at[kMaxSlots];             // request i's first table entry
 };
@@ -69,9 +69,13 @@ struct PlanShared {
 // Whether an earlier request names the same slot.
 __device__ __forceinline__ bool repeated(const int *slot, int i)
 {
+    const int mine = slot[i];
     bool again = false;
-    for (int j = 0; j < i; j++)
-        again |= slot[j] == slot[i];
+    for (int j = 0; j < i; j += 4) {       // what lies past i holds other requests: not counted
+        const int4 s = *reinterpret_cast<const int4 *>(slot + j);
+        again |= s.x == mine || (j + 1 < i && s.y == mine) || (j + 2 < i && s.z == mine) ||
+                 (j + 3 < i && s.w == mine);
+    }
     return again;
 }
 
@@ -503,6 +507,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs p)
         return;
     }
     const int vecs = p.D / 8;
+    constexpr int kUnroll = 4;
     for (int t = t0 + blockIdx.y * 8 + warp; t < t1; t += gridDim.y * 8) {
         const int pos = len - (t1 - t);
         const int e = pos / p.page;
@@ -513,14 +518,27 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs p)
             continue;
         }
         const int64_t to = pg * p.page_stride + (pos - e * p.page) * p.tok_stride;
-        for (int i = lane; i < p.Hkv * vecs; i += 32) {
-            const int h = i / vecs, c = (i - h * vecs) * 8;
-            const int4 kv = __ldcs(reinterpret_cast<const int4 *>(p.k + t * p.k_tok + h * p.k_head +
-                                                                  c));
-            const int4 vv = __ldcs(reinterpret_cast<const int4 *>(p.v + t * p.v_tok + h * p.v_head +
-                                                                  c));
-            *reinterpret_cast<int4 *>(p.kp + to + h * p.head_stride + c) = kv;
-            *reinterpret_cast<int4 *>(p.vp + to + h * p.head_stride + c) = vv;
+        // kUnroll 16-byte values of k and of v in flight a lane
+        for (int i0 = lane; i0 < p.Hkv * vecs; i0 += 32 * kUnroll) {
+            int4 kv[kUnroll], vv[kUnroll];
+            int64_t at[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; u++) {
+                const int i = i0 + 32 * u, h = i / vecs, c = (i - h * vecs) * 8;
+                at[u] = to + h * p.head_stride + c;
+                if (i < p.Hkv * vecs) {
+                    kv[u] = __ldcs(reinterpret_cast<const int4 *>(p.k + t * p.k_tok +
+                                                                  h * p.k_head + c));
+                    vv[u] = __ldcs(reinterpret_cast<const int4 *>(p.v + t * p.v_tok +
+                                                                  h * p.v_head + c));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; u++)
+                if (i0 + 32 * u < p.Hkv * vecs) {
+                    *reinterpret_cast<int4 *>(p.kp + at[u]) = kv[u];
+                    *reinterpret_cast<int4 *>(p.vp + at[u]) = vv[u];
+                }
         }
     }
 }
