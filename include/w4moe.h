@@ -411,9 +411,9 @@ int w4_moe_layer_from_logits(const uint16_t *x, const float *logits, int M, int 
 
 /* --------------------------------------------------------------------------
  * w4_moe_layer_few -- the whole routed-expert layer for a few tokens, in one
- * cooperative launch (a CTA per SM, grid barriers between its steps): M <= 32 tokens and M * k <= 256 assignments, where an expert sees
- * a handful of tokens and the layer is the stream of the touched experts'
- * packed weights.  Same inputs and output as w4_moe_layer; the result differs
+ * cooperative launch (a CTA per SM, grid barriers between its steps): M <= 32
+ * tokens and M * k <= 256 assignments, where an expert sees a handful of tokens
+ * and the layer is the stream of the touched experts' packed weights.  Same inputs and output as w4_moe_layer; the result differs
  * from it in rounding only.  The packed codes enter the tensor cores as they
  * are (exact fp16 subnormals) and a group's scale and zero are applied to the
  * fp32 sums, so no weight is rounded; activations and h are fp16 (beyond its

@@ -8,6 +8,14 @@ synthetic workloads (``workloads``) used by the tests and the benchmark.
     q, s, z = w4.w4_quantize(W_fp32_cuda, group=128)
     ids, w = w4.w4_moe_route(logits, k=8)
     out = w4.w4_moe_layer(x_bf16, ids, w, (gu_q, gu_s, gu_z), (dn_q, dn_s, dn_z))
+
+A decoding step has the layer for a few tokens, a paged cache and attention:
+
+    w4.w4_kv_reserve(table, lens, refs, slots, new_lens, page_size)
+    w4.w4_kv_append(k_pages, v_pages, table, lens, k, v, q_offsets)
+    o = w4.w4_attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets,
+                                 group_offsets, shared_lens, max_q=1)
+    out, ids, w = w4.w4_moe_layer_few_from_logits(x, logits, 8, gate_up, down)
 """
 from ._lib import (W4_DEV_BAD_EXPERT_ID, W4_DEV_FP16_RANGE, W4_DEV_OUT_OF_BOUNDS,
                    W4_DEV_PIPELINE_TIMEOUT,

@@ -24,7 +24,18 @@
 // Roles of a CTA's twelve warps: warps 0-3 and 4-7 are the softmax of streams
 // 0 and 1 (a thread per row), warp 8 loads K and V by TMA into a ring of
 // slots, warps 9 and 10 issue the MMAs (of both streams of a pair; of streams 0
-// and 1), warp 11 only completes its group of four.  While one stream's softmax runs the tensor cores work for the other.
+// and 1), warp 11 only completes its group of four.  While one stream's softmax
+// runs the tensor cores work for the other.
+//
+// Bounds and measured times (GB300, both kernels, back to back in a graph):
+//   32 questions about 120,000 shared tokens, 32/4 heads of 128: 72 us; 257 MB
+//     (38 us at the copy bandwidth), 63 GFLOP (32 us).  The pairs' loop takes
+//     some 3000 cycles a tile against 2048 of MMAs: a stream's S, softmax, P and
+//     O follow one another, and two streams do not quite cover it
+//   64 sequences of 33 to 1500 tokens behind 8192: 59 us; 242 MB (36 us).  Plan 4 us,
+//     first tile 6, change of piece 1.5 each, join and its launch 6
+//   four times 256 queries over 4096 + 256: 47 us; 37 GFLOP (19 us), the pairs' loop
+//   two sequences of 240 tokens: 14 us, all of it plan, one tile and join
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -96,10 +107,15 @@ struct AttnArgs {
 };
 
 // An item is kItemCost + its tiles long when the work is split: fetching its
-// queries and storing its sums takes about as long as that many tiles.
+// queries and storing its sums takes about as long as that many tiles.  (With 1
+// and 3 instead of 2: 64 ragged sequences behind 8192 tokens 61.4 and 60.4 us
+// against 58.6, four canvases of 256 queries 57.0 and 47.5 against 46.7, nine small
+// groups 25.8 and 27.3 against 26.3.)
 constexpr int kItemCost = 2;
 // A CTA's time for a single tile in those of a pair's, as the CTAs are divided
-// between the two.
+// between the two.  (With 0.5, 0.7, 1.0: 120,000 shared tokens and short tails 84.6,
+// 73.6 and 75.7 us, nine small groups 27.6, 26.2 and 27.4.  Both kinds on every CTA, the
+// pairs first: 74.1 and 32.7.)
 constexpr float kSingleWeight = 0.7f;
 
 // Worker w's share of a region's `all` begins here.
@@ -795,8 +811,8 @@ struct Kernel {
     // and the next QK of stream 0, then of stream 1.  That keeps the streams half
     // a period apart, one's softmax under the other's MMAs; two issuers drift
     // into step and leave the tensor cores idle during both softmaxes
-    // (4400 cycles a pair tile, against 2048 of MMAs).  Single items' streams are
-    // independent and bound by their loads; each has its own issuer.
+    // (4400 cycles a pair tile instead of 3000; its MMAs take 2048).  Single items'
+    // streams are independent and bound by their loads; each has its own issuer.
     static __device__ void issuer(const AttnArgs &p, Shared &s, uint8_t *qbuf, uint8_t *ring,
                                   int stream)
     {
@@ -1208,7 +1224,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
 // values.  A warp has 16 of those and every SPLIT-th piece, kBatch pieces'
 // loads in flight; the SPLIT parts are added up at the end, in a fixed order.
 // Few rows can have many pieces (one long prefix cut for every CTA), many rows
-// have few: SPLIT is 4 up to kJoinFewRows rows in all and 1 above.
+// have few: SPLIT is 4 up to kJoinFewRows rows in all and 1 above.  (Both kernels with
+// SPLIT 4 and 1: 1024 rows of 120,000 shared tokens 72 and 93 us, 1024 of 64 ragged sequences 59
+// and 65, some 5000 of nine small groups 28.0 and 26.2, 16384 of four canvases 60 and 47.)
 constexpr int kJoinFewRows = 4096;
 template <int D, int SPLIT> constexpr int kJoinSides = 8 / SPLIT < D / 16 ? 8 / SPLIT : D / 16;
 

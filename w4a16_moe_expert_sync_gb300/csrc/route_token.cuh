@@ -1,6 +1,5 @@
 // route_token.cuh -- the router's arithmetic for one token, shared by the
-// router, the fused alignment and the few-token layer (bit-identical ids and
-// weights in all of them).
+// router and the fused alignment (bit-identical ids and weights in both).
 #pragma once
 
 #include <cfloat>
