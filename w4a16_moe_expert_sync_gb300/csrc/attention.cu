@@ -1234,7 +1234,7 @@ template <int D, bool BF16, int SPLIT>
 __global__ void __launch_bounds__(32 * SPLIT *kJoinSides<D, SPLIT>, SPLIT == 1 ? 3 : 2)
     attn_join_kernel(const __grid_constant__ AttnArgs p)
 {
-    constexpr int kBatch = SPLIT == 1 ? 2 : 4, kSides = kJoinSides<D, SPLIT>;
+    constexpr int kBatch = SPLIT == 1 ? 2 : 3, kSides = kJoinSides<D, SPLIT>;
     __shared__ float4 so[SPLIT][4][kSides][32];
     __shared__ float2 sm[SPLIT][kSides][32];
     pdl_wait();
@@ -1248,9 +1248,11 @@ __global__ void __launch_bounds__(32 * SPLIT *kJoinSides<D, SPLIT>, SPLIT == 1 ?
         const int i = min(i0 + lane, n - 1), head = i / rows, row = i - head * rows;
         float m = -INFINITY, l = 0.0f;
         float4 o[4] = {};
-#pragma unroll
+        // (the loop and the batches stay small: the kernel is short enough for the
+        // fetching of its instructions to show)
+#pragma unroll 1
         for (int k = 0; k < 2; k++) {          // the prefix's pieces, the sequence's own
-            const Entry &en = j.e[k];
+            const Entry en = k ? j.e[1] : j.e[0];
             if (en.span == 0)
                 continue;
             const int er = row + en.row, step = en.pair ? 2 * kRows : kRows;
