@@ -28,13 +28,14 @@
 // runs the tensor cores work for the other.
 //
 // Bounds and measured times (GB300, both kernels, back to back in a graph):
-//   32 questions about 120,000 shared tokens, 32/4 heads of 128: 72 us; 257 MB
+//   32 questions about 120,000 shared tokens, 32/4 heads of 128: 69 us; 257 MB
 //     (38 us at the copy bandwidth), 63 GFLOP (32 us).  The pairs' loop takes
-//     some 3000 cycles a tile against 2048 of MMAs: a stream's S, softmax, P and
-//     O follow one another, and two streams do not quite cover it
-//   64 sequences of 33 to 1500 tokens behind 8192: 59 us; 242 MB (36 us).  Plan 4 us,
+//     some 3000 cycles a tile; its MMAs take 2048, and so do the 256 KB that it
+//     moves through shared memory (their operands, and K and V as they land).
+//     Without the exponentials it is no faster: the softmax does not pace it
+//   64 sequences of 33 to 1500 tokens behind 8192: 58 us; 242 MB (36 us).  Plan 4 us,
 //     first tile 6, change of piece 1.5 each, join and its launch 6
-//   four times 256 queries over 4096 + 256: 47 us; 37 GFLOP (19 us), the pairs' loop
+//   four times 256 queries over 4096 + 256: 46 us; 37 GFLOP (19 us), the pairs' loop
 //   two sequences of 240 tokens: 14 us, all of it plan, one tile and join
 #include <algorithm>
 #include <atomic>

@@ -9,7 +9,7 @@
 // the pool's front stays dense.  Finding them is a scan of refs by one CTA
 // (4096 pages a round, 7 to 10 us for a few thousand pages); the rest are plain
 // grid-wide copies, bound by HBM.  Measured on GB300, against the bytes at the copy
-// bandwidth: whole pages 1.47 GB in 244 us (217) and 2.61 GB in 417 us (385, with the
+// bandwidth: whole pages 1.47 GB in 232 us (217) and 2.61 GB in 382 us (385, with the
 // plan and the table); releasing, reserving and filling 48 prompts, 574 MB, 97 us (85);
 // releasing and forking 96 drafts, 271 MB, 40 us (40).
 #include <algorithm>
@@ -330,10 +330,13 @@ __global__ void __launch_bounds__(256) kv_fork_kernel(uint8_t *cache, int64_t pa
 
 // ------------------------------------------------------------- copy pages
 // Whole pages by bulk copies through shared memory: one warp a CTA walks its
-// chunks of at most 16 KB, lane 0 issuing; the loads run kAhead chunks before
+// chunks of at most 32 KB, lane 0 issuing; the loads run kAhead chunks before
 // the stores, and a slot is loaded again once its store has read it.  No value
-// passes through registers, so two warps an SM keep 2 x 96 KB under way.
-constexpr int kSlots = 6, kAhead = 3, kChunk = 16 * 1024;
+// passes through registers, so two warps an SM keep 2 x 96 KB under way.  (1.47 GB
+// and 2.61 GB: six slots of 16 KB, three ahead, 245 and 418 us; six, one ahead 264 and
+// 451; three of 32 KB, two ahead 241 and 400, one ahead 232 and 382; two of 48 KB 239
+// and 401; one warp an SM, three of 64 KB 244 and 406.)
+constexpr int kSlots = 3, kAhead = 1, kChunk = 32 * 1024;
 
 __device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes)
 {
