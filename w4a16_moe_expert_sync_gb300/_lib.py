@@ -731,12 +731,16 @@ def _kv_pool(pool, P):
     return pool.numel() * 2 // max(P * page_bytes, 1), page_bytes, page
 
 
-def _kv_lists(*ts):
+def _kv_lists(first, *others):
     """The length of equally long int32 lists."""
-    _require_int32(*ts)
-    if any(t.dim() != 1 or t.shape != ts[0].shape for t in ts):
+    _require_int32(first, *others)
+    shape = first.shape
+    if len(shape) != 1:
         raise ValueError("slots and page lists must be one-dimensional and equally long")
-    return ts[0].shape[0]
+    for t in others:
+        if t.shape != shape:
+            raise ValueError("slots and page lists must be one-dimensional and equally long")
+    return shape[0]
 
 
 def _kv_workspace(workspace, P, n, device):
@@ -802,7 +806,8 @@ def w4_kv_compact(pool, table, refs, table_out=None, refs_out=None, workspace=No
     table_out = table if table_out is None else table_out
     refs_out = refs if refs_out is None else refs_out
     _require_int32(table, refs, table_out, refs_out, dev_status)
-    if table.dim() != 2 or refs.dim() != 1 or table_out.shape != table.shape or refs_out.shape != refs.shape:
+    if table.dim() != 2 or refs.dim() != 1 or table_out.shape != table.shape or \
+            refs_out.shape != refs.shape:
         raise ValueError("table_out and refs_out must have the shapes of table and refs")
     B, W = table.shape
     P = refs.shape[0]
@@ -897,7 +902,8 @@ def w4_attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets, group_off
         workspace = torch.empty(
             max(w4_attn_shared_prefix_workspace_size(T, B, G, max_q, Hq, Hkv, D), 256)
             if Hkv and Hq % Hkv == 0 else 256, dtype=torch.uint8, device=q.device)
-    _require_cuda(workspace)
+    else:
+        _require_cuda(workspace)
     _check(load_library().w4_attn_shared_prefix(
         q.data_ptr(), qs[0], qs[1], k_pages.data_ptr(), v_pages.data_ptr(), *strides[:3], P, page,
         table.data_ptr(), W, lens.data_ptr(), q_offsets.data_ptr(), T, B, max_q,
