@@ -243,6 +243,27 @@ def test_strided_inputs_other_stream_and_graph(lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("D", [64, 128])
+def test_layouts_of_the_pages(lib, page, D):
+    """Heads inside the tokens, outside them, outside them in a wider pool, and
+    tokens wider than their heads: the same values, the same result."""
+    import torch
+    c = _build([450, 20, 470, 300], [2, 1, 3, 1], [3], [17], 8, 4, D, page, "bfloat16", seed=page)
+    want = _run(lib, c, True)
+    _check(want, c, True)
+    P, Hkv = c["cache"].shape[1], 4
+    outside = c["cache"].transpose(2, 3).contiguous().transpose(2, 3)
+    wider = torch.full((2, P, Hkv + 2, page, D), float("nan"), device="cuda").bfloat16()
+    wider = wider[:, :, 1:1 + Hkv].transpose(2, 3)
+    tokens = torch.full((2, P, page, Hkv + 1, D), float("nan"), device="cuda").bfloat16()[:, :, :, 1:]
+    apart = torch.full((2, P, page, Hkv, D + 8), float("nan"), device="cuda").bfloat16()[..., :D]
+    for x in (outside, wider, tokens, apart):
+        x.copy_(c["cache"])
+        assert torch.equal(_run(lib, dict(c, cache=x), True), want)
+
+
+@pytest.mark.gpu
 def test_bad_inputs_on_the_device_are_flagged(lib):
     import torch
     good = _build([100, 90, 80], [1, 1, 1], [], [], 4, 2, 64, 16, "bfloat16", seed=6)

@@ -87,8 +87,20 @@ struct Seg {
     int piece;                             // where its sums go; -1: nowhere
 };
 
+// How TMA sees the pages.  kRows: values, tokens, heads, pages; a box is 64 values of
+// each of a page's tokens, and the 64-value blocks of a K or V tile lie one after the
+// other.  Pages of kShortPage tokens with more than one such block have a box with all
+// of them, which lie in turn there, 8 tokens each: half as many boxes.  (128 sequences
+// of 6000 tokens in pages of 16, heads of 128: 104 us by kRows, 87 like this; larger
+// pages gain nothing.)  The axes are then 64 values, 8 tokens, blocks, the page's groups
+// of 8 tokens and one more: with the heads side by side their blocks are one axis, with
+// the heads of all pages evenly spaced they are one axis with the pages; else
+// (kGroups) a box is 8 tokens.
+enum class PageView { kRows, kHeadsAsBlocks, kHeadsAsPages, kGroups };
+constexpr int kShortPage = 16;
+
 struct AttnArgs {
-    CUtensorMap k_map, v_map;              // [P][Hkv][page][D], box 1 x 1 x page x 64
+    CUtensorMap k_map, v_map;              // see PageView
     const uint16_t *q;
     uint16_t *out;
     const int32_t *table, *lens, *q_offsets, *group_offsets, *shared;
@@ -103,6 +115,7 @@ struct AttnArgs {
     float scale_log2;
     uint64_t wait_ns;
     int T, B, G, W, P, page, page_shift, Hq, Hkv, rep, max_q, causal;
+    PageView view;
     int rows_b;                            // a sequence's single item's rows at most
     int cap_a, cap_g, cap_b;               // pieces that the workspace holds; cap_b: all single
 };
@@ -193,16 +206,28 @@ __device__ __forceinline__ void mma_ss_elect(uint32_t d, uint64_t a, uint64_t b,
 
 // A 128-byte-swizzled operand whose contiguous axis is N (V: a token's
 // values): 64 values x 8 tokens to an atom of 1024 bytes, 8-token groups
-// 1024 bytes apart, 64-value blocks `block` bytes apart.
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t addr, uint32_t block)
+// `group` bytes apart, 64-value blocks `block` bytes apart.  It does for K as well,
+// whose contiguous axis is the contraction: there blocks are operands of their own.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t addr, uint32_t group, uint32_t block)
 {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
     d |= static_cast<uint64_t>(block >> 4) << 16;
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(group >> 4) << 32;
     d |= static_cast<uint64_t>(1) << 46;
     d |= static_cast<uint64_t>(2) << 61;
     return d;
+}
+
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                            int u, int v, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v),
+        "r"(smem_u32(bar))
+        : "memory");
 }
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z,
@@ -423,10 +448,14 @@ __device__ __forceinline__ int find_entry(const int *start, int n, int x)
     return lo;
 }
 
-template <int D, bool BF16>
+// IN_TURN: a K or V tile's blocks of 64 values lie in turn (see PageView).
+template <int D, bool BF16, bool IN_TURN>
 struct Kernel {
     static constexpr int kBlocks = D / 64;                     // 128-byte column blocks
     static constexpr int kTileBytes = kKeys * D * 2;           // a K, V or Q tile
+    // bytes from 8 of a K or V tile's tokens to the next, from a block to the next
+    static constexpr int kGroup = IN_TURN ? 1024 * kBlocks : 1024;
+    static constexpr int kBlock = IN_TURN ? 1024 : kKeys * 128;
     static constexpr int kSlots = 160 * 1024 / kTileBytes;
     static constexpr int kQBytes = 2 * kTileBytes;
     static constexpr int kRingBytes = kSlots * kTileBytes;
@@ -666,11 +695,25 @@ struct Kernel {
             *static_cast<volatile int *>(&s.requested) = fill + 1;
         }
         __syncwarp();
-        const int boxes = kKeys / p.page * kBlocks;
-        const int pg = __shfl_sync(0xffffffffu, page_id, lane / kBlocks);
-        if (lane < boxes)
-            tma_load_4d(dst + (lane % kBlocks) * (kKeys * 128) + (lane / kBlocks) * p.page * 128,
-                        map, (lane % kBlocks) * 64, 0, head, pg, &s.full[slot]);
+        if constexpr (IN_TURN) {
+            const int tok = p.view == PageView::kGroups ? lane * 8 : lane << p.page_shift;
+            const int pg = __shfl_sync(0xffffffffu, page_id, (tok & (kKeys - 1)) >> p.page_shift);
+            uint8_t *to = dst + tok / 8 * kGroup;
+            if (tok >= kKeys)
+                ;
+            else if (p.view == PageView::kHeadsAsBlocks)
+                tma_load_5d(to, map, 0, 0, head * kBlocks, 0, pg, &s.full[slot]);
+            else if (p.view == PageView::kHeadsAsPages)
+                tma_load_5d(to, map, 0, 0, 0, 0, pg * p.Hkv + head, &s.full[slot]);
+            else
+                tma_load_5d(to, map, 0, tok & (p.page - 1), 0, head, pg, &s.full[slot]);
+        } else {
+            const int boxes = kKeys / p.page * kBlocks;
+            const int pg = __shfl_sync(0xffffffffu, page_id, lane / kBlocks);
+            if (lane < boxes)
+                tma_load_4d(dst + (lane % kBlocks) * kBlock + (lane / kBlocks) * p.page * 128, map,
+                            (lane % kBlocks) * 64, 0, head, pg, &s.full[slot]);
+        }
     }
 
     // The id of this lane's page of tile t: P, which reads as zeros, past the
@@ -766,12 +809,11 @@ struct Kernel {
         tc_fence_after();
         __syncwarp();
         const uint64_t qd = sdesc_sw128(smem_u32(qbuf + stream * kTileBytes));
-        const uint64_t kd = sdesc_sw128(smem_u32(ring + slot * kTileBytes));
+        const uint64_t kd = sdesc_mn_sw128(smem_u32(ring + slot * kTileBytes), kGroup, kBlock);
 #pragma unroll
-        for (int k = 0; k < D / 16; k++) {
-            const int off = (k / 4) * (kKeys * 128 >> 4) + (k % 4) * 2;
-            mma_ss_elect(s.tmem + kS + 128 * stream, qd + off, kd + off, kQk, k > 0);
-        }
+        for (int k = 0; k < D / 16; k++)
+            mma_ss_elect(s.tmem + kS + 128 * stream, qd + (k / 4) * (kRows * 128 >> 4) + k % 4 * 2,
+                         kd + (k / 4) * (kBlock >> 4) + k % 4 * 2, kQk, k > 0);
         tc_commit_elect(&s.s_full[stream]);
         if (last_use)
             tc_commit_elect(&s.empty[slot]);
@@ -788,15 +830,15 @@ struct Kernel {
         __syncwarp();
         const uint32_t va = smem_u32(ring + slot * kTileBytes);
         const uint32_t ts = s.tmem + kS + 128 * stream, to = s.tmem + kO + D * stream;
-        const uint64_t vd = sdesc_mn_sw128(va, kKeys * 128);
+        const uint64_t vd = sdesc_mn_sw128(va, kGroup, kBlock);
         if (before <= 0 && keys > kKeys - 16) {
 #pragma unroll
             for (int k = 0; k < kKeys / 16; k++)
-                tc_mma_ts_elect(to, ts + 8 * k, vd + k * (2048 >> 4), kPv, !first || k > 0);
+                tc_mma_ts_elect(to, ts + 8 * k, vd + k * (2 * kGroup >> 4), kPv, !first || k > 0);
         } else {
             const int begin = max(before, 0) / 16, end = (min(keys, kKeys) + 15) / 16;
             for (int k = begin; k < end; k++)
-                tc_mma_ts_elect(to, ts + 8 * k, vd + k * (2048 >> 4), kPv, !first || k > begin);
+                tc_mma_ts_elect(to, ts + 8 * k, vd + k * (2 * kGroup >> 4), kPv, !first || k > begin);
         }
         if (last_use)
             tc_commit_elect(&s.empty[slot]);
@@ -1112,8 +1154,9 @@ struct Kernel {
         auto clear = [&](int from, int to) {
             for (int i = at; i < (to - from) * 8 * kBlocks; i += step) {
                 const int row = from + i / (8 * kBlocks), c = i % (8 * kBlocks);
-                *reinterpret_cast<uint4 *>(v + (c / 8) * (kKeys * 128) + row * 128 +
-                                           (c % 8) * 16) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(v + (c / 8) * kBlock + (row / 8) * kGroup +
+                                           (row % 8) * 128 + (c % 8) * 16) =
+                    make_uint4(0, 0, 0, 0);
             }
         };
         if (before > 0)
@@ -1159,10 +1202,10 @@ struct Kernel {
     }
 };
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool IN_TURN>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ AttnArgs p)
 {
-    using K = Kernel<D, BF16>;
+    using K = Kernel<D, BF16, IN_TURN>;
     extern __shared__ __align__(1024) uint8_t raw[];
     __shared__ __align__(16) typename K::Shared s;
     uint8_t *qbuf = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -1368,17 +1411,38 @@ EncodeFn encode_fn()
     return fn;
 }
 
-bool encode_pages(CUtensorMap *map, const AttnProblem &q, const uint16_t *base)
+PageView view_of(const AttnProblem &q)
 {
-    const cuuint64_t dim[4] = {static_cast<cuuint64_t>(q.D), static_cast<cuuint64_t>(q.page),
-                               static_cast<cuuint64_t>(q.Hkv), static_cast<cuuint64_t>(q.P)};
-    const cuuint64_t stride[3] = {static_cast<cuuint64_t>(q.tok_stride) * 2,
-                                  static_cast<cuuint64_t>(q.head_stride) * 2,
-                                  static_cast<cuuint64_t>(q.page_stride) * 2};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(q.page), 1, 1};
-    const cuuint32_t step[4] = {1, 1, 1, 1};
+    if (q.page > kShortPage || q.D == 64)
+        return PageView::kRows;
+    if (q.head_stride == q.D)
+        return PageView::kHeadsAsBlocks;
+    if (q.page_stride == q.Hkv * q.head_stride &&
+        (static_cast<int64_t>(q.P) + 1) * q.Hkv < (1ll << 31))
+        return PageView::kHeadsAsPages;
+    return PageView::kGroups;
+}
+
+// What lies past the last page reads as zeros.
+bool encode_pages(CUtensorMap *map, const AttnProblem &q, PageView view, const uint16_t *base)
+{
+    const bool rows = view == PageView::kRows, heads = view == PageView::kHeadsAsBlocks;
+    const bool groups = view == PageView::kGroups, together = view == PageView::kHeadsAsPages;
+    const cuuint64_t tok = static_cast<cuuint64_t>(q.tok_stride) * 2;
+    const cuuint64_t head = static_cast<cuuint64_t>(q.head_stride) * 2;
+    const cuuint64_t page = static_cast<cuuint64_t>(q.page_stride) * 2;
+    const cuuint64_t P = q.P, Hkv = q.Hkv, size = q.page, D = q.D, blocks = D / 64;
+    const cuuint64_t dim4[4] = {D, size, Hkv, P}, stride4[3] = {tok, head, page};
+    const cuuint32_t box4[4] = {64, static_cast<cuuint32_t>(size), 1, 1};
+    const cuuint64_t dim5[5] = {64, groups ? size : 8, heads ? Hkv * blocks : blocks,
+                                groups ? Hkv : size / 8, together ? P * Hkv : P};
+    const cuuint64_t stride5[4] = {tok, 128, groups ? head : 8 * tok, together ? head : page};
+    const cuuint32_t box5[5] = {64, 8, static_cast<cuuint32_t>(blocks),
+                                groups ? 1u : static_cast<cuuint32_t>(size / 8), 1};
+    const cuuint32_t step[5] = {1, 1, 1, 1, 1};
     return encode_fn()(map, q.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                       4, const_cast<uint16_t *>(base), dim, stride, box, step,
+                       rows ? 4 : 5, const_cast<uint16_t *>(base), rows ? dim4 : dim5,
+                       rows ? stride4 : stride5, rows ? box4 : box5, step,
                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1422,11 +1486,11 @@ Space space_of(int T, int B, int G, int max_q, int Hq, int Hkv, int D)
     return s;
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool IN_TURN>
 cudaError_t launch_variant(const AttnArgs &a, int dev, int sms, cudaStream_t stream)
 {
-    using K = Kernel<D, BF16>;
-    auto kern = attn_kernel<D, BF16>;
+    using K = Kernel<D, BF16, IN_TURN>;
+    auto kern = attn_kernel<D, BF16, IN_TURN>;
     static std::atomic<uint64_t> raised{0};      // devices whose limit is raised already
     cudaError_t err;
     if (!(raised.load(std::memory_order_relaxed) >> (dev & 63) & 1u)) {
@@ -1466,7 +1530,9 @@ cudaError_t launch_attn(const AttnProblem &q, cudaStream_t stream)
     AttnArgs a{};
     if (!encode_fn())
         return cudaErrorNotSupported;
-    if (!encode_pages(&a.k_map, q, q.k_pages) || !encode_pages(&a.v_map, q, q.v_pages))
+    a.view = view_of(q);
+    if (!encode_pages(&a.k_map, q, a.view, q.k_pages) ||
+        !encode_pages(&a.v_map, q, a.view, q.v_pages))
         return cudaErrorInvalidValue;
     const Space s = space_of(q.T, q.B, q.G, q.max_q, q.Hq, q.Hkv, q.D);
     uint8_t *ws = static_cast<uint8_t *>(q.workspace);
@@ -1504,11 +1570,14 @@ cudaError_t launch_attn(const AttnProblem &q, cudaStream_t stream)
     a.rep = q.Hq / q.Hkv;
     a.max_q = q.max_q;
     a.causal = q.causal;
+    if (a.view != PageView::kRows)             // D is 128
+        return q.bf16 ? launch_variant<128, true, true>(a, dev, sms, stream)
+                      : launch_variant<128, false, true>(a, dev, sms, stream);
     if (q.D == 128)
-        return q.bf16 ? launch_variant<128, true>(a, dev, sms, stream)
-                      : launch_variant<128, false>(a, dev, sms, stream);
-    return q.bf16 ? launch_variant<64, true>(a, dev, sms, stream)
-                  : launch_variant<64, false>(a, dev, sms, stream);
+        return q.bf16 ? launch_variant<128, true, false>(a, dev, sms, stream)
+                      : launch_variant<128, false, false>(a, dev, sms, stream);
+    return q.bf16 ? launch_variant<64, true, false>(a, dev, sms, stream)
+                  : launch_variant<64, false, false>(a, dev, sms, stream);
 }
 
 }  // namespace w4
