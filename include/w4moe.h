@@ -710,15 +710,16 @@ int w4_attn_shared_prefix(const uint16_t *q, int64_t q_tok_stride, int64_t q_hea
                           w4_stream_t stream);
 
 /* --------------------------------------------------------------------------
- * w4_test_pipeline_hooks -- a test hook of the grouped GEMMs (not for
- * production use): for later w4_grouped_gemm_gate_up / _down / _down_combine
- * calls and the layer's GEMMs made from the calling thread, every pipeline
- * wait gives up after wait_limit_ns (0: back to the default of one second)
- * and, if withhold_first_scales is nonzero, each CTA withholds the copy of
- * its first unit's scales and zeros, so that its waits run out: the kernel
- * then sets W4_DEV_PIPELINE_TIMEOUT, lets its own copies land, drains its
- * MMAs, frees its tensor memory and exits, leaving its outputs incomplete
- * and the context usable.  Returns W4_OK.
+ * w4_test_pipeline_hooks -- a test hook of the grouped GEMMs and attention (not
+ * for production use): for later w4_grouped_gemm_gate_up / _down /
+ * _down_combine calls, the layer's GEMMs and w4_attn_shared_prefix called from
+ * the calling thread, every pipeline wait gives up after wait_limit_ns (0: back
+ * to the default of one second) and, if withhold_first_scales is nonzero, each
+ * CTA withholds the copy of its first unit's scales and zeros (attention: never
+ * counts its first K tile as landed), so that its waits run out: the kernel then sets
+ * W4_DEV_PIPELINE_TIMEOUT, lets its own copies land, drains its MMAs, frees its
+ * tensor memory and exits, leaving its outputs incomplete and the context
+ * usable.  Returns W4_OK.
  * ------------------------------------------------------------------------ */
 int w4_test_pipeline_hooks(uint64_t wait_limit_ns, int withhold_first_scales);
 

@@ -114,6 +114,7 @@ struct AttnArgs {
     int64_t q_tok, q_head;
     float scale_log2;
     uint64_t wait_ns;
+    int withhold;                          // test hook: slot 0's barrier never completes
     int T, B, G, W, P, page, page_shift, Hq, Hkv, rep, max_q, causal;
     PageView view;
     int rows_b;                            // a sequence's single item's rows at most
@@ -466,7 +467,7 @@ struct Kernel {
 
     struct Shared {
         alignas(8) uint64_t full[kSlots], empty[kSlots];
-        uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2], drained[2];
+        uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2], cleared, drained[2];
         uint32_t tmem;
         int abort_flag;
         int requested;                         // fills requested of the ring so far
@@ -637,6 +638,10 @@ struct Kernel {
         return r + (which == 0 ? min(r, s.tiles[1]) : min(r + 1, s.tiles[0]));
     }
 
+    // Every wait has a limit.  A role whose wait gives up, by the limit or because
+    // another's has, returns without a further copy, MMA or store; what is under
+    // way by then is awaited before tensor memory is freed and the CTA ends (issuer,
+    // softmax, land).
     static __device__ __forceinline__ bool wait(const AttnArgs &p, Shared &s, uint64_t *bar,
                                                 uint32_t parity)
     {
@@ -649,27 +654,29 @@ struct Kernel {
     // yet to land; by its parity alone that would pass for landed.  Hence first
     // the count of fills requested: when this one has been, the slot's last has
     // been used, and the parity says what it means.
-    static __device__ __forceinline__ void wait_full(const AttnArgs &p, Shared &s, int fill)
+    static __device__ __forceinline__ bool wait_full(const AttnArgs &p, Shared &s, int fill)
     {
-        volatile int *requested = &s.requested;
+        volatile int *requested = &s.requested, *abort_flag = &s.abort_flag;
         if (!__all_sync(0xffffffffu, *requested > fill)) {
             const uint64_t t0 = global_timer_ns();
             for (uint32_t it = 1; !__all_sync(0xffffffffu, *requested > fill); it++) {
                 __nanosleep(20);
                 if ((it & 63u) == 0) {
+                    if (__any_sync(0xffffffffu, *abort_flag != 0))
+                        return false;
                     const bool late = global_timer_ns() - t0 > p.wait_ns;
                     if (__any_sync(0xffffffffu, late)) {
                         if ((threadIdx.x & 31) == 0) {
-                            s.abort_flag = 1;
+                            *abort_flag = 1;
                             if (p.status)
                                 atomicOr(p.status, kDevPipelineTimeout);
                         }
-                        return;
+                        return false;
                     }
                 }
             }
         }
-        wait(p, s, &s.full[fill % kSlots], (fill / kSlots) & 1);
+        return wait(p, s, &s.full[fill % kSlots], (fill / kSlots) & 1);
     }
 
     // One look at whether fill `fill` has landed.
@@ -681,13 +688,13 @@ struct Kernel {
     }
 
     // ------------------------------------------------------------- loading
-    static __device__ void load_slot(const AttnArgs &p, Shared &s, uint8_t *ring, int fill,
+    static __device__ bool load_slot(const AttnArgs &p, Shared &s, uint8_t *ring, int fill,
                                      const CUtensorMap *map, int head, int page_id,
                                      int lane)
     {
         const int slot = fill % kSlots, use = fill / kSlots;
-        if (use > 0)
-            wait(p, s, &s.empty[slot], (use - 1) & 1);
+        if (use > 0 && !wait(p, s, &s.empty[slot], (use - 1) & 1))
+            return false;
         uint8_t *dst = ring + slot * kTileBytes;
         if (lane == 0) {
             mbar_arrive_expect_tx(&s.full[slot], kTileBytes);
@@ -713,6 +720,19 @@ struct Kernel {
             if (lane < boxes)
                 tma_load_4d(dst + (lane % kBlocks) * kBlock + (lane / kBlocks) * p.page * 128, map,
                             (lane % kBlocks) * 64, 0, head, pg, &s.full[slot]);
+        }
+        return true;
+    }
+
+    // Every fill requested has landed, or had its time to: a slot is requested anew
+    // only after its last fill was used, so only the last of each can be under way.
+    // One warp, once no role requests any more.
+    static __device__ void land(Shared &s)
+    {
+        const int n = s.requested;
+        for (int slot = 0; slot < min(n, kSlots); slot++) {
+            const int fill = (n - 1 - slot) / kSlots * kSlots + slot;
+            mbar_drain(&s.full[slot], (fill / kSlots) & 1);
         }
     }
 
@@ -790,8 +810,9 @@ struct Kernel {
                 }
             }
             if (held) {
-                load_slot(p, s, ring, 2 * fill, &p.k_map, held_head, held_id, lane);
-                load_slot(p, s, ring, 2 * fill + 1, &p.v_map, held_head, held_id, lane);
+                if (!load_slot(p, s, ring, 2 * fill, &p.k_map, held_head, held_id, lane) ||
+                    !load_slot(p, s, ring, 2 * fill + 1, &p.v_map, held_head, held_id, lane))
+                    return;
                 fill++;
             }
             more = held = got;
@@ -856,8 +877,8 @@ struct Kernel {
     // into step and leave the tensor cores idle during both softmaxes
     // (4400 cycles a pair tile instead of 3000; its MMAs take 2048).  Single items'
     // streams are independent and bound by their loads; each has its own issuer.
-    static __device__ void issuer(const AttnArgs &p, Shared &s, uint8_t *qbuf, uint8_t *ring,
-                                  int stream)
+    static __device__ __forceinline__ void issue_all(const AttnArgs &p, Shared &s, uint8_t *qbuf,
+                                                     uint8_t *ring, int stream)
     {
         uint32_t seg_phase = 0, tile_phase = 0;
         if (stream == 0) {
@@ -867,22 +888,27 @@ struct Kernel {
                 const int tiles = g.tiles, base = g.kbase + g.tile0 * kKeys;
                 if (tiles == 0)
                     continue;
-                wait_full(p, s, 2 * r);
+                if (!wait_full(p, s, 2 * r))
+                    return;
                 for (int st = 0; st < 2; st++) {
-                    wait(p, s, &s.q_ready[st], seg_phase);
+                    if (!wait(p, s, &s.q_ready[st], seg_phase))
+                        return;
                     issue_qk(p, s, qbuf, ring, st, 2 * r, st == 1);
                 }
                 seg_phase ^= 1;
                 for (int t = 0; t < tiles; t++, r++) {
-                    wait_full(p, s, 2 * r + 1);
+                    if (!wait_full(p, s, 2 * r + 1))
+                        return;
                     bool here = t + 1 < tiles && landed(s, 2 * r + 2);
                     for (int st = 0; st < 2; st++) {
-                        wait(p, s, &s.p_ready[st], tile_phase);
+                        if (!wait(p, s, &s.p_ready[st], tile_phase))
+                            return;
                         const int at = base + t * kKeys;
                         issue_pv(p, s, ring, st, 2 * r + 1, g.k0 - at, g.k1 - at, t == 0,
                                  t == tiles - 1, st == 1);
                         if (t + 1 < tiles && !here) {
-                            wait_full(p, s, 2 * r + 2);
+                            if (!wait_full(p, s, 2 * r + 2))
+                                return;
                             here = true;
                         }
                         if (t + 1 < tiles)
@@ -898,24 +924,33 @@ struct Kernel {
             const int tiles = g.tiles, base = g.kbase + g.tile0 * kKeys;
             if (tiles == 0)
                 continue;
-            wait(p, s, &s.q_ready[stream], seg_phase);
+            if (!wait(p, s, &s.q_ready[stream], seg_phase))
+                return;
             seg_phase ^= 1;
             for (int t = 0; t < tiles; t++, r++) {
                 const int fill = 2 * fill_of(s, stream, r);
-                wait_full(p, s, fill);
+                if (!wait_full(p, s, fill))
+                    return;
                 issue_qk(p, s, qbuf, ring, stream, fill, true);
-                wait_full(p, s, fill + 1);
-                wait(p, s, &s.p_ready[stream], tile_phase);
+                if (!wait_full(p, s, fill + 1) || !wait(p, s, &s.p_ready[stream], tile_phase))
+                    return;
                 tile_phase ^= 1;
                 const int at = base + t * kKeys;
                 issue_pv(p, s, ring, stream, fill + 1, g.k0 - at, g.k1 - at, t == 0,
                          t == tiles - 1, true);
             }
         }
+    }
+
+    static __device__ void issuer(const AttnArgs &p, Shared &s, uint8_t *qbuf, uint8_t *ring,
+                                  int stream)
+    {
+        issue_all(p, s, qbuf, ring, stream);
         // nothing of this warp's is under way when the CTA ends
         __syncwarp();
         tc_commit_elect(&s.drained[stream]);
-        wait(p, s, &s.drained[stream], 0);
+        mbar_drain(&s.drained[stream], 0);
+        __syncwarp();
     }
 
     // ------------------------------------------------------------- softmax
@@ -924,12 +959,20 @@ struct Kernel {
     static __device__ void softmax(const AttnArgs &p, Shared &s, uint8_t *qbuf, uint8_t *ring,
                                    int stream)
     {
+        if (!all_pieces(p, s, qbuf, ring, stream))
+            cp_async_wait_all();               // queries on their way
+    }
+
+    // False once a wait has given up.
+    static __device__ __forceinline__ bool all_pieces(const AttnArgs &p, Shared &s, uint8_t *qbuf,
+                                                      uint8_t *ring, int stream)
+    {
         const int tid = threadIdx.x & 127, warp = tid >> 5;
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
         const uint32_t ts = s.tmem + lanes + kS + 128 * stream;
         const uint32_t to = s.tmem + lanes + kO + D * stream;
         uint8_t *q = qbuf + stream * kTileBytes;
-        uint32_t s_phase = 0, o_phase = 0;
+        uint32_t s_phase = 0, o_phase = 0, clear_phase = 0;
         // a CTA has pairs, or each stream its own single items
         const bool pair = s.segs[2] > 0;
         const int which = pair ? 2 : stream, count = s.segs[which];
@@ -978,7 +1021,8 @@ struct Kernel {
             float m = -INFINITY, l = 0.0f;     // m in units of log2
             int base = g.kbase + g.tile0 * kKeys;
             for (int t = 0; t < g.tiles; t++, r++, base += kKeys) {
-                wait(p, s, &s.s_full[stream], s_phase);
+                if (!wait(p, s, &s.s_full[stream], s_phase))
+                    return false;
                 s_phase ^= 1;
                 tc_fence_after();
                 if (t == g.tiles - 1 && another) {
@@ -990,9 +1034,10 @@ struct Kernel {
                 if (busy)
                     tile(p, ts, to, limit == INT_MAX ? 0 : g.k0 - base,
                          limit == INT_MAX ? kKeys : limit - base, t > 0, m, l);
-                if ((g.k1 - base < kKeys && (g.k1 & 15)) || (g.k0 > base && (g.k0 & 15)))
-                    clear_ends(p, s, ring, 2 * fill_of(s, which, r) + 1, g.k0 - base,
-                               g.k1 - base, pair, stream, tid);
+                if (((g.k1 - base < kKeys && (g.k1 & 15)) || (g.k0 > base && (g.k0 & 15))) &&
+                    !clear_ends(p, s, ring, 2 * fill_of(s, which, r) + 1, g.k0 - base,
+                                g.k1 - base, pair, stream, tid, clear_phase))
+                    return false;
                 // one arrival a warp: a thread's each would take a few cycles of the barrier
                 tc_fence_before();
                 __syncwarp();
@@ -1007,12 +1052,14 @@ struct Kernel {
                 hand_over(i + 1);
             }
             if (g.tiles > 0) {
-                wait(p, s, &s.o_full[stream], o_phase);
+                if (!wait(p, s, &s.o_full[stream], o_phase))
+                    return false;
                 o_phase ^= 1;
                 tc_fence_after();
             }
             store(p, g, pair, pair ? stream * kRows : 0, rows, to, m, l, tid);
         }
+        return true;
     }
 
     // A stream's rows of a piece.
@@ -1144,11 +1191,13 @@ struct Kernel {
     // these lie in: P is zero there, but memory nobody has written may hold NaN.
     // In a pair both streams clear, and wait for each other, before either uses
     // the tile.
-    static __device__ void clear_ends(const AttnArgs &p, Shared &s, uint8_t *ring, int fill,
-                                      int before, int valid, bool pair, int stream, int tid)
+    static __device__ bool clear_ends(const AttnArgs &p, Shared &s, uint8_t *ring, int fill,
+                                      int before, int valid, bool pair, int stream, int tid,
+                                      uint32_t &phase)
     {
         const int slot = fill % kSlots;
-        wait_full(p, s, fill);
+        if (!wait_full(p, s, fill))
+            return false;
         uint8_t *v = ring + slot * kTileBytes;
         const int at = pair ? stream * 128 + tid : tid, step = pair ? 256 : 128;
         auto clear = [&](int from, int to) {
@@ -1165,8 +1214,13 @@ struct Kernel {
             clear(valid, (valid + 15) & ~15);
         fence_proxy_async_smem();
         __syncwarp();
-        if (pair)
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (pair) {
+            mbar_arrive_elect(&s.cleared);
+            if (!wait(p, s, &s.cleared, phase))
+                return false;
+            phase ^= 1;
+        }
+        return true;
     }
 
     // A piece's sums: [D / 4][rows][4] floats, so that a warp's rows are
@@ -1214,7 +1268,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     if (tid == 0) {
         for (int i = 0; i < K::kSlots; i++) {
-            mbar_init(&s.full[i], 1);
+            mbar_init(&s.full[i], p.withhold && i == 0 ? 2 : 1);
             mbar_init(&s.empty[i], 1);
         }
         for (int i = 0; i < 2; i++) {
@@ -1224,6 +1278,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             mbar_init(&s.o_full[i], 1);
             mbar_init(&s.drained[i], 1);
         }
+        mbar_init(&s.cleared, 2 * kRows / 32);
         s.abort_flag = 0;
         s.requested = 0;
         fence_mbar_init();
@@ -1256,6 +1311,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     tc_fence_before();
     __syncthreads();
     if (warp == 8) {
+        if (*static_cast<volatile int *>(&s.abort_flag)) {
+            K::land(s);
+            __syncwarp();
+        }
         tc_fence_after();
         __syncwarp();
         tmem_dealloc(s.tmem, 512);
@@ -1558,6 +1617,7 @@ cudaError_t launch_attn(const AttnProblem &q, cudaStream_t stream)
     a.q_head = q.q_head;
     a.scale_log2 = q.scale * 1.4426950408889634f;
     a.wait_ns = pipeline_test_hooks().wait_ns;
+    a.withhold = pipeline_test_hooks().withhold_sz;
     a.T = q.T;
     a.B = q.B;
     a.G = q.G;

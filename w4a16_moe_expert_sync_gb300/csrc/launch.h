@@ -105,7 +105,8 @@ struct GroupedGemmProblem {
     bool test_withhold_sz = false;
 };
 
-// The test hooks of the calling thread, applied to its grouped GEMM launches.
+// The test hooks of the calling thread, applied to its launches of the kernels that
+// w4_test_pipeline_hooks names.
 struct PipelineTestHooks {
     uint64_t wait_ns = 1000000000ull;
     bool withhold_sz = false;

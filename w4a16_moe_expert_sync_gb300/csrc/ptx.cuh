@@ -182,6 +182,16 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, v
     return mbar_wait_warp_a(smem_u32(bar), parity, abort_flag, dev_status, timeout_bit, limit_ns);
 }
 
+// A wait for what this CTA itself has under way (a copy, MMAs), before it ends:
+// bounded, and whether or not the CTA has aborted.
+__device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity)
+{
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (global_timer_ns() - t0 > 200000000ull)
+            return;
+}
+
 // One arrival per warp, made by an elected lane without a branch (call with
 // the warp converged, after whatever the arrival must publish).
 __device__ __forceinline__ void mbar_arrive_elect_a(uint32_t bar)
