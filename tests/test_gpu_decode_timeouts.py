@@ -50,3 +50,12 @@ def test_attention(lib, hooks, lens, nqs, groups, shared, Hq, Hkv, D, page):
     from test_gpu_attention import _build, _run
     c = _build(lens, nqs, groups, shared, Hq, Hkv, D, page, "bfloat16", seed=7)
     _times_out(lib, hooks, lambda st: _run(lib, c, True, dev_status=st))
+
+
+@pytest.mark.parametrize("M,d,m,E,k", [(1, 128, 64, 1, 1), (7, 2816, 704, 16, 8), (32, 384, 192, 12, 8),
+                                       (3, 6144, 64, 4, 2)])
+def test_few_token_layer(lib, hooks, M, d, m, E, k):
+    from test_gpu_few import _inputs
+    x, logits, gu, dn = _inputs(M, d, m, E, k)
+    _times_out(lib, hooks,
+               lambda st: lib.w4_moe_layer_few_from_logits(x, logits, k, gu, dn, dev_status=st)[0])

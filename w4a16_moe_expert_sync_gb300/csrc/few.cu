@@ -63,6 +63,7 @@ struct FewArgs {
     uint16_t *out;                     // [M, d] bf16
     int32_t *dev_status;
     uint64_t wait_ns;
+    int withhold;                      // test hook: the rings' first stages never complete
     int M, d, m, E, k;                 // M <= the grid
     int scale_bytes;                   // a warp's ring of scales
     int cols;                          // activation columns that fit
@@ -299,11 +300,31 @@ __host__ __device__ constexpr int col_stride(int K, int G)
     return (2 * K + 4 * G + 127) / 128 * 128 + 64;
 }
 
-// The rest of a wait that its first try did not end, out of the hot loop.
-__device__ __noinline__ void wait_long(uint32_t bar, uint32_t phase, volatile int *abort_flag,
+// The rest of a wait that its first try did not end, out of the hot loop: for stage
+// `stage` of a ring whose next request goes to `ask`.  Once it has given up, by its
+// limit or because another warp's has, and what the ring has under way (all of it, if
+// stage is ask) has landed or had its time to, the warp is `gone`: nothing is requested
+// or awaited any more.  (Votes keep it uniform: a __syncwarp at its end, or the answer
+// returned, makes the caller's loop 10 KB longer and the layer 4 to 6 us slower.)
+__device__ __noinline__ void wait_long(uint64_t *full, int stage, int ask, uint32_t phase, int depth,
+                                       volatile int *gone, volatile int *abort_flag,
                                        int32_t *status, uint64_t limit_ns)
 {
-    mbar_wait_warp_a(bar, phase, abort_flag, status, kDevPipelineTimeout, limit_ns);
+    if (__any_sync(0xffffffffu, *gone != 0))
+        return;
+    if (mbar_wait_warp(full + stage, phase, abort_flag, status, kDevPipelineTimeout, limit_ns))
+        return;
+    const uint64_t t0 = global_timer_ns();
+    for (int n = ask > stage ? ask - stage : ask - stage + depth; n > 0; n--) {
+        while (!__all_sync(0xffffffffu, mbar_try_wait(full + stage, phase)))
+            if (__any_sync(0xffffffffu, global_timer_ns() - t0 > 200000000ull))
+                break;
+        if (++stage == depth) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+    *gone = 1;
 }
 
 // NW warps, each with a ring of DEPTH units.
@@ -314,6 +335,7 @@ struct Layer {
     struct Mem {
         alignas(8) uint64_t full[NW][DEPTH];
         int abort_flag;
+        int gone[NW];                          // see wait_long
         int head_task[NW];
         alignas(16) float head[NW][32][4];
     };
@@ -481,6 +503,9 @@ struct Layer {
         const int row = ((g & 1) << 2) | (g & 2) | (g >> 2);
         const int code0 = UP ? row * 128 + ((t4 ^ row) * 16)
                              : row * 128 + (((t4 >> 1) ^ row) * 16) + (t4 & 1) * 8;
+        // A warp that is gone goes on without copies or waits and meets the others at
+        // their barriers; what it stores is in its place, and worth nothing.
+        volatile int *gone = &mem.gone[warp];
         bool first_pass = true;
 
         for (int p0 = t0; p0 < t1 || first_pass;) {
@@ -509,7 +534,7 @@ struct Layer {
             int re = s.expert[rj];
             auto ask = [&]() {                 // one lane asks; all keep count
                 if (left > 0) {
-                    if (lane == 0)
+                    if (lane == 0 && !*gone)
                         request<UP>(p, re, rt, rb, left == u1 - u0 || rb == 0,
                                     ring.buf + ring.ask_stage * kUnitBytes,
                                     ring.full + ring.ask_stage, scales + rn * 64 * G);
@@ -572,7 +597,8 @@ struct Layer {
                 for (; unit < end; unit++) {
                     const uint32_t bar = smem_u32(ring.full + ring.stage);
                     if (!__all_sync(0xffffffffu, mbar_try_wait_a(bar, ring.phase)))
-                        wait_long(bar, ring.phase, &mem.abort_flag, p.dev_status, p.wait_ns);
+                        wait_long(ring.full, ring.stage, ring.ask_stage, ring.phase, DEPTH, gone,
+                                  &mem.abort_flag, p.dev_status, p.wait_ns);
                     const uint8_t *st = ring.buf + ring.stage * kUnitBytes;
                     auto group = [&](int j) {
                         uint32_t q0[T::kWords], q1[T::kWords];
@@ -681,8 +707,10 @@ __global__ void __launch_bounds__(32 * NW, 1) few_layer_kernel(const __grid_cons
     typename L::Ring ring = {dyn + warp * L::kRingBytes, mem.full[warp], 0, 0, 0};
     if (threadIdx.x == 0) {
         for (int i = 0; i < NW * DEPTH; i++)
-            mbar_init(&mem.full[0][0] + i, 1);
+            mbar_init(&mem.full[0][0] + i, p.withhold && i % DEPTH == 0 ? 2 : 1);
         mem.abort_flag = 0;
+        for (int i = 0; i < NW; i++)
+            mem.gone[i] = 0;
         fence_mbar_init();
         prefetch_tmap(&p.gu_map);
         prefetch_tmap(&p.dn_map);
@@ -846,6 +874,7 @@ cudaError_t launch_few(const FewProblem &q, cudaStream_t stream)
     a.out = q.out;
     a.dev_status = q.dev_status;
     a.wait_ns = pipeline_test_hooks().wait_ns;
+    a.withhold = pipeline_test_hooks().withhold_sz;
     a.M = q.M;
     a.d = q.d;
     a.m = q.m;
