@@ -712,12 +712,13 @@ int w4_attn_shared_prefix(const uint16_t *q, int64_t q_tok_stride, int64_t q_hea
 /* --------------------------------------------------------------------------
  * w4_test_pipeline_hooks -- a test hook of the kernels with pipelines (not for
  * production use): for later w4_grouped_gemm_gate_up / _down / _down_combine
- * calls, the layer's GEMMs, w4_attn_shared_prefix and w4_moe_layer_few* called
- * from the calling thread, every pipeline wait gives up after wait_limit_ns (0:
- * back to the default of one second) and, if withhold_first_scales is nonzero,
- * each CTA withholds the copy of its first unit's scales and zeros (attention:
- * never counts its first K tile as landed; the few-token layer: each warp its
- * first unit), so that its waits run out: the kernel then sets
+ * calls, the layer's GEMMs, w4_attn_shared_prefix, w4_moe_layer_few*,
+ * w4_kv_copy_pages and w4_kv_compact called from the calling thread, every
+ * pipeline wait gives up after wait_limit_ns (0: back to the default of one
+ * second) and, if withhold_first_scales is nonzero, each CTA withholds the copy
+ * of its first unit's scales and zeros (attention: never counts its first K tile
+ * as landed; the few-token layer: each warp its first unit; page copies: the
+ * first piece), so that its waits run out: the kernel then sets
  * W4_DEV_PIPELINE_TIMEOUT, lets its own copies land, drains its MMAs, frees its
  * tensor memory and exits, leaving its outputs incomplete and the context
  * usable.  Returns W4_OK.

@@ -59,3 +59,25 @@ def test_few_token_layer(lib, hooks, M, d, m, E, k):
     x, logits, gu, dn = _inputs(M, d, m, E, k)
     _times_out(lib, hooks,
                lambda st: lib.w4_moe_layer_few_from_logits(x, logits, k, gu, dn, dev_status=st)[0])
+
+
+@pytest.mark.parametrize("planes,page,Hkv,D", [(1, 4, 1, 8), (2, 16, 2, 64), (6, 64, 8, 128)])
+def test_page_copies(lib, hooks, planes, page, Hkv, D):
+    import torch
+    P = 900
+    pool = torch.randn((planes, P, page, Hkv, D), device="cuda").bfloat16()
+    perm = torch.randperm(P, device="cuda").int()
+    refs = (torch.rand(P, device="cuda") < 0.4).int()
+    table = torch.where(refs > 0, torch.arange(P, device="cuda").int(), -1)[None]
+
+    def copy(st):
+        out = pool.clone()
+        lib.w4_kv_copy_pages(out, perm[:400].contiguous(), perm[400:800].contiguous(), dev_status=st)
+        return out
+
+    def compact(st):
+        out = pool.clone()
+        lib.w4_kv_compact(out, table.clone(), refs.clone(), dev_status=st)
+        return out
+    _times_out(lib, hooks, copy)
+    _times_out(lib, hooks, compact)

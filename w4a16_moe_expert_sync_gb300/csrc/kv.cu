@@ -350,7 +350,8 @@ __global__ void __launch_bounds__(32) kv_copy_kernel(uint8_t *cache, int planes,
                                                      const int32_t *dst, const int32_t *count,
                                                      int n, int32_t *status,
                                                      const int32_t *table_in, int32_t *table_out,
-                                                     int64_t entries, const int32_t *remap)
+                                                     int64_t entries, const int32_t *remap,
+                                                     uint64_t wait_ns, int withhold)
 {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ __align__(8) uint64_t full[kSlots];
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(32) kv_copy_kernel(uint8_t *cache, int planes,
     const int lane = threadIdx.x;
     if (lane == 0) {
         for (int i = 0; i < kSlots; i++)
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], withhold && i == 0 ? 2 : 1);   // test hook: slot 0 never completes
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -379,11 +380,15 @@ __global__ void __launch_bounds__(32) kv_copy_kernel(uint8_t *cache, int planes,
     uint8_t *to[kAhead];                   // of the chunks loaded and not yet stored (lane 0)
     uint32_t size[kAhead];
     int issued = 0, stored = 0;
+    bool ok = true;                        // false once a wait has given up: no more loads, stores
     auto store_next = [&](uint8_t *out, uint32_t bytes) {
         const int slot = stored % kSlots;
-        if (mbar_wait(&full[slot], (stored / kSlots) & 1, &abort_flag, status, kDevPipelineTimeout))
+        ok = ok && mbar_wait(&full[slot], (stored / kSlots) & 1, &abort_flag, status,
+                             kDevPipelineTimeout, wait_ns);
+        if (ok) {
             bulk_store(out, ring + slot * kChunk, bytes);
-        stored++;
+            stored++;
+        }
     };
     for (int64_t c0 = blockIdx.x; c0 < chunks; c0 += 32ll * gridDim.x) {
         // the next 32 chunks' places, a lane each: one memory latency for all
@@ -406,10 +411,12 @@ __global__ void __launch_bounds__(32) kv_copy_kernel(uint8_t *cache, int planes,
         for (int l = 0; l < 32; l++) {
             const int64_t f = __shfl_sync(0xffffffffu, from, l), t = __shfl_sync(0xffffffffu, into, l);
             const uint32_t size_l = __shfl_sync(0xffffffffu, bytes, l);
-            if (f < 0 || lane != 0)
+            if (f < 0 || lane != 0 || !ok)
                 continue;
             if (issued - stored == kAhead) {
                 store_next(to[0], size[0]);
+                if (!ok)
+                    continue;
 #pragma unroll
                 for (int u = 0; u + 1 < kAhead; u++) {
                     to[u] = to[u + 1];
@@ -437,6 +444,9 @@ __global__ void __launch_bounds__(32) kv_copy_kernel(uint8_t *cache, int planes,
         for (int u = 0; u < kAhead; u++)
             if (stored < issued)
                 store_next(to[u], size[u]);
+        // after a wait that gave up, the loads still under way land
+        for (; stored < issued; stored++)
+            mbar_drain(&full[stored % kSlots], (stored / kSlots) & 1);
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 }
@@ -618,7 +628,9 @@ cudaError_t launch_kv_copy(uint8_t *cache, int planes, int64_t page_bytes, int P
     return launch_pdl(kv_copy_kernel, dim3(grid), dim3(32), kSlots * kChunk, stream, cache, planes,
                       page_bytes, P, src, dst, static_cast<const int32_t *>(nullptr), n, status,
                       static_cast<const int32_t *>(nullptr), static_cast<int32_t *>(nullptr),
-                      static_cast<int64_t>(0), static_cast<const int32_t *>(nullptr));
+                      static_cast<int64_t>(0), static_cast<const int32_t *>(nullptr),
+                      pipeline_test_hooks().wait_ns,
+                      static_cast<int>(pipeline_test_hooks().withhold_sz));
 }
 
 cudaError_t launch_kv_compact(uint8_t *cache, int planes, int64_t page_bytes, const int32_t *table,
@@ -638,7 +650,9 @@ cudaError_t launch_kv_compact(uint8_t *cache, int planes, int64_t page_bytes, co
     return launch_pdl(kv_copy_kernel, dim3(2 * sm_count()), dim3(32), kSlots * kChunk, stream, cache,
                       planes, page_bytes, P, static_cast<const int32_t *>(src),
                       static_cast<const int32_t *>(dst), static_cast<const int32_t *>(count), 0,
-                      status, table, table_out, entries, static_cast<const int32_t *>(remap));
+                      status, table, table_out, entries, static_cast<const int32_t *>(remap),
+                      pipeline_test_hooks().wait_ns,
+                      static_cast<int>(pipeline_test_hooks().withhold_sz));
 }
 
 size_t kv_workspace_bytes(int P, int n)
