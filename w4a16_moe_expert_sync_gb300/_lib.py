@@ -145,6 +145,33 @@ def _stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _scratch(shape, dtype, device, stream):
+    """Memory that a call on `stream` needs until its kernels have run: of that
+    stream's pool, so that nothing takes it before they have, once it is let go."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _result(shape, dtype, device, stream):
+    """A tensor that a call on `stream` fills and returns: of that stream's pool, for
+    earlier work of another stream may still use what that one's pool hands out, and
+    held, once let go, until the current stream's work of then has run."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    t = _scratch(shape, dtype, device, stream)
+    if t.numel():
+        current = torch.cuda.current_stream(t.device)
+        if current.cuda_stream != stream.cuda_stream:
+            t.record_stream(current)
+    return t
+
+
 def _require_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
@@ -175,9 +202,9 @@ def w4_quantize(W, group: int, out=None, stream=None):
         W = W.unsqueeze(0)
     E, N, K = W.shape
     if out is None:
-        out = (torch.empty((E, N, K // 2), dtype=torch.uint8, device=W.device),
-               torch.empty((E, N, K // group), dtype=torch.float16, device=W.device),
-               torch.empty((E, N, K // group), dtype=torch.float16, device=W.device))
+        out = (_result((E, N, K // 2), torch.uint8, W.device, stream),
+               _result((E, N, K // group), torch.float16, W.device, stream),
+               _result((E, N, K // group), torch.float16, W.device, stream))
     q, s, z = out
     _check(load_library().w4_quantize(_ptr(W), E, N, K, group, _ptr(q), _ptr(s), _ptr(z),
                                       _stream(stream)), "w4_quantize")
@@ -189,8 +216,8 @@ def w4_moe_route(logits, k: int, stream=None):
     import torch
     _require_cuda(logits)
     M, E = logits.shape
-    ids = torch.empty((M, k), dtype=torch.int32, device=logits.device)
-    w = torch.empty((M, k), dtype=torch.float32, device=logits.device)
+    ids = _result((M, k), torch.int32, logits.device, stream)
+    w = _result((M, k), torch.float32, logits.device, stream)
     _check(load_library().w4_moe_route(_ptr(logits), M, E, k, _ptr(ids), _ptr(w),
                                        _stream(stream)), "w4_moe_route")
     return ids, w
@@ -220,10 +247,10 @@ def w4_moe_align(topk_ids, E: int, block_m: int = 16, dev_status=None, out=None,
         r = out
         r.update(M=M, k=k, E=E, block_m=block_m)
     else:
-        r = dict(sorted_ids=torch.empty(cap, dtype=torch.int32, device=dev),
-                 block_expert=torch.empty(cap // block_m, dtype=torch.int32, device=dev),
-                 expert_offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
-                 num_padded=torch.empty(1, dtype=torch.int32, device=dev),
+        r = dict(sorted_ids=_result(cap, torch.int32, dev, stream),
+                 block_expert=_result(cap // block_m, torch.int32, dev, stream),
+                 expert_offsets=_result(E + 1, torch.int32, dev, stream),
+                 num_padded=_result(1, torch.int32, dev, stream),
                  M=M, k=k, E=E, block_m=block_m)
     _check(load_library().w4_moe_align(_ptr(topk_ids), M, k, E, block_m, _ptr(r["sorted_ids"]),
                                        _ptr(r["block_expert"]), _ptr(r["expert_offsets"]),
@@ -242,7 +269,7 @@ def w4_gather_activations(x, align: dict, out=None, dev_status=None, stream=None
     M, d = x.shape
     cap = align["sorted_ids"].numel()
     if out is None:
-        out = torch.empty((cap, d + SUM_COLS), dtype=torch.float16, device=x.device)
+        out = _result((cap, d + SUM_COLS), torch.float16, x.device, stream)
     _check(load_library().w4_gather_activations(
         _ptr(x), M, d, align["k"], align["E"], align["block_m"], _ptr(align["sorted_ids"]),
         _ptr(align["num_padded"]), _ptr(out), _ptr(dev_status), _stream(stream)),
@@ -260,13 +287,13 @@ def w4_moe_align_gather(topk_ids, x, E: int, block_m: int = 16, dev_status=None,
     cap = w4_moe_align_capacity(M, k, E, block_m)
     dev = x.device
     if out is None:
-        out = dict(sorted_ids=torch.empty(cap, dtype=torch.int32, device=dev),
-                   block_expert=torch.empty(cap // block_m, dtype=torch.int32, device=dev),
-                   expert_offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
-                   num_padded=torch.empty(1, dtype=torch.int32, device=dev))
+        out = dict(sorted_ids=_result(cap, torch.int32, dev, stream),
+                   block_expert=_result(cap // block_m, torch.int32, dev, stream),
+                   expert_offsets=_result(E + 1, torch.int32, dev, stream),
+                   num_padded=_result(1, torch.int32, dev, stream))
     out.update(M=M, k=k, E=E, block_m=block_m)
     if xg is None:
-        xg = torch.empty((cap, d + SUM_COLS), dtype=torch.float16, device=dev)
+        xg = _result((cap, d + SUM_COLS), torch.float16, dev, stream)
     _check(load_library().w4_moe_align_gather(
         _ptr(topk_ids), _ptr(x), M, d, k, E, block_m, _ptr(out["sorted_ids"]),
         _ptr(out["block_expert"]), _ptr(out["expert_offsets"]), _ptr(out["num_padded"]),
@@ -286,7 +313,7 @@ def w4_grouped_gemm_gate_up(xg, gu_q, gu_s, gu_z, align: dict, group: int = 128,
     m = two_m // 2
     cap = align["sorted_ids"].numel()
     if h is None:
-        h = torch.empty((cap, m + SUM_COLS), dtype=torch.float16, device=xg.device)
+        h = _result((cap, m + SUM_COLS), torch.float16, xg.device, stream)
     _check(load_library().w4_grouped_gemm_gate_up(
         _ptr(xg), M, d, m, E, align["k"], align["block_m"], _ptr(gu_q), _ptr(gu_s), _ptr(gu_z),
         group, _ptr(align["sorted_ids"]), _ptr(align["expert_offsets"]), _ptr(h),
@@ -316,7 +343,7 @@ def w4_grouped_gemm_down(h, dn_q, dn_s, dn_z, align: dict, group: int = 64, y=No
     m = half_m * 2
     M, k = align["M"], align["k"]
     if y is None:
-        y = torch.empty((M * k, d), dtype=torch.float32, device=h.device)
+        y = _result((M * k, d), torch.float32, h.device, stream)
     _check(load_library().w4_grouped_gemm_down(
         _ptr(h), M, d, m, E, k, align["block_m"], _ptr(dn_q), _ptr(dn_s), _ptr(dn_z), group,
         _ptr(align["sorted_ids"]), _ptr(align["expert_offsets"]), _ptr(y), _ptr(dev_status),
@@ -331,7 +358,7 @@ def w4_moe_combine_fixed_order(y, topk_ids, topk_weights, E: int, out=None, stre
     M, k = topk_ids.shape
     d = y.shape[1]
     if out is None:
-        out = torch.empty((M, d), dtype=torch.bfloat16, device=y.device)
+        out = _result((M, d), torch.bfloat16, y.device, stream)
     _check(load_library().w4_moe_combine_fixed_order(
         _ptr(y), _ptr(topk_ids), _ptr(topk_weights), M, k, d, E, _ptr(out), _stream(stream)),
         "w4_moe_combine_fixed_order")
@@ -346,9 +373,9 @@ def w4_moe_combine_prepare(topk_ids, E: int, d: int, counters=None, out=None, st
     _require_cuda(topk_ids, counters, out)
     M, k = topk_ids.shape
     if counters is None:
-        counters = torch.empty((M, d // 128), dtype=torch.int32, device=topk_ids.device)
+        counters = _result((M, d // 128), torch.int32, topk_ids.device, stream)
     if out is None:
-        out = torch.empty((M, d), dtype=torch.bfloat16, device=topk_ids.device)
+        out = _result((M, d), torch.bfloat16, topk_ids.device, stream)
     _check(load_library().w4_moe_combine_prepare(
         _ptr(topk_ids), M, k, E, d, _ptr(counters), _ptr(out), _stream(stream)),
         "w4_moe_combine_prepare")
@@ -367,7 +394,7 @@ def w4_grouped_gemm_down_combine(h, dn_q, dn_s, dn_z, align: dict, topk_ids, top
     m = half_m * 2
     M, k = align["M"], align["k"]
     if y is None:
-        y = torch.empty((M * k, d), dtype=torch.float32, device=h.device)
+        y = _result((M * k, d), torch.float32, h.device, stream)
     _check(load_library().w4_grouped_gemm_down_combine(
         _ptr(h), M, d, m, E, k, align["block_m"], _ptr(dn_q), _ptr(dn_s), _ptr(dn_z), group,
         _ptr(align["sorted_ids"]), _ptr(align["expert_offsets"]), _ptr(topk_ids),
@@ -395,9 +422,9 @@ def w4_moe_layer(x, topk_ids, topk_weights, gu, dn, block_m: int = 16, gu_group:
     k = topk_ids.shape[1]
     need = w4_moe_layer_workspace_size(M, d, m, E, k, block_m)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _scratch(need, torch.uint8, x.device, stream)
     if out is None:
-        out = torch.empty((M, d), dtype=torch.bfloat16, device=x.device)
+        out = _result((M, d), torch.bfloat16, x.device, stream)
     _check(load_library().w4_moe_layer(
         _ptr(x), _ptr(topk_ids), _ptr(topk_weights), M, d, m, E, k, block_m, _ptr(gu_q),
         _ptr(gu_s), _ptr(gu_z), gu_group, _ptr(dn_q), _ptr(dn_s), _ptr(dn_z), dn_group,
@@ -447,17 +474,17 @@ def w4_moe_route_align_gather(logits, x, k: int, block_m: int = 16, dev_status=N
     cap = w4_moe_align_capacity(M, k, E, block_m)
     dev = x.device
     if out is None:
-        out = dict(sorted_ids=torch.empty(cap, dtype=torch.int32, device=dev),
-                   block_expert=torch.empty(cap // block_m, dtype=torch.int32, device=dev),
-                   expert_offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
-                   num_padded=torch.empty(1, dtype=torch.int32, device=dev))
+        out = dict(sorted_ids=_result(cap, torch.int32, dev, stream),
+                   block_expert=_result(cap // block_m, torch.int32, dev, stream),
+                   expert_offsets=_result(E + 1, torch.int32, dev, stream),
+                   num_padded=_result(1, torch.int32, dev, stream))
     out.update(M=M, k=k, E=E, block_m=block_m)
     if xg is None:
-        xg = torch.empty((cap, d + SUM_COLS), dtype=torch.float16, device=dev)
+        xg = _result((cap, d + SUM_COLS), torch.float16, dev, stream)
     if ids is None:
-        ids = torch.empty((M, k), dtype=torch.int32, device=dev)
+        ids = _result((M, k), torch.int32, dev, stream)
     if weights is None:
-        weights = torch.empty((M, k), dtype=torch.float32, device=dev)
+        weights = _result((M, k), torch.float32, dev, stream)
     _check(load_library().w4_moe_route_align_gather(
         _ptr(logits), _ptr(x), M, d, k, E, block_m, _ptr(ids), _ptr(weights),
         _ptr(out["sorted_ids"]), _ptr(out["block_expert"]), _ptr(out["expert_offsets"]),
@@ -481,13 +508,13 @@ def w4_moe_layer_from_logits(x, logits, k: int, gu, dn, block_m: int = 16, gu_gr
     m = two_m // 2
     need = w4_moe_layer_workspace_size(M, d, m, E, k, block_m)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _scratch(need, torch.uint8, x.device, stream)
     if out is None:
-        out = torch.empty((M, d), dtype=torch.bfloat16, device=x.device)
+        out = _result((M, d), torch.bfloat16, x.device, stream)
     if ids is None:
-        ids = torch.empty((M, k), dtype=torch.int32, device=x.device)
+        ids = _result((M, k), torch.int32, x.device, stream)
     if weights is None:
-        weights = torch.empty((M, k), dtype=torch.float32, device=x.device)
+        weights = _result((M, k), torch.float32, x.device, stream)
     _check(load_library().w4_moe_layer_from_logits(
         _ptr(x), _ptr(logits), M, d, m, E, k, block_m, _ptr(gu_q), _ptr(gu_s), _ptr(gu_z),
         gu_group, _ptr(dn_q), _ptr(dn_s), _ptr(dn_z), dn_group, _ptr(workspace),
@@ -500,7 +527,7 @@ def w4_moe_layer_few_workspace_size(M, d, m, E, k) -> int:
     return int(load_library().w4_moe_layer_few_workspace_size(M, d, m, E, k))
 
 
-def _few_inputs(x, k, gu, dn, gu_group, dn_group, workspace, dev_status):
+def _few_inputs(x, k, gu, dn, gu_group, dn_group, workspace, dev_status, stream):
     """(M, d, m, E, the workspace) of a few-token call, with x, the weights and
     the workspace checked."""
     import torch
@@ -517,8 +544,7 @@ def _few_inputs(x, k, gu, dn, gu_group, dn_group, workspace, dev_status):
               (gz, f16, g_shape, "gu's zeros"), (dq, u8, (E, d, m // 2), "dn's codes"),
               (ds, f16, d_shape, "dn's scales"), (dz, f16, d_shape, "dn's zeros")))
     if workspace is None:
-        workspace = torch.empty(w4_moe_layer_few_workspace_size(M, d, m, E, k), dtype=u8,
-                                device=x.device)
+        workspace = _scratch(w4_moe_layer_few_workspace_size(M, d, m, E, k), u8, x.device, stream)
     _require_cuda(workspace, dev_status)
     return M, d, m, E, workspace
 
@@ -531,11 +557,13 @@ def w4_moe_layer_few(x, topk_ids, topk_weights, gu, dn, gu_group: int = 128, dn_
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids must be [M, k]")
     k = topk_ids.shape[1]
-    M, d, m, E, workspace = _few_inputs(x, k, gu, dn, gu_group, dn_group, workspace, dev_status)
+    M, d, m, E, workspace = _few_inputs(x, k, gu, dn, gu_group, dn_group, workspace, dev_status,
+                                        stream)
     _require(((topk_ids, torch.int32, (M, k), "topk_ids"),
               (topk_weights, torch.float32, (M, k), "topk_weights")))
     if out is None:
-        out = torch.empty_like(x)
+        out = torch.empty_like(x) if stream is None else \
+            _result(x.shape, x.dtype, x.device, stream)
     else:
         _require(((out, torch.bfloat16, (M, d), "out"),))
     _check(load_library().w4_moe_layer_few(
@@ -552,18 +580,20 @@ def w4_moe_layer_few_from_logits(x, logits, k: int, gu, dn, gu_group: int = 128,
     """w4_moe_layer_few with the router in its launch: from the logits
     [M, E] fp32.  Returns (out, topk_ids, topk_weights)."""
     import torch
-    M, d, m, E, workspace = _few_inputs(x, k, gu, dn, gu_group, dn_group, workspace, dev_status)
+    M, d, m, E, workspace = _few_inputs(x, k, gu, dn, gu_group, dn_group, workspace, dev_status,
+                                        stream)
     _require(((logits, torch.float32, (M, E), "logits"),))
     if out is None:
-        out = torch.empty_like(x)
+        out = torch.empty_like(x) if stream is None else \
+            _result(x.shape, x.dtype, x.device, stream)
     else:
         _require(((out, torch.bfloat16, (M, d), "out"),))
     if ids is None:
-        ids = torch.empty((M, k), dtype=torch.int32, device=x.device)
+        ids = _result((M, k), torch.int32, x.device, stream)
     else:
         _require(((ids, torch.int32, (M, k), "ids"),))
     if weights is None:
-        weights = torch.empty((M, k), dtype=torch.float32, device=x.device)
+        weights = _result((M, k), torch.float32, x.device, stream)
     else:
         _require(((weights, torch.float32, (M, k), "weights"),))
     _check(load_library().w4_moe_layer_few_from_logits(
@@ -610,10 +640,10 @@ def w4_w4a16_linear(x, q, s, z, group: int = 128, workspace=None, out=None, dev_
     M, K = x.shape
     N = q.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = _result((M, N), torch.bfloat16, x.device, stream)
     need = w4_w4a16_linear_workspace_size(M, K, N, group)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+        workspace = _scratch(max(need, 256), torch.uint8, x.device, stream)
     _check(load_library().w4_w4a16_linear(
         _ptr(x), M, K, N, _ptr(q), _ptr(s), _ptr(z), group, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(out), _ptr(dev_status),
@@ -627,12 +657,11 @@ def w4_w4a16_linear(x, q, s, z, group: int = 128, workspace=None, out=None, dev_
 def w4_rmsnorm(x, weight, eps: float = 1e-6, out=None, stream=None):
     """fused_rmsnorm: y = x / sqrt(mean(x^2) + eps) * weight over the last
     axis; x [..., d] and weight [d] bf16, y bf16."""
-    import torch
     _require_cuda(x, weight, out)
     d = x.shape[-1]
     M = x.numel() // d if d else 0
     if out is None:
-        out = torch.empty_like(x)
+        out = _result(x.shape, x.dtype, x.device, stream)
     _check(load_library().w4_rmsnorm(_ptr(x), _ptr(weight), M, d, float(eps), _ptr(out),
                                      _stream(stream)), "w4_rmsnorm")
     return out
@@ -642,12 +671,12 @@ def w4_sample_logits_workspace_size(M: int, V: int) -> int:
     return int(load_library().w4_sample_logits_workspace_size(M, V))
 
 
-def _sampler_ws(logits, workspace):
+def _sampler_ws(logits, workspace, stream):
     import torch
     M, V = logits.shape
     need = w4_sample_logits_workspace_size(M, V)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=logits.device)
+        workspace = _scratch(max(need, 16), torch.uint8, logits.device, stream)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -665,13 +694,13 @@ def w4_sample_logits(logits, seed: int = 0, offset: int = 0, entropy=True, sampl
         if spec is False or spec is None:
             return None
         if spec is True:
-            return torch.empty(M, dtype=dtype, device=dev)
+            return _result(M, dtype, dev, stream)
         _require_cuda(spec)
         return spec
     ent = out(entropy, torch.float32)
     smp = out(sample, torch.int64)
     amx = out(argmax, torch.int64)
-    ws, ws_bytes = _sampler_ws(logits, workspace)
+    ws, ws_bytes = _sampler_ws(logits, workspace, stream)
     _check(load_library().w4_sample_logits(
         _ptr(logits), M, V, seed & (2**64 - 1), offset & (2**64 - 1), _ptr(ent), _ptr(smp),
         _ptr(amx), _ptr(ws), ws_bytes, _stream(stream)), "w4_sample_logits")
@@ -743,10 +772,10 @@ def _kv_lists(first, *others):
     return shape[0]
 
 
-def _kv_workspace(workspace, P, n, device):
+def _kv_workspace(workspace, P, n, device, stream):
     import torch
     if workspace is None:
-        workspace = torch.empty(w4_kv_workspace_size(P, n), dtype=torch.uint8, device=device)
+        workspace = _scratch(w4_kv_workspace_size(P, n), torch.uint8, device, stream)
     _require_cuda(workspace)
     return workspace, workspace.nbytes
 
@@ -780,7 +809,7 @@ def w4_kv_fork(pool, table, lens, refs, parents, children, workspace=None, dev_s
     B, W, P = _kv_state(table, lens, refs, dev_status)
     planes, page_bytes, page = _kv_pool(pool, P)
     n = _kv_lists(parents, children)
-    workspace, nbytes = _kv_workspace(workspace, P, n, pool.device)
+    workspace, nbytes = _kv_workspace(workspace, P, n, pool.device, stream)
     _check(load_library().w4_kv_fork(_ptr(pool), planes, page_bytes, _ptr(table), B, W, _ptr(lens),
                                      _ptr(refs), P, _ptr(parents), _ptr(children), n, page,
                                      _ptr(workspace), nbytes, _ptr(dev_status), _stream(stream)),
@@ -812,7 +841,7 @@ def w4_kv_compact(pool, table, refs, table_out=None, refs_out=None, workspace=No
     B, W = table.shape
     P = refs.shape[0]
     planes, page_bytes, _ = _kv_pool(pool, P)
-    workspace, nbytes = _kv_workspace(workspace, P, 0, pool.device)
+    workspace, nbytes = _kv_workspace(workspace, P, 0, pool.device, stream)
     _check(load_library().w4_kv_compact(_ptr(pool), planes, page_bytes, _ptr(table), B, W,
                                         _ptr(refs), P, _ptr(table_out), _ptr(refs_out),
                                         _ptr(workspace), nbytes, _ptr(dev_status),
@@ -895,13 +924,13 @@ def w4_attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets, group_off
     if G < 0 or (G > 0 and (shared_lens is None or shared_lens.numel() != G)):
         raise ValueError("group_offsets must be [G + 1] and shared_lens [G]")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=dtype, device=q.device)
+        out = _result((T, Hq, D), dtype, q.device, stream)
     else:
         _require(((out, dtype, (T, Hq, D), "out"),))
     if workspace is None:
-        workspace = torch.empty(
+        workspace = _scratch(
             max(w4_attn_shared_prefix_workspace_size(T, B, G, max_q, Hq, Hkv, D), 256)
-            if Hkv and Hq % Hkv == 0 else 256, dtype=torch.uint8, device=q.device)
+            if Hkv and Hq % Hkv == 0 else 256, torch.uint8, q.device, stream)
     else:
         _require_cuda(workspace)
     _check(load_library().w4_attn_shared_prefix(
