@@ -416,9 +416,11 @@ int w4_moe_layer_from_logits(const uint16_t *x, const float *logits, int M, int 
  * and the layer is the stream of the touched experts' packed weights.  Same inputs and output as w4_moe_layer; the result differs
  * from it in rounding only.  The packed codes enter the tensor cores as they
  * are (exact fp16 subnormals) and a group's scale and zero are applied to the
- * fp32 sums, so no weight is rounded; activations and h are fp16 (beyond its
- * finite range: saturated, W4_DEV_FP16_RANGE), sums and the combine (fma
- * chain in slot order) are fp32, out is rounded once.  Bit-identical reruns.
+ * fp32 sums, so no weight is rounded; activations and h enter them as fp16
+ * (beyond its finite range: saturated, W4_DEV_FP16_RANGE; a group of 128 or 64
+ * whose values are all below 2^-7 is scaled up by a power of two first, so that
+ * small ones keep their bits), sums and the combine (fma chain in slot order) are
+ * fp32, out is rounded once.  Bit-identical reruns.
  *
  *   x [M, d] bf16, topk_ids [M, k] int32, topk_weights [M, k] fp32,
  *   out [M, d] bf16; ids outside [0, E) contribute nothing and set

@@ -28,15 +28,16 @@
 // are requested before the grid barrier that ends gate_up.
 //
 // Bound by HBM.  Measured at d = 2816, m = 704, E = 128, k = 8 (GB300, back to back in
-// a graph): 1 token 18.6 us (25.8 MB, 3.8 us at the copy bandwidth: routing, jobs, two
-// grid barriers and the first loads' latency), 7 tokens 42 us (150 MB, 22 us), 32
-// tokens 84 us (360 MB, 53 us).  At 32 tokens gate_up streams at 6.5 TB/s after 9 us of
+// a graph): 1 token 18.4 us (25.8 MB, 3.8 us at the copy bandwidth: routing, jobs, two
+// grid barriers and the first loads' latency), 7 tokens 45 us (150 MB, 22 us), 32
+// tokens 89 us (360 MB, 53 us).  At 32 tokens gate_up streams at 6.5 TB/s after 9 us of
 // routing and staging, down, with twice the scales, at 5.3; each barrier waits 2 to 7 us
 // for the last CTA.
 #include <algorithm>
 #include <atomic>
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 #include "../../include/w4moe.h"
 #include "launch.h"
@@ -58,7 +59,7 @@ struct FewArgs {
     int32_t *ids;                      // [M, k]
     float *w;                          // [M, k]
     const uint16_t *gu_s, *gu_z, *dn_s, *dn_z;
-    uint16_t *h;                       // [M k, m] fp16
+    float *h;                          // [M k, m]
     float *y;                          // [M k, d] fp32
     uint16_t *out;                     // [M, d] bf16
     int32_t *dev_status;
@@ -78,6 +79,7 @@ using Seen = uint8_t[kChunks][kMaxE];
 
 struct Shared {
     int n;                             // jobs
+    int scaled;                        // of a pass: whether a group is scaled (see Columns)
     int warp_sum[32];
     int16_t expert[kMaxA];
     int16_t count[kMaxA];
@@ -271,10 +273,34 @@ __device__ __forceinline__ float gelu_tanh_f(float v)
     return __fdividef(v, 1.0f + __expf(-2.0f * u));
 }
 
-// fp16 with saturation to the finite range (NaN stays NaN).
-__device__ __forceinline__ uint16_t to_half_sat(float v)
+// Saturation to fp16's finite range (NaN stays NaN).
+__device__ __forceinline__ float saturated(float v)
 {
-    return __half_as_ushort(__float2half_rn(fabsf(v) > 65504.0f ? copysignf(65504.0f, v) : v));
+    return fabsf(v) > 65504.0f ? copysignf(65504.0f, v) : v;
+}
+
+// 2^n.
+__device__ __forceinline__ float power(int n)
+{
+    return __uint_as_float(static_cast<uint32_t>(127 + n) << 23);
+}
+
+// Two values in fp16.
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// By how many powers of two a group is scaled up, of which `lanes` lanes side by side
+// hold 4 values each: to 2^14 .. 2^15 if they are all below 2^-7, else not at all.
+__device__ __noinline__ int shift_of(float a, float b, float c, float d, int lanes)
+{
+    float top = fmaxf(fmaxf(fabsf(a), fabsf(b)), fmaxf(fabsf(c), fabsf(d)));   // NaN does not count
+    for (int o = lanes / 2; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    return top < 0.0078125f ? min(141 - static_cast<int>(__float_as_uint(top) >> 23), 100) : 0;
 }
 
 // ----------------------------------------------------------------- streams
@@ -295,9 +321,9 @@ __host__ __device__ constexpr int scale_bufs(int depth, int K)
 }
 __host__ __device__ constexpr int col_stride(int K, int G)
 {
-    // fp16 values, then the fp32 sums of the groups; an odd multiple of 64 so
-    // that neighbouring columns' chunks fall in distinct banks
-    return (2 * K + 4 * G + 127) / 128 * 128 + 64;
+    // fp16 values, then the groups' sums and their factors (fp32); an odd multiple of 64
+    // so that neighbouring columns' chunks fall in distinct banks
+    return (2 * K + 8 * G + 127) / 128 * 128 + 64;
 }
 
 // The rest of a wait that its first try did not end, out of the hot loop: for stage
@@ -306,8 +332,8 @@ __host__ __device__ constexpr int col_stride(int K, int G)
 // stage is ask) has landed or had its time to, the warp is `gone`: nothing is requested
 // or awaited any more.  (Votes keep it uniform: a __syncwarp at its end, or the answer
 // returned, makes the caller's loop 10 KB longer and the layer 4 to 6 us slower.)
-__device__ __noinline__ void wait_long(uint64_t *full, int stage, int ask, uint32_t phase, int depth,
-                                       volatile int *gone, volatile int *abort_flag,
+__device__ __noinline__ void wait_long(uint64_t *full, int stage, int ask, uint32_t phase,
+                                       int depth, volatile int *gone, volatile int *abort_flag,
                                        int32_t *status, uint64_t limit_ns)
 {
     if (__any_sync(0xffffffffu, *gone != 0))
@@ -394,7 +420,7 @@ struct Layer {
                 const float hv = gelu_tanh_f(acc[c] * kSub) * (acc[2 + c] * kSub);
                 if (!(fabsf(hv) <= 65504.0f) && p.dev_status)
                     atomicOr(p.dev_status, kDevFp16Range);
-                p.h[a * p.m + tile * 8 + row] = to_half_sat(hv);
+                p.h[a * p.m + tile * 8 + row] = saturated(hv);
             } else {
                 float *y = p.y + a * p.d + tile * 16 + row;
                 y[0] = acc[c] * kSub;
@@ -404,18 +430,25 @@ struct Layer {
     }
 
     // The activations of a pass's columns, fp16 in the MMA's order, and their
-    // groups' sums times -2^-24.  A warp takes one column's 128 elements at a
-    // time, kBatch of them per call: load reads them, put stores them.
+    // groups' sums times -2^-24.  A group whose values are all below 2^-7 is scaled up
+    // by a power of two before it is rounded, so that it keeps fp16's 11 bits and h,
+    // which goes with the square of x, does not vanish; the inverse is its factor.  (In
+    // other groups what fp16 lacks is at most 2^-18 of the largest.)  Passes without such
+    // a group run a loop that knows no factors: 32 tokens 89 us, 97 where every group
+    // is small, 91 to 92 with the factors in one loop for all.
+    // A warp takes one column's 128 elements at a time, kBatch of them per call: load
+    // reads them, put stores them.
     template <bool UP> struct Columns {
         using T = Step<UP>;
-        static constexpr int kBatch = 4;
+        // (1, 7 and 32 tokens: 18.4, 45.5 and 88.8 us; 4 and 4: 19.1, 46.1, 89.1)
+        static constexpr int kBatch = UP ? 3 : 2;
         const FewArgs &p;
-        const Shared &s;
+        Shared &s;
         uint8_t *xbuf;
         int items, blocks, warp, lane;
-        uint2 v[kBatch];
+        std::conditional_t<UP, uint2, float4> v[kBatch];
 
-        __device__ __forceinline__ Columns(const FewArgs &p_, const Shared &s_, uint8_t *xbuf_,
+        __device__ __forceinline__ Columns(const FewArgs &p_, Shared &s_, uint8_t *xbuf_,
                                            int cols, int warp_, int lane_)
             : p(p_), s(s_), xbuf(xbuf_), warp(warp_), lane(lane_)
         {
@@ -433,11 +466,13 @@ struct Layer {
             for (int u = 0; u < kBatch; u++) {
                 const int c = warp + (batch * kBatch + u) * NW, col = c / blocks;
                 const int el = (c - col * blocks) * 128 + lane * 4;
-                v[u] = make_uint2(0, 0);
+                v[u] = {};
                 if (c < items && el < K) {
                     const int64_t a = s.col_a[col];
-                    v[u] = __ldcg(reinterpret_cast<const uint2 *>(
-                        (UP ? p.x + a / p.k * p.d : p.h + a * p.m) + el));
+                    if constexpr (UP)
+                        v[u] = __ldcg(reinterpret_cast<const uint2 *>(p.x + a / p.k * p.d + el));
+                    else
+                        v[u] = __ldcg(reinterpret_cast<const float4 *>(p.h + a * p.m + el));
                 }
             }
         }
@@ -454,16 +489,41 @@ struct Layer {
                 const int gi = el / T::kGroup, i8 = (el % T::kGroup) / 8;   // word in the group
                 uint16_t *dst = reinterpret_cast<uint16_t *>(
                     xc + gi * T::kGroup * 2 + (i8 % T::kWords) * 64 + (i8 / T::kWords) * 16);
+                float f[4];
+                if constexpr (UP) {
+                    f[0] = __uint_as_float(v[u].x << 16);
+                    f[1] = __uint_as_float(v[u].x & 0xFFFF0000u);
+                    f[2] = __uint_as_float(v[u].y << 16);
+                    f[3] = __uint_as_float(v[u].y & 0xFFFF0000u);
+                } else {
+                    f[0] = v[u].x;
+                    f[1] = v[u].y;
+                    f[2] = v[u].z;
+                    f[3] = v[u].w;
+                }
+                if constexpr (UP) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        range |= !(fabsf(f[i]) <= 65504.0f);
+                        f[i] = saturated(f[i]);
+                    }
+                }
+                uint32_t h01 = half_pair(f[0], f[1]), h23 = half_pair(f[2], f[3]);
+                int up = 0;
+                // an exponent field from 8 on: 2^-7 at least
+                const unsigned large =
+                    __ballot_sync(0xffffffffu, ((h01 | h23) & 0x60006000u) != 0 || !in);
+                if (UP ? large == 0 : (large & 0xFFFFu) == 0 || large >> 16 == 0) {
+                    up = shift_of(f[0], f[1], f[2], f[3], T::kGroup / 4);
+                    h01 = half_pair(f[0] * power(up), f[1] * power(up));
+                    h23 = half_pair(f[2] * power(up), f[3] * power(up));
+                    s.scaled = 1;
+                }
                 float sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const uint32_t bits = i < 2 ? v[u].x : v[u].y;
-                    uint16_t hb = static_cast<uint16_t>(i & 1 ? bits >> 16 : bits);
-                    if constexpr (UP) {
-                        const float f = __uint_as_float(static_cast<uint32_t>(hb) << 16);
-                        range |= !(fabsf(f) <= 65504.0f);
-                        hb = to_half_sat(f);
-                    }
+                    const uint32_t bits = i < 2 ? h01 : h23;
+                    const uint16_t hb = static_cast<uint16_t>(i & 1 ? bits >> 16 : bits);
                     sum += __half2float(__ushort_as_half(hb));
                     if (in)
                         dst[perm8((lane & 1) * 4 + i)] = hb;
@@ -471,13 +531,52 @@ struct Layer {
 #pragma unroll
                 for (int o = T::kGroup / 8; o > 0; o >>= 1)
                     sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (in && (lane & (T::kGroup / 4 - 1)) == 0)
-                    reinterpret_cast<float *>(xc + 2 * K)[gi] = -sum / kSub;
+                if (in && (lane & (T::kGroup / 4 - 1)) == 0) {
+                    float *t = reinterpret_cast<float *>(xc + 2 * K) + gi;
+                    t[0] = -sum / kSub;
+                    t[K / T::kGroup] = power(-up);
+                }
             }
             if (range && p.dev_status)
                 atomicOr(p.dev_status, kDevFp16Range);
         }
     };
+
+    // Adds group j of a unit to a lane's sums: codes at st + code0, activations at xc,
+    // sums (and, G further, factors) of its two columns, scales and zeros at sc.
+    template <bool UP, bool SCALED>
+    static __device__ __forceinline__ void add_group(const uint8_t *st, int code0,
+                                                     const uint8_t *xc, const float *sum0,
+                                                     const float *sum1, const uint16_t *sc, int G,
+                                                     int j, float (&acc)[4])
+    {
+        using T = Step<UP>;
+        uint32_t q0[T::kWords], q1[T::kWords];
+        if constexpr (UP) {
+            const uint8_t *c = st + (code0 ^ (64 * j));
+            *reinterpret_cast<uint4 *>(q0) = *reinterpret_cast<const uint4 *>(c);
+            *reinterpret_cast<uint4 *>(q1) = *reinterpret_cast<const uint4 *>(c + 1024);
+        } else {
+            const uint8_t *c = st + (code0 ^ (32 * j));
+            *reinterpret_cast<uint2 *>(q0) = *reinterpret_cast<const uint2 *>(c);
+            *reinterpret_cast<uint2 *>(q1) = *reinterpret_cast<const uint2 *>(c + 1024);
+        }
+        const uint4 *b = reinterpret_cast<const uint4 *>(xc + j * T::kGroup * 2);
+        float lo[4] = {}, hi[4] = {};
+#pragma unroll
+        for (int w = 0; w < T::kWords; w++)
+            mma_word(lo, hi, q0[w], q1[w], b[4 * w]);
+        // 2^-24 of the sum: acc += s (lo + hi / 16 - z 2^-24 sum)
+        const float s0 = half_bits(sc + j), s1 = half_bits(sc + 8 * G + j);
+        const float z0 = half_bits(sc + 16 * G + j), z1 = half_bits(sc + 24 * G + j);
+        const float a0 = sum0[j], a1 = sum1[j];
+        // s times a factor, a power of two, is exact
+        const float f0 = SCALED ? sum0[G + j] : 1.0f, f1 = SCALED ? sum1[G + j] : 1.0f;
+        acc[0] = fmaf(s0 * f0, fmaf(z0, a0, fmaf(hi[0], 0.0625f, lo[0])), acc[0]);
+        acc[1] = fmaf(s0 * f1, fmaf(z0, a1, fmaf(hi[1], 0.0625f, lo[1])), acc[1]);
+        acc[2] = fmaf(s1 * f0, fmaf(z1, a0, fmaf(hi[2], 0.0625f, lo[2])), acc[2]);
+        acc[3] = fmaf(s1 * f1, fmaf(z1, a1, fmaf(hi[3], 0.0625f, lo[3])), acc[3]);
+    }
 
     // The CTA's share of a step.  `between` runs once, after the first
     // requests are on their way; down's activations are read after it, gate_up's
@@ -511,6 +610,8 @@ struct Layer {
         for (int p0 = t0; p0 < t1 || first_pass;) {
             // the jobs whose columns fit together (one pass, unless many
             // tokens share few experts)
+            if (threadIdx.x == 0)
+                s.scaled = 0;
             const int job0 = p0 / per_job;
             int job1 = job0, cols = 0;
             while (p0 < t1 && job1 * per_job < t1 && cols + s.count[job1] <= p.cols) {
@@ -580,92 +681,74 @@ struct Layer {
             int sn = 0;
             bool begun = unit == 0;            // this warp holds the task's first unit
             float acc[4] = {};
-            for (int u = u0; u < u1;) {
-                const int job = task / per_job, n = s.count[job];
-                const uint8_t *xj = xbuf + s.col0[job] * stride;
-                const uint8_t *xc = xj + (g < n ? g : 0) * stride + t4 * 16 + unit * 512;
-                const int first_group = unit * T::kUnitGroups;
-                const float *sum0 = reinterpret_cast<const float *>(
-                    xj + (2 * t4 < n ? 2 * t4 : 0) * stride + 2 * K) + first_group;
-                const float *sum1 = reinterpret_cast<const float *>(
-                    xj + (2 * t4 + 1 < n ? 2 * t4 + 1 : 0) * stride + 2 * K) + first_group;
-                const uint16_t *sc = reinterpret_cast<const uint16_t *>(scales + sn * 64 * G) +
-                                     row * G + first_group;
-                const int end = min(per_task, unit + u1 - u);
-                u += end - unit;
-                int groups = G - first_group;              // left in the task
-                for (; unit < end; unit++) {
-                    const uint32_t bar = smem_u32(ring.full + ring.stage);
-                    if (!__all_sync(0xffffffffu, mbar_try_wait_a(bar, ring.phase)))
-                        wait_long(ring.full, ring.stage, ring.ask_stage, ring.phase, DEPTH, gone,
-                                  &mem.abort_flag, p.dev_status, p.wait_ns);
-                    const uint8_t *st = ring.buf + ring.stage * kUnitBytes;
-                    auto group = [&](int j) {
-                        uint32_t q0[T::kWords], q1[T::kWords];
-                        if constexpr (UP) {
-                            const uint8_t *c = st + (code0 ^ (64 * j));
-                            *reinterpret_cast<uint4 *>(q0) = *reinterpret_cast<const uint4 *>(c);
-                            *reinterpret_cast<uint4 *>(q1) =
-                                *reinterpret_cast<const uint4 *>(c + 1024);
+            auto consume = [&](auto scaled) {
+                for (int u = u0; u < u1;) {
+                    const int job = task / per_job, n = s.count[job];
+                    const uint8_t *xj = xbuf + s.col0[job] * stride;
+                    const uint8_t *xc = xj + (g < n ? g : 0) * stride + t4 * 16 + unit * 512;
+                    const int first_group = unit * T::kUnitGroups;
+                    const float *sum0 = reinterpret_cast<const float *>(
+                        xj + (2 * t4 < n ? 2 * t4 : 0) * stride + 2 * K) + first_group;
+                    const float *sum1 = reinterpret_cast<const float *>(
+                        xj + (2 * t4 + 1 < n ? 2 * t4 + 1 : 0) * stride + 2 * K) + first_group;
+                    const uint16_t *sc = reinterpret_cast<const uint16_t *>(scales + sn * 64 * G) +
+                                         row * G + first_group;
+                    const int end = min(per_task, unit + u1 - u);
+                    u += end - unit;
+                    int groups = G - first_group;              // left in the task
+                    for (; unit < end; unit++) {
+                        const uint32_t bar = smem_u32(ring.full + ring.stage);
+                        if (!__all_sync(0xffffffffu, mbar_try_wait_a(bar, ring.phase)))
+                            wait_long(ring.full, ring.stage, ring.ask_stage, ring.phase, DEPTH,
+                                      gone, &mem.abort_flag, p.dev_status, p.wait_ns);
+                        const uint8_t *st = ring.buf + ring.stage * kUnitBytes;
+                        auto group = [&](int j) {
+                            add_group<UP, scaled>(st, code0, xc, sum0, sum1, sc, G, j, acc);
+                        };
+                        // whole units without a branch between their groups, so that
+                        // the groups' loads and MMAs overlap
+                        if (groups >= T::kUnitGroups) {
+#pragma unroll
+                            for (int j = 0; j < T::kUnitGroups; j++)
+                                group(j);
                         } else {
-                            const uint8_t *c = st + (code0 ^ (32 * j));
-                            *reinterpret_cast<uint2 *>(q0) = *reinterpret_cast<const uint2 *>(c);
-                            *reinterpret_cast<uint2 *>(q1) =
-                                *reinterpret_cast<const uint2 *>(c + 1024);
-                        }
-                        const uint4 *b = reinterpret_cast<const uint4 *>(xc + j * T::kGroup * 2);
-                        float lo[4] = {}, hi[4] = {};
-#pragma unroll
-                        for (int w = 0; w < T::kWords; w++)
-                            mma_word(lo, hi, q0[w], q1[w], b[4 * w]);
-                        // 2^-24 of the sum: acc += s (lo + hi / 16 - z 2^-24 sum)
-                        const float s0 = half_bits(sc + j), s1 = half_bits(sc + 8 * G + j);
-                        const float z0 = half_bits(sc + 16 * G + j), z1 = half_bits(sc + 24 * G + j);
-                        const float a0 = sum0[j], a1 = sum1[j];
-                        acc[0] = fmaf(s0, fmaf(z0, a0, fmaf(hi[0], 0.0625f, lo[0])), acc[0]);
-                        acc[1] = fmaf(s0, fmaf(z0, a1, fmaf(hi[1], 0.0625f, lo[1])), acc[1]);
-                        acc[2] = fmaf(s1, fmaf(z1, a0, fmaf(hi[2], 0.0625f, lo[2])), acc[2]);
-                        acc[3] = fmaf(s1, fmaf(z1, a1, fmaf(hi[3], 0.0625f, lo[3])), acc[3]);
-                    };
-                    // whole units without a branch between their groups, so that
-                    // the groups' loads and MMAs overlap
-                    if (groups >= T::kUnitGroups) {
-#pragma unroll
-                        for (int j = 0; j < T::kUnitGroups; j++)
-                            group(j);
-                    } else {
 #pragma unroll 1
-                        for (int j = 0; j < groups; j++)
-                            group(j);
+                            for (int j = 0; j < groups; j++)
+                                group(j);
+                        }
+                        groups -= T::kUnitGroups;
+                        xc += 512;
+                        sum0 += T::kUnitGroups;
+                        sum1 += T::kUnitGroups;
+                        sc += T::kUnitGroups;
+                        if (++ring.stage == DEPTH) {
+                            ring.stage = 0;
+                            ring.phase ^= 1;
+                        }
+                        __syncwarp();
+                        ask();
                     }
-                    groups -= T::kUnitGroups;
-                    xc += 512;
-                    sum0 += T::kUnitGroups;
-                    sum1 += T::kUnitGroups;
-                    sc += T::kUnitGroups;
-                    if (++ring.stage == DEPTH) {
-                        ring.stage = 0;
-                        ring.phase ^= 1;
+                    if (unit == per_task) {
+                        if (begun)
+                            finish<UP>(p, s, task, acc, row, t4);
+                        else {                     // begun by an earlier warp
+                            *reinterpret_cast<float4 *>(mem.head[warp][lane]) =
+                                make_float4(acc[0], acc[1], acc[2], acc[3]);
+                            if (lane == 0)
+                                mem.head_task[warp] = task;
+                        }
+                        unit = 0;
+                        task++;
+                        begun = true;
+                        sn = sn + 1 == nbuf ? 0 : sn + 1;
+                        acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
                     }
-                    __syncwarp();
-                    ask();
                 }
-                if (unit == per_task) {
-                    if (begun)
-                        finish<UP>(p, s, task, acc, row, t4);
-                    else {                     // begun by an earlier warp
-                        *reinterpret_cast<float4 *>(mem.head[warp][lane]) =
-                            make_float4(acc[0], acc[1], acc[2], acc[3]);
-                        if (lane == 0)
-                            mem.head_task[warp] = task;
-                    }
-                    unit = 0;
-                    task++;
-                    begun = true;
-                    sn = sn + 1 == nbuf ? 0 : sn + 1;
-                    acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
-                }
-            }
+            };
+            if (s.scaled)
+                consume(std::true_type{});
+            else
+                consume(std::false_type{});
             const bool open = u0 < u1 && unit != 0;    // the last task goes on in a later warp
             if (open && !begun) {                      // and began in an earlier one
                 *reinterpret_cast<float4 *>(mem.head[warp][lane]) =
@@ -836,7 +919,10 @@ bool encode_rows(CUtensorMap *map, const uint8_t *base, int row_bytes, int rows,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t h_bytes(int M, int m, int k) { return (static_cast<size_t>(M) * k * m * 2 + 255) / 256 * 256; }
+size_t h_bytes(int M, int m, int k)
+{
+    return (static_cast<size_t>(M) * k * m * 4 + 255) / 256 * 256;
+}
 
 }  // namespace
 
@@ -869,7 +955,7 @@ cudaError_t launch_few(const FewProblem &q, cudaStream_t stream)
     a.gu_z = q.gu_z;
     a.dn_s = q.dn_s;
     a.dn_z = q.dn_z;
-    a.h = static_cast<uint16_t *>(q.workspace);
+    a.h = static_cast<float *>(q.workspace);
     a.y = reinterpret_cast<float *>(static_cast<uint8_t *>(q.workspace) + h_bytes(q.M, q.m, q.k));
     a.out = q.out;
     a.dev_status = q.dev_status;

@@ -150,7 +150,7 @@ struct FewProblem {
     float *w;                   // [M, k]
     const uint8_t *gu_q, *dn_q;
     const uint16_t *gu_s, *gu_z, *dn_s, *dn_z;
-    void *workspace;            // few_workspace_bytes: h fp16, y fp32
+    void *workspace;            // few_workspace_bytes: h and y, fp32
     uint16_t *out;              // [M, d] bf16
     int32_t *dev_status;
     int M, d, m, E, k;
