@@ -693,8 +693,9 @@ int w4_kv_append(uint16_t *k_pages, uint16_t *v_pages, int64_t page_stride, int6
  * W4_DEV_BAD_PAGE) are flagged; the queries concerned get unspecified values.
  * With offsets that do not ascend nothing is computed (W4_DEV_BAD_SLOT).
  * Scores, maximum and denominator are fp32; the weights are rounded to the
- * values' type for the product with V; partial sums are fp32, joined in a
- * fixed order: bit-identical reruns on one GPU model.  Two launches.
+ * values' type for the product with V (fp16: one 2^32 below the largest is lost
+ * there); partial sums are fp32, joined in a fixed order: bit-identical reruns on
+ * one GPU model.  Two launches.
  * Requires D = 64 or 128, page_size 16, 32, 64 or 128, Hkv dividing Hq,
  * max_q >= 1, scale > 0, B + G <= 4000, pointers 16-byte aligned, strides
  * multiples of 8 elements, T * Hq * D and the tiles below 2^31.

@@ -1124,8 +1124,11 @@ struct Kernel {
 
     // P of one tile from its S; columns outside [lo, hi) are masked.  m is the
     // reference of the exponents, not always the maximum: it moves only when
-    // the maximum has outgrown it by 2^8, so O is seldom rescaled; P <= 2^8
-    // stays within fp16.  P is rounded to the values' type for the MMA (its
+    // the maximum has grown by more than 2^8 since it last moved, so O is seldom
+    // rescaled.  For bf16 it moves to the maximum, for fp16 to 2^7 below, so that P lies
+    // in 0 .. 2^15 and a weight vanishes only 2^32 below the largest (2^25 otherwise: a
+    // hundred thousand keys beside one that outweighs them can be 0.4 % of the result).
+    // P is rounded to the values' type for the MMA (its
     // denominator sums the unrounded).  When S is here, every MMA before it has
     // completed, so O may be changed.
     static __device__ __forceinline__ void tile(const AttnArgs &p, uint32_t ts, uint32_t to, int lo,
@@ -1144,10 +1147,11 @@ struct Kernel {
         for (int c = 0; c < 128; c += 2)
             top[c / 2 & 3] = max3(top[c / 2 & 3], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
         const float tm = max3(fmaxf(top[0], top[1]), top[2], top[3]) * p.scale_log2;
-        const bool move = tm > m + 8.0f;       // also from -inf
+        constexpr float kLift = BF16 ? 0.0f : 7.0f;
+        const bool move = tm > m + (8.0f + kLift);         // also from -inf
         if (__any_sync(0xffffffffu, move)) {
-            const float alpha = move ? ex2(m - tm) : 1.0f;
-            m = move ? tm : m;
+            const float alpha = move ? ex2(m - (tm - kLift)) : 1.0f;
+            m = move ? tm - kLift : m;
             l *= alpha;
             if (has_o)
                 rescale(to, alpha);
