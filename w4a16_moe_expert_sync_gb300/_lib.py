@@ -545,7 +545,8 @@ def _few_inputs(x, k, gu, dn, gu_group, dn_group, workspace, dev_status, stream)
               (ds, f16, d_shape, "dn's scales"), (dz, f16, d_shape, "dn's zeros")))
     if workspace is None:
         workspace = _scratch(w4_moe_layer_few_workspace_size(M, d, m, E, k), u8, x.device, stream)
-    _require_cuda(workspace, dev_status)
+    _require_cuda(workspace)
+    _require_int32(dev_status)
     return M, d, m, E, workspace
 
 
