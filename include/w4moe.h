@@ -77,7 +77,9 @@ typedef enum {
 
 #define W4_DEV_BAD_SLOT 0x20           /* a sequence slot (or its length, or its
                                          place in q_offsets) is out of range,
-                                         named twice or not empty; skipped       */
+                                         named twice or not empty, or it would
+                                         grow into a page that others hold;
+                                         skipped                                 */
 #define W4_DEV_BAD_PAGE 0x40           /* a page id outside [0, P), or a page
                                          freed more often than held; skipped     */
 #define W4_DEV_NO_PAGES 0x80           /* too few free pages; the sequences from
@@ -594,13 +596,17 @@ int w4_gumbel_argmax_sample(const float *logits, int M, int64_t V, uint64_t seed
  * lowest free id first, to the requests in order, so a sequence of calls
  * gives the same pages on every run.  Nothing is read back: what the device
  * finds wrong is skipped and OR-ed into *dev_status (may be NULL).
+ * The caller may lower a length (tokens taken back): the slot keeps the pages
+ * behind it until it grows again or is freed.
  * Requires page_size >= 1, page_bytes a multiple of 16 page_size, a 16-byte
  * aligned pool, B * W and P below 2^30, and n <= 1024 per call of reserve and
  * fork.  n = 0 does nothing.
  * ========================================================================== */
 
 /* w4_kv_reserve -- grow slots[i] to new_lens[i] tokens (>= its length), taking
- * the pages that needs; lens is set to new_lens.  One launch. */
+ * the pages that needs and that it does not hold yet; lens is set to new_lens.  A
+ * slot whose length has been lowered into a page that other slots hold cannot grow
+ * (W4_DEV_BAD_SLOT): fork a copy of it and free it.  One launch. */
 int w4_kv_reserve(int32_t *table, int B, int W, int32_t *lens, int32_t *refs, int P,
                   const int32_t *slots, const int32_t *new_lens, int n, int page_size,
                   int32_t *dev_status, w4_stream_t stream);

@@ -168,6 +168,16 @@ __global__ void __launch_bounds__(kPlanThreads) kv_reserve_kernel(
             first = (len + page - 1) / page;
             const int last = want / page + (want % page != 0);
             ok = len >= 0 && want >= len && last <= W;
+            // From the page of the next token on, what the slot holds already (its
+            // length has been lowered) it keeps; a page that others hold too is not
+            // to be written.
+            if (ok && want > len) {
+                const int32_t *row = table + static_cast<int64_t>(slot) * W;
+                int c = len / page;
+                for (; ok && c < last && row[c] >= 0 && row[c] < P; c++)
+                    ok = refs[row[c]] <= 1;
+                first = max(first, c);
+            }
             need = ok ? last - first : 0;
         }
         if (!ok)
@@ -237,7 +247,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(
     int len = 0, full = 0, need = 0;
     if (i < n) {
         ok = a >= 0 && a < B && b >= 0 && b < B && a != b && lens[b] == 0 &&
-             !repeated(s.slot, i);
+             table[static_cast<int64_t>(b) * W] == -1 && !repeated(s.slot, i);
         if (ok) {
             len = lens[a];
             full = len / page;
