@@ -82,9 +82,10 @@ typedef enum {
                                          skipped                                 */
 #define W4_DEV_BAD_PAGE 0x40           /* a page id outside [0, P), or a page
                                          freed more often than held; skipped     */
-#define W4_DEV_NO_PAGES 0x80           /* too few free pages; the sequences from
-                                         the first that lacks one on are left
-                                         as they were                            */
+#define W4_DEV_NO_PAGES 0x80           /* too few free pages; from the first
+                                         request that lacks one on, those that
+                                         need a page leave their slots as they
+                                         were (those that need none are served)  */
 
 /* Human-readable name of a w4_status value (static string). */
 const char *w4_status_string(int status);

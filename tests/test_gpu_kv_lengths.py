@@ -154,3 +154,28 @@ def test_random_histories_with_lowered_lengths(lib, planes, P, page, B, W):
                 if p >= 0:
                     held[p] = held.get(p, 0) + 1
         assert [held.get(p, 0) for p in range(P)] == m.refs
+
+
+def test_requests_that_need_no_page_are_served_behind_one_that_lacks_some(lib):
+    import torch
+    m, d = _state((1, 2), 8, 4, 6, 8)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    m.reserve([1, 2], [6, 8])
+    lib.w4_kv_reserve(d.table, d.lens, d.refs, _ints([1, 2]), _ints([6, 8]), 4)
+    d.check(m)                               # four pages in use, four free
+    args = [0, 1, 3, 4, 2], [20, 8, 1, 0, 9]     # five pages; none; one; none; one
+    assert m.reserve(*args) == w4.W4_DEV_NO_PAGES
+    lib.w4_kv_reserve(d.table, d.lens, d.refs, _ints(args[0]), _ints(args[1]), 4, dev_status=st)
+    assert int(st) == w4.W4_DEV_NO_PAGES
+    d.check(m)
+    assert m.lens == [0, 8, 8, 0, 0, 0]
+    m.reserve([0, 1], [12, 10])              # one is left behind: seven and one in use
+    lib.w4_kv_reserve(d.table, d.lens, d.refs, _ints([0, 1]), _ints([12, 10]), 4)
+    d.check(m)
+    st.zero_()
+    args = [1, 2], [3, 4]                    # a tail page, and full pages alone
+    assert m.fork(*args) == w4.W4_DEV_NO_PAGES
+    lib.w4_kv_fork(d.pool, d.table, d.lens, d.refs, _ints(args[0]), _ints(args[1]), dev_status=st)
+    assert int(st) == w4.W4_DEV_NO_PAGES
+    d.check(m)
+    assert m.lens == [12, 10, 8, 0, 8, 0]

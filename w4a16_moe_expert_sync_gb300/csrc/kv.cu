@@ -99,7 +99,8 @@ __device__ __forceinline__ int owner_of(const int *start, int n, int rank)
 
 // Hands the `total` lowest free pages out: page of rank r goes to table entry
 // at[i] + r - start[i] of slot[i].  Returns how many requests, in order, got
-// all of theirs; the pages of the first that did not are given back.
+// all of theirs; the pages of the first that did not are given back.  (A request
+// that needs none is served wherever it stands.)
 __device__ int hand_out(PlanShared &s, int n, int total, int32_t *table, int W, int32_t *refs,
                         int P)
 {
