@@ -445,7 +445,8 @@ int w4_moe_layer_few(const uint16_t *x, const int32_t *topk_ids, const float *to
 /* w4_moe_layer_few_from_logits -- w4_moe_layer_few with the router in
  * its launch: from the logits [M, E] fp32.  topk_ids and topk_weights are
  * outputs, bit-identical to w4_moe_route's; out is bit-identical to
- * w4_moe_route followed by w4_moe_layer_few.  k <= E. */
+ * w4_moe_route followed by w4_moe_layer_few.  A token with NaN among its logits
+ * is excepted: it gets some ids in [0, E), the other tokens their own.  k <= E. */
 int w4_moe_layer_few_from_logits(const uint16_t *x, const float *logits, int M, int d, int m,
                                  int E, int k, const uint8_t *gu_q, const uint16_t *gu_s,
                                  const uint16_t *gu_z, int gu_group, const uint8_t *dn_q,

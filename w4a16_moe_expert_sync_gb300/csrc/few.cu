@@ -42,6 +42,7 @@
 #include "../../include/w4moe.h"
 #include "launch.h"
 #include "ptx.cuh"
+#include "route_token.cuh"
 
 namespace w4 {
 
@@ -91,7 +92,7 @@ struct Shared {
 };
 
 // The k experts of one token by one warp, ties to the lower index: the same
-// ids as route_token's (for logits that are not NaN).  Floats are compared as
+// ids as route_token's, for a row without NaN (with NaN: some ids in [0, E)).  Floats are compared as
 // integers in the same order, a round is two warp reductions.  Lane j < k
 // returns the j-th choice.
 template <int EPL>
@@ -154,21 +155,16 @@ __device__ void load_routing(const FewArgs &p, Shared &s, Seen &seen)
     __syncthreads();
 }
 
-// The router's results of token t, by one warp: its ids and their weights
-// with route_token's arithmetic (float64, summed in slot order).
+// The router's results of token t, by one warp: its ids and their weights.
 __device__ void publish_routing(const FewArgs &p, const Shared &s, int t, int lane)
 {
     const int e = lane < p.k ? s.ids[t * p.k + lane] : 0;
     const float v = lane < p.k ? __ldg(p.logits + static_cast<int64_t>(t) * p.E + e) : 0.0f;
     const float top = __shfl_sync(0xffffffffu, v, 0);
-    const double ex =
-        lane < p.k ? exp(static_cast<double>(v) - static_cast<double>(top)) : 0.0;
-    double sum = 0.0;
-    for (int j = 0; j < p.k; j++)
-        sum += __shfl_sync(0xffffffffu, ex, j);
+    const float w = chosen_weight(v, top, p.k, lane);
     if (lane < p.k) {
         p.ids[t * p.k + lane] = e;
-        p.w[t * p.k + lane] = static_cast<float>(ex / sum);
+        p.w[t * p.k + lane] = w;
     }
 }
 

@@ -1,11 +1,27 @@
 // route_token.cuh -- the router's arithmetic for one token, shared by the
-// router and the fused alignment (bit-identical ids and weights in both).
+// router, the fused alignment and (the weights) the few-token layer: bit-identical
+// weights in all.
 #pragma once
 
 #include <cfloat>
 #include <cstdint>
 
 namespace w4 {
+
+// The weights of a token's k chosen experts, by one warp: lane j < k has the j-th
+// choice's logit and gets its weight, `top` is the first's.  In float64,
+// rounded to fp32 once: exp(l_j - l_top) over the sum of the k selected, summed
+// in slot order.  That is the renormalised softmax of the k (the full
+// softmax's normaliser cancels), so the fp32 result is the float64 softmax's,
+// bar a float64 rounding difference that lands on an fp32 rounding boundary.
+__device__ __forceinline__ float chosen_weight(float logit, float top, int k, int lane)
+{
+    const double ex = lane < k ? exp(static_cast<double>(logit) - static_cast<double>(top)) : 0.0;
+    double sum = 0.0;
+    for (int j = 0; j < k; j++)
+        sum += __shfl_sync(0xffffffffu, ex, j);
+    return lane < k ? static_cast<float>(ex / sum) : 0.0f;
+}
 
 // The router for one token, computed by one warp: the k largest logits by k
 // rounds of a warp arg-max (ties to the lower expert index), then softmax
@@ -60,17 +76,8 @@ __device__ __forceinline__ void route_token(const float *__restrict__ row, int E
             my_idx = be;
         }
     }
-    // The weights in float64, rounded to fp32 once: exp(l_j - l_top) over
-    // the sum of the k selected, summed in slot order.  That is the
-    // renormalised softmax of the k (the full softmax's normaliser cancels),
-    // so the fp32 result is the float64 softmax's, bar a float64 rounding
-    // difference that lands on an fp32 rounding boundary.
-    const double ex = lane < k ? exp(static_cast<double>(my_val) - static_cast<double>(top)) : 0.0;
-    double sum = 0.0;
-    for (int j = 0; j < k; j++)
-        sum += __shfl_sync(0xffffffffu, ex, j);
     *id = lane < k ? my_idx : -1;
-    *w = lane < k ? static_cast<float>(ex / sum) : 0.0f;
+    *w = chosen_weight(my_val, top, k, lane);
 }
 
 }  // namespace w4
