@@ -836,6 +836,10 @@ __global__ void __launch_bounds__(32 * NW, 1) few_layer_kernel(const __grid_cons
 template <int NW, int DEPTH>
 bool plan(int d, int m, int *scale_bytes, int *cols, size_t *smem)
 {
+    *scale_bytes = *cols = 0;
+    *smem = 0;
+    if (d > 65536 || m > 65536)        // no column of these fits, and 32 bits hold the rest
+        return false;
     const int Gu = d / 128, Gd = m / 64;
     *scale_bytes = 64 * std::max(scale_bufs(DEPTH, d) * Gu, scale_bufs(DEPTH, m) * Gd);
     // the static arrays, up to the dynamic part's alignment
