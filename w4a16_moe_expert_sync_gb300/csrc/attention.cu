@@ -44,6 +44,7 @@
 #include <cuda_fp16.h>
 
 #include "../../include/w4moe.h"
+#include "checks.cuh"
 #include "launch.h"
 #include "ptx.cuh"
 
@@ -593,7 +594,8 @@ struct Kernel {
                 }
                 g.tiles = max(end - g.tile0, 0);
                 g.piece = item + w;
-                segs[g.piece] = g;
+                if (W4_IN_BOUNDS(g.piece >= 0 && g.piece < (pair ? p.cap_a : p.cap_b), p.status))
+                    segs[g.piece] = g;
                 if (i == 0)
                     s.first[which] = g;
                 mine += g.tiles;
@@ -1235,6 +1237,10 @@ struct Kernel {
         const int kind = pair ? 0 : g.seq < 0 ? 1 : 2;
         const int all = rows_of(p, kind);
         const int64_t base = static_cast<int64_t>(g.piece) * all;
+        if (!W4_IN_BOUNDS(g.piece >= 0 && row + rows <= all &&
+                              g.piece < (kind == 0 ? p.cap_a : kind == 1 ? p.cap_g : p.cap_b),
+                          p.status))
+            return;
         if (tid < rows)
             (pair ? p.ml[0] : kind == 1 ? p.ml[1] : p.ml[2])[base + row + tid] = make_float2(m, l);
         __syncwarp();
@@ -1451,8 +1457,10 @@ __global__ void __launch_bounds__(32 * SPLIT *kJoinSides<D, SPLIT>, SPLIT == 1 ?
             }
             uint4 *out = reinterpret_cast<uint4 *>(
                 p.out + (static_cast<int64_t>(tok) * p.Hq + h) * D + cg * 16);
-            out[0] = make_uint4(r[0], r[1], r[2], r[3]);
-            out[1] = make_uint4(r[4], r[5], r[6], r[7]);
+            if (W4_IN_BOUNDS(tok >= 0 && tok < p.T && h < p.Hq, p.status)) {
+                out[0] = make_uint4(r[0], r[1], r[2], r[3]);
+                out[1] = make_uint4(r[4], r[5], r[6], r[7]);
+            }
         }
         __syncthreads();
     }

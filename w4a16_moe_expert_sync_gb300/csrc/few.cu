@@ -40,6 +40,7 @@
 #include <type_traits>
 
 #include "../../include/w4moe.h"
+#include "checks.cuh"
 #include "launch.h"
 #include "ptx.cuh"
 #include "route_token.cuh"
@@ -416,8 +417,11 @@ struct Layer {
                 const float hv = gelu_tanh_f(acc[c] * kSub) * (acc[2 + c] * kSub);
                 if (!(fabsf(hv) <= 65504.0f) && p.dev_status)
                     atomicOr(p.dev_status, kDevFp16Range);
-                p.h[a * p.m + tile * 8 + row] = saturated(hv);
+                if (W4_IN_BOUNDS(a < p.M * p.k && tile * 8 + row < p.m, p.dev_status))
+                    p.h[a * p.m + tile * 8 + row] = saturated(hv);
             } else {
+                if (!W4_IN_BOUNDS(a < p.M * p.k && tile * 16 + row + 8 < p.d, p.dev_status))
+                    continue;
                 float *y = p.y + a * p.d + tile * 16 + row;
                 y[0] = acc[c] * kSub;
                 y[8] = acc[2 + c] * kSub;

@@ -16,6 +16,7 @@
 #include <atomic>
 
 #include "../../include/w4moe.h"
+#include "checks.cuh"
 #include "launch.h"
 #include "ptx.cuh"
 
@@ -101,8 +102,8 @@ __device__ __forceinline__ int owner_of(const int *start, int n, int rank)
 // at[i] + r - start[i] of slot[i].  Returns how many requests, in order, got
 // all of theirs; the pages of the first that did not are given back.  (A request
 // that needs none is served wherever it stands.)
-__device__ int hand_out(PlanShared &s, int n, int total, int32_t *table, int W, int32_t *refs,
-                        int P)
+__device__ int hand_out(PlanShared &s, int n, int total, int32_t *table, int B, int W,
+                        int32_t *refs, int P, int32_t *status)
 {
     const int tid = threadIdx.x;
     int found = 0;
@@ -120,9 +121,11 @@ __device__ int hand_out(PlanShared &s, int n, int total, int32_t *table, int W, 
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             if (open[i] && rank < total) {
-                const int r = owner_of(s.start, n, rank);
-                table[static_cast<int64_t>(s.slot[r]) * W + s.at[r] + rank - s.start[r]] = p + i;
-                refs[p + i] = 1;
+                const int r = owner_of(s.start, n, rank), col = s.at[r] + rank - s.start[r];
+                if (W4_IN_BOUNDS(s.slot[r] >= 0 && s.slot[r] < B && col >= 0 && col < W, status)) {
+                    table[static_cast<int64_t>(s.slot[r]) * W + col] = p + i;
+                    refs[p + i] = 1;
+                }
             }
             rank += open[i];
         }
@@ -142,7 +145,8 @@ __device__ int hand_out(PlanShared &s, int n, int total, int32_t *table, int W, 
     for (int r = s.start[served] + tid; r < found; r += kPlanThreads) {
         int32_t *e = &table[static_cast<int64_t>(s.slot[served]) * W + s.at[served] + r -
                             s.start[served]];
-        refs[*e] = 0;
+        if (W4_IN_BOUNDS(*e >= 0 && *e < P, status))
+            refs[*e] = 0;
         *e = -1;
     }
     return served;
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_reserve_kernel(
         s.start[n] = total;
     __syncthreads();
     // threads past n hold start = total as well, which the search never reaches
-    const int served = hand_out(s, n, total, table, W, refs, P);
+    const int served = hand_out(s, n, total, table, B, W, refs, P, status);
     if (ok) {
         if (i < served || need == 0)
             lens[slot] = want;
@@ -265,7 +269,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(
     if (i == 0)
         s.start[n] = total;
     __syncthreads();               // every length is read before one is written
-    const int served = hand_out(s, n, total, table, W, refs, P);
+    const int served = hand_out(s, n, total, table, B, W, refs, P, status);
     __syncthreads();
     if (i < n) {
         const bool done = ok && (i < served || need == 0);
@@ -317,6 +321,8 @@ __global__ void __launch_bounds__(256) kv_fork_kernel(uint8_t *cache, int64_t pa
     if (blockIdx.y == 0) {
         int32_t *to = table + static_cast<int64_t>(b) * W;
         for (int c = threadIdx.x; c < full; c += blockDim.x) {
+            if (!W4_IN_BOUNDS(c < W, status))
+                break;
             const int p = from[c];
             const bool ok = p >= 0 && p < P;
             to[c] = ok ? p : -1;
@@ -335,8 +341,9 @@ __global__ void __launch_bounds__(256) kv_fork_kernel(uint8_t *cache, int64_t pa
         return;
     }
     uint8_t *plane = cache + static_cast<int64_t>(blockIdx.y) * P * page_bytes;
-    copy_bytes(plane + pl.y * page_bytes, plane + old * page_bytes,
-               page_bytes / page * (len % page));
+    if (W4_IN_BOUNDS(full < W && pl.y < P, status))
+        copy_bytes(plane + pl.y * page_bytes, plane + old * page_bytes,
+                   page_bytes / page * (len % page));
 }
 
 // ------------------------------------------------------------- copy pages
@@ -415,6 +422,8 @@ __global__ void __launch_bounds__(32) kv_copy_kernel(uint8_t *cache, int planes,
                 into = (plane * P + b) * page_bytes + part * kChunk;
                 bytes = static_cast<uint32_t>(min(static_cast<int64_t>(kChunk),
                                                   page_bytes - part * kChunk));
+                if (!W4_IN_BOUNDS(into + bytes <= planes * P * page_bytes, status))
+                    from = -1;
             } else if (plane == 0 && part == 0) {
                 raise_status(status, W4_DEV_BAD_PAGE);
             }
@@ -467,7 +476,7 @@ __global__ void __launch_bounds__(32) kv_copy_kernel(uint8_t *cache, int planes,
 // among those (holes), k-th to k-th: sources and destinations never overlap.
 __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(
     const int32_t *refs, int32_t *refs_out, int P, int32_t *count, int32_t *src, int32_t *dst,
-    int32_t *remap)
+    int32_t *remap, int32_t *status)
 {
     __shared__ int sums[2][33];
     const int tid = threadIdx.x;
@@ -487,9 +496,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(
         // in the round that contains `live` as two halves of a word
         int total;
         const int before = block_exclusive_sum(hole + (mover << 16), sums[round], &total);
-        if (hole)
+        // as many movers as holes: half of the pages at most
+        if (hole && W4_IN_BOUNDS(holes + (before & 0xFFFF) < P / 2, status))
             dst[holes + (before & 0xFFFF)] = p;
-        if (mover)
+        if (mover && W4_IN_BOUNDS(movers + (before >> 16) < P / 2, status))
             src[movers + (before >> 16)] = p;
         if (in)
             remap[p] = p;
@@ -504,6 +514,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(
     __syncthreads();
     for (int i = tid; i < movers; i += kPlanThreads) {
         const int a = src[i], b = dst[i];
+        if (!W4_IN_BOUNDS(a >= 0 && a < P && b >= 0 && b < P, status))
+            continue;
         remap[a] = b;
         refs_out[b] = refs[a];
         refs_out[a] = 0;
@@ -545,6 +557,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs p)
                 raise_status(p.status, W4_DEV_BAD_PAGE);
             continue;
         }
+        if (!W4_IN_BOUNDS(pos - e * p.page >= 0 && pos - e * p.page < p.page, p.status))
+            continue;
         const int64_t to = pg * p.page_stride + (pos - e * p.page) * p.tok_stride;
         // kUnroll 16-byte values of k and of v in flight a lane
         for (int i0 = lane; i0 < p.Hkv * vecs; i0 += 32 * kUnroll) {
@@ -652,7 +666,7 @@ cudaError_t launch_kv_compact(uint8_t *cache, int planes, int64_t page_bytes, co
     int32_t *count = static_cast<int32_t *>(workspace), *src = count + 4;
     int32_t *dst = src + P / 2, *remap = dst + P / 2;
     cudaError_t err = launch_pdl(kv_compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream,
-                                 refs, refs_out, P, count, src, dst, remap);
+                                 refs, refs_out, P, count, src, dst, remap, status);
     if (err != cudaSuccess)
         return err;
     err = raise_copy_limit();
