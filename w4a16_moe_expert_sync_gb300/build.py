@@ -15,7 +15,7 @@ SOURCES = ["api.cu", "quantize.cu", "route_align.cu", "combine.cu", "grouped_gem
            "static_scratch.cu", "rmsnorm.cu", "sampler.cu", "dense_gemm.cu",
            "few.cu", "kv.cu", "attention.cu"]
 HEADERS = ["launch.h", "ptx.cuh", "korder.cuh", "combine_fold.cuh", "checks.cuh",
-           "route_token.cuh"]
+           "route_token.cuh", "attention_plan.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

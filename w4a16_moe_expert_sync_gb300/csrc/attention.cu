@@ -44,6 +44,7 @@
 #include <cuda_fp16.h>
 
 #include "../../include/w4moe.h"
+#include "attention_plan.cuh"
 #include "checks.cuh"
 #include "launch.h"
 #include "ptx.cuh"
@@ -52,8 +53,13 @@ namespace w4 {
 
 namespace {
 
-constexpr int kRows = 128;                 // rows of a stream's tile
-constexpr int kKeys = 128;                 // keys of a tile
+using plan::kItemCost;
+using plan::kKeys;
+using plan::kRows;
+using plan::pair_ctas;
+using plan::worker_begin;
+using plan::worker_of;
+
 constexpr int kThreads = 32 * 12;
 // Registers a thread: 168 at launch; the loading warps give some of theirs to
 // the softmax warps, which hold a row of 128 scores (2 x 216 + 72 = 3 x 168).
@@ -121,42 +127,6 @@ struct AttnArgs {
     int rows_b;                            // a sequence's single item's rows at most
     int cap_a, cap_g, cap_b;               // pieces that the workspace holds; cap_b: all single
 };
-
-// An item is kItemCost + its tiles long when the work is split: fetching its
-// queries and storing its sums takes about as long as that many tiles.  (With 1
-// and 3 instead of 2: 64 ragged sequences behind 8192 tokens 61.4 and 60.4 us
-// against 58.6, four canvases of 256 queries 57.0 and 47.5 against 46.7, nine small
-// groups 25.8 and 27.3 against 26.3.)
-constexpr int kItemCost = 2;
-// A CTA's time for a single tile in those of a pair's, as the CTAs are divided
-// between the two.  (With 0.5, 0.7, 1.0: 120,000 shared tokens and short tails 84.6,
-// 73.6 and 75.7 us, nine small groups 27.6, 26.2 and 27.4.  Both kinds on every CTA, the
-// pairs first: 74.1 and 32.7.)
-constexpr float kSingleWeight = 0.7f;
-
-// Worker w's share of a region's `all` begins here.
-__device__ __forceinline__ int worker_begin(int all, int workers, int w)
-{
-    if (all < (1 << 22))                       // workers <= 512: 32 bits do
-        return static_cast<int>(static_cast<uint32_t>(all) * w / workers);
-    return static_cast<int>(static_cast<int64_t>(all) * w / workers);
-}
-// The worker whose share place x is in.
-__device__ __forceinline__ int worker_of(int all, int workers, int x)
-{
-    if (all < (1 << 22))                       // workers <= 512: 32 bits do
-        return static_cast<int>((static_cast<uint32_t>(x + 1) * workers - 1) / all);
-    return static_cast<int>((static_cast<int64_t>(x + 1) * workers - 1) / all);
-}
-// How many CTAs take the pairs; the others, two streams each, take the single
-// items.  No worker goes without a share.
-__device__ __forceinline__ int pair_ctas(int singles, int pairs, int grid)
-{
-    if (pairs == 0 || singles == 0)
-        return min(pairs, grid);
-    const float part = pairs / (pairs + kSingleWeight * singles);
-    return min(pairs, max(1, min(grid - 1, static_cast<int>(part * grid + 0.5f))));
-}
 
 // ------------------------------------------------------------- tensor memory
 // All 128 columns of this thread's lane, and the wait for them.
@@ -387,10 +357,8 @@ __device__ __forceinline__ Work work_of(const AttnArgs &p, const Index &x, int e
     }
     const int rows = w.tokens * p.rep;
     if (rows > 0 && w.k1 > w.k0) {
-        const int base = w.k0 >> p.page_shift << p.page_shift;
-        const bool pair = rows > kRows;
-        w.span = (w.k1 - base + kKeys - 1) / kKeys + kItemCost;
-        w.row_tiles_pair = pair ? 2 * ((rows + 2 * kRows - 1) / (2 * kRows)) + 1 : 2;
+        w.span = plan::key_tiles(w.k0, w.k1, p.page_shift) + kItemCost;
+        w.row_tiles_pair = 2 * plan::row_tiles(rows) + plan::is_pair(rows);
     }
     return w;
 }
@@ -480,7 +448,7 @@ struct Kernel {
     // The plan: this CTA's pieces into the workspace, the first ones also into
     // shared memory.  Scratch is the queries' room and the ring (192 KB at least,
     // 48 bytes an entry), before anything is loaded into them.
-    static __device__ void plan(const AttnArgs &p, Shared &s, uint8_t *scratch)
+    static __device__ void make_plan(const AttnArgs &p, Shared &s, uint8_t *scratch)
     {
         const int n = p.G + p.B, tid = threadIdx.x;
         Work *work = reinterpret_cast<Work *>(scratch);                // [n]
@@ -586,12 +554,9 @@ struct Kernel {
                 g.rows = min(step, wa.tokens * p.rep - g.row0);
                 g.tile0 = max(lo - t0, 0);
                 int end = min(hi - t0, wa.span - kItemCost);
-                if (p.causal && g.seq >= 0) {
-                    // no row of this item sees beyond its last token's position
-                    const int last = (g.row0 + g.rows - 1) / p.rep;
-                    const int limit = wa.k1 - wa.tokens + last + 1;
-                    end = min(end, (max(limit - g.kbase, 0) + kKeys - 1) / kKeys);
-                }
+                if (p.causal && g.seq >= 0)
+                    end = min(end, plan::causal_tiles(wa.k1, wa.tokens, g.kbase,
+                                                      g.row0 + g.rows - 1, p.rep));
                 g.tiles = max(end - g.tile0, 0);
                 g.piece = item + w;
                 if (W4_IN_BOUNDS(g.piece >= 0 && g.piece < (pair ? p.cap_a : p.cap_b), p.status))
@@ -630,14 +595,9 @@ struct Kernel {
         __syncthreads();
     }
 
-    // The pair of slots (K, then V) of a pair's tile r, or of a stream's tile r
-    // of its single items: the loader takes the streams' tiles in turn, and a
-    // stream that has none left drops out.  A CTA has pairs or single items.
     static __device__ __forceinline__ int fill_of(const Shared &s, int which, int r)
     {
-        if (which == 2)
-            return r;
-        return r + (which == 0 ? min(r, s.tiles[1]) : min(r + 1, s.tiles[0]));
+        return plan::fill_of(s.tiles[0], s.tiles[1], which, r);
     }
 
     // Every wait has a limit.  A role whose wait gives up, by the limit or because
@@ -1301,7 +1261,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
     pdl_wait();
     pdl_trigger();
-    K::plan(p, s, qbuf);
+    K::make_plan(p, s, qbuf);
     fence_proxy_async_smem();              // the plan's scratch becomes queries and ring
     tc_fence_before();
     __syncthreads();
@@ -1531,12 +1491,10 @@ Space space_of(int T, int B, int G, int max_q, int Hq, int Hkv, int D)
 {
     Space s{};
     const int64_t rep = Hq / Hkv;
-    // Each worker cuts at most one item more.  An entry of R > 128 rows has at
-    // most R / 128 pair items, and a row is in two entries; groups come first
-    // among the single items.
-    s.cap_a = static_cast<int>(std::min<int64_t>(2 * T * rep / kRows * Hkv, 1 << 24)) + kMaxGrid;
-    s.cap_g = G * Hkv + 2 * kMaxGrid;
-    s.cap_b = s.cap_g + B * Hkv;
+    const plan::Caps caps = plan::caps_of(T, rep, B, G, Hkv, kMaxGrid);
+    s.cap_a = caps.pairs;
+    s.cap_g = caps.groups;
+    s.cap_b = caps.singles;
     s.rows_b = static_cast<int>(std::min<int64_t>(rep * max_q, kRows));
     size_t at = 0;
     auto take = [&](size_t bytes) {
