@@ -410,7 +410,8 @@ def w4_moe_layer_workspace_size(M, d, m, E, k, block_m=16) -> int:
 def w4_moe_layer(x, topk_ids, topk_weights, gu, dn, block_m: int = 16, gu_group: int = 128,
                  dn_group: int = 64, workspace=None, out=None, dev_status=None, stream=None):
     """The whole routed-expert layer (align+gather, gate_up + activation,
-    down, fixed-order combine) as four launches on the current stream."""
+    down, fixed-order combine) as four launches on the current stream.  For up
+    to 32 tokens w4_moe_layer_few is the faster one."""
     import torch
     gu_q, gu_s, gu_z = gu
     dn_q, dn_s, dn_z = dn
@@ -497,7 +498,8 @@ def w4_moe_layer_from_logits(x, logits, k: int, gu, dn, block_m: int = 16, gu_gr
                              dn_group: int = 64, workspace=None, out=None, ids=None,
                              weights=None, dev_status=None, stream=None):
     """w4_moe_layer with the router in its first launch: from the logits
-    [M, E] fp32.  Returns (out, topk_ids, topk_weights)."""
+    [M, E] fp32.  Returns (out, topk_ids, topk_weights).  For up to 32 tokens
+    w4_moe_layer_few_from_logits is the faster one."""
     import torch
     gu_q, gu_s, gu_z = gu
     dn_q, dn_s, dn_z = dn

@@ -33,7 +33,7 @@
 //     some 3000 cycles a tile; its MMAs take 2048, and so do the 256 KB that it
 //     moves through shared memory (their operands, and K and V as they land).
 //     Without the exponentials it is 1 to 3 % faster: the softmax does not pace it
-//   64 sequences of 33 to 1500 tokens behind 8192: 58 us; 242 MB (36 us).  Plan 4 us,
+//   64 sequences of 33 to 1500 tokens behind 8192: 59 us; 242 MB (36 us).  Plan 4 us,
 //     first tile 6, change of piece 1.5 each, join and its launch 6
 //   four times 256 queries over 4096 + 256: 46 us; 37 GFLOP (19 us), the pairs' loop
 //   two sequences of 240 tokens: 14 us, all of it plan, one tile and join
@@ -98,9 +98,9 @@ struct Seg {
 // each of a page's tokens, and the 64-value blocks of a K or V tile lie one after the
 // other.  Pages of kShortPage tokens with more than one such block have a box with all
 // of them, which lie in turn there, 8 tokens each: half as many boxes.  (128 sequences
-// of 6000 tokens in pages of 16, heads of 128: 104 us by kRows, 87 like this; larger
-// pages gain nothing.)  The axes are then 64 values, 8 tokens, blocks, the page's groups
-// of 8 tokens and one more: with the heads side by side their blocks are one axis, with
+// of 6000 tokens in pages of 16, one kv and two query heads of 128, 396 MB: 104 us by
+// kRows, 87 like this; larger pages gain nothing.)  The axes are then 64 values, 8 tokens,
+// blocks, the page's groups of 8 tokens and one more: with the heads side by side their blocks are one axis, with
 // the heads of all pages evenly spaced they are one axis with the pages; else
 // (kGroups) a box is 8 tokens.
 enum class PageView { kRows, kHeadsAsBlocks, kHeadsAsPages, kGroups };

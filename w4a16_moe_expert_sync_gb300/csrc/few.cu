@@ -28,11 +28,12 @@
 // are requested before the grid barrier that ends gate_up.
 //
 // Bound by HBM.  Measured at d = 2816, m = 704, E = 128, k = 8 (GB300, back to back in
-// a graph): 1 token 18.4 us (25.8 MB, 3.8 us at the copy bandwidth: routing, jobs, two
-// grid barriers and the first loads' latency), 7 tokens 45 us (150 MB, 22 us), 32
-// tokens 89 us (360 MB, 53 us).  At 32 tokens gate_up streams at 6.5 TB/s after 9 us of
-// routing and staging, down, with twice the scales, at 5.3; each barrier waits 2 to 7 us
-// for the last CTA.
+// a graph): 1 token 19.0 us (25.8 MB, 3.8 us at the copy bandwidth), 7 tokens 44 us (150
+// MB, 22 us), 32 tokens 87 us (360 MB, 53 us).  Clocks of one token: routing and jobs 2.5,
+// first requests 1.8, staging 1, gate_up's units 2.3 and its end 1.7, barrier 2.6, down's
+// staging 1.3, units 1.3 and end 1.3, barrier 2.4, the rest launch and combine.  At 32
+// tokens gate_up streams at 6.4 TB/s after 9.4 us of routing and staging, down, with twice
+// the scales, at 5.0; CTAs wait 2.4 to 8 us at the first barrier, 1 to 3.5 at the second.
 #include <algorithm>
 #include <atomic>
 #include <cooperative_groups.h>
@@ -881,8 +882,8 @@ cudaError_t launch_variant(FewArgs a, int dev, int sms, cudaStream_t stream)
 
 // Sixteen warps with two units each in flight where the scales' rings and a
 // job's columns leave room for it, else eight warps with three.  (At d = 2816, m = 704,
-// sixteen and eight: 1 token 18.6 and 18.4 us, 7 tokens 42.4 and 49.8, 32 tokens 83.6 and
-// 104.8.)
+// sixteen and eight: 1 token 18.6 and 18.6 us, 7 tokens 45.4 and 54.8, 32 tokens 89 and
+// 117.)
 bool wide_fits(int d, int m)
 {
     int sb, cols;

@@ -9,9 +9,10 @@
 // the pool's front stays dense.  Finding them is a scan of refs by one CTA
 // (4096 pages a round, 7 to 10 us for a few thousand pages); the rest are plain
 // grid-wide copies, bound by HBM.  Measured on GB300, against the bytes at the copy
-// bandwidth: whole pages 1.47 GB in 232 us (217) and 2.61 GB in 382 us (385, with the
-// plan and the table); releasing, reserving and filling 48 prompts, 574 MB, 97 us (85);
-// releasing and forking 96 drafts, 271 MB, 40 us (40).
+// bandwidth: whole pages 1.47 GB in 232 us (217) and, with the plan and the table, 2.50 to
+// 2.63 GB in 372 to 404 us (369 to 388: how many pages move, and from where, differs);
+// releasing, reserving and filling 48 prompts, 574 MB, 98 us (85); releasing and forking
+// 96 drafts, 271 MB, 41 us (40).
 #include <algorithm>
 #include <atomic>
 
