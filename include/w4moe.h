@@ -667,6 +667,93 @@ int w4_kv_append(uint16_t *k_pages, uint16_t *v_pages, int64_t page_stride, int6
                  int64_t v_head_stride, const int32_t *q_offsets, int T, int32_t *dev_status,
                  w4_stream_t stream);
 
+/* w4_kv_keep -- keep the accepted ones of each slot's new tokens (a path of a
+ * tree of drafts) and take the others back, in every plane: slot b's last
+ * n = q_offsets[b + 1] - q_offsets[b] tokens are new, and those of them that
+ * kept[kept_offsets[b]] .. kept[kept_offsets[b + 1] - 1] name (counted from the
+ * first new one, strictly ascending) move together behind the older ones.
+ *   q_offsets, kept_offsets  [B + 1] int32, ascending
+ *   kept                     [n_kept] int32
+ *   lens_out                 [B] out: lens[b] - n + the number kept; may be lens
+ * The slot keeps its pages, as where the caller lowers a length himself.  A slot
+ * whose new tokens lie in a page that others hold (refs > 1) and would be written
+ * there, whose lists do not ascend within their bounds or whose new tokens are more
+ * than its length (W4_DEV_BAD_SLOT), or with a page id outside [0, P) among those
+ * concerned (W4_DEV_BAD_PAGE), is left as it was.  B = 0 does nothing.
+ * Requires W * page_size below 2^31.  One launch. */
+int w4_kv_keep(void *pool, int planes, int64_t page_bytes, const int32_t *table, int B, int W,
+               const int32_t *lens, const int32_t *refs, int P, const int32_t *q_offsets,
+               const int32_t *kept, const int32_t *kept_offsets, int n_kept, int page_size,
+               int32_t *lens_out, int32_t *dev_status, w4_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * w4_rope_steps -- the table of a position rotation's frequencies that the calls
+ * below take.  steps is HOST memory, [rot / 2] int64: copy it to the device once.
+ * Pair i turns by f_i = base^(-2 i / rot) radians a position, where the context is
+ * to be longer than the one trained (factor > 1) by
+ *   W4_ROPE_LINEAR  f_i / factor
+ *   W4_ROPE_BASE    base times factor^(rot / (rot - 2)): the slowest pair's frequency
+ *                   divided by factor, the fastest's kept
+ *   W4_ROPE_PARTS   f_i g + f_i / factor (1 - g), g = (r - low) / (high - low) within
+ *                   [0, 1], r = trained_len f_i / (2 pi) the turns within the trained
+ *                   length: what turns often is kept, what turns seldom divided
+ * trained_len, low and high are read by W4_ROPE_PARTS only; factor = 1 changes
+ * nothing.  A step is f_i / (2 pi) modulo 1 in units of 2^-64, so that an angle is
+ * an integer product that drops whole turns exactly.  Host only: no GPU needed.
+ * ------------------------------------------------------------------------ */
+#define W4_ROPE_LINEAR 0
+#define W4_ROPE_BASE 1
+#define W4_ROPE_PARTS 2
+int w4_rope_steps(int rot, double base, int method, double factor, double trained_len, double low,
+                  double high, int64_t *steps);
+
+/* --------------------------------------------------------------------------
+ * w4_qk_norm_rope -- queries and keys of new tokens, normed for each head and
+ * rotated by their position, in one pass:
+ *   u = x / sqrt(mean(x^2) + eps) * weight over a head's D values (without a weight
+ *   u = x), then for the pairs (a, b) of its first `rot` values, at angle
+ *   t = position * f_i:  (a cos t - b sin t, a sin t + b cos t) * amplitude
+ *
+ *   q, k        [T, Hq, D], [T, Hkv, D] 16-bit, strides of tokens and heads in
+ *               elements; Hq or Hkv may be 0
+ *   positions   [T] int32, any values
+ *   steps       [rot / 2] int64 on the device, from w4_rope_steps; rot = 0: no rotation
+ *   q_weight, k_weight  [D] of q's type, or NULL: no norm
+ *   interleaved 0: pair i is values i and i + rot / 2; else 2 i and 2 i + 1
+ *   dtype       0: bf16, 1: fp16
+ *   amplitude   multiplies the rotated values (1 where nothing asks for another)
+ *   q_out, k_out  like q and k, with strides of their own; they may be q and k
+ * Arithmetic is fp32, every value rounded once; angles are exact to 2^-31 of a turn
+ * for positions up to 2^23 (beyond, the frequencies' rounding to 53 bits shows).  Requires D a multiple of 8 up to 256, rot a multiple of 16 up
+ * to D, pointers 16-byte aligned, strides multiples of 8 elements.  One launch.
+ * ------------------------------------------------------------------------ */
+int w4_qk_norm_rope(const uint16_t *q, int64_t q_tok_stride, int64_t q_head_stride,
+                    const uint16_t *k, int64_t k_tok_stride, int64_t k_head_stride,
+                    const int32_t *positions, const int64_t *steps, const uint16_t *q_weight,
+                    const uint16_t *k_weight, int T, int Hq, int Hkv, int D, int rot,
+                    int interleaved, int dtype, float eps, float amplitude, uint16_t *q_out,
+                    int64_t q_out_tok_stride, int64_t q_out_head_stride, uint16_t *k_out,
+                    int64_t k_out_tok_stride, int64_t k_out_head_stride, w4_stream_t stream);
+
+/* w4_kv_append_rope -- w4_qk_norm_rope on the way into a paged cache: the queries
+ * go to q_out, the keys, normed and rotated, and the values, as they are, to their
+ * pages as by w4_kv_append (arguments as there and above).
+ *   positions   [T] int32 of the rotation, or NULL: a token's place in its sequence
+ *               (drafts of a tree stand at their depth instead)
+ * A token whose page is none (W4_DEV_BAD_PAGE) has its query written all the same.
+ * Rows of no sequence are not written.  With offsets that do not ascend within
+ * [0, T] nothing is (W4_DEV_BAD_SLOT).  Hq may be 0.  One launch. */
+int w4_kv_append_rope(uint16_t *k_pages, uint16_t *v_pages, int64_t page_stride, int64_t tok_stride,
+                      int64_t head_stride, int P, int page_size, const int32_t *table, int B, int W,
+                      const int32_t *lens, const uint16_t *q, int64_t q_tok_stride,
+                      int64_t q_head_stride, const uint16_t *k, int64_t k_tok_stride,
+                      int64_t k_head_stride, const uint16_t *v, int64_t v_tok_stride,
+                      int64_t v_head_stride, const int32_t *q_offsets, const int32_t *positions,
+                      const int64_t *steps, const uint16_t *q_weight, const uint16_t *k_weight,
+                      int T, int Hq, int Hkv, int D, int rot, int interleaved, int dtype, float eps,
+                      float amplitude, uint16_t *q_out, int64_t q_out_tok_stride,
+                      int64_t q_out_head_stride, int32_t *dev_status, w4_stream_t stream);
+
 /* --------------------------------------------------------------------------
  * w4_attn_shared_prefix -- attention over the paged cache for a batch whose
  * sequences share prefixes, each prefix read and multiplied once for its group

@@ -109,6 +109,13 @@ def load_library(path: str | None = None):
             "w4_kv_compact": ([V, I, I64, V, I, I, V, I, V, V, V, SZ, V, V], I),
             "w4_kv_append": ([V, V, I64, I64, I64, I, I, I, I, V, I, I, V, V, I64, I64, V, I64, I64,
                               V, I, V, V], I),
+            "w4_kv_keep": ([V, I, I64, V, I, I, V, V, I, V, V, V, I, I, V, V, V], I),
+            "w4_rope_steps": ([I, ctypes.c_double, I] + [ctypes.c_double] * 4 + [V], I),
+            "w4_qk_norm_rope": ([V, I64, I64, V, I64, I64, V, V, V, V, I, I, I, I, I, I, I,
+                                 ctypes.c_float, ctypes.c_float, V, I64, I64, V, I64, I64, V], I),
+            "w4_kv_append_rope": ([V, V, I64, I64, I64, I, I, V, I, I, V, V, I64, I64, V, I64, I64,
+                                   V, I64, I64, V, V, V, V, V, I, I, I, I, I, I, I, ctypes.c_float,
+                                   ctypes.c_float, V, I64, I64, V, V], I),
             "w4_attn_shared_prefix_workspace_size": ([I, I, I, I, I, I, I], SZ),
             "w4_attn_shared_prefix": ([V, I64, I64, V, V, I64, I64, I64, I, I, V, I, V, V, I, I, I,
                                        V, V, I, I, I, I, I, I, ctypes.c_float, V, SZ, V, V, V], I),
@@ -899,6 +906,141 @@ def w4_kv_append(k_pages, v_pages, table, lens, k, v, q_offsets, dev_status=None
         k_pages.data_ptr(), v_pages.data_ptr(), *strides[:3], P, page, Hkv, D, table.data_ptr(), B,
         W, lens.data_ptr(), k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
         q_offsets.data_ptr(), k.shape[0], _ptr(dev_status), _stream(stream)), "w4_kv_append")
+
+
+def w4_kv_keep(pool, table, lens, refs, q_offsets, kept, kept_offsets, lens_out=None,
+               dev_status=None, stream=None):
+    """Keep the accepted ones of each slot's new tokens: of slot b's last
+    q_offsets[b + 1] - q_offsets[b] tokens those that kept[kept_offsets[b]:
+    kept_offsets[b + 1]] names (ascending, from 0) move together in every plane,
+    the others are taken back.  Returns the new lengths: lens_out, by default
+    lens itself."""
+    lens_out = lens if lens_out is None else lens_out
+    B, W, P = _kv_state(table, lens, refs, dev_status)
+    planes, page_bytes, page = _kv_pool(pool, P)
+    _require_int32(q_offsets, kept, kept_offsets, lens_out)
+    if q_offsets.shape != (B + 1,) or kept_offsets.shape != (B + 1,) or kept.dim() != 1 or \
+            lens_out.shape != lens.shape:
+        raise ValueError("q_offsets and kept_offsets must be [B + 1], kept a list, lens_out [B]")
+    _on_current_device(pool, table, lens, refs, q_offsets, kept, kept_offsets, lens_out, dev_status)
+    _check(load_library().w4_kv_keep(_ptr(pool), planes, page_bytes, _ptr(table), B, W, _ptr(lens),
+                                     _ptr(refs), P, _ptr(q_offsets), _ptr(kept), _ptr(kept_offsets),
+                                     kept.shape[0], page, _ptr(lens_out), _ptr(dev_status),
+                                     _stream(stream)), "w4_kv_keep")
+    return lens_out
+
+
+# --------------------------------------------------------------------------
+# Norms and rotation of queries and keys
+# --------------------------------------------------------------------------
+_ROPE_METHODS = {"linear": 0, "base": 1, "parts": 2}
+
+
+def w4_rope_steps(rot: int, base: float = 10000.0, method: str = "linear", factor: float = 1.0,
+                  trained_len: float = 0.0, low: float = 0.0, high: float = 0.0, device="cuda"):
+    """The rotation's frequencies base^(-2 i / rot) as a table [rot / 2] int64 for
+    w4_qk_norm_rope and w4_kv_append_rope, made once.  For contexts longer than the
+    trained one by `factor`: method "linear" divides them by it, "base" raises the
+    base, "parts" divides those that turn less than `low` times within trained_len,
+    keeps those that turn more than `high` times and mixes between."""
+    import torch
+    if method not in _ROPE_METHODS:
+        raise ValueError(f"method must be one of {sorted(_ROPE_METHODS)}")
+    steps = torch.empty(max(rot // 2, 0), dtype=torch.int64)
+    _check(load_library().w4_rope_steps(rot, base, _ROPE_METHODS[method], factor, trained_len, low,
+                                        high, _ptr(steps)), "w4_rope_steps")
+    return steps.to(device)
+
+
+def _on_current_device(*ts):
+    """The kernels run on the current device: tensors of another one are refused."""
+    import torch
+    dev = torch._C._cuda_getDevice()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors passed to the CUDA library must live on the current device")
+
+
+def _rope_inputs(q, k, steps, positions, q_weight, k_weight, q_out, stream):
+    """(type, T, Hq, Hkv, D, strides of q, k and q_out, q_out) of a rotation's inputs."""
+    import torch
+    dtype = q.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError("q and k must be bf16 or fp16")
+    qs, ks = _rows16(q, dtype, "q"), _rows16(k, dtype, "k")
+    if q.dim() != 3 or k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D]")
+    T, Hq, D = q.shape
+    if steps.dtype is not torch.int64 or steps.dim() != 1 or not steps.is_contiguous():
+        raise ValueError("steps must be a table of w4_rope_steps")
+    if positions is not None:
+        _require_int32(positions)
+        if positions.shape != (T,):
+            raise ValueError("positions must be [T]")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _require(((w, dtype, (D,), name),))
+    if q_out is None:
+        q_out = _result((T, Hq, D), dtype, q.device, stream)
+    elif q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    os_ = _rows16(q_out, dtype, "q_out")
+    _on_current_device(q, k, steps, positions, q_weight, k_weight, q_out)
+    return dtype, T, Hq, k.shape[1], D, qs, ks, os_, q_out
+
+
+def w4_qk_norm_rope(q, k, positions, steps, q_weight=None, k_weight=None, eps: float = 1e-6,
+                    interleaved: bool = False, amplitude: float = 1.0, q_out=None, k_out=None,
+                    stream=None):
+    """Queries [T, Hq, D] and keys [T, Hkv, D] (any strides of tokens and heads)
+    normed for each head (with a weight [D]) and their first 2 len(steps) values
+    rotated by positions [T] int32, in one pass.  Returns (q_out, k_out); they may
+    be q and k themselves."""
+    dtype, T, Hq, Hkv, D, qs, ks, os_, q_out = _rope_inputs(q, k, steps, positions, q_weight,
+                                                            k_weight, q_out, stream)
+    import torch
+    if positions is None:
+        raise ValueError("positions must be [T]")
+    if k_out is None:
+        k_out = _result(k.shape, dtype, k.device, stream)
+    elif k_out.shape != k.shape:
+        raise ValueError("k_out must have k's shape")
+    kos = _rows16(k_out, dtype, "k_out")
+    _on_current_device(k_out)
+    _check(load_library().w4_qk_norm_rope(
+        q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], positions.data_ptr(),
+        steps.data_ptr(), _ptr(q_weight), _ptr(k_weight), T, Hq, Hkv, D, 2 * steps.shape[0],
+        int(interleaved), 0 if dtype is torch.bfloat16 else 1, eps, amplitude, q_out.data_ptr(),
+        os_[0], os_[1], k_out.data_ptr(), kos[0], kos[1], _stream(stream)), "w4_qk_norm_rope")
+    return q_out, k_out
+
+
+def w4_kv_append_rope(k_pages, v_pages, table, lens, q, k, v, q_offsets, steps, positions=None,
+                      q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                      amplitude: float = 1.0, q_out=None, dev_status=None, stream=None):
+    """w4_qk_norm_rope and w4_kv_append in one pass: returns the queries, writes the
+    keys and values [T, Hkv, D] of the slots' last tokens into their pages.
+    positions defaults to the tokens' places in their sequences."""
+    import torch
+    kdtype, (P, page, Hkv, D), strides = _kv_planes(k_pages, v_pages)
+    dtype, T, Hq, k_heads, q_d, qs, ks, os_, q_out = _rope_inputs(q, k, steps, positions, q_weight,
+                                                                  k_weight, q_out, stream)
+    vs = _rows16(v, dtype, "v")
+    _require_int32(table, lens, q_offsets, dev_status)
+    if kdtype is not dtype or k_heads != Hkv or q_d != D or v.shape != k.shape:
+        raise ValueError("k and v must be [T, Hkv, D] of the pages' type")
+    B, W = _kv_batch(table, lens, q_offsets)
+    _on_current_device(k_pages, v_pages, table, lens, v, q_offsets, dev_status)
+    if B == 0:
+        return q_out
+    _check(load_library().w4_kv_append_rope(
+        k_pages.data_ptr(), v_pages.data_ptr(), *strides[:3], P, page, table.data_ptr(), B, W,
+        lens.data_ptr(), q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(),
+        vs[0], vs[1], q_offsets.data_ptr(), _ptr(positions), steps.data_ptr(), _ptr(q_weight),
+        _ptr(k_weight), T, Hq, Hkv, D, 2 * steps.shape[0], int(interleaved),
+        0 if dtype is torch.bfloat16 else 1, eps, amplitude, q_out.data_ptr(), os_[0], os_[1],
+        _ptr(dev_status), _stream(stream)), "w4_kv_append_rope")
+    return q_out
 
 
 def w4_attn_shared_prefix_workspace_size(T: int, B: int, G: int, max_q: int, Hq: int, Hkv: int,

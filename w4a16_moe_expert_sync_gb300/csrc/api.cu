@@ -2,6 +2,7 @@
 // validation on the host, then kernel launches on the caller's stream.  No
 // device allocation, no synchronisation, no device-to-host reads.
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -1049,6 +1050,238 @@ int w4_kv_append(uint16_t *k_pages, uint16_t *v_pages, int64_t page_stride, int6
     a.T = T;
     cudaError_t err = w4::launch_kv_append(a, as_stream(stream));
     return err == cudaSuccess ? W4_OK : cuda_fail(err, "kv_append launch");
+}
+
+int w4_kv_keep(void *pool, int planes, int64_t page_bytes, const int32_t *table, int B, int W,
+               const int32_t *lens, const int32_t *refs, int P, const int32_t *q_offsets,
+               const int32_t *kept, const int32_t *kept_offsets, int n_kept, int page_size,
+               int32_t *lens_out, int32_t *dev_status, w4_stream_t stream)
+{
+    if (n_kept < 0 || B < 0)
+        return fail(W4_ERR_INVALID_ARG, "bad sizes n_kept=%d B=%d", n_kept, B);
+    if (B == 0)
+        return W4_OK;
+    if (int rc = check_kv_state(table, B, W, lens, refs, P))
+        return rc;
+    if (int rc = check_kv_pool(pool, planes, page_bytes, page_size))
+        return rc;
+    if (!q_offsets || !kept_offsets || !lens_out || (n_kept > 0 && !kept))
+        return fail(W4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned4(q_offsets) || !aligned4(kept) || !aligned4(kept_offsets) || !aligned4(lens_out))
+        return fail(W4_ERR_MISALIGNED, "index arrays must be 4-byte aligned");
+    if (static_cast<int64_t>(W) * page_size >= (1ll << 31) || B > (1 << 24))
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "need W * page_size below 2^31 and B up to 2^24");
+    if (int rc = check_device())
+        return rc;
+    w4::KvKeep k{};
+    k.pool = static_cast<uint8_t *>(pool);
+    k.page_bytes = page_bytes;
+    k.table = table;
+    k.lens = lens;
+    k.refs = refs;
+    k.q_offsets = q_offsets;
+    k.kept = kept;
+    k.kept_offsets = kept_offsets;
+    k.lens_out = lens_out;
+    k.dev_status = dev_status;
+    k.planes = planes;
+    k.P = P;
+    k.B = B;
+    k.W = W;
+    k.page = page_size;
+    k.n_kept = n_kept;
+    cudaError_t err = w4::launch_kv_keep(k, as_stream(stream));
+    return err == cudaSuccess ? W4_OK : cuda_fail(err, "kv_keep launch");
+}
+
+// --------------------------------------------------- norms and rotation
+int w4_rope_steps(int rot, double base, int method, double factor, double trained_len, double low,
+                  double high, int64_t *steps)
+{
+    if (rot < 0 || rot % 2 || (rot > 0 && !steps))
+        return fail(W4_ERR_INVALID_ARG, "rot must be even (got %d) and steps not NULL", rot);
+    if (!(base > 0.0) || !std::isfinite(base) || !(factor > 0.0) || !std::isfinite(factor))
+        return fail(W4_ERR_INVALID_ARG, "base and factor must be positive and finite");
+    if (method != W4_ROPE_LINEAR && method != W4_ROPE_BASE && method != W4_ROPE_PARTS)
+        return fail(W4_ERR_INVALID_ARG, "unknown method %d", method);
+    if (method == W4_ROPE_PARTS && (!(trained_len > 0.0) || !std::isfinite(trained_len) ||
+                                    !(high > low) || !std::isfinite(high) || !std::isfinite(low)))
+        return fail(W4_ERR_INVALID_ARG, "need trained_len > 0 and low < high");
+    if (method == W4_ROPE_BASE && rot == 2)
+        return fail(W4_ERR_INVALID_ARG, "raising the base needs rot > 2");
+    constexpr double kTurn = 6.283185307179586476925286766559;
+    const double b =
+        method == W4_ROPE_BASE && rot > 2 ? base * std::pow(factor, rot / (rot - 2.0)) : base;
+    for (int i = 0; i < rot / 2; i++) {
+        const double f = std::pow(b, -2.0 * i / rot);
+        double scaled = method == W4_ROPE_LINEAR ? f / factor : f;
+        if (method == W4_ROPE_PARTS) {
+            const double turns = trained_len * f / kTurn;
+            const double x = (turns - low) / (high - low), keep = x < 0.0 ? 0.0 : x > 1.0 ? 1.0 : x;
+            scaled = f * keep + f / factor * (1.0 - keep);
+        }
+        // the fraction of a turn: whole turns at integer positions change nothing
+        const double turns = scaled / kTurn, part = turns - std::floor(turns);
+        const double bits = std::ldexp(part, 64);
+        steps[i] = static_cast<int64_t>(bits < 18446744073709551616.0 ? static_cast<uint64_t>(bits)
+                                                                      : 0);
+    }
+    return W4_OK;
+}
+
+namespace {
+// What both rotations ask of queries, keys, weights and steps.
+int check_rope(const w4::RopeProblem &r, float eps)
+{
+    if (r.T < 0 || r.Hq < 0 || r.Hkv < 0 || r.D <= 0 || r.rot < 0)
+        return fail(W4_ERR_INVALID_ARG, "bad sizes T=%d Hq=%d Hkv=%d D=%d rot=%d", r.T, r.Hq,
+                    r.Hkv, r.D, r.rot);
+    if (!(eps >= 0.0f) || !std::isfinite(eps) || !std::isfinite(r.amplitude))
+        return fail(W4_ERR_INVALID_ARG, "eps must not be negative, eps and amplitude finite");
+    if (r.D % 8 || r.D > 256)
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "D must be a multiple of 8 up to 256 (got %d)", r.D);
+    if (r.rot % 16 || r.rot > r.D)
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "rot must be a multiple of 16 up to D (got %d of %d)",
+                    r.rot, r.D);
+    if (static_cast<int64_t>(r.Hq) + 2ll * r.Hkv > 65536)
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "need Hq + 2 Hkv up to 65536 (got %d, %d)", r.Hq,
+                    r.Hkv);
+    if (r.T > 0 && ((r.Hq > 0 && (!r.q || !r.q_out)) || (r.Hkv > 0 && !r.k) ||
+                    (r.rot > 0 && !r.steps)))
+        return fail(W4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned16(r.q) || !aligned16(r.k) || !aligned16(r.q_out) || !aligned16(r.q_weight) ||
+        !aligned16(r.k_weight) ||
+        (r.q_tok | r.q_head | r.k_tok | r.k_head | r.q_out_tok | r.q_out_head) & 7)
+        return fail(W4_ERR_MISALIGNED, "queries, keys and weights must be 16-byte aligned and "
+                                       "strides multiples of 8 elements");
+    if (!aligned4(r.positions) || (reinterpret_cast<uintptr_t>(r.steps) & 7u))
+        return fail(W4_ERR_MISALIGNED, "positions must be 4-byte, steps 8-byte aligned");
+    return W4_OK;
+}
+}  // namespace
+
+int w4_qk_norm_rope(const uint16_t *q, int64_t q_tok_stride, int64_t q_head_stride,
+                    const uint16_t *k, int64_t k_tok_stride, int64_t k_head_stride,
+                    const int32_t *positions, const int64_t *steps, const uint16_t *q_weight,
+                    const uint16_t *k_weight, int T, int Hq, int Hkv, int D, int rot,
+                    int interleaved, int dtype, float eps, float amplitude, uint16_t *q_out,
+                    int64_t q_out_tok_stride, int64_t q_out_head_stride, uint16_t *k_out,
+                    int64_t k_out_tok_stride, int64_t k_out_head_stride, w4_stream_t stream)
+{
+    w4::RopeProblem r{};
+    r.q = q;
+    r.q_tok = q_tok_stride;
+    r.q_head = q_head_stride;
+    r.k = k;
+    r.k_tok = k_tok_stride;
+    r.k_head = k_head_stride;
+    r.q_out = q_out;
+    r.q_out_tok = q_out_tok_stride;
+    r.q_out_head = q_out_head_stride;
+    r.k_out = k_out;
+    r.k_out_tok = k_out_tok_stride;
+    r.k_out_head = k_out_head_stride;
+    r.positions = positions;
+    r.steps = steps;
+    r.q_weight = q_weight;
+    r.k_weight = k_weight;
+    r.T = T;
+    r.Hq = Hq;
+    r.Hkv = Hkv;
+    r.D = D;
+    r.rot = rot;
+    r.interleaved = interleaved != 0;
+    r.bf16 = dtype == 0;
+    r.eps = eps;
+    r.amplitude = amplitude;
+    if (dtype != 0 && dtype != 1)
+        return fail(W4_ERR_INVALID_ARG, "dtype must be 0 or 1 (got %d)", dtype);
+    if (int rc = check_rope(r, eps))
+        return rc;
+    if (T == 0 || Hq + Hkv == 0)
+        return W4_OK;
+    if (!positions || (Hkv > 0 && !k_out))
+        return fail(W4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned16(k_out) || (k_out_tok_stride | k_out_head_stride) & 7)
+        return fail(W4_ERR_MISALIGNED, "outputs must be 16-byte aligned and their strides multiples "
+                                       "of 8 elements");
+    if (int rc = check_device())
+        return rc;
+    cudaError_t err = w4::launch_rope(r, as_stream(stream));
+    return err == cudaSuccess ? W4_OK : cuda_fail(err, "qk_norm_rope launch");
+}
+
+int w4_kv_append_rope(uint16_t *k_pages, uint16_t *v_pages, int64_t page_stride, int64_t tok_stride,
+                      int64_t head_stride, int P, int page_size, const int32_t *table, int B, int W,
+                      const int32_t *lens, const uint16_t *q, int64_t q_tok_stride,
+                      int64_t q_head_stride, const uint16_t *k, int64_t k_tok_stride,
+                      int64_t k_head_stride, const uint16_t *v, int64_t v_tok_stride,
+                      int64_t v_head_stride, const int32_t *q_offsets, const int32_t *positions,
+                      const int64_t *steps, const uint16_t *q_weight, const uint16_t *k_weight,
+                      int T, int Hq, int Hkv, int D, int rot, int interleaved, int dtype, float eps,
+                      float amplitude, uint16_t *q_out, int64_t q_out_tok_stride,
+                      int64_t q_out_head_stride, int32_t *dev_status, w4_stream_t stream)
+{
+    w4::RopeProblem r{};
+    r.q = q;
+    r.q_tok = q_tok_stride;
+    r.q_head = q_head_stride;
+    r.k = k;
+    r.k_tok = k_tok_stride;
+    r.k_head = k_head_stride;
+    r.v = v;
+    r.v_tok = v_tok_stride;
+    r.v_head = v_head_stride;
+    r.q_out = q_out;
+    r.q_out_tok = q_out_tok_stride;
+    r.q_out_head = q_out_head_stride;
+    r.k_pages = k_pages;
+    r.v_pages = v_pages;
+    r.page_stride = page_stride;
+    r.tok_stride = tok_stride;
+    r.head_stride = head_stride;
+    r.table = table;
+    r.lens = lens;
+    r.q_offsets = q_offsets;
+    r.positions = positions;
+    r.steps = steps;
+    r.q_weight = q_weight;
+    r.k_weight = k_weight;
+    r.dev_status = dev_status;
+    r.T = T;
+    r.Hq = Hq;
+    r.Hkv = Hkv;
+    r.D = D;
+    r.rot = rot;
+    r.interleaved = interleaved != 0;
+    r.P = P;
+    r.page = page_size;
+    r.B = B;
+    r.W = W;
+    r.bf16 = dtype == 0;
+    r.eps = eps;
+    r.amplitude = amplitude;
+    if (dtype != 0 && dtype != 1)
+        return fail(W4_ERR_INVALID_ARG, "dtype must be 0 or 1 (got %d)", dtype);
+    if (int rc = check_kv_state(table, B, W, lens, lens, P))
+        return rc;
+    if (int rc = check_rope(r, eps))
+        return rc;
+    if (!k_pages || !v_pages || !q_offsets || (T > 0 && !v))
+        return fail(W4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (page_size <= 0 || Hkv <= 0)
+        return fail(W4_ERR_INVALID_ARG, "bad sizes page_size=%d Hkv=%d", page_size, Hkv);
+    if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(v) ||
+        (page_stride | tok_stride | head_stride | v_tok_stride | v_head_stride) & 7 ||
+        !aligned4(q_offsets))
+        return fail(W4_ERR_MISALIGNED, "pointers must be 16-byte aligned and strides multiples of "
+                                       "8 elements");
+    if (T == 0)
+        return W4_OK;
+    if (int rc = check_device())
+        return rc;
+    cudaError_t err = w4::launch_rope(r, as_stream(stream));
+    return err == cudaSuccess ? W4_OK : cuda_fail(err, "kv_append_rope launch");
 }
 
 // ---------------------------------------------------------------- attention

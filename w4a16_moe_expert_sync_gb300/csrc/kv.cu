@@ -586,6 +586,98 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs p)
     }
 }
 
+// ------------------------------------------------------------------- keep
+// Slot b's accepted tokens: of its last n = q_offsets[b + 1] - q_offsets[b] tokens the
+// kept[i]-th goes to place i.  kept ascends, so place i is never behind kept[i], and a
+// thread that moves one 16-byte column of all kept tokens in order, kKeepBatch at a time,
+// reads each before anything is written over it: no scratch, no barrier between tokens.
+// A cluster of CTAs has one slot, a column of one plane a thread; the slot's new length
+// (often over the old one) is written once all of them have read the old one.
+constexpr int kKeepThreads = 512;
+constexpr int kKeepBatch = 8;
+constexpr int kKeepStage = 256;            // kept tokens whose rows are in shared memory
+constexpr int kKeepCluster = 8;            // CTAs a slot at most (the portable size)
+
+__global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const KvKeep p)
+{
+    __shared__ int64_t from[kKeepStage], to[kKeepStage];   // rows of a plane
+    pdl_wait();
+    pdl_trigger();
+    int b, rank, ctas;
+    asm("mov.u32 %0, %%clusterid.x;" : "=r"(b));
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+    const int tid = threadIdx.x;
+    const int t0 = p.q_offsets[b], t1 = p.q_offsets[b + 1], len = p.lens[b];
+    const int c0 = p.kept_offsets[b], c1 = p.kept_offsets[b + 1];
+    const int32_t *table = p.table + static_cast<int64_t>(b) * p.W;
+    const int64_t n = static_cast<int64_t>(t1) - t0, count = static_cast<int64_t>(c1) - c0;
+    // what makes no sense leaves the slot as it is; every CTA of it sees that alike
+    bool ok = t0 >= 0 && n >= 0 && n <= len && c0 >= 0 && count >= 0 && c1 <= p.n_kept &&
+              count <= n && len <= static_cast<int64_t>(p.W) * p.page;
+    const int base = ok ? len - static_cast<int>(n) : 0;
+    bool bad_page = false;
+    for (int i = tid; ok && i < count; i += kKeepThreads) {
+        const int k = p.kept[c0 + i];
+        if (k < 0 || k >= n || (i > 0 && k <= p.kept[c0 + i - 1])) {
+            ok = false;
+        } else if (k != i) {
+            const int src = table[(base + k) / p.page], dst = table[(base + i) / p.page];
+            if (src < 0 || src >= p.P || dst < 0 || dst >= p.P)
+                bad_page = true;
+            else if (p.refs[dst] > 1)      // others hold it: nothing is written there
+                ok = false;
+        }
+    }
+    const bool any_page = __syncthreads_or(bad_page);
+    ok = __syncthreads_and(ok) != 0;
+    const bool served = ok && !any_page;
+    // every CTA of the slot has read its length when the barrier is complete
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (served) {
+        const int64_t row_vecs = p.page_bytes / (16ll * p.page), columns = p.planes * row_vecs;
+        const int64_t plane_vecs = static_cast<int64_t>(p.P) * p.page * row_vecs;
+        for (int i0 = 0; i0 < count; i0 += kKeepStage) {
+            const int m = static_cast<int>(min(count - i0, static_cast<int64_t>(kKeepStage)));
+            __syncthreads();
+            if (tid < m) {
+                const int k = base + p.kept[c0 + i0 + tid], d = base + i0 + tid;
+                // a token that is in its place already is not moved
+                from[tid] = k == d ? -1
+                                   : static_cast<int64_t>(table[k / p.page]) * p.page + k % p.page;
+                to[tid] = static_cast<int64_t>(table[d / p.page]) * p.page + d % p.page;
+            }
+            __syncthreads();
+            for (int64_t col = rank * kKeepThreads + tid; col < columns;
+                 col += static_cast<int64_t>(ctas) * kKeepThreads) {
+                const int64_t plane = col / row_vecs;
+                int4 *at = reinterpret_cast<int4 *>(p.pool) + plane * plane_vecs +
+                           (col - plane * row_vecs);
+                for (int i = 0; i < m; i += kKeepBatch) {
+                    int4 v[kKeepBatch];
+#pragma unroll
+                    for (int u = 0; u < kKeepBatch; u++)
+                        if (i + u < m && from[i + u] >= 0)
+                            v[u] = at[from[i + u] * row_vecs];
+#pragma unroll
+                    for (int u = 0; u < kKeepBatch; u++)
+                        if (i + u < m && from[i + u] >= 0 &&
+                            W4_IN_BOUNDS(to[i + u] >= 0 &&
+                                             to[i + u] < static_cast<int64_t>(p.P) * p.page,
+                                         p.dev_status))
+                            at[to[i + u] * row_vecs] = v[u];
+                }
+            }
+        }
+    }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank == 0 && tid == 0) {
+        if (!served)
+            raise_status(p.dev_status, ok ? W4_DEV_BAD_PAGE : W4_DEV_BAD_SLOT);
+        p.lens_out[b] = served ? base + static_cast<int>(count) : len;
+    }
+}
+
 int sm_count()
 {
     int dev = 0, sms = 0;
@@ -685,6 +777,29 @@ size_t kv_workspace_bytes(int P, int n)
 {
     // compaction: a count, two lists of at most P / 2 pages, the map; fork: its plan
     return std::max(16 + 4 * (2 * static_cast<size_t>(P / 2) + P), 8 * static_cast<size_t>(n));
+}
+
+cudaError_t launch_kv_keep(const KvKeep &p, cudaStream_t stream)
+{
+    const int64_t columns = p.planes * (p.page_bytes / (16ll * p.page));
+    const int64_t want = (columns + kKeepThreads - 1) / kKeepThreads;
+    int cluster = 1;
+    while (cluster < kKeepCluster && cluster < want)
+        cluster *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster) * p.B);
+    cfg.blockDim = dim3(kKeepThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kv_keep_kernel, p);
 }
 
 cudaError_t launch_kv_append(const KvAppend &q, cudaStream_t stream)

@@ -188,6 +188,36 @@ struct KvAppend {
 };
 cudaError_t launch_kv_append(const KvAppend &p, cudaStream_t stream);
 
+// The accepted ones of each slot's last tokens moved together (kv.cu).
+struct KvKeep {
+    uint8_t *pool;                      // [planes][P][page_bytes]
+    int64_t page_bytes;
+    const int32_t *table, *lens, *refs, *q_offsets, *kept, *kept_offsets;
+    int32_t *lens_out, *dev_status;
+    int planes, P, B, W, page, n_kept;
+};
+cudaError_t launch_kv_keep(const KvKeep &p, cudaStream_t stream);
+
+// Norms and rotation of queries and keys (rope.cu); with v_pages keys and values go to
+// their pages.  Strides in elements.
+struct RopeProblem {
+    const uint16_t *q, *k, *v;                  // [T][Hq or Hkv][D]
+    int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head;
+    uint16_t *q_out, *k_out;                    // k_out: without pages
+    int64_t q_out_tok, q_out_head, k_out_tok, k_out_head;
+    uint16_t *k_pages, *v_pages;                // [P][page][Hkv][D]
+    int64_t page_stride, tok_stride, head_stride;
+    const int32_t *table, *lens, *q_offsets;    // with pages
+    const int32_t *positions;                   // [T]; NULL with pages: the tokens' places
+    const int64_t *steps;                       // [rot / 2]
+    const uint16_t *q_weight, *k_weight;        // [D] or NULL
+    int32_t *dev_status;
+    int T, Hq, Hkv, D, rot, interleaved, P, page, B, W;
+    bool bf16;
+    float eps, amplitude, inv_d;                // inv_d: set by launch_rope
+};
+cudaError_t launch_rope(const RopeProblem &p, cudaStream_t stream);
+
 // Attention over a paged cache with shared prefixes (attention.cu): two
 // launches.  Strides in elements.
 struct AttnProblem {
