@@ -521,6 +521,26 @@ int w4_w4a16_linear(const uint16_t *x, int M, int K, int N, const uint8_t *q, co
                     const uint16_t *z, int group, void *workspace, size_t workspace_bytes,
                     uint16_t *y, int32_t *dev_status, w4_stream_t stream);
 
+/* --------------------------------------------------------------------------
+ * w4_w4a16_linear_few -- w4_w4a16_linear for a few tokens (M <= 32), in one launch
+ * and without a workspace: the projections of a decoding step, where the product is
+ * the stream of the packed weights.
+ *
+ *   x          [M, K] bf16 in
+ *   q          [N, K/2] uint8, w4_quantize's layout; s, z [N, K/group] fp16
+ *   y          [M, N] bf16 out
+ * Codes and activations enter the tensor cores exactly; a group's scale and zero are
+ * applied to its fp32 sum, and y is rounded once.  (Activations of 2^57 and more, or
+ * not finite, make their token's results so.)  A token's results depend on neither the
+ * other tokens' values nor where it stands among as many; bit-identical reruns.
+ * Requires M <= 32, group 64 or 128 dividing K, K up to 13,568, N * K below 2^33,
+ * N below 2^30, x and q 16-byte aligned, s, z and y 4-byte aligned.  M = 0 or N = 0
+ * does nothing.
+ * ------------------------------------------------------------------------ */
+int w4_w4a16_linear_few(const uint16_t *x, int M, int K, int N, const uint8_t *q,
+                        const uint16_t *s, const uint16_t *z, int group, uint16_t *y,
+                        w4_stream_t stream);
+
 /* ==========================================================================
  * Beside the layer: the per-step kernels of the denoising loop
  * ========================================================================== */

@@ -101,6 +101,7 @@ def load_library(path: str | None = None):
                                               V, V, V, V, V], I),
             "w4_w4a16_linear_workspace_size": ([I, I, I, I], SZ),
             "w4_w4a16_linear": ([V, I, I, I, V, V, V, I, V, SZ, V, V, V], I),
+            "w4_w4a16_linear_few": ([V, I, I, I, V, V, V, I, V, V], I),
             "w4_kv_workspace_size": ([I, I], SZ),
             "w4_kv_reserve": ([V, I, I, V, V, I, V, V, I, I, V, V], I),
             "w4_kv_free": ([V, I, I, V, V, I, V, I, V, V], I),
@@ -196,6 +197,15 @@ def _require(specs):
             raise ValueError("tensors passed to the CUDA library must be contiguous")
         if t.dtype is not dtype or t.shape != shape:
             raise ValueError(f"{name} must be {list(shape)} {dtype}, not {list(t.shape)} {t.dtype}")
+
+
+def _on_current_device(*ts):
+    """The kernels run on the current device: tensors of another one are refused."""
+    import torch
+    dev = torch._C._cuda_getDevice()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors passed to the CUDA library must live on the current device")
 
 
 # --------------------------------------------------------------------------
@@ -661,6 +671,28 @@ def w4_w4a16_linear(x, q, s, z, group: int = 128, workspace=None, out=None, dev_
     return out
 
 
+def w4_w4a16_linear_few(x, q, s, z, group: int = 128, out=None, stream=None):
+    """w4_w4a16_linear for up to 32 rows, in one launch without a workspace: y [M, N]
+    bf16 = x [M, K] bf16 . deq(W)^T with W packed as w4_quantize writes it."""
+    import torch
+    if x.dim() != 2 or q.dim() != 2 or group <= 0:
+        raise ValueError("x must be [M, K] and the packed weight [N, K / 2]")
+    M, K = x.shape
+    N = q.shape[0]
+    f16 = torch.float16
+    _require(((x, torch.bfloat16, (M, K), "x"), (q, torch.uint8, (N, K // 2), "q"),
+              (s, f16, (N, K // group), "s"), (z, f16, (N, K // group), "z")))
+    if out is None:
+        out = _result((M, N), torch.bfloat16, x.device, stream)
+    else:
+        _require(((out, torch.bfloat16, (M, N), "out"),))
+    _on_current_device(x, q, s, z, out)
+    _check(load_library().w4_w4a16_linear_few(
+        x.data_ptr(), M, K, N, q.data_ptr(), s.data_ptr(), z.data_ptr(), group, out.data_ptr(),
+        _stream(stream)), "w4_w4a16_linear_few")
+    return out
+
+
 # --------------------------------------------------------------------------
 # Beside the layer: RMSNorm and the sampler ("dg-w4-kernels" -- RMSNorm, Sampler)
 # --------------------------------------------------------------------------
@@ -950,15 +982,6 @@ def w4_rope_steps(rot: int, base: float = 10000.0, method: str = "linear", facto
     _check(load_library().w4_rope_steps(rot, base, _ROPE_METHODS[method], factor, trained_len, low,
                                         high, _ptr(steps)), "w4_rope_steps")
     return steps.to(device)
-
-
-def _on_current_device(*ts):
-    """The kernels run on the current device: tensors of another one are refused."""
-    import torch
-    dev = torch._C._cuda_getDevice()
-    for t in ts:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors passed to the CUDA library must live on the current device")
 
 
 def _rope_inputs(q, k, steps, positions, q_weight, k_weight, q_out, stream):

@@ -1538,3 +1538,28 @@ int w4_w4a16_linear(const uint16_t *x, int M, int K, int N, const uint8_t *q, co
         return fail(W4_ERR_UNSUPPORTED_SHAPE, "%s", why);
     return err == cudaSuccess ? W4_OK : cuda_fail(err, "dense GEMM launch");
 }
+
+int w4_w4a16_linear_few(const uint16_t *x, int M, int K, int N, const uint8_t *q,
+                        const uint16_t *s, const uint16_t *z, int group, uint16_t *y,
+                        w4_stream_t stream)
+{
+    if (M < 0 || K <= 0 || N < 0)
+        return fail(W4_ERR_INVALID_ARG, "bad sizes M=%d K=%d N=%d", M, K, N);
+    if (M == 0 || N == 0)
+        return W4_OK;
+    if (!x || !q || !s || !z || !y)
+        return fail(W4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (group != 64 && group != 128)
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "group must be 64 or 128 (got %d)", group);
+    if (M > 32 || K % group || K > 13568)
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "need M <= 32 and K a multiple of the group up to "
+                                              "13568 (M=%d K=%d group=%d)", M, K, group);
+    if (N >= (1 << 30) || static_cast<int64_t>(N) * K >= (1ll << 33))
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "need N below 2^30 and N * K below 2^33");
+    if (!aligned16(x) || !aligned16(q) || !aligned4(s) || !aligned4(z) || !aligned4(y))
+        return fail(W4_ERR_MISALIGNED, "x and q must be 16-byte aligned, s, z and y 4-byte aligned");
+    if (int rc = check_device())
+        return rc;
+    cudaError_t err = w4::launch_few_linear(x, M, K, N, q, s, z, group, y, as_stream(stream));
+    return err == cudaSuccess ? W4_OK : cuda_fail(err, "few-token linear launch");
+}
