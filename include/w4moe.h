@@ -830,9 +830,32 @@ int w4_attn_shared_prefix(const uint16_t *q, int64_t q_tok_stride, int64_t q_hea
                           w4_stream_t stream);
 
 /* --------------------------------------------------------------------------
+ * w4_attn_tree -- w4_attn_shared_prefix for trees of drafted tokens: a sequence's
+ * n = q_offsets[b + 1] - q_offsets[b] queries stand at its last n positions, and
+ * each sees all keys before those and, of the n, those that its bits name
+ *
+ *   tree        [T, tree_words] uint32: bit j % 32 of word j / 32 of row t: whether
+ *               query t sees the j-th new token of its own sequence (usually its
+ *               ancestors and itself); bits past the n are ignored
+ *   tree_words  words a row, for max_q tokens at least
+ * Everything else as in w4_attn_shared_prefix, the workspace's size as well; a
+ * query whose bits are all zero in a sequence without older keys sees nothing:
+ * zeros.  A value v of a token that is not finite may also reach queries of its
+ * sequence that do not see it.  Two launches.
+ * ------------------------------------------------------------------------ */
+int w4_attn_tree(const uint16_t *q, int64_t q_tok_stride, int64_t q_head_stride,
+                 const uint16_t *k_pages, const uint16_t *v_pages, int64_t page_stride,
+                 int64_t tok_stride, int64_t head_stride, int P, int page_size,
+                 const int32_t *table, int W, const int32_t *lens, const int32_t *q_offsets, int T,
+                 int B, int max_q, const uint32_t *tree, int tree_words,
+                 const int32_t *group_offsets, const int32_t *shared_lens, int G, int Hq, int Hkv,
+                 int D, int dtype, float scale, void *workspace, size_t workspace_bytes,
+                 uint16_t *out, int32_t *dev_status, w4_stream_t stream);
+
+/* --------------------------------------------------------------------------
  * w4_test_pipeline_hooks -- a test hook of the kernels with pipelines (not for
  * production use): for later w4_grouped_gemm_gate_up / _down / _down_combine
- * calls, the layer's GEMMs, w4_attn_shared_prefix, w4_moe_layer_few*,
+ * calls, the layer's GEMMs, w4_attn_shared_prefix, w4_attn_tree, w4_moe_layer_few*,
  * w4_kv_copy_pages and w4_kv_compact called from the calling thread, every
  * pipeline wait gives up after wait_limit_ns (0: back to the default of one
  * second) and, if withhold_first_scales is nonzero, each CTA withholds the copy

@@ -120,6 +120,8 @@ def load_library(path: str | None = None):
             "w4_attn_shared_prefix_workspace_size": ([I, I, I, I, I, I, I], SZ),
             "w4_attn_shared_prefix": ([V, I64, I64, V, V, I64, I64, I64, I, I, V, I, V, V, I, I, I,
                                        V, V, I, I, I, I, I, I, ctypes.c_float, V, SZ, V, V, V], I),
+            "w4_attn_tree": ([V, I64, I64, V, V, I64, I64, I64, I, I, V, I, V, V, I, I, I, V, I, V, V,
+                              I, I, I, I, I, ctypes.c_float, V, SZ, V, V, V], I),
             "w4_rmsnorm": ([V, V, I, I, ctypes.c_float, V, V], I),
             "w4_sample_logits_workspace_size": ([I, I64], SZ),
             "w4_sample_logits": ([V, I, I64, U64, U64, V, V, V, V, SZ, V], I),
@@ -1071,15 +1073,13 @@ def w4_attn_shared_prefix_workspace_size(T: int, B: int, G: int, max_q: int, Hq:
     return int(load_library().w4_attn_shared_prefix_workspace_size(T, B, G, max_q, Hq, Hkv, D))
 
 
-def w4_attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets, group_offsets=None,
-                          shared_lens=None, max_q: int = 1, causal: bool = True, scale=None,
-                          workspace=None, out=None, dev_status=None, stream=None):
-    """Attention of q [T, Hq, D] (any strides of tokens and heads) over one
-    layer's pages [P, page_size, Hkv, D]; sequences group_offsets[g] ..
-    group_offsets[g + 1] share their first shared_lens[g] tokens, which are read
-    once for the group.  scale defaults to 1 / sqrt(D).  Returns out [T, Hq, D]."""
+def _attn_inputs(q, k_pages, v_pages, table, lens, q_offsets, group_offsets, shared_lens, max_q,
+                 workspace, out, dev_status, stream):
+    """(type, shape and strides of the pages, T, Hq, B, W, G, strides of q, workspace,
+    out) of an attention call, with its arguments checked."""
     import torch
-    dtype, (P, page, Hkv, D), strides = _kv_planes(k_pages, v_pages)
+    dtype, shape, strides = _kv_planes(k_pages, v_pages)
+    Hkv, D = shape[2:]
     qs = _rows16(q, dtype, "q")
     _require_int32(table, lens, q_offsets, group_offsets, shared_lens, dev_status)
     if q.dim() != 3 or (dtype is not torch.bfloat16 and dtype is not torch.float16):
@@ -1101,6 +1101,20 @@ def w4_attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets, group_off
             if Hkv and Hq % Hkv == 0 else 256, torch.uint8, q.device, stream)
     else:
         _require_cuda(workspace)
+    return dtype, shape, strides, T, Hq, B, W, G, qs, workspace, out
+
+
+def w4_attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets, group_offsets=None,
+                          shared_lens=None, max_q: int = 1, causal: bool = True, scale=None,
+                          workspace=None, out=None, dev_status=None, stream=None):
+    """Attention of q [T, Hq, D] (any strides of tokens and heads) over one
+    layer's pages [P, page_size, Hkv, D]; sequences group_offsets[g] ..
+    group_offsets[g + 1] share their first shared_lens[g] tokens, which are read
+    once for the group.  scale defaults to 1 / sqrt(D).  Returns out [T, Hq, D]."""
+    import torch
+    dtype, (P, page, Hkv, D), strides, T, Hq, B, W, G, qs, workspace, out = _attn_inputs(
+        q, k_pages, v_pages, table, lens, q_offsets, group_offsets, shared_lens, max_q, workspace,
+        out, dev_status, stream)
     _check(load_library().w4_attn_shared_prefix(
         q.data_ptr(), qs[0], qs[1], k_pages.data_ptr(), v_pages.data_ptr(), *strides[:3], P, page,
         table.data_ptr(), W, lens.data_ptr(), q_offsets.data_ptr(), T, B, max_q,
@@ -1108,4 +1122,29 @@ def w4_attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets, group_off
         0 if dtype is torch.bfloat16 else 1, int(causal), D ** -0.5 if scale is None else scale,
         workspace.data_ptr(), workspace.nbytes, out.data_ptr(), _ptr(dev_status),
         _stream(stream)), "w4_attn_shared_prefix")
+    return out
+
+
+def w4_attn_tree(q, k_pages, v_pages, table, lens, q_offsets, tree, group_offsets=None,
+                 shared_lens=None, max_q: int = 1, scale=None, workspace=None, out=None,
+                 dev_status=None, stream=None):
+    """w4_attn_shared_prefix for trees of drafted tokens: bit j % 32 of word j // 32 of
+    row t of tree [T, words] int32 tells whether query t sees its sequence's j-th new
+    token; the older ones it sees all.  Returns out [T, Hq, D]."""
+    import torch
+    dtype, (P, page, Hkv, D), strides, T, Hq, B, W, G, qs, workspace, out = _attn_inputs(
+        q, k_pages, v_pages, table, lens, q_offsets, group_offsets, shared_lens, max_q, workspace,
+        out, dev_status, stream)
+    _require_int32(tree)
+    if tree.dim() != 2 or tree.shape[0] != T:
+        raise ValueError("tree must be [T, words], a bit for each of max_q tokens in a row")
+    _on_current_device(q, k_pages, v_pages, table, lens, q_offsets, tree, group_offsets,
+                       shared_lens, workspace, out, dev_status)
+    _check(load_library().w4_attn_tree(
+        q.data_ptr(), qs[0], qs[1], k_pages.data_ptr(), v_pages.data_ptr(), *strides[:3], P, page,
+        table.data_ptr(), W, lens.data_ptr(), q_offsets.data_ptr(), T, B, max_q, tree.data_ptr(),
+        tree.shape[1], _ptr(group_offsets), _ptr(shared_lens), G, Hq, Hkv, D,
+        0 if dtype is torch.bfloat16 else 1, D ** -0.5 if scale is None else scale,
+        workspace.data_ptr(), workspace.nbytes, out.data_ptr(), _ptr(dev_status),
+        _stream(stream)), "w4_attn_tree")
     return out

@@ -1292,15 +1292,16 @@ size_t w4_attn_shared_prefix_workspace_size(int T, int B, int G, int max_q, int 
     return w4::attn_workspace_bytes(T, B, G, max_q, Hq, Hkv, D);
 }
 
-int w4_attn_shared_prefix(const uint16_t *q, int64_t q_tok_stride, int64_t q_head_stride,
-                          const uint16_t *k_pages, const uint16_t *v_pages, int64_t page_stride,
-                          int64_t tok_stride, int64_t head_stride, int P, int page_size,
-                          const int32_t *table, int W, const int32_t *lens,
-                          const int32_t *q_offsets, int T, int B, int max_q,
-                          const int32_t *group_offsets, const int32_t *shared_lens, int G, int Hq,
-                          int Hkv, int D, int dtype, int causal, float scale, void *workspace,
-                          size_t workspace_bytes, uint16_t *out, int32_t *dev_status,
-                          w4_stream_t stream)
+// Both attentions; tree NULL: causal counts.
+static int run_attn(const uint16_t *q, int64_t q_tok_stride, int64_t q_head_stride,
+                    const uint16_t *k_pages, const uint16_t *v_pages, int64_t page_stride,
+                    int64_t tok_stride, int64_t head_stride, int P, int page_size,
+                    const int32_t *table, int W, const int32_t *lens, const int32_t *q_offsets,
+                    int T, int B, int max_q, const int32_t *group_offsets,
+                    const int32_t *shared_lens, int G, int Hq, int Hkv, int D, int dtype,
+                    int causal, const uint32_t *tree, int tree_words, float scale,
+                    void *workspace, size_t workspace_bytes, uint16_t *out, int32_t *dev_status,
+                    w4_stream_t stream)
 {
     if (T < 0 || B < 0 || G < 0 || max_q <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || P <= 0 ||
         W <= 0 || (dtype != 0 && dtype != 1))
@@ -1372,10 +1373,50 @@ int w4_attn_shared_prefix(const uint16_t *q, int64_t q_tok_stride, int64_t q_hea
     p.D = D;
     p.max_q = max_q;
     p.causal = causal != 0;
+    p.tree = tree;
+    p.tree_words = tree_words;
     p.bf16 = dtype == 0;
     p.scale = scale;
     cudaError_t err = w4::launch_attn(p, as_stream(stream));
     return err == cudaSuccess ? W4_OK : cuda_fail(err, "attention launch");
+}
+
+int w4_attn_shared_prefix(const uint16_t *q, int64_t q_tok_stride, int64_t q_head_stride,
+                          const uint16_t *k_pages, const uint16_t *v_pages, int64_t page_stride,
+                          int64_t tok_stride, int64_t head_stride, int P, int page_size,
+                          const int32_t *table, int W, const int32_t *lens,
+                          const int32_t *q_offsets, int T, int B, int max_q,
+                          const int32_t *group_offsets, const int32_t *shared_lens, int G, int Hq,
+                          int Hkv, int D, int dtype, int causal, float scale, void *workspace,
+                          size_t workspace_bytes, uint16_t *out, int32_t *dev_status,
+                          w4_stream_t stream)
+{
+    return run_attn(q, q_tok_stride, q_head_stride, k_pages, v_pages, page_stride, tok_stride,
+                    head_stride, P, page_size, table, W, lens, q_offsets, T, B, max_q,
+                    group_offsets, shared_lens, G, Hq, Hkv, D, dtype, causal, nullptr, 0, scale,
+                    workspace, workspace_bytes, out, dev_status, stream);
+}
+
+int w4_attn_tree(const uint16_t *q, int64_t q_tok_stride, int64_t q_head_stride,
+                 const uint16_t *k_pages, const uint16_t *v_pages, int64_t page_stride,
+                 int64_t tok_stride, int64_t head_stride, int P, int page_size,
+                 const int32_t *table, int W, const int32_t *lens, const int32_t *q_offsets, int T,
+                 int B, int max_q, const uint32_t *tree, int tree_words,
+                 const int32_t *group_offsets, const int32_t *shared_lens, int G, int Hq, int Hkv,
+                 int D, int dtype, float scale, void *workspace, size_t workspace_bytes,
+                 uint16_t *out, int32_t *dev_status, w4_stream_t stream)
+{
+    if (tree_words < 0 || (max_q > 0 && tree_words < (max_q - 1) / 32 + 1))
+        return fail(W4_ERR_INVALID_ARG, "a row of tree must have a bit for each of max_q tokens "
+                    "(max_q=%d tree_words=%d)", max_q, tree_words);
+    if (T > 0 && B > 0 && !tree)
+        return fail(W4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned4(tree))
+        return fail(W4_ERR_MISALIGNED, "tree must be 4-byte aligned");
+    return run_attn(q, q_tok_stride, q_head_stride, k_pages, v_pages, page_stride, tok_stride,
+                    head_stride, P, page_size, table, W, lens, q_offsets, T, B, max_q,
+                    group_offsets, shared_lens, G, Hq, Hkv, D, dtype, 0, tree, tree_words, scale,
+                    workspace, workspace_bytes, out, dev_status, stream);
 }
 
 // ------------------------------------------------------------------ RMSNorm

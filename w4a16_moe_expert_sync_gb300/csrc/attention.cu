@@ -126,6 +126,8 @@ struct AttnArgs {
     PageView view;
     int rows_b;                            // a sequence's single item's rows at most
     int cap_a, cap_g, cap_b;               // pieces that the workspace holds; cap_b: all single
+    const uint32_t *tree;                  // [T][tree_words], bit j of a row: its j-th new token
+    int tree_words;
 };
 
 // ------------------------------------------------------------- tensor memory
@@ -419,7 +421,8 @@ __device__ __forceinline__ int find_entry(const int *start, int n, int x)
 }
 
 // IN_TURN: a K or V tile's blocks of 64 values lie in turn (see PageView).
-template <int D, bool BF16, bool IN_TURN>
+// TREE: of its sequence's new tokens a query sees those that its bits in p.tree name.
+template <int D, bool BF16, bool IN_TURN, bool TREE>
 struct Kernel {
     static constexpr int kBlocks = D / 64;                     // 128-byte column blocks
     static constexpr int kTileBytes = kKeys * D * 2;           // a K, V or Q tile
@@ -948,15 +951,17 @@ struct Kernel {
                 load_q(p, q, g, g.row0 + (pair ? stream * kRows : 0), rows_here(g, pair, stream),
                        tid);
         };
-        // How many keys this thread's row of a piece sees.  The lanes part ways in
-        // it, and the tensor-memory instructions that follow need them together
-        // again.
+        // How many keys this thread's row of a piece sees, and (a tree's) which of them
+        // are named by bits.  The lanes part ways in it, and the tensor-memory
+        // instructions that follow need them together again.
+        Window window{INT_MAX, nullptr}, next_window = window;
         auto sees = [&](int i) {
             const Seg &g = piece(i);
             int n = INT_MAX;                   // no row: nothing to mask, nothing kept
+            next_window.from = INT_MAX;
             if (tid < rows_here(g, pair, stream)) {
                 const int row = g.row0 + (pair ? stream * kRows : 0) + tid;
-                n = min(limit_of(p, g, g.tok0 + row / p.rep), g.k1);
+                n = min(limit_of(p, g, g.tok0 + row / p.rep, next_window), g.k1);
             }
             __syncwarp();
             return n;
@@ -974,8 +979,9 @@ struct Kernel {
             fetch(0);
             hand_over(0);
             limit = sees(0);
+            window = next_window;
         }
-        for (int i = 0, r = 0; i < count; i++, limit = next) {
+        for (int i = 0, r = 0; i < count; i++, limit = next, window = next_window) {
             const bool another = i + 1 < count;
             const Seg g = piece(i);
             const int rows = rows_here(g, pair, stream);
@@ -995,7 +1001,7 @@ struct Kernel {
                 __syncwarp();
                 if (busy)
                     tile(p, ts, to, limit == INT_MAX ? 0 : g.k0 - base,
-                         limit == INT_MAX ? kKeys : limit - base, t > 0, m, l);
+                         limit == INT_MAX ? kKeys : limit - base, window, base, t > 0, m, l);
                 if (((g.k1 - base < kKeys && (g.k1 & 15)) || (g.k0 > base && (g.k0 & 15))) &&
                     !clear_ends(p, s, ring, 2 * fill_of(s, which, r) + 1, g.k0 - base,
                                 g.k1 - base, pair, stream, tid, clear_phase))
@@ -1061,8 +1067,14 @@ struct Kernel {
         }
     }
 
-    // How many keys, from position 0, the query token sees.
-    static __device__ int limit_of(const AttnArgs &p, const Seg &g, int tok)
+    // Where the keys of a query's sequence begin whose visibility its bits tell.
+    struct Window {
+        int from;                              // their first position; INT_MAX: no row
+        const uint32_t *bits;
+    };
+
+    // How many keys, from position 0, the query token sees at most.
+    static __device__ int limit_of(const AttnArgs &p, const Seg &g, int tok, Window &window)
     {
         int b = g.seq;
         if (b < 0) {                           // the sequence of a group that has the token
@@ -1081,7 +1093,25 @@ struct Kernel {
             }
         }
         const int len = min(max(p.lens[b], 0), p.W * p.page);
+        if constexpr (TREE) {
+            window.from = len - (p.q_offsets[b + 1] - p.q_offsets[b]);
+            window.bits = p.tree + static_cast<int64_t>(tok) * p.tree_words;
+            return len;
+        }
         return p.causal ? len - (p.q_offsets[b + 1] - tok) + 1 : len;
+    }
+
+    // 32 columns' bits, the first of which is the window's at-th key: ones before the
+    // window, the row's words in it, zeros past those.
+    static __device__ __forceinline__ uint32_t window_word(const AttnArgs &p, const uint32_t *bits,
+                                                           int at)
+    {
+        if (at <= -32)
+            return ~0u;
+        const int j = at >> 5;
+        const uint32_t a = j < 0 ? ~0u : j < p.tree_words ? __ldg(bits + j) : 0u;
+        const uint32_t b = j + 1 < p.tree_words ? __ldg(bits + j + 1) : 0u;
+        return __funnelshift_r(a, b, at & 31);
     }
 
     // P of one tile from its S; columns outside [lo, hi) are masked.  m is the
@@ -1094,10 +1124,28 @@ struct Kernel {
     // denominator sums the unrounded).  When S is here, every MMA before it has
     // completed, so O may be changed.
     static __device__ __forceinline__ void tile(const AttnArgs &p, uint32_t ts, uint32_t to, int lo,
-                                                int hi, bool has_o, float &m, float &l)
+                                                int hi, const Window &window, int base, bool has_o,
+                                                float &m, float &l)
     {
         uint32_t v[128];
         tmem_ld_32x32b_x128(ts, v);
+        if constexpr (TREE) {
+            // few tiles of a sequence hold its new tokens
+            const bool mine = window.from != INT_MAX && window.from < base + kKeys;
+            if (__any_sync(0xffffffffu, mine)) {
+                uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+                if (mine) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        seen[i] = window_word(p, window.bits, base + 32 * i - window.from);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 128; c++)
+                    if (!(seen[c / 32] >> (c % 32) & 1u))
+                        v[c] = 0xff800000u;    // -inf
+            }
+        }
         if (__any_sync(0xffffffffu, lo > 0 || hi < kKeys)) {
 #pragma unroll
             for (int c = 0; c < 128; c++)
@@ -1226,10 +1274,10 @@ struct Kernel {
     }
 };
 
-template <int D, bool BF16, bool IN_TURN>
+template <int D, bool BF16, bool IN_TURN, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant__ AttnArgs p)
 {
-    using K = Kernel<D, BF16, IN_TURN>;
+    using K = Kernel<D, BF16, IN_TURN, TREE>;
     extern __shared__ __align__(1024) uint8_t raw[];
     __shared__ __align__(16) typename K::Shared s;
     uint8_t *qbuf = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -1515,11 +1563,11 @@ Space space_of(int T, int B, int G, int max_q, int Hq, int Hkv, int D)
     return s;
 }
 
-template <int D, bool BF16, bool IN_TURN>
+template <int D, bool BF16, bool IN_TURN, bool TREE>
 cudaError_t launch_variant(const AttnArgs &a, int dev, int sms, cudaStream_t stream)
 {
-    using K = Kernel<D, BF16, IN_TURN>;
-    auto kern = attn_kernel<D, BF16, IN_TURN>;
+    using K = Kernel<D, BF16, IN_TURN, TREE>;
+    auto kern = attn_kernel<D, BF16, IN_TURN, TREE>;
     static std::atomic<uint64_t> raised{0};      // devices whose limit is raised already
     cudaError_t err;
     if (!(raised.load(std::memory_order_relaxed) >> (dev & 63) & 1u)) {
@@ -1539,6 +1587,20 @@ cudaError_t launch_variant(const AttnArgs &a, int dev, int sms, cudaStream_t str
                           dim3(128 * kJoinSides<D, 4>), 0, stream, a);
     return launch_pdl(attn_join_kernel<D, BF16, 1>, dim3(a.B, y, D / 16 / kJoinSides<D, 1>),
                       dim3(32 * kJoinSides<D, 1>), 0, stream, a);
+}
+
+template <bool TREE>
+cudaError_t launch_kind(const AttnProblem &q, const AttnArgs &a, int dev, int sms,
+                        cudaStream_t stream)
+{
+    if (a.view != PageView::kRows)             // D is 128
+        return q.bf16 ? launch_variant<128, true, true, TREE>(a, dev, sms, stream)
+                      : launch_variant<128, false, true, TREE>(a, dev, sms, stream);
+    if (q.D == 128)
+        return q.bf16 ? launch_variant<128, true, false, TREE>(a, dev, sms, stream)
+                      : launch_variant<128, false, false, TREE>(a, dev, sms, stream);
+    return q.bf16 ? launch_variant<64, true, false, TREE>(a, dev, sms, stream)
+                  : launch_variant<64, false, false, TREE>(a, dev, sms, stream);
 }
 
 }  // namespace
@@ -1600,14 +1662,10 @@ cudaError_t launch_attn(const AttnProblem &q, cudaStream_t stream)
     a.rep = q.Hq / q.Hkv;
     a.max_q = q.max_q;
     a.causal = q.causal;
-    if (a.view != PageView::kRows)             // D is 128
-        return q.bf16 ? launch_variant<128, true, true>(a, dev, sms, stream)
-                      : launch_variant<128, false, true>(a, dev, sms, stream);
-    if (q.D == 128)
-        return q.bf16 ? launch_variant<128, true, false>(a, dev, sms, stream)
-                      : launch_variant<128, false, false>(a, dev, sms, stream);
-    return q.bf16 ? launch_variant<64, true, false>(a, dev, sms, stream)
-                  : launch_variant<64, false, false>(a, dev, sms, stream);
+    a.tree = q.tree;
+    a.tree_words = q.tree_words;
+    return q.tree ? launch_kind<true>(q, a, dev, sms, stream)
+                  : launch_kind<false>(q, a, dev, sms, stream);
 }
 
 }  // namespace w4

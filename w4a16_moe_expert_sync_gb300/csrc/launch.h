@@ -235,6 +235,8 @@ struct AttnProblem {
     uint16_t *out;                      // [T][Hq][D]
     int32_t *dev_status;
     int T, B, G, W, P, page, Hq, Hkv, D, max_q, causal;
+    const uint32_t *tree;               // [T][tree_words] bits, or NULL (then causal counts)
+    int tree_words;
     bool bf16;
     float scale;
 };
