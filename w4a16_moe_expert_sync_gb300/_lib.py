@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import threading
 
 from .build import LIB as _LIB_PATH
@@ -132,8 +133,30 @@ def load_library(path: str | None = None):
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = res
+        codes = {V: "Q", I: "i", I64: "q", SZ: "Q", ctypes.c_float: "f"}
+        for name in _PACKED:
+            fn = getattr(lib, name + "_packed")
+            fn.argtypes, fn.restype = [ctypes.c_char_p], I
+            pack = struct.Struct("".join(codes[a] for a in sig[name][0])).pack
+            _packed_calls[name] = fn, pack
         _lib = lib
         return lib
+
+
+# calls with many arguments, which go over in one buffer (csrc/packed.cu)
+_PACKED = ("w4_w4a16_linear_few", "w4_qk_norm_rope", "w4_kv_append_rope", "w4_kv_keep",
+           "w4_attn_shared_prefix", "w4_attn_tree")
+_packed_calls: dict = {}
+
+
+def _call(name: str, *args):
+    """Calls one of _PACKED, NULL pointers as 0, and checks its status."""
+    if _lib is None:
+        load_library()
+    fn, pack = _packed_calls[name]
+    rc = fn(pack(*args))
+    if rc:
+        _check(rc, name)
 
 
 def _check(rc: int, what: str):
@@ -202,12 +225,32 @@ def _require(specs):
 
 
 def _on_current_device(*ts):
-    """The kernels run on the current device: tensors of another one are refused."""
+    """The kernels run on the current device: tensors of another one, or of none, are
+    refused.  Returns the device."""
     import torch
-    dev = torch._C._cuda_getDevice()
-    for t in ts:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors passed to the CUDA library must live on the current device")
+    devices = {t.get_device() for t in ts if t is not None}
+    if -1 in devices:
+        raise ValueError("tensors passed to the CUDA library must live on the GPU")
+    current = torch._C._cuda_getDevice()
+    if devices != {current}:
+        raise ValueError("tensors passed to the CUDA library must live on the current device")
+    return current
+
+
+def _raw_stream(stream, device):
+    """The handle of a call's stream, by default the device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _result_like(t, stream):
+    """_result of t's shape and type."""
+    import torch
+    if stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return _result(t.shape, t.dtype, t.device, stream)
 
 
 # --------------------------------------------------------------------------
@@ -681,17 +724,19 @@ def w4_w4a16_linear_few(x, q, s, z, group: int = 128, out=None, stream=None):
         raise ValueError("x must be [M, K] and the packed weight [N, K / 2]")
     M, K = x.shape
     N = q.shape[0]
-    f16 = torch.float16
-    _require(((x, torch.bfloat16, (M, K), "x"), (q, torch.uint8, (N, K // 2), "q"),
-              (s, f16, (N, K // group), "s"), (z, f16, (N, K // group), "z")))
+    bf16, f16, groups = torch.bfloat16, torch.float16, (N, K // group)
+    if x.dtype is not bf16 or q.dtype is not torch.uint8 or s.dtype is not f16 or \
+            z.dtype is not f16 or q.shape[1] != K // 2 or s.shape != groups or z.shape != groups:
+        raise ValueError("x must be [M, K] bf16, q [N, K / 2] uint8, s and z [N, K / group] fp16")
+    if not (x.is_contiguous() and q.is_contiguous() and s.is_contiguous() and z.is_contiguous()):
+        raise ValueError("tensors passed to the CUDA library must be contiguous")
+    device = _on_current_device(x, q, s, z, out)
     if out is None:
-        out = _result((M, N), torch.bfloat16, x.device, stream)
-    else:
-        _require(((out, torch.bfloat16, (M, N), "out"),))
-    _on_current_device(x, q, s, z, out)
-    _check(load_library().w4_w4a16_linear_few(
-        x.data_ptr(), M, K, N, q.data_ptr(), s.data_ptr(), z.data_ptr(), group, out.data_ptr(),
-        _stream(stream)), "w4_w4a16_linear_few")
+        out = _result((M, N), bf16, x.device, stream)
+    elif out.dtype is not bf16 or out.shape != (M, N) or not out.is_contiguous():
+        raise ValueError("out must be [M, N] bf16, contiguous")
+    _call("w4_w4a16_linear_few", x.data_ptr(), M, K, N, q.data_ptr(), s.data_ptr(), z.data_ptr(),
+          group, out.data_ptr(), _raw_stream(stream, device))
     return out
 
 
@@ -956,11 +1001,12 @@ def w4_kv_keep(pool, table, lens, refs, q_offsets, kept, kept_offsets, lens_out=
     if q_offsets.shape != (B + 1,) or kept_offsets.shape != (B + 1,) or kept.dim() != 1 or \
             lens_out.shape != lens.shape:
         raise ValueError("q_offsets and kept_offsets must be [B + 1], kept a list, lens_out [B]")
-    _on_current_device(pool, table, lens, refs, q_offsets, kept, kept_offsets, lens_out, dev_status)
-    _check(load_library().w4_kv_keep(_ptr(pool), planes, page_bytes, _ptr(table), B, W, _ptr(lens),
-                                     _ptr(refs), P, _ptr(q_offsets), _ptr(kept), _ptr(kept_offsets),
-                                     kept.shape[0], page, _ptr(lens_out), _ptr(dev_status),
-                                     _stream(stream)), "w4_kv_keep")
+    device = _on_current_device(pool, table, lens, refs, q_offsets, kept, kept_offsets, lens_out,
+                                dev_status)
+    _call("w4_kv_keep", pool.data_ptr(), planes, page_bytes, table.data_ptr(), B, W,
+          lens.data_ptr(), refs.data_ptr(), P, q_offsets.data_ptr(), kept.data_ptr(),
+          kept_offsets.data_ptr(), kept.shape[0], page, lens_out.data_ptr(),
+          0 if dev_status is None else dev_status.data_ptr(), _raw_stream(stream, device))
     return lens_out
 
 
@@ -986,32 +1032,46 @@ def w4_rope_steps(rot: int, base: float = 10000.0, method: str = "linear", facto
     return steps.to(device)
 
 
-def _rope_inputs(q, k, steps, positions, q_weight, k_weight, q_out, stream):
-    """(type, T, Hq, Hkv, D, strides of q, k and q_out, q_out) of a rotation's inputs."""
+def _rope_inputs(q, k, steps, positions, q_weight, k_weight):
+    """(0 or 1 for the type, shape of q, kv heads, strides of q and k) of a rotation's
+    inputs, checked but for their device."""
     import torch
     dtype = q.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float16:
-        raise ValueError("q and k must be bf16 or fp16")
-    qs, ks = _rows16(q, dtype, "q"), _rows16(k, dtype, "k")
-    if q.dim() != 3 or k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+    code = 0 if dtype is torch.bfloat16 else 1 if dtype is torch.float16 else -1
+    if code < 0 or k.dtype is not dtype:
+        raise ValueError("q and k must be of one type, bf16 or fp16")
+    qs, ks = q.stride(), k.stride()
+    if len(qs) != 3 or len(ks) != 3 or qs[2] != 1 or ks[2] != 1:
+        raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D], contiguous along the last axis")
+    shape = q.shape
+    T, _, D = shape
+    k_tokens, Hkv, k_d = k.shape
+    if k_tokens != T or k_d != D:
         raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D]")
-    T, Hq, D = q.shape
     if steps.dtype is not torch.int64 or steps.dim() != 1 or not steps.is_contiguous():
         raise ValueError("steps must be a table of w4_rope_steps")
-    if positions is not None:
-        _require_int32(positions)
-        if positions.shape != (T,):
-            raise ValueError("positions must be [T]")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _require(((w, dtype, (D,), name),))
-    if q_out is None:
-        q_out = _result((T, Hq, D), dtype, q.device, stream)
-    elif q_out.shape != q.shape:
-        raise ValueError("q_out must have q's shape")
-    os_ = _rows16(q_out, dtype, "q_out")
-    _on_current_device(q, k, steps, positions, q_weight, k_weight, q_out)
-    return dtype, T, Hq, k.shape[1], D, qs, ks, os_, q_out
+    if positions is not None and (positions.dtype is not torch.int32 or
+                                  positions.shape != (T,) or not positions.is_contiguous()):
+        raise ValueError("positions must be [T] int32, contiguous")
+    if q_weight is not None and (q_weight.dtype is not dtype or q_weight.shape != (D,) or
+                                 not q_weight.is_contiguous()):
+        raise ValueError("q_weight must be [D] of q's type, contiguous")
+    if k_weight is not None and (k_weight.dtype is not dtype or k_weight.shape != (D,) or
+                                 not k_weight.is_contiguous()):
+        raise ValueError("k_weight must be [D] of q's type, contiguous")
+    return code, shape, Hkv, qs, ks
+
+
+def _rope_out(out, like, stream, what):
+    """(result, its strides of tokens and heads): a new one like `like`, or out, checked."""
+    if out is None:
+        out = _result_like(like, stream)
+        _, H, D = out.shape
+        return out, H * D, D
+    strides = out.stride()
+    if out.shape != like.shape or out.dtype is not like.dtype or strides[2] != 1:
+        raise ValueError(f"{what}_out must be like {what}, contiguous along the last axis")
+    return out, strides[0], strides[1]
 
 
 def w4_qk_norm_rope(q, k, positions, steps, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -1021,22 +1081,17 @@ def w4_qk_norm_rope(q, k, positions, steps, q_weight=None, k_weight=None, eps: f
     normed for each head (with a weight [D]) and their first 2 len(steps) values
     rotated by positions [T] int32, in one pass.  Returns (q_out, k_out); they may
     be q and k themselves."""
-    dtype, T, Hq, Hkv, D, qs, ks, os_, q_out = _rope_inputs(q, k, steps, positions, q_weight,
-                                                            k_weight, q_out, stream)
-    import torch
     if positions is None:
-        raise ValueError("positions must be [T]")
-    if k_out is None:
-        k_out = _result(k.shape, dtype, k.device, stream)
-    elif k_out.shape != k.shape:
-        raise ValueError("k_out must have k's shape")
-    kos = _rows16(k_out, dtype, "k_out")
-    _on_current_device(k_out)
-    _check(load_library().w4_qk_norm_rope(
-        q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], positions.data_ptr(),
-        steps.data_ptr(), _ptr(q_weight), _ptr(k_weight), T, Hq, Hkv, D, 2 * steps.shape[0],
-        int(interleaved), 0 if dtype is torch.bfloat16 else 1, eps, amplitude, q_out.data_ptr(),
-        os_[0], os_[1], k_out.data_ptr(), kos[0], kos[1], _stream(stream)), "w4_qk_norm_rope")
+        raise ValueError("positions must be [T] int32, contiguous")
+    code, (T, Hq, D), Hkv, qs, ks = _rope_inputs(q, k, steps, positions, q_weight, k_weight)
+    device = _on_current_device(q, k, positions, steps, q_weight, k_weight, q_out, k_out)
+    q_out, q_tok, q_head = _rope_out(q_out, q, stream, "q")
+    k_out, k_tok, k_head = _rope_out(k_out, k, stream, "k")
+    _call("w4_qk_norm_rope", q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
+          positions.data_ptr(), steps.data_ptr(), 0 if q_weight is None else q_weight.data_ptr(),
+          0 if k_weight is None else k_weight.data_ptr(), T, Hq, Hkv, D, 2 * steps.shape[0],
+          bool(interleaved), code, eps, amplitude, q_out.data_ptr(), q_tok, q_head, k_out.data_ptr(),
+          k_tok, k_head, _raw_stream(stream, device))
     return q_out, k_out
 
 
@@ -1046,25 +1101,30 @@ def w4_kv_append_rope(k_pages, v_pages, table, lens, q, k, v, q_offsets, steps, 
     """w4_qk_norm_rope and w4_kv_append in one pass: returns the queries, writes the
     keys and values [T, Hkv, D] of the slots' last tokens into their pages.
     positions defaults to the tokens' places in their sequences."""
-    import torch
-    kdtype, (P, page, Hkv, D), strides = _kv_planes(k_pages, v_pages)
-    dtype, T, Hq, k_heads, q_d, qs, ks, os_, q_out = _rope_inputs(q, k, steps, positions, q_weight,
-                                                                  k_weight, q_out, stream)
-    vs = _rows16(v, dtype, "v")
-    _require_int32(table, lens, q_offsets, dev_status)
-    if kdtype is not dtype or k_heads != Hkv or q_d != D or v.shape != k.shape:
+    code, (T, Hq, D), Hkv, qs, ks = _rope_inputs(q, k, steps, positions, q_weight, k_weight)
+    dtype, pages, ps, vs = q.dtype, k_pages.shape, k_pages.stride(), v.stride()
+    if k_pages.dtype is not dtype or v_pages.dtype is not dtype or len(ps) != 4 or ps[3] != 1 or \
+            v_pages.shape != pages or v_pages.stride() != ps:
+        raise ValueError("k_pages and v_pages must be alike, [P, page_size, Hkv, D] of q's type, "
+                         "contiguous along the last axis")
+    P, page, heads, d = pages
+    if heads != Hkv or d != D or v.dtype is not dtype or v.shape != k.shape or vs[2] != 1:
         raise ValueError("k and v must be [T, Hkv, D] of the pages' type")
+    _require_int32(table, lens, q_offsets, dev_status)
     B, W = _kv_batch(table, lens, q_offsets)
-    _on_current_device(k_pages, v_pages, table, lens, v, q_offsets, dev_status)
+    device = _on_current_device(k_pages, v_pages, table, lens, q, k, v, q_offsets, steps, positions,
+                                q_weight, k_weight, q_out, dev_status)
+    q_out, q_tok, q_head = _rope_out(q_out, q, stream, "q")
     if B == 0:
         return q_out
-    _check(load_library().w4_kv_append_rope(
-        k_pages.data_ptr(), v_pages.data_ptr(), *strides[:3], P, page, table.data_ptr(), B, W,
-        lens.data_ptr(), q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(),
-        vs[0], vs[1], q_offsets.data_ptr(), _ptr(positions), steps.data_ptr(), _ptr(q_weight),
-        _ptr(k_weight), T, Hq, Hkv, D, 2 * steps.shape[0], int(interleaved),
-        0 if dtype is torch.bfloat16 else 1, eps, amplitude, q_out.data_ptr(), os_[0], os_[1],
-        _ptr(dev_status), _stream(stream)), "w4_kv_append_rope")
+    _call("w4_kv_append_rope", k_pages.data_ptr(), v_pages.data_ptr(), ps[0], ps[1], ps[2], P, page,
+          table.data_ptr(), B, W, lens.data_ptr(), q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0],
+          ks[1], v.data_ptr(), vs[0], vs[1], q_offsets.data_ptr(),
+          0 if positions is None else positions.data_ptr(), steps.data_ptr(),
+          0 if q_weight is None else q_weight.data_ptr(),
+          0 if k_weight is None else k_weight.data_ptr(), T, Hq, Hkv, D, 2 * steps.shape[0],
+          bool(interleaved), code, eps, amplitude, q_out.data_ptr(), q_tok, q_head,
+          0 if dev_status is None else dev_status.data_ptr(), _raw_stream(stream, device))
     return q_out
 
 
@@ -1073,13 +1133,11 @@ def w4_attn_shared_prefix_workspace_size(T: int, B: int, G: int, max_q: int, Hq:
     return int(load_library().w4_attn_shared_prefix_workspace_size(T, B, G, max_q, Hq, Hkv, D))
 
 
-def _attn_inputs(q, k_pages, v_pages, table, lens, q_offsets, group_offsets, shared_lens, max_q,
-                 workspace, out, dev_status, stream):
-    """(type, shape and strides of the pages, T, Hq, B, W, G, strides of q, workspace,
-    out) of an attention call, with its arguments checked."""
+def _attn(name, masks, q, k_pages, v_pages, table, lens, q_offsets, group_offsets, shared_lens,
+          max_q, scale, workspace, out, dev_status, stream):
+    """Either attention: masks(T) gives its arguments behind max_q and those before scale."""
     import torch
-    dtype, shape, strides = _kv_planes(k_pages, v_pages)
-    Hkv, D = shape[2:]
+    dtype, (P, page, Hkv, D), strides = _kv_planes(k_pages, v_pages)
     qs = _rows16(q, dtype, "q")
     _require_int32(table, lens, q_offsets, group_offsets, shared_lens, dev_status)
     if q.dim() != 3 or (dtype is not torch.bfloat16 and dtype is not torch.float16):
@@ -1091,8 +1149,9 @@ def _attn_inputs(q, k_pages, v_pages, table, lens, q_offsets, group_offsets, sha
     G = 0 if group_offsets is None else group_offsets.numel() - 1
     if G < 0 or (G > 0 and (shared_lens is None or shared_lens.numel() != G)):
         raise ValueError("group_offsets must be [G + 1] and shared_lens [G]")
+    behind, before = masks(T)
     if out is None:
-        out = _result((T, Hq, D), dtype, q.device, stream)
+        out = _result_like(q, stream)
     else:
         _require(((out, dtype, (T, Hq, D), "out"),))
     if workspace is None:
@@ -1101,7 +1160,14 @@ def _attn_inputs(q, k_pages, v_pages, table, lens, q_offsets, group_offsets, sha
             if Hkv and Hq % Hkv == 0 else 256, torch.uint8, q.device, stream)
     else:
         _require_cuda(workspace)
-    return dtype, shape, strides, T, Hq, B, W, G, qs, workspace, out
+    _call(name, q.data_ptr(), qs[0], qs[1], k_pages.data_ptr(), v_pages.data_ptr(), *strides[:3], P,
+          page, table.data_ptr(), W, lens.data_ptr(), q_offsets.data_ptr(), T, B, max_q, *behind,
+          0 if group_offsets is None else group_offsets.data_ptr(),
+          0 if shared_lens is None else shared_lens.data_ptr(), G, Hq, Hkv, D,
+          0 if dtype is torch.bfloat16 else 1, *before, D ** -0.5 if scale is None else scale,
+          workspace.data_ptr(), workspace.nbytes, out.data_ptr(),
+          0 if dev_status is None else dev_status.data_ptr(), _stream(stream))
+    return out
 
 
 def w4_attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets, group_offsets=None,
@@ -1111,18 +1177,9 @@ def w4_attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets, group_off
     layer's pages [P, page_size, Hkv, D]; sequences group_offsets[g] ..
     group_offsets[g + 1] share their first shared_lens[g] tokens, which are read
     once for the group.  scale defaults to 1 / sqrt(D).  Returns out [T, Hq, D]."""
-    import torch
-    dtype, (P, page, Hkv, D), strides, T, Hq, B, W, G, qs, workspace, out = _attn_inputs(
-        q, k_pages, v_pages, table, lens, q_offsets, group_offsets, shared_lens, max_q, workspace,
-        out, dev_status, stream)
-    _check(load_library().w4_attn_shared_prefix(
-        q.data_ptr(), qs[0], qs[1], k_pages.data_ptr(), v_pages.data_ptr(), *strides[:3], P, page,
-        table.data_ptr(), W, lens.data_ptr(), q_offsets.data_ptr(), T, B, max_q,
-        _ptr(group_offsets), _ptr(shared_lens), G, Hq, Hkv, D,
-        0 if dtype is torch.bfloat16 else 1, int(causal), D ** -0.5 if scale is None else scale,
-        workspace.data_ptr(), workspace.nbytes, out.data_ptr(), _ptr(dev_status),
-        _stream(stream)), "w4_attn_shared_prefix")
-    return out
+    return _attn("w4_attn_shared_prefix", lambda T: ((), (bool(causal),)), q, k_pages, v_pages,
+                 table, lens, q_offsets, group_offsets, shared_lens, max_q, scale, workspace, out,
+                 dev_status, stream)
 
 
 def w4_attn_tree(q, k_pages, v_pages, table, lens, q_offsets, tree, group_offsets=None,
@@ -1131,20 +1188,12 @@ def w4_attn_tree(q, k_pages, v_pages, table, lens, q_offsets, tree, group_offset
     """w4_attn_shared_prefix for trees of drafted tokens: bit j % 32 of word j // 32 of
     row t of tree [T, words] int32 tells whether query t sees its sequence's j-th new
     token; the older ones it sees all.  Returns out [T, Hq, D]."""
-    import torch
-    dtype, (P, page, Hkv, D), strides, T, Hq, B, W, G, qs, workspace, out = _attn_inputs(
-        q, k_pages, v_pages, table, lens, q_offsets, group_offsets, shared_lens, max_q, workspace,
-        out, dev_status, stream)
-    _require_int32(tree)
-    if tree.dim() != 2 or tree.shape[0] != T:
-        raise ValueError("tree must be [T, words], a bit for each of max_q tokens in a row")
-    _on_current_device(q, k_pages, v_pages, table, lens, q_offsets, tree, group_offsets,
-                       shared_lens, workspace, out, dev_status)
-    _check(load_library().w4_attn_tree(
-        q.data_ptr(), qs[0], qs[1], k_pages.data_ptr(), v_pages.data_ptr(), *strides[:3], P, page,
-        table.data_ptr(), W, lens.data_ptr(), q_offsets.data_ptr(), T, B, max_q, tree.data_ptr(),
-        tree.shape[1], _ptr(group_offsets), _ptr(shared_lens), G, Hq, Hkv, D,
-        0 if dtype is torch.bfloat16 else 1, D ** -0.5 if scale is None else scale,
-        workspace.data_ptr(), workspace.nbytes, out.data_ptr(), _ptr(dev_status),
-        _stream(stream)), "w4_attn_tree")
-    return out
+    def masks(T):
+        _require_int32(tree)
+        if tree.dim() != 2 or tree.shape[0] != T:
+            raise ValueError("tree must be [T, words], a bit for each of max_q tokens in a row")
+        _on_current_device(q, k_pages, v_pages, table, lens, q_offsets, tree, group_offsets,
+                           shared_lens, workspace, out, dev_status)
+        return (tree.data_ptr(), tree.shape[1]), ()
+    return _attn("w4_attn_tree", masks, q, k_pages, v_pages, table, lens, q_offsets, group_offsets,
+                 shared_lens, max_q, scale, workspace, out, dev_status, stream)

@@ -1143,8 +1143,8 @@ int check_rope(const w4::RopeProblem &r, float eps)
     if (r.rot % 16 || r.rot > r.D)
         return fail(W4_ERR_UNSUPPORTED_SHAPE, "rot must be a multiple of 16 up to D (got %d of %d)",
                     r.rot, r.D);
-    if (static_cast<int64_t>(r.Hq) + 2ll * r.Hkv > 65536)
-        return fail(W4_ERR_UNSUPPORTED_SHAPE, "need Hq + 2 Hkv up to 65536 (got %d, %d)", r.Hq,
+    if (static_cast<int64_t>(r.Hq) + 2ll * r.Hkv > 65535)
+        return fail(W4_ERR_UNSUPPORTED_SHAPE, "need Hq + 2 Hkv up to 65535 (got %d, %d)", r.Hq,
                     r.Hkv);
     if (r.T > 0 && ((r.Hq > 0 && (!r.q || !r.q_out)) || (r.Hkv > 0 && !r.k) ||
                     (r.rot > 0 && !r.steps)))

@@ -12,10 +12,12 @@
 // argument of sincospif, 2^-32 of a turn from the product.  No table of
 // cosines by position is kept, nothing is read but the rot / 2 steps.
 //
-// A CTA takes a few tokens.  Its threads first request their heads' values,
-// then work out the tokens' cosines and sines once for all heads into shared
-// memory.  A head is a group of 8, 16 or 32 lanes with 16 bytes each; the values
-// of the other half that a pair needs come by shuffles.
+// A group of 4, 8 or 16 lanes takes some heads of one token.  A lane has 16 of a
+// head's values: 8 first ones of pairs and the 8 second ones (or 8 neighbouring pairs),
+// so that it turns them by itself, with weights, cosines and sines multiplied together
+// once for all its heads:
+//   out = (x P + partner R) / rms,   P = w A cos t,  R = -+ w' A sin t
+// kRopeBatch heads are in flight a lane.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -31,9 +33,10 @@ namespace w4 {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 16;            // of a CTA at most
-constexpr int kRopeBatch = 4;              // heads in flight a thread
+constexpr int kRopeThreads = 128;
+constexpr int kRopeBatch = 4;              // heads in flight a lane
+constexpr int kRopeHeads = 16;             // of a group at most
+constexpr int kRopeOffsets = 4096;         // sequences whose offsets are staged in shared memory
 
 template <bool BF16> __device__ __forceinline__ float2 unpack2(uint32_t v)
 {
@@ -53,7 +56,7 @@ template <bool BF16> __device__ __forceinline__ uint32_t round2(float lo, float 
     return r;
 }
 
-template <bool BF16> __device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8])
+template <bool BF16> __device__ __forceinline__ void unpack8(const uint4 &v, float *f)
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -64,245 +67,285 @@ template <bool BF16> __device__ __forceinline__ void unpack8(const uint4 &v, flo
     }
 }
 
-// Where the tokens of a CTA go: their sequence's page, or nowhere.
-struct Place {
-    int pos;                               // position of the rotation
-    int valid;                             // whether the token is of a sequence
-    int page;                              // its page, or -1
-    int slot;                              // and its place there
-};
-
-// The tokens' sequences, by all threads: each looks at its share of the offsets.  With
-// offsets that do not ascend from 0 to T no token is of a sequence.
-__device__ __forceinline__ void find_places(const RopeProblem &p, int t0, int n, Place *place)
+template <bool BF16> __device__ __forceinline__ uint4 round8(const float *f)
 {
-    const int tid = threadIdx.x;
+    return make_uint4(round2<BF16>(f[0], f[1]), round2<BF16>(f[2], f[3]),
+                      round2<BF16>(f[4], f[5]), round2<BF16>(f[6], f[7]));
+}
+
+// The sequence that token t is of, or -1; offsets ascend.
+__device__ __forceinline__ int sequence_of(const int32_t *offsets, int B, int t)
+{
+    // one new token each: a step of decoding
+    if (t < B && offsets[t] == t && offsets[t + 1] == t + 1)
+        return t;
+    if (t < offsets[0] || t >= offsets[B])
+        return -1;
+    int lo = 0, hi = B - 1;                // the last sequence that begins at t or before
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (offsets[mid] <= t)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// Whether the offsets ascend within [0, T], by the whole CTA; they are staged if they fit.
+__device__ __forceinline__ bool offsets_ascend(const RopeProblem &p, int32_t *staged)
+{
     bool bad = false;
-    if (tid < n)
-        place[tid].valid = 0;
-    __syncthreads();
-    for (int b = tid; b < p.B; b += kRopeThreads) {
-        const int a = __ldg(p.q_offsets + b), e = __ldg(p.q_offsets + b + 1);
-        if (a < 0 || e < a || e > p.T) {
-            bad = true;
-            continue;
-        }
-        for (int t = max(a, t0); t < min(e, t0 + n); t++) {
-            const int at = max(p.lens[b], 0) - (e - t);
-            const int entry = at >= 0 ? at / p.page : 0;
-            const int id = at >= 0 && entry < p.W
-                               ? __ldg(p.table + static_cast<int64_t>(b) * p.W + entry)
-                               : -1;
-            Place &out = place[t - t0];
-            out.pos = p.positions ? p.positions[t] : at;
-            out.page = id >= 0 && id < p.P ? id : -1;
-            out.slot = at - entry * p.page;
-            out.valid = 1;
-            if (out.page < 0 && p.dev_status)
-                atomicOr(p.dev_status, W4_DEV_BAD_PAGE);
-        }
+    for (int b = threadIdx.x; b <= p.B; b += kRopeThreads) {
+        const int a = __ldg(p.q_offsets + b);
+        bad |= a < 0 || a > p.T || (b > 0 && a < __ldg(p.q_offsets + b - 1));
+        if (p.B <= kRopeOffsets)
+            staged[b] = a;
     }
-    if (__syncthreads_or(bad)) {
-        if (tid < n)
-            place[tid].valid = 0;
-        if (tid == 0 && blockIdx.x == 0 && p.dev_status)
-            atomicOr(p.dev_status, W4_DEV_BAD_SLOT);
-        __syncthreads();
-    }
+    return __syncthreads_or(bad) == 0;
 }
 
-// Where pair f of a token stands in shared memory: a lane's pairs two by two, side by
-// side with the other lanes' same two, so that 16-byte reads meet no bank twice.
-__device__ __forceinline__ int turn_at(int f, int lane_pairs, int half)
-{
-    const int chunk = f / lane_pairs, i = f - chunk * lane_pairs;
-    return ((i >> 1) * (half / lane_pairs) + chunk) * 2 + (i & 1);
-}
-
-// LANES: a head's lanes, 8 values each, D / 8 of them in use.
+// LANES: a head's lanes, 16 values each.
 template <int LANES, bool BF16, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeProblem p, int tokens)
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeProblem p, int heads)
 {
     constexpr int kGroups = kRopeThreads / LANES;
-    // [tokens][rot / 2]: A cos, A sin of a token's pairs in the order of turn_at
-    extern __shared__ __align__(16) float2 turn[];
-    __shared__ Place place[kRopeTokens];
+    extern __shared__ int32_t staged[];
     pdl_wait();
     pdl_trigger();
-    const int tid = threadIdx.x, c = tid % LANES, group = tid / LANES;
-    const int t0 = blockIdx.x * tokens, n = min(tokens, p.T - t0);
-    const int rows = p.Hq + (APPEND ? 2 : 1) * p.Hkv, items = n * rows;
-    const int half = p.rot / 2, chunks = p.D / 8;
-    const int lane_pairs = p.interleaved ? 4 : 8;          // pairs that a lane has values of
-    const bool in_head = c < chunks;
+    const int lane = threadIdx.x & 31, l = threadIdx.x % LANES;
+    const unsigned mates = (LANES == 32 ? ~0u : (1u << LANES) - 1u) << (lane / LANES * LANES);
+    // a CTA's groups have neighbouring tokens and the same heads
+    const int t = blockIdx.x * kGroups + threadIdx.x / LANES, part = blockIdx.y;
+    const int all = p.Hq + (APPEND ? 2 : 1) * p.Hkv;
+    const int row0 = part * heads, row1 = min(row0 + heads, all);
 
-    // an item is one head of one token: queries, keys, values
-    auto source = [&](int item) -> const uint4 * {
-        const int t = item / rows, r = item - t * rows;
-        const int64_t tok = t0 + t;
-        const uint16_t *x;
-        if (r < p.Hq)
-            x = p.q + tok * p.q_tok + static_cast<int64_t>(r) * p.q_head;
-        else if (!APPEND || r < p.Hq + p.Hkv)
-            x = p.k + tok * p.k_tok + static_cast<int64_t>(r - p.Hq) * p.k_head;
-        else
-            x = p.v + tok * p.v_tok + static_cast<int64_t>(r - p.Hq - p.Hkv) * p.v_head;
-        return reinterpret_cast<const uint4 *>(x + c * 8);
-    };
-    uint4 v[kRopeBatch];
-    auto request = [&](int first) {
-#pragma unroll
-        for (int u = 0; u < kRopeBatch; u++) {
-            const int item = first + u * kGroups;
-            v[u] = make_uint4(0, 0, 0, 0);
-            if (item < items && in_head)
-                v[u] = __ldcs(source(item));
-        }
-    };
-    request(group);
-
-    if constexpr (APPEND)
-        find_places(p, t0, n, place);
-    for (int i = tid; i < n * half; i += kRopeThreads) {
-        const int t = i / half, f = i - t * half;
-        const int pos = APPEND ? place[t].pos : __ldg(p.positions + t0 + t);
-        if (APPEND && !place[t].valid)
-            continue;
-        const uint64_t angle = static_cast<uint64_t>(static_cast<int64_t>(pos)) *
-                               static_cast<uint64_t>(__ldg(p.steps + f));
-        // half turns in [-1, 1)
-        const float x = static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f;
-        float sn, cs;
-        sincospif(x, &sn, &cs);
-        turn[t * half + turn_at(f, lane_pairs, half)] =
-            make_float2(cs * p.amplitude, sn * p.amplitude);
+    // this lane's two 16-byte chunks of a head
+    const int turned_lanes = p.rot / 16, chunks = p.D / 8;
+    const bool turned = l < turned_lanes;
+    int c0 = l, c1 = l + turned_lanes;
+    if (!turned) {
+        c0 = 2 * l;                        // 2 turned_lanes + 2 (l - turned_lanes)
+        c1 = c0 + 1;
     }
-    __syncthreads();
+    const bool has0 = c0 < chunks, has1 = c1 < chunks;
 
-    // this lane's pairs: in halves its values are all first ones or all second ones of
-    // pairs whose others the lane `other` holds
-    const bool turned = c * 8 < p.rot, second = c * 8 >= half;
-    const int other = p.interleaved || !turned ? c : second ? c - half / 8 : c + half / 8;
-    for (int first = group; first < (items + kGroups - 1) / kGroups * kGroups;
-         first += kRopeBatch * kGroups) {
-        if (first != group)
-            request(first);
+    int pos = 0, page = -1, slot = 0;
+    bool valid = t < p.T;
+    if constexpr (APPEND) {
+        if (!offsets_ascend(p, staged)) {
+            if (blockIdx.x == 0 && threadIdx.x == 0 && p.dev_status)
+                atomicOr(p.dev_status, W4_DEV_BAD_SLOT);
+            return;
+        }
+        if (valid) {
+            const int32_t *offsets = p.B <= kRopeOffsets ? staged : p.q_offsets;
+            const int b = sequence_of(offsets, p.B, t);
+            valid = b >= 0;
+            if (valid) {
+                const int at = max(__ldg(p.lens + b), 0) - (offsets[b + 1] - t);
+                const int entry = at >= 0 ? at / p.page : 0;
+                if (at >= 0 && entry < p.W)
+                    page = __ldg(p.table + static_cast<int64_t>(b) * p.W + entry);
+                if (page >= p.P)
+                    page = -1;
+                slot = at - entry * p.page;
+                pos = p.positions ? __ldg(p.positions + t) : at;
+                if (page < 0 && part == 0 && l == 0 && p.dev_status)
+                    atomicOr(p.dev_status, W4_DEV_BAD_PAGE);
+            }
+        }
+    } else if (valid) {
+        pos = __ldg(p.positions + t);
+    }
+    if (!valid)
+        return;                            // its mates too
+
+    float cs[8], sn[8];
 #pragma unroll
-        for (int u = 0; u < kRopeBatch; u++) {
-            const int item = first + u * kGroups;
-            if (item - group >= items)         // alike for the whole CTA
-                break;
-            const int t = min(item, items - 1) / rows, r = min(item, items - 1) - t * rows;
-            const bool is_q = r < p.Hq, is_v = APPEND && r >= p.Hq + p.Hkv;
-            uint4 out = v[u];
-            float x[8], y[8];
-            unpack8<BF16>(v[u], x);
-            const uint16_t *weight = is_q ? p.q_weight : p.k_weight;
-            float inv = 1.0f;
-            if (p.q_weight || p.k_weight) {    // alike for the whole CTA
-                float s = 0.0f;
+    for (int i = 0; i < 8; i++) {
+        cs[i] = 1.0f;
+        sn[i] = 0.0f;
+        if (turned) {
+            // in neighbouring pairs chunk c has pairs 4 c .. 4 c + 3
+            const int f = p.interleaved ? (i < 4 ? c0 * 4 + i : c1 * 4 + i - 4) : l * 8 + i;
+            const uint64_t angle = static_cast<uint64_t>(static_cast<int64_t>(pos)) *
+                                   static_cast<uint64_t>(__ldg(p.steps + f));
+            // half turns in [-1, 1)
+            const float x = static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f;
+            sincospif(x, &sn[i], &cs[i]);
+            cs[i] *= p.amplitude;
+            sn[i] *= p.amplitude;
+        }
+    }
+
+    // Heads [h, h_end) of one kind, from and to memory with these strides.
+    auto run = [&](const uint16_t *from, int64_t from_head, uint16_t *to, int64_t to_head, int n,
+                   const uint16_t *weight) {
+        float P[16], R[16];
+        {
+            float w[16];
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    s = fmaf(x[i], x[i], s);
-#pragma unroll
-                for (int o = LANES / 2; o > 0; o >>= 1)
-                    s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (weight && !is_v) {
-                    inv = rsqrtf(s * p.inv_d + p.eps);
-                    if (in_head) {
-                        float w[8];
-                        unpack8<BF16>(__ldg(reinterpret_cast<const uint4 *>(weight + c * 8)), w);
-#pragma unroll
-                        for (int i = 0; i < 8; i++)
-                            x[i] *= inv * w[i];
-                    }
-                }
+            for (int i = 0; i < 16; i++)
+                w[i] = 1.0f;
+            if (weight) {
+                if (has0)
+                    unpack8<BF16>(__ldg(reinterpret_cast<const uint4 *>(weight + c0 * 8)), w);
+                if (has1)
+                    unpack8<BF16>(__ldg(reinterpret_cast<const uint4 *>(weight + c1 * 8)), w + 8);
             }
             if (p.interleaved) {
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    y[i] = x[i ^ 1];
+                for (int i = 0; i < 8; i++) {
+                    P[2 * i] = w[2 * i] * cs[i];
+                    P[2 * i + 1] = w[2 * i + 1] * cs[i];
+                    R[2 * i] = -w[2 * i + 1] * sn[i];
+                    R[2 * i + 1] = w[2 * i] * sn[i];
+                }
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    y[i] = __shfl_sync(0xffffffffu, x[i], other, LANES);
+                for (int i = 0; i < 8; i++) {
+                    P[i] = w[i] * cs[i];
+                    P[8 + i] = w[8 + i] * cs[i];
+                    R[i] = -w[8 + i] * sn[i];
+                    R[8 + i] = w[i] * sn[i];
+                }
             }
-            if (item >= items || !in_head || (APPEND && !place[t].valid))
-                continue;
-            if (!is_v) {
-                if (turned) {
-                    const int stride = half / lane_pairs;
-                    const float4 *tp = reinterpret_cast<const float4 *>(turn + t * half) +
-                                       (p.interleaved ? c : second ? c - stride : c);
+        }
+        for (int h0 = 0; h0 < n; h0 += kRopeBatch) {
+            uint4 v[kRopeBatch][2];
+#pragma unroll
+            for (int u = 0; u < kRopeBatch; u++) {
+                const uint16_t *x = from + (h0 + u) * from_head;
+                v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
+                if (h0 + u < n && has0)
+                    v[u][0] = __ldcs(reinterpret_cast<const uint4 *>(x + c0 * 8));
+                if (h0 + u < n && has1)
+                    v[u][1] = __ldcs(reinterpret_cast<const uint4 *>(x + c1 * 8));
+            }
+#pragma unroll
+            for (int u = 0; u < kRopeBatch; u++) {
+                if (h0 + u >= n)
+                    break;
+                float x[16], y[16];
+                unpack8<BF16>(v[u][0], x);
+                unpack8<BF16>(v[u][1], x + 8);
+                float inv = 1.0f;
+                if (weight) {
+                    float s[4] = {};
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        s[i & 3] = fmaf(x[i], x[i], s[i & 3]);
+                    float sum = (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+                    for (int o = LANES / 2; o > 0; o >>= 1)
+                        sum += __shfl_xor_sync(mates, sum, o);
+                    inv = rsqrtf(fmaf(sum, p.inv_d, p.eps));
+                }
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    y[i] = x[i] * P[i];
+                if (turned) {              // (others' partners may be infinite: not times zero)
                     if (p.interleaved) {
 #pragma unroll
-                        for (int i = 0; i < 2; i++) {
-                            const float4 cs = tp[i * stride];
-                            x[4 * i] = fmaf(-y[4 * i], cs.y, x[4 * i] * cs.x);
-                            x[4 * i + 1] = fmaf(y[4 * i + 1], cs.y, x[4 * i + 1] * cs.x);
-                            x[4 * i + 2] = fmaf(-y[4 * i + 2], cs.w, x[4 * i + 2] * cs.z);
-                            x[4 * i + 3] = fmaf(y[4 * i + 3], cs.w, x[4 * i + 3] * cs.z);
-                        }
+                        for (int i = 0; i < 16; i++)
+                            y[i] = fmaf(x[i ^ 1], R[i], y[i]);
                     } else {
-                        const float sign = second ? 1.0f : -1.0f;
 #pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            const float4 cs = tp[i * stride];
-                            x[2 * i] = fmaf(sign * y[2 * i], cs.y, x[2 * i] * cs.x);
-                            x[2 * i + 1] = fmaf(sign * y[2 * i + 1], cs.w, x[2 * i + 1] * cs.z);
-                        }
+                        for (int i = 0; i < 16; i++)
+                            y[i] = fmaf(x[i ^ 8], R[i], y[i]);
                     }
                 }
-                out = make_uint4(round2<BF16>(x[0], x[1]), round2<BF16>(x[2], x[3]),
-                                 round2<BF16>(x[4], x[5]), round2<BF16>(x[6], x[7]));
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    y[i] *= inv;
+                uint16_t *o = to + (h0 + u) * to_head;
+                if (has0)
+                    *reinterpret_cast<uint4 *>(o + c0 * 8) = round8<BF16>(y);
+                if (has1)
+                    *reinterpret_cast<uint4 *>(o + c1 * 8) = round8<BF16>(y + 8);
             }
-            const int64_t tok = t0 + t;
-            uint16_t *to;
-            if (is_q) {
-                to = p.q_out + tok * p.q_out_tok + static_cast<int64_t>(r) * p.q_out_head;
-            } else if constexpr (APPEND) {
-                const Place at = place[t];
-                if (at.page < 0)
-                    continue;
-                if (!W4_IN_BOUNDS(at.page < p.P && at.slot >= 0 && at.slot < p.page, p.dev_status))
-                    continue;
-                to = (is_v ? p.v_pages : p.k_pages) + at.page * p.page_stride +
-                     at.slot * p.tok_stride +
-                     static_cast<int64_t>(r - p.Hq - (is_v ? p.Hkv : 0)) * p.head_stride;
-            } else {
-                to = p.k_out + tok * p.k_out_tok + static_cast<int64_t>(r - p.Hq) * p.k_out_head;
+        }
+    };
+    const int64_t tok = t;
+    if (row0 < p.Hq)
+        run(p.q + tok * p.q_tok + row0 * p.q_head, p.q_head,
+            p.q_out + tok * p.q_out_tok + row0 * p.q_out_head, p.q_out_head,
+            min(row1, p.Hq) - row0, p.q_weight);
+    const int k0 = max(row0 - p.Hq, 0), k1 = min(row1 - p.Hq, p.Hkv);
+    uint16_t *k_to;
+    int64_t k_head;
+    if constexpr (APPEND) {
+        if (!(page >= 0 && W4_IN_BOUNDS(page < p.P && slot >= 0 && slot < p.page, p.dev_status)))
+            return;
+        k_to = p.k_pages + page * p.page_stride + slot * p.tok_stride;
+        k_head = p.head_stride;
+    } else {
+        k_to = p.k_out + tok * p.k_out_tok;
+        k_head = p.k_out_head;
+    }
+    if (k0 < k1)
+        run(p.k + tok * p.k_tok + k0 * p.k_head, p.k_head, k_to + k0 * k_head, k_head, k1 - k0,
+            p.k_weight);
+    if constexpr (APPEND) {
+        const int v0 = max(row0 - p.Hq - p.Hkv, 0), v1 = row1 - p.Hq - p.Hkv;
+        const uint16_t *from = p.v + tok * p.v_tok;
+        uint16_t *to = p.v_pages + page * p.page_stride + slot * p.tok_stride;
+        for (int h0 = v0; h0 < v1; h0 += kRopeBatch) {
+            uint4 v[kRopeBatch][2];
+#pragma unroll
+            for (int u = 0; u < kRopeBatch; u++) {
+                const uint16_t *x = from + (h0 + u) * p.v_head;
+                if (h0 + u < v1 && has0)
+                    v[u][0] = __ldcs(reinterpret_cast<const uint4 *>(x + c0 * 8));
+                if (h0 + u < v1 && has1)
+                    v[u][1] = __ldcs(reinterpret_cast<const uint4 *>(x + c1 * 8));
             }
-            *reinterpret_cast<uint4 *>(to + c * 8) = out;
+#pragma unroll
+            for (int u = 0; u < kRopeBatch; u++) {
+                uint16_t *o = to + (h0 + u) * p.head_stride;
+                if (h0 + u < v1 && has0)
+                    *reinterpret_cast<uint4 *>(o + c0 * 8) = v[u][0];
+                if (h0 + u < v1 && has1)
+                    *reinterpret_cast<uint4 *>(o + c1 * 8) = v[u][1];
+            }
         }
     }
 }
 
 template <int LANES>
-cudaError_t launch_lanes(const RopeProblem &p, int tokens, cudaStream_t stream)
+cudaError_t launch_lanes(const RopeProblem &p, int sms, cudaStream_t stream)
 {
-    const dim3 grid((p.T + tokens - 1) / tokens), block(kRopeThreads);
-    const size_t smem = sizeof(float2) * tokens * (p.rot / 2);
+    const int rows = p.Hq + (p.v_pages ? 2 : 1) * p.Hkv;
+    constexpr int kGroups = kRopeThreads / LANES;
+    // a group's heads: few where there are few in all, so that every SM has some
+    const int64_t fair = static_cast<int64_t>(p.T) * rows / (static_cast<int64_t>(sms) * 16 * kGroups);
+    const int most = static_cast<int>(std::min<int64_t>(std::max<int64_t>(fair, 1), kRopeHeads));
+    const int parts = (rows + most - 1) / most, heads = (rows + parts - 1) / parts;
+    const dim3 grid((p.T + kGroups - 1) / kGroups, parts), block(kRopeThreads);
+    const size_t smem = p.v_pages && p.B <= kRopeOffsets ? sizeof(int32_t) * (p.B + 1) : 0;
     if (p.v_pages)
-        return p.bf16 ? launch_pdl(rope_kernel<LANES, true, true>, grid, block, smem, stream, p, tokens)
-                      : launch_pdl(rope_kernel<LANES, false, true>, grid, block, smem, stream, p,
-                                   tokens);
-    return p.bf16 ? launch_pdl(rope_kernel<LANES, true, false>, grid, block, smem, stream, p, tokens)
-                  : launch_pdl(rope_kernel<LANES, false, false>, grid, block, smem, stream, p, tokens);
+        return p.bf16 ? launch_pdl(rope_kernel<LANES, true, true>, grid, block, smem, stream, p, heads)
+                      : launch_pdl(rope_kernel<LANES, false, true>, grid, block, smem, stream, p, heads);
+    return p.bf16 ? launch_pdl(rope_kernel<LANES, true, false>, grid, block, smem, stream, p, heads)
+                  : launch_pdl(rope_kernel<LANES, false, false>, grid, block, smem, stream, p, heads);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeProblem &q, cudaStream_t stream)
 {
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess)
+        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess)
+        return err;
     RopeProblem p = q;
     p.inv_d = 1.0f / static_cast<float>(p.D);
-    const int rows = p.Hq + (p.v_pages ? 2 : 1) * p.Hkv;
-    const int lanes = p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32;
-    // as many tokens as give every group one batch
-    const int tokens = std::min(std::max(kRopeThreads / lanes * kRopeBatch / rows, 1), kRopeTokens);
-    return lanes == 8 ? launch_lanes<8>(p, tokens, stream)
-           : lanes == 16 ? launch_lanes<16>(p, tokens, stream)
-                         : launch_lanes<32>(p, tokens, stream);
+    return p.D <= 64    ? launch_lanes<4>(p, sms, stream)
+           : p.D <= 128 ? launch_lanes<8>(p, sms, stream)
+                        : launch_lanes<16>(p, sms, stream);
 }
 
 }  // namespace w4
