@@ -533,8 +533,8 @@ int w4_w4a16_linear(const uint16_t *x, int M, int K, int N, const uint8_t *q, co
  * applied to its fp32 sum, and y is rounded once.  (Activations of 2^57 and more, or
  * not finite, make their token's results so.)  A token's results depend on neither the
  * other tokens' values nor where it stands among as many; bit-identical reruns.
- * Requires M <= 32, group 64 or 128 dividing K, K up to 13,568, N * K below 2^33,
- * N below 2^30, x and q 16-byte aligned, s, z and y 4-byte aligned.  M = 0 or N = 0
+ * Requires M <= 32, group 64 or 128 dividing K, K up to 11,264, N * K below 2^33,
+ * N below 2^30, x and q 16-byte aligned, y 4-byte, s and z 2-byte aligned.  M = 0 or N = 0
  * does nothing.
  * ------------------------------------------------------------------------ */
 int w4_w4a16_linear_few(const uint16_t *x, int M, int K, int N, const uint8_t *q,

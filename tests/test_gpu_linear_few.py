@@ -48,8 +48,8 @@ def _check(got, x, q, s, z, group):
     (16, 2816, 2816, 128), (17, 384, 31, 128), (24, 448, 4864, 64), (25, 2816, 10000, 128),
     (32, 2816, 4111, 128), (32, 64, 20000, 64),
     # activations that do not fit at once: two tiles, one tile of tokens a pass
-    (32, 4096, 515, 128), (31, 8192, 130, 64), (19, 6464, 77, 64), (32, 13568, 40, 128),
-    (9, 13568, 2500, 64), (1, 13568, 1, 128)])
+    (32, 4096, 515, 128), (31, 8192, 130, 64), (19, 6464, 77, 64), (32, 11264, 40, 128),
+    (9, 11264, 2500, 64), (1, 11264, 1, 128)])
 def test_linear(lib, M, K, N, group):
     x, q, s, z = _inputs(M, K, N, group, M + K)
     y = lib.w4_w4a16_linear_few(x, q, s, z, group)
@@ -149,9 +149,9 @@ def test_calls_refused():
         return lib.w4_w4a16_linear_few(x, M, K, N, q, s, z, group, y, None)
     for kw, want in [(dict(x=None), 1), (dict(q=None), 1), (dict(s=None), 1), (dict(z=None), 1),
                      (dict(y=None), 1), (dict(M=-1), 1), (dict(K=0), 1), (dict(N=-1), 1),
-                     (dict(M=33), 2), (dict(K=192), 2), (dict(K=13696), 2), (dict(group=32), 2),
+                     (dict(M=33), 2), (dict(K=192), 2), (dict(K=11392), 2), (dict(group=32), 2),
                      (dict(group=256), 2), (dict(N=1 << 30, K=128), 2), (dict(N=1 << 26, K=1 << 13), 2),
-                     (dict(x=at + 8), 3), (dict(q=at + 4), 3), (dict(s=at + 2), 3), (dict(y=at + 2), 3)]:
+                     (dict(x=at + 8), 3), (dict(q=at + 4), 3), (dict(s=at + 1), 3), (dict(y=at + 2), 3)]:
         assert linear(**kw) == want, kw
     assert linear(M=0) == 0 and linear(N=0) == 0
     assert ctypes.sizeof(ctypes.c_void_p) == 8

@@ -38,6 +38,7 @@ int cuda_fail(cudaError_t err, const char *what)
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned2(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 
 cudaStream_t as_stream(w4_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
@@ -1592,13 +1593,13 @@ int w4_w4a16_linear_few(const uint16_t *x, int M, int K, int N, const uint8_t *q
         return fail(W4_ERR_INVALID_ARG, "NULL pointer argument");
     if (group != 64 && group != 128)
         return fail(W4_ERR_UNSUPPORTED_SHAPE, "group must be 64 or 128 (got %d)", group);
-    if (M > 32 || K % group || K > 13568)
+    if (M > 32 || K % group || K > 11264)
         return fail(W4_ERR_UNSUPPORTED_SHAPE, "need M <= 32 and K a multiple of the group up to "
-                                              "13568 (M=%d K=%d group=%d)", M, K, group);
+                                              "11264 (M=%d K=%d group=%d)", M, K, group);
     if (N >= (1 << 30) || static_cast<int64_t>(N) * K >= (1ll << 33))
         return fail(W4_ERR_UNSUPPORTED_SHAPE, "need N below 2^30 and N * K below 2^33");
-    if (!aligned16(x) || !aligned16(q) || !aligned4(s) || !aligned4(z) || !aligned4(y))
-        return fail(W4_ERR_MISALIGNED, "x and q must be 16-byte aligned, s, z and y 4-byte aligned");
+    if (!aligned16(x) || !aligned16(q) || !aligned2(s) || !aligned2(z) || !aligned4(y))
+        return fail(W4_ERR_MISALIGNED, "x and q must be 16-byte aligned, y 4-byte, s and z 2-byte aligned");
     if (int rc = check_device())
         return rc;
     cudaError_t err = w4::launch_few_linear(x, M, K, N, q, s, z, group, y, as_stream(stream));

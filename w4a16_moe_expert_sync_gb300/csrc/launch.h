@@ -159,7 +159,7 @@ bool few_supported(int M, int d, int m, int k);
 size_t few_workspace_bytes(int M, int d, int m, int k);
 cudaError_t launch_few(const FewProblem &p, cudaStream_t stream);
 
-// The dense W4A16 linear for a few tokens (linear_few.cu): M <= 32, K <= 13568.
+// The dense W4A16 linear for a few tokens (linear_few.cu): M <= 32, K <= 11264.
 cudaError_t launch_few_linear(const uint16_t *x, int M, int K, int N, const uint8_t *q,
                               const uint16_t *s, const uint16_t *z, int group, uint16_t *y,
                               cudaStream_t stream);

@@ -14,10 +14,12 @@
 // group is free as long as codes and activations agree on it: a lane takes the 8 codes
 // of a word, and the activations are stored to match.
 //
-// A task is 16 RT weight rows, a unit 128 codes of each.  A CTA takes an equal
-// contiguous share of the tasks, its warps equal shares of those tasks' units; a task
-// that crosses warps is added up in warp order through shared memory.  Sums run in a
-// fixed order: bit-identical reruns.
+// A task is 16 RT weight rows, a unit 128 codes of each.  A CTA has up to 8 NT of the
+// tokens and an equal contiguous share of the tasks, its warps equal shares of those
+// tasks' units; a task that crosses warps is added up in warp order through shared
+// memory.  A lane copies the codes that it will use itself into its own ring in shared
+// memory, S units ahead, and waits for nobody else's.  Sums run in a fixed order:
+// bit-identical reruns.
 #include <algorithm>
 #include <atomic>
 #include <cuda_fp16.h>
@@ -60,31 +62,27 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
     return r;
 }
 
-__device__ __forceinline__ uint4 load_codes16(const uint8_t *p)
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *to, const void *from)
 {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint2 load_codes8(const uint8_t *p)
-{
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-                 : "=r"(v.x), "=r"(v.y)
-                 : "l"(p));
-    return v;
+    static_assert(BYTES == 8 || BYTES == 16);
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
+                     : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(to)), "l"(from)
+                     : "memory");
 }
 
 __device__ __forceinline__ float half_of(uint16_t h) { return __half2float(__ushort_as_half(h)); }
 
-// NT: tiles of 8 tokens; RT: tiles of 16 weight rows; NW: warps; PF: units in flight a warp.
-template <int GROUP, int NT, int RT, int NW, int PF>
+// NT: tiles of 8 tokens; RT: tiles of 16 weight rows; NW: warps; S: units in flight a warp.
+template <int GROUP, int NT, int RT, int NW, int S>
 struct FewLinear {
     static constexpr int kGroups = 128 / GROUP;            // of a unit
     static constexpr int kWords = 4 / kGroups;             // of a lane's row and group
     static constexpr int kRows = 16 * RT;
+    static constexpr int kRingBytes = NW * S * RT * 1024;
 
     // Bytes of a tile of 8 tokens: the activations [block][4][8 tokens][4] x 16 bytes, then
     // the groups' sums [block][groups][8 tokens].
@@ -93,55 +91,55 @@ struct FewLinear {
         return blocks * (4 * 512 + kGroups * 32);
     }
 
-    // A lane's codes, scales and zeros of one unit: of weight rows 2 g and 2 g + 1 of each
-    // row tile.
+    // Of a unit in flight, by lane: a scale or zero of weight row 2 g or 2 g + 1 of each row
+    // tile (s, z, s, z for the four lanes of g); its codes are in the ring.
     struct Unit {
-        uint32_t q[RT][2][4];
-        uint16_t s[RT][2][kGroups], z[RT][2][kGroups];
+        uint16_t sz[RT][kGroups];
     };
 
+    // Requests a unit: the lane's codes of rows 2 g and 2 g + 1 into its 32 RT bytes of the slot.
     static __device__ __forceinline__ void load(const FewLinearArgs &p, int64_t row0, int block,
-                                                int lane, Unit &u)
+                                                int lane, uint8_t *slot, Unit &u)
     {
         const int g = lane >> 2, t4 = lane & 3, G = p.K / GROUP;
+        const uint16_t *sz = t4 & 1 ? p.z : p.s;
 #pragma unroll
-        for (int r = 0; r < RT; r++)
+        for (int r = 0; r < RT; r++) {
+            // rows past the last one repeat it; what they give is not stored
+            const int64_t last = static_cast<int64_t>(p.N) - 1, row = row0 + r * 16 + 2 * g;
 #pragma unroll
             for (int i = 0; i < 2; i++) {
-                // rows past the last one repeat it; what they give is not stored
-                const int64_t row = min(row0 + r * 16 + 2 * g + i, static_cast<int64_t>(p.N) - 1);
-                const uint8_t *q = p.q + row * (p.K / 2) + block * 64;
+                const uint8_t *q = p.q + min(row + i, last) * (p.K / 2) + block * 64;
+                uint8_t *to = slot + (r * 2 + i) * 512 + lane * 16;
                 if constexpr (GROUP == 128) {
-                    const uint4 v = load_codes16(q + t4 * 16);
-                    u.q[r][i][0] = v.x;
-                    u.q[r][i][1] = v.y;
-                    u.q[r][i][2] = v.z;
-                    u.q[r][i][3] = v.w;
+                    copy_async<16>(to, q + t4 * 16);
                 } else {
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        uint2 v = make_uint2(0, 0);
-                        if (block * 2 + h < G)
-                            v = load_codes8(q + h * 32 + t4 * 8);
-                        u.q[r][i][2 * h] = v.x;
-                        u.q[r][i][2 * h + 1] = v.y;
-                    }
-                }
-#pragma unroll
-                for (int h = 0; h < kGroups; h++) {
-                    const int64_t at = row * G + block * kGroups + h;
-                    const bool in = kGroups == 1 || block * kGroups + h < G;
-                    u.s[r][i][h] = in ? __ldg(p.s + at) : static_cast<uint16_t>(0);
-                    u.z[r][i][h] = in ? __ldg(p.z + at) : static_cast<uint16_t>(0);
+                    copy_async<8>(to, q + t4 * 8);
+                    // of half a unit at the end the first half stands for the second,
+                    // whose scales are zero
+                    copy_async<8>(to + 8, q + (block * 2 + 1 < G ? 32 : 0) + t4 * 8);
                 }
             }
+#pragma unroll
+            for (int h = 0; h < kGroups; h++)
+                u.sz[r][h] = kGroups == 1 || block * kGroups + h < G
+                                 ? __ldg(sz + min(row + (t4 >> 1), last) * G + block * kGroups + h)
+                                 : static_cast<uint16_t>(0);
+        }
     }
 
     static __device__ __forceinline__ void add(const uint8_t *xs, int tile_stride, int blocks,
-                                               int block, int lane, const Unit &u,
-                                               float (&acc)[RT][NT][4])
+                                               int block, int lane, const uint8_t *slot,
+                                               const Unit &u, float (&acc)[RT][NT][4])
     {
         const int t4 = lane & 3;
+        uint32_t q[RT][2][4];
+#pragma unroll
+        for (int r = 0; r < RT; r++)
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+                *reinterpret_cast<uint4 *>(q[r][i]) =
+                    *reinterpret_cast<const uint4 *>(slot + (r * 2 + i) * 512 + lane * 16);
 #pragma unroll
         for (int h = 0; h < kGroups; h++) {
             float part[RT][NT][4] = {};
@@ -155,7 +153,7 @@ struct FewLinear {
                                                             (block * 4 + j) * 512 + lane * 16);
 #pragma unroll
                 for (int r = 0; r < RT; r++) {
-                    const uint32_t w0 = u.q[r][0][j], w1 = u.q[r][1][j];
+                    const uint32_t w0 = q[r][0][j], w1 = q[r][1][j];
                     const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
 #pragma unroll
                     for (int n = 0; n < NT; n++) {
@@ -166,64 +164,79 @@ struct FewLinear {
                     }
                 }
             }
+            float2 sum[NT];
 #pragma unroll
-            for (int n = 0; n < NT; n++) {
-                const float2 sum = *reinterpret_cast<const float2 *>(
+            for (int n = 0; n < NT; n++)
+                sum[n] = *reinterpret_cast<const float2 *>(
                     xs + n * tile_stride + blocks * 2048 + (block * kGroups + h) * 32 + t4 * 8);
 #pragma unroll
-                for (int r = 0; r < RT; r++)
+            for (int r = 0; r < RT; r++) {
+                const float mine = half_of(u.sz[r][h]);
 #pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        const float s = half_of(u.s[r][i][h]), z = half_of(u.z[r][i][h]);
+                for (int i = 0; i < 2; i++) {
+                    const float s = __shfl_sync(0xffffffffu, mine, 2 * i, 4);
+                    const float z = __shfl_sync(0xffffffffu, mine, 2 * i + 1, 4);
+#pragma unroll
+                    for (int n = 0; n < NT; n++) {
                         float *a = &acc[r][n][2 * i];
-                        a[0] = fmaf(s, fmaf(-z, sum.x, part[r][n][2 * i]), a[0]);
-                        a[1] = fmaf(s, fmaf(-z, sum.y, part[r][n][2 * i + 1]), a[1]);
+                        a[0] = fmaf(s, fmaf(-z, sum[n].x, part[r][n][2 * i]), a[0]);
+                        a[1] = fmaf(s, fmaf(-z, sum[n].y, part[r][n][2 * i + 1]), a[1]);
                     }
+                }
             }
         }
     }
 
     // Activations t0 .. t0 + 8 NT of x into shared memory, in the order of the codes, with
-    // their groups' sums; tokens past the last and columns past K are zero.
-    static __device__ void stage(const FewLinearArgs &p, int t0, uint8_t *xs, int tile_stride)
+    // their groups' sums; tokens past the last and columns past K are zero.  A warp takes a
+    // tile's block at a time, a lane what the MMA's lane of that place will read: 4 words of
+    // one token.
+    static __device__ __forceinline__ void stage(const FewLinearArgs &p, int t0, uint8_t *xs,
+                                                 int tile_stride, int lane, int warp)
     {
-        const int words = p.blocks * 16, lane = threadIdx.x & 31;
-        const int items = 8 * NT * words;
-        for (int i0 = threadIdx.x - lane; i0 < items; i0 += 32 * NW) {
-            const int i = i0 + lane, tok = i / words, word = i - tok * words;
-            const int t = t0 + tok;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (t < p.M && word * 8 < p.K)
-                v = __ldg(reinterpret_cast<const uint4 *>(p.x + static_cast<int64_t>(t) * p.K +
-                                                          word * 8));
-            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-            float f[8], sum = 0.0f;
+        const int tok = lane >> 2, t4 = lane & 3;
+        for (int i = warp; i < NT * p.blocks; i += NW) {
+            const int n = i / p.blocks, block = i - n * p.blocks, t = t0 + n * 8 + tok;
+            const uint16_t *x = p.x + static_cast<int64_t>(t) * p.K + block * 128;
+            uint4 v[4];
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                f[2 * e] = __uint_as_float(in[e] << 16);
-                f[2 * e + 1] = __uint_as_float(in[e] & 0xFFFF0000u);
+            for (int j = 0; j < 4; j++) {
+                // in a unit of two groups the lane has two words of each
+                const int word = kGroups == 1 ? t4 * 4 + j : (j >> 1) * 8 + t4 * 2 + (j & 1);
+                v[j] = make_uint4(0, 0, 0, 0);
+                if (t < p.M && block * 128 + word * 8 < p.K)
+                    v[j] = __ldg(reinterpret_cast<const uint4 *>(x + word * 8));
+            }
+            uint8_t *tile = xs + n * tile_stride;
+            float sums[kGroups] = {};
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const uint32_t in[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    f[2 * e] = __uint_as_float(in[e] << 16);
+                    f[2 * e + 1] = __uint_as_float(in[e] & 0xFFFF0000u);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    sums[j / kWords] += f[e];
+                uint4 out;
+                out.x = bf16_pair(f[0] * kUp, f[4] * kUp);
+                out.y = bf16_pair(f[2] * kUp, f[6] * kUp);
+                out.z = bf16_pair(f[1] * kUpHigh, f[5] * kUpHigh);
+                out.w = bf16_pair(f[3] * kUpHigh, f[7] * kUpHigh);
+                *reinterpret_cast<uint4 *>(tile + (block * 4 + j) * 512 + lane * 16) = out;
             }
 #pragma unroll
-            for (int e = 0; e < 8; e++)
-                sum += f[e];
-            uint4 out;
-            out.x = bf16_pair(f[0] * kUp, f[4] * kUp);
-            out.y = bf16_pair(f[2] * kUp, f[6] * kUp);
-            out.z = bf16_pair(f[1] * kUpHigh, f[5] * kUpHigh);
-            out.w = bf16_pair(f[3] * kUpHigh, f[7] * kUpHigh);
-            // words of a group in the order of the lanes that hold their codes
-            constexpr int kLaneWords = kWords;
-            const int block = word / 16, h = word % 16 / (16 / kGroups);
-            const int in_group = word % (16 / kGroups), t4 = in_group / kLaneWords;
-            const int j = h * kLaneWords + in_group % kLaneWords;
-            uint8_t *tile = xs + (tok >> 3) * tile_stride;
-            *reinterpret_cast<uint4 *>(tile + (block * 4 + j) * 512 + (tok & 7) * 64 + t4 * 16) = out;
-#pragma unroll
-            for (int o = 8 / kGroups; o > 0; o >>= 1)
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (in_group == 0)
-                *reinterpret_cast<float *>(tile + p.blocks * 2048 + (block * kGroups + h) * 32 +
-                                           (tok & 7) * 4) = sum * kSum;
+            for (int h = 0; h < kGroups; h++) {
+                float sum = sums[h];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                if (t4 == 0)
+                    *reinterpret_cast<float *>(tile + p.blocks * 2048 +
+                                               (block * kGroups + h) * 32 + tok * 4) = sum * kSum;
+            }
         }
     }
 
@@ -269,112 +282,120 @@ struct FewLinear {
     }
 };
 
-template <int GROUP, int NT, int RT, int NW, int PF>
-__global__ void __launch_bounds__(32 * NW, 1) few_linear_kernel(const FewLinearArgs p)
+// CTA (share, part): its share of the tasks, for the part's 8 NT tokens.  The parts of a
+// share run side by side, so the weights come from HBM once.
+template <int GROUP, int NT, int RT, int NW, int S>
+__global__ void __launch_bounds__(32 * NW, 1) few_linear_kernel(const FewLinearArgs p, int parts)
 {
-    using F = FewLinear<GROUP, NT, RT, NW, PF>;
+    using F = FewLinear<GROUP, NT, RT, NW, S>;
     extern __shared__ __align__(16) uint8_t xs[];
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int tile_stride = F::tile_bytes(p.blocks);
-    // each warp's sums of the task that another one began
+    // each warp's sums of the task that another one began, then its ring
     float4 *heads = reinterpret_cast<float4 *>(xs + NT * tile_stride);
+    uint8_t *ring = xs + NT * tile_stride + F::kHeadBytes + warp * (S * RT * 1024);
+    const int share = blockIdx.x / parts, shares = gridDim.x / parts;
+    const int t0 = (blockIdx.x - share * parts) * (8 * NT);
     const int tasks = (p.N + F::kRows - 1) / F::kRows;
-    const int a = static_cast<int>(static_cast<int64_t>(tasks) * blockIdx.x / gridDim.x);
-    const int e = static_cast<int>(static_cast<int64_t>(tasks) * (blockIdx.x + 1) / gridDim.x);
-    const int units = (e - a) * p.blocks;                  // below 2^31: blocks <= 104
+    const int a = static_cast<int>(static_cast<int64_t>(tasks) * share / shares);
+    const int e = static_cast<int>(static_cast<int64_t>(tasks) * (share + 1) / shares);
+    const int units = (e - a) * p.blocks;
     const int u0 = static_cast<int>(static_cast<int64_t>(units) * warp / NW);
     const int u1 = static_cast<int>(static_cast<int64_t>(units) * (warp + 1) / NW);
     pdl_wait();
     pdl_trigger();
-    for (int t0 = 0; t0 < p.M; t0 += 8 * NT) {
-        typename F::Unit ring[PF];
-        // the next unit to request, the next to add
-        int ask = u0, ask_task = u0 / p.blocks, ask_block = u0 - ask_task * p.blocks;
-        int task = ask_task, block = ask_block;
-        auto request = [&](typename F::Unit &u) {
-            if (ask < u1)
-                F::load(p, static_cast<int64_t>(a + ask_task) * F::kRows, ask_block, lane, u);
-            ask++;
-            if (++ask_block == p.blocks) {
-                ask_block = 0;
-                ask_task++;
-            }
-        };
+    typename F::Unit unit[S];
+    // the next unit to request, the next to add
+    int ask = u0, ask_task = u0 / p.blocks, ask_block = u0 - ask_task * p.blocks;
+    int task = ask_task, block = ask_block;
+    auto request = [&](int slot) {
+        if (ask < u1)
+            F::load(p, static_cast<int64_t>(a + ask_task) * F::kRows, ask_block, lane,
+                    ring + slot * (RT * 1024), unit[slot]);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ask++;
+        if (++ask_block == p.blocks) {
+            ask_block = 0;
+            ask_task++;
+        }
+    };
 #pragma unroll
-        for (int i = 0; i < PF; i++)
-            request(ring[i]);
-        F::stage(p, t0, xs, tile_stride);
-        __syncthreads();
-        float acc[RT][NT][4] = {};
-        bool in_head = block > 0 && u0 < u1;       // another warp has the task's first part
-        for (int u = u0; u < u1;) {
+    for (int i = 0; i < S; i++)
+        request(i);
+    F::stage(p, t0, xs, tile_stride, lane, warp);
+    __syncthreads();
+    float acc[RT][NT][4] = {};
+    bool in_head = block > 0 && u0 < u1;       // another warp has the task's first part
+    for (int u = u0; u < u1;) {
 #pragma unroll
-            for (int i = 0; i < PF; i++) {
-                if (u < u1) {
-                    F::add(xs, tile_stride, p.blocks, block, lane, ring[i], acc);
-                    request(ring[i]);
-                    u++;
-                    if (++block == p.blocks) {
-                        if (in_head)
-                            F::put_head(heads, warp, lane, acc);
-                        else
-                            F::store(p, t0, static_cast<int64_t>(a + task) * F::kRows, lane, acc);
-                        in_head = false;
+        for (int i = 0; i < S; i++) {
+            if (u < u1) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+                F::add(xs, tile_stride, p.blocks, block, lane, ring + i * (RT * 1024), unit[i], acc);
+                request(i);
+                u++;
+                if (++block == p.blocks) {
+                    if (in_head)
+                        F::put_head(heads, warp, lane, acc);
+                    else
+                        F::store(p, t0, static_cast<int64_t>(a + task) * F::kRows, lane, acc);
+                    in_head = false;
 #pragma unroll
-                        for (int r = 0; r < RT; r++)
+                    for (int r = 0; r < RT; r++)
 #pragma unroll
-                            for (int n = 0; n < NT; n++)
+                        for (int n = 0; n < NT; n++)
 #pragma unroll
-                                for (int c = 0; c < 4; c++)
-                                    acc[r][n][c] = 0.0f;
-                        block = 0;
-                        task++;
-                    }
+                            for (int c = 0; c < 4; c++)
+                                acc[r][n][c] = 0.0f;
+                    block = 0;
+                    task++;
                 }
             }
         }
-        // a share that ends inside the task it began in is a head as a whole
-        const bool open = block > 0 && !in_head && u0 < u1;
-        if (in_head)
-            F::put_head(heads, warp, lane, acc);
-        __syncthreads();
-        if (open) {
-            // the rest of this task lies with the warps behind
-            const int end = (task + 1) * p.blocks;
-            for (int w = warp + 1; w < NW; w++) {
-                const int w0 = static_cast<int>(static_cast<int64_t>(units) * w / NW);
-                const int w1 = static_cast<int>(static_cast<int64_t>(units) * (w + 1) / NW);
-                if (w0 >= end)
-                    break;
-                if (w0 == w1)
-                    continue;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    // a share that ends inside the task it began in is a head as a whole
+    const bool open = block > 0 && !in_head && u0 < u1;
+    if (in_head)
+        F::put_head(heads, warp, lane, acc);
+    __syncthreads();
+    if (open) {
+        // the rest of this task lies with the warps behind
+        const int end = (task + 1) * p.blocks;
+        for (int w = warp + 1; w < NW; w++) {
+            const int w0 = static_cast<int>(static_cast<int64_t>(units) * w / NW);
+            const int w1 = static_cast<int>(static_cast<int64_t>(units) * (w + 1) / NW);
+            if (w0 >= end)
+                break;
+            if (w0 == w1)
+                continue;
 #pragma unroll
-                for (int r = 0; r < RT; r++)
+            for (int r = 0; r < RT; r++)
 #pragma unroll
-                    for (int n = 0; n < NT; n++) {
-                        const float4 v = heads[((w * RT + r) * NT + n) * 32 + lane];
-                        acc[r][n][0] += v.x;
-                        acc[r][n][1] += v.y;
-                        acc[r][n][2] += v.z;
-                        acc[r][n][3] += v.w;
-                    }
-            }
-            F::store(p, t0, static_cast<int64_t>(a + task) * F::kRows, lane, acc);
+                for (int n = 0; n < NT; n++) {
+                    const float4 v = heads[((w * RT + r) * NT + n) * 32 + lane];
+                    acc[r][n][0] += v.x;
+                    acc[r][n][1] += v.y;
+                    acc[r][n][2] += v.z;
+                    acc[r][n][3] += v.w;
+                }
         }
-        __syncthreads();                   // the sums have been read: the next tokens may come
+        F::store(p, t0, static_cast<int64_t>(a + task) * F::kRows, lane, acc);
     }
 }
 
 constexpr int kMaxSmem = 227 * 1024;
-constexpr int kMaxBlocks = 13568 / 128;
-using Narrowest = FewLinear<64, 1, 1, 16, 3>;
-static_assert(Narrowest::tile_bytes(kMaxBlocks) + Narrowest::kHeadBytes <= kMaxSmem);
 
-template <int GROUP, int NT, int RT, int NW, int PF>
+template <class F> constexpr int smem_of(int blocks, int nt)
+{
+    return nt * F::tile_bytes(blocks) + F::kHeadBytes + F::kRingBytes;
+}
+
+template <int GROUP, int NT, int RT, int NW, int S>
 cudaError_t launch_few_linear_as(const FewLinearArgs &a, int sms, int dev, cudaStream_t stream)
 {
-    using F = FewLinear<GROUP, NT, RT, NW, PF>;
-    auto kern = few_linear_kernel<GROUP, NT, RT, NW, PF>;
+    using F = FewLinear<GROUP, NT, RT, NW, S>;
+    auto kern = few_linear_kernel<GROUP, NT, RT, NW, S>;
     static std::atomic<uint64_t> raised{0};      // devices whose limit is raised already
     if (!(raised.load(std::memory_order_relaxed) >> (dev & 63) & 1u)) {
         cudaError_t err =
@@ -383,28 +404,30 @@ cudaError_t launch_few_linear_as(const FewLinearArgs &a, int sms, int dev, cudaS
             return err;
         raised.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
     }
-    const int tasks = (a.N + F::kRows - 1) / F::kRows;
-    const int smem = NT * F::tile_bytes(a.blocks) + F::kHeadBytes;
-    return launch_pdl(kern, dim3(std::min(tasks, sms)), dim3(32 * NW), smem, stream, a);
+    const int tasks = (a.N + F::kRows - 1) / F::kRows, parts = (a.M + 8 * NT - 1) / (8 * NT);
+    const int shares = std::min(tasks, std::max(sms / parts, 1));
+    return launch_pdl(kern, dim3(shares * parts), dim3(32 * NW), smem_of<F>(a.blocks, NT), stream, a,
+                      parts);
 }
 
-// Whether the instance's tokens fit shared memory at once.
-template <class F> bool fits(int blocks, int nt)
-{
-    return nt * F::tile_bytes(blocks) + F::kHeadBytes <= kMaxSmem;
-}
+constexpr int kMaxBlocks = 11264 / 128;
+using Narrowest = FewLinear<64, 1, 1, 16, 2>;
+static_assert(smem_of<Narrowest>(kMaxBlocks, 1) <= kMaxSmem);
 
 template <int GROUP>
 cudaError_t launch_few_linear_group(const FewLinearArgs &a, int sms, int dev, cudaStream_t stream)
 {
-    // as many tiles of 8 tokens at once as there are and as fit; with more the weights
-    // are read again
+    // Tiles of 8 tokens at once: two share the unpacking of the codes.  Two tiles of weight
+    // rows share the reading of the activations, where there are enough of them for every SM.
     const int tiles = (a.M + 7) / 8;
-    if (tiles > 2 && fits<FewLinear<GROUP, 4, 2, 8, 3>>(a.blocks, 4))
-        return launch_few_linear_as<GROUP, 4, 2, 8, 3>(a, sms, dev, stream);
-    if (tiles > 1 && fits<FewLinear<GROUP, 2, 2, 16, 2>>(a.blocks, 2))
+    const bool many = a.N >= 64 * sms;
+    if (tiles > 1 && many && smem_of<FewLinear<GROUP, 2, 2, 16, 2>>(a.blocks, 2) <= kMaxSmem)
         return launch_few_linear_as<GROUP, 2, 2, 16, 2>(a, sms, dev, stream);
-    return launch_few_linear_as<GROUP, 1, 1, 16, 3>(a, sms, dev, stream);
+    if (many && smem_of<FewLinear<GROUP, 1, 2, 16, 3>>(a.blocks, 1) <= kMaxSmem)
+        return launch_few_linear_as<GROUP, 1, 2, 16, 3>(a, sms, dev, stream);
+    if (smem_of<FewLinear<GROUP, 1, 1, 16, 4>>(a.blocks, 1) <= kMaxSmem)
+        return launch_few_linear_as<GROUP, 1, 1, 16, 4>(a, sms, dev, stream);
+    return launch_few_linear_as<GROUP, 1, 1, 16, 2>(a, sms, dev, stream);
 }
 
 }  // namespace
