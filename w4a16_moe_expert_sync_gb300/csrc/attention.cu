@@ -53,7 +53,7 @@ namespace w4 {
 
 namespace {
 
-using plan::kItemCost;
+using plan::item_cost;
 using plan::kKeys;
 using plan::kRows;
 using plan::pair_ctas;
@@ -68,7 +68,7 @@ constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 // A group's prefix (first G) or a sequence's own keys.
 struct Entry {
     int place, item0;                      // length and items before it, in its region
-    int span;                              // of one item: kItemCost + tiles; 0: nothing
+    int span;                              // of one item: item_cost + tiles; 0: nothing
     int row_tiles;                         // items per kv head
     int pair;
     int row;                               // a sequence's first row among its group's
@@ -313,7 +313,7 @@ __device__ __forceinline__ int rows_of(const AttnArgs &p, int kind)
 }
 
 // An entry's queries and keys, and its items: span is an item's length in the
-// split (kItemCost + tiles; 0: nothing to do), items of one kv head.
+// split (item_cost + tiles; 0: nothing to do), items of one kv head.
 struct Work {
     int tok0, tokens, k0, k1;
     int span, row_tiles_pair;              // 2 row_tiles + pair
@@ -323,6 +323,7 @@ struct Work {
 
 // What entry e asks for.  More than max_q tokens a sequence: nothing.  Offsets
 // that do not ascend within their bounds set bad.
+template <bool TREE>
 __device__ __forceinline__ Work work_of(const AttnArgs &p, const Index &x, int e, bool flag,
                                         bool &bad)
 {
@@ -359,7 +360,7 @@ __device__ __forceinline__ Work work_of(const AttnArgs &p, const Index &x, int e
     }
     const int rows = w.tokens * p.rep;
     if (rows > 0 && w.k1 > w.k0) {
-        w.span = plan::key_tiles(w.k0, w.k1, p.page_shift) + kItemCost;
+        w.span = plan::key_tiles(w.k0, w.k1, p.page_shift) + item_cost(TREE, plan::is_pair(rows));
         w.row_tiles_pair = 2 * plan::row_tiles(rows) + plan::is_pair(rows);
     }
     return w;
@@ -475,7 +476,7 @@ struct Kernel {
         int4 sum = make_int4(0, 0, 0, 0);
         bool bad = false;
         for (int e = e0; e < e1; e++) {
-            const Work w = work_of(p, x, e, blockIdx.x == 0, bad);
+            const Work w = work_of<TREE>(p, x, e, blockIdx.x == 0, bad);
             const int items = w.row_tiles() * p.Hkv;
             work[e] = w;
             (w.pair() ? sum.z : sum.x) += items * w.span;
@@ -509,7 +510,8 @@ struct Kernel {
             en.item0 = start[(en.pair ? 3 * n : n) + e];
             return en;
         };
-        const int for_pairs = pair_ctas(total.x, total.z, gridDim.x);
+        const int for_pairs = TREE ? plan::tree_pair_ctas(total.x, total.z, gridDim.x)
+                                    : pair_ctas(total.x, total.z, gridDim.x);
         const int for_singles = gridDim.x - for_pairs;
         // warps 0, 1 and 2 work out the pieces of streams 0 and 1 and of the pairs
         const int which = tid >> 5, lane = tid & 31;
@@ -543,7 +545,7 @@ struct Kernel {
                 const int item = first + i, e = find_entry(is, n, item);
                 const Work wa = work[e];
                 const int local = item - is[e];
-                const int t0 = ts[e] + local * wa.span + kItemCost;   // its first tile's place
+                const int t0 = ts[e] + local * wa.span + item_cost(TREE, pair);   // first tile
                 Seg g;
                 g.seq = e < p.G ? -1 : e - p.G;
                 g.row_of_table = e < p.G ? x.group_offsets[e] : e - p.G;
@@ -556,7 +558,7 @@ struct Kernel {
                 g.row0 = (local - g.head * wa.row_tiles()) * step;
                 g.rows = min(step, wa.tokens * p.rep - g.row0);
                 g.tile0 = max(lo - t0, 0);
-                int end = min(hi - t0, wa.span - kItemCost);
+                int end = min(hi - t0, wa.span - item_cost(TREE, pair));
                 if (p.causal && g.seq >= 0)
                     end = min(end, plan::causal_tiles(wa.k1, wa.tokens, g.kbase,
                                                       g.row0 + g.rows - 1, p.rep));
@@ -954,7 +956,7 @@ struct Kernel {
         // How many keys this thread's row of a piece sees, and (a tree's) which of them
         // are named by bits.  The lanes part ways in it, and the tensor-memory
         // instructions that follow need them together again.
-        Window window{INT_MAX, nullptr}, next_window = window;
+        Window window{INT_MAX, nullptr, {0, 0}}, next_window = window;
         auto sees = [&](int i) {
             const Seg &g = piece(i);
             int n = INT_MAX;                   // no row: nothing to mask, nothing kept
@@ -1071,6 +1073,7 @@ struct Kernel {
     struct Window {
         int from;                              // their first position; INT_MAX: no row
         const uint32_t *bits;
+        uint32_t first[2];                     // the first words of them, read in time
     };
 
     // How many keys, from position 0, the query token sees at most.
@@ -1096,6 +1099,8 @@ struct Kernel {
         if constexpr (TREE) {
             window.from = len - (p.q_offsets[b + 1] - p.q_offsets[b]);
             window.bits = p.tree + static_cast<int64_t>(tok) * p.tree_words;
+            window.first[0] = __ldg(window.bits);
+            window.first[1] = p.tree_words > 1 ? __ldg(window.bits + 1) : 0u;
             return len;
         }
         return p.causal ? len - (p.q_offsets[b + 1] - tok) + 1 : len;
@@ -1103,15 +1108,16 @@ struct Kernel {
 
     // 32 columns' bits, the first of which is the window's at-th key: ones before the
     // window, the row's words in it, zeros past those.
-    static __device__ __forceinline__ uint32_t window_word(const AttnArgs &p, const uint32_t *bits,
+    static __device__ __forceinline__ uint32_t window_word(const AttnArgs &p, const Window &window,
                                                            int at)
     {
-        if (at <= -32)
-            return ~0u;
-        const int j = at >> 5;
-        const uint32_t a = j < 0 ? ~0u : j < p.tree_words ? __ldg(bits + j) : 0u;
-        const uint32_t b = j + 1 < p.tree_words ? __ldg(bits + j + 1) : 0u;
-        return __funnelshift_r(a, b, at & 31);
+        auto word = [&](int j) {
+            return j < 0               ? ~0u
+                   : j < 2             ? (j == 0 ? window.first[0] : window.first[1])
+                   : j < p.tree_words ? __ldg(window.bits + j)
+                                       : 0u;
+        };
+        return at <= -32 ? ~0u : __funnelshift_r(word(at >> 5), word((at >> 5) + 1), at & 31);
     }
 
     // P of one tile from its S; columns outside [lo, hi) are masked.  m is the
@@ -1137,7 +1143,7 @@ struct Kernel {
                 if (mine) {
 #pragma unroll
                     for (int i = 0; i < 4; i++)
-                        seen[i] = window_word(p, window.bits, base + 32 * i - window.from);
+                        seen[i] = window_word(p, window, base + 32 * i - window.from);
                 }
                 __syncwarp();
 #pragma unroll

@@ -23,11 +23,17 @@ constexpr int kKeys = 128;                 // keys of a tile
 // against 58.6, four canvases of 256 queries 57.0 and 47.5 against 46.7, nine small
 // groups 25.8 and 27.3 against 26.3.)
 constexpr int kItemCost = 2;
+// Trees: a pair's item holds up its CTA for 6.6 us, and pair items of few tiles (each
+// sequence's own keys, its tree's rows times the heads) are many.
+constexpr int kTreePairCost = 5;
+constexpr float kTreeSingleWeight = 0.8f;
 // A CTA's time for a single tile in those of a pair's, as the CTAs are divided
 // between the two.  (With 0.5, 0.7, 1.0: 120,000 shared tokens and short tails 84.6,
 // 73.6 and 75.7 us, nine small groups 27.6, 26.2 and 27.4.  Both kinds on every CTA, the
 // pairs first: 74.1 and 32.7.)
 constexpr float kSingleWeight = 0.7f;
+
+W4_PLAN int item_cost(bool tree, bool pair) { return tree && pair ? kTreePairCost : kItemCost; }
 
 W4_PLAN int smaller(int a, int b) { return a < b ? a : b; }
 W4_PLAN int larger(int a, int b) { return a > b ? a : b; }
@@ -55,6 +61,21 @@ W4_PLAN int pair_ctas(int singles, int pairs, int grid)
     const float part = pairs / (pairs + kSingleWeight * singles);
     return smaller(pairs,
                    larger(1, smaller(grid - 1, static_cast<int>(part * grid + 0.5f))));
+}
+
+// The same for trees, whose few single items (small trees' own keys) are short: of the
+// two divisions next to even the one whose slower kind is the faster.
+W4_PLAN int tree_pair_ctas(int singles, int pairs, int grid)
+{
+    if (pairs == 0 || singles == 0)
+        return smaller(pairs, grid);
+    const float weighted = kTreeSingleWeight * singles;
+    const int low = larger(1, smaller(grid - 2, static_cast<int>(pairs / (pairs + weighted) * grid)));
+    const float with_low = pairs / static_cast<float>(low), rest_low = weighted / (grid - low);
+    const float with_high = pairs / (low + 1.0f), rest_high = weighted / (grid - low - 1);
+    const bool high = (with_high > rest_high ? with_high : rest_high) <
+                      (with_low > rest_low ? with_low : rest_low);
+    return smaller(pairs, larger(1, low + high));
 }
 
 // The tiles of an entry's keys k0 .. k1, which start where k0's page does.
