@@ -24,7 +24,7 @@
 // Roles of a CTA's twelve warps: warps 0-3 and 4-7 are the softmax of streams
 // 0 and 1 (a thread per row), warp 8 loads K and V by TMA into a ring of
 // slots, warps 9 and 10 issue the MMAs (of both streams of a pair; of streams 0
-// and 1), warp 11 only completes its group of four.  While one stream's softmax
+// and 1), warp 11 only completes its group of four (trees with heads of 64: loads V).  While one stream's softmax
 // runs the tensor cores work for the other.
 //
 // Bounds and measured times (GB300, both kernels, back to back in a graph):
@@ -434,16 +434,22 @@ struct Kernel {
     static constexpr int kQBytes = 2 * kTileBytes;
     static constexpr int kRingBytes = kSlots * kTileBytes;
     static constexpr size_t kSmem = 1024 + kQBytes + kRingBytes;
-    static constexpr uint32_t kS = 0, kO = 256;                // TMEM columns of stream 0
+    // Heads of 64 leave room for a third S: a pair's streams then take the three in turn,
+    // and a tile's QK need not wait for the softmax and PV of its stream's last.
+    static constexpr bool kAhead = TREE && D == 64;
+    static constexpr uint32_t kS = 0, kO = kAhead ? 384 : 256; // TMEM columns of stream 0
     static constexpr uint32_t kQk = idesc_16bit_f32(128, kKeys, BF16);
     static constexpr uint32_t kPv = idesc_16bit_f32(128, D, BF16) | (1u << 16);   // V is N-major
 
     struct Shared {
         alignas(8) uint64_t full[kSlots], empty[kSlots];
         uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2], cleared, drained[2];
+        // kAhead: those of odd tiles, for either side may then be a tile ahead of the other
+        // and a wait by parity must not pass two phases; a PV of the stream's
+        uint64_t s_full_odd[2], p_ready_odd[2], o_done[2];
         uint32_t tmem;
         int abort_flag;
-        int requested;                         // fills requested of the ring so far
+        int requested[2];                      // fills requested so far (kAhead: of K, of V)
         int seg0[3], segs[3], tiles[3];        // single items of streams 0 and 1; pairs
         Seg first[3];                          // the first piece of each
         int4 sums[kThreads / 32];
@@ -623,10 +629,12 @@ struct Kernel {
     // been used, and the parity says what it means.
     static __device__ __forceinline__ bool wait_full(const AttnArgs &p, Shared &s, int fill)
     {
-        volatile int *requested = &s.requested, *abort_flag = &s.abort_flag;
-        if (!__all_sync(0xffffffffu, *requested > fill)) {
+        // (kAhead: K and V are requested by two warps, each in its own slots)
+        volatile int *requested = &s.requested[kAhead ? fill & 1 : 0], *abort_flag = &s.abort_flag;
+        const int asked = kAhead ? fill >> 1 : fill;
+        if (!__all_sync(0xffffffffu, *requested > asked)) {
             const uint64_t t0 = global_timer_ns();
-            for (uint32_t it = 1; !__all_sync(0xffffffffu, *requested > fill); it++) {
+            for (uint32_t it = 1; !__all_sync(0xffffffffu, *requested > asked); it++) {
                 __nanosleep(20);
                 if ((it & 63u) == 0) {
                     if (__any_sync(0xffffffffu, *abort_flag != 0))
@@ -649,7 +657,7 @@ struct Kernel {
     // One look at whether fill `fill` has landed.
     static __device__ __forceinline__ bool landed(Shared &s, int fill)
     {
-        volatile int *requested = &s.requested;
+        volatile int *requested = &s.requested[0];
         return __all_sync(0xffffffffu, *requested > fill) &&
                __all_sync(0xffffffffu, mbar_try_wait(&s.full[fill % kSlots], (fill / kSlots) & 1));
     }
@@ -666,7 +674,8 @@ struct Kernel {
         if (lane == 0) {
             mbar_arrive_expect_tx(&s.full[slot], kTileBytes);
             __threadfence_block();
-            *static_cast<volatile int *>(&s.requested) = fill + 1;
+            *static_cast<volatile int *>(&s.requested[kAhead ? fill & 1 : 0]) =
+                kAhead ? (fill >> 1) + 1 : fill + 1;
         }
         __syncwarp();
         if constexpr (IN_TURN) {
@@ -696,10 +705,13 @@ struct Kernel {
     // One warp, once no role requests any more.
     static __device__ void land(Shared &s)
     {
-        const int n = s.requested;
-        for (int slot = 0; slot < min(n, kSlots); slot++) {
-            const int fill = (n - 1 - slot) / kSlots * kSlots + slot;
-            mbar_drain(&s.full[slot], (fill / kSlots) & 1);
+        // kAhead: K has the even slots, V the odd ones
+        constexpr int kKinds = kAhead ? 2 : 1, kOwn = kSlots / kKinds;
+        static_assert(!kAhead || kSlots % 2 == 0);
+        for (int kind = 0; kind < kKinds; kind++) {
+            const int n = s.requested[kind];
+            for (int slot = 0; slot < min(n, kOwn); slot++)
+                mbar_drain(&s.full[slot * kKinds + kind], (n - 1 - slot) / kOwn & 1);
         }
     }
 
@@ -749,6 +761,60 @@ struct Kernel {
         return w;
     }
 
+    // The tiles of K (kind 0) or of V in the order of fill_of, by a warp of their own each: a
+    // request takes some hundred cycles a box, and with one warp for both it is the slower
+    // half of a pair tile with heads of 64 (pages of 16 tokens: 3000 cycles).  Page ids are
+    // read two tiles before they are used.
+    struct Ahead {
+        bool got, in;                          // a tile; whether this lane has a page of it
+        int head, id;
+    };
+    static __device__ void loader_of(const AttnArgs &p, Shared &s, uint8_t *ring, int lane, int kind)
+    {
+        Walk pairs = walk(p, s, 2), one = walk(p, s, 0), two = walk(p, s, 1);
+        bool first = false;                    // whose turn it was last
+        auto next = [&]() {
+            Ahead n{true, false, 0, p.P};
+            auto take = [&](Walk &w) {
+                n.head = w.g.head;
+                const int key = w.g.kbase + w.t * kKeys + lane * p.page;
+                n.in = lane < kKeys / p.page && key < w.g.k1;
+                if (n.in)
+                    n.id = __ldg(p.table + static_cast<int64_t>(w.g.row_of_table) * p.W +
+                                 (key >> p.page_shift));
+                w.t++;
+            };
+            if (pairs.more()) {
+                take(pairs);
+            } else {
+                const bool a = one.more(), b = two.more();
+                first = a && !(first && b);    // streams in turn; one that is out drops out
+                if (first)
+                    take(one);
+                else if (b)
+                    take(two);
+                else
+                    n.got = false;
+            }
+            return n;
+        };
+        Ahead a = next(), b = next();
+        for (int tile = 0; a.got; tile++) {
+            const Ahead c = next();
+            if (a.id < 0 || a.id > p.P || (a.in && a.id == p.P)) {
+                if (p.status && kind == 0)
+                    atomicOr(p.status, W4_DEV_BAD_PAGE);
+                a.id = p.P;
+            }
+            __syncwarp();
+            if (!load_slot(p, s, ring, 2 * tile + kind, kind ? &p.v_map : &p.k_map, a.head, a.id,
+                           lane))
+                return;
+            a = b;
+            b = c;
+        }
+    }
+
     // The tiles in the order of fill_of; a tile's page ids are read while the
     // tile before it waits for its slots.
     static __device__ void loader(const AttnArgs &p, Shared &s, uint8_t *ring, int lane)
@@ -791,7 +857,8 @@ struct Kernel {
     // ------------------------------------------------------------- issuing
     // S = Q K^T of a stream's tile, whose K has landed; it is let go with the last use.
     static __device__ __forceinline__ void issue_qk(const AttnArgs &p, Shared &s, uint8_t *qbuf,
-                                                    uint8_t *ring, int stream, int fill, bool last_use)
+                                                    uint8_t *ring, int stream, int buf, int fill,
+                                                    bool last_use, uint64_t *s_full)
     {
         const int slot = fill % kSlots;
         tc_fence_after();
@@ -800,9 +867,9 @@ struct Kernel {
         const uint64_t kd = sdesc_mn_sw128(smem_u32(ring + slot * kTileBytes), kGroup, kBlock);
 #pragma unroll
         for (int k = 0; k < D / 16; k++)
-            mma_ss_elect(s.tmem + kS + 128 * stream, qd + (k / 4) * (kRows * 128 >> 4) + k % 4 * 2,
+            mma_ss_elect(s.tmem + kS + 128 * buf, qd + (k / 4) * (kRows * 128 >> 4) + k % 4 * 2,
                          kd + (k / 4) * (kBlock >> 4) + k % 4 * 2, kQk, k > 0);
-        tc_commit_elect(&s.s_full[stream]);
+        tc_commit_elect(s_full);
         if (last_use)
             tc_commit_elect(&s.empty[slot]);
     }
@@ -810,14 +877,14 @@ struct Kernel {
     // O (+)= P V of a stream's tile, whose V has landed, 16 keys at a time; steps that lie wholly
     // before the entry's first key or past its last stay out.
     static __device__ __forceinline__ void issue_pv(const AttnArgs &p, Shared &s, uint8_t *ring,
-                                                    int stream, int fill, int before, int keys,
-                                                    bool first, bool last, bool last_use)
+                                                    int stream, int buf, int fill, int before,
+                                                    int keys, bool first, bool last, bool last_use)
     {
         const int slot = fill % kSlots;
         tc_fence_after();
         __syncwarp();
         const uint32_t va = smem_u32(ring + slot * kTileBytes);
-        const uint32_t ts = s.tmem + kS + 128 * stream, to = s.tmem + kO + D * stream;
+        const uint32_t ts = s.tmem + kS + 128 * buf, to = s.tmem + kO + D * stream;
         const uint64_t vd = sdesc_mn_sw128(va, kGroup, kBlock);
         if (before <= 0 && keys > kKeys - 16) {
 #pragma unroll
@@ -860,9 +927,43 @@ struct Kernel {
                 for (int st = 0; st < 2; st++) {
                     if (!wait(p, s, &s.q_ready[st], seg_phase))
                         return;
-                    issue_qk(p, s, qbuf, ring, st, 2 * r, st == 1);
+                    issue_qk(p, s, qbuf, ring, st, st, 2 * r, st == 1,
+                             kAhead && (r & 1) ? &s.s_full_odd[st] : &s.s_full[st]);
                 }
                 seg_phase ^= 1;
+                if constexpr (kAhead) {
+                    // step n is stream n % 2's tile n / 2, in S n % 3; its QK follows the PV
+                    // that was the last to use that S, of step n - 3
+                    if (tiles > 1) {
+                        if (!wait_full(p, s, 2 * r + 2))
+                            return;
+                        issue_qk(p, s, qbuf, ring, 0, 2, 2 * r + 2, false,
+                                 r & 1 ? &s.s_full[0] : &s.s_full_odd[0]);
+                    }
+                    int buf = 0;
+                    for (int n = 0; n < 2 * tiles; n++) {
+                        const int st = n & 1, t = n >> 1, ahead = (n + 3) >> 1;
+                        if (st == 0 && !wait_full(p, s, 2 * (r + t) + 1))
+                            return;
+                        // (tile r + t of the CTA's)
+                        if (!wait(p, s, (r + t) & 1 ? &s.p_ready_odd[st] : &s.p_ready[st],
+                                  (r + t) >> 1 & 1))
+                            return;
+                        const int at = base + t * kKeys;
+                        issue_pv(p, s, ring, st, buf, 2 * (r + t) + 1, g.k0 - at, g.k1 - at, t == 0,
+                                 t == tiles - 1, st == 1);
+                        tc_commit_elect(&s.o_done[st]);
+                        if (ahead < tiles) {
+                            if (st == 1 && !wait_full(p, s, 2 * (r + ahead)))
+                                return;
+                            issue_qk(p, s, qbuf, ring, st ^ 1, buf, 2 * (r + ahead), st == 0,
+                                     (r + ahead) & 1 ? &s.s_full_odd[st ^ 1] : &s.s_full[st ^ 1]);
+                        }
+                        buf = buf == 2 ? 0 : buf + 1;
+                    }
+                    r += tiles;
+                    continue;
+                }
                 for (int t = 0; t < tiles; t++, r++) {
                     if (!wait_full(p, s, 2 * r + 1))
                         return;
@@ -871,7 +972,7 @@ struct Kernel {
                         if (!wait(p, s, &s.p_ready[st], tile_phase))
                             return;
                         const int at = base + t * kKeys;
-                        issue_pv(p, s, ring, st, 2 * r + 1, g.k0 - at, g.k1 - at, t == 0,
+                        issue_pv(p, s, ring, st, st, 2 * r + 1, g.k0 - at, g.k1 - at, t == 0,
                                  t == tiles - 1, st == 1);
                         if (t + 1 < tiles && !here) {
                             if (!wait_full(p, s, 2 * r + 2))
@@ -879,7 +980,8 @@ struct Kernel {
                             here = true;
                         }
                         if (t + 1 < tiles)
-                            issue_qk(p, s, qbuf, ring, st, 2 * r + 2, st == 1);
+                            issue_qk(p, s, qbuf, ring, st, st, 2 * r + 2, st == 1,
+                                     &s.s_full[st]);
                     }
                     tile_phase ^= 1;
                 }
@@ -898,12 +1000,12 @@ struct Kernel {
                 const int fill = 2 * fill_of(s, stream, r);
                 if (!wait_full(p, s, fill))
                     return;
-                issue_qk(p, s, qbuf, ring, stream, fill, true);
+                issue_qk(p, s, qbuf, ring, stream, stream, fill, true, &s.s_full[stream]);
                 if (!wait_full(p, s, fill + 1) || !wait(p, s, &s.p_ready[stream], tile_phase))
                     return;
                 tile_phase ^= 1;
                 const int at = base + t * kKeys;
-                issue_pv(p, s, ring, stream, fill + 1, g.k0 - at, g.k1 - at, t == 0,
+                issue_pv(p, s, ring, stream, stream, fill + 1, g.k0 - at, g.k1 - at, t == 0,
                          t == tiles - 1, true);
             }
         }
@@ -936,7 +1038,7 @@ struct Kernel {
     {
         const int tid = threadIdx.x & 127, warp = tid >> 5;
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-        const uint32_t ts = s.tmem + lanes + kS + 128 * stream;
+        uint32_t ts = s.tmem + lanes + kS + 128 * stream;
         const uint32_t to = s.tmem + lanes + kO + D * stream;
         uint8_t *q = qbuf + stream * kTileBytes;
         uint32_t s_phase = 0, o_phase = 0, clear_phase = 0;
@@ -990,10 +1092,17 @@ struct Kernel {
             const bool busy = rows > (tid & ~31);
             float m = -INFINITY, l = 0.0f;     // m in units of log2
             int base = g.kbase + g.tile0 * kKeys;
+            if constexpr (kAhead)
+                ts = s.tmem + lanes + kS + 128 * stream;
             for (int t = 0; t < g.tiles; t++, r++, base += kKeys) {
-                if (!wait(p, s, &s.s_full[stream], s_phase))
-                    return false;
-                s_phase ^= 1;
+                if (kAhead && pair) {
+                    if (!wait(p, s, r & 1 ? &s.s_full_odd[stream] : &s.s_full[stream], r >> 1 & 1))
+                        return false;
+                } else {
+                    if (!wait(p, s, &s.s_full[stream], s_phase))
+                        return false;
+                    s_phase ^= 1;
+                }
                 tc_fence_after();
                 if (t == g.tiles - 1 && another) {
                     fetch(i + 1);
@@ -1001,9 +1110,13 @@ struct Kernel {
                 }
                 // a warp without rows leaves P as it is: a row's P only meets its own O
                 __syncwarp();
-                if (busy)
-                    tile(p, ts, to, limit == INT_MAX ? 0 : g.k0 - base,
-                         limit == INT_MAX ? kKeys : limit - base, window, base, t > 0, m, l);
+                if (busy &&
+                    !tile(p, s, ts, to, limit == INT_MAX ? 0 : g.k0 - base,
+                          limit == INT_MAX ? kKeys : limit - base, window, base, t > 0,
+                          kAhead && pair ? &s.o_done[stream] : nullptr, r - 1, m, l))
+                    return false;
+                if (kAhead && pair)            // the S of two steps on
+                    ts += ts - (s.tmem + lanes + kS) == 0 ? 256 : -128;
                 if (((g.k1 - base < kKeys && (g.k1 & 15)) || (g.k0 > base && (g.k0 & 15))) &&
                     !clear_ends(p, s, ring, 2 * fill_of(s, which, r) + 1, g.k0 - base,
                                 g.k1 - base, pair, stream, tid, clear_phase))
@@ -1011,7 +1124,8 @@ struct Kernel {
                 // one arrival a warp: a thread's each would take a few cycles of the barrier
                 tc_fence_before();
                 __syncwarp();
-                mbar_arrive_elect(&s.p_ready[stream]);
+                mbar_arrive_elect(kAhead && pair && (r & 1) ? &s.p_ready_odd[stream]
+                                                            : &s.p_ready[stream]);
             }
             if (another) {
                 if (g.tiles == 0) {
@@ -1129,8 +1243,11 @@ struct Kernel {
     // P is rounded to the values' type for the MMA (its
     // denominator sums the unrounded).  When S is here, every MMA before it has
     // completed, so O may be changed.
-    static __device__ __forceinline__ void tile(const AttnArgs &p, uint32_t ts, uint32_t to, int lo,
-                                                int hi, const Window &window, int base, bool has_o,
+    // (Not with o_done: there the PV before may be under way; it is awaited where O changes.)
+    // False once a wait has given up.
+    static __device__ __forceinline__ bool tile(const AttnArgs &p, Shared &s, uint32_t ts,
+                                                uint32_t to, int lo, int hi, const Window &window,
+                                                int base, bool has_o, uint64_t *o_done, int last_pv,
                                                 float &m, float &l)
     {
         uint32_t v[128];
@@ -1169,8 +1286,14 @@ struct Kernel {
             const float alpha = move ? ex2(m - (tm - kLift)) : 1.0f;
             m = move ? tm - kLift : m;
             l *= alpha;
-            if (has_o)
+            if (has_o) {
+                if (o_done) {
+                    if (!wait(p, s, o_done, last_pv & 1))
+                        return false;
+                    tc_fence_after();
+                }
                 rescale(to, alpha);
+            }
         }
         const float ref = m == -INFINITY ? 0.0f : m;
         const uint64_t scale2 = both(p.scale_log2), ref2 = both(-ref);
@@ -1190,6 +1313,7 @@ struct Kernel {
         const uint64_t all = add2(sum[0], sum[1]);
         l += low(all) + high(all);
         tmem_wait_st();
+        return true;
     }
 
     static __device__ __forceinline__ void rescale(uint32_t to, float alpha)
@@ -1301,10 +1425,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             mbar_init(&s.p_ready[i], kRows / 32);
             mbar_init(&s.o_full[i], 1);
             mbar_init(&s.drained[i], 1);
+            mbar_init(&s.o_done[i], 1);
+            mbar_init(&s.s_full_odd[i], 1);
+            mbar_init(&s.p_ready_odd[i], kRows / 32);
         }
         mbar_init(&s.cleared, 2 * kRows / 32);
         s.abort_flag = 0;
-        s.requested = 0;
+        s.requested[0] = s.requested[1] = 0;
         fence_mbar_init();
         prefetch_tmap(&p.k_map);
         prefetch_tmap(&p.v_map);
@@ -1326,7 +1453,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
         K::softmax(p, s, qbuf, ring, warp >> 2);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == 8)
+        if (K::kAhead && warp == 8)
+            K::loader_of(p, s, ring, lane, 0);
+        else if (K::kAhead && warp == 11)
+            K::loader_of(p, s, ring, lane, 1);
+        else if (warp == 8)
             K::loader(p, s, ring, lane);
         else if (warp < 11)
             K::issuer(p, s, qbuf, ring, warp - 9);
