@@ -446,7 +446,7 @@ struct Kernel {
         uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2], cleared, drained[2];
         // kAhead: those of odd tiles, for either side may then be a tile ahead of the other
         // and a wait by parity must not pass two phases; a PV of the stream's
-        uint64_t s_full_odd[2], p_ready_odd[2], o_done[2];
+        uint64_t s_full_odd[2], p_ready_odd[2], o_done[2], o_done_odd[2];
         uint32_t tmem;
         int abort_flag;
         int requested[2];                      // fills requested so far (kAhead: of K, of V)
@@ -901,6 +901,70 @@ struct Kernel {
             tc_commit_elect(&s.o_full[stream]);
     }
 
+    // A pair's MMAs with three S buffers, the PVs by one warp and the QKs by the other (a
+    // warp beside two of softmax takes some 50 cycles an MMA: both kinds by one warp paced the
+    // loop).  Step n is stream n % 2's tile n / 2 of the CTA's, in S n % 3.  The QK of step n + 3
+    // goes into the S that step n leaves, once its PV is done.  Of the barriers in pairs an odd
+    // tile of the CTA's has the second: either side may be a tile ahead of the other, and a
+    // wait by parity must not pass two phases.
+    static __device__ __forceinline__ uint64_t *of_tile(uint64_t *even, uint64_t *odd, int stream,
+                                                        int tile)
+    {
+        return (tile & 1 ? odd : even) + stream;
+    }
+
+    static __device__ __forceinline__ void issue_pvs_ahead(const AttnArgs &p, Shared &s, uint8_t *ring)
+    {
+        const Seg *segs = p.segs + p.cap_b + s.seg0[2];
+        for (int i = 0, r = 0, buf = 0; i < s.segs[2]; i++) {
+            const Seg &g = i == 0 ? s.first[2] : segs[i];
+            const int tiles = g.tiles, base = g.kbase + g.tile0 * kKeys;
+            for (int n = 0; n < 2 * tiles; n++) {
+                const int st = n & 1, t = n >> 1, tile = r + t, at = base + t * kKeys;
+                if (st == 0 && !wait_full(p, s, 2 * tile + 1))
+                    return;
+                if (!wait(p, s, of_tile(s.p_ready, s.p_ready_odd, st, tile), tile >> 1 & 1))
+                    return;
+                issue_pv(p, s, ring, st, buf, 2 * tile + 1, g.k0 - at, g.k1 - at, t == 0,
+                         t == tiles - 1, st == 1);
+                tc_commit_elect(of_tile(s.o_done, s.o_done_odd, st, tile));
+                buf = buf == 2 ? 0 : buf + 1;
+            }
+            r += tiles;
+        }
+    }
+
+    static __device__ __forceinline__ void issue_qks_ahead(const AttnArgs &p, Shared &s,
+                                                           uint8_t *qbuf, uint8_t *ring)
+    {
+        const Seg *segs = p.segs + p.cap_b + s.seg0[2];
+        uint32_t seg_phase = 0;
+        for (int i = 0, r = 0, buf = 0; i < s.segs[2]; i++) {
+            const Seg &g = i == 0 ? s.first[2] : segs[i];
+            const int tiles = g.tiles;
+            for (int n = 0; n < 2 * tiles; n++) {
+                const int st = n & 1, tile = r + (n >> 1);
+                if (st == 0 && !wait_full(p, s, 2 * tile))
+                    return;
+                if (n < 2) {
+                    if (!wait(p, s, &s.q_ready[st], seg_phase))
+                        return;
+                    seg_phase ^= st;
+                }
+                // the S that it writes is that of the step three before
+                const int before = 2 * r + n - 3;
+                if (before >= 0 &&
+                    !wait(p, s, of_tile(s.o_done, s.o_done_odd, before & 1, before >> 1),
+                          before >> 2 & 1))
+                    return;
+                issue_qk(p, s, qbuf, ring, st, buf, 2 * tile, st == 1,
+                         of_tile(s.s_full, s.s_full_odd, st, tile));
+                buf = buf == 2 ? 0 : buf + 1;
+            }
+            r += tiles;
+        }
+    }
+
     // A stream's MMAs in turn: S of a tile, then, when its P is there, O.  The
     // next tile's S overwrites this one's P: MMAs of one thread complete in
     // order.
@@ -915,7 +979,14 @@ struct Kernel {
                                                      uint8_t *ring, int stream)
     {
         uint32_t seg_phase = 0, tile_phase = 0;
-        if (stream == 0) {
+        if (kAhead && s.segs[2] > 0) {
+            if (stream == 0)
+                issue_pvs_ahead(p, s, ring);
+            else
+                issue_qks_ahead(p, s, qbuf, ring);
+            return;
+        }
+        if (stream == 0 && !kAhead) {
             const Seg *segs = p.segs + p.cap_b + s.seg0[2];
             for (int i = 0, r = 0; i < s.segs[2]; i++) {
                 const Seg &g = i == 0 ? s.first[2] : segs[i];
@@ -927,43 +998,9 @@ struct Kernel {
                 for (int st = 0; st < 2; st++) {
                     if (!wait(p, s, &s.q_ready[st], seg_phase))
                         return;
-                    issue_qk(p, s, qbuf, ring, st, st, 2 * r, st == 1,
-                             kAhead && (r & 1) ? &s.s_full_odd[st] : &s.s_full[st]);
+                    issue_qk(p, s, qbuf, ring, st, st, 2 * r, st == 1, &s.s_full[st]);
                 }
                 seg_phase ^= 1;
-                if constexpr (kAhead) {
-                    // step n is stream n % 2's tile n / 2, in S n % 3; its QK follows the PV
-                    // that was the last to use that S, of step n - 3
-                    if (tiles > 1) {
-                        if (!wait_full(p, s, 2 * r + 2))
-                            return;
-                        issue_qk(p, s, qbuf, ring, 0, 2, 2 * r + 2, false,
-                                 r & 1 ? &s.s_full[0] : &s.s_full_odd[0]);
-                    }
-                    int buf = 0;
-                    for (int n = 0; n < 2 * tiles; n++) {
-                        const int st = n & 1, t = n >> 1, ahead = (n + 3) >> 1;
-                        if (st == 0 && !wait_full(p, s, 2 * (r + t) + 1))
-                            return;
-                        // (tile r + t of the CTA's)
-                        if (!wait(p, s, (r + t) & 1 ? &s.p_ready_odd[st] : &s.p_ready[st],
-                                  (r + t) >> 1 & 1))
-                            return;
-                        const int at = base + t * kKeys;
-                        issue_pv(p, s, ring, st, buf, 2 * (r + t) + 1, g.k0 - at, g.k1 - at, t == 0,
-                                 t == tiles - 1, st == 1);
-                        tc_commit_elect(&s.o_done[st]);
-                        if (ahead < tiles) {
-                            if (st == 1 && !wait_full(p, s, 2 * (r + ahead)))
-                                return;
-                            issue_qk(p, s, qbuf, ring, st ^ 1, buf, 2 * (r + ahead), st == 0,
-                                     (r + ahead) & 1 ? &s.s_full_odd[st ^ 1] : &s.s_full[st ^ 1]);
-                        }
-                        buf = buf == 2 ? 0 : buf + 1;
-                    }
-                    r += tiles;
-                    continue;
-                }
                 for (int t = 0; t < tiles; t++, r++) {
                     if (!wait_full(p, s, 2 * r + 1))
                         return;
@@ -1092,11 +1129,9 @@ struct Kernel {
             const bool busy = rows > (tid & ~31);
             float m = -INFINITY, l = 0.0f;     // m in units of log2
             int base = g.kbase + g.tile0 * kKeys;
-            if constexpr (kAhead)
-                ts = s.tmem + lanes + kS + 128 * stream;
             for (int t = 0; t < g.tiles; t++, r++, base += kKeys) {
                 if (kAhead && pair) {
-                    if (!wait(p, s, r & 1 ? &s.s_full_odd[stream] : &s.s_full[stream], r >> 1 & 1))
+                    if (!wait(p, s, of_tile(s.s_full, s.s_full_odd, stream, r), r >> 1 & 1))
                         return false;
                 } else {
                     if (!wait(p, s, &s.s_full[stream], s_phase))
@@ -1113,7 +1148,8 @@ struct Kernel {
                 if (busy &&
                     !tile(p, s, ts, to, limit == INT_MAX ? 0 : g.k0 - base,
                           limit == INT_MAX ? kKeys : limit - base, window, base, t > 0,
-                          kAhead && pair ? &s.o_done[stream] : nullptr, r - 1, m, l))
+                          kAhead && pair ? of_tile(s.o_done, s.o_done_odd, stream, r - 1) : nullptr,
+                          (r - 1) >> 1 & 1, m, l))
                     return false;
                 if (kAhead && pair)            // the S of two steps on
                     ts += ts - (s.tmem + lanes + kS) == 0 ? 256 : -128;
@@ -1124,8 +1160,8 @@ struct Kernel {
                 // one arrival a warp: a thread's each would take a few cycles of the barrier
                 tc_fence_before();
                 __syncwarp();
-                mbar_arrive_elect(kAhead && pair && (r & 1) ? &s.p_ready_odd[stream]
-                                                            : &s.p_ready[stream]);
+                mbar_arrive_elect(kAhead && pair ? of_tile(s.p_ready, s.p_ready_odd, stream, r)
+                                                 : &s.p_ready[stream]);
             }
             if (another) {
                 if (g.tiles == 0) {
@@ -1247,7 +1283,7 @@ struct Kernel {
     // False once a wait has given up.
     static __device__ __forceinline__ bool tile(const AttnArgs &p, Shared &s, uint32_t ts,
                                                 uint32_t to, int lo, int hi, const Window &window,
-                                                int base, bool has_o, uint64_t *o_done, int last_pv,
+                                                int base, bool has_o, uint64_t *o_done, uint32_t pv_phase,
                                                 float &m, float &l)
     {
         uint32_t v[128];
@@ -1288,7 +1324,7 @@ struct Kernel {
             l *= alpha;
             if (has_o) {
                 if (o_done) {
-                    if (!wait(p, s, o_done, last_pv & 1))
+                    if (!wait(p, s, o_done, pv_phase))
                         return false;
                     tc_fence_after();
                 }
@@ -1426,6 +1462,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
             mbar_init(&s.o_full[i], 1);
             mbar_init(&s.drained[i], 1);
             mbar_init(&s.o_done[i], 1);
+            mbar_init(&s.o_done_odd[i], 1);
             mbar_init(&s.s_full_odd[i], 1);
             mbar_init(&s.p_ready_odd[i], kRows / 32);
         }
