@@ -17,6 +17,16 @@ from .build import LIB as _LIB_PATH
 
 _lock = threading.Lock()
 _lib = None
+_torch = None
+
+
+def _load_torch():
+    """torch, for the calls where an import statement's half microsecond counts."""
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                       "include", "w4moe.h")
@@ -173,7 +183,7 @@ def _ptr(t):
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
-    import torch
+    torch = _torch or _load_torch()
     # the handle alone: building a Stream object costs several microseconds a call
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
@@ -194,7 +204,7 @@ def _result(shape, dtype, device, stream):
     """A tensor that a call on `stream` fills and returns: of that stream's pool, for
     earlier work of another stream may still use what that one's pool hands out, and
     held, once let go, until the current stream's work of then has run."""
-    import torch
+    torch = _torch or _load_torch()
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     t = _scratch(shape, dtype, device, stream)
@@ -227,7 +237,7 @@ def _require(specs):
 def _on_current_device(*ts):
     """The kernels run on the current device: tensors of another one, or of none, are
     refused.  Returns the device."""
-    import torch
+    torch = _torch or _load_torch()
     devices = {t.get_device() for t in ts if t is not None}
     if -1 in devices:
         raise ValueError("tensors passed to the CUDA library must live on the GPU")
@@ -241,13 +251,13 @@ def _raw_stream(stream, device):
     """The handle of a call's stream, by default the device's current one."""
     if stream is not None:
         return stream.cuda_stream
-    import torch
+    torch = _torch or _load_torch()
     return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _result_like(t, stream):
     """_result of t's shape and type."""
-    import torch
+    torch = _torch or _load_torch()
     if stream is None:
         return torch.empty_like(t, memory_format=torch.contiguous_format)
     return _result(t.shape, t.dtype, t.device, stream)
@@ -719,7 +729,7 @@ def w4_w4a16_linear(x, q, s, z, group: int = 128, workspace=None, out=None, dev_
 def w4_w4a16_linear_few(x, q, s, z, group: int = 128, out=None, stream=None):
     """w4_w4a16_linear for up to 32 rows, in one launch without a workspace: y [M, N]
     bf16 = x [M, K] bf16 . deq(W)^T with W packed as w4_quantize writes it."""
-    import torch
+    torch = _torch or _load_torch()
     if x.dim() != 2 or q.dim() != 2 or group <= 0:
         raise ValueError("x must be [M, K] and the packed weight [N, K / 2]")
     M, K = x.shape
@@ -817,7 +827,7 @@ def w4_gumbel_argmax_sample(logits, seed: int, offset: int = 0, workspace=None, 
 # --------------------------------------------------------------------------
 def _require_int32(*ts):
     """Contiguous int32 CUDA tensors (or None)."""
-    import torch
+    torch = _torch or _load_torch()
     int32 = torch.int32
     for t in ts:
         if t is None:
@@ -1035,7 +1045,7 @@ def w4_rope_steps(rot: int, base: float = 10000.0, method: str = "linear", facto
 def _rope_inputs(q, k, steps, positions, q_weight, k_weight):
     """(0 or 1 for the type, shape of q, kv heads, strides of q and k) of a rotation's
     inputs, checked but for their device."""
-    import torch
+    torch = _torch or _load_torch()
     dtype = q.dtype
     code = 0 if dtype is torch.bfloat16 else 1 if dtype is torch.float16 else -1
     if code < 0 or k.dtype is not dtype:
@@ -1136,7 +1146,7 @@ def w4_attn_shared_prefix_workspace_size(T: int, B: int, G: int, max_q: int, Hq:
 def _attn(name, masks, q, k_pages, v_pages, table, lens, q_offsets, group_offsets, shared_lens,
           max_q, scale, workspace, out, dev_status, stream):
     """Either attention: masks(T) gives its arguments behind max_q and those before scale."""
-    import torch
+    torch = _torch or _load_torch()
     dtype, (P, page, Hkv, D), strides = _kv_planes(k_pages, v_pages)
     qs = _rows16(q, dtype, "q")
     _require_int32(table, lens, q_offsets, group_offsets, shared_lens, dev_status)
