@@ -539,7 +539,7 @@ int w4_w4a16_linear(const uint16_t *x, int M, int K, int N, const uint8_t *q, co
  * ------------------------------------------------------------------------ */
 int w4_w4a16_linear_few(const uint16_t *x, int M, int K, int N, const uint8_t *q,
                         const uint16_t *s, const uint16_t *z, int group, uint16_t *y,
-                        w4_stream_t stream);
+                        int32_t *dev_status, w4_stream_t stream);
 
 /* ==========================================================================
  * Beside the layer: the per-step kernels of the denoising loop

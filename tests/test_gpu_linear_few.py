@@ -59,6 +59,57 @@ def test_linear(lib, M, K, N, group):
 
 
 @gpu
+@pytest.mark.parametrize("M,K,N", [
+    (9, 512, 20000), (16, 640, 19457), (13, 2816, 19584), (17, 512, 40001), (32, 1408, 38912),
+    (25, 2816, 30000), (32, 3200, 19999), (10, 5632, 19456), (31, 5632, 20011), (32, 7168, 19456)])
+def test_many_rows(lib, M, K, N):
+    """From 19456 rows on (on 152 SMs) more than 8 tokens go through the tensor memory, in
+    parts of 32 or 16 as they fit, where they do."""
+    import torch
+    x, q, s, z = _inputs(M, K, N, 128, M + K)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = lib.w4_w4a16_linear_few(x, q, s, z, dev_status=status)
+    _check(y, x, q, s, z, 128)
+    assert torch.equal(lib.w4_w4a16_linear_few(x, q, s, z), y) and int(status) == 0
+
+
+@gpu
+@pytest.mark.parametrize("M", [12, 30])
+def test_many_rows_and_odd_activations(lib, M):
+    """Groups of zeros, one large value among small ones, subnormals, what is not finite,
+    scaling by powers of two, the order of the tokens."""
+    import math
+    import torch
+    x, q, s, z = _inputs(M, 1024, 19500, 128, 3)
+    x[1, 128:256], x[2] = 0.0, 0.0
+    x[3, 5] = 30000.0
+    x[4, 300:400] *= 2.0 ** -12
+    x[5] = x[5] * 2.0 ** -120
+    x[6, 512:640] = 2.0 ** -133
+    want = lib.w4_w4a16_linear_few(x, q, s, z)
+    # what activations lose is below 2^-22 of their group's largest, times 15 + 15 scales
+    ref, S = _reference(x, q, s, z, 128)
+    top = x.double().abs().view(M, 8, 128).amax(-1)
+    loss = 2.0 ** -22 * 128 * 15 * top @ s.double().abs().T
+    tol = 2.0 ** -8 * ref.abs() * (1 + 2.0 ** -8) + 2.0 ** -15 * S + loss + 2.0 ** -133
+    bad = ~((want.double() - ref).abs() <= tol)
+    assert not bool(bad.any()), (bad.sum(1).tolist(), ((want.double() - ref).abs() / tol).amax(1))
+    assert bool((want[2] == 0).all())
+    other = x.clone()
+    other[7, 3], other[8, 1000], other[9] = math.nan, math.inf, 1e30
+    got = lib.w4_w4a16_linear_few(other, q, s, z)
+    same = [t for t in range(M) if t not in (7, 8, 9)]
+    assert torch.equal(got[same], want[same])
+    assert not bool(got[7].isfinite().any()) and not bool(got[8].isfinite().any())
+    order = torch.randperm(M, device="cuda")
+    assert torch.equal(lib.w4_w4a16_linear_few(x[order].contiguous(), q, s, z), want[order])
+    plain = [t for t in range(M) if t not in (5, 6)]
+    for e in (-40, -10, 40):
+        y = lib.w4_w4a16_linear_few(x * 2.0 ** e, q, s, z)
+        assert torch.equal(y[plain], want[plain] * 2.0 ** e)
+
+
+@gpu
 def test_every_row_count(lib):
     """Tasks and units that cross warps in every way."""
     for N in list(range(1, 70)) + [151 * 16, 152 * 16 + 1, 153 * 32 + 5, 304 * 16 + 15]:
@@ -146,7 +197,7 @@ def test_calls_refused():
     at = 0x10000
 
     def linear(x=at, M=1, K=256, N=64, q=at, s=at, z=at, group=128, y=at):
-        return lib.w4_w4a16_linear_few(x, M, K, N, q, s, z, group, y, None)
+        return lib.w4_w4a16_linear_few(x, M, K, N, q, s, z, group, y, None, None)
     for kw, want in [(dict(x=None), 1), (dict(q=None), 1), (dict(s=None), 1), (dict(z=None), 1),
                      (dict(y=None), 1), (dict(M=-1), 1), (dict(K=0), 1), (dict(N=-1), 1),
                      (dict(M=33), 2), (dict(K=192), 2), (dict(K=11392), 2), (dict(group=32), 2),

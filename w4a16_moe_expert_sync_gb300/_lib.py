@@ -112,7 +112,7 @@ def load_library(path: str | None = None):
                                               V, V, V, V, V], I),
             "w4_w4a16_linear_workspace_size": ([I, I, I, I], SZ),
             "w4_w4a16_linear": ([V, I, I, I, V, V, V, I, V, SZ, V, V, V], I),
-            "w4_w4a16_linear_few": ([V, I, I, I, V, V, V, I, V, V], I),
+            "w4_w4a16_linear_few": ([V, I, I, I, V, V, V, I, V, V, V], I),
             "w4_kv_workspace_size": ([I, I], SZ),
             "w4_kv_reserve": ([V, I, I, V, V, I, V, V, I, I, V, V], I),
             "w4_kv_free": ([V, I, I, V, V, I, V, I, V, V], I),
@@ -726,7 +726,7 @@ def w4_w4a16_linear(x, q, s, z, group: int = 128, workspace=None, out=None, dev_
     return out
 
 
-def w4_w4a16_linear_few(x, q, s, z, group: int = 128, out=None, stream=None):
+def w4_w4a16_linear_few(x, q, s, z, group: int = 128, out=None, dev_status=None, stream=None):
     """w4_w4a16_linear for up to 32 rows, in one launch without a workspace: y [M, N]
     bf16 = x [M, K] bf16 . deq(W)^T with W packed as w4_quantize writes it."""
     torch = _torch or _load_torch()
@@ -740,13 +740,15 @@ def w4_w4a16_linear_few(x, q, s, z, group: int = 128, out=None, stream=None):
         raise ValueError("x must be [M, K] bf16, q [N, K / 2] uint8, s and z [N, K / group] fp16")
     if not (x.is_contiguous() and q.is_contiguous() and s.is_contiguous() and z.is_contiguous()):
         raise ValueError("tensors passed to the CUDA library must be contiguous")
-    device = _on_current_device(x, q, s, z, out)
+    _require_int32(dev_status)
+    device = _on_current_device(x, q, s, z, out, dev_status)
     if out is None:
         out = _result((M, N), bf16, x.device, stream)
     elif out.dtype is not bf16 or out.shape != (M, N) or not out.is_contiguous():
         raise ValueError("out must be [M, N] bf16, contiguous")
     _call("w4_w4a16_linear_few", x.data_ptr(), M, K, N, q.data_ptr(), s.data_ptr(), z.data_ptr(),
-          group, out.data_ptr(), _raw_stream(stream, device))
+          group, out.data_ptr(), 0 if dev_status is None else dev_status.data_ptr(),
+          _raw_stream(stream, device))
     return out
 
 

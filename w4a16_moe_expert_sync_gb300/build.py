@@ -14,7 +14,7 @@ LIB = os.path.join(BUILD, "libw4moe.so")
 SOURCES = ["api.cu", "quantize.cu", "route_align.cu", "combine.cu", "grouped_gemm.cu",
            "static_scratch.cu", "rmsnorm.cu", "sampler.cu", "dense_gemm.cu",
            "few.cu", "kv.cu", "attention.cu", "rope.cu",
-           "linear_few.cu", "packed.cu"]
+           "linear_few.cu", "linear_few_wide.cu", "packed.cu"]
 HEADERS = ["launch.h", "ptx.cuh", "korder.cuh", "combine_fold.cuh", "checks.cuh",
            "route_token.cuh", "attention_plan.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1583,7 +1583,7 @@ int w4_w4a16_linear(const uint16_t *x, int M, int K, int N, const uint8_t *q, co
 
 int w4_w4a16_linear_few(const uint16_t *x, int M, int K, int N, const uint8_t *q,
                         const uint16_t *s, const uint16_t *z, int group, uint16_t *y,
-                        w4_stream_t stream)
+                        int32_t *dev_status, w4_stream_t stream)
 {
     if (M < 0 || K <= 0 || N < 0)
         return fail(W4_ERR_INVALID_ARG, "bad sizes M=%d K=%d N=%d", M, K, N);
@@ -1602,6 +1602,17 @@ int w4_w4a16_linear_few(const uint16_t *x, int M, int K, int N, const uint8_t *q
         return fail(W4_ERR_MISALIGNED, "x and q must be 16-byte aligned, y 4-byte, s and z 2-byte aligned");
     if (int rc = check_device())
         return rc;
-    cudaError_t err = w4::launch_few_linear(x, M, K, N, q, s, z, group, y, as_stream(stream));
+    w4::FewLinearProblem l{};
+    l.x = x;
+    l.q = q;
+    l.s = s;
+    l.z = z;
+    l.y = y;
+    l.dev_status = dev_status;
+    l.M = M;
+    l.K = K;
+    l.N = N;
+    l.group = group;
+    cudaError_t err = w4::launch_few_linear(l, as_stream(stream));
     return err == cudaSuccess ? W4_OK : cuda_fail(err, "few-token linear launch");
 }

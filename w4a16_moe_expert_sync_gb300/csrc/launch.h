@@ -159,10 +159,19 @@ bool few_supported(int M, int d, int m, int k);
 size_t few_workspace_bytes(int M, int d, int m, int k);
 cudaError_t launch_few(const FewProblem &p, cudaStream_t stream);
 
-// The dense W4A16 linear for a few tokens (linear_few.cu): M <= 32, K <= 11264.
-cudaError_t launch_few_linear(const uint16_t *x, int M, int K, int N, const uint8_t *q,
-                              const uint16_t *s, const uint16_t *z, int group, uint16_t *y,
-                              cudaStream_t stream);
+// The dense W4A16 linear for a few tokens: M <= 32, K <= 11264 (linear_few.cu); for more
+// than 8 and many rows, if few_linear_wide_tokens is not 0, linear_few_wide.cu.
+struct FewLinearProblem {
+    const uint16_t *x;                  // [M, K] bf16
+    const uint8_t *q;                   // [N, K / 2]
+    const uint16_t *s, *z;              // [N, K / group] fp16
+    uint16_t *y;                        // [M, N] bf16
+    int32_t *dev_status;
+    int M, K, N, group;
+};
+cudaError_t launch_few_linear(const FewLinearProblem &p, cudaStream_t stream);
+int few_linear_wide_tokens(int M, int K, int group);
+cudaError_t launch_few_linear_wide(const FewLinearProblem &p, cudaStream_t stream);
 
 // Pages of a key/value cache (kv.cu).  status may be NULL.
 cudaError_t launch_kv_reserve(int32_t *table, int B, int W, int32_t *lens, int32_t *refs, int P,

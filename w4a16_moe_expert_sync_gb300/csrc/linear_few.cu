@@ -385,6 +385,7 @@ __global__ void __launch_bounds__(32 * NW, 1) few_linear_kernel(const FewLinearA
 }
 
 constexpr int kMaxSmem = 227 * 1024;
+constexpr int kWideRows = 128;             // an SM, from which on linear_few_wide.cu is taken
 
 template <class F> constexpr int smem_of(int blocks, int nt)
 {
@@ -432,9 +433,7 @@ cudaError_t launch_few_linear_group(const FewLinearArgs &a, int sms, int dev, cu
 
 }  // namespace
 
-cudaError_t launch_few_linear(const uint16_t *x, int M, int K, int N, const uint8_t *q,
-                              const uint16_t *s, const uint16_t *z, int group, uint16_t *y,
-                              cudaStream_t stream)
+cudaError_t launch_few_linear(const FewLinearProblem &q, cudaStream_t stream)
 {
     int dev = 0, sms = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -442,18 +441,20 @@ cudaError_t launch_few_linear(const uint16_t *x, int M, int K, int N, const uint
         err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (err != cudaSuccess)
         return err;
+    if (q.N >= kWideRows * sms && few_linear_wide_tokens(q.M, q.K, q.group) > 0)
+        return launch_few_linear_wide(q, stream);
     FewLinearArgs a{};
-    a.x = x;
-    a.q = q;
-    a.s = s;
-    a.z = z;
-    a.y = y;
-    a.M = M;
-    a.K = K;
-    a.N = N;
-    a.blocks = (K + 127) / 128;
-    return group == 128 ? launch_few_linear_group<128>(a, sms, dev, stream)
-                        : launch_few_linear_group<64>(a, sms, dev, stream);
+    a.x = q.x;
+    a.q = q.q;
+    a.s = q.s;
+    a.z = q.z;
+    a.y = q.y;
+    a.M = q.M;
+    a.K = q.K;
+    a.N = q.N;
+    a.blocks = (q.K + 127) / 128;
+    return q.group == 128 ? launch_few_linear_group<128>(a, sms, dev, stream)
+                          : launch_few_linear_group<64>(a, sms, dev, stream);
 }
 
 }  // namespace w4

@@ -1,0 +1,586 @@
+// linear_few_wide.cu -- the W4A16 linear for 9 to 32 tokens and many rows, on tcgen05:
+//   y[t, n] = sum_g s[n, g] (sum_{k in g} q[n, k] x[t, k] - z[n, g] sum_{k in g} x[t, k])
+// for groups of 128.  linear_few.cu is the plain form of it; beyond 8 tokens its warps'
+// MMAs and the unpacking of the codes for them take longer than the weights' way from HBM.
+//
+// A nibble is the e4m3 number q 2^-9, subnormals included, so a word of eight codes is two
+// words of MMA operand for two ANDs and a shift: A, 128 weight rows in tensor memory.  B is
+// the activations as e4m3 pairs x 2^e = P1 + P2 / 32, e for each token and group of 128 such
+// that the largest lies in [2^7, 2^8): 4 bits each, which is all of a bf16 value down to 2^-13
+// of the group's largest; what smaller ones lose is below 2^-22 of the largest.  P1 and P2
+// are columns of one MMA (kind::f8f6f4, M 128, N twice the tokens), each group's sums
+// have accumulators of their own, and a thread, which holds a weight row, adds
+//   s (2^(9 - e) (D1 + D2 / 32) - z sum x)
+// to its 32-bit sums, token by token.
+//
+// A CTA takes 128 rows at a time, its groups in turn by two sets of four warps (a warp per
+// 32 rows): a set unpacks a group into its A, hands it to its MMA warp, and takes the sums of
+// its group before while the tensor cores work.  The sets' sums of a task meet in tensor
+// memory, in a fixed order: bit-identical reruns.  Codes arrive by TMA, kSlots groups ahead.
+#include <algorithm>
+#include <atomic>
+#include <cuda_fp16.h>
+
+#include "../../include/w4moe.h"
+#include "checks.cuh"
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace w4 {
+
+namespace {
+
+constexpr int kRows = 128;                 // of a task
+constexpr int kGroup = 128;
+constexpr int kSlotBytes = kRows * kGroup / 2;
+constexpr int kThreads = 32 * 11;          // two sets of four, two MMA warps, the loader
+constexpr int kMaxSlots = 16;
+constexpr int kMaxSmem = 227 * 1024;
+
+struct WideArgs {
+    CUtensorMap map;                       // codes [N][K / 2] bytes, box 64 x 128
+    const uint16_t *x;                     // [M, K] bf16
+    const uint16_t *s, *z;                 // [N, K / 128] fp16
+    uint16_t *y;                           // [M, N] bf16
+    int32_t *dev_status;
+    uint64_t wait_ns;
+    int withhold;                          // test hook: the first slot never completes
+    int M, K, N, groups, slots;
+};
+
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float low(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float high(uint64_t x)
+{
+    return __uint_as_float(static_cast<uint32_t>(x >> 32));
+}
+
+// Two values in e4m3 (the first in the lower byte), and back.
+__device__ __forceinline__ uint32_t to_e4m3(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 from_e4m3(uint32_t v)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// One group: four steps of 32 codes, A in tensor memory (8 columns a step), by one elected
+// lane; the sums begin anew.
+__device__ __forceinline__ void mma_group(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, f, e;\n\t.reg .b64 y;\n\t.reg .b32 x;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\tsetp.ne.b32 f, 0, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, f;\n\t"
+        "add.s32 x, %1, 8;\n\tadd.s64 y, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [x], y, %3, p;\n\t"
+        "add.s32 x, %1, 16;\n\tadd.s64 y, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [x], y, %3, p;\n\t"
+        "add.s32 x, %1, 24;\n\tadd.s64 y, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [x], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc)
+        : "memory");
+}
+
+// TOK: tokens, 16 or 32.
+template <int TOK> struct Wide {
+    static constexpr int kN = 2 * TOK;
+    static constexpr int kXBytes = kN * kGroup;            // a group's B
+    static constexpr uint32_t kD = 128, kX = kD + 4 * kN;  // TMEM columns; A from 0 on
+    static constexpr uint32_t kIdesc = idesc_f16_f32(128, kN);   // (e4m3: the same bits)
+
+    struct Shared {
+        alignas(8) uint64_t full[kMaxSlots], empty[kMaxSlots];
+        uint64_t a_full[2][2], d_full[2][2], x_full[4], x_empty[4], drained[2];
+        uint32_t tmem;
+        int abort_flag;
+    };
+
+    static __host__ __device__ constexpr int fixed_bytes(int groups)
+    {
+        return 1024 + groups * (kXBytes + 8 * TOK);
+    }
+
+    static __device__ __forceinline__ bool wait(const WideArgs &p, Shared &s, uint64_t *bar,
+                                                uint32_t parity)
+    {
+        return mbar_wait_warp(bar, parity, &s.abort_flag, p.dev_status, kDevPipelineTimeout,
+                              p.wait_ns);
+    }
+
+    // The activations of tokens t0 .. t0 + TOK as B of every group, and for each two tokens
+    // (2^(9 - e), 2^(9 - e), sum x, sum x).  16 lanes have a token's group, 8 values each, in
+    // the order of the unpacked codes (0 2 4 6 1 3 5 7).
+    static __device__ void stage(const WideArgs &p, int t0, uint8_t *xs, float *fs, int warp, int lane)
+    {
+        constexpr int kBatch = 4, kWarps = kThreads / 32 - 1;
+        const int items = p.groups * TOK, sub = lane >> 4, l = lane & 15;
+        for (int i0 = warp * 2 * kBatch; i0 < items; i0 += kWarps * 2 * kBatch) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; u++) {
+                const int i = i0 + 2 * u + sub, tok = i % TOK, t = t0 + tok;
+                v[u] = make_uint4(0, 0, 0, 0);
+                if (i < items && t < p.M)
+                    v[u] = __ldg(reinterpret_cast<const uint4 *>(
+                        p.x + static_cast<int64_t>(t) * p.K + i / TOK * kGroup + l * 8));
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; u++) {
+                const int i = i0 + 2 * u + sub, tok = i % TOK, g = i / TOK;
+                const uint32_t in[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                float f[8], sum = 0.0f;
+                uint32_t top = 0;              // magnitudes compare as integers
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    f[2 * e] = __uint_as_float(in[e] << 16);
+                    f[2 * e + 1] = __uint_as_float(in[e] & 0xFFFF0000u);
+                    top = max(top, max((in[e] << 16) & 0x7FFFFFFFu, in[e] & 0x7FFF0000u));
+                    sum += f[2 * e] + f[2 * e + 1];
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) {
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                }
+                // the largest becomes 2^7 .. 2^8 (below 2^-120 less, for 2^e has to be a number)
+                const int e = min(max(134 - static_cast<int>(top >> 23), -118), 127);
+                const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                uint32_t part[2][4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int a = (j & 1) * 4 + (j >> 1);              // values a and a + 2
+                    const float v0 = f[a] * up, v1 = f[a + 2] * up;
+                    part[0][j] = to_e4m3(v0, v1);
+                    const float2 back = from_e4m3(part[0][j]);
+                    part[1][j] = to_e4m3((v0 - back.x) * 32.0f, (v1 - back.y) * 32.0f);
+                }
+                if (i >= items)
+                    continue;
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const int n = h * TOK + tok;
+                    // j = 0, 2: values 0 2, 1 3; j = 1, 3: 4 6, 5 7
+                    const uint2 out = make_uint2(part[h][0] | part[h][1] << 16,
+                                                 part[h][2] | part[h][3] << 16);
+                    *reinterpret_cast<uint2 *>(xs + g * kXBytes + n * 128 +
+                                               (((l >> 1) ^ (n & 7)) << 4) + (l & 1) * 8) = out;
+                }
+                if (l == 0) {
+                    float *to = fs + (g * (TOK / 2) + (tok >> 1)) * 4 + (tok & 1);
+                    to[0] = __uint_as_float(static_cast<uint32_t>(127 + 9 - e) << 23);
+                    to[2] = sum;
+                }
+            }
+        }
+    }
+
+    static __device__ bool load(const WideArgs &p, Shared &s, uint8_t *ring, int row0, int idx, int lane)
+    {
+        const int slot = idx % p.slots, use = idx / p.slots;
+        if (use > 0 && !wait(p, s, &s.empty[slot], (use - 1) & 1))
+            return false;
+        const int task = idx / p.groups, g = idx - task * p.groups;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&s.full[slot], kSlotBytes);
+            tma_load_2d(ring + slot * kSlotBytes, &p.map, g * (kGroup / 2), row0 + task * kRows,
+                        &s.full[slot], l2_policy_evict_first());
+        }
+        __syncwarp();
+        return true;
+    }
+
+    // Set w's MMAs.
+    static __device__ void issuer(const WideArgs &p, Shared &s, const uint8_t *xs, int w, int total)
+    {
+        const uint32_t tmem = s.tmem;
+        const uint64_t bd = sdesc_sw128(smem_u32(xs));
+        for (int idx = w, i = 0; idx < total; idx += 2, i++) {
+            const int b = i & 1, g = idx % p.groups;
+            if (!wait(p, s, &s.a_full[w][b], i >> 1 & 1))
+                break;
+            tc_fence_after();
+            __syncwarp();
+            mma_group(tmem + kD + kN * (2 * w + b), tmem + 32 * (2 * w + b),
+                      bd + static_cast<uint64_t>(g) * (kXBytes >> 4), kIdesc);
+            tc_commit_elect(&s.d_full[w][b]);
+        }
+        // nothing of this warp's is under way when the CTA ends
+        __syncwarp();
+        tc_commit_elect(&s.drained[w]);
+        mbar_drain(&s.drained[w], 0);
+        __syncwarp();
+    }
+
+    static __device__ __forceinline__ void load_sums(uint32_t taddr, uint32_t (&r)[kN])
+    {
+        if constexpr (TOK == 16)
+            tmem_ld_32x32b_x32(taddr, r);
+        else
+            asm volatile(
+                "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+                "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+                "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+                "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+                "tcgen05.wait::ld.sync.aligned;"
+                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                  "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                  "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+                  "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                  "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+                  "=r"(r[30]), "=r"(r[31]), "=r"(r[kN - 32]), "=r"(r[kN - 31]), "=r"(r[kN - 30]),
+                  "=r"(r[kN - 29]), "=r"(r[kN - 28]), "=r"(r[kN - 27]), "=r"(r[kN - 26]),
+                  "=r"(r[kN - 25]), "=r"(r[kN - 24]), "=r"(r[kN - 23]), "=r"(r[kN - 22]),
+                  "=r"(r[kN - 21]), "=r"(r[kN - 20]), "=r"(r[kN - 19]), "=r"(r[kN - 18]),
+                  "=r"(r[kN - 17]), "=r"(r[kN - 16]), "=r"(r[kN - 15]), "=r"(r[kN - 14]),
+                  "=r"(r[kN - 13]), "=r"(r[kN - 12]), "=r"(r[kN - 11]), "=r"(r[kN - 10]),
+                  "=r"(r[kN - 9]), "=r"(r[kN - 8]), "=r"(r[kN - 7]), "=r"(r[kN - 6]),
+                  "=r"(r[kN - 5]), "=r"(r[kN - 4]), "=r"(r[kN - 3]), "=r"(r[kN - 2]),
+                  "=r"(r[kN - 1])
+                : "r"(taddr)
+                : "memory");
+    }
+
+    // A warp of set w: 32 rows of every second group.
+    static __device__ void worker(const WideArgs &p, Shared &s, const uint8_t *ring, const float *fs,
+                                  int t0, int row0, int w, int quarter, int lane, int total)
+    {
+        const uint32_t tmem = s.tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const int mine = quarter * 32 + lane;
+        uint64_t acc[TOK / 2];
+#pragma unroll
+        for (int i = 0; i < TOK / 2; i++)
+            acc[i] = 0;
+        // scales and zeros of the groups to come, three steps ahead
+        constexpr int kAhead = 3;
+        uint16_t sc[kAhead], ze[kAhead];
+        auto scales = [&](int idx, uint16_t &sv, uint16_t &zv) {
+            const int task = idx / p.groups, g = idx - task * p.groups;
+            const int64_t row = min(row0 + task * kRows + mine, p.N - 1);
+            sv = idx < total ? __ldg(p.s + row * p.groups + g) : static_cast<uint16_t>(0);
+            zv = idx < total ? __ldg(p.z + row * p.groups + g) : static_cast<uint16_t>(0);
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; i++)
+            scales(w + 2 * i, sc[i], ze[i]);
+        int task = w / p.groups, done = 0;         // of the group whose sums come next
+        for (int i = 0, idx = w; idx < total + 2; i++, idx += 2) {
+            if (idx < total) {
+                const int slot = idx % p.slots;
+                if (!wait(p, s, &s.full[slot], idx / p.slots & 1))
+                    return;
+                uint32_t q[16], a[32];
+                const uint8_t *row = ring + slot * kSlotBytes + mine * 64;
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    *reinterpret_cast<uint4 *>(q + 4 * j) =
+                        *reinterpret_cast<const uint4 *>(row + ((j ^ (mine >> 1 & 3)) << 4));
+#pragma unroll
+                for (int j = 0; j < 16; j++) {
+                    a[2 * j] = q[j] & 0x0F0F0F0Fu;
+                    a[2 * j + 1] = q[j] >> 4 & 0x0F0F0F0Fu;
+                }
+                __syncwarp();
+                mbar_arrive_elect(&s.empty[slot]);
+                tmem_st_32x32b_x32(tmem + 32 * (2 * w + (i & 1)), a);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                mbar_arrive_elect(&s.a_full[w][i & 1]);
+            }
+            if (i == 0)
+                continue;
+            // the sums of the step before
+            const int b = (i - 1) & 1, last = idx - 2;
+            if (!wait(p, s, &s.d_full[w][b], (i - 1) >> 1 & 1))
+                return;
+            tc_fence_after();
+            __syncwarp();
+            uint32_t d[kN];
+            load_sums(tmem + kD + kN * (2 * w + b), d);
+            const int g = last - task * p.groups;
+            const float sv = __half2float(__ushort_as_half(sc[0]));
+            const float zv = __half2float(__ushort_as_half(ze[0]));
+#pragma unroll
+            for (int j = 0; j + 1 < kAhead; j++) {
+                sc[j] = sc[j + 1];
+                ze[j] = ze[j + 1];
+            }
+            scales(last + 2 * kAhead, sc[kAhead - 1], ze[kAhead - 1]);
+            const uint64_t s2 = pair_of(sv, sv), z2 = pair_of(-zv, -zv);
+            const uint64_t small = pair_of(0.03125f, 0.03125f);
+            const ulonglong2 *f = reinterpret_cast<const ulonglong2 *>(fs) + g * (TOK / 2);
+#pragma unroll
+            for (int j = 0; j < TOK / 2; j++) {
+                const ulonglong2 fv = f[j];            // two tokens' factors, their sums
+                const uint64_t d1 = static_cast<uint64_t>(d[2 * j + 1]) << 32 | d[2 * j];
+                const uint64_t d2 = static_cast<uint64_t>(d[TOK + 2 * j + 1]) << 32 | d[TOK + 2 * j];
+                acc[j] = fma2(s2, fma2(fv.x, fma2(d2, small, d1), mul2(z2, fv.y)), acc[j]);
+            }
+            if (last + 2 >= (task + 1) * p.groups) {   // the set's last group of the task
+                if (!finish(p, s, t0, row0 + task * kRows + mine, w, quarter, lane, done, tmem, acc))
+                    return;
+                done++;
+                task++;
+#pragma unroll
+                for (int j = 0; j < TOK / 2; j++)
+                    acc[j] = 0;
+            }
+        }
+    }
+
+    // A task's sums: the second set's through tensor memory to the first, which stores them.
+    static __device__ __forceinline__ bool finish(const WideArgs &p, Shared &s, int t0, int row, int w,
+                                                  int quarter, int lane, int done, uint32_t tmem,
+                                                  const uint64_t (&acc)[TOK / 2])
+    {
+        uint32_t v[TOK];
+        if (w == 1) {
+            if (done > 0 && !wait(p, s, &s.x_empty[quarter], (done - 1) & 1))
+                return false;
+            tc_fence_after();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < TOK / 2; j++) {
+                v[2 * j] = static_cast<uint32_t>(acc[j]);
+                v[2 * j + 1] = static_cast<uint32_t>(acc[j] >> 32);
+            }
+            if constexpr (TOK == 16)
+                tmem_st_32x32b_x16(tmem + kX, v);
+            else
+                tmem_st_32x32b_x32(tmem + kX, v);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_elect(&s.x_full[quarter]);
+            return true;
+        }
+        if (!wait(p, s, &s.x_full[quarter], done & 1))
+            return false;
+        tc_fence_after();
+        __syncwarp();
+        if constexpr (TOK == 16)
+            tmem_ld_32x32b_x16(tmem + kX, v);
+        else
+            tmem_ld_32x32b_x32(tmem + kX, v);
+        tc_fence_before();
+        __syncwarp();
+        mbar_arrive_elect(&s.x_empty[quarter]);
+#pragma unroll
+        for (int j = 0; j < TOK / 2; j++) {
+            const uint32_t r = bf16_pair(low(acc[j]) + __uint_as_float(v[2 * j]),
+                                         high(acc[j]) + __uint_as_float(v[2 * j + 1]));
+            const int t = t0 + 2 * j;
+            uint16_t *y = p.y + static_cast<int64_t>(t) * p.N + row;
+            if (row < p.N && t < p.M)
+                y[0] = static_cast<uint16_t>(r);
+            if (row < p.N && t + 1 < p.M)
+                y[p.N] = static_cast<uint16_t>(r >> 16);
+        }
+        __syncwarp();
+        return true;
+    }
+};
+
+// CTA (share, part): its share of the tasks, for the part's TOK tokens.
+template <int TOK>
+__global__ void __launch_bounds__(kThreads, 1)
+    few_linear_wide_kernel(const __grid_constant__ WideArgs p, int parts)
+{
+    using W = Wide<TOK>;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    __shared__ __align__(16) typename W::Shared s;
+    uint8_t *ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    uint8_t *xs = ring + p.slots * kSlotBytes;
+    float *fs = reinterpret_cast<float *>(xs + p.groups * W::kXBytes);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int share = blockIdx.x / parts, shares = gridDim.x / parts;
+    const int t0 = (blockIdx.x - share * parts) * TOK;
+    const int tasks = (p.N + kRows - 1) / kRows;
+    const int first = static_cast<int>(static_cast<int64_t>(tasks) * share / shares);
+    const int end = static_cast<int>(static_cast<int64_t>(tasks) * (share + 1) / shares);
+    const int row0 = first * kRows, total = (end - first) * p.groups;
+    if (tid == 0) {
+        for (int i = 0; i < p.slots; i++) {
+            mbar_init(&s.full[i], p.withhold && i == 0 ? 2 : 1);
+            mbar_init(&s.empty[i], 4);
+        }
+        for (int i = 0; i < 2; i++) {
+            for (int j = 0; j < 2; j++) {
+                mbar_init(&s.a_full[i][j], 4);
+                mbar_init(&s.d_full[i][j], 1);
+            }
+            mbar_init(&s.drained[i], 1);
+        }
+        for (int i = 0; i < 4; i++) {
+            mbar_init(&s.x_full[i], 1);
+            mbar_init(&s.x_empty[i], 1);
+        }
+        s.abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&p.map);
+    }
+    if (warp == 10) {
+        tmem_alloc(&s.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();
+    pdl_trigger();
+    const int ahead = min(p.slots, total);
+    if (warp == 10) {
+        for (int i = 0; i < ahead; i++)
+            W::load(p, s, ring, row0, i, lane);
+    } else {
+        W::stage(p, t0, xs, fs, warp, lane);
+        fence_proxy_async_smem();
+    }
+    __syncthreads();
+    if (warp < 8) {
+        W::worker(p, s, ring, fs, t0, row0, warp >> 2, warp & 3, lane, total);
+    } else if (warp < 10) {
+        W::issuer(p, s, xs, warp - 8, total);
+    } else {
+        int i = ahead;
+        while (i < total && W::load(p, s, ring, row0, i, lane))
+            i++;
+        // every copy requested has landed, or had its time to: of a slot only the last can be
+        // under way
+        for (int slot = 0; slot < min(i, p.slots); slot++)
+            mbar_drain(&s.full[slot], (i - 1 - slot) / p.slots & 1);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 10) {
+        tc_fence_after();
+        __syncwarp();
+        tmem_dealloc(s.tmem, 512);
+    }
+}
+
+using EncodeFn = decltype(&cuTensorMapEncodeTiled);
+
+EncodeFn encode_fn()
+{
+    static EncodeFn fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                             cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<EncodeFn>(ptr);
+    }();
+    return fn;
+}
+
+// Slots that fit beside the activations: even, so that a slot is always the same set's.
+int slots_of(int groups, int tok)
+{
+    const int fixed = tok == 16 ? Wide<16>::fixed_bytes(groups) : Wide<32>::fixed_bytes(groups);
+    return std::min((kMaxSmem - 2048 - fixed) / kSlotBytes / 2 * 2, kMaxSlots);
+}
+
+template <int TOK>
+cudaError_t launch_as(WideArgs &a, int sms, int dev, cudaStream_t stream)
+{
+    auto kern = few_linear_wide_kernel<TOK>;
+    static std::atomic<uint64_t> raised{0};      // devices whose limit is raised already
+    if (!(raised.load(std::memory_order_relaxed) >> (dev & 63) & 1u)) {
+        cudaError_t err =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 2048);
+        if (err != cudaSuccess)
+            return err;
+        raised.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+    }
+    a.slots = slots_of(a.groups, TOK);
+    const int parts = (a.M + TOK - 1) / TOK, tasks = (a.N + kRows - 1) / kRows;
+    const int shares = std::min(tasks, std::max(sms / parts, 1));
+    const int smem = Wide<TOK>::fixed_bytes(a.groups) + a.slots * kSlotBytes;
+    return launch_pdl(kern, dim3(shares * parts), dim3(kThreads), smem, stream, a, parts);
+}
+
+}  // namespace
+
+// The tokens of a CTA, 32 or 16; 0: the shape is not for this kernel.
+int few_linear_wide_tokens(int M, int K, int group)
+{
+    constexpr int kLeast = 4;                  // slots, and groups
+    if (group != kGroup || K < kLeast * kGroup || M <= 8)
+        return 0;
+    const int groups = K / kGroup;
+    if (M > 16 && slots_of(groups, 32) >= kLeast)
+        return 32;
+    return slots_of(groups, 16) >= kLeast ? 16 : 0;
+}
+
+cudaError_t launch_few_linear_wide(const FewLinearProblem &q, cudaStream_t stream)
+{
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess)
+        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess)
+        return err;
+    if (!encode_fn())
+        return cudaErrorNotSupported;
+    WideArgs a{};
+    const cuuint64_t dim[2] = {static_cast<cuuint64_t>(q.K / 2), static_cast<cuuint64_t>(q.N)};
+    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(q.K / 2)};
+    const cuuint32_t box[2] = {kGroup / 2, kRows}, step[2] = {1, 1};
+    if (encode_fn()(&a.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(q.q), dim, stride,
+                    box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    a.x = q.x;
+    a.s = q.s;
+    a.z = q.z;
+    a.y = q.y;
+    a.dev_status = q.dev_status;
+    a.wait_ns = pipeline_test_hooks().wait_ns;
+    a.withhold = pipeline_test_hooks().withhold_sz;
+    a.M = q.M;
+    a.K = q.K;
+    a.N = q.N;
+    a.groups = q.K / kGroup;
+    return few_linear_wide_tokens(q.M, q.K, kGroup) == 32 ? launch_as<32>(a, sms, dev, stream)
+                                                         : launch_as<16>(a, sms, dev, stream);
+}
+
+}  // namespace w4
