@@ -13,10 +13,10 @@
 //   s (2^(9 - e) (D1 + D2 / 32) - z sum x)
 // to its 32-bit sums, token by token.
 //
-// A CTA takes 128 rows at a time, its groups in turn by two sets of four warps (a warp per
-// 32 rows): a set unpacks a group into its A, hands it to its MMA warp, and takes the sums of
-// its group before while the tensor cores work.  The sets' sums of a task meet in tensor
-// memory, in a fixed order: bit-identical reruns.  Codes arrive by TMA, kSlots groups ahead.
+// A CTA takes 128 rows at a time, its groups in turn by two sets of warps: four that unpack (a
+// warp per 32 rows), one that issues the MMAs, four that add the sums up.  The sets' sums of a
+// task meet in tensor memory, in a fixed order: bit-identical reruns.  Codes arrive by TMA, up
+// to 16 groups ahead.
 #include <algorithm>
 #include <atomic>
 #include <cuda_fp16.h>
@@ -33,7 +33,9 @@ namespace {
 constexpr int kRows = 128;                 // of a task
 constexpr int kGroup = 128;
 constexpr int kSlotBytes = kRows * kGroup / 2;
-constexpr int kThreads = 32 * 11;          // two sets of four, two MMA warps, the loader
+// first warps of the roles behind the eight that unpack
+constexpr int kAdd = 8, kIssue = 16, kLoad = 18;
+constexpr int kThreads = 32 * 19;
 constexpr int kMaxSlots = 16;
 constexpr int kMaxSmem = 227 * 1024;
 
@@ -121,7 +123,7 @@ template <int TOK> struct Wide {
 
     struct Shared {
         alignas(8) uint64_t full[kMaxSlots], empty[kMaxSlots];
-        uint64_t a_full[2][2], d_full[2][2], x_full[4], x_empty[4], drained[2];
+        uint64_t a_full[2][2], d_full[2][2], d_empty[2][2], x_full[4], x_empty[4], drained[2];
         uint32_t tmem;
         int abort_flag;
     };
@@ -143,7 +145,7 @@ template <int TOK> struct Wide {
     // the order of the unpacked codes (0 2 4 6 1 3 5 7).
     static __device__ void stage(const WideArgs &p, int t0, uint8_t *xs, float *fs, int warp, int lane)
     {
-        constexpr int kBatch = 4, kWarps = kThreads / 32 - 1;
+        constexpr int kBatch = 4, kWarps = kLoad;
         const int items = p.groups * TOK, sub = lane >> 4, l = lane & 15;
         for (int i0 = warp * 2 * kBatch; i0 < items; i0 += kWarps * 2 * kBatch) {
             uint4 v[kBatch];
@@ -205,19 +207,41 @@ template <int TOK> struct Wide {
         }
     }
 
-    static __device__ bool load(const WideArgs &p, Shared &s, uint8_t *ring, int row0, int idx, int lane)
-    {
-        const int slot = idx % p.slots, use = idx / p.slots;
-        if (use > 0 && !wait(p, s, &s.empty[slot], (use - 1) & 1))
-            return false;
-        const int task = idx / p.groups, g = idx - task * p.groups;
-        if (lane == 0) {
-            mbar_arrive_expect_tx(&s.full[slot], kSlotBytes);
-            tma_load_2d(ring + slot * kSlotBytes, &p.map, g * (kGroup / 2), row0 + task * kRows,
-                        &s.full[slot], l2_policy_evict_first());
+    // A role's place: its next group, its slot and how often the slots have been gone through
+    // (counters: with divisions each role's step took some hundred cycles longer).
+    struct Place {
+        int task, g, slot, phase;
+        __device__ __forceinline__ void next(const WideArgs &p, int by)
+        {
+            g += by;
+            if (g >= p.groups) {
+                g -= p.groups;
+                task++;
+            }
+            slot += by;
+            if (slot >= p.slots) {
+                slot -= p.slots;
+                phase ^= 1;
+            }
         }
-        __syncwarp();
-        return true;
+    };
+
+    // The groups' codes in turn; returns how many were requested.
+    static __device__ int load(const WideArgs &p, Shared &s, uint8_t *ring, int row0, int lane, Place &at,
+                               int from, int to)
+    {
+        const uint64_t policy = l2_policy_evict_first();
+        for (int i = from; i < to; i++, at.next(p, 1)) {
+            if (i >= p.slots && !wait(p, s, &s.empty[at.slot], at.phase ^ 1))
+                return i;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&s.full[at.slot], kSlotBytes);
+                tma_load_2d(ring + at.slot * kSlotBytes, &p.map, at.g * (kGroup / 2),
+                            row0 + at.task * kRows, &s.full[at.slot], policy);
+            }
+            __syncwarp();
+        }
+        return to;
     }
 
     // Set w's MMAs.
@@ -225,9 +249,11 @@ template <int TOK> struct Wide {
     {
         const uint32_t tmem = s.tmem;
         const uint64_t bd = sdesc_sw128(smem_u32(xs));
-        for (int idx = w, i = 0; idx < total; idx += 2, i++) {
-            const int b = i & 1, g = idx % p.groups;
-            if (!wait(p, s, &s.a_full[w][b], i >> 1 & 1))
+        Place at{0, w, w, 0};
+        for (int idx = w, i = 0; idx < total; idx += 2, i++, at.next(p, 2)) {
+            const int b = i & 1, g = at.g;
+            if (!wait(p, s, &s.a_full[w][b], i >> 1 & 1) ||
+                (i > 1 && !wait(p, s, &s.d_empty[w][b], (i - 2) >> 1 & 1)))
                 break;
             tc_fence_after();
             __syncwarp();
@@ -242,39 +268,68 @@ template <int TOK> struct Wide {
         __syncwarp();
     }
 
-    static __device__ __forceinline__ void load_sums(uint32_t taddr, uint32_t (&r)[kN])
+    // 16 columns from t0 and 16 from t1 of this thread's lane.
+    static __device__ __forceinline__ void load_sums(uint32_t t0, uint32_t t1, uint32_t (&a)[16],
+                                                     uint32_t (&b)[16])
     {
-        if constexpr (TOK == 16)
-            tmem_ld_32x32b_x32(taddr, r);
-        else
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
-                "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-                "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-                "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
-                "tcgen05.wait::ld.sync.aligned;"
-                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                  "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-                  "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-                  "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-                  "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
-                  "=r"(r[30]), "=r"(r[31]), "=r"(r[kN - 32]), "=r"(r[kN - 31]), "=r"(r[kN - 30]),
-                  "=r"(r[kN - 29]), "=r"(r[kN - 28]), "=r"(r[kN - 27]), "=r"(r[kN - 26]),
-                  "=r"(r[kN - 25]), "=r"(r[kN - 24]), "=r"(r[kN - 23]), "=r"(r[kN - 22]),
-                  "=r"(r[kN - 21]), "=r"(r[kN - 20]), "=r"(r[kN - 19]), "=r"(r[kN - 18]),
-                  "=r"(r[kN - 17]), "=r"(r[kN - 16]), "=r"(r[kN - 15]), "=r"(r[kN - 14]),
-                  "=r"(r[kN - 13]), "=r"(r[kN - 12]), "=r"(r[kN - 11]), "=r"(r[kN - 10]),
-                  "=r"(r[kN - 9]), "=r"(r[kN - 8]), "=r"(r[kN - 7]), "=r"(r[kN - 6]),
-                  "=r"(r[kN - 5]), "=r"(r[kN - 4]), "=r"(r[kN - 3]), "=r"(r[kN - 2]),
-                  "=r"(r[kN - 1])
-                : "r"(taddr)
-                : "memory");
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+            "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+            "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
+            "tcgen05.wait::ld.sync.aligned;"
+            : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]),
+              "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]),
+              "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]),
+              "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]), "=r"(b[10]),
+              "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
+            : "r"(t0), "r"(t1)
+            : "memory");
     }
 
-    // A warp of set w: 32 rows of every second group.
-    static __device__ void worker(const WideArgs &p, Shared &s, const uint8_t *ring, const float *fs,
-                                  int t0, int row0, int w, int quarter, int lane, int total)
+    // A warp that unpacks 32 rows of set w's groups.
+    static __device__ void unpack(const WideArgs &p, Shared &s, const uint8_t *ring, int w, int quarter,
+                                  int lane, int total)
+    {
+        const uint32_t tmem = s.tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const int mine = quarter * 32 + lane;
+        Place at{0, w, w, 0};
+        for (int idx = w, i = 0; idx < total; idx += 2, i++, at.next(p, 2)) {
+            const int slot = at.slot, b = i & 1;
+            if (!wait(p, s, &s.full[slot], at.phase))
+                return;
+            uint32_t q[16], a[32];
+            const uint8_t *row = ring + slot * kSlotBytes + mine * 64;
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                *reinterpret_cast<uint4 *>(q + 4 * j) =
+                    *reinterpret_cast<const uint4 *>(row + ((j ^ (mine >> 1 & 3)) << 4));
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+                a[2 * j] = q[j] & 0x0F0F0F0Fu;
+                a[2 * j + 1] = q[j] >> 4 & 0x0F0F0F0Fu;
+            }
+            // these reads come before the copy that overwrites the slot, which is another proxy's:
+            // without the fence some rows were the next codes in a call of fifty
+            fence_proxy_async_smem();
+            __syncwarp();
+            mbar_arrive_elect(&s.empty[slot]);
+            // the MMAs that read this A last are done when their sums are there
+            if (i > 1 && !wait(p, s, &s.d_full[w][b], (i - 2) >> 1 & 1))
+                return;
+            tc_fence_after();
+            __syncwarp();
+            tmem_st_32x32b_x32(tmem + 32 * (2 * w + b), a);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_elect(&s.a_full[w][b]);
+        }
+    }
+
+    // A warp that adds up 32 rows of set w's groups.
+    static __device__ void add(const WideArgs &p, Shared &s, const float *fs, int t0, int row0, int w,
+                               int quarter, int lane, int total)
     {
         const uint32_t tmem = s.tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const int mine = quarter * 32 + lane;
@@ -282,77 +337,59 @@ template <int TOK> struct Wide {
 #pragma unroll
         for (int i = 0; i < TOK / 2; i++)
             acc[i] = 0;
-        // scales and zeros of the groups to come, three steps ahead
-        constexpr int kAhead = 3;
+        // scales and zeros of the groups to come, four steps ahead
+        constexpr int kAhead = 4;
         uint16_t sc[kAhead], ze[kAhead];
+        Place to{0, w, w, 0}, at = to;
         auto scales = [&](int idx, uint16_t &sv, uint16_t &zv) {
-            const int task = idx / p.groups, g = idx - task * p.groups;
-            const int64_t row = min(row0 + task * kRows + mine, p.N - 1);
-            sv = idx < total ? __ldg(p.s + row * p.groups + g) : static_cast<uint16_t>(0);
-            zv = idx < total ? __ldg(p.z + row * p.groups + g) : static_cast<uint16_t>(0);
+            const int64_t row = min(row0 + to.task * kRows + mine, p.N - 1);
+            sv = idx < total ? __ldg(p.s + row * p.groups + to.g) : static_cast<uint16_t>(0);
+            zv = idx < total ? __ldg(p.z + row * p.groups + to.g) : static_cast<uint16_t>(0);
+            to.next(p, 2);
         };
 #pragma unroll
         for (int i = 0; i < kAhead; i++)
             scales(w + 2 * i, sc[i], ze[i]);
-        int task = w / p.groups, done = 0;         // of the group whose sums come next
-        for (int i = 0, idx = w; idx < total + 2; i++, idx += 2) {
-            if (idx < total) {
-                const int slot = idx % p.slots;
-                if (!wait(p, s, &s.full[slot], idx / p.slots & 1))
-                    return;
-                uint32_t q[16], a[32];
-                const uint8_t *row = ring + slot * kSlotBytes + mine * 64;
+        for (int idx0 = w, i0 = 0; idx0 < total; idx0 += 2 * kAhead, i0 += kAhead)
 #pragma unroll
-                for (int j = 0; j < 4; j++)
-                    *reinterpret_cast<uint4 *>(q + 4 * j) =
-                        *reinterpret_cast<const uint4 *>(row + ((j ^ (mine >> 1 & 3)) << 4));
-#pragma unroll
-                for (int j = 0; j < 16; j++) {
-                    a[2 * j] = q[j] & 0x0F0F0F0Fu;
-                    a[2 * j + 1] = q[j] >> 4 & 0x0F0F0F0Fu;
-                }
-                __syncwarp();
-                mbar_arrive_elect(&s.empty[slot]);
-                tmem_st_32x32b_x32(tmem + 32 * (2 * w + (i & 1)), a);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                mbar_arrive_elect(&s.a_full[w][i & 1]);
-            }
-            if (i == 0)
-                continue;
-            // the sums of the step before
-            const int b = (i - 1) & 1, last = idx - 2;
-            if (!wait(p, s, &s.d_full[w][b], (i - 1) >> 1 & 1))
-                return;
-            tc_fence_after();
-            __syncwarp();
-            uint32_t d[kN];
-            load_sums(tmem + kD + kN * (2 * w + b), d);
-            const int g = last - task * p.groups;
-            const float sv = __half2float(__ushort_as_half(sc[0]));
-            const float zv = __half2float(__ushort_as_half(ze[0]));
-#pragma unroll
-            for (int j = 0; j + 1 < kAhead; j++) {
-                sc[j] = sc[j + 1];
-                ze[j] = ze[j + 1];
-            }
-            scales(last + 2 * kAhead, sc[kAhead - 1], ze[kAhead - 1]);
+        for (int u = 0; u < kAhead; u++) {
+            const int idx = idx0 + 2 * u, i = i0 + u;
+            if (idx >= total)
+                break;
+            const int b = i & 1, g = at.g, task = at.task;
+            const float sv = __half2float(__ushort_as_half(sc[u]));
+            const float zv = __half2float(__ushort_as_half(ze[u]));
+            scales(idx + 2 * kAhead, sc[u], ze[u]);
             const uint64_t s2 = pair_of(sv, sv), z2 = pair_of(-zv, -zv);
             const uint64_t small = pair_of(0.03125f, 0.03125f);
             const ulonglong2 *f = reinterpret_cast<const ulonglong2 *>(fs) + g * (TOK / 2);
+            if (!wait(p, s, &s.d_full[w][b], i >> 1 & 1))
+                return;
+            tc_fence_after();
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < TOK / 2; j++) {
-                const ulonglong2 fv = f[j];            // two tokens' factors, their sums
-                const uint64_t d1 = static_cast<uint64_t>(d[2 * j + 1]) << 32 | d[2 * j];
-                const uint64_t d2 = static_cast<uint64_t>(d[TOK + 2 * j + 1]) << 32 | d[TOK + 2 * j];
-                acc[j] = fma2(s2, fma2(fv.x, fma2(d2, small, d1), mul2(z2, fv.y)), acc[j]);
+            for (int c = 0; c < TOK; c += 16) {
+                uint32_t d1[16], d2[16];
+                const uint32_t at = tmem + kD + kN * (2 * w + b) + c;
+                load_sums(at, at + TOK, d1, d2);
+                if (c + 16 == TOK) {
+                    tc_fence_before();
+                    __syncwarp();
+                    mbar_arrive_elect(&s.d_empty[w][b]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const ulonglong2 fv = f[c / 2 + j];    // two tokens' factors, their sums
+                    const uint64_t e1 = static_cast<uint64_t>(d1[2 * j + 1]) << 32 | d1[2 * j];
+                    const uint64_t e2 = static_cast<uint64_t>(d2[2 * j + 1]) << 32 | d2[2 * j];
+                    acc[c / 2 + j] = fma2(s2, fma2(fv.x, fma2(e2, small, e1), mul2(z2, fv.y)),
+                                          acc[c / 2 + j]);
+                }
             }
-            if (last + 2 >= (task + 1) * p.groups) {   // the set's last group of the task
-                if (!finish(p, s, t0, row0 + task * kRows + mine, w, quarter, lane, done, tmem, acc))
+            at.next(p, 2);
+            if (at.task != task) {                         // that was the set's last of the task
+                if (!finish(p, s, t0, row0 + task * kRows + mine, w, quarter, task, tmem, acc))
                     return;
-                done++;
-                task++;
 #pragma unroll
                 for (int j = 0; j < TOK / 2; j++)
                     acc[j] = 0;
@@ -362,7 +399,7 @@ template <int TOK> struct Wide {
 
     // A task's sums: the second set's through tensor memory to the first, which stores them.
     static __device__ __forceinline__ bool finish(const WideArgs &p, Shared &s, int t0, int row, int w,
-                                                  int quarter, int lane, int done, uint32_t tmem,
+                                                  int quarter, int done, uint32_t tmem,
                                                   const uint64_t (&acc)[TOK / 2])
     {
         uint32_t v[TOK];
@@ -441,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 2; j++) {
                 mbar_init(&s.a_full[i][j], 4);
                 mbar_init(&s.d_full[i][j], 1);
+                mbar_init(&s.d_empty[i][j], 4);
             }
             mbar_init(&s.drained[i], 1);
         }
@@ -452,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
         prefetch_tmap(&p.map);
     }
-    if (warp == 10) {
+    if (warp == kLoad) {
         tmem_alloc(&s.tmem, 512);
         tmem_relinquish();
     }
@@ -462,22 +500,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     pdl_trigger();
     const int ahead = min(p.slots, total);
-    if (warp == 10) {
-        for (int i = 0; i < ahead; i++)
-            W::load(p, s, ring, row0, i, lane);
+    typename W::Place place{0, 0, 0, 0};
+    if (warp == kLoad) {
+        W::load(p, s, ring, row0, lane, place, 0, ahead);
     } else {
         W::stage(p, t0, xs, fs, warp, lane);
         fence_proxy_async_smem();
     }
     __syncthreads();
-    if (warp < 8) {
-        W::worker(p, s, ring, fs, t0, row0, warp >> 2, warp & 3, lane, total);
-    } else if (warp < 10) {
-        W::issuer(p, s, xs, warp - 8, total);
+    if (warp < kAdd) {
+        W::unpack(p, s, ring, warp >> 2, warp & 3, lane, total);
+    } else if (warp < kIssue) {
+        W::add(p, s, fs, t0, row0, (warp - kAdd) >> 2, warp & 3, lane, total);
+    } else if (warp < kLoad) {
+        W::issuer(p, s, xs, warp - kIssue, total);
     } else {
-        int i = ahead;
-        while (i < total && W::load(p, s, ring, row0, i, lane))
-            i++;
+        const int i = W::load(p, s, ring, row0, lane, place, ahead, total);
         // every copy requested has landed, or had its time to: of a slot only the last can be
         // under way
         for (int slot = 0; slot < min(i, p.slots); slot++)
@@ -486,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 10) {
+    if (warp == kLoad) {
         tc_fence_after();
         __syncwarp();
         tmem_dealloc(s.tmem, 512);
