@@ -529,9 +529,10 @@ int w4_w4a16_linear(const uint16_t *x, int M, int K, int N, const uint8_t *q, co
  *   x          [M, K] bf16 in
  *   q          [N, K/2] uint8, w4_quantize's layout; s, z [N, K/group] fp16
  *   y          [M, N] bf16 out
- * Codes and activations enter the tensor cores exactly; a group's scale and zero are
- * applied to its fp32 sum, and y is rounded once.  (Activations of 2^57 and more, or
- * not finite, make their token's results so.)  A token's results depend on neither the
+ * Codes enter the tensor cores exactly, and so do activations (with more than 8 tokens,
+ * 256 rows an SM and groups of 128: but for 2^-22 of their group's largest); a group's scale
+ * and zero are applied to its fp32 sum, and y is rounded once.  (Activations of 2^57 and
+ * more, or not finite, make their token's results so.)  dev_status may be NULL.  A token's results depend on neither the
  * other tokens' values nor where it stands among as many; bit-identical reruns.
  * Requires M <= 32, group 64 or 128 dividing K, K up to 11,264, N * K below 2^33,
  * N below 2^30, x and q 16-byte aligned, y 4-byte, s and z 2-byte aligned.  M = 0 or N = 0
@@ -856,6 +857,7 @@ int w4_attn_tree(const uint16_t *q, int64_t q_tok_stride, int64_t q_head_stride,
  * w4_test_pipeline_hooks -- a test hook of the kernels with pipelines (not for
  * production use): for later w4_grouped_gemm_gate_up / _down / _down_combine
  * calls, the layer's GEMMs, w4_attn_shared_prefix, w4_attn_tree, w4_moe_layer_few*,
+ * w4_w4a16_linear_few (for many rows),
  * w4_kv_copy_pages and w4_kv_compact called from the calling thread, every
  * pipeline wait gives up after wait_limit_ns (0: back to the default of one
  * second) and, if withhold_first_scales is nonzero, each CTA withholds the copy

@@ -230,6 +230,57 @@ def test_more_queries_than_max_q_are_flagged(lib):
     assert int(status) == w4.W4_DEV_BAD_SLOT
 
 
+@gpu
+@pytest.mark.parametrize("befores,nodes,Hq,Hkv,D,page", [
+    ([5000, 300], [90, 40], 12, 2, 64, 16),                     # pairs, three S in turn
+    ([700] * 6, [9] * 6, 4, 2, 64, 64),                         # single items
+    ([3000], [70], 16, 4, 128, 16)])
+def test_waits_that_give_up(lib, befores, nodes, Hq, Hkv, D, page):
+    """The first keys never land: the status says so, and the context goes on."""
+    import time
+    import torch
+    r = random.Random(4)
+    c = _build([a + n for a, n in zip(befores, nodes)], nodes, [], [], Hq, Hkv, D, page, "bfloat16")
+    tree = _words([b for n in nodes for b in _random_tree(r, n)], 3)
+    want, hooks = _run(lib, c, tree), lib.load_library().w4_test_pipeline_hooks
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    t = time.monotonic()
+    try:
+        hooks(2_000_000, 1)
+        _run(lib, c, tree, dev_status=status)
+        torch.cuda.synchronize()
+    finally:
+        hooks(0, 0)
+    assert int(status) & w4.W4_DEV_PIPELINE_TIMEOUT and time.monotonic() - t < 30
+    status.zero_()
+    for _ in range(3):
+        assert torch.equal(_run(lib, c, tree, dev_status=status), want)
+    assert int(status) == 0
+
+
+@gpu
+@pytest.mark.parametrize("D,page", [(64, 16), (64, 128), (128, 32)])
+def test_long_sequences_and_many_calls(lib, D, page):
+    """Items that are cut for many CTAs, several pieces a CTA, pages that are none, the same
+    bits every time."""
+    import torch
+    r = random.Random(7)
+    befores, nodes = [20000, 9000, 1, 130], [64, 100, 128, 3]
+    c = _build([a + n for a, n in zip(befores, nodes)], nodes, [], [], 12, 2, D, page, "float16",
+               poison=False, seed=3)
+    bits = [b for n in nodes for b in _random_tree(r, n)]
+    tree = _words(bits, 4)
+    want = _run(lib, c, tree)
+    _check(want, c, bits)
+    assert all(torch.equal(_run(lib, c, tree), want) for _ in range(60))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c["table"][3, 0] = 10 ** 6
+    got = _run(lib, c, tree, dev_status=status)
+    assert int(status) == w4.W4_DEV_BAD_PAGE
+    assert torch.equal(got[:292], want[:292])
+
+
 def test_calls_refused():
     lib = w4.load_library()
     at = 0x10000

@@ -20,6 +20,13 @@
 // memory.  A lane copies the codes that it will use itself into its own ring in shared
 // memory, S units ahead, and waits for nobody else's.  Sums run in a fixed order:
 // bit-identical reruns.
+//
+// Measured on GB300 from a graph: 1 token, 2816 -> 4096: 4.4 us (latency: launch, the
+// activations' way to shared memory, one round of copies, the warps' sums; 0.9 for the
+// bytes); 11 tokens, 704 -> 2815, groups of 64: 3.2; 8 tokens, 2816 -> 262144: 74 (60 at the
+// copy bandwidth).  With 16 tokens there it is 85, the MMAs (2 cycles each an SM) and the
+// unpacking at some 45 % of their rates each; codes requested into registers instead of the
+// ring: 87 and 101, and 7 for the small ones.
 #include <algorithm>
 #include <atomic>
 #include <cuda_fp16.h>
@@ -385,7 +392,10 @@ __global__ void __launch_bounds__(32 * NW, 1) few_linear_kernel(const FewLinearA
 }
 
 constexpr int kMaxSmem = 227 * 1024;
-constexpr int kWideRows = 128;             // an SM, from which on linear_few_wide.cu is taken
+// Rows an SM from which on linear_few_wide.cu is taken for more than 8 tokens: two tasks of
+// 128.  (Here and there, groups of 128, us: K 2816, 16 tokens: 19456 rows 11.6 and 12.6, 38912
+// 18.1 and 17.4, 116736 42 and 36; 32 tokens 16.7 and 18.1, 28.1 and 24.7, 73.5 and 51.7.)
+constexpr int kWideRows = 256;
 
 template <class F> constexpr int smem_of(int blocks, int nt)
 {
