@@ -108,10 +108,11 @@ def test_results_belong_to_the_stream(lib, monkeypatch, name):
 
 @pytest.mark.parametrize("name", ["linear", "rope", "append", "tree", "keep"])
 def test_another_current_device_is_refused(lib, monkeypatch, name):
-    import torch
+    from w4a16_moe_expert_sync_gb300 import _lib
     d = _setup()
     call = _calls(lib, d)[name]
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    call()
+    monkeypatch.setattr(_lib, "_current_device", lambda: 1)
     with pytest.raises(ValueError):
         call()
 

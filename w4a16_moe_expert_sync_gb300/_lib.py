@@ -22,8 +22,10 @@ _torch = None
 
 def _load_torch():
     """torch, for the calls where an import statement's half microsecond counts."""
-    global _torch
+    global _torch, _current_device, _raw_current_stream
     import torch
+    _current_device = torch._C._cuda_getDevice
+    _raw_current_stream = torch._C._cuda_getCurrentRawStream
     _torch = torch
     return torch
 
@@ -161,10 +163,11 @@ _packed_calls: dict = {}
 
 def _call(name: str, *args):
     """Calls one of _PACKED, NULL pointers as 0, and checks its status."""
-    if _lib is None:
+    call = _packed_calls.get(name)
+    if call is None:
         load_library()
-    fn, pack = _packed_calls[name]
-    rc = fn(pack(*args))
+        call = _packed_calls[name]
+    rc = call[0](call[1](*args))
     if rc:
         _check(rc, name)
 
@@ -234,32 +237,52 @@ def _require(specs):
             raise ValueError(f"{name} must be {list(shape)} {dtype}, not {list(t.shape)} {t.dtype}")
 
 
-def _on_current_device(*ts):
+def _current_device():
+    """The current device (torch's own function once torch is loaded)."""
+    _load_torch()
+    return _current_device()
+
+
+def _raw_current_stream(device):
+    _load_torch()
+    return _raw_current_stream(device)
+
+
+def _wrong_device(*ts):
     """The kernels run on the current device: tensors of another one, or of none, are
-    refused.  Returns the device."""
-    torch = _torch or _load_torch()
-    devices = {t.get_device() for t in ts if t is not None}
-    if -1 in devices:
+    refused."""
+    if any(t is not None and not t.is_cuda for t in ts):
         raise ValueError("tensors passed to the CUDA library must live on the GPU")
-    current = torch._C._cuda_getDevice()
-    if devices != {current}:
-        raise ValueError("tensors passed to the CUDA library must live on the current device")
-    return current
+    raise ValueError("tensors passed to the CUDA library must live on the current device")
+
+
+def _on_current_device(*ts):
+    """Refuses tensors that are not on the current device.  Returns the device."""
+    for t in ts:
+        if t is not None and not t.is_cuda:
+            _wrong_device(t)
+    device = _current_device()
+    for t in ts:
+        if t is not None and t.get_device() != device:
+            _wrong_device(t)
+    return device
 
 
 def _raw_stream(stream, device):
     """The handle of a call's stream, by default the device's current one."""
-    if stream is not None:
-        return stream.cuda_stream
+    return _raw_current_stream(device) if stream is None else stream.cuda_stream
+
+
+def _empty_like(t):
+    """A new tensor of t's shape and type, contiguous."""
     torch = _torch or _load_torch()
-    return torch._C._cuda_getCurrentRawStream(device)
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _result_like(t, stream):
     """_result of t's shape and type."""
-    torch = _torch or _load_torch()
     if stream is None:
-        return torch.empty_like(t, memory_format=torch.contiguous_format)
+        return _empty_like(t)
     return _result(t.shape, t.dtype, t.device, stream)
 
 
@@ -740,12 +763,21 @@ def w4_w4a16_linear_few(x, q, s, z, group: int = 128, out=None, dev_status=None,
         raise ValueError("x must be [M, K] bf16, q [N, K / 2] uint8, s and z [N, K / group] fp16")
     if not (x.is_contiguous() and q.is_contiguous() and s.is_contiguous() and z.is_contiguous()):
         raise ValueError("tensors passed to the CUDA library must be contiguous")
-    _require_int32(dev_status)
-    device = _on_current_device(x, q, s, z, out, dev_status)
+    if not x.is_cuda:
+        _wrong_device(x)
+    device = _current_device()
+    if x.get_device() != device or q.get_device() != device or s.get_device() != device or \
+            z.get_device() != device:
+        _wrong_device(x, q, s, z)
+    if dev_status is not None:
+        _require_int32(dev_status)
+        _on_current_device(dev_status)
     if out is None:
-        out = _result((M, N), bf16, x.device, stream)
-    elif out.dtype is not bf16 or out.shape != (M, N) or not out.is_contiguous():
-        raise ValueError("out must be [M, N] bf16, contiguous")
+        out = torch.empty((M, N), dtype=bf16, device=x.device) if stream is None else \
+            _result((M, N), bf16, x.device, stream)
+    elif out.dtype is not bf16 or out.shape != (M, N) or not out.is_contiguous() or \
+            out.get_device() != device:
+        raise ValueError("out must be [M, N] bf16, contiguous, on the current device")
     _call("w4_w4a16_linear_few", x.data_ptr(), M, K, N, q.data_ptr(), s.data_ptr(), z.data_ptr(),
           group, out.data_ptr(), 0 if dev_status is None else dev_status.data_ptr(),
           _raw_stream(stream, device))
@@ -829,17 +861,15 @@ def w4_gumbel_argmax_sample(logits, seed: int, offset: int = 0, workspace=None, 
 # --------------------------------------------------------------------------
 def _require_int32(*ts):
     """Contiguous int32 CUDA tensors (or None)."""
-    torch = _torch or _load_torch()
-    int32 = torch.int32
+    int32 = (_torch or _load_torch()).int32
     for t in ts:
-        if t is None:
+        if t is None or (t.is_cuda and t.dtype is int32 and t.is_contiguous()):
             continue
         if not t.is_cuda:
             raise ValueError("tensors passed to the CUDA library must live on the GPU")
         if not t.is_contiguous():
             raise ValueError("tensors passed to the CUDA library must be contiguous")
-        if t.dtype is not int32:
-            raise ValueError("tables, lengths, slots, page lists and status must be int32")
+        raise ValueError("tables, lengths, slots, page lists and status must be int32")
 
 
 def _kv_state(table, lens, refs, dev_status):
@@ -1045,8 +1075,8 @@ def w4_rope_steps(rot: int, base: float = 10000.0, method: str = "linear", facto
 
 
 def _rope_inputs(q, k, steps, positions, q_weight, k_weight):
-    """(0 or 1 for the type, shape of q, kv heads, strides of q and k) of a rotation's
-    inputs, checked but for their device."""
+    """(0 or 1 for the type, shape of q, kv heads, strides of q and k, the device) of a
+    rotation's inputs, checked."""
     torch = _torch or _load_torch()
     dtype = q.dtype
     code = 0 if dtype is torch.bfloat16 else 1 if dtype is torch.float16 else -1
@@ -1071,7 +1101,15 @@ def _rope_inputs(q, k, steps, positions, q_weight, k_weight):
     if k_weight is not None and (k_weight.dtype is not dtype or k_weight.shape != (D,) or
                                  not k_weight.is_contiguous()):
         raise ValueError("k_weight must be [D] of q's type, contiguous")
-    return code, shape, Hkv, qs, ks
+    if not q.is_cuda:
+        _wrong_device(q)
+    device = _current_device()
+    if q.get_device() != device or k.get_device() != device or steps.get_device() != device or \
+            (positions is not None and positions.get_device() != device) or \
+            (q_weight is not None and q_weight.get_device() != device) or \
+            (k_weight is not None and k_weight.get_device() != device):
+        _wrong_device(q, k, steps, positions, q_weight, k_weight)
+    return code, shape, Hkv, qs, ks, device
 
 
 def _rope_out(out, like, stream, what):
@@ -1081,6 +1119,8 @@ def _rope_out(out, like, stream, what):
         _, H, D = out.shape
         return out, H * D, D
     strides = out.stride()
+    if out.get_device() != like.get_device():
+        _wrong_device(out)
     if out.shape != like.shape or out.dtype is not like.dtype or strides[2] != 1:
         raise ValueError(f"{what}_out must be like {what}, contiguous along the last axis")
     return out, strides[0], strides[1]
@@ -1095,10 +1135,13 @@ def w4_qk_norm_rope(q, k, positions, steps, q_weight=None, k_weight=None, eps: f
     be q and k themselves."""
     if positions is None:
         raise ValueError("positions must be [T] int32, contiguous")
-    code, (T, Hq, D), Hkv, qs, ks = _rope_inputs(q, k, steps, positions, q_weight, k_weight)
-    device = _on_current_device(q, k, positions, steps, q_weight, k_weight, q_out, k_out)
-    q_out, q_tok, q_head = _rope_out(q_out, q, stream, "q")
-    k_out, k_tok, k_head = _rope_out(k_out, k, stream, "k")
+    code, (T, Hq, D), Hkv, qs, ks, device = _rope_inputs(q, k, steps, positions, q_weight, k_weight)
+    if q_out is None and k_out is None and stream is None:
+        q_out, k_out = _empty_like(q), _empty_like(k)
+        q_tok, q_head, k_tok, k_head = Hq * D, D, Hkv * D, D
+    else:
+        q_out, q_tok, q_head = _rope_out(q_out, q, stream, "q")
+        k_out, k_tok, k_head = _rope_out(k_out, k, stream, "k")
     _call("w4_qk_norm_rope", q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
           positions.data_ptr(), steps.data_ptr(), 0 if q_weight is None else q_weight.data_ptr(),
           0 if k_weight is None else k_weight.data_ptr(), T, Hq, Hkv, D, 2 * steps.shape[0],
@@ -1113,7 +1156,7 @@ def w4_kv_append_rope(k_pages, v_pages, table, lens, q, k, v, q_offsets, steps, 
     """w4_qk_norm_rope and w4_kv_append in one pass: returns the queries, writes the
     keys and values [T, Hkv, D] of the slots' last tokens into their pages.
     positions defaults to the tokens' places in their sequences."""
-    code, (T, Hq, D), Hkv, qs, ks = _rope_inputs(q, k, steps, positions, q_weight, k_weight)
+    code, (T, Hq, D), Hkv, qs, ks, device = _rope_inputs(q, k, steps, positions, q_weight, k_weight)
     dtype, pages, ps, vs = q.dtype, k_pages.shape, k_pages.stride(), v.stride()
     if k_pages.dtype is not dtype or v_pages.dtype is not dtype or len(ps) != 4 or ps[3] != 1 or \
             v_pages.shape != pages or v_pages.stride() != ps:
@@ -1124,9 +1167,16 @@ def w4_kv_append_rope(k_pages, v_pages, table, lens, q, k, v, q_offsets, steps, 
         raise ValueError("k and v must be [T, Hkv, D] of the pages' type")
     _require_int32(table, lens, q_offsets, dev_status)
     B, W = _kv_batch(table, lens, q_offsets)
-    device = _on_current_device(k_pages, v_pages, table, lens, q, k, v, q_offsets, steps, positions,
-                                q_weight, k_weight, q_out, dev_status)
-    q_out, q_tok, q_head = _rope_out(q_out, q, stream, "q")
+    if k_pages.get_device() != device or v_pages.get_device() != device or \
+            v.get_device() != device or table.get_device() != device or \
+            lens.get_device() != device or q_offsets.get_device() != device:
+        _wrong_device(k_pages, v_pages, v, table, lens, q_offsets)
+    if dev_status is not None:
+        _on_current_device(dev_status)
+    if q_out is None and stream is None:
+        q_out, q_tok, q_head = _empty_like(q), Hq * D, D
+    else:
+        q_out, q_tok, q_head = _rope_out(q_out, q, stream, "q")
     if B == 0:
         return q_out
     _call("w4_kv_append_rope", k_pages.data_ptr(), v_pages.data_ptr(), ps[0], ps[1], ps[2], P, page,
@@ -1178,7 +1228,8 @@ def _attn(name, masks, q, k_pages, v_pages, table, lens, q_offsets, group_offset
           0 if shared_lens is None else shared_lens.data_ptr(), G, Hq, Hkv, D,
           0 if dtype is torch.bfloat16 else 1, *before, D ** -0.5 if scale is None else scale,
           workspace.data_ptr(), workspace.nbytes, out.data_ptr(),
-          0 if dev_status is None else dev_status.data_ptr(), _stream(stream))
+          0 if dev_status is None else dev_status.data_ptr(),
+          _raw_stream(stream, _current_device()))
     return out
 
 
