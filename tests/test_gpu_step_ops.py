@@ -149,3 +149,42 @@ def test_results_do_not_depend_on_what_the_workspace_held(lib):
     assert torch.equal(calls["tree"](workspace=ws), want)
     ws.fill_(0)
     assert torch.equal(calls["tree"](workspace=ws), want)
+
+
+def test_each_reads_what_the_one_before_wrote(lib):
+    """A chain whose kernels begin while the one before still runs, over the same buffers
+    with other values every time: as with a wait between all of them."""
+    import torch
+    d = _setup()
+    c, steps = d["c"], lib.w4_rope_steps(64)
+    _, w2, s2, z2 = (t.cuda() for t in d["wide"])
+    kp, vp = c["cache"][0].clone(), c["cache"][1].clone()
+    x, kv = torch.empty_like(d["x"]), torch.empty((9, 12, 64), dtype=torch.bfloat16, device="cuda")
+    qr, o, y = torch.empty_like(c["q"]), torch.empty_like(c["q"]), []
+    g = torch.Generator("cuda").manual_seed(8)
+    inputs = [torch.randn(x.shape, device="cuda", generator=g).bfloat16() for _ in range(12)]
+    norm = torch.ones(1024, device="cuda").bfloat16()
+    ys = [torch.empty((9, 39000), dtype=torch.bfloat16, device="cuda") for _ in inputs]
+
+    def run(wait):
+        y.clear()
+        for i, v in enumerate(inputs):
+            lib.w4_rmsnorm(v, norm, out=x)
+            wait()
+            lib.w4_w4a16_linear_few(x, d["q"], d["s"], d["z"], out=kv.view(9, -1))
+            wait()
+            lib.w4_kv_append_rope(kp, vp, c["table"], c["lens"], kv[:, :8], kv[:, 8:10], kv[:, 10:],
+                                  c["q_offsets"], steps, q_weight=d["w"], k_weight=d["w"], q_out=qr)
+            wait()
+            lib.w4_attn_tree(qr, kp, vp, c["table"], c["lens"], c["q_offsets"], d["tree"], max_q=6,
+                             out=o)
+            wait()
+            lib.w4_w4a16_linear_few(o.view(9, -1), w2, s2, z2, out=ys[i])
+            wait()
+            y.append((qr.clone(), o.clone(), ys[i].clone()))
+        torch.cuda.synchronize()
+        return list(y)
+    want = run(torch.cuda.synchronize)
+    for _ in range(3):
+        got = run(lambda: None)
+        assert all(torch.equal(a, b) for p, q in zip(got, want) for a, b in zip(p, q))

@@ -37,6 +37,10 @@
 //     first tile 6, change of piece 1.5 each, join and its launch 6
 //   four times 256 queries over 4096 + 256: 46 us; 37 GFLOP (19 us), the pairs' loop
 //   two sequences of 240 tokens: 14 us, all of it plan, one tile and join
+//   trees: 32 of 11 to 60 drafts behind 6029 shared tokens and 430 to 770 own: 131 us;
+//     125 GFLOP (64 us), 1.73 a tile of a pair, 6.6 an item, join 17
+//   four trees of 81 to 92 drafts, sequences of 35,000 to 44,000, 24/4 heads of 64, fp16:
+//     124 us; 84 GFLOP (43 us), 1.3 a tile of a pair: the softmax's chain
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -780,8 +784,7 @@ struct Kernel {
                 const int key = w.g.kbase + w.t * kKeys + lane * p.page;
                 n.in = lane < kKeys / p.page && key < w.g.k1;
                 if (n.in)
-                    n.id = __ldg(p.table + static_cast<int64_t>(w.g.row_of_table) * p.W +
-                                 (key >> p.page_shift));
+                    n.id = p.table[static_cast<int64_t>(w.g.row_of_table) * p.W + (key >> p.page_shift)];
                 w.t++;
             };
             if (pairs.more()) {
@@ -1249,8 +1252,8 @@ struct Kernel {
         if constexpr (TREE) {
             window.from = len - (p.q_offsets[b + 1] - p.q_offsets[b]);
             window.bits = p.tree + static_cast<int64_t>(tok) * p.tree_words;
-            window.first[0] = __ldg(window.bits);
-            window.first[1] = p.tree_words > 1 ? __ldg(window.bits + 1) : 0u;
+            window.first[0] = *window.bits;
+            window.first[1] = p.tree_words > 1 ? window.bits[1] : 0u;
             return len;
         }
         return p.causal ? len - (p.q_offsets[b + 1] - tok) + 1 : len;
@@ -1264,7 +1267,7 @@ struct Kernel {
         auto word = [&](int j) {
             return j < 0               ? ~0u
                    : j < 2             ? (j == 0 ? window.first[0] : window.first[1])
-                   : j < p.tree_words ? __ldg(window.bits + j)
+                   : j < p.tree_words ? window.bits[j]
                                        : 0u;
         };
         return at <= -32 ? ~0u : __funnelshift_r(word(at >> 5), word((at >> 5) + 1), at & 31);

@@ -130,7 +130,7 @@ struct FewLinear {
 #pragma unroll
             for (int h = 0; h < kGroups; h++)
                 u.sz[r][h] = kGroups == 1 || block * kGroups + h < G
-                                 ? __ldg(sz + min(row + (t4 >> 1), last) * G + block * kGroups + h)
+                                 ? sz[min(row + (t4 >> 1), last) * G + block * kGroups + h]
                                  : static_cast<uint16_t>(0);
         }
     }
@@ -212,7 +212,7 @@ struct FewLinear {
                 const int word = kGroups == 1 ? t4 * 4 + j : (j >> 1) * 8 + t4 * 2 + (j & 1);
                 v[j] = make_uint4(0, 0, 0, 0);
                 if (t < p.M && block * 128 + word * 8 < p.K)
-                    v[j] = __ldg(reinterpret_cast<const uint4 *>(x + word * 8));
+                    v[j] = *reinterpret_cast<const uint4 *>(x + word * 8);
             }
             uint8_t *tile = xs + n * tile_stride;
             float sums[kGroups] = {};

@@ -101,6 +101,16 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
     return r;
 }
 
+// A scale or zero.  Non-coherent, so that a row's neighbouring ones stay in L1 across the
+// fences (coherent loads: 32 tokens, 2816 -> 262144, 217 us instead of 107); volatile, so
+// that none moves before the wait for the kernel that may have written them.
+__device__ __forceinline__ uint16_t load_weight(const uint16_t *at)
+{
+    uint16_t v;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(at));
+    return v;
+}
+
 // One group: four steps of 32 codes, A in tensor memory (8 columns a step), by one elected
 // lane; the sums begin anew.
 __device__ __forceinline__ void mma_group(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc)
@@ -160,8 +170,8 @@ template <int TOK> struct Wide {
                 const int i = i0 + 2 * u + sub, tok = i % TOK, t = t0 + tok;
                 v[u] = make_uint4(0, 0, 0, 0);
                 if (i < items && t < p.M)
-                    v[u] = __ldg(reinterpret_cast<const uint4 *>(
-                        p.x + static_cast<int64_t>(t) * p.K + i / TOK * kGroup + l * 8));
+                    v[u] = *reinterpret_cast<const uint4 *>(
+                        p.x + static_cast<int64_t>(t) * p.K + i / TOK * kGroup + l * 8);
             }
 #pragma unroll
             for (int u = 0; u < kBatch; u++) {
@@ -349,8 +359,8 @@ template <int TOK> struct Wide {
         Place to{0, w, w, 0}, at = to;
         auto scales = [&](int idx, uint16_t &sv, uint16_t &zv) {
             const int64_t row = min(row0 + to.task * kRows + mine, p.N - 1);
-            sv = idx < total ? __ldg(p.s + row * p.groups + to.g) : static_cast<uint16_t>(0);
-            zv = idx < total ? __ldg(p.z + row * p.groups + to.g) : static_cast<uint16_t>(0);
+            sv = idx < total ? load_weight(p.s + row * p.groups + to.g) : static_cast<uint16_t>(0);
+            zv = idx < total ? load_weight(p.z + row * p.groups + to.g) : static_cast<uint16_t>(0);
             to.next(p, 2);
         };
 #pragma unroll

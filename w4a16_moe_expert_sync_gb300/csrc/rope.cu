@@ -20,7 +20,7 @@
 // kRopeBatch heads are in flight a lane.
 //
 // Bound by HBM, small calls by latency.  Measured on GB300 from a graph: 16387 tokens of
-// 36 heads of 128, 302 MB, 54 us (45 at the copy bandwidth); 62,000 tokens of 32 heads into
+// 36 heads of 128, 302 MB, 54 us (45 at the copy bandwidth); 64,800 tokens of 32 heads into
 // pages, 1.06 GB, 188 us (157); one token of 24 heads 2.9 us, 64 appended ones 4.1.  (2 heads
 // in flight: 65 and 220 us, 8: 56 and 264 for the registers; a CTA of 256 threads 67 and 309;
 // at most 16 heads a group 54 and 197.)
@@ -103,8 +103,8 @@ __device__ __forceinline__ bool offsets_ascend(const RopeProblem &p, int32_t *st
 {
     bool bad = false;
     for (int b = threadIdx.x; b <= p.B; b += kRopeThreads) {
-        const int a = __ldg(p.q_offsets + b);
-        bad |= a < 0 || a > p.T || (b > 0 && a < __ldg(p.q_offsets + b - 1));
+        const int a = p.q_offsets[b];
+        bad |= a < 0 || a > p.T || (b > 0 && a < p.q_offsets[b - 1]);
         if (p.B <= kRopeOffsets)
             staged[b] = a;
     }
@@ -117,8 +117,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeProblem
 {
     constexpr int kGroups = kRopeThreads / LANES;
     extern __shared__ int32_t staged[];
-    pdl_wait();
-    pdl_trigger();
+    pdl_wait();                            // (no load here is a non-coherent one: this kernel
+    pdl_trigger();                         // begins while the one before still writes)
     const int lane = threadIdx.x & 31, l = threadIdx.x % LANES;
     const unsigned mates = (LANES == 32 ? ~0u : (1u << LANES) - 1u) << (lane / LANES * LANES);
     // a CTA's groups have neighbouring tokens and the same heads
@@ -149,20 +149,20 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeProblem
             const int b = sequence_of(offsets, p.B, t);
             valid = b >= 0;
             if (valid) {
-                const int at = max(__ldg(p.lens + b), 0) - (offsets[b + 1] - t);
+                const int at = max(p.lens[b], 0) - (offsets[b + 1] - t);
                 const int entry = at >= 0 ? at / p.page : 0;
                 if (at >= 0 && entry < p.W)
-                    page = __ldg(p.table + static_cast<int64_t>(b) * p.W + entry);
+                    page = p.table[static_cast<int64_t>(b) * p.W + entry];
                 if (page >= p.P)
                     page = -1;
                 slot = at - entry * p.page;
-                pos = p.positions ? __ldg(p.positions + t) : at;
+                pos = p.positions ? p.positions[t] : at;
                 if (page < 0 && part == 0 && l == 0 && p.dev_status)
                     atomicOr(p.dev_status, W4_DEV_BAD_PAGE);
             }
         }
     } else if (valid) {
-        pos = __ldg(p.positions + t);
+        pos = p.positions[t];
     }
     if (!valid)
         return;                            // its mates too
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeProblem
             // in neighbouring pairs chunk c has pairs 4 c .. 4 c + 3
             const int f = p.interleaved ? (i < 4 ? c0 * 4 + i : c1 * 4 + i - 4) : l * 8 + i;
             const uint64_t angle = static_cast<uint64_t>(static_cast<int64_t>(pos)) *
-                                   static_cast<uint64_t>(__ldg(p.steps + f));
+                                   static_cast<uint64_t>(p.steps[f]);
             // half turns in [-1, 1)
             const float x = static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f;
             sincospif(x, &sn[i], &cs[i]);
@@ -196,9 +196,9 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeProblem
                 w[i] = 1.0f;
             if (weight) {
                 if (has0)
-                    unpack8<BF16>(__ldg(reinterpret_cast<const uint4 *>(weight + c0 * 8)), w);
+                    unpack8<BF16>(*reinterpret_cast<const uint4 *>(weight + c0 * 8), w);
                 if (has1)
-                    unpack8<BF16>(__ldg(reinterpret_cast<const uint4 *>(weight + c1 * 8)), w + 8);
+                    unpack8<BF16>(*reinterpret_cast<const uint4 *>(weight + c1 * 8), w + 8);
             }
             if (p.interleaved) {
 #pragma unroll
@@ -328,7 +328,7 @@ cudaError_t launch_lanes(const RopeProblem &p, int sms, cudaStream_t stream)
     const int64_t fair = static_cast<int64_t>(p.T) * rows / (static_cast<int64_t>(sms) * 16 * kGroups);
     const int most = static_cast<int>(std::min<int64_t>(std::max<int64_t>(fair, 1), kRopeHeads));
     const int parts = (rows + most - 1) / most, heads = (rows + parts - 1) / parts;
-    const dim3 grid((p.T + kGroups - 1) / kGroups, parts), block(kRopeThreads);
+    const dim3 grid((static_cast<unsigned>(p.T) + kGroups - 1) / kGroups, parts), block(kRopeThreads);
     const size_t smem = p.v_pages && p.B <= kRopeOffsets ? sizeof(int32_t) * (p.B + 1) : 0;
     if (p.v_pages)
         return p.bf16 ? launch_pdl(rope_kernel<LANES, true, true>, grid, block, smem, stream, p, heads)
