@@ -512,7 +512,8 @@ int w4_moe_layer_static_scratch(const uint16_t *x, const int32_t *topk_ids,
  * dequantised once per pass of up to 256 token rows, and narrow outputs
  * split the contraction (fp32 partial sums in the workspace, added in split
  * order by one more launch; the split depends on the shape only, so results
- * are the same on every GPU).  Two or three launches.
+ * are the same on every GPU).  Two or three launches.  (For up to 32 rows
+ * w4_w4a16_linear_few takes less: one launch, any N, no rounding of x.)
  * Requires group 64 or 128, K >= 256 a multiple of the group and of 64 with
  * K / group <= 32, N a multiple of 128.  dev_status may be NULL.
  * ------------------------------------------------------------------------ */
@@ -696,7 +697,7 @@ int w4_kv_append(uint16_t *k_pages, uint16_t *v_pages, int64_t page_stride, int6
  *   q_offsets, kept_offsets  [B + 1] int32, ascending
  *   kept                     [n_kept] int32
  *   lens_out                 [B] out: lens[b] - n + the number kept; may be lens
- * The slot keeps its pages, as where the caller lowers a length himself.  A slot
+ * The slot keeps its pages, as where the caller lowers a length.  A slot
  * whose new tokens lie in a page that others hold (refs > 1) and would be written
  * there, whose lists do not ascend within their bounds or whose new tokens are more
  * than its length (W4_DEV_BAD_SLOT), or with a page id outside [0, P) among those
@@ -744,9 +745,11 @@ int w4_rope_steps(int rot, double base, int method, double factor, double traine
  *   dtype       0: bf16, 1: fp16
  *   amplitude   multiplies the rotated values (1 where nothing asks for another)
  *   q_out, k_out  like q and k, with strides of their own; they may be q and k
- * Arithmetic is fp32, every value rounded once; angles are exact to 2^-31 of a turn
- * for positions up to 2^23 (beyond, the frequencies' rounding to 53 bits shows).  Requires D a multiple of 8 up to 256, rot a multiple of 16 up
- * to D, pointers 16-byte aligned, strides multiples of 8 elements.  One launch.
+ *               themselves, and else have no memory in common with any input
+ * Arithmetic is fp32 (a head whose sum of squares is beyond its range: zeros), every
+ * value rounded once; angles are exact to 2^-31 of a turn
+ * for positions up to 2^23 (beyond, the frequencies' rounding to 53 bits shows).
+ * Requires D a multiple of 8 up to 256, rot a multiple of 16 up to D, pointers 16-byte aligned, strides multiples of 8 elements.  One launch.
  * ------------------------------------------------------------------------ */
 int w4_qk_norm_rope(const uint16_t *q, int64_t q_tok_stride, int64_t q_head_stride,
                     const uint16_t *k, int64_t k_tok_stride, int64_t k_head_stride,

@@ -285,6 +285,20 @@ def test_captured_and_on_another_stream(lib):
         assert torch.equal(out, want) and torch.equal(c["pool"], pool)
 
 
+@gpu
+def test_results_that_overlap_are_refused(lib):
+    import torch
+    q, k, _, _ = _inputs(4, 2, 2, 64, "bfloat16", 3)
+    pos, steps = torch.zeros(4, dtype=torch.int32, device="cuda"), lib.w4_rope_steps(64)
+    flat = torch.zeros(4 * 2 * 64, dtype=torch.bfloat16, device="cuda")
+    for strides in ((0, 64, 1), (128, 0, 1), (128, 56, 1), (56, 256, 1)):
+        bad = flat.as_strided((4, 2, 64), strides)
+        with pytest.raises(ValueError, match="overlap"):
+            lib.w4_qk_norm_rope(q, k, pos, steps, q_out=bad)
+        with pytest.raises(ValueError, match="overlap"):
+            lib.w4_qk_norm_rope(q, k, pos, steps, k_out=bad)
+
+
 # ------------------------------------------------------------------- without a GPU
 def _steps(rot, *a, **kw):
     return [s % 2 ** 64 for s in w4.w4_rope_steps(rot, *a, device="cpu", **kw).tolist()]

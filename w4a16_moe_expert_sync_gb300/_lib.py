@@ -732,7 +732,8 @@ def w4_w4a16_linear_workspace_size(M: int, K: int, N: int, group: int = 128) -> 
 def w4_w4a16_linear(x, q, s, z, group: int = 128, workspace=None, out=None, dev_status=None,
                     stream=None):
     """w4a16_linear: y [M, N] bf16 = x [M, K] bf16 . deq(W)^T with W packed as
-    w4_quantize writes it (q [N, K/2] uint8, s/z [N, K/group] fp16)."""
+    w4_quantize writes it (q [N, K/2] uint8, s/z [N, K/group] fp16).  For up to 32
+    rows w4_w4a16_linear_few takes less time."""
     import torch
     _require_cuda(x, q, s, z, workspace, out, dev_status)
     M, K = x.shape
@@ -1123,6 +1124,9 @@ def _rope_out(out, like, stream, what):
         _wrong_device(out)
     if out.shape != like.shape or out.dtype is not like.dtype or strides[2] != 1:
         raise ValueError(f"{what}_out must be like {what}, contiguous along the last axis")
+    T, H, D = out.shape
+    if (T > 1 and strides[0] < D) or (H > 1 and strides[1] < D):
+        raise ValueError(f"{what}_out's tokens or heads overlap")
     return out, strides[0], strides[1]
 
 
@@ -1132,7 +1136,7 @@ def w4_qk_norm_rope(q, k, positions, steps, q_weight=None, k_weight=None, eps: f
     """Queries [T, Hq, D] and keys [T, Hkv, D] (any strides of tokens and heads)
     normed for each head (with a weight [D]) and their first 2 len(steps) values
     rotated by positions [T] int32, in one pass.  Returns (q_out, k_out); they may
-    be q and k themselves."""
+    be q and k themselves, and else have no memory in common with an input."""
     if positions is None:
         raise ValueError("positions must be [T] int32, contiguous")
     code, (T, Hq, D), Hkv, qs, ks, device = _rope_inputs(q, k, steps, positions, q_weight, k_weight)
