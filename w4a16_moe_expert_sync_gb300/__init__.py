@@ -16,6 +16,15 @@ A decoding step has the layer for a few tokens, a paged cache and attention:
     o = w4.w4_attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets,
                                  group_offsets, shared_lens, max_q=1)
     out, ids, w = w4.w4_moe_layer_few_from_logits(x, logits, 8, gate_up, down)
+
+A step that verifies a tree of drafts has projections for few rows, the rotation on
+the way into the cache, attention by ancestors, and keeps the accepted path:
+
+    qkv = w4.w4_w4a16_linear_few(x, *weight)
+    q = w4.w4_kv_append_rope(k_pages, v_pages, table, lens, q, k, v, q_offsets, steps,
+                             positions=depths)
+    o = w4.w4_attn_tree(q, k_pages, v_pages, table, lens, q_offsets, tree, max_q=n)
+    w4.w4_kv_keep(pool, table, lens, refs, q_offsets, kept, kept_offsets)
 """
 from ._lib import (W4_DEV_BAD_EXPERT_ID, W4_DEV_FP16_RANGE, W4_DEV_OUT_OF_BOUNDS,
                    W4_DEV_PIPELINE_TIMEOUT,
