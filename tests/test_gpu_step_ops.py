@@ -107,14 +107,18 @@ def test_results_belong_to_the_stream(lib, monkeypatch, name):
 
 
 @pytest.mark.parametrize("name", ["linear", "rope", "append", "tree", "keep"])
-def test_another_current_device_is_refused(lib, monkeypatch, name):
+def test_another_current_device_is_refused(lib, name):
     from w4a16_moe_expert_sync_gb300 import _lib
     d = _setup()
     call = _calls(lib, d)[name]
     call()
-    monkeypatch.setattr(_lib, "_current_device", lambda: 1)
-    with pytest.raises(ValueError):
-        call()
+    _lib._calls().pretend_device(1)
+    try:
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    finally:
+        _lib._calls().pretend_device(-1)
+    call()
 
 
 def test_two_graphs_share_a_workspace(lib):

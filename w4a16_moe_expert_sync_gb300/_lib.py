@@ -2,18 +2,20 @@
 the same names, taking torch tensors.  Argument marshalling only: shapes are
 read from the tensors, outputs are allocated with torch (device memory), the
 pointers and the current CUDA stream are passed through, and a nonzero status
-raises W4Error.  Every step of the layer runs in the library's CUDA kernels;
+raises W4Error.  (A step's calls of a few microseconds on the GPU go the same way in
+C++: csrc/calls.cpp.)  Every step of the layer runs in the library's CUDA kernels;
 there is no fallback of any kind.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
-import struct
 import threading
 
-from .build import LIB as _LIB_PATH
+from .build import LIB as _LIB_PATH, calls_path
 
 _lock = threading.Lock()
 _lib = None
@@ -22,10 +24,8 @@ _torch = None
 
 def _load_torch():
     """torch, for the calls where an import statement's half microsecond counts."""
-    global _torch, _current_device, _raw_current_stream
+    global _torch
     import torch
-    _current_device = torch._C._cuda_getDevice
-    _raw_current_stream = torch._C._cuda_getCurrentRawStream
     _torch = torch
     return torch
 
@@ -145,31 +145,37 @@ def load_library(path: str | None = None):
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = res
-        codes = {V: "Q", I: "i", I64: "q", SZ: "Q", ctypes.c_float: "f"}
-        for name in _PACKED:
-            fn = getattr(lib, name + "_packed")
-            fn.argtypes, fn.restype = [ctypes.c_char_p], I
-            pack = struct.Struct("".join(codes[a] for a in sig[name][0])).pack
-            _packed_calls[name] = fn, pack
         _lib = lib
         return lib
 
 
-# calls with many arguments, which go over in one buffer (csrc/packed.cu)
-_PACKED = ("w4_w4a16_linear_few", "w4_qk_norm_rope", "w4_kv_append_rope", "w4_kv_keep",
-           "w4_attn_shared_prefix", "w4_attn_tree")
-_packed_calls: dict = {}
+_calls_module = None
 
 
-def _call(name: str, *args):
-    """Calls one of _PACKED, NULL pointers as 0, and checks its status."""
-    call = _packed_calls.get(name)
-    if call is None:
-        load_library()
-        call = _packed_calls[name]
-    rc = call[0](call[1](*args))
-    if rc:
-        _check(rc, name)
+def _calls():
+    """The module that calls a step's entry points (csrc/calls.cpp), bound to the library."""
+    global _calls_module
+    lib = load_library()
+    with _lock:
+        if _calls_module is not None:
+            return _calls_module
+        import torch                       # its libraries are the module's too
+        path = calls_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build the CUDA library first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')")
+        loader = importlib.machinery.ExtensionFileLoader("w4_calls", path)
+        module = importlib.util.module_from_spec(
+            importlib.machinery.ModuleSpec("w4_calls", loader, origin=path))
+        loader.exec_module(module)
+        functions = (ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "w4_w4a16_linear_few", "w4_qk_norm_rope", "w4_kv_append_rope", "w4_kv_keep",
+            "w4_attn_shared_prefix", "w4_attn_tree", "w4_attn_shared_prefix_workspace_size"))
+        module.bind(*functions, _check,
+                    lambda t, shape, stream: _result(shape, t.dtype, t.device, stream),
+                    lambda t, nbytes, stream: _scratch(nbytes, torch.uint8, t.device, stream))
+        _calls_module = module
+        return module
 
 
 def _check(rc: int, what: str):
@@ -235,55 +241,6 @@ def _require(specs):
             raise ValueError("tensors passed to the CUDA library must be contiguous")
         if t.dtype is not dtype or t.shape != shape:
             raise ValueError(f"{name} must be {list(shape)} {dtype}, not {list(t.shape)} {t.dtype}")
-
-
-def _current_device():
-    """The current device (torch's own function once torch is loaded)."""
-    _load_torch()
-    return _current_device()
-
-
-def _raw_current_stream(device):
-    _load_torch()
-    return _raw_current_stream(device)
-
-
-def _wrong_device(*ts):
-    """The kernels run on the current device: tensors of another one, or of none, are
-    refused."""
-    if any(t is not None and not t.is_cuda for t in ts):
-        raise ValueError("tensors passed to the CUDA library must live on the GPU")
-    raise ValueError("tensors passed to the CUDA library must live on the current device")
-
-
-def _on_current_device(*ts):
-    """Refuses tensors that are not on the current device.  Returns the device."""
-    for t in ts:
-        if t is not None and not t.is_cuda:
-            _wrong_device(t)
-    device = _current_device()
-    for t in ts:
-        if t is not None and t.get_device() != device:
-            _wrong_device(t)
-    return device
-
-
-def _raw_stream(stream, device):
-    """The handle of a call's stream, by default the device's current one."""
-    return _raw_current_stream(device) if stream is None else stream.cuda_stream
-
-
-def _empty_like(t):
-    """A new tensor of t's shape and type, contiguous."""
-    torch = _torch or _load_torch()
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
-
-
-def _result_like(t, stream):
-    """_result of t's shape and type."""
-    if stream is None:
-        return _empty_like(t)
-    return _result(t.shape, t.dtype, t.device, stream)
 
 
 # --------------------------------------------------------------------------
@@ -753,36 +710,7 @@ def w4_w4a16_linear(x, q, s, z, group: int = 128, workspace=None, out=None, dev_
 def w4_w4a16_linear_few(x, q, s, z, group: int = 128, out=None, dev_status=None, stream=None):
     """w4_w4a16_linear for up to 32 rows, in one launch without a workspace: y [M, N]
     bf16 = x [M, K] bf16 . deq(W)^T with W packed as w4_quantize writes it."""
-    torch = _torch or _load_torch()
-    if x.dim() != 2 or q.dim() != 2 or group <= 0:
-        raise ValueError("x must be [M, K] and the packed weight [N, K / 2]")
-    M, K = x.shape
-    N = q.shape[0]
-    bf16, f16, groups = torch.bfloat16, torch.float16, (N, K // group)
-    if x.dtype is not bf16 or q.dtype is not torch.uint8 or s.dtype is not f16 or \
-            z.dtype is not f16 or q.shape[1] != K // 2 or s.shape != groups or z.shape != groups:
-        raise ValueError("x must be [M, K] bf16, q [N, K / 2] uint8, s and z [N, K / group] fp16")
-    if not (x.is_contiguous() and q.is_contiguous() and s.is_contiguous() and z.is_contiguous()):
-        raise ValueError("tensors passed to the CUDA library must be contiguous")
-    if not x.is_cuda:
-        _wrong_device(x)
-    device = _current_device()
-    if x.get_device() != device or q.get_device() != device or s.get_device() != device or \
-            z.get_device() != device:
-        _wrong_device(x, q, s, z)
-    if dev_status is not None:
-        _require_int32(dev_status)
-        _on_current_device(dev_status)
-    if out is None:
-        out = torch.empty((M, N), dtype=bf16, device=x.device) if stream is None else \
-            _result((M, N), bf16, x.device, stream)
-    elif out.dtype is not bf16 or out.shape != (M, N) or not out.is_contiguous() or \
-            out.get_device() != device:
-        raise ValueError("out must be [M, N] bf16, contiguous, on the current device")
-    _call("w4_w4a16_linear_few", x.data_ptr(), M, K, N, q.data_ptr(), s.data_ptr(), z.data_ptr(),
-          group, out.data_ptr(), 0 if dev_status is None else dev_status.data_ptr(),
-          _raw_stream(stream, device))
-    return out
+    return (_calls_module or _calls()).linear_few(x, q, s, z, group, out, dev_status, stream)
 
 
 # --------------------------------------------------------------------------
@@ -1037,20 +965,9 @@ def w4_kv_keep(pool, table, lens, refs, q_offsets, kept, kept_offsets, lens_out=
     kept_offsets[b + 1]] names (ascending, from 0) move together in every plane,
     the others are taken back.  Returns the new lengths: lens_out, by default
     lens itself."""
-    lens_out = lens if lens_out is None else lens_out
-    B, W, P = _kv_state(table, lens, refs, dev_status)
-    planes, page_bytes, page = _kv_pool(pool, P)
-    _require_int32(q_offsets, kept, kept_offsets, lens_out)
-    if q_offsets.shape != (B + 1,) or kept_offsets.shape != (B + 1,) or kept.dim() != 1 or \
-            lens_out.shape != lens.shape:
-        raise ValueError("q_offsets and kept_offsets must be [B + 1], kept a list, lens_out [B]")
-    device = _on_current_device(pool, table, lens, refs, q_offsets, kept, kept_offsets, lens_out,
-                                dev_status)
-    _call("w4_kv_keep", pool.data_ptr(), planes, page_bytes, table.data_ptr(), B, W,
-          lens.data_ptr(), refs.data_ptr(), P, q_offsets.data_ptr(), kept.data_ptr(),
-          kept_offsets.data_ptr(), kept.shape[0], page, lens_out.data_ptr(),
-          0 if dev_status is None else dev_status.data_ptr(), _raw_stream(stream, device))
-    return lens_out
+    return (_calls_module or _calls()).kv_keep(pool, table, lens, refs, q_offsets, kept, kept_offsets,
+                                               lens if lens_out is None else lens_out, dev_status,
+                                               stream)
 
 
 # --------------------------------------------------------------------------
@@ -1075,61 +992,6 @@ def w4_rope_steps(rot: int, base: float = 10000.0, method: str = "linear", facto
     return steps.to(device)
 
 
-def _rope_inputs(q, k, steps, positions, q_weight, k_weight):
-    """(0 or 1 for the type, shape of q, kv heads, strides of q and k, the device) of a
-    rotation's inputs, checked."""
-    torch = _torch or _load_torch()
-    dtype = q.dtype
-    code = 0 if dtype is torch.bfloat16 else 1 if dtype is torch.float16 else -1
-    if code < 0 or k.dtype is not dtype:
-        raise ValueError("q and k must be of one type, bf16 or fp16")
-    qs, ks = q.stride(), k.stride()
-    if len(qs) != 3 or len(ks) != 3 or qs[2] != 1 or ks[2] != 1:
-        raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D], contiguous along the last axis")
-    shape = q.shape
-    T, _, D = shape
-    k_tokens, Hkv, k_d = k.shape
-    if k_tokens != T or k_d != D:
-        raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D]")
-    if steps.dtype is not torch.int64 or steps.dim() != 1 or not steps.is_contiguous():
-        raise ValueError("steps must be a table of w4_rope_steps")
-    if positions is not None and (positions.dtype is not torch.int32 or
-                                  positions.shape != (T,) or not positions.is_contiguous()):
-        raise ValueError("positions must be [T] int32, contiguous")
-    if q_weight is not None and (q_weight.dtype is not dtype or q_weight.shape != (D,) or
-                                 not q_weight.is_contiguous()):
-        raise ValueError("q_weight must be [D] of q's type, contiguous")
-    if k_weight is not None and (k_weight.dtype is not dtype or k_weight.shape != (D,) or
-                                 not k_weight.is_contiguous()):
-        raise ValueError("k_weight must be [D] of q's type, contiguous")
-    if not q.is_cuda:
-        _wrong_device(q)
-    device = _current_device()
-    if q.get_device() != device or k.get_device() != device or steps.get_device() != device or \
-            (positions is not None and positions.get_device() != device) or \
-            (q_weight is not None and q_weight.get_device() != device) or \
-            (k_weight is not None and k_weight.get_device() != device):
-        _wrong_device(q, k, steps, positions, q_weight, k_weight)
-    return code, shape, Hkv, qs, ks, device
-
-
-def _rope_out(out, like, stream, what):
-    """(result, its strides of tokens and heads): a new one like `like`, or out, checked."""
-    if out is None:
-        out = _result_like(like, stream)
-        _, H, D = out.shape
-        return out, H * D, D
-    strides = out.stride()
-    if out.get_device() != like.get_device():
-        _wrong_device(out)
-    if out.shape != like.shape or out.dtype is not like.dtype or strides[2] != 1:
-        raise ValueError(f"{what}_out must be like {what}, contiguous along the last axis")
-    T, H, D = out.shape
-    if (T > 1 and strides[0] < D) or (H > 1 and strides[1] < D):
-        raise ValueError(f"{what}_out's tokens or heads overlap")
-    return out, strides[0], strides[1]
-
-
 def w4_qk_norm_rope(q, k, positions, steps, q_weight=None, k_weight=None, eps: float = 1e-6,
                     interleaved: bool = False, amplitude: float = 1.0, q_out=None, k_out=None,
                     stream=None):
@@ -1137,21 +999,8 @@ def w4_qk_norm_rope(q, k, positions, steps, q_weight=None, k_weight=None, eps: f
     normed for each head (with a weight [D]) and their first 2 len(steps) values
     rotated by positions [T] int32, in one pass.  Returns (q_out, k_out); they may
     be q and k themselves, and else have no memory in common with an input."""
-    if positions is None:
-        raise ValueError("positions must be [T] int32, contiguous")
-    code, (T, Hq, D), Hkv, qs, ks, device = _rope_inputs(q, k, steps, positions, q_weight, k_weight)
-    if q_out is None and k_out is None and stream is None:
-        q_out, k_out = _empty_like(q), _empty_like(k)
-        q_tok, q_head, k_tok, k_head = Hq * D, D, Hkv * D, D
-    else:
-        q_out, q_tok, q_head = _rope_out(q_out, q, stream, "q")
-        k_out, k_tok, k_head = _rope_out(k_out, k, stream, "k")
-    _call("w4_qk_norm_rope", q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
-          positions.data_ptr(), steps.data_ptr(), 0 if q_weight is None else q_weight.data_ptr(),
-          0 if k_weight is None else k_weight.data_ptr(), T, Hq, Hkv, D, 2 * steps.shape[0],
-          bool(interleaved), code, eps, amplitude, q_out.data_ptr(), q_tok, q_head, k_out.data_ptr(),
-          k_tok, k_head, _raw_stream(stream, device))
-    return q_out, k_out
+    return (_calls_module or _calls()).qk_norm_rope(q, k, positions, steps, q_weight, k_weight, eps,
+                                                    interleaved, amplitude, q_out, k_out, stream)
 
 
 def w4_kv_append_rope(k_pages, v_pages, table, lens, q, k, v, q_offsets, steps, positions=None,
@@ -1160,81 +1009,14 @@ def w4_kv_append_rope(k_pages, v_pages, table, lens, q, k, v, q_offsets, steps, 
     """w4_qk_norm_rope and w4_kv_append in one pass: returns the queries, writes the
     keys and values [T, Hkv, D] of the slots' last tokens into their pages.
     positions defaults to the tokens' places in their sequences."""
-    code, (T, Hq, D), Hkv, qs, ks, device = _rope_inputs(q, k, steps, positions, q_weight, k_weight)
-    dtype, pages, ps, vs = q.dtype, k_pages.shape, k_pages.stride(), v.stride()
-    if k_pages.dtype is not dtype or v_pages.dtype is not dtype or len(ps) != 4 or ps[3] != 1 or \
-            v_pages.shape != pages or v_pages.stride() != ps:
-        raise ValueError("k_pages and v_pages must be alike, [P, page_size, Hkv, D] of q's type, "
-                         "contiguous along the last axis")
-    P, page, heads, d = pages
-    if heads != Hkv or d != D or v.dtype is not dtype or v.shape != k.shape or vs[2] != 1:
-        raise ValueError("k and v must be [T, Hkv, D] of the pages' type")
-    _require_int32(table, lens, q_offsets, dev_status)
-    B, W = _kv_batch(table, lens, q_offsets)
-    if k_pages.get_device() != device or v_pages.get_device() != device or \
-            v.get_device() != device or table.get_device() != device or \
-            lens.get_device() != device or q_offsets.get_device() != device:
-        _wrong_device(k_pages, v_pages, v, table, lens, q_offsets)
-    if dev_status is not None:
-        _on_current_device(dev_status)
-    if q_out is None and stream is None:
-        q_out, q_tok, q_head = _empty_like(q), Hq * D, D
-    else:
-        q_out, q_tok, q_head = _rope_out(q_out, q, stream, "q")
-    if B == 0:
-        return q_out
-    _call("w4_kv_append_rope", k_pages.data_ptr(), v_pages.data_ptr(), ps[0], ps[1], ps[2], P, page,
-          table.data_ptr(), B, W, lens.data_ptr(), q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0],
-          ks[1], v.data_ptr(), vs[0], vs[1], q_offsets.data_ptr(),
-          0 if positions is None else positions.data_ptr(), steps.data_ptr(),
-          0 if q_weight is None else q_weight.data_ptr(),
-          0 if k_weight is None else k_weight.data_ptr(), T, Hq, Hkv, D, 2 * steps.shape[0],
-          bool(interleaved), code, eps, amplitude, q_out.data_ptr(), q_tok, q_head,
-          0 if dev_status is None else dev_status.data_ptr(), _raw_stream(stream, device))
-    return q_out
+    return (_calls_module or _calls()).kv_append_rope(
+        k_pages, v_pages, table, lens, q, k, v, q_offsets, steps, positions, q_weight, k_weight, eps,
+        interleaved, amplitude, q_out, dev_status, stream)
 
 
 def w4_attn_shared_prefix_workspace_size(T: int, B: int, G: int, max_q: int, Hq: int, Hkv: int,
                                          D: int) -> int:
     return int(load_library().w4_attn_shared_prefix_workspace_size(T, B, G, max_q, Hq, Hkv, D))
-
-
-def _attn(name, masks, q, k_pages, v_pages, table, lens, q_offsets, group_offsets, shared_lens,
-          max_q, scale, workspace, out, dev_status, stream):
-    """Either attention: masks(T) gives its arguments behind max_q and those before scale."""
-    torch = _torch or _load_torch()
-    dtype, (P, page, Hkv, D), strides = _kv_planes(k_pages, v_pages)
-    qs = _rows16(q, dtype, "q")
-    _require_int32(table, lens, q_offsets, group_offsets, shared_lens, dev_status)
-    if q.dim() != 3 or (dtype is not torch.bfloat16 and dtype is not torch.float16):
-        raise ValueError("q must be [T, Hq, D] of the pages' type, bf16 or fp16")
-    T, Hq, q_d = q.shape
-    if q_d != D:
-        raise ValueError("q must be [T, Hq, D] of the pages' type, bf16 or fp16")
-    B, W = _kv_batch(table, lens, q_offsets)
-    G = 0 if group_offsets is None else group_offsets.numel() - 1
-    if G < 0 or (G > 0 and (shared_lens is None or shared_lens.numel() != G)):
-        raise ValueError("group_offsets must be [G + 1] and shared_lens [G]")
-    behind, before = masks(T)
-    if out is None:
-        out = _result_like(q, stream)
-    else:
-        _require(((out, dtype, (T, Hq, D), "out"),))
-    if workspace is None:
-        workspace = _scratch(
-            max(w4_attn_shared_prefix_workspace_size(T, B, G, max_q, Hq, Hkv, D), 256)
-            if Hkv and Hq % Hkv == 0 else 256, torch.uint8, q.device, stream)
-    else:
-        _require_cuda(workspace)
-    _call(name, q.data_ptr(), qs[0], qs[1], k_pages.data_ptr(), v_pages.data_ptr(), *strides[:3], P,
-          page, table.data_ptr(), W, lens.data_ptr(), q_offsets.data_ptr(), T, B, max_q, *behind,
-          0 if group_offsets is None else group_offsets.data_ptr(),
-          0 if shared_lens is None else shared_lens.data_ptr(), G, Hq, Hkv, D,
-          0 if dtype is torch.bfloat16 else 1, *before, D ** -0.5 if scale is None else scale,
-          workspace.data_ptr(), workspace.nbytes, out.data_ptr(),
-          0 if dev_status is None else dev_status.data_ptr(),
-          _raw_stream(stream, _current_device()))
-    return out
 
 
 def w4_attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets, group_offsets=None,
@@ -1244,9 +1026,9 @@ def w4_attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets, group_off
     layer's pages [P, page_size, Hkv, D]; sequences group_offsets[g] ..
     group_offsets[g + 1] share their first shared_lens[g] tokens, which are read
     once for the group.  scale defaults to 1 / sqrt(D).  Returns out [T, Hq, D]."""
-    return _attn("w4_attn_shared_prefix", lambda T: ((), (bool(causal),)), q, k_pages, v_pages,
-                 table, lens, q_offsets, group_offsets, shared_lens, max_q, scale, workspace, out,
-                 dev_status, stream)
+    return (_calls_module or _calls()).attn(q, k_pages, v_pages, table, lens, q_offsets, None, causal,
+                                            group_offsets, shared_lens, max_q, scale, workspace, out,
+                                            dev_status, stream)
 
 
 def w4_attn_tree(q, k_pages, v_pages, table, lens, q_offsets, tree, group_offsets=None,
@@ -1255,12 +1037,8 @@ def w4_attn_tree(q, k_pages, v_pages, table, lens, q_offsets, tree, group_offset
     """w4_attn_shared_prefix for trees of drafted tokens: bit j % 32 of word j // 32 of
     row t of tree [T, words] int32 tells whether query t sees its sequence's j-th new
     token; the older ones it sees all.  Returns out [T, Hq, D]."""
-    def masks(T):
-        _require_int32(tree)
-        if tree.dim() != 2 or tree.shape[0] != T:
-            raise ValueError("tree must be [T, words], a bit for each of max_q tokens in a row")
-        _on_current_device(q, k_pages, v_pages, table, lens, q_offsets, tree, group_offsets,
-                           shared_lens, workspace, out, dev_status)
-        return (tree.data_ptr(), tree.shape[1]), ()
-    return _attn("w4_attn_tree", masks, q, k_pages, v_pages, table, lens, q_offsets, group_offsets,
-                 shared_lens, max_q, scale, workspace, out, dev_status, stream)
+    if tree is None:
+        raise ValueError("tree must be [T, words], a bit for each of max_q tokens in a row")
+    return (_calls_module or _calls()).attn(q, k_pages, v_pages, table, lens, q_offsets, tree, False,
+                                            group_offsets, shared_lens, max_q, scale, workspace, out,
+                                            dev_status, stream)

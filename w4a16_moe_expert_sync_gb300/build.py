@@ -1,10 +1,15 @@
-"""Build libw4moe.so in-tree with nvcc for sm_103a (one -gencode, parallel TUs)."""
+"""Build libw4moe.so in-tree with nvcc for sm_103a (one -gencode, parallel TUs), and the
+module beside it that calls it with torch tensors."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
+import re
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -14,9 +19,10 @@ LIB = os.path.join(BUILD, "libw4moe.so")
 SOURCES = ["api.cu", "quantize.cu", "route_align.cu", "combine.cu", "grouped_gemm.cu",
            "static_scratch.cu", "rmsnorm.cu", "sampler.cu", "dense_gemm.cu",
            "few.cu", "kv.cu", "attention.cu", "rope.cu",
-           "linear_few.cu", "linear_few_wide.cu", "packed.cu"]
+           "linear_few.cu", "linear_few_wide.cu"]
 HEADERS = ["launch.h", "ptx.cuh", "korder.cuh", "combine_fold.cuh", "checks.cuh",
            "route_token.cuh", "attention_plan.cuh"]
+CALLS_SOURCE = os.path.join(CSRC, "calls.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -27,20 +33,30 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA library cannot be built")
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
+def calls_path() -> str:
+    """The module of csrc/calls.cpp: one for each version of torch, whose headers it takes."""
+    version = re.sub(r"\W", "_", importlib.metadata.version("torch"))
+    return os.path.join(BUILD, f"w4_calls_torch_{version}.so")
+
+
+def _stale(target: str, sources: list) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    deps += [os.path.join(ROOT, "include", "w4moe.h"), os.path.abspath(__file__)]
+    t = os.path.getmtime(target)
+    deps = sources + [os.path.join(ROOT, "include", "w4moe.h"), os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in deps)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every translation unit and link the shared library; returns its path."""
-    if not force and not ptxas_info and not _stale():
-        return LIB
-    return _compile(BUILD, LIB, [], verbose, ptxas_info)
+    """Compile every translation unit and link the shared library, and the module beside
+    it; returns the library's path."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        calls = ex.submit(_compile_calls) if force or _stale(calls_path(), [CALLS_SOURCE]) else None
+        if force or ptxas_info or _stale(LIB, [os.path.join(CSRC, f) for f in SOURCES + HEADERS]):
+            _compile(BUILD, LIB, [], verbose, ptxas_info)
+        if calls:
+            calls.result()
+    return LIB
 
 
 def build_checked(out_dir: str) -> str:
@@ -49,6 +65,27 @@ def build_checked(out_dir: str) -> str:
     store), built into out_dir for the tests; returns its path."""
     return _compile(out_dir, os.path.join(out_dir, "libw4moe_checked.so"), ["-DW4_CHECK_BOUNDS"],
                     False, False)
+
+
+def _compile_calls() -> None:
+    gxx = shutil.which("g++")
+    if not gxx:
+        raise RuntimeError("g++ not found: the module that calls the CUDA library cannot be built")
+    os.makedirs(BUILD, exist_ok=True)
+    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    includes = [os.path.join(torch, "include"), os.path.join(torch, "include/torch/csrc/api/include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    libs, out = os.path.join(torch, "lib"), calls_path()
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           *[x for i in includes for x in ("-isystem", i)], CALLS_SOURCE, "-o", tmp, "-L", libs,
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
+           f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
 
 
 def _compile(build_dir: str, lib: str, defines: list, verbose: bool, ptxas_info: bool) -> str:
