@@ -18,11 +18,14 @@
 // task meet in tensor memory, in a fixed order: bit-identical reruns.  Codes arrive by TMA, up
 // to 16 groups ahead.
 //
-// Measured on GB300, 2816 -> 262144: 16 tokens 73.5 us, 32 tokens 107 (393 and 409 MB, 58 and
+// Measured on GB300, 2816 -> 262144: 16 tokens 73.5 us, 32 tokens 99 (393 and 409 MB, 58 and
 // 60 us at the copy bandwidth).  With 32 tokens the activations leave room for four groups
-// only, whose round trip paces the loop (with all arithmetic taken out 86 us, with 16 tokens
-// 63); asking for the codes in L2 ahead of that changes nothing.  One warp for unpacking and
-// adding up: 130 and 150; a division by the slots or groups in each role's step: 124 and 142.
+// only, whose round trip takes 86 us with all arithmetic taken out (with 16 tokens 63), and the
+// roles' steps, each a chain of waits, take 0.34 us a group whatever the slots; asking for the
+// codes in L2 ahead changes nothing.  Others, 32 tokens: a thread adds up one row of all tokens
+// 107; a fifth slot 97, but for what it takes to tell the slot's turns 83 with 16 tokens; two CTAs
+// with half of the groups each, sums joined through the other's shared memory 162; one warp
+// for unpacking and adding up 150; a division by the slots or groups in each role's step 142.
 #include <algorithm>
 #include <atomic>
 #include <cuda_fp16.h>
@@ -41,7 +44,6 @@ constexpr int kGroup = 128;
 constexpr int kSlotBytes = kRows * kGroup / 2;
 // first warps of the roles behind the eight that unpack
 constexpr int kAdd = 8, kIssue = 16, kLoad = 18;
-constexpr int kThreads = 32 * 19;
 constexpr int kMaxSlots = 16;
 constexpr int kMaxSmem = 227 * 1024;
 
@@ -133,6 +135,13 @@ __device__ __forceinline__ void mma_group(uint32_t d, uint32_t a, uint64_t b, ui
 // TOK: tokens, 16 or 32.
 template <int TOK> struct Wide {
     static constexpr int kN = 2 * TOK;
+    // With 32 tokens the warps that add up take more than an even share of the registers: 256
+    // threads of 80, 256 of 128, 128 of 56 of the launch's 640 of 96 (104 us without; the last
+    // warp only completes its group of four).  With 16 tokens they need no more.
+    static constexpr bool kSplit = TOK == 32;
+    static constexpr int kThreads = 32 * (kSplit ? 20 : 19);
+    static constexpr int kUnpackRegs = 80, kAddRegs = 128, kOtherRegs = 56;
+    static constexpr int kSplitSum = 256 * kUnpackRegs + 256 * kAddRegs + 128 * kOtherRegs;
     static constexpr int kXBytes = kN * kGroup;            // a group's B
     static constexpr uint32_t kD = 128, kX = kD + 4 * kN;  // TMEM columns; A from 0 on
     static constexpr uint32_t kIdesc = idesc_f16_f32(128, kN);   // (e4m3: the same bits)
@@ -284,22 +293,36 @@ template <int TOK> struct Wide {
         __syncwarp();
     }
 
-    // 16 columns from t0 and 16 from t1 of this thread's lane.
-    static __device__ __forceinline__ void load_sums(uint32_t t0, uint32_t t1, uint32_t (&a)[16],
-                                                     uint32_t (&b)[16])
+    // 16 columns from t0 and 16 from t1, of 16 of the warp's lanes: a thread gets rows l / 4
+    // and l / 4 + 8 of them, columns 2 (l % 4) and the next of each 8: of a row in v[4 i + 2 r].
+    static __device__ __forceinline__ void load_sums(uint32_t t0, uint32_t t1, uint32_t (&a)[8],
+                                                     uint32_t (&b)[8])
     {
         asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
-            "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
-            "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
-            "tcgen05.wait::ld.sync.aligned;"
+            "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+            "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];"
             : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]),
-              "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]),
-              "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]),
-              "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]), "=r"(b[10]),
-              "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
+              "=r"(a[7]), "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]),
+              "=r"(b[6]), "=r"(b[7])
             : "r"(t0), "r"(t1)
+            : "memory");
+    }
+    static __device__ __forceinline__ void wait_loads(uint32_t (&a)[8], uint32_t (&b)[8])
+    {
+        // (what was loaded is not there before it)
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]),
+                       "+r"(a[6]), "+r"(a[7]), "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]),
+                       "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])
+                     :
+                     : "memory");
+    }
+    // 16 columns of 16 lanes in that layout.
+    static __device__ __forceinline__ void store_sums(uint32_t to, const float (&v)[8])
+    {
+        asm volatile(
+            "tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(to),
+            "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
             : "memory");
     }
 
@@ -343,16 +366,22 @@ template <int TOK> struct Wide {
         }
     }
 
-    // A warp that adds up 32 rows of set w's groups.
+    // A warp that adds up 32 rows of set w's groups.  A thread has 4 of the rows and a quarter of
+    // the tokens, so that it reads a quarter of the tokens' factors (a row of all tokens a thread:
+    // 16 reads of 16 bytes a group, the same for all lanes and four wavefronts each).  Its
+    // accumulators are in the order of load_sums, by 16 tokens and 16 rows.
     static __device__ void add(const WideArgs &p, Shared &s, const float *fs, int t0, int row0, int w,
                                int quarter, int lane, int total)
     {
         const uint32_t tmem = s.tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const int mine = quarter * 32 + lane;
-        uint64_t acc[TOK / 2];
+        uint64_t acc[TOK / 16][2][4];
+        auto clear = [&]() {
 #pragma unroll
-        for (int i = 0; i < TOK / 2; i++)
-            acc[i] = 0;
+            for (int i = 0; i < TOK / 2; i++)
+                acc[i / 8][i / 4 % 2][i % 4] = 0;
+        };
+        clear();
         // scales and zeros of the groups to come, four steps ahead
         constexpr int kAhead = 4;
         uint16_t sc[kAhead], ze[kAhead];
@@ -373,42 +402,60 @@ template <int TOK> struct Wide {
             if (idx >= total)
                 break;
             const int b = i & 1, g = at.g, task = at.task;
-            const float sv = __half2float(__ushort_as_half(sc[u]));
-            const float zv = __half2float(__ushort_as_half(ze[u]));
+            const uint32_t scale = sc[u] | static_cast<uint32_t>(ze[u]) << 16;
             scales(idx + 2 * kAhead, sc[u], ze[u]);
-            const uint64_t s2 = pair_of(sv, sv), z2 = pair_of(-zv, -zv);
+            uint64_t s2[4], z2[4];
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const uint32_t v = __shfl_sync(0xffffffffu, scale, 8 * r + (lane >> 2));
+                const float sv = __half2float(__ushort_as_half(static_cast<uint16_t>(v)));
+                const float zv = -__half2float(__ushort_as_half(static_cast<uint16_t>(v >> 16)));
+                s2[r] = pair_of(sv, sv);
+                z2[r] = pair_of(zv, zv);
+            }
             const uint64_t small = pair_of(0.03125f, 0.03125f);
-            const ulonglong2 *f = reinterpret_cast<const ulonglong2 *>(fs) + g * (TOK / 2);
+            const ulonglong2 *f =
+                reinterpret_cast<const ulonglong2 *>(fs) + g * (TOK / 2) + (lane & 3);
             if (!wait(p, s, &s.d_full[w][b], i >> 1 & 1))
                 return;
             tc_fence_after();
             __syncwarp();
+            uint32_t d1[2][8], d2[2][8];
+            const uint32_t d = tmem + kD + kN * (2 * w + b);
+            load_sums(d, d + TOK, d1[0], d2[0]);
 #pragma unroll
-            for (int c = 0; c < TOK; c += 16) {
-                uint32_t d1[16], d2[16];
-                const uint32_t at = tmem + kD + kN * (2 * w + b) + c;
-                load_sums(at, at + TOK, d1, d2);
-                if (c + 16 == TOK) {
+            for (int i = 0; i < TOK / 8; i++) {                // 16 tokens, 16 rows
+                const int c = i / 2, h = i % 2;
+                wait_loads(d1[h], d2[h]);
+                if (i + 1 < TOK / 8) {
+                    const uint32_t next = d + (i + 1) / 2 * 16 + (((i + 1) % 2 * 16) << 16);
+                    load_sums(next, next + TOK, d1[h ^ 1], d2[h ^ 1]);
+                } else {
                     tc_fence_before();
                     __syncwarp();
                     mbar_arrive_elect(&s.d_empty[w][b]);
                 }
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const ulonglong2 fv = f[c / 2 + j];    // two tokens' factors, their sums
-                    const uint64_t e1 = static_cast<uint64_t>(d1[2 * j + 1]) << 32 | d1[2 * j];
-                    const uint64_t e2 = static_cast<uint64_t>(d2[2 * j + 1]) << 32 | d2[2 * j];
-                    acc[c / 2 + j] = fma2(s2, fma2(fv.x, fma2(e2, small, e1), mul2(z2, fv.y)),
-                                          acc[c / 2 + j]);
+                for (int j = 0; j < 2; j++) {
+                    const ulonglong2 fv = f[c * 8 + j * 4];    // two tokens' factors, their sums
+#pragma unroll
+                    for (int r = 0; r < 2; r++) {
+                        const int at = 4 * j + 2 * r;
+                        const uint64_t e1 = static_cast<uint64_t>(d1[h][at + 1]) << 32 | d1[h][at];
+                        const uint64_t e2 = static_cast<uint64_t>(d2[h][at + 1]) << 32 | d2[h][at];
+                        uint64_t &to = acc[c][h][2 * j + r];
+                        to = fma2(s2[2 * h + r],
+                                  fma2(fv.x, fma2(e2, small, e1),
+                                       mul2(z2[2 * h + r], fv.y)),
+                                  to);
+                    }
                 }
             }
             at.next(p, 2);
             if (at.task != task) {                         // that was the set's last of the task
                 if (!finish(p, s, t0, row0 + task * kRows + mine, w, quarter, task, tmem, acc))
                     return;
-#pragma unroll
-                for (int j = 0; j < TOK / 2; j++)
-                    acc[j] = 0;
+                clear();
             }
         }
     }
@@ -416,7 +463,7 @@ template <int TOK> struct Wide {
     // A task's sums: the second set's through tensor memory to the first, which stores them.
     static __device__ __forceinline__ bool finish(const WideArgs &p, Shared &s, int t0, int row, int w,
                                                   int quarter, int done, uint32_t tmem,
-                                                  const uint64_t (&acc)[TOK / 2])
+                                                  const uint64_t (&acc)[TOK / 16][2][4])
     {
         uint32_t v[TOK];
         if (w == 1) {
@@ -426,8 +473,8 @@ template <int TOK> struct Wide {
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < TOK / 2; j++) {
-                v[2 * j] = static_cast<uint32_t>(acc[j]);
-                v[2 * j + 1] = static_cast<uint32_t>(acc[j] >> 32);
+                v[2 * j] = static_cast<uint32_t>(acc[j / 8][j / 4 % 2][j % 4]);
+                v[2 * j + 1] = static_cast<uint32_t>(acc[j / 8][j / 4 % 2][j % 4] >> 32);
             }
             if constexpr (TOK == 16)
                 tmem_st_32x32b_x16(tmem + kX, v);
@@ -447,13 +494,29 @@ template <int TOK> struct Wide {
             tmem_ld_32x32b_x16(tmem + kX, v);
         else
             tmem_ld_32x32b_x32(tmem + kX, v);
+        // from a thread's own values to its row's, for wider stores
+#pragma unroll
+        for (int i = 0; i < TOK / 8; i++) {
+            float sum[8];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const uint64_t mine = acc[i / 2][i % 2][j];
+                sum[2 * j] = low(mine) + __uint_as_float(v[8 * i + 2 * j]);
+                sum[2 * j + 1] = high(mine) + __uint_as_float(v[8 * i + 2 * j + 1]);
+            }
+            store_sums(tmem + kX + i / 2 * 16 + ((i % 2 * 16) << 16), sum);
+        }
+        tmem_wait_st();
+        if constexpr (TOK == 16)
+            tmem_ld_32x32b_x16(tmem + kX, v);
+        else
+            tmem_ld_32x32b_x32(tmem + kX, v);
         tc_fence_before();
         __syncwarp();
         mbar_arrive_elect(&s.x_empty[quarter]);
 #pragma unroll
         for (int j = 0; j < TOK / 2; j++) {
-            const uint32_t r = bf16_pair(low(acc[j]) + __uint_as_float(v[2 * j]),
-                                         high(acc[j]) + __uint_as_float(v[2 * j + 1]));
+            const uint32_t r = bf16_pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
             const int t = t0 + 2 * j;
             uint16_t *y = p.y + static_cast<int64_t>(t) * p.N + row;
             if (row < p.N && t < p.M)
@@ -468,7 +531,7 @@ template <int TOK> struct Wide {
 
 // CTA (share, part): its share of the tasks, for the part's TOK tokens.
 template <int TOK>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Wide<TOK>::kThreads, 1)
     few_linear_wide_kernel(const __grid_constant__ WideArgs p, int parts)
 {
     using W = Wide<TOK>;
@@ -519,18 +582,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     typename W::Place place{0, 0, 0, 0};
     if (warp == kLoad) {
         W::load(p, s, ring, row0, lane, place, 0, ahead);
-    } else {
+    } else if (warp < kLoad) {
         W::stage(p, t0, xs, fs, warp, lane);
         fence_proxy_async_smem();
     }
     __syncthreads();
+    if constexpr (W::kSplit) {
+        if (warp < kAdd)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kUnpackRegs));
+        else if (warp < kIssue)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(W::kAddRegs));
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kOtherRegs));
+    }
     if (warp < kAdd) {
         W::unpack(p, s, ring, warp >> 2, warp & 3, lane, total);
     } else if (warp < kIssue) {
         W::add(p, s, fs, t0, row0, (warp - kAdd) >> 2, warp & 3, lane, total);
     } else if (warp < kLoad) {
         W::issuer(p, s, xs, warp - kIssue, total);
-    } else {
+    } else if (warp == kLoad) {
         const int i = W::load(p, s, ring, row0, lane, place, ahead, total);
         // every copy requested has landed, or had its time to: of a slot only the last can be
         // under way
@@ -580,13 +651,20 @@ cudaError_t launch_as(WideArgs &a, int sms, int dev, cudaStream_t stream)
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 2048);
         if (err != cudaSuccess)
             return err;
+        if (Wide<TOK>::kSplit) {               // what setmaxnreg shares out is there
+            cudaFuncAttributes attr;
+            if ((err = cudaFuncGetAttributes(&attr, kern)) != cudaSuccess)
+                return err;
+            if (attr.numRegs * Wide<TOK>::kThreads < Wide<TOK>::kSplitSum)
+                return cudaErrorLaunchOutOfResources;
+        }
         raised.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
     }
     a.slots = slots_of(a.groups, TOK);
     const int parts = (a.M + TOK - 1) / TOK, tasks = (a.N + kRows - 1) / kRows;
     const int shares = std::min(tasks, std::max(sms / parts, 1));
     const int smem = Wide<TOK>::fixed_bytes(a.groups) + a.slots * kSlotBytes;
-    return launch_pdl(kern, dim3(shares * parts), dim3(kThreads), smem, stream, a, parts);
+    return launch_pdl(kern, dim3(shares * parts), dim3(Wide<TOK>::kThreads), smem, stream, a, parts);
 }
 
 }  // namespace
