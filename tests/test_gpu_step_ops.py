@@ -192,3 +192,53 @@ def test_each_reads_what_the_one_before_wrote(lib):
     for _ in range(3):
         got = run(lambda: None)
         assert all(torch.equal(a, b) for p, q in zip(got, want) for a, b in zip(p, q))
+
+
+def test_from_two_threads(lib):
+    """Two threads with a stream each, the same inputs: the same results as alone."""
+    import threading
+    import torch
+    d = _setup()
+    calls = _calls(lib, d)
+    names = ("linear", "wide", "rope", "tree")
+    want = {n: [t.clone() for t in _list(calls[n]())] for n in names}
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    got = {n: _list(calls[n]()) for n in names}
+                    torch.cuda.current_stream().synchronize()
+                    wrong.extend(n for n in names
+                                 if not all(torch.equal(a, b) for a, b in zip(got[n], want[n])))
+        except Exception as e:                 # noqa: BLE001 (shown by the assertion)
+            wrong.append(repr(e))
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_results_are_ordinary_tensors(lib):
+    """In inference mode too, and of inputs that ask for gradients (none is given)."""
+    import torch
+    d = _setup()
+    calls = _calls(lib, d)
+    want = calls["linear"]()
+    assert not want.requires_grad and want.device == d["x"].device and want.is_contiguous()
+    with torch.inference_mode():
+        got = calls["linear"]()
+        assert got.is_inference() and torch.equal(got.clone(), want)
+    x = d["x"].clone().requires_grad_()
+    got = lib.w4_w4a16_linear_few(x, d["q"], d["s"], d["z"])
+    assert not got.requires_grad and torch.equal(got, want)
+    w = torch.nn.Parameter(torch.ones(3, device="cuda", dtype=torch.bfloat16))
+    (got[:, :3] * w).sum().backward()
+    assert w.grad is not None
+    with pytest.raises(lib.W4Error, match="M <= 32"):
+        lib.w4_w4a16_linear_few(torch.zeros((33, 1024), device="cuda").bfloat16(), d["q"], d["s"],
+                                d["z"])

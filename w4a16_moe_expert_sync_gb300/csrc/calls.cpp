@@ -364,9 +364,9 @@ int batch(const Tensor &table, const Tensor &lens, const Tensor &q_offsets)
 PyObject *kv_append_rope(PyObject *const *a)
 {
     const Tensor &kp = tensor(a[0]), &vp = tensor(a[1]), &table = tensor(a[2]), &lens = tensor(a[3]);
-    const RopeInputs r = rope_inputs(a[4], a[5], a[8], a[9], a[10], a[11]);
     const Tensor &v = tensor(a[6]), &q_offsets = tensor(a[7]);
     const Tensor *status = optional(a[16]);
+    const RopeInputs r = rope_inputs(a[4], a[5], a[8], a[9], a[10], a[11]);
     const float eps = number(a[12]), amplitude = number(a[14]);
     const bool interleaved = truth(a[13]);
     if (kp.scalar_type() != r.q.scalar_type() || vp.scalar_type() != r.q.scalar_type() ||
