@@ -18,7 +18,7 @@
 // task meet in tensor memory, in a fixed order: bit-identical reruns.  Codes arrive by TMA, up
 // to 16 groups ahead.
 //
-// Measured on GB300, 2816 -> 262144: 16 tokens 73.5 us, 32 tokens 99 (393 and 409 MB, 58 and
+// Measured on GB300, 2816 -> 262144: 16 tokens 73.5 us, 32 tokens 97 (393 and 409 MB, 58 and
 // 60 us at the copy bandwidth).  With 32 tokens the activations leave room for four groups
 // only, whose round trip takes 86 us with all arithmetic taken out (with 16 tokens 63), and the
 // roles' steps, each a chain of waits, take 0.34 us a group whatever the slots; asking for the
@@ -136,7 +136,7 @@ __device__ __forceinline__ void mma_group(uint32_t d, uint32_t a, uint64_t b, ui
 template <int TOK> struct Wide {
     static constexpr int kN = 2 * TOK;
     // With 32 tokens the warps that add up take more than an even share of the registers: 256
-    // threads of 80, 256 of 128, 128 of 56 of the launch's 640 of 96 (104 us without; the last
+    // threads of 80, 256 of 128, 128 of 56 of the launch's 640 of 96 (107 us without; the last
     // warp only completes its group of four).  With 16 tokens they need no more.
     static constexpr bool kSplit = TOK == 32;
     static constexpr int kThreads = 32 * (kSplit ? 20 : 19);
@@ -382,28 +382,23 @@ template <int TOK> struct Wide {
                 acc[i / 8][i / 4 % 2][i % 4] = 0;
         };
         clear();
-        // scales and zeros of the groups to come, four steps ahead
-        constexpr int kAhead = 4;
-        uint16_t sc[kAhead], ze[kAhead];
+        // scale and zero of the group to come.  (Further ahead, the loop unrolled for it, costs
+        // more than it hides: the roles' code together is more than the instruction cache
+        // holds.  4 ahead 98 us, 6 ahead 106.)
         Place to{0, w, w, 0}, at = to;
-        auto scales = [&](int idx, uint16_t &sv, uint16_t &zv) {
+        uint16_t sc, ze;
+        auto scales = [&](int idx) {
             const int64_t row = min(row0 + to.task * kRows + mine, p.N - 1);
-            sv = idx < total ? load_weight(p.s + row * p.groups + to.g) : static_cast<uint16_t>(0);
-            zv = idx < total ? load_weight(p.z + row * p.groups + to.g) : static_cast<uint16_t>(0);
+            sc = idx < total ? load_weight(p.s + row * p.groups + to.g) : static_cast<uint16_t>(0);
+            ze = idx < total ? load_weight(p.z + row * p.groups + to.g) : static_cast<uint16_t>(0);
             to.next(p, 2);
         };
-#pragma unroll
-        for (int i = 0; i < kAhead; i++)
-            scales(w + 2 * i, sc[i], ze[i]);
-        for (int idx0 = w, i0 = 0; idx0 < total; idx0 += 2 * kAhead, i0 += kAhead)
-#pragma unroll
-        for (int u = 0; u < kAhead; u++) {
-            const int idx = idx0 + 2 * u, i = i0 + u;
-            if (idx >= total)
-                break;
+        scales(w);
+#pragma unroll 1
+        for (int idx = w, i = 0; idx < total; idx += 2, i++) {
             const int b = i & 1, g = at.g, task = at.task;
-            const uint32_t scale = sc[u] | static_cast<uint32_t>(ze[u]) << 16;
-            scales(idx + 2 * kAhead, sc[u], ze[u]);
+            const uint32_t scale = sc | static_cast<uint32_t>(ze) << 16;
+            scales(idx + 2);
             uint64_t s2[4], z2[4];
 #pragma unroll
             for (int r = 0; r < 4; r++) {
