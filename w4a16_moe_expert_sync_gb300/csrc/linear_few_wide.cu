@@ -70,6 +70,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
 {
     uint64_t r;
@@ -166,62 +172,77 @@ template <int TOK> struct Wide {
     }
 
     // The activations of tokens t0 .. t0 + TOK as B of every group, and for each two tokens
-    // (2^(9 - e), 2^(9 - e), sum x, sum x).  16 lanes have a token's group, 8 values each, in
+    // (2^(9 - e), 2^(9 - e), sum x, sum x).  8 lanes have a token's group, 16 values each, in
     // the order of the unpacked codes (0 2 4 6 1 3 5 7).
     static __device__ void stage(const WideArgs &p, int t0, uint8_t *xs, float *fs, int warp, int lane)
     {
-        constexpr int kBatch = 4, kWarps = kLoad;
-        const int items = p.groups * TOK, sub = lane >> 4, l = lane & 15;
-        for (int i0 = warp * 2 * kBatch; i0 < items; i0 += kWarps * 2 * kBatch) {
-            uint4 v[kBatch];
+        constexpr int kBatch = 2, kWarps = kLoad;
+        const int items = p.groups * TOK, sub = lane >> 3, l = lane & 7;
+        const uint64_t minus = pair_of(-1.0f, -1.0f), widen = pair_of(32.0f, 32.0f);
+#pragma unroll 1
+        for (int i0 = warp * 4 * kBatch; i0 < items; i0 += kWarps * 4 * kBatch) {
+            uint4 v[kBatch][2];
 #pragma unroll
             for (int u = 0; u < kBatch; u++) {
-                const int i = i0 + 2 * u + sub, tok = i % TOK, t = t0 + tok;
-                v[u] = make_uint4(0, 0, 0, 0);
-                if (i < items && t < p.M)
-                    v[u] = *reinterpret_cast<const uint4 *>(
-                        p.x + static_cast<int64_t>(t) * p.K + i / TOK * kGroup + l * 8);
+                const int i = i0 + 4 * u + sub, tok = i % TOK, t = t0 + tok;
+                v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
+                if (i < items && t < p.M) {
+                    const uint4 *x = reinterpret_cast<const uint4 *>(
+                        p.x + static_cast<int64_t>(t) * p.K + i / TOK * kGroup + l * 16);
+                    v[u][0] = x[0];
+                    v[u][1] = x[1];
+                }
             }
 #pragma unroll
             for (int u = 0; u < kBatch; u++) {
-                const int i = i0 + 2 * u + sub, tok = i % TOK, g = i / TOK;
-                const uint32_t in[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-                float f[8], sum = 0.0f;
-                uint32_t top = 0;              // magnitudes compare as integers
+                const int i = i0 + 4 * u + sub, tok = i % TOK, g = i / TOK;
+                const uint32_t in[8] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w,
+                                        v[u][1].x, v[u][1].y, v[u][1].z, v[u][1].w};
+                float f[16];
+                uint64_t sums = 0;
+                uint32_t tops = 0;             // magnitudes compare as integers
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
+                for (int e = 0; e < 8; e++) {
                     f[2 * e] = __uint_as_float(in[e] << 16);
                     f[2 * e + 1] = __uint_as_float(in[e] & 0xFFFF0000u);
-                    top = max(top, max((in[e] << 16) & 0x7FFFFFFFu, in[e] & 0x7FFF0000u));
-                    sum += f[2 * e] + f[2 * e + 1];
+                    tops = __vmaxu2(tops, in[e] & 0x7FFF7FFFu);
+                    sums = add2(sums, pair_of(f[2 * e], f[2 * e + 1]));
                 }
+                float sum = low(sums) + high(sums);
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1) {
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                for (int o = 4; o > 0; o >>= 1) {
+                    tops = __vmaxu2(tops, __shfl_xor_sync(0xffffffffu, tops, o));
                     sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 }
+                const uint32_t top = max(tops & 0xFFFFu, tops >> 16);
                 // the largest becomes 2^7 .. 2^8 (below 2^-120 less, for 2^e has to be a number)
-                const int e = min(max(134 - static_cast<int>(top >> 23), -118), 127);
+                const int e = min(max(134 - static_cast<int>(top >> 7), -118), 127);
                 const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-                uint32_t part[2][4];
+                const uint64_t up2 = pair_of(up, up);
+                uint32_t out[2][4];
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    const int a = (j & 1) * 4 + (j >> 1);              // values a and a + 2
-                    const float v0 = f[a] * up, v1 = f[a + 2] * up;
-                    part[0][j] = to_e4m3(v0, v1);
-                    const float2 back = from_e4m3(part[0][j]);
-                    part[1][j] = to_e4m3((v0 - back.x) * 32.0f, (v1 - back.y) * 32.0f);
+                    // words of values 0 2 4 6, 1 3 5 7 and the same of the next eight
+                    uint32_t part[2][2];
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const int a = (j >> 1) * 8 + (j & 1) + 4 * h;
+                        const uint64_t y = mul2(pair_of(f[a], f[a + 2]), up2);
+                        part[0][h] = to_e4m3(low(y), high(y));
+                        const float2 back = from_e4m3(part[0][h]);
+                        const uint64_t rest = mul2(fma2(pair_of(back.x, back.y), minus, y), widen);
+                        part[1][h] = to_e4m3(low(rest), high(rest));
+                    }
+                    out[0][j] = part[0][0] | part[0][1] << 16;
+                    out[1][j] = part[1][0] | part[1][1] << 16;
                 }
                 if (i >= items)
                     continue;
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
                     const int n = h * TOK + tok;
-                    // j = 0, 2: values 0 2, 1 3; j = 1, 3: 4 6, 5 7
-                    const uint2 out = make_uint2(part[h][0] | part[h][1] << 16,
-                                                 part[h][2] | part[h][3] << 16);
-                    *reinterpret_cast<uint2 *>(xs + g * kXBytes + n * 128 +
-                                               (((l >> 1) ^ (n & 7)) << 4) + (l & 1) * 8) = out;
+                    *reinterpret_cast<uint4 *>(xs + g * kXBytes + n * 128 + ((l ^ (n & 7)) << 4)) =
+                        make_uint4(out[h][0], out[h][1], out[h][2], out[h][3]);
                 }
                 if (l == 0) {
                     float *to = fs + (g * (TOK / 2) + (tok >> 1)) * 4 + (tok & 1);
