@@ -392,10 +392,13 @@ __global__ void __launch_bounds__(32 * NW, 1) few_linear_kernel(const FewLinearA
 }
 
 constexpr int kMaxSmem = 227 * 1024;
-// Rows an SM from which on linear_few_wide.cu is taken for more than 8 tokens: two tasks of
-// 128.  (Here and there, groups of 128, us: K 2816, 16 tokens: 19456 rows 11.6 and 12.6, 38912
-// 18.1 and 17.4, 116736 42 and 36; 32 tokens 16.7 and 18.1, 28.1 and 24.7, 73.5 and 51.7.)
-constexpr int kWideRows = 256;
+// Rows from which on linear_few_wide.cu is taken for more than 8 tokens: a task of 128 for each
+// SM, two where K is short and the tasks are over soon.  (Here and there, groups of 128, us, 16
+// tokens: K 1024, 19456 rows 6.2 and 6.2, 29184 7.2 and 8.1, 77824 12.3 and 12.2; K 2816,
+// 14592 10.1 and 10.6, 19456 11.7 and 10.9, 29184 15.8 and 16.1; K 5632, 19456 26.0 and 21.5.
+// 32 tokens: K 1024, 19456 8.0 and 8.3; K 2816, 19456 16.7 and 15.3, 29184 23.2 and 21.6; K 5632,
+// 14592 34.4 and 30.0.  8 tokens: K 2816, 19456 9.0 and 10.9, 262144 68.3 and 66.6.)
+constexpr int wide_rows(int K) { return K >= 2048 ? 128 : 256; }
 
 template <class F> constexpr int smem_of(int blocks, int nt)
 {
@@ -451,7 +454,7 @@ cudaError_t launch_few_linear(const FewLinearProblem &q, cudaStream_t stream)
         err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (err != cudaSuccess)
         return err;
-    if (q.N >= kWideRows * sms && few_linear_wide_tokens(q.M, q.K, q.group) > 0)
+    if (q.N >= wide_rows(q.K) * sms && few_linear_wide_tokens(q.M, q.K, q.group) > 0)
         return launch_few_linear_wide(q, stream);
     FewLinearArgs a{};
     a.x = q.x;
