@@ -18,14 +18,16 @@
 // task meet in tensor memory, in a fixed order: bit-identical reruns.  Codes arrive by TMA, up
 // to 16 groups ahead.
 //
-// Measured on GB300, 2816 -> 262144: 16 tokens 73.5 us, 32 tokens 97 (393 and 409 MB, 58 and
+// Measured on GB300, 2816 -> 262144: 16 tokens 68 us, 32 tokens 94 (393 and 409 MB, 58 and
 // 60 us at the copy bandwidth).  With 32 tokens the activations leave room for four groups
 // only, whose round trip takes 86 us with all arithmetic taken out (with 16 tokens 63), and the
 // roles' steps, each a chain of waits, take 0.34 us a group whatever the slots; asking for the
-// codes in L2 ahead changes nothing.  Others, 32 tokens: a thread adds up one row of all tokens
-// 107; a fifth slot 97, but for what it takes to tell the slot's turns 83 with 16 tokens; two CTAs
-// with half of the groups each, sums joined through the other's shared memory 162; one warp
-// for unpacking and adding up 150; a division by the slots or groups in each role's step 142.
+// codes in L2 ahead changes nothing.  Others, 32 tokens, step by step: one warp for unpacking and
+// adding up 150, a division by the slots or groups in each role's step 142, a thread adds up one
+// row of all tokens 107, the adding loop unrolled four times 99, activations laid out 8 values a
+// lane instead of 16 97; a fifth slot 1 to 2 less, but for what it takes to tell the slot's turns
+// 83 with 16 tokens instead of 73; two CTAs with half of the groups each, sums joined through the
+// other's shared memory 162.
 #include <algorithm>
 #include <atomic>
 #include <cuda_fp16.h>
