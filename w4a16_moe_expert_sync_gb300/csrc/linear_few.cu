@@ -17,7 +17,7 @@
 // A task is 16 RT weight rows, a unit 128 codes of each.  A CTA has up to 8 NT of the
 // tokens and an equal contiguous share of the tasks, its warps equal shares of those
 // tasks' units; a task that crosses warps is added up in warp order through shared
-// memory.  A lane copies the codes that it will use itself into its own ring in shared
+// memory.  A warp copies the codes that it will use itself into its own ring in shared
 // memory, S units ahead, and waits for nobody else's.  Sums run in a fixed order:
 // bit-identical reruns.
 //
@@ -69,16 +69,10 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
     return r;
 }
 
-template <int BYTES>
 __device__ __forceinline__ void copy_async(void *to, const void *from)
 {
-    static_assert(BYTES == 8 || BYTES == 16);
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
-                     : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(to)), "l"(from)
-                     : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
+                 : "memory");
 }
 
 __device__ __forceinline__ float half_of(uint16_t h) { return __half2float(__ushort_as_half(h)); }
@@ -104,7 +98,14 @@ struct FewLinear {
         uint16_t sz[RT][kGroups];
     };
 
-    // Requests a unit: the lane's codes of rows 2 g and 2 g + 1 into its 32 RT bytes of the slot.
+    // Where a unit's half (a group of 64) of the rows of lanes g lies in their 64 bytes: other
+    // rows' other way round, so that eight bytes of four rows have banks of their own.
+    static __device__ __forceinline__ int half_at(int g, int h) { return (h ^ (g >> 1 & 1)) * 32; }
+
+    // Requests a unit: the codes of rows 2 g and 2 g + 1 into the slot, 16 bytes a lane and row.
+    // With groups of 128 they are the lane's own; with groups of 64 two lanes have 8 of them
+    // each, and the warp waits for one another.  (Copies of 8 bytes, each lane's own, go
+    // through what is left of L1: 5632 -> 38912 73 us.)
     static __device__ __forceinline__ void load(const FewLinearArgs &p, int64_t row0, int block,
                                                 int lane, uint8_t *slot, Unit &u)
     {
@@ -117,14 +118,14 @@ struct FewLinear {
 #pragma unroll
             for (int i = 0; i < 2; i++) {
                 const uint8_t *q = p.q + min(row + i, last) * (p.K / 2) + block * 64;
-                uint8_t *to = slot + (r * 2 + i) * 512 + lane * 16;
+                uint8_t *to = slot + (r * 2 + i) * 512 + g * 64;
                 if constexpr (GROUP == 128) {
-                    copy_async<16>(to, q + t4 * 16);
+                    copy_async(to + t4 * 16, q + t4 * 16);
                 } else {
-                    copy_async<8>(to, q + t4 * 8);
                     // of half a unit at the end the first half stands for the second,
                     // whose scales are zero
-                    copy_async<8>(to + 8, q + (block * 2 + 1 < G ? 32 : 0) + t4 * 8);
+                    const int c = block * 2 + 1 < G ? t4 : t4 & 1;
+                    copy_async(to + half_at(g, t4 >> 1) + (t4 & 1) * 16, q + c * 16);
                 }
             }
 #pragma unroll
@@ -139,14 +140,23 @@ struct FewLinear {
                                                int block, int lane, const uint8_t *slot,
                                                const Unit &u, float (&acc)[RT][NT][4])
     {
-        const int t4 = lane & 3;
+        const int g = lane >> 2, t4 = lane & 3;
         uint32_t q[RT][2][4];
 #pragma unroll
         for (int r = 0; r < RT; r++)
 #pragma unroll
-            for (int i = 0; i < 2; i++)
-                *reinterpret_cast<uint4 *>(q[r][i]) =
-                    *reinterpret_cast<const uint4 *>(slot + (r * 2 + i) * 512 + lane * 16);
+            for (int i = 0; i < 2; i++) {
+                const uint8_t *row = slot + (r * 2 + i) * 512 + g * 64;
+                if constexpr (GROUP == 128) {
+                    *reinterpret_cast<uint4 *>(q[r][i]) =
+                        *reinterpret_cast<const uint4 *>(row + t4 * 16);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; h++)
+                        *reinterpret_cast<uint2 *>(q[r][i] + 2 * h) =
+                            *reinterpret_cast<const uint2 *>(row + half_at(g, h) + t4 * 8);
+                }
+            }
 #pragma unroll
         for (int h = 0; h < kGroups; h++) {
             float part[RT][NT][4] = {};
@@ -338,7 +348,11 @@ __global__ void __launch_bounds__(32 * NW, 1) few_linear_kernel(const FewLinearA
         for (int i = 0; i < S; i++) {
             if (u < u1) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+                if constexpr (GROUP == 64)
+                    __syncwarp();              // other lanes' copies
                 F::add(xs, tile_stride, p.blocks, block, lane, ring + i * (RT * 1024), unit[i], acc);
+                if constexpr (GROUP == 64)
+                    __syncwarp();              // and reads
                 request(i);
                 u++;
                 if (++block == p.blocks) {
