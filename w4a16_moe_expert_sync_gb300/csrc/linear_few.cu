@@ -406,6 +406,12 @@ __global__ void __launch_bounds__(32 * NW, 1) few_linear_kernel(const FewLinearA
 }
 
 constexpr int kMaxSmem = 227 * 1024;
+// Up to here 60 KB are left of L1, in which scales and zeros stay, two bytes a row and group,
+// until the rest of their sectors is used; above it 28.  (1 token, 38912 rows, us: groups of 128
+// <1, 2, 16, 3> and <1, 2, 16, 2>, K 5632 28.3 and 24.5, K 7040 40.6 and 30.8; <1, 2, 16, 2> and
+// <1, 1, 16, 3>, K 8192 45.4 and 42.1; groups of 64 <1, 2, 16, 3> and <1, 1, 16, 2>, K 4096 30.8 and
+// 33.0, K 5632 44.8 and 29.8, K 7040 59.9 and 37.9, K 8192 73.4 and 63.0.)
+constexpr int kRoomySmem = 195 * 1024;
 // Rows from which on linear_few_wide.cu is taken for more than 8 tokens: a task of 128 for each
 // SM, two where K is short and the tasks are over soon.  (Here and there, groups of 128, us, 16
 // tokens: K 1024, 19456 rows 6.2 and 6.2, 29184 7.2 and 8.1, 77824 12.3 and 12.2; K 2816,
@@ -451,10 +457,14 @@ cudaError_t launch_few_linear_group(const FewLinearArgs &a, int sms, int dev, cu
     const bool many = a.N >= 64 * sms;
     if (tiles > 1 && many && smem_of<FewLinear<GROUP, 2, 2, 16, 2>>(a.blocks, 2) <= kMaxSmem)
         return launch_few_linear_as<GROUP, 2, 2, 16, 2>(a, sms, dev, stream);
-    if (many && smem_of<FewLinear<GROUP, 1, 2, 16, 3>>(a.blocks, 1) <= kMaxSmem)
+    if (many && smem_of<FewLinear<GROUP, 1, 2, 16, 3>>(a.blocks, 1) <= kRoomySmem)
         return launch_few_linear_as<GROUP, 1, 2, 16, 3>(a, sms, dev, stream);
-    if (smem_of<FewLinear<GROUP, 1, 1, 16, 4>>(a.blocks, 1) <= kMaxSmem)
+    if (GROUP == 128 && many && smem_of<FewLinear<GROUP, 1, 2, 16, 2>>(a.blocks, 1) <= kRoomySmem)
+        return launch_few_linear_as<GROUP, 1, 2, 16, 2>(a, sms, dev, stream);
+    if (!many && smem_of<FewLinear<GROUP, 1, 1, 16, 4>>(a.blocks, 1) <= kRoomySmem)
         return launch_few_linear_as<GROUP, 1, 1, 16, 4>(a, sms, dev, stream);
+    if (GROUP == 128 && smem_of<FewLinear<GROUP, 1, 1, 16, 3>>(a.blocks, 1) <= kRoomySmem)
+        return launch_few_linear_as<GROUP, 1, 1, 16, 3>(a, sms, dev, stream);
     return launch_few_linear_as<GROUP, 1, 1, 16, 2>(a, sms, dev, stream);
 }
 
