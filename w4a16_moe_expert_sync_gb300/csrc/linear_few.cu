@@ -23,10 +23,12 @@
 //
 // Measured on GB300 from a graph: 1 token, 2816 -> 4096: 4.4 us (latency: launch, the
 // activations' way to shared memory, one round of copies, the warps' sums; 0.9 for the
-// bytes); 11 tokens, 704 -> 2815, groups of 64: 3.2; 8 tokens, 2816 -> 262144: 74 (60 at the
-// copy bandwidth).  With 16 tokens there it is 85, the MMAs (2 cycles each an SM) and the
-// unpacking at some 45 % of their rates each; codes requested into registers instead of the
-// ring: 87 and 101, and 7 for the small ones.
+// bytes); 11 tokens, 704 -> 2815, groups of 64: 3.1; 8 tokens, 2816 -> 262144: 68 to 74 (60 at
+// the copy bandwidth), 8192 -> 38912 43 (25), with groups of 64 64 (27): the scales' sectors, and
+// where the activations take most of shared memory little is in flight.  With 16 tokens the
+// MMAs (2 cycles each an SM) and the unpacking are at some 45 % of their rates each (2816 ->
+// 262144 85); codes requested into registers instead of the ring: 87 and 101, and 7 for the
+// small ones.
 #include <algorithm>
 #include <atomic>
 #include <cuda_fp16.h>
