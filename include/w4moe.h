@@ -530,11 +530,12 @@ int w4_w4a16_linear(const uint16_t *x, int M, int K, int N, const uint8_t *q, co
  *   x          [M, K] bf16 in
  *   q          [N, K/2] uint8, w4_quantize's layout; s, z [N, K/group] fp16
  *   y          [M, N] bf16 out
- * Codes enter the tensor cores exactly, and so do activations (with more than 8 tokens,
- * 128 rows an SM and groups of 128: but for 2^-22 of their group's largest); a group's scale
+ * Codes enter the tensor cores exactly, and so do activations (with more than 8 tokens
+ * and 128 rows an SM: but for 2^-22 of their group's largest); a group's scale
  * and zero are applied to its fp32 sum, and y is rounded once.  (Activations of 2^57 and
- * more, or not finite, make their token's results so.)  dev_status may be NULL.  A token's results depend on neither the
- * other tokens' values nor where it stands among as many; bit-identical reruns.
+ * more, or not finite, make their token's results so.)  A token's results depend on
+ * neither the other tokens' values nor where it stands among as many; bit-identical
+ * reruns.  dev_status may be NULL.
  * Requires M <= 32, group 64 or 128 dividing K, K up to 11,264, N * K below 2^33,
  * N below 2^30, x and q 16-byte aligned, y 4-byte, s and z 2-byte aligned.  M = 0 or N = 0
  * does nothing.

@@ -75,6 +75,28 @@ def test_many_rows(lib, M, K, N):
 
 
 @gpu
+@pytest.mark.parametrize("M,K,N", [
+    (9, 512, 77900), (16, 2816, 38912), (32, 2816, 39040), (13, 5632, 19456), (25, 5120, 20001),
+    (32, 640, 80007), (11, 704, 80000), (17, 8192, 19456)])
+def test_many_rows_groups_of_64(lib, M, K, N):
+    """Two groups a step of the tensor memory, where K is whole steps and the activations
+    fit; groups of zeros, large values, small ones and zeros of the weights among them."""
+    import torch
+    x, q, s, z = _inputs(M, K, N, 64, M + K)
+    x[1, 64:128], x[2, 5], x[3, 192:256] = 0.0, 3000.0, x[3, 192:256] * 2.0 ** -12
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = lib.w4_w4a16_linear_few(x, q, s, z, 64, dev_status=status)
+    _check(y, x, q, s, z, 64)
+    for _ in range(20):
+        assert torch.equal(lib.w4_w4a16_linear_few(x, q, s, z, 64), y)
+    assert int(status) == 0
+    # a token by itself among as many, and scaled by a power of two
+    one = torch.zeros_like(x)
+    one[4] = x[4] * 0.25
+    assert torch.equal(lib.w4_w4a16_linear_few(one, q, s, z, 64)[4], y[4] * 0.25)
+
+
+@gpu
 @pytest.mark.parametrize("M", [12, 30])
 def test_many_rows_and_odd_activations(lib, M):
     """Groups of zeros, one large value among small ones, subnormals, what is not finite,

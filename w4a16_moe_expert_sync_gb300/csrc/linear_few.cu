@@ -420,7 +420,14 @@ constexpr int kRoomySmem = 195 * 1024;
 // 14592 10.1 and 10.6, 19456 11.7 and 10.9, 29184 15.8 and 16.1; K 5632, 19456 26.0 and 21.5.
 // 32 tokens: K 1024, 19456 8.0 and 8.3; K 2816, 19456 16.7 and 15.3, 29184 23.2 and 21.6; K 5632,
 // 14592 34.4 and 30.0.  8 tokens: K 2816, 19456 9.0 and 10.9, 262144 68.3 and 66.6.)
-constexpr int wide_rows(int K) { return K >= 2048 ? 128 : 256; }
+// With groups of 64 a step there has twice the sums to add up: the same rows only where K is
+// too long for two tiles of tokens here.  (16 tokens: K 1024, 38912 rows 8.9 and 9.8, 131072 22.1
+// and 21.4; K 2816, 29184 16.2 and 18.6, 38912 19.6 and 18.9, 131072 54.5 and 48.2; K 5632, 19456
+// 29.3 and 25.1, 38912 52.2 and 39.9; 32 tokens 98.0 and 71.1.)
+constexpr int wide_rows(int K, int group)
+{
+    return group == 128 ? (K >= 2048 ? 128 : 256) : K >= 4096 ? 128 : K >= 2048 ? 256 : 512;
+}
 
 template <class F> constexpr int smem_of(int blocks, int nt)
 {
@@ -480,7 +487,7 @@ cudaError_t launch_few_linear(const FewLinearProblem &q, cudaStream_t stream)
         err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (err != cudaSuccess)
         return err;
-    if (q.N >= wide_rows(q.K) * sms && few_linear_wide_tokens(q.M, q.K, q.group) > 0)
+    if (q.N >= wide_rows(q.K, q.group) * sms && few_linear_wide_tokens(q.M, q.K, q.group) > 0)
         return launch_few_linear_wide(q, stream);
     FewLinearArgs a{};
     a.x = q.x;

@@ -1,6 +1,6 @@
 // linear_few_wide.cu -- the W4A16 linear for 9 to 32 tokens and many rows, on tcgen05:
 //   y[t, n] = sum_g s[n, g] (sum_{k in g} q[n, k] x[t, k] - z[n, g] sum_{k in g} x[t, k])
-// for groups of 128.  linear_few.cu is the plain form of it; beyond 8 tokens its warps'
+// for groups of 128, or of 64 by twos.  linear_few.cu is the plain form of it; beyond 8 tokens its warps'
 // MMAs and the unpacking of the codes for them take longer than the weights' way from HBM.
 //
 // A nibble is the e4m3 number q 2^-9, subnormals included, so a word of eight codes is two
@@ -42,7 +42,7 @@ namespace w4 {
 namespace {
 
 constexpr int kRows = 128;                 // of a task
-constexpr int kGroup = 128;
+constexpr int kGroup = 128;                // codes of a step: one group, or two of 64
 constexpr int kSlotBytes = kRows * kGroup / 2;
 // first warps of the roles behind the eight that unpack
 constexpr int kAdd = 8, kIssue = 16, kLoad = 18;
@@ -52,7 +52,7 @@ constexpr int kMaxSmem = 227 * 1024;
 struct WideArgs {
     CUtensorMap map;                       // codes [N][K / 2] bytes, box 64 x 128
     const uint16_t *x;                     // [M, K] bf16
-    const uint16_t *s, *z;                 // [N, K / 128] fp16
+    const uint16_t *s, *z;                 // [N, K / group] fp16
     uint16_t *y;                           // [M, N] bf16
     int32_t *dev_status;
     uint64_t wait_ns;
@@ -140,8 +140,25 @@ __device__ __forceinline__ void mma_group(uint32_t d, uint32_t a, uint64_t b, ui
         : "memory");
 }
 
-// TOK: tokens, 16 or 32.
-template <int TOK> struct Wide {
+// Half of that, for a group of 64.
+__device__ __forceinline__ void mma_half(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, f, e;\n\t.reg .b64 y;\n\t.reg .b32 x;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\tsetp.ne.b32 f, 0, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, f;\n\t"
+        "add.s32 x, %1, 8;\n\tadd.s64 y, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [x], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc)
+        : "memory");
+}
+
+// TOK: tokens, 16 or 32 (of groups of 64: 16, for two groups' sums a step take the columns of
+// 32 tokens).
+template <int TOK, int GROUP> struct Wide {
+    static_assert(TOK == 16 || GROUP == 128);
+    static constexpr int kSub = kGroup / GROUP;            // groups of a step
     static constexpr int kN = 2 * TOK;
     // With 32 tokens the warps that add up take more than an even share of the registers: 256
     // threads of 80, 256 of 128, 128 of 56 of the launch's 640 of 96 (107 us without; the last
@@ -150,8 +167,8 @@ template <int TOK> struct Wide {
     static constexpr int kThreads = 32 * (kSplit ? 20 : 19);
     static constexpr int kUnpackRegs = 80, kAddRegs = 128, kOtherRegs = 56;
     static constexpr int kSplitSum = 256 * kUnpackRegs + 256 * kAddRegs + 128 * kOtherRegs;
-    static constexpr int kXBytes = kN * kGroup;            // a group's B
-    static constexpr uint32_t kD = 128, kX = kD + 4 * kN;  // TMEM columns; A from 0 on
+    static constexpr int kXBytes = kN * kGroup;            // a step's B
+    static constexpr uint32_t kD = 128, kX = kD + 4 * kN * kSub;  // TMEM columns; A from 0 on
     static constexpr uint32_t kIdesc = idesc_f16_f32(128, kN);   // (e4m3: the same bits)
 
     struct Shared {
@@ -163,7 +180,7 @@ template <int TOK> struct Wide {
 
     static __host__ __device__ constexpr int fixed_bytes(int groups)
     {
-        return 1024 + groups * (kXBytes + 8 * TOK);
+        return 1024 + groups * (kXBytes + 8 * TOK * kSub);
     }
 
     static __device__ __forceinline__ bool wait(const WideArgs &p, Shared &s, uint64_t *bar,
@@ -174,7 +191,7 @@ template <int TOK> struct Wide {
     }
 
     // The activations of tokens t0 .. t0 + TOK as B of every group, and for each two tokens
-    // (2^(9 - e), 2^(9 - e), sum x, sum x).  8 lanes have a token's group, 16 values each, in
+    // (2^(9 - e), 2^(9 - e), sum x, sum x).  8 lanes have a token's step, 16 values each, in
     // the order of the unpacked codes (0 2 4 6 1 3 5 7).
     static __device__ void stage(const WideArgs &p, int t0, uint8_t *xs, float *fs, int warp, int lane)
     {
@@ -212,7 +229,7 @@ template <int TOK> struct Wide {
                 }
                 float sum = low(sums) + high(sums);
 #pragma unroll
-                for (int o = 4; o > 0; o >>= 1) {
+                for (int o = 4 / kSub; o > 0; o >>= 1) {
                     tops = __vmaxu2(tops, __shfl_xor_sync(0xffffffffu, tops, o));
                     sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 }
@@ -246,8 +263,9 @@ template <int TOK> struct Wide {
                     *reinterpret_cast<uint4 *>(xs + g * kXBytes + n * 128 + ((l ^ (n & 7)) << 4)) =
                         make_uint4(out[h][0], out[h][1], out[h][2], out[h][3]);
                 }
-                if (l == 0) {
-                    float *to = fs + (g * (TOK / 2) + (tok >> 1)) * 4 + (tok & 1);
+                if (l % (8 / kSub) == 0) {
+                    const int group = g * kSub + l / (8 / kSub);
+                    float *to = fs + (group * (TOK / 2) + (tok >> 1)) * 4 + (tok & 1);
                     to[0] = __uint_as_float(static_cast<uint32_t>(127 + 9 - e) << 23);
                     to[2] = sum;
                 }
@@ -305,8 +323,14 @@ template <int TOK> struct Wide {
                 break;
             tc_fence_after();
             __syncwarp();
-            mma_group(tmem + kD + kN * (2 * w + b), tmem + 32 * (2 * w + b),
-                      bd + static_cast<uint64_t>(g) * (kXBytes >> 4), kIdesc);
+            const uint32_t d = tmem + kD + kN * kSub * (2 * w + b), a = tmem + 32 * (2 * w + b);
+            const uint64_t x = bd + static_cast<uint64_t>(g) * (kXBytes >> 4);
+            if constexpr (kSub == 1) {
+                mma_group(d, a, x, kIdesc);
+            } else {
+                mma_half(d, a, x, kIdesc);
+                mma_half(d + kN, a + 16, x + 4, kIdesc);
+            }
             tc_commit_elect(&s.d_full[w][b]);
         }
         // nothing of this warp's is under way when the CTA ends
@@ -409,44 +433,60 @@ template <int TOK> struct Wide {
         // more than it hides: the roles' code together is more than the instruction cache
         // holds.  4 ahead 98 us, 6 ahead 106.)
         Place to{0, w, w, 0}, at = to;
-        uint16_t sc, ze;
+        uint16_t sc[kSub], ze[kSub];
         auto scales = [&](int idx) {
             const int64_t row = min(row0 + to.task * kRows + mine, p.N - 1);
-            sc = idx < total ? load_weight(p.s + row * p.groups + to.g) : static_cast<uint16_t>(0);
-            ze = idx < total ? load_weight(p.z + row * p.groups + to.g) : static_cast<uint16_t>(0);
+            const int64_t at = (row * p.groups + to.g) * kSub;
+#pragma unroll
+            for (int k = 0; k < kSub; k++) {
+                sc[k] = idx < total ? load_weight(p.s + at + k) : static_cast<uint16_t>(0);
+                ze[k] = idx < total ? load_weight(p.z + at + k) : static_cast<uint16_t>(0);
+            }
             to.next(p, 2);
         };
         scales(w);
 #pragma unroll 1
         for (int idx = w, i = 0; idx < total; idx += 2, i++) {
             const int b = i & 1, g = at.g, task = at.task;
-            const uint32_t scale = sc | static_cast<uint32_t>(ze) << 16;
-            scales(idx + 2);
-            uint64_t s2[4], z2[4];
+            uint32_t scale[kSub];
 #pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const uint32_t v = __shfl_sync(0xffffffffu, scale, 8 * r + (lane >> 2));
-                const float sv = __half2float(__ushort_as_half(static_cast<uint16_t>(v)));
-                const float zv = -__half2float(__ushort_as_half(static_cast<uint16_t>(v >> 16)));
-                s2[r] = pair_of(sv, sv);
-                z2[r] = pair_of(zv, zv);
-            }
+            for (int k = 0; k < kSub; k++)
+                scale[k] = sc[k] | static_cast<uint32_t>(ze[k]) << 16;
+            scales(idx + 2);
             const uint64_t small = pair_of(0.03125f, 0.03125f);
             const ulonglong2 *f =
-                reinterpret_cast<const ulonglong2 *>(fs) + g * (TOK / 2) + (lane & 3);
+                reinterpret_cast<const ulonglong2 *>(fs) + g * kSub * (TOK / 2) + (lane & 3);
+            uint64_t s2[4], z2[4];
+            // the four rows' scales and zeros of the step's group k
+            auto share = [&](int k) {
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const uint32_t v = __shfl_sync(0xffffffffu, scale[k], 8 * r + (lane >> 2));
+                    const float sv = __half2float(__ushort_as_half(static_cast<uint16_t>(v)));
+                    const float zv = -__half2float(__ushort_as_half(static_cast<uint16_t>(v >> 16)));
+                    s2[r] = pair_of(sv, sv);
+                    z2[r] = pair_of(zv, zv);
+                }
+            };
+            share(0);
             if (!wait(p, s, &s.d_full[w][b], i >> 1 & 1))
                 return;
             tc_fence_after();
             __syncwarp();
             uint32_t d1[2][8], d2[2][8];
-            const uint32_t d = tmem + kD + kN * (2 * w + b);
+            const uint32_t d = tmem + kD + kN * kSub * (2 * w + b);
             load_sums(d, d + TOK, d1[0], d2[0]);
+            constexpr int kParts = TOK / 8;                    // of 16 tokens and 16 rows, of a group
 #pragma unroll
-            for (int i = 0; i < TOK / 8; i++) {                // 16 tokens, 16 rows
-                const int c = i / 2, h = i % 2;
+            for (int j0 = 0; j0 < kParts * kSub; j0++) {
+                const int k = j0 / kParts, i = j0 % kParts, c = i / 2, h = i % 2;
+                if (k > 0 && i == 0)
+                    share(k);
                 wait_loads(d1[h], d2[h]);
-                if (i + 1 < TOK / 8) {
-                    const uint32_t next = d + (i + 1) / 2 * 16 + (((i + 1) % 2 * 16) << 16);
+                if (j0 + 1 < kParts * kSub) {
+                    const int n = (j0 + 1) % kParts;
+                    const uint32_t next =
+                        d + (j0 + 1) / kParts * kN + n / 2 * 16 + ((n % 2 * 16) << 16);
                     load_sums(next, next + TOK, d1[h ^ 1], d2[h ^ 1]);
                 } else {
                     tc_fence_before();
@@ -455,7 +495,8 @@ template <int TOK> struct Wide {
                 }
 #pragma unroll
                 for (int j = 0; j < 2; j++) {
-                    const ulonglong2 fv = f[c * 8 + j * 4];    // two tokens' factors, their sums
+                    // two tokens' factors, their sums
+                    const ulonglong2 fv = f[k * (TOK / 2) + c * 8 + j * 4];
 #pragma unroll
                     for (int r = 0; r < 2; r++) {
                         const int at = 4 * j + 2 * r;
@@ -463,9 +504,7 @@ template <int TOK> struct Wide {
                         const uint64_t e2 = static_cast<uint64_t>(d2[h][at + 1]) << 32 | d2[h][at];
                         uint64_t &to = acc[c][h][2 * j + r];
                         to = fma2(s2[2 * h + r],
-                                  fma2(fv.x, fma2(e2, small, e1),
-                                       mul2(z2[2 * h + r], fv.y)),
-                                  to);
+                                  fma2(fv.x, fma2(e2, small, e1), mul2(z2[2 * h + r], fv.y)), to);
                     }
                 }
             }
@@ -548,11 +587,11 @@ template <int TOK> struct Wide {
 };
 
 // CTA (share, part): its share of the tasks, for the part's TOK tokens.
-template <int TOK>
-__global__ void __launch_bounds__(Wide<TOK>::kThreads, 1)
+template <int TOK, int GROUP>
+__global__ void __launch_bounds__(Wide<TOK, GROUP>::kThreads, 1)
     few_linear_wide_kernel(const __grid_constant__ WideArgs p, int parts)
 {
-    using W = Wide<TOK>;
+    using W = Wide<TOK, GROUP>;
     extern __shared__ __align__(1024) uint8_t raw[];
     __shared__ __align__(16) typename W::Shared s;
     uint8_t *ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -653,36 +692,37 @@ EncodeFn encode_fn()
 }
 
 // Slots that fit beside the activations: even, so that a slot is always the same set's.
-int slots_of(int groups, int tok)
+template <int TOK, int GROUP> int slots_of(int groups)
 {
-    const int fixed = tok == 16 ? Wide<16>::fixed_bytes(groups) : Wide<32>::fixed_bytes(groups);
-    return std::min((kMaxSmem - 2048 - fixed) / kSlotBytes / 2 * 2, kMaxSlots);
+    return std::min((kMaxSmem - 2048 - Wide<TOK, GROUP>::fixed_bytes(groups)) / kSlotBytes / 2 * 2,
+                    kMaxSlots);
 }
 
-template <int TOK>
+template <int TOK, int GROUP>
 cudaError_t launch_as(WideArgs &a, int sms, int dev, cudaStream_t stream)
 {
-    auto kern = few_linear_wide_kernel<TOK>;
+    using W = Wide<TOK, GROUP>;
+    auto kern = few_linear_wide_kernel<TOK, GROUP>;
     static std::atomic<uint64_t> raised{0};      // devices whose limit is raised already
     if (!(raised.load(std::memory_order_relaxed) >> (dev & 63) & 1u)) {
         cudaError_t err =
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 2048);
         if (err != cudaSuccess)
             return err;
-        if (Wide<TOK>::kSplit) {               // what setmaxnreg shares out is there
+        if (W::kSplit) {                       // what setmaxnreg shares out is there
             cudaFuncAttributes attr;
             if ((err = cudaFuncGetAttributes(&attr, kern)) != cudaSuccess)
                 return err;
-            if (attr.numRegs * Wide<TOK>::kThreads < Wide<TOK>::kSplitSum)
+            if (attr.numRegs * W::kThreads < W::kSplitSum)
                 return cudaErrorLaunchOutOfResources;
         }
         raised.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
     }
-    a.slots = slots_of(a.groups, TOK);
+    a.slots = slots_of<TOK, GROUP>(a.groups);
     const int parts = (a.M + TOK - 1) / TOK, tasks = (a.N + kRows - 1) / kRows;
     const int shares = std::min(tasks, std::max(sms / parts, 1));
-    const int smem = Wide<TOK>::fixed_bytes(a.groups) + a.slots * kSlotBytes;
-    return launch_pdl(kern, dim3(shares * parts), dim3(Wide<TOK>::kThreads), smem, stream, a, parts);
+    const int smem = W::fixed_bytes(a.groups) + a.slots * kSlotBytes;
+    return launch_pdl(kern, dim3(shares * parts), dim3(W::kThreads), smem, stream, a, parts);
 }
 
 }  // namespace
@@ -690,13 +730,15 @@ cudaError_t launch_as(WideArgs &a, int sms, int dev, cudaStream_t stream)
 // The tokens of a CTA, 32 or 16; 0: the shape is not for this kernel.
 int few_linear_wide_tokens(int M, int K, int group)
 {
-    constexpr int kLeast = 4;                  // slots, and groups
-    if (group != kGroup || K < kLeast * kGroup || M <= 8)
+    constexpr int kLeast = 4;                  // slots, and steps
+    if (K % kGroup || K < kLeast * kGroup || M <= 8)
         return 0;
-    const int groups = K / kGroup;
-    if (M > 16 && slots_of(groups, 32) >= kLeast)
+    const int steps = K / kGroup;
+    if (group == 64)
+        return slots_of<16, 64>(steps) >= kLeast ? 16 : 0;
+    if (M > 16 && slots_of<32, 128>(steps) >= kLeast)
         return 32;
-    return slots_of(groups, 16) >= kLeast ? 16 : 0;
+    return slots_of<16, 128>(steps) >= kLeast ? 16 : 0;
 }
 
 cudaError_t launch_few_linear_wide(const FewLinearProblem &q, cudaStream_t stream)
@@ -729,8 +771,10 @@ cudaError_t launch_few_linear_wide(const FewLinearProblem &q, cudaStream_t strea
     a.K = q.K;
     a.N = q.N;
     a.groups = q.K / kGroup;
-    return few_linear_wide_tokens(q.M, q.K, kGroup) == 32 ? launch_as<32>(a, sms, dev, stream)
-                                                         : launch_as<16>(a, sms, dev, stream);
+    if (q.group == 64)
+        return launch_as<16, 64>(a, sms, dev, stream);
+    return few_linear_wide_tokens(q.M, q.K, q.group) == 32 ? launch_as<32, 128>(a, sms, dev, stream)
+                                                           : launch_as<16, 128>(a, sms, dev, stream);
 }
 
 }  // namespace w4
