@@ -745,8 +745,9 @@ int w4_rope_steps(int rot, double base, int method, double factor, double traine
  *   interleaved 0: pair i is values i and i + rot / 2; else 2 i and 2 i + 1
  *   dtype       0: bf16, 1: fp16
  *   amplitude   multiplies the rotated values (1 where nothing asks for another)
- *   q_out, k_out  like q and k, with strides of their own; they may be q and k
- *               themselves, and else have no memory in common with any input
+ *   q_out, k_out  like q and k, with strides of their own that keep tokens and heads
+ *               apart; they may be q and k themselves, and else have no memory in common
+ *               with any input
  * Arithmetic is fp32 (a head whose sum of squares is beyond its range: zeros), every
  * value rounded once; angles are exact to 2^-31 of a turn
  * for positions up to 2^23 (beyond, the frequencies' rounding to 53 bits shows).

@@ -21,8 +21,9 @@ SOURCES = ["api.cu", "quantize.cu", "route_align.cu", "combine.cu", "grouped_gem
            "few.cu", "kv.cu", "attention.cu", "rope.cu",
            "linear_few.cu", "linear_few_wide.cu"]
 HEADERS = ["launch.h", "ptx.cuh", "korder.cuh", "combine_fold.cuh", "checks.cuh",
-           "route_token.cuh", "attention_plan.cuh"]
+           "route_token.cuh", "attention_plan.cuh", "strides.h"]
 CALLS_SOURCE = os.path.join(CSRC, "calls.cpp")
+CALLS_HEADERS = [os.path.join(CSRC, "strides.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -51,7 +52,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     """Compile every translation unit and link the shared library, and the module beside
     it; returns the library's path."""
     with cf.ThreadPoolExecutor(max_workers=1) as ex:
-        calls = ex.submit(_compile_calls) if force or _stale(calls_path(), [CALLS_SOURCE]) else None
+        calls = ex.submit(_compile_calls) if force or _stale(calls_path(), [CALLS_SOURCE, *CALLS_HEADERS]) else None
         if force or ptxas_info or _stale(LIB, [os.path.join(CSRC, f) for f in SOURCES + HEADERS]):
             _compile(BUILD, LIB, [], verbose, ptxas_info)
         if calls:

@@ -9,6 +9,7 @@
 
 #include "../../include/w4moe.h"
 #include "launch.h"
+#include "strides.h"
 
 namespace w4 {
 PipelineTestHooks &pipeline_test_hooks()
@@ -1157,6 +1158,8 @@ int check_rope(const w4::RopeProblem &r, float eps)
                                        "strides multiples of 8 elements");
     if (!aligned4(r.positions) || (reinterpret_cast<uintptr_t>(r.steps) & 7u))
         return fail(W4_ERR_MISALIGNED, "positions must be 4-byte, steps 8-byte aligned");
+    if (w4::rows_overlap(r.T, r.Hq, r.D, r.q_out_tok, r.q_out_head))
+        return fail(W4_ERR_INVALID_ARG, "tokens or heads of q_out overlap");
     return W4_OK;
 }
 }  // namespace
@@ -1206,6 +1209,8 @@ int w4_qk_norm_rope(const uint16_t *q, int64_t q_tok_stride, int64_t q_head_stri
     if (!aligned16(k_out) || (k_out_tok_stride | k_out_head_stride) & 7)
         return fail(W4_ERR_MISALIGNED, "outputs must be 16-byte aligned and their strides multiples "
                                        "of 8 elements");
+    if (w4::rows_overlap(T, Hkv, D, k_out_tok_stride, k_out_head_stride))
+        return fail(W4_ERR_INVALID_ARG, "tokens or heads of k_out overlap");
     if (int rc = check_device())
         return rc;
     cudaError_t err = w4::launch_rope(r, as_stream(stream));

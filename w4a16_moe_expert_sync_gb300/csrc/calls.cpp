@@ -21,6 +21,7 @@
 #include <optional>
 
 #include "../../include/w4moe.h"
+#include "strides.h"
 
 namespace {
 
@@ -318,8 +319,7 @@ Tensor rope_out(PyObject *own_, PyObject *like_, PyObject *stream)
     if (own->sizes() != like.sizes() || own->scalar_type() != like.scalar_type() ||
         own->stride(2) != 1)
         throw Refused{"q_out and k_out must be like q and k, contiguous along the last axis"};
-    const int64_t D = own->size(2);
-    if ((own->size(0) > 1 && own->stride(0) < D) || (own->size(1) > 1 && own->stride(1) < D))
+    if (w4::rows_overlap(own->size(0), own->size(1), own->size(2), own->stride(0), own->stride(1)))
         throw Refused{"tokens or heads of q_out or k_out overlap"};
     return *own;
 }
