@@ -472,9 +472,8 @@ PyObject *attn(PyObject *const *a)
         if (tree->dim() != 2 || tree->size(0) != T)
             throw Refused{"tree must be [T, words], a bit for each of max_q tokens in a row"};
         words = size(tree->size(1));
-        on_device({&q, &kp, &vp, &table, &lens, &q_offsets, tree, group_offsets, shared, ws, own,
-                   status});
     }
+    on_device({&q, &kp, &vp, &table, &lens, &q_offsets, tree, group_offsets, shared, ws, own, status});
     if (own) {
         if (!own->is_cuda())
             throw Refused{kNotOnGpu};
