@@ -531,9 +531,12 @@ int w4_w4a16_linear(const uint16_t *x, int M, int K, int N, const uint8_t *q, co
  *   q          [N, K/2] uint8, w4_quantize's layout; s, z [N, K/group] fp16
  *   y          [M, N] bf16 out
  * Codes enter the tensor cores exactly, and so do activations (with more than 8 tokens
- * and 128 rows an SM: but for 2^-22 of their group's largest); a group's scale
- * and zero are applied to its fp32 sum, and y is rounded once.  (Activations of 2^57 and
- * more, or not finite, make their token's results so.)  A token's results depend on
+ * and many rows, 128 to 512 an SM by K and the group: but for 2^-22 of their group's
+ * largest); a group's scale and zero are applied to its fp32 sum, and y is rounded once.
+ * Range: a token with an activation beyond 2^57 has results that are as exact or not
+ * finite, one with an activation that is not finite has none that is; below, a group's
+ * sum before its scale is held in steps of 2^-86 (with many rows: of fp32's own), so
+ * results below 2^-70 may lose bits.  A token's results depend on
  * neither the other tokens' values nor where it stands among as many; bit-identical
  * reruns.  dev_status may be NULL.
  * Requires M <= 32, group 64 or 128 dividing K, K up to 11,264, N * K below 2^33,

@@ -234,7 +234,9 @@ template <int TOK, int GROUP> struct Wide {
                     sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 }
                 const uint32_t top = max(tops & 0xFFFFu, tops >> 16);
-                // the largest becomes 2^7 .. 2^8 (below 2^-120 less, for 2^e has to be a number)
+                // the largest becomes 2^7 .. 2^8 (below 2^-120 less, for 2^e has to be a number; from
+                // 2^126 on 2^(9 - e) is none: its token's results become NaN, for the parts would be
+                // cut off at e4m3's largest value)
                 const int e = min(max(134 - static_cast<int>(top >> 7), -118), 127);
                 const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
                 const uint64_t up2 = pair_of(up, up);
@@ -266,7 +268,8 @@ template <int TOK, int GROUP> struct Wide {
                 if (l % (8 / kSub) == 0) {
                     const int group = g * kSub + l / (8 / kSub);
                     float *to = fs + (group * (TOK / 2) + (tok >> 1)) * 4 + (tok & 1);
-                    to[0] = __uint_as_float(static_cast<uint32_t>(127 + 9 - e) << 23);
+                    to[0] = __uint_as_float(top >> 7 > 252 ? 0x7FC00000u
+                                                           : static_cast<uint32_t>(127 + 9 - e) << 23);
                     to[2] = sum;
                 }
             }
