@@ -10,6 +10,7 @@ import re
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -36,8 +37,23 @@ def _nvcc() -> str:
 
 def calls_path() -> str:
     """The module of csrc/calls.cpp: one for each version of torch, whose headers it takes."""
-    version = re.sub(r"\W", "_", importlib.metadata.version("torch"))
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:        # torch from a folder of its own
+        from torch import __version__ as version
+    version = re.sub(r"\W", "_", version)
     return os.path.join(BUILD, f"w4_calls_torch_{version}.so")
+
+
+def _no_calls() -> str | None:
+    """What the module needs and this machine lacks; the library needs none of it."""
+    if importlib.util.find_spec("torch") is None:
+        return "torch"
+    if not shutil.which("g++"):
+        return "g++"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers"
+    return None
 
 
 def _stale(target: str, sources: list) -> bool:
@@ -50,9 +66,15 @@ def _stale(target: str, sources: list) -> bool:
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile every translation unit and link the shared library, and the module beside
-    it; returns the library's path."""
+    it where this machine has what that needs; returns the library's path."""
+    lacking = _no_calls()
+    if lacking:
+        warnings.warn(f"no {lacking}: only the library is built, not the module of the calls that "
+                      "need it", stacklevel=2)
     with cf.ThreadPoolExecutor(max_workers=1) as ex:
-        calls = ex.submit(_compile_calls) if force or _stale(calls_path(), [CALLS_SOURCE, *CALLS_HEADERS]) else None
+        calls = None
+        if not lacking and (force or _stale(calls_path(), [CALLS_SOURCE, *CALLS_HEADERS])):
+            calls = ex.submit(_compile_calls)
         if force or ptxas_info or _stale(LIB, [os.path.join(CSRC, f) for f in SOURCES + HEADERS]):
             _compile(BUILD, LIB, [], verbose, ptxas_info)
         if calls:
@@ -70,8 +92,6 @@ def build_checked(out_dir: str) -> str:
 
 def _compile_calls() -> None:
     gxx = shutil.which("g++")
-    if not gxx:
-        raise RuntimeError("g++ not found: the module that calls the CUDA library cannot be built")
     os.makedirs(BUILD, exist_ok=True)
     torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
