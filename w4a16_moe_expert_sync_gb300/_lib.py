@@ -150,6 +150,15 @@ def load_library(path: str | None = None):
 
 
 _calls_module = None
+_calls_file = None                         # the module's path, once asked for
+
+
+def _calls_built() -> bool:
+    """Whether the module has been built for this version of torch."""
+    global _calls_file
+    if _calls_file is None:
+        _calls_file = calls_path()
+    return os.path.exists(_calls_file)
 
 
 def _calls():
@@ -160,10 +169,10 @@ def _calls():
         if _calls_module is not None:
             return _calls_module
         import torch                       # its libraries are the module's too
-        path = calls_path()
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build the CUDA library first "
-                               "(python -c 'import __graft_entry__ as g; g.build()')")
+        if not _calls_built():
+            raise RuntimeError(f"{_calls_file} is missing: build the CUDA library for this version of "
+                               "torch first (python -c 'import __graft_entry__ as g; g.build()')")
+        path = _calls_file
         loader = importlib.machinery.ExtensionFileLoader("w4_calls", path)
         module = importlib.util.module_from_spec(
             importlib.machinery.ModuleSpec("w4_calls", loader, origin=path))
@@ -1026,9 +1035,54 @@ def w4_attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets, group_off
     layer's pages [P, page_size, Hkv, D]; sequences group_offsets[g] ..
     group_offsets[g + 1] share their first shared_lens[g] tokens, which are read
     once for the group.  scale defaults to 1 / sqrt(D).  Returns out [T, Hq, D]."""
+    if _calls_module is None and not _calls_built():
+        return _attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets, group_offsets,
+                                   shared_lens, max_q, causal, scale, workspace, out, dev_status,
+                                   stream)
     return (_calls_module or _calls()).attn(q, k_pages, v_pages, table, lens, q_offsets, None, causal,
                                             group_offsets, shared_lens, max_q, scale, workspace, out,
                                             dev_status, stream)
+
+
+def _attn_shared_prefix(q, k_pages, v_pages, table, lens, q_offsets, group_offsets, shared_lens,
+                        max_q, causal, scale, workspace, out, dev_status, stream):
+    """The same call of the library where the module has not been built for this torch."""
+    torch = _torch or _load_torch()
+    dtype, (P, page, Hkv, D), strides = _kv_planes(k_pages, v_pages)
+    qs = _rows16(q, dtype, "q")
+    _require_int32(table, lens, q_offsets, group_offsets, shared_lens, dev_status)
+    if q.dim() != 3 or (dtype is not torch.bfloat16 and dtype is not torch.float16):
+        raise ValueError("q must be [T, Hq, D] of the pages' type, bf16 or fp16")
+    T, Hq, q_d = q.shape
+    if q_d != D:
+        raise ValueError("q must be [T, Hq, D] of the pages' type, bf16 or fp16")
+    B, W = _kv_batch(table, lens, q_offsets)
+    G = 0 if group_offsets is None else group_offsets.numel() - 1
+    if G < 0 or (G > 0 and (shared_lens is None or shared_lens.numel() != G)):
+        raise ValueError("group_offsets must be [G + 1] and shared_lens [G]")
+    if out is not None:
+        _require(((out, dtype, (T, Hq, D), "out"),))
+    if workspace is not None:
+        _require_cuda(workspace)
+    device = torch.cuda.current_device()
+    for t in (q, k_pages, v_pages, table, lens, q_offsets, group_offsets, shared_lens, workspace, out,
+              dev_status):
+        if t is not None and t.get_device() != device:
+            raise ValueError("tensors passed to the CUDA library must live on the current device")
+    if out is None:
+        out = _result((T, Hq, D), dtype, q.device, stream)
+    if workspace is None:
+        workspace = _scratch(
+            max(w4_attn_shared_prefix_workspace_size(T, B, G, max_q, Hq, Hkv, D), 256)
+            if Hkv and Hq % Hkv == 0 else 256, torch.uint8, q.device, stream)
+    _check(load_library().w4_attn_shared_prefix(
+        q.data_ptr(), qs[0], qs[1], k_pages.data_ptr(), v_pages.data_ptr(), *strides[:3], P, page,
+        table.data_ptr(), W, lens.data_ptr(), q_offsets.data_ptr(), T, B, max_q,
+        _ptr(group_offsets), _ptr(shared_lens), G, Hq, Hkv, D,
+        0 if dtype is torch.bfloat16 else 1, int(causal), D ** -0.5 if scale is None else scale,
+        workspace.data_ptr(), workspace.nbytes, out.data_ptr(), _ptr(dev_status),
+        _stream(stream)), "w4_attn_shared_prefix")
+    return out
 
 
 def w4_attn_tree(q, k_pages, v_pages, table, lens, q_offsets, tree, group_offsets=None,
