@@ -38,8 +38,10 @@ struct Library {
     decltype(&w4_attn_tree) attn_tree;
     decltype(&w4_attn_shared_prefix_workspace_size) attn_workspace_size;
     PyObject *check, *result, *workspace;
-    int device;                            // a test's stand-in for the current device, or -1
 } lib;
+
+// A test's stand-in for the calling thread's current device, or -1.
+thread_local int pretended_device = -1;
 
 struct Refused {                           // becomes a ValueError
     const char *why;
@@ -111,7 +113,10 @@ bool truth(PyObject *o)
     return v != 0;
 }
 
-int current_device() { return lib.device >= 0 ? lib.device : c10::cuda::current_device(); }
+int current_device()
+{
+    return pretended_device >= 0 ? pretended_device : c10::cuda::current_device();
+}
 
 // A call's stream: a Stream's handle, or the current device's current one.
 w4_stream_t stream_of(PyObject *stream)
@@ -561,14 +566,14 @@ PyObject *bind(PyObject *const *a)
         Py_XDECREF(*own[i]);
         *own[i] = a[7 + i];
     }
-    lib.device = -1;
     Py_RETURN_NONE;
 }
 
-// (device): stands for the current one until it is -1 (for tests)
+// (device): stands for the calling thread's current one until it is -1 (for tests: tensors
+// of another device than the current one, where there is only one)
 PyObject *pretend_device(PyObject *const *a)
 {
-    lib.device = integer(a[0]);
+    pretended_device = integer(a[0]);
     Py_RETURN_NONE;
 }
 
@@ -594,6 +599,5 @@ PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "w4_calls", nullptr, -1, method
 
 PyMODINIT_FUNC PyInit_w4_calls()
 {
-    lib.device = -1;
     return PyModule_Create(&module_def);
 }
