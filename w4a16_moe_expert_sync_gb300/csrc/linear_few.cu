@@ -51,6 +51,7 @@ struct FewLinearArgs {
     const uint8_t *q;                      // [N, K / 2]
     const uint16_t *s, *z;                 // [N, K / group] fp16
     uint16_t *y;                           // [M, N] bf16
+    int32_t *dev_status;
     int M, K, N;
     int blocks;                            // of 128 codes, the last may be half of one
 };
@@ -245,7 +246,8 @@ struct FewLinear {
                 out.y = bf16_pair(f[2] * kUp, f[6] * kUp);
                 out.z = bf16_pair(f[1] * kUpHigh, f[5] * kUpHigh);
                 out.w = bf16_pair(f[3] * kUpHigh, f[7] * kUpHigh);
-                *reinterpret_cast<uint4 *>(tile + (block * 4 + j) * 512 + lane * 16) = out;
+                if (W4_IN_BOUNDS(n < NT && block * 4 + j < p.blocks * 4, p.dev_status))
+                    *reinterpret_cast<uint4 *>(tile + (block * 4 + j) * 512 + lane * 16) = out;
             }
 #pragma unroll
             for (int h = 0; h < kGroups; h++) {
@@ -271,6 +273,12 @@ struct FewLinear {
                     make_float4(acc[r][n][0], acc[r][n][1], acc[r][n][2], acc[r][n][3]);
     }
 
+    // Whether y has n values from `at` on.
+    static __device__ __forceinline__ bool in_y(const FewLinearArgs &p, const uint16_t *at, int n)
+    {
+        return at >= p.y && at + n <= p.y + static_cast<int64_t>(p.M) * p.N;
+    }
+
     // A finished task's sums to y, two neighbouring rows of a token at a time.
     static __device__ __forceinline__ void store(const FewLinearArgs &p, int t0, int64_t row0,
                                                  int lane, const float (&acc)[RT][NT][4])
@@ -289,11 +297,12 @@ struct FewLinear {
                     const uint32_t v = bf16_pair(acc[r][n][c] * kDown, acc[r][n][2 + c] * kDown);
                     uint16_t *y = p.y + static_cast<int64_t>(t) * p.N + row;
                     if (row + 1 < p.N && (p.N & 1) == 0) {
-                        *reinterpret_cast<uint32_t *>(y) = v;
+                        if (W4_IN_BOUNDS(in_y(p, y, 2), p.dev_status))
+                            *reinterpret_cast<uint32_t *>(y) = v;
                     } else {
-                        if (row < p.N)
+                        if (row < p.N && W4_IN_BOUNDS(in_y(p, y, 1), p.dev_status))
                             y[0] = static_cast<uint16_t>(v);
-                        if (row + 1 < p.N)
+                        if (row + 1 < p.N && W4_IN_BOUNDS(in_y(p, y + 1, 1), p.dev_status))
                             y[1] = static_cast<uint16_t>(v >> 16);
                     }
                 }
@@ -495,6 +504,7 @@ cudaError_t launch_few_linear(const FewLinearProblem &q, cudaStream_t stream)
     a.s = q.s;
     a.z = q.z;
     a.y = q.y;
+    a.dev_status = q.dev_status;
     a.M = q.M;
     a.K = q.K;
     a.N = q.N;

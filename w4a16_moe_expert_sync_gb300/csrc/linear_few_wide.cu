@@ -262,7 +262,8 @@ template <int TOK, int GROUP> struct Wide {
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
                     const int n = h * TOK + tok;
-                    *reinterpret_cast<uint4 *>(xs + g * kXBytes + n * 128 + ((l ^ (n & 7)) << 4)) =
+                    if (W4_IN_BOUNDS(g < p.groups, p.dev_status))
+                        *reinterpret_cast<uint4 *>(xs + g * kXBytes + n * 128 + ((l ^ (n & 7)) << 4)) =
                         make_uint4(out[h][0], out[h][1], out[h][2], out[h][3]);
                 }
                 if (l % (8 / kSub) == 0) {
@@ -440,10 +441,13 @@ template <int TOK, int GROUP> struct Wide {
         auto scales = [&](int idx) {
             const int64_t row = min(row0 + to.task * kRows + mine, p.N - 1);
             const int64_t at = (row * p.groups + to.g) * kSub;
+            const bool there =
+                idx < total && W4_IN_BOUNDS(at >= 0 && at + kSub <= static_cast<int64_t>(p.N) *
+                                                                        p.groups * kSub, p.dev_status);
 #pragma unroll
             for (int k = 0; k < kSub; k++) {
-                sc[k] = idx < total ? load_weight(p.s + at + k) : static_cast<uint16_t>(0);
-                ze[k] = idx < total ? load_weight(p.z + at + k) : static_cast<uint16_t>(0);
+                sc[k] = there ? load_weight(p.s + at + k) : static_cast<uint16_t>(0);
+                ze[k] = there ? load_weight(p.z + at + k) : static_cast<uint16_t>(0);
             }
             to.next(p, 2);
         };
@@ -520,6 +524,12 @@ template <int TOK, int GROUP> struct Wide {
         }
     }
 
+    // Whether y has a value at `at`.
+    static __device__ __forceinline__ bool in_y(const WideArgs &p, const uint16_t *at)
+    {
+        return at >= p.y && at < p.y + static_cast<int64_t>(p.M) * p.N;
+    }
+
     // A task's sums: the second set's through tensor memory to the first, which stores them.
     static __device__ __forceinline__ bool finish(const WideArgs &p, Shared &s, int t0, int row, int w,
                                                   int quarter, int done, uint32_t tmem,
@@ -579,9 +589,9 @@ template <int TOK, int GROUP> struct Wide {
             const uint32_t r = bf16_pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
             const int t = t0 + 2 * j;
             uint16_t *y = p.y + static_cast<int64_t>(t) * p.N + row;
-            if (row < p.N && t < p.M)
+            if (row < p.N && t < p.M && W4_IN_BOUNDS(in_y(p, y), p.dev_status))
                 y[0] = static_cast<uint16_t>(r);
-            if (row < p.N && t + 1 < p.M)
+            if (row < p.N && t + 1 < p.M && W4_IN_BOUNDS(in_y(p, y + p.N), p.dev_status))
                 y[p.N] = static_cast<uint16_t>(r >> 16);
         }
         __syncwarp();
