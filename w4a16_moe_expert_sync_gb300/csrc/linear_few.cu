@@ -477,12 +477,14 @@ cudaError_t launch_few_linear_group(const FewLinearArgs &a, int sms, int dev, cu
         return launch_few_linear_as<GROUP, 2, 2, 16, 2>(a, sms, dev, stream);
     if (many && smem_of<FewLinear<GROUP, 1, 2, 16, 3>>(a.blocks, 1) <= kRoomySmem)
         return launch_few_linear_as<GROUP, 1, 2, 16, 3>(a, sms, dev, stream);
-    if (GROUP == 128 && many && smem_of<FewLinear<GROUP, 1, 2, 16, 2>>(a.blocks, 1) <= kRoomySmem)
-        return launch_few_linear_as<GROUP, 1, 2, 16, 2>(a, sms, dev, stream);
+    if constexpr (GROUP == 128)
+        if (many && smem_of<FewLinear<GROUP, 1, 2, 16, 2>>(a.blocks, 1) <= kRoomySmem)
+            return launch_few_linear_as<GROUP, 1, 2, 16, 2>(a, sms, dev, stream);
     if (!many && smem_of<FewLinear<GROUP, 1, 1, 16, 4>>(a.blocks, 1) <= kRoomySmem)
         return launch_few_linear_as<GROUP, 1, 1, 16, 4>(a, sms, dev, stream);
-    if (GROUP == 128 && smem_of<FewLinear<GROUP, 1, 1, 16, 3>>(a.blocks, 1) <= kRoomySmem)
-        return launch_few_linear_as<GROUP, 1, 1, 16, 3>(a, sms, dev, stream);
+    if constexpr (GROUP == 128)
+        if (smem_of<FewLinear<GROUP, 1, 1, 16, 3>>(a.blocks, 1) <= kRoomySmem)
+            return launch_few_linear_as<GROUP, 1, 1, 16, 3>(a, sms, dev, stream);
     return launch_few_linear_as<GROUP, 1, 1, 16, 2>(a, sms, dev, stream);
 }
 
