@@ -752,9 +752,10 @@ int w4_rope_steps(int rot, double base, int method, double factor, double traine
  *               apart; they may be q and k themselves, and else have no memory in common
  *               with any input
  * Arithmetic is fp32 (a head whose sum of squares is beyond its range: zeros), every
- * value rounded once; angles are exact to 2^-31 of a turn
- * for positions up to 2^23 (beyond, the frequencies' rounding to 53 bits shows).
- * Requires D a multiple of 8 up to 256, rot a multiple of 16 up to D, pointers 16-byte aligned, strides multiples of 8 elements.  One launch.
+ * value rounded once; angles are exact to 2^-25 of a turn
+ * for positions up to 2^26 (beyond, the frequencies' rounding to 53 bits shows).
+ * Requires D a multiple of 8 up to 256, rot a multiple of 16 up to D, pointers 16-byte
+ * aligned, strides multiples of 8 elements.  One launch.
  * ------------------------------------------------------------------------ */
 int w4_qk_norm_rope(const uint16_t *q, int64_t q_tok_stride, int64_t q_head_stride,
                     const uint16_t *k, int64_t k_tok_stride, int64_t k_head_stride,

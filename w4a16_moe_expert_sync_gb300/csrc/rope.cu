@@ -8,9 +8,10 @@
 //
 // Angles.  A frequency is held as the fraction of a turn per position, 64 bits
 // after the point (a step).  pos * step modulo 2^64 is then the angle with its
-// whole turns dropped exactly, whatever the position; its upper 32 bits are the
-// argument of sincospif, 2^-32 of a turn from the product.  No table of
-// cosines by position is kept, nothing is read but the rot / 2 steps.
+// whole turns dropped exactly, whatever the position; its upper 32 bits, rounded
+// to fp32's 24 (2^-26 of a turn where that is near a half), are the argument of
+// sincospif.  No table of cosines by position is kept, nothing is read but the
+// rot / 2 steps.
 //
 // A group of 4, 8 or 16 lanes takes some heads of one token.  A lane has 16 of a
 // head's values: 8 first ones of pairs and the 8 second ones (or 8 neighbouring pairs),
