@@ -1279,8 +1279,10 @@ struct Kernel {
     // rescaled.  For bf16 it moves to the maximum, for fp16 to 2^7 below, so that P lies
     // in 0 .. 2^15 and a weight vanishes only 2^32 below the largest (2^25 otherwise: a
     // hundred thousand keys beside one that outweighs them can be 0.4 % of the result).
-    // P is rounded to the values' type for the MMA (its
-    // denominator sums the unrounded).  When S is here, every MMA before it has
+    // P is rounded to the values' type, for the MMA takes both operands of one (its
+    // denominator sums the unrounded): an output's error against 64 bits, 2-norm, is 1.1 to
+    // 1.4 times that of its own rounding (trees, bf16: 0.0019 to 0.0023 instead of 0.0017;
+    // fp16: 0.00029 instead of 0.00021).  P in two parts would double the PVs.  When S is here, every MMA before it has
     // completed, so O may be changed.
     // (Not with o_done: there the PV before may be under way; it is awaited where O changes.)
     // False once a wait has given up.
