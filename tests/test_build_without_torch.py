@@ -70,3 +70,21 @@ def test_torch_without_metadata(monkeypatch):
     name = os.path.basename(build.calls_path())
     assert name.startswith("w4_calls_torch_") and name.endswith(".so")
     assert "".join(c if c.isalnum() else "_" for c in torch.__version__) in name
+
+
+@pytest.mark.parametrize("lack", [_lack_torch, _lack_gxx, _lack_headers])
+def test_the_build_entry_loads_what_was_built(built, monkeypatch, tmp_path, lack):
+    import __graft_entry__
+    import oracle
+    import w4a16_moe_expert_sync_gb300 as w4
+    from w4a16_moe_expert_sync_gb300 import _lib
+    for module, name in ((oracle, "build"), (w4, "load_library"), (_lib, "_calls")):
+        monkeypatch.setattr(module, name, lambda name=name: built.append(name))
+    monkeypatch.setattr(build, "_stale", lambda *a: True)
+    __graft_entry__.build()
+    assert sorted(built) == ["_calls", "build", "library", "load_library", "module"]
+    del built[:]
+    lack(monkeypatch, tmp_path)
+    with pytest.warns(UserWarning, match="only the library"):
+        __graft_entry__.build()
+    assert sorted(built) == ["build", "library", "load_library"]

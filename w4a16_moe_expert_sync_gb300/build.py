@@ -45,7 +45,7 @@ def calls_path() -> str:
     return os.path.join(BUILD, f"w4_calls_torch_{version}.so")
 
 
-def _no_calls() -> str | None:
+def calls_lack() -> str | None:
     """What the module needs and this machine lacks; the library needs none of it."""
     if importlib.util.find_spec("torch") is None:
         return "torch"
@@ -67,7 +67,7 @@ def _stale(target: str, sources: list) -> bool:
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile every translation unit and link the shared library, and the module beside
     it where this machine has what that needs; returns the library's path."""
-    lacking = _no_calls()
+    lacking = calls_lack()
     if lacking:
         warnings.warn(f"no {lacking}: only the library is built, not the module of the calls that "
                       "need it", stacklevel=2)
